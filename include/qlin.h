@@ -508,6 +508,113 @@ qlin_status decode_lanes_t158(const t158_model *m, float *kv_caches, int n_seqs,
 int decode_lanes_t158_launches(const t158_model *m, int n_lanes);
 qlin_status decode_lanes_t158_status(void *workspace, qlin_stream_t stream);
 
+/* ========================================================================
+ * Many sequences, and beams of one prompt.  The citric page's "Many users at
+ * once" keeps one cache per user; these operators are what its lanes need when
+ * a model's layers see a window only, when users share a prompt, and when the
+ * next tokens come from a beam search.  They have no counterpart on the pages.
+ * ====================================================================== */
+
+/* The keys and values of n_seqs sequences, `rows` rows each: KV head g of row
+ * r of sequence s is the head_dim values at
+ * k + s * seq_stride + r * row_stride + g * head_dim (strides in elements; v
+ * alike).  k and v are device pointers, 16-byte aligned, both strides
+ * multiples of 16 bytes and below 2^40 bytes, row_stride >= n_kv * head_dim.
+ * type: fp32, or bf16 (bits).  A layer of decode_lanes_t158's caches is
+ * {kv_caches + (2 layer) * max_pos * kv_dim, kv_caches + (2 layer + 1) *
+ * max_pos * kv_dim, 2 n_layers max_pos kv_dim, kv_dim, n_seqs, max_pos,
+ * QLIN_KV_F32}. */
+typedef enum { QLIN_KV_F32 = 0, QLIN_KV_BF16 = 1 } qlin_kv_type;
+typedef struct {
+    const void *k, *v;
+    int64_t seq_stride, row_stride;
+    int32_t n_seqs, rows;
+    int32_t type; /* qlin_kv_type */
+    int32_t reserved0;
+} qlin_kv;
+
+/* Attention over lanes with a sliding window and first tokens that stay
+ * visible.  Lane i is the token at positions[i] of sequence seqs[i] (device
+ * int32 [n_lanes]; one token of each of many users, chunks of prompts, or
+ * both; lanes of one sequence that stand next to each other share its reads).
+ * It sees the keys at positions j <= p with j > p - window or j < sinks; with
+ * window 0 every j <= p.  Query head h (KV head h / (n_heads / n_kv)) gets
+ * sum_j w_j v_j, w = softmax over the seen j of q . k_j / sqrt(head_dim).
+ * q, out: device fp32 [n_lanes][n_heads][head_dim], 16-byte aligned, not
+ * overlapping.  kv (host) describes the caches; the lanes' own rows are in
+ * them already.  head_dim: a multiple of 16, 16..256; n_lanes: 1..4096.
+ * A lane with a negative position is padding: its outputs are zeros.  A lane
+ * whose sequence or position is out of range gets zeros too and sets bit 0 of
+ * *status_word (device int32, may be NULL; bit 1: a bounded device wait gave
+ * up; nothing clears it).  Rows that a lane does not see never reach its
+ * outputs, whatever they hold; NaN or an infinity in a q, k or v that it sees
+ * makes its outputs NaN (of the heads concerned).
+ * fp32 accuracy with either cache type: the products run on the tensor cores
+ * on bf16 terms that carry all 24 significant bits, with fp32 accumulation,
+ * and the softmax is in fp32; |x| above the largest bf16 (about 3.39e38)
+ * counts as an infinity.
+ * workspace: device, 16-byte aligned, qlin_attention_lanes_workspace_size
+ * bytes (0 for sizes out of range), owned by the caller, any content; calls
+ * sharing it must not overlap on the GPU.  The call issues a fixed sequence of
+ * kernels with no host synchronisation and can be captured. */
+size_t qlin_attention_lanes_workspace_size(int n_lanes, int n_heads, int n_kv, int head_dim);
+qlin_status qlin_attention_lanes(const float *q, const qlin_kv *kv, const int32_t *positions, const int32_t *seqs,
+                                 int n_lanes, int n_heads, int n_kv, int head_dim, int window, int sinks, float *out,
+                                 int32_t *status_word, void *workspace, size_t workspace_bytes, qlin_stream_t stream);
+
+/* The same for lanes that share prompts kept once.  Lane i continues prompt
+ * prefix_of[i] (device int32 [n_lanes], NULL: prompt 0 for every lane), whose
+ * first prefix_len[f] rows (device int32 [prefix->n_seqs]) are the keys and
+ * values of positions 0 .. prefix_len[f]-1; position prefix_len[f] + r is row r
+ * of the lane's own sequence in kv.  positions[i] counts from the prompt's
+ * start.  A prompt's rows are read once for the lanes of it that stand next to
+ * each other.  Both caches have the same type.  Everything else, the
+ * workspace's size included, as qlin_attention_lanes; a lane whose prompt or
+ * prompt length is out of range counts as one out of range. */
+qlin_status qlin_attention_prefix(const float *q, const qlin_kv *prefix, const int32_t *prefix_len,
+                                  const int32_t *prefix_of, const qlin_kv *kv, const int32_t *positions,
+                                  const int32_t *seqs, int n_lanes, int n_heads, int n_kv, int head_dim, int window,
+                                  int sinks, float *out, int32_t *status_word, void *workspace,
+                                  size_t workspace_bytes, qlin_stream_t stream);
+
+/* Beam search's selection.  Group g has `beams` beams with running scores
+ * scores[g][b] and logits row g * beams + b (device fp32, rows row_stride
+ * floats apart).  A beam offers scores[g][b] + logits[v] - log sum_v
+ * exp(logits[v]) for every word v; a finished one (finished[g][b] != 0, device
+ * uint8, may be NULL) offers only itself: the token eos with its score
+ * unchanged.  The n_out largest of each group come out in descending order
+ * (ties: the lower beam, then the lower word): out_scores, parents (the beam's
+ * number in its group) and tokens, [n_groups][n_out] each.  Offers of minus
+ * infinity (a beam with that score, a word with that logit) are not taken;
+ * where a group has fewer than n_out others, the rest of its lists is minus
+ * infinity, -1 and -1.  A beam whose logits hold a NaN or plus infinity offers
+ * nothing.  Offers are formed and compared in fp64; out_scores may be scores
+ * of the next call, but not of this one.  beams: 1..64, n_out: 1..128, vocab:
+ * up to 2^24.  Pointers 4-byte aligned (logits 16-byte aligned with row_stride
+ * % 4 == 0 are read fastest).  workspace: device, 16-byte aligned,
+ * qlin_beam_select_workspace_size bytes (0 for sizes out of range), any
+ * content; calls sharing it must not overlap. */
+size_t qlin_beam_select_workspace_size(int n_groups, int beams, int vocab, int n_out);
+qlin_status qlin_beam_select(const float *logits, int64_t row_stride, const float *scores, const uint8_t *finished,
+                             int eos, int n_groups, int beams, int vocab, int n_out, float *out_scores,
+                             int32_t *parents, int32_t *tokens, void *workspace, size_t workspace_bytes,
+                             qlin_stream_t stream);
+
+/* The beams' states follow the selection, in place: in every plane, rows 0 ..
+ * n_rows[g]-1 of beam b of group g become those that beam parents[g][b] of the
+ * group had before the call.  cache: device; beam b of group g starts at
+ * (g * beams + b) * seq_stride, its plane pl at pl * plane_stride, its row r at
+ * r * row_bytes (all in bytes and multiples of 16; any type of row; the beams'
+ * rows must not overlap).  n_planes is 2 n_layers for decode_lanes_t158's
+ * caches.  parents: device int32 [n_groups][beams]; a parent out of range (-1)
+ * leaves the beam as it is.  n_rows: device int32 [n_groups], cut to 0 ..
+ * max_rows; NULL: max_rows for all.  Rows behind n_rows[g] are left alone.  A
+ * beam that is its own parent moves nothing.  beams: 1..64.  status_word as
+ * above (bit 1 only). */
+qlin_status qlin_beam_reorder(void *cache, int64_t seq_stride, int64_t plane_stride, int n_planes, int64_t row_bytes,
+                              int max_rows, const int32_t *parents, const int32_t *n_rows, int n_groups, int beams,
+                              int32_t *status_word, qlin_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

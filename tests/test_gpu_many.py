@@ -1,0 +1,344 @@
+"""GPU parity of the attention over lanes (windows, first tokens, shared
+prompts) against the definition in 64 bits, lane by lane.
+
+Tolerance.  A score is a sum of up to 256 products of 24-bit factors in fp32:
+with half a step (2^-24) lost per term, random in sign, the error is about
+sqrt(3 * 256) * 2^-24 of the running sum, whose size here stays below about 8
+(scores of standard deviation 2): 1.3e-5 in the worst key, and the weights
+have that relative error.  A row's outputs are weighted means, so their
+2-norm is off by at most that much relatively; 2e-5 leaves a factor 1.5.  A
+wrongly seen or unseen key among n moves a row by about 1/sqrt(n), 3e-2 at
+n = 1000."""
+import numpy as np
+import pytest
+
+from gpu_util import device
+
+pytestmark = pytest.mark.gpu
+TOL = 2e-5
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return device()
+
+
+def _ref(q, keys, vals, p, window, sinks, n_kv):
+    """one lane in 64 bits: q [H][hd]; keys, vals [>= p + 1][n_kv][hd], by position"""
+    H, hd = q.shape
+    j = np.arange(p + 1)
+    seen = (j > p - window) | (j < sinks) if window else np.ones(p + 1, bool)
+    k, v = keys[: p + 1][seen].astype(np.float64), vals[: p + 1][seen].astype(np.float64)
+    out = np.zeros((H, hd))
+    for h in range(H):
+        g = h // (H // n_kv)
+        s = k[:, g] @ q[h].astype(np.float64) / np.sqrt(hd)
+        w = np.exp(s - s.max())
+        out[h] = (w / w.sum()) @ v[:, g]
+    return out
+
+
+def _close(got, ref):
+    """every row of every lane and head by its own 2-norm"""
+    e = np.linalg.norm(got - ref, axis=-1) / np.maximum(np.linalg.norm(ref, axis=-1), 1e-30)
+    assert np.isfinite(got).all()
+    assert e.max() <= TOL, f"worst row {np.unravel_index(e.argmax(), e.shape)}: {e.max()}"
+
+
+class Caches:
+    """caches [n_seqs][layers][2][rows][kv_dim], the last layer's the ones used"""
+
+    def __init__(self, dev, kind, n_seqs, rows, n_kv, hd, seed=0, layers=2, fill=None):
+        import torch
+
+        from weight_streaming_gemv_gb300 import qlin
+
+        g = torch.Generator(device=dev).manual_seed(seed)
+        t = torch.randn((n_seqs, layers, 2, rows, n_kv * hd), generator=g, device=dev)
+        self.t = t.to(torch.bfloat16 if kind == "bf16" else torch.float32)
+        self.n_kv, self.hd, self.rows = n_kv, hd, rows
+        self.k, self.v = self.t[:, -1, 0], self.t[:, -1, 1]
+        self.c = qlin.kv_cache(self.k, self.v)
+
+    def host(self, s):
+        f = lambda x: x[s].float().cpu().numpy().reshape(self.rows, self.n_kv, self.hd)
+        return f(self.k), f(self.v)
+
+
+def _i32(x, dev):
+    import torch
+
+    return torch.as_tensor(np.ascontiguousarray(x, np.int32)).to(dev)
+
+
+class Call:
+    """One set of buffers around the two entry points."""
+
+    def __init__(self, dev, n_lanes, H, n_kv, hd, seed=1, extra=3):
+        import torch
+
+        from weight_streaming_gemv_gb300 import qlin
+
+        g = torch.Generator(device=dev).manual_seed(seed)
+        self.n, self.H, self.n_kv, self.hd = n_lanes, H, n_kv, hd
+        self.q = torch.randn((n_lanes, H, hd), generator=g, device=dev) * 2
+        self.out = torch.full((n_lanes + extra, H, hd), 7.5, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.bytes = qlin.qlin_attention_lanes_workspace_size(n_lanes, H, n_kv, hd)
+        self.ws = torch.randint(0, 255, (self.bytes,), dtype=torch.uint8, device=dev)
+
+    def lanes(self, kv, pos, seqs, window=0, sinks=0, stream=None):
+        from weight_streaming_gemv_gb300 import qlin
+
+        qlin.qlin_attention_lanes(self.q, kv.c, pos, seqs, self.n, self.H, self.n_kv, self.hd, window, sinks,
+                                  self.out, self.status, self.ws, self.bytes, stream)
+
+    def prefix(self, pre, plen, pof, kv, pos, seqs, window=0, sinks=0, stream=None):
+        from weight_streaming_gemv_gb300 import qlin
+
+        qlin.qlin_attention_prefix(self.q, pre.c, plen, pof, kv.c, pos, seqs, self.n, self.H, self.n_kv, self.hd,
+                                   window, sinks, self.out, self.status, self.ws, self.bytes, stream)
+
+    def result(self, status=0):
+        import torch
+
+        torch.cuda.synchronize()
+        assert int(self.status.item()) == status
+        got = self.out.cpu().numpy()
+        assert (got[self.n:] == 7.5).all(), "rows behind the last lane were written"
+        return got[: self.n]
+
+
+def _check_lanes(dev, kind, n_seqs, rows, H, n_kv, hd, pos, seqs, window, sinks, seed=0, status=0):
+    kv = Caches(dev, kind, n_seqs, rows, n_kv, hd, seed)
+    c = Call(dev, len(pos), H, n_kv, hd, seed + 1)
+    c.lanes(kv, _i32(pos, dev), _i32(seqs, dev), window, sinks)
+    got, q = c.result(status), c.q.cpu().numpy()
+    ref = np.zeros_like(got, dtype=np.float64)
+    for i, (p, s) in enumerate(zip(pos, seqs)):
+        if 0 <= p < rows and 0 <= s < n_seqs:
+            ref[i] = _ref(q[i], *kv.host(s), p, window, sinks, n_kv)
+    _close(got, ref)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("p", [0, 1, 63, 64, 127, 128, 129, 255, 300, 1000])
+def test_one_token(dev, kind, p):
+    _check_lanes(dev, kind, 1, p + 1, 4, 1, 256, [p], [0], 0, 0, seed=p)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("H,n_kv,hd", [(4, 1, 256), (1, 1, 16), (2, 2, 32), (3, 1, 64), (16, 2, 128), (10, 2, 80),
+                                       (8, 8, 64), (6, 2, 192), (71, 1, 64), (130, 2, 48), (8, 1, 240)])
+def test_head_layouts(dev, kind, H, n_kv, hd):
+    # one token each, at positions around a block of 128 rows
+    pos, seqs = [0, 5, 127, 128, 260, 399], [3, 1, 0, 4, 2, 5]
+    _check_lanes(dev, kind, 6, 400, H, n_kv, hd, pos, seqs, 0, 0, seed=H)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (7, 3), (64, 4), (128, 0), (129, 130), (200, 4), (511, 1),
+                                          (4000, 4), (2147483647, 2147483647), (1, 2147483647)])
+def test_windows(dev, kind, window, sinks):
+    # single tokens of many users at mixed positions, two of them in one sequence
+    pos = [0, 1, 63, 127, 128, 200, 511, 640, 699, 350]
+    seqs = [0, 1, 2, 3, 4, 0, 1, 2, 3, 3]
+    _check_lanes(dev, kind, 5, 700, 4, 2, 64, pos, seqs, window, sinks, seed=window % 97)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (33, 0), (100, 4), (1, 2)])
+@pytest.mark.parametrize("H,n_kv,hd", [(4, 1, 256), (6, 2, 64), (40, 1, 32)])
+def test_prompt_chunks(dev, kind, window, sinks, H, n_kv, hd):
+    # two prompts' chunks, a token between them, padding, and a chunk listed backwards
+    pos = list(range(90, 90 + 131)) + [40] + [-1] * 3 + list(range(0, 70)) + [-1] + list(range(39, -1, -1))
+    seqs = [1] * 131 + [3] + [0] * 3 + [2] * 70 + [2] + [0] * 40
+    _check_lanes(dev, kind, 4, 256, H, n_kv, hd, pos, seqs, window, sinks, seed=window)
+
+
+def test_many_lanes_of_short_sequences(dev):
+    # more lanes than SMs by far, each with a handful of keys
+    pos = [i % 5 for i in range(4096)]
+    seqs = [i % 64 for i in range(4096)]
+    _check_lanes(dev, "f32", 64, 8, 2, 2, 16, pos, seqs, 3, 1)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_long_context(dev, kind):
+    _check_lanes(dev, kind, 2, 40000, 8, 2, 128, [39999, 17], [1, 0], 0, 0)
+    _check_lanes(dev, kind, 2, 40000, 8, 2, 128, [39998, 39999], [1, 1], 20000, 130)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_unseen_rows_never_reach_the_outputs(dev, kind):
+    import torch
+
+    S, R, H, n_kv, hd, W, sinks = 3, 300, 4, 2, 64, 50, 3
+    pos = [170, 20] + list(range(100, 164))
+    seqs = [0, 1] + [2] * 64
+    for bad in (float("nan"), float("inf"), -float("inf"), 3.4e38):
+        kv = Caches(dev, kind, S, R, n_kv, hd, 3)
+        clean = [kv.host(s) for s in range(S)]
+        for t in (kv.k, kv.v):
+            t[0, 171:] = bad
+            t[0, 3:121] = bad
+            t[1, 21:] = bad
+            t[2, 164:] = bad
+            t[2, 3:51] = bad
+        c = Call(dev, len(pos), H, n_kv, hd)
+        c.lanes(kv, _i32(pos, dev), _i32(seqs, dev), W, sinks)
+        got, q = c.result(), c.q.cpu().numpy()
+        _close(got, np.stack([_ref(q[i], *clean[s], p, W, sinks, n_kv) for i, (p, s) in enumerate(zip(pos, seqs))]))
+    # a row that some lanes of a chunk see and others do not: NaN for those that see it, and only those
+    for which in range(2):
+        kv = Caches(dev, kind, S, R, n_kv, hd, 3)
+        (kv.k, kv.v)[which][2, 130, :hd] = float("nan")  # KV head 0 alone
+        c = Call(dev, len(pos), H, n_kv, hd)
+        c.lanes(kv, _i32(pos, dev), _i32(seqs, dev), W, sinks)
+        torch.cuda.synchronize()
+        got, q = c.out.cpu().numpy()[: len(pos)], c.q.cpu().numpy()
+        for i, (p, s) in enumerate(zip(pos, seqs)):
+            sees = s == 2 and 130 <= p < 130 + W
+            ref = _ref(q[i], *clean[s], p, W, sinks, n_kv)
+            _close(got[i, H // 2:], ref[H // 2:])
+            if sees:
+                assert np.isnan(got[i, : H // 2]).all(axis=-1 if which == 0 else None).all() or which == 1
+                assert np.isnan(got[i, : H // 2]).any(axis=-1).all()
+            else:
+                _close(got[i, : H // 2], ref[: H // 2])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_lanes_out_of_range(dev, kind):
+    # position and sequence out of range: zeros and the status bit; padding alone: zeros, no status
+    _check_lanes(dev, kind, 3, 40, 2, 1, 64, [39, 40, 5, -1, 5, 2147483647, 7], [0, 1, 3, 0, -1, 2, 2], 0, 0, status=1)
+    _check_lanes(dev, kind, 3, 40, 2, 1, 64, [-1, -5, -2147483648], [0, 99, -1], 0, 0)
+    c = Call(dev, 2, 2, 1, 64)
+    pre, kv = Caches(dev, kind, 2, 16, 1, 64), Caches(dev, kind, 2, 16, 1, 64)
+    for plen, pof, pos in [([17, 3], [0, 1], [4, 4]), ([-1, 3], [0, 1], [4, 4]), ([5, 3], [2, 1], [4, 4]),
+                           ([5, 3], [-1, 1], [4, 4]), ([5, 3], [0, 1], [21, 4])]:
+        c.status.zero_()
+        c.prefix(pre, _i32(plen, dev), _i32(pof, dev), kv, _i32(pos, dev), _i32([0, 1], dev))
+        got, q = c.result(1), c.q.cpu().numpy()
+        assert (got[0] == 0).all()
+        (pk, pv), (k, v) = pre.host(1), kv.host(1)
+        _close(got[1], _ref(q[1], np.concatenate([pk[:3], k]), np.concatenate([pv[:3], v]), 4, 0, 0, 1))
+
+
+def test_large_scores_and_equal_scores(dev):
+    # a running maximum that keeps rising, and rows whose weights are all equal
+    import torch
+
+    kv = Caches(dev, "f32", 2, 900, 1, 64, 5)
+    ramp = torch.arange(900, device=dev, dtype=torch.float32)[:, None] / 40.0
+    kv.k[0] = ramp * torch.ones((1, 64), device=dev) / 8.0
+    kv.k[1] = 0.0
+    c = Call(dev, 3, 1, 1, 64)
+    c.q[0] = 4.0
+    c.q[1] = -4.0
+    c.lanes(kv, _i32([899, 899, 899], dev), _i32([0, 0, 1], dev))
+    got, q = c.result(), c.q.cpu().numpy()
+    # scores up to 90 (all 64 products of one sign): half a step of 90 is 2^-18
+    ref = np.stack([_ref(q[i], *kv.host(s), 899, 0, 0, 1) for i, s in enumerate([0, 0, 1])])
+    e = np.linalg.norm(got - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+    assert e.max() <= 8 * 64 * 2.0 ** -24 * 90, e
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,n_kv,hd", [(1, 4, 1, 256), (4, 4, 1, 256), (16, 8, 2, 128), (64, 4, 1, 64), (5, 3, 3, 80)])
+@pytest.mark.parametrize("P", [0, 1, 127, 128, 700])
+def test_shared_prompt(dev, kind, B, H, n_kv, hd, P):
+    R = 40
+    pre, kv = Caches(dev, kind, 1, max(P, 1), n_kv, hd, 7), Caches(dev, kind, B, R, n_kv, hd, 8)
+    own = [(7 * i) % R for i in range(B)]  # own rows - 1
+    pos = [P + o for o in own]
+    if P > 5:
+        pos[0] = P - 5  # a lane that is still inside the prompt
+    c = Call(dev, B, H, n_kv, hd)
+    c.prefix(pre, _i32([P], dev), None, kv, _i32(pos, dev), _i32(np.arange(B), dev))
+    got, q = c.result(), c.q.cpu().numpy()
+    pk, pv = pre.host(0)
+    ref = []
+    for i in range(B):
+        k, v = kv.host(i)
+        ref.append(_ref(q[i], np.concatenate([pk[:P], k]), np.concatenate([pv[:P], v]), pos[i], 0, 0, n_kv))
+    _close(got, np.stack(ref))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 0), (30, 4), (200, 3), (150, 170), (1, 0)])
+def test_several_prompts(dev, kind, window, sinks):
+    # prompts of several lengths (one empty), lanes of one prompt beside each other and apart, chunks of
+    # one sequence behind a prompt, windows that end inside the prompt or behind it
+    plens = [160, 0, 37, 129]
+    pre, kv = Caches(dev, kind, 4, 160, 2, 64, 9), Caches(dev, kind, 9, 64, 2, 64, 10)
+    pof = [0, 0, 0, 3, 3, 1, 1, 2, 0, 2] + [3] * 30
+    seqs = [0, 1, 2, 3, 4, 5, 6, 7, 8, 7] + [4] * 30
+    own = [0, 9, 63, 40, 5, 3, 63, 20, 33, 21] + list(range(6, 36))
+    pos = [plens[f] + o for f, o in zip(pof, own)]
+    c = Call(dev, len(pos), 6, 2, 64)
+    c.prefix(pre, _i32(plens, dev), _i32(pof, dev), kv, _i32(pos, dev), _i32(seqs, dev), window, sinks)
+    got, q = c.result(), c.q.cpu().numpy()
+    ref = []
+    for i, (f, s, p) in enumerate(zip(pof, seqs, pos)):
+        (pk, pv), (k, v) = pre.host(f), kv.host(s)
+        n = plens[f]
+        ref.append(_ref(q[i], np.concatenate([pk[:n], k]), np.concatenate([pv[:n], v]), p, window, sinks, 2))
+    _close(got, np.stack(ref))
+
+
+def test_offsets_past_32_bits(dev):
+    # the second sequence starts more than 2^31 elements (2^32 bytes) behind the first
+    import torch
+
+    from weight_streaming_gemv_gb300 import qlin
+
+    rows, kvd, stride = 300, 64, (1 << 31) + 4096
+    buf = torch.empty(stride + 2 * rows * kvd, dtype=torch.bfloat16, device=dev)
+    view = lambda off: buf.as_strided((2, rows, kvd), (stride, kvd, 1), off)
+    k, v = view(0), view(rows * kvd)
+    for s in range(2):
+        k[s] = torch.randn((rows, kvd), device=dev).to(torch.bfloat16)
+        v[s] = torch.randn((rows, kvd), device=dev).to(torch.bfloat16)
+    c = Call(dev, 2, 2, 1, 64)
+    kv = type("K", (), {"c": qlin.kv_cache(k, v)})
+    c.lanes(kv, _i32([299, 150], dev), _i32([1, 0], dev))
+    got, q = c.result(), c.q.cpu().numpy()
+    f = lambda t, s: t[s].float().cpu().numpy().reshape(rows, 1, 64)
+    _close(got, np.stack([_ref(q[i], f(k, s), f(v, s), p, 0, 0, 1) for i, (p, s) in enumerate([(299, 1), (150, 0)])]))
+
+
+def test_captured_and_on_another_stream(dev):
+    import torch
+
+    kv = Caches(dev, "bf16", 4, 500, 1, 128, 11)
+    c = Call(dev, 4, 4, 1, 128)
+    pos, seqs = _i32([0, 0, 0, 0], dev), _i32([0, 1, 2, 3], dev)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        c.lanes(kv, pos, seqs, 100, 2, st)
+    st.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.lanes(kv, pos, seqs, 100, 2)
+        c.lanes(kv, pos, seqs, 100, 2)  # the same workspace twice in a row
+    q = c.q.cpu().numpy()
+    for ps in ([499, 3, 128, 250], [5, 499, 0, 127], [-1, 100, 101, 102]):
+        pos.copy_(_i32(ps, dev))
+        graph.replay()
+        got = c.result()
+        ref = np.stack([_ref(q[i], *kv.host(i), p, 100, 2, 1) if p >= 0 else np.zeros((4, 128)) for i, p in enumerate(ps)])
+        _close(got, ref)
+
+
+def test_same_inputs_same_bits(dev):
+    kv = Caches(dev, "f32", 8, 3000, 2, 128, 12)
+    c = Call(dev, 8, 8, 2, 128)
+    pos, seqs = _i32([2999, 100, 2000, 1500, 3, 2998, 640, 1], dev), _i32(np.arange(8), dev)
+    c.lanes(kv, pos, seqs)
+    first = c.result().copy()
+    for _ in range(3):
+        c.ws.random_(0, 255)
+        c.lanes(kv, pos, seqs)
+        np.testing.assert_array_equal(c.result(), first)

@@ -1,0 +1,618 @@
+// Beam search over many sequences: the selection over beams and vocabulary
+// (qlin_beam_select) and the reordering of the beams' states that follows it
+// (qlin_beam_reorder).
+//
+// Selection.  A live beam b of a group with running score s_b and logits x_b
+// offers the candidates c(b, v) = s_b + x_b[v] - lse_b, lse_b = log sum_v
+// exp(x_b[v]); a finished beam offers itself alone, with its score and the
+// end token.  The n largest of a group come out in descending order, ties to
+// the lower b * vocab + v.
+//
+// Two launches.  beam_slice_kernel reads every logit once: a CTA holds one
+// slice of one beam's row in registers, forms the slice's part of the sum and
+// finds its n largest logits (inside a beam the order of the candidates is the
+// order of the logits).  beam_merge_kernel, one CTA per group, adds the sums
+// up and merges the slices' sorted lists.  Bound by the logits' bytes from a
+// few rows on; below that by the two launches.
+//
+// Two beams' candidates can lie closer together than fp32 resolves, so lse
+// and the candidates are held in fp64.  The sum's parts are exact to scale: a
+// slice sums 2^(x log2(e) - e) with a whole number e that follows from its
+// largest logit, so slices are brought to one scale by powers of two.  (Logits
+// beyond 2^24, where masks of the type's lowest value lie, take the slice's
+// largest logit itself as the scale.)  Each term is one fp32 exp2 (relative error
+// about 2^-22, independent from term to term), summed in fp32 over a thread's
+// few values and in fp64 from there.
+//
+// Reordering.  new[b] = old[parent[b]] for every beam that does not keep its
+// place, in place: a CTA brings the same stretch of every beam that is wanted
+// elsewhere into shared memory by bulk copies, and once all have landed writes
+// it to every beam that takes it by bulk stores.  Stretches are disjoint, so
+// the order in which CTAs run does not matter, each wanted byte is read once,
+// and beams that stay cost nothing.
+#include "common.cuh"
+#include "stream.cuh"
+#include "tcgen05.cuh"
+
+namespace qlin {
+namespace {
+
+constexpr int kMaxBeams = 64;
+constexpr int kMaxOut = 128;
+
+// ---------------------------------------------------------------- selection
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBuf = 1024;  // candidates of a slice ranked in shared memory
+
+// fp32 as an unsigned whole number in the same order
+__device__ __forceinline__ uint32_t ord32(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float unord32(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+// larger value first, then the lower index
+__device__ __forceinline__ uint64_t cand_key(float v, uint32_t idx) { return ((uint64_t)ord32(v) << 32) | (uint32_t)~idx; }
+
+constexpr uint32_t kOrdNegInf = 0x007fffffu;  // ord32(-inf); anything above it is a candidate
+
+struct SelPart {  // a slice's part of its beam's sum of exponentials
+    double sum;  // times 2^sel_exp(m), or times exp(m) where sel_wide(m)
+    float m;     // the slice's largest logit
+    int count;   // candidates listed
+};
+constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.9259629911266175e-8f;
+__device__ __forceinline__ bool sel_wide(float m) { return !(fabsf(m) <= 16777216.0f); }
+__device__ __forceinline__ float sel_exp(float m) { return ceilf(__fmul_rn(m, kLog2eHi)); }
+
+struct SelWs {
+    SelPart *part;  // [rows][S]
+    uint64_t *cand; // [rows][S][n], descending keys
+    size_t bytes;
+};
+
+size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+SelWs carve_sel(int rows, int S, int n, char *base) {
+    SelWs w{};
+    const size_t a = align256(sizeof(SelPart) * (size_t)rows * S);
+    w.part = (SelPart *)base;
+    w.cand = (uint64_t *)(base ? base + a : nullptr);
+    w.bytes = a + align256(8 * (size_t)rows * S * n);
+    return w;
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *finished, int row) {
+    return !(finished && finished[row]) && scores[row] > -__int_as_float(0x7f800000);
+}
+
+// grid (S, rows).  Thread t holds VPT values of the slice [slice, slice + 256
+// VPT): 16-byte groups t, t + 256, ... with VEC (rows 16-byte aligned), single
+// values t, t + 256, ... without.
+template <int VPT, bool VEC>
+__global__ void __launch_bounds__(kSelThreads)
+    beam_slice_kernel(const float *__restrict__ logits, int64_t row_stride, const float *__restrict__ scores,
+                      const uint8_t *__restrict__ finished, int V, int n, SelPart *part, uint64_t *cand) {
+    __shared__ float wmax[kSelWarps];
+    __shared__ double wsum[kSelWarps];
+    __shared__ uint32_t wkth[kSelWarps];
+    __shared__ int count;
+    __shared__ uint64_t buf[kSelBuf];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = blockIdx.y, S = gridDim.x, sl = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!beam_live(scores, finished, row)) return;  // (the merge skips its parts)
+    const float ninf = -__int_as_float(0x7f800000);
+    const int v0 = sl * (kSelThreads * VPT);
+    const float *x = logits + (int64_t)row * row_stride;
+    float v[VPT];
+    auto index = [&](int j) { return VEC ? v0 + ((j >> 2) * kSelThreads + tid) * 4 + (j & 3) : v0 + j * kSelThreads + tid; };
+    if (tid == 0) count = 0;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int j = 0; j < VPT; j += 4) {
+            const int i = index(j);
+            float4 f = make_float4(ninf, ninf, ninf, ninf);
+            if (i + 3 < V) {
+                f = __ldcs(reinterpret_cast<const float4 *>(x + i));
+            } else {
+                if (i < V) f.x = x[i];
+                if (i + 1 < V) f.y = x[i + 1];
+                if (i + 2 < V) f.z = x[i + 2];
+            }
+            v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            const int i = index(j);
+            v[j] = i < V ? __ldcs(x + i) : ninf;
+        }
+    }
+    float tmax = ninf;
+#pragma unroll
+    for (int j = 0; j < VPT; j++) tmax = fmaxf(tmax, v[j]);
+    // the k-th largest of the warp's thread maxima, k = ceil(n / warps): at
+    // least n values of the slice are no smaller than the least of the warps'
+    uint32_t mine = ord32(tmax), kth = 0, wtop = 0;
+    const int k = (n + kSelWarps - 1) / kSelWarps;  // at most 16
+    for (int r = 0; r < k; r++) {
+        kth = __reduce_max_sync(0xffffffffu, mine);
+        if (r == 0) wtop = kth;
+        const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
+        if (lane == __ffs(who) - 1) mine = 0;
+    }
+    if (lane == 0) wmax[warp] = unord32(wtop), wkth[warp] = kth;
+    __syncthreads();
+    float m = wmax[0];
+    uint32_t thr = wkth[0];
+#pragma unroll
+    for (int w = 1; w < kSelWarps; w++) m = fmaxf(m, wmax[w]), thr = min(thr, wkth[w]);
+    const bool wide = sel_wide(m);
+    const float ef = sel_exp(m);
+    float s = 0.0f;
+    bool bad = false;  // NaN or +infinity: the beam's sum becomes NaN
+#pragma unroll
+    for (int j = 0; j < VPT; j++) {
+        // x log2(e) - e with log2(e) in two parts: the rounding of one would
+        // be the same for a whole beam
+        const float y = wide ? __fmul_rn(__fsub_rn(v[j], m), kLog2eHi)
+                             : __fmaf_rn(v[j], kLog2eLo, __fmaf_rn(v[j], kLog2eHi, -ef));
+        s += v[j] > ninf ? ex2_approx(y) : 0.0f;
+        bad |= !(v[j] < -ninf);
+    }
+    double d = bad ? (double)__int_as_float(0x7fc00000) : (double)s;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if (lane == 0) wsum[warp] = d;
+    // the values no smaller than the threshold
+    if (thr < kOrdNegInf + 1) thr = kOrdNegInf + 1;
+#pragma unroll
+    for (int j = 0; j < VPT; j++) {
+        const uint32_t o = ord32(v[j]);
+        if (o >= thr && v[j] == v[j]) {
+            const int at = atomicAdd(&count, 1);
+            if (at < kSelBuf) buf[at] = cand_key(v[j], (uint32_t)index(j));
+        }
+    }
+    __syncthreads();
+    int c = count;
+    if (c > kSelBuf) {
+        // many equal values: the n-th largest key bit by bit, then the n keys
+        // no smaller (keys are unique)
+        uint64_t t = 0;
+        for (int bit = 63; bit >= 0; bit--) {
+            const uint64_t tt = t | (1ull << bit);
+            int nn = 0;
+#pragma unroll
+            for (int j = 0; j < VPT; j++) nn += v[j] == v[j] && cand_key(v[j], (uint32_t)index(j)) >= tt;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) nn += __shfl_xor_sync(0xffffffffu, nn, off);
+            __syncthreads();
+            if (lane == 0) wkth[warp] = (uint32_t)nn;
+            __syncthreads();
+            nn = 0;
+#pragma unroll
+            for (int w = 0; w < kSelWarps; w++) nn += (int)wkth[w];
+            if (nn >= n) t = tt;
+        }
+        if (tid == 0) count = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            const uint64_t key = cand_key(v[j], (uint32_t)index(j));
+            if (v[j] == v[j] && key >= t) {
+                const int at = atomicAdd(&count, 1);
+                if (at < kSelBuf) buf[at] = key;
+            }
+        }
+        __syncthreads();
+        c = min(count, kSelBuf);
+    }
+    const int64_t ps = (int64_t)row * S + sl;
+    if (tid == 0) {
+        SelPart p;
+        p.sum = 0.0;
+#pragma unroll
+        for (int w = 0; w < kSelWarps; w++) p.sum += wsum[w];
+        p.m = m;
+        p.count = min(c, n);
+        part[ps] = p;
+    }
+    // a key's place is the number of larger ones
+    for (int i = tid; i < c; i += kSelThreads) {
+        const uint64_t key = buf[i];
+        int r = 0;
+        for (int q = 0; q < c; q++) r += buf[q] > key;
+        if (r < n) cand[ps * n + r] = key;
+    }
+}
+
+constexpr int kMergeThreads = 512;
+constexpr int kOnly = 255;  // above kMaxOut
+
+__device__ __forceinline__ bool better(double c, int64_t at, double bc, int64_t bat) {
+    return c > bc || (c == bc && at < bat);
+}
+
+// One CTA per group: lse of every live beam, then n rounds of taking the best
+// head of the beams' sorted lists (S lists per live beam, one entry for a
+// finished one).
+__global__ void __launch_bounds__(kMergeThreads)
+    beam_merge_kernel(const SelPart *__restrict__ part, const uint64_t *__restrict__ cand,
+                      const float *__restrict__ scores, const uint8_t *__restrict__ finished, int eos, int beams, int V,
+                      int S, int n, float *out_scores, int32_t *parents, int32_t *tokens) {
+    __shared__ double lse[kMaxBeams];  // the log of a beam's sum, less top
+    __shared__ float top[kMaxBeams];   // its largest logit
+    __shared__ double wc[kMergeThreads / 32];
+    __shared__ int64_t wat[kMergeThreads / 32];
+    __shared__ int wlist[kMergeThreads / 32];
+    __shared__ int won;
+    extern __shared__ uint8_t heads[];  // [beams * S]: the next entry of each list (kOnly: the beam itself)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float ninf = -__int_as_float(0x7f800000);
+    const double dninf = (double)ninf;
+    for (int b = warp; b < beams; b += kMergeThreads / 32) {
+        const int row = g * beams + b;
+        double l = 0.0;
+        float big = ninf;
+        if (beam_live(scores, finished, row)) {
+            const SelPart *p = part + (int64_t)row * S;
+            for (int i = lane; i < S; i += 32) big = fmaxf(big, __ldcg(&p[i].m));
+            big = warp_max(big);
+            const double M = (double)big, E = (double)sel_exp(big);
+            const double ln2 = 0.69314718055994530942;
+            double s = 0.0;
+            for (int i = lane; i < S; i += 32) {
+                const float mi = __ldcg(&p[i].m);
+                const double si = __ldcg(&p[i].sum);
+                if (!sel_wide(big)) {  // (a wide slice is below every other one here: nothing, or NaN)
+                    const int sh = sel_wide(mi) ? -1000 : max((int)(sel_exp(mi) - (float)E), -1000);
+                    s += si * __hiloint2double((sh + 1023) << 20, 0);
+                } else if (mi > ninf) {
+                    s += si * exp((sel_wide(mi) ? (double)mi : (double)sel_exp(mi) * ln2) - M);
+                } else {
+                    s += si;  // 0, or NaN
+                }
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            l = log(s) + (sel_wide(big) ? 0.0 : E * ln2 - M);
+        }
+        if (lane == 0) lse[b] = l, top[b] = big;
+    }
+    const int lists = beams * S;
+    for (int i = tid; i < lists; i += kMergeThreads) {
+        const int row = g * beams + i / S;
+        // a list that has nothing starts behind its end
+        heads[i] = beam_live(scores, finished, row) ? 0 : (finished && finished[row] && i % S == 0) ? kOnly : n;
+    }
+    __syncthreads();
+    // the head of list i
+    auto head = [&](int i, double &c, int64_t &at) {
+        const int b = i / S, row = g * beams + b, h = heads[i];
+        c = dninf, at = INT64_MAX;
+        if (h == kOnly) {
+            c = (double)scores[row];
+            at = (int64_t)b * V + eos;
+        } else if (h < n && h < __ldcg(&part[(int64_t)row * S + i % S].count)) {
+            const uint64_t k = __ldcg(&cand[((int64_t)row * S + i % S) * n + h]);
+            c = (double)scores[row] + (((double)unord32((uint32_t)(k >> 32)) - (double)top[b]) - lse[b]);
+            at = (int64_t)b * V + (uint32_t)~(uint32_t)k;
+        }
+        if (!(c > dninf)) c = dninf, at = INT64_MAX;  // NaN: nothing of this beam
+    };
+    double mc = dninf;
+    int64_t mat = INT64_MAX;
+    int mlist = -1;
+    auto rescan = [&]() {
+        mc = dninf, mat = INT64_MAX, mlist = -1;
+        for (int i = tid; i < lists; i += kMergeThreads) {
+            double c;
+            int64_t at;
+            head(i, c, at);
+            if (better(c, at, mc, mat)) mc = c, mat = at, mlist = i;
+        }
+    };
+    rescan();
+    for (int r = 0; r < n; r++) {
+        double c = mc;
+        int64_t at = mat;
+        int li = mlist;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const double oc = __shfl_xor_sync(0xffffffffu, c, off);
+            const int64_t oat = __shfl_xor_sync(0xffffffffu, at, off);
+            const int ol = __shfl_xor_sync(0xffffffffu, li, off);
+            if (better(oc, oat, c, at)) c = oc, at = oat, li = ol;
+        }
+        if (lane == 0) wc[warp] = c, wat[warp] = at, wlist[warp] = li;
+        __syncthreads();
+        if (warp == 0) {
+            c = lane < kMergeThreads / 32 ? wc[lane] : dninf;
+            at = lane < kMergeThreads / 32 ? wat[lane] : INT64_MAX;
+            li = lane < kMergeThreads / 32 ? wlist[lane] : -1;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                const double oc = __shfl_xor_sync(0xffffffffu, c, off);
+                const int64_t oat = __shfl_xor_sync(0xffffffffu, at, off);
+                const int ol = __shfl_xor_sync(0xffffffffu, li, off);
+                if (better(oc, oat, c, at)) c = oc, at = oat, li = ol;
+            }
+            if (lane == 0) {
+                const bool none = at == INT64_MAX;
+                const int64_t o = (int64_t)g * n + r;
+                out_scores[o] = none ? ninf : (float)c;
+                parents[o] = none ? -1 : (int)(at / V);
+                tokens[o] = none ? -1 : (int)(at % V);
+                won = none ? -1 : li;
+                if (!none) heads[li] = heads[li] == kOnly ? n : heads[li] + 1;
+            }
+        }
+        __syncthreads();
+        if (won == mlist && won >= 0) rescan();
+    }
+}
+
+// ---------------------------------------------------------------- reordering
+constexpr int kRoStages = 3;
+constexpr int kRoSmem = 192 * 1024;  // the stages' bytes
+constexpr int kRoMaxChunk = 16384, kRoMinChunk = 1024;
+
+struct RoArgs {
+    char *cache;
+    int64_t seq_stride, plane_stride;
+    int n_planes;
+    int64_t row_bytes;
+    int max_rows;
+    const int32_t *parents;
+    const int32_t *rows;
+    int n_groups, beams;
+    int32_t *status;
+};
+
+// One warp per CTA: the copies need no other threads.  CTA c takes the items
+// c, c + grid, ... of every group; an item is one stretch of at most `chunk`
+// bytes of one plane, of every beam.
+__global__ void __launch_bounds__(32) beam_reorder_kernel(RoArgs A) {
+    extern __shared__ __align__(128) uint8_t ro_smem[];
+    __shared__ uint64_t full[kRoStages];
+    __shared__ int src[kMaxBeams];        // slot -> source beam
+    __shared__ int slot_of[kMaxBeams];    // source beam -> slot
+    __shared__ int dst[kMaxBeams];        // moved beams
+    __shared__ int dst_slot[kMaxBeams];
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        for (int s = 0; s < kRoStages; s++) mbar_init(&full[s], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int filled = 0;  // stages filled so far: fill f uses stage f % kRoStages
+    bool ok = true;
+    int64_t skip = blockIdx.x;  // items until this CTA's next one
+    for (int g = 0; g < A.n_groups && ok; g++) {
+        const int nrows = A.rows ? min(max(A.rows[g], 0), A.max_rows) : A.max_rows;
+        // moved beams and the distinct beams they take
+        uint64_t want = 0;
+        int nd = 0;
+        for (int b0 = 0; b0 < A.beams; b0 += 32) {
+            const int b = b0 + lane;
+            const int p = b < A.beams ? A.parents[(int64_t)g * A.beams + b] : -1;
+            const bool moved = p >= 0 && p < A.beams && p != b;
+            const uint32_t bal = __ballot_sync(0xffffffffu, moved);
+            if (moved) {
+                const int at = nd + __popc(bal & ((1u << lane) - 1u));
+                dst[at] = b;
+                dst_slot[at] = p;  // the beam for now
+            }
+            nd += __popc(bal);
+            uint64_t w = moved ? 1ull << p : 0ull;
+            w = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)w) |
+                (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(w >> 32)) << 32;
+            want |= w;
+        }
+        const int ns = __popcll(want);
+        if (ns == 0 || nrows == 0) continue;
+        __syncwarp();
+        for (int b = lane; b < A.beams; b += 32)
+            if (want >> b & 1) {
+                const int sidx = __popcll(want & ((1ull << b) - 1ull));
+                src[sidx] = b;
+                slot_of[b] = sidx;
+            }
+        __syncwarp();
+        for (int i = lane; i < nd; i += 32) dst_slot[i] = slot_of[dst_slot[i]];
+        __syncwarp();
+        const int64_t plane = (int64_t)nrows * A.row_bytes;
+        // as much of a stage as the sources fill, but enough items for every CTA
+        const int64_t even = (plane * A.n_planes / gridDim.x + 127) / 128 * 128;
+        const int cap = (int)min((int64_t)min(kRoMaxChunk, kRoSmem / kRoStages / ns / 128 * 128),
+                                 max(even, (int64_t)kRoMinChunk));
+        const int64_t parts = (plane + cap - 1) / cap;
+        const int chunk = (int)((plane + parts * 16 - 1) / (parts * 16) * 16);
+        const int64_t per = (plane + chunk - 1) / chunk;
+        const int64_t items = (int64_t)A.n_planes * per;
+        char *base = A.cache + (int64_t)g * A.beams * A.seq_stride;
+        if (skip >= items) {
+            skip -= items;
+            continue;
+        }
+        const int64_t mine = (items - skip + gridDim.x - 1) / gridDim.x;
+        auto where = [&](int64_t k, int64_t &off, uint32_t &bytes) {
+            const int64_t it = skip + k * gridDim.x, pl = it / per, at = (it - pl * per) * chunk;
+            off = pl * A.plane_stride + at;
+            bytes = (uint32_t)min((int64_t)chunk, plane - at);
+        };
+        auto load = [&](int64_t k, int f) {
+            int64_t off;
+            uint32_t bytes;
+            where(k, off, bytes);
+            const int st = f % kRoStages;
+            uint8_t *to = ro_smem + (size_t)st * (kRoSmem / kRoStages);
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes * (uint32_t)ns);
+            __syncwarp();
+            for (int i = lane; i < ns; i += 32)
+                bulk_g2s_l2(to + (size_t)i * chunk, base + (int64_t)src[i] * A.seq_stride + off, bytes, &full[st]);
+        };
+        const int f0 = filled;
+        for (int64_t k = 0; k < min((int64_t)kRoStages - 1, mine); k++) load(k, f0 + (int)k);
+        for (int64_t k = 0; k < mine; k++) {
+            const int f = f0 + (int)k, st = f % kRoStages;
+            if (__any_sync(0xffffffffu, !mbar_wait(&full[st], (uint32_t)(f / kRoStages) & 1u))) {
+                if (lane == 0) raise_status(A.status, kStatusTimeout);
+                for (int64_t j = k + 1; j < min(k + kRoStages - 1, mine); j++)  // the copies behind it
+                    mbar_wait(&full[(f0 + (int)j) % kRoStages], (uint32_t)((f0 + (int)j) / kRoStages) & 1u);
+                ok = false;
+                break;
+            }
+            int64_t off;
+            uint32_t bytes;
+            where(k, off, bytes);
+            const uint8_t *from = ro_smem + (size_t)st * (kRoSmem / kRoStages);
+            for (int i = lane; i < nd; i += 32)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                 base + (int64_t)dst[i] * A.seq_stride + off),
+                             "r"(smem_addr(from + (size_t)dst_slot[i] * chunk)), "r"(bytes)
+                             : "memory");
+            bulk_commit_group();
+            // the stage of item k - 1 takes item k + stages - 1 once its stores have read it
+            if (k + kRoStages - 1 < mine) {
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                __syncwarp();
+                load(k + kRoStages - 1, f + kRoStages - 1);
+            }
+        }
+        filled = f0 + (int)mine;
+        bulk_wait_read_all();
+        __syncwarp();
+        skip = (skip + mine * gridDim.x) - items;
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// Values per thread of a slice: the largest slice that still gives two CTAs
+// per SM, so that a few rows are read by all SMs.
+int sel_vpt(int rows, int V) {
+    for (int vpt : {32, 16, 8})
+        if ((int64_t)rows * ((V + kSelThreads * vpt - 1) / (kSelThreads * vpt)) >= 2 * 152) return vpt;
+    return 4;
+}
+int sel_slices(int rows, int V) {
+    const int per = kSelThreads * sel_vpt(rows, V);
+    return (V + per - 1) / per;
+}
+
+template <int VPT>
+const void *slice_kernel(bool vec) {
+    return vec ? (const void *)beam_slice_kernel<VPT, true> : (const void *)beam_slice_kernel<VPT, false>;
+}
+
+bool sel_sizes_ok(int n_groups, int beams, int vocab, int n_out) {
+    return n_groups >= 1 && beams >= 1 && beams <= kMaxBeams && vocab >= 1 && vocab <= (1 << 24) && n_out >= 1 &&
+           n_out <= kMaxOut && (int64_t)n_groups * beams <= 65535;
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" {
+
+size_t qlin_beam_select_workspace_size(int n_groups, int beams, int vocab, int n_out) {
+    if (!sel_sizes_ok(n_groups, beams, vocab, n_out)) return 0;
+    const int rows = n_groups * beams;
+    return carve_sel(rows, sel_slices(rows, vocab), n_out, nullptr).bytes;
+}
+
+qlin_status qlin_beam_select(const float *logits, int64_t row_stride, const float *scores, const uint8_t *finished,
+                             int eos, int n_groups, int beams, int vocab, int n_out, float *out_scores,
+                             int32_t *parents, int32_t *tokens, void *workspace, size_t workspace_bytes,
+                             qlin_stream_t stream) {
+    qlin::clear_error();
+    QLIN_REQUIRE(logits && scores && out_scores && parents && tokens && workspace, QLIN_ERR_INVALID_ARG,
+                 "qlin_beam_select: null pointer");
+    QLIN_REQUIRE(n_groups >= 1 && beams >= 1 && vocab >= 1 && n_out >= 1, QLIN_ERR_INVALID_ARG,
+                 "qlin_beam_select: n_groups %d, beams %d, vocab %d, n_out %d", n_groups, beams, vocab, n_out);
+    QLIN_REQUIRE(sel_sizes_ok(n_groups, beams, vocab, n_out), QLIN_ERR_UNSUPPORTED,
+                 "qlin_beam_select: at most %d beams, %d outputs, %d words and 65535 rows (%d groups of %d, %d, %d)",
+                 kMaxBeams, kMaxOut, 1 << 24, n_groups, beams, n_out, vocab);
+    QLIN_REQUIRE(row_stride >= vocab, QLIN_ERR_INVALID_ARG, "qlin_beam_select: row_stride %lld < vocab %d",
+                 (long long)row_stride, vocab);
+    QLIN_REQUIRE(!finished || (eos >= 0 && eos < vocab), QLIN_ERR_INVALID_ARG,
+                 "qlin_beam_select: eos %d outside the vocabulary", eos);
+    QLIN_REQUIRE(aligned4(logits) && aligned4(scores) && aligned4(out_scores) && aligned4(parents) && aligned4(tokens),
+                 QLIN_ERR_INVALID_ARG, "qlin_beam_select: pointer not 4-byte aligned");
+    QLIN_REQUIRE(aligned16(workspace), QLIN_ERR_INVALID_ARG, "qlin_beam_select: workspace not 16-byte aligned");
+    const int rows = n_groups * beams, S = sel_slices(rows, vocab);
+    const SelWs w = carve_sel(rows, S, n_out, (char *)workspace);
+    QLIN_REQUIRE(workspace_bytes >= w.bytes, QLIN_ERR_INVALID_ARG, "qlin_beam_select: workspace %zu < %zu bytes",
+                 workspace_bytes, w.bytes);
+    const bool vec = aligned16(logits) && row_stride % 4 == 0;
+    const void *k = nullptr;
+    switch (sel_vpt(rows, vocab)) {
+        case 32: k = slice_kernel<32>(vec); break;
+        case 16: k = slice_kernel<16>(vec); break;
+        case 8: k = slice_kernel<8>(vec); break;
+        default: k = slice_kernel<4>(vec); break;
+    }
+    void *a0[] = {(void *)&logits, (void *)&row_stride, (void *)&scores, (void *)&finished, (void *)&vocab,
+                  (void *)&n_out, (void *)&w.part, (void *)&w.cand};
+    if (qlin_status st = launch_pdl(k, dim3(S, rows), dim3(kSelThreads), 0, (cudaStream_t)stream, a0,
+                                    "beam_slice_kernel"))
+        return st;
+    void *a1[] = {(void *)&w.part, (void *)&w.cand, (void *)&scores, (void *)&finished, (void *)&eos, (void *)&beams,
+                  (void *)&vocab, (void *)&S, (void *)&n_out, (void *)&out_scores, (void *)&parents, (void *)&tokens};
+    const size_t smem = (size_t)beams * S;
+    if (smem > 40 * 1024) blocks_per_sm((const void *)beam_merge_kernel, smem);  // raises the limit once
+    return launch_pdl((const void *)beam_merge_kernel, dim3(n_groups), dim3(kMergeThreads), smem, (cudaStream_t)stream,
+                      a1, "beam_merge_kernel");
+}
+
+qlin_status qlin_beam_reorder(void *cache, int64_t seq_stride, int64_t plane_stride, int n_planes, int64_t row_bytes,
+                              int max_rows, const int32_t *parents, const int32_t *n_rows, int n_groups, int beams,
+                              int32_t *status_word, qlin_stream_t stream) {
+    qlin::clear_error();
+    QLIN_REQUIRE(cache && parents, QLIN_ERR_INVALID_ARG, "qlin_beam_reorder: null pointer");
+    QLIN_REQUIRE(n_planes >= 1 && max_rows >= 1 && n_groups >= 1 && beams >= 1 && row_bytes >= 16, QLIN_ERR_INVALID_ARG,
+                 "qlin_beam_reorder: n_planes %d, max_rows %d, n_groups %d, beams %d, row_bytes %lld", n_planes,
+                 max_rows, n_groups, beams, (long long)row_bytes);
+    QLIN_REQUIRE(beams <= kMaxBeams, QLIN_ERR_UNSUPPORTED, "qlin_beam_reorder: %d beams, at most %d", beams, kMaxBeams);
+    QLIN_REQUIRE(aligned16(cache) && row_bytes % 16 == 0 && seq_stride % 16 == 0 && plane_stride % 16 == 0,
+                 QLIN_ERR_INVALID_ARG, "qlin_beam_reorder: cache, row_bytes and strides are multiples of 16 bytes");
+    QLIN_REQUIRE(row_bytes <= (int64_t)1 << 40 && seq_stride >= 0 && seq_stride <= (int64_t)1 << 46 &&
+                     plane_stride >= 0 && plane_stride <= (int64_t)1 << 46,
+                 QLIN_ERR_INVALID_ARG, "qlin_beam_reorder: a stride is out of range");
+    // every beam's rows are its own: planes inside a sequence, or sequences inside a plane
+    const __int128 plane = (__int128)row_bytes * max_rows, seqs = (__int128)n_groups * beams;
+    const bool seq_major = (n_planes == 1 || plane_stride >= plane) &&
+                           (seqs == 1 || seq_stride >= (__int128)plane_stride * (n_planes - 1) + plane);
+    const bool plane_major = (seqs == 1 || seq_stride >= plane) &&
+                             (n_planes == 1 || plane_stride >= (__int128)seq_stride * (seqs - 1) + plane);
+    QLIN_REQUIRE(seq_major || plane_major, QLIN_ERR_INVALID_ARG, "qlin_beam_reorder: the beams' rows overlap");
+    QLIN_REQUIRE(aligned4(parents) && aligned4(n_rows) && aligned4(status_word), QLIN_ERR_INVALID_ARG,
+                 "qlin_beam_reorder: pointer not 4-byte aligned");
+    QLIN_REQUIRE(kRoSmem + 1024 <= max_smem_optin(), QLIN_ERR_UNSUPPORTED, "qlin_beam_reorder: shared memory");
+    blocks_per_sm((const void *)beam_reorder_kernel, kRoSmem);  // raises the limit once
+    RoArgs A{(char *)cache, seq_stride, plane_stride, n_planes, row_bytes, max_rows, parents, n_rows, n_groups, beams,
+             status_word};
+    void *args[] = {(void *)&A};
+    return launch_pdl((const void *)beam_reorder_kernel, dim3(sm_count()), dim3(32), kRoSmem, (cudaStream_t)stream, args,
+                      "beam_reorder_kernel");
+}
+
+}  // extern "C"

@@ -51,6 +51,18 @@ class T158SketchC(ctypes.Structure):
     ]
 
 
+class QlinKvC(ctypes.Structure):
+    """Mirror of ``qlin_kv``."""
+
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("seq_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64), ("n_seqs", ctypes.c_int32), ("rows", ctypes.c_int32),
+        ("type", ctypes.c_int32), ("reserved0", ctypes.c_int32),
+    ]
+
+
+KV_F32, KV_BF16 = 0, 1
+
 _P, _I, _I64, _F, _D, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double,
                              ctypes.c_size_t)
 _ST = ctypes.c_int
@@ -110,6 +122,13 @@ SIGNATURES = {
     "decode_lanes_t158_launches": ([ctypes.POINTER(T158ModelC), _I], _I),
     "decode_lanes_t158_status": ([_P, _P], _ST),
     "decode_step_t158_sketch_status": ([ctypes.POINTER(T158ModelC), ctypes.POINTER(T158SketchC), _P, _P], _ST),
+    "qlin_attention_lanes_workspace_size": ([_I, _I, _I, _I], _SZ),
+    "qlin_attention_lanes": ([_P, ctypes.POINTER(QlinKvC), _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P], _ST),
+    "qlin_attention_prefix": ([_P, ctypes.POINTER(QlinKvC), _P, _P, ctypes.POINTER(QlinKvC), _P, _P, _I, _I, _I, _I,
+                               _I, _I, _P, _P, _P, _SZ, _P], _ST),
+    "qlin_beam_select_workspace_size": ([_I, _I, _I, _I], _SZ),
+    "qlin_beam_select": ([_P, _I64, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P], _ST),
+    "qlin_beam_reorder": ([_P, _I64, _I64, _I, _I64, _I, _P, _P, _I, _I, _P, _P], _ST),
 }
 
 
@@ -421,3 +440,56 @@ def qlin_t158_i8_skip(xq, x_scale, w_groups, gpitch, w_scale, y, acc, N, K, work
     _check("qlin_t158_i8_skip", lib().qlin_t158_i8_skip(_ptr(xq), _ptr(x_scale), _ptr(w_groups), gpitch, w_scale,
                                                         _ptr(y), _ptr(acc), N, K, _ptr(workspace), workspace_bytes,
                                                         _stream(stream)))
+
+
+def kv_cache(k, v) -> QlinKvC:
+    """The ``qlin_kv`` of two tensors [n_seqs][rows][n_kv * head_dim] (float32, bfloat16, or int16 holding bf16
+    bits; any strides but the last's), which the caller keeps."""
+    if k.dim() != 3 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(2) != 1:
+        raise ValueError("kv_cache: k and v are [n_seqs][rows][n_kv * head_dim] tensors of one shape, type and "
+                         "strides, the last axis contiguous")
+    kinds = {"torch.float32": KV_F32, "torch.bfloat16": KV_BF16, "torch.int16": KV_BF16}
+    if str(k.dtype) not in kinds:
+        raise ValueError(f"kv_cache: type {k.dtype}")
+    c = QlinKvC()
+    c.k, c.v, c.type = k.data_ptr(), v.data_ptr(), kinds[str(k.dtype)]
+    c.seq_stride, c.row_stride = k.stride(0), k.stride(1)
+    c.n_seqs, c.rows = k.shape[0], k.shape[1]
+    return c
+
+
+def qlin_attention_lanes_workspace_size(n_lanes, n_heads, n_kv, head_dim) -> int:
+    return int(lib().qlin_attention_lanes_workspace_size(n_lanes, n_heads, n_kv, head_dim))
+
+
+def qlin_attention_lanes(q, kv: QlinKvC, positions, seqs, n_lanes, n_heads, n_kv, head_dim, window, sinks, out,
+                         status_word, workspace, workspace_bytes, stream=None):
+    _check("qlin_attention_lanes", lib().qlin_attention_lanes(
+        _ptr(q), ctypes.byref(kv), _ptr(positions), _ptr(seqs), n_lanes, n_heads, n_kv, head_dim, window, sinks,
+        _ptr(out), _ptr(status_word), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qlin_attention_prefix(q, prefix: QlinKvC, prefix_len, prefix_of, kv: QlinKvC, positions, seqs, n_lanes, n_heads,
+                          n_kv, head_dim, window, sinks, out, status_word, workspace, workspace_bytes, stream=None):
+    _check("qlin_attention_prefix", lib().qlin_attention_prefix(
+        _ptr(q), ctypes.byref(prefix), _ptr(prefix_len), _ptr(prefix_of), ctypes.byref(kv), _ptr(positions),
+        _ptr(seqs), n_lanes, n_heads, n_kv, head_dim, window, sinks, _ptr(out), _ptr(status_word), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def qlin_beam_select_workspace_size(n_groups, beams, vocab, n_out) -> int:
+    return int(lib().qlin_beam_select_workspace_size(n_groups, beams, vocab, n_out))
+
+
+def qlin_beam_select(logits, row_stride, scores, finished, eos, n_groups, beams, vocab, n_out, out_scores, parents,
+                     tokens, workspace, workspace_bytes, stream=None):
+    _check("qlin_beam_select", lib().qlin_beam_select(
+        _ptr(logits), row_stride, _ptr(scores), _ptr(finished), eos, n_groups, beams, vocab, n_out, _ptr(out_scores),
+        _ptr(parents), _ptr(tokens), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qlin_beam_reorder(cache, seq_stride, plane_stride, n_planes, row_bytes, max_rows, parents, n_rows, n_groups,
+                      beams, status_word=None, stream=None):
+    _check("qlin_beam_reorder", lib().qlin_beam_reorder(
+        _ptr(cache), seq_stride, plane_stride, n_planes, row_bytes, max_rows, _ptr(parents), _ptr(n_rows), n_groups,
+        beams, _ptr(status_word), _stream(stream)))
