@@ -519,7 +519,8 @@ qlin_status decode_lanes_t158_status(void *workspace, qlin_stream_t stream);
  * r of sequence s is the head_dim values at
  * k + s * seq_stride + r * row_stride + g * head_dim (strides in elements; v
  * alike).  k and v are device pointers, 16-byte aligned, both strides
- * multiples of 16 bytes and below 2^40 bytes, row_stride >= n_kv * head_dim.
+ * multiples of 16 bytes and below 2^40 bytes, row_stride >= n_kv * head_dim;
+ * rows is at most 2^30.
  * type: fp32, or bf16 (bits).  A layer of decode_lanes_t158's caches is
  * {kv_caches + (2 layer) * max_pos * kv_dim, kv_caches + (2 layer + 1) *
  * max_pos * kv_dim, 2 n_layers max_pos kv_dim, kv_dim, n_seqs, max_pos,
