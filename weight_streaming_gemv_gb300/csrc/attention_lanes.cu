@@ -24,24 +24,29 @@
 // accumulated (three for a bf16 cache, six for an fp32 one; what is left out
 // is below 2^-24 of the product).
 //
-// A pass over the keys with a running maximum: thread t of four warps owns key
-// t of a 128-key chunk (a tensor-memory lane).  The maximum of a row is over
-// threads, so it is only taken when some score exceeds the one in use by 2^8
-// (and for a tile's first chunk): otherwise weights relative to the maximum in
-// use stay below 2^8 and nothing needs rescaling.  The sums stay in each
-// thread's registers until the end.
+// A pass over the keys with a running maximum: the rows go to warpgroups, 16
+// each, and thread t of one owns key t of a 128-key chunk (a tensor-memory
+// lane).  The maximum of a row is over threads, so it is only taken when some
+// score exceeds the one in use by 2^8 (and for a tile's first chunk):
+// otherwise weights relative to the maximum in use stay below 2^8 and nothing
+// needs rescaling.  The sums stay in each thread's registers until the end,
+// and so do the outputs: the tensor cores' accumulation rounds toward zero, so
+// they sum over one chunk only, and a score's main products (hi x hi) are
+// summed apart from the small ones.
 //
 // Work is dealt out by 128-key chunks: every CTA (one per SM) takes an equal
 // run of the (tile, KV head, chunk) units, so a long sequence is split over
 // many SMs and many short ones are packed, whatever the lengths, which are
 // read on the device.  A tile that lies in one CTA is finished there; the
-// others leave partial sums that a second kernel merges.  A planning kernel
-// finds the tiles first.
+// others leave partial sums that a second kernel merges.  Up to 64 lanes every
+// CTA plans for itself (one warp, a lane or two per thread); from there a
+// kernel of one CTA plans once for all.
 //
-// Keys and values go through a ring of 16 KB slots (x 3 terms): 128 keys x 64
-// dims of K, 64 keys x 128 dims of V.  A bf16 cache's are tensor copies (TMA,
-// 128-byte swizzle) straight from the cache; an fp32 cache's are loaded, split
-// and stored by eight warps.
+// Keys and values go through a ring of 16 KB slots (x 3 terms for an fp32
+// cache): 128 keys x 64 dims of K, 64 keys x 128 dims of V.  The shared memory
+// that the plan's widest tile leaves is ring.  A bf16 cache's are tensor
+// copies (TMA, 128-byte swizzle) straight from the cache; an fp32 cache's are
+// loaded, split and stored by eight warps.
 //
 // Rows that nobody in the tile may see (behind the last position, before the
 // window) are set to zero before their product, and a value that only some
@@ -91,7 +96,8 @@ static_assert(sizeof(AlTile) == 64, "tiles are loaded 16 bytes at a time");
 
 struct AlPlanHead {
     int64_t units;
-    int64_t grid;  // CTAs with work: the launch's, or one per unit if there are fewer
+    int grid;  // CTAs with work: the launch's, or one per unit if there are fewer
+    int rmax;  // rows of the widest tile
 };
 
 struct AlWs {
@@ -113,6 +119,7 @@ struct AlDims {
     int cap;    // partial rows per slot
     int streams;  // 1: own caches only, 2
     int grid;
+    int merge;  // (lane, head)s per block of the merging kernel
     float c;    // log2(e) / sqrt(hd)
 };
 
@@ -124,51 +131,56 @@ __device__ __forceinline__ float al_ex2(float x) {
 
 // ------------------------------------------------------------------ the plan
 constexpr int kPlanThreads = 1024, kPlanPer = kMaxLanes / kPlanThreads;
+constexpr int kSelfPlan = 64;  // lanes up to which every CTA plans for itself, on one warp
 
-// Inclusive scans over the block (every thread calls them).
-__device__ __forceinline__ int plan_scan_max(int v, int *red) {
+struct AlSelfPlan {  // in shared memory
+    AlPlanHead head;
+    AlTile tiles[2 * kSelfPlan];
+    int first;
+};
+struct AlSelfScratch {
+    int tile_of[2 * kSelfPlan];
+    int pos[kSelfPlan], seq[kSelfPlan], pre[kSelfPlan];
+};
+
+// Scans over T consecutive threads (a warp, or a whole block; all call them):
+// the reduction of the threads before this one, and of all.
+template <int T, bool MAX>
+__device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t init, int64_t *red, int64_t &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t in = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v = max(v, o);
+        const int64_t o = __shfl_up_sync(0xffffffffu, in, off);
+        if (lane >= off) in = MAX ? max(in, o) : in + o;
+    }
+    int64_t ex = __shfl_up_sync(0xffffffffu, in, 1);
+    if (lane == 0) ex = init;
+    if (T == 32) {
+        total = __shfl_sync(0xffffffffu, in, 31);
+        return ex;
     }
     __syncthreads();
-    if (lane == 31) red[warp] = v;
+    if (lane == 31) red[warp] = in;
     __syncthreads();
-    int before = -1;
-    for (int w = 0; w < warp; w++) before = max(before, red[w]);
-    return max(v, before);
-}
-__device__ __forceinline__ int64_t plan_scan_sum(int64_t v, int64_t *red, int64_t &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += o;
+    total = init;
+    for (int w = 0; w < T / 32; w++) {
+        if (w == warp) ex = MAX ? max(ex, total) : ex + total;
+        total = MAX ? max(total, red[w]) : total + red[w];
     }
-    __syncthreads();
-    if (lane == 31) red[warp] = v;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < kPlanThreads / 32; w++) {
-        if (w < warp) before += red[w];
-        total += red[w];
-    }
-    return v + before;
+    return ex;
 }
 
-// One CTA: checks the lanes, cuts them into tiles and deals the units out.
-__global__ void __launch_bounds__(kPlanThreads) al_plan_kernel(AlArgs A, AlDims D, AlWs W) {
-    extern __shared__ int pl_smem[];  // [3][n]: position (-1: no lane), sequence, prompt
-    __shared__ int redi[32];
-    __shared__ int64_t redl[32];
-    const int tid = threadIdx.x, n = A.n_lanes;
-    int *spos = pl_smem, *sseq = spos + n, *spre = sseq + n;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = tid; i < n; i += kPlanThreads) {
+// Checks the lanes, cuts them into tiles and deals the units out.  T threads
+// (T == 32: one warp) with PER consecutive lanes each; spos (-1: no lane),
+// sseq, spre: [n_lanes] scratch.  first: the first tile of CTA `cta`, or of
+// every CTA if that is negative.
+template <int T, int PER>
+__device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int *spos, int *sseq, int *spre, int64_t *red,
+                                          AlPlanHead *head, int *first, int cta, int *tile_of, AlTile *tiles_out,
+                                          int32_t *status) {
+    const int tid = T == 32 ? (int)(threadIdx.x & 31) : (int)threadIdx.x, n = A.n_lanes;
+    for (int i = tid; i < n; i += T) {
         const int p = A.positions[i], s = A.seqs[i];
         int f = 0, P = 0;
         bool ok = s >= 0 && s < A.own.n_seqs;
@@ -179,97 +191,128 @@ __global__ void __launch_bounds__(kPlanThreads) al_plan_kernel(AlArgs A, AlDims 
             ok = ok && P >= 0 && P <= A.pre.rows;
         }
         ok = ok && p - P < A.own.rows;
-        if (p >= 0 && !ok) raise_status(A.status, kStatusBadLane);
+        if (p >= 0 && !ok) raise_status(status, kStatusBadLane);
         spos[i] = p >= 0 && ok ? p : -1;
         sseq[i] = s;
         spre[i] = f;
     }
-    __syncthreads();
-    int64_t units = 0, tu0[2][kPlanPer], tun[2][kPlanPer];
-    int tiles = 0, tix[2][kPlanPer];
-    const int i0 = tid * kPlanPer;
+    if (T == 32)
+        __syncwarp();
+    else
+        __syncthreads();
+    int64_t units = 0, tu0[2][PER], tun[2][PER];
+    int tiles = 0, rmax = 0, tix[2][PER];
+    const int i0 = tid * PER;
+#pragma unroll
     for (int st = 0; st < 2; st++) {
 #pragma unroll
-        for (int e = 0; e < kPlanPer; e++) tun[st][e] = 0;
+        for (int e = 0; e < PER; e++) tun[st][e] = tu0[st][e] = 0, tix[st][e] = 0;
         if (st == 0 && D.streams == 1) continue;
         auto same = [&](int a, int b) { return spre[a] == spre[b] && (st == 0 || sseq[a] == sseq[b]); };
         // where each lane's run of lanes of one sequence starts
-        int rs[kPlanPer], last = -1;
-        for (int e = 0; e < kPlanPer; e++) {
+        int rs[PER], last = -1;
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
             const int i = i0 + e;
             if (i < n && spos[i] >= 0 && (i == 0 || spos[i - 1] < 0 || !same(i, i - 1))) last = i;
             rs[e] = last;
         }
-        int before = plan_scan_max(last, redi);
-        before = __shfl_up_sync(0xffffffffu, before, 1);
-        if ((tid & 31) == 0) {
-            before = -1;
-            for (int w = 0; w < (tid >> 5); w++) before = max(before, redi[w]);
-        }
-        AlTile t[kPlanPer];
-        int64_t mine = 0;  // tiles << 40 | units would overflow: two scans
+        int64_t tot;
+        const int before = (int)plan_scan<T, true>(last, -1, red, tot);
         int nt = 0;
-        for (int e = 0; e < kPlanPer; e++) {
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
             const int i = i0 + e;
             if (rs[e] < 0) rs[e] = before;
-            const bool start = i < n && spos[i] >= 0 && (i - rs[e]) % D.LT == 0;
-            t[e].nl = 0;
-            if (!start) continue;
-            int nl = 0, pmin = INT_MAX, pmax = -1;
-            for (int j = i; j < n && nl < D.LT && spos[j] >= 0 && same(i, j); j++, nl++) {
-                pmin = min(pmin, spos[j]);
-                pmax = max(pmax, spos[j]);
-            }
-            const int P = A.pre.k ? A.prefix_len[spre[i]] : 0;
-            const int64_t base = st == 0 ? 0 : P, lim = st == 0 ? P : A.own.rows;
-            const int64_t hi = min((int64_t)pmax - base, lim - 1);
-            const int64_t lo = A.window ? max((int64_t)0, (int64_t)pmin - A.window + 1 - base) : 0;
-            const int64_t sk = max((int64_t)0, min((int64_t)A.sinks - base, hi + 1));
-            const int64_t cf = lo / kChunk, main = lo <= hi ? hi / kChunk - cf + 1 : 0;
-            int64_t ns = A.window ? (sk + kChunk - 1) / kChunk : 0;
-            if (main > 0) ns = min(ns, cf);
-            t[e].lane0 = i, t[e].nl = nl, t[e].stream = st, t[e].nch = (int)(ns + main), t[e].nsink = (int)ns;
-            t[e].cfirst = (int)cf, t[e].slot = st == 0 ? spre[i] : sseq[i], t[e].base = (int)base, t[e].lim = (int)lim;
-            t[e].pmin = pmin, t[e].pmax = pmax, t[e].pad = 0;
-            nt++;
-            tun[st][e] = (ns + main) * A.n_kv * D.HB;
-            mine += tun[st][e];
+            rs[e] = i < n && spos[i] >= 0 ? (i - rs[e]) % D.LT : -1;  // the lane's place in its tile
+            nt += rs[e] == 0;
         }
-        int64_t tot_t, tot_u;
-        int ti = tiles + (int)(plan_scan_sum(nt, redl, tot_t) - nt);
-        int64_t u = units + plan_scan_sum(mine, redl, tot_u) - mine;
-        for (int e = 0; e < kPlanPer; e++) {
+        int64_t tot_t, tot_u, mine = 0;
+        int ti = tiles + (int)plan_scan<T, false>(nt, 0, red, tot_t);
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
             const int i = i0 + e;
-            if (t[e].nl) {
-                t[e].unit0 = u;
-                W.tiles[ti] = t[e];
-                tu0[st][e] = u;
-                tix[st][e] = ti;
-                u += tun[st][e];
-                ti++;
+            if (rs[e] == 0) {
+                int nl = 0, pmin = INT_MAX, pmax = -1;
+                for (int j = i; j < n && nl < D.LT && spos[j] >= 0 && same(i, j); j++, nl++) {
+                    pmin = min(pmin, spos[j]);
+                    pmax = max(pmax, spos[j]);
+                }
+                const int P = A.pre.k ? A.prefix_len[spre[i]] : 0;
+                const int64_t base = st == 0 ? 0 : P, lim = st == 0 ? P : A.own.rows;
+                const int64_t hi = min((int64_t)pmax - base, lim - 1);
+                const int64_t lo = A.window ? max((int64_t)0, (int64_t)pmin - A.window + 1 - base) : 0;
+                const int64_t sk = max((int64_t)0, min((int64_t)A.sinks - base, hi + 1));
+                const int64_t cf = lo / kChunk, main = lo <= hi ? hi / kChunk - cf + 1 : 0;
+                int64_t ns = A.window ? (sk + kChunk - 1) / kChunk : 0;
+                if (main > 0) ns = min(ns, cf);
+                AlTile t;
+                t.unit0 = 0;
+                t.lane0 = i, t.nl = nl, t.stream = st, t.nch = (int)(ns + main), t.nsink = (int)ns, t.cfirst = (int)cf;
+                t.slot = st == 0 ? spre[i] : sseq[i], t.base = (int)base, t.lim = (int)lim;
+                t.pmin = pmin, t.pmax = pmax, t.pad = 0;
+                tiles_out[ti] = t;
+                tix[st][e] = ti++;
+                tun[st][e] = (ns + main) * A.n_kv * D.HB;
+                mine += tun[st][e];
+                if (ns + main > 0) rmax = max(rmax, nl * min(D.group, D.R));
             }
-            if (i < n) W.tile_of[(int64_t)st * n + i] = spos[i] >= 0 ? ti - 1 : -1;
+            if (i < n) tile_of[(int64_t)st * n + i] = rs[e] >= 0 ? ti - 1 : -1;
         }
+        int64_t u = units + plan_scan<T, false>(mine, 0, red, tot_u);
+#pragma unroll
+        for (int e = 0; e < PER; e++)
+            if (rs[e] == 0) {
+                tiles_out[tix[st][e]].unit0 = tu0[st][e] = u;
+                u += tun[st][e];
+            }
         tiles += (int)tot_t;
         units += tot_u;
     }
     if (D.streams == 1)
-        for (int i = tid; i < n; i += kPlanThreads) W.tile_of[i] = -1;
+        for (int i = tid; i < n; i += T) tile_of[i] = -1;
+    int64_t widest;
+    plan_scan<T, true>(rmax, 0, red, widest);
     // CTA b takes the units [U b / grid, U (b + 1) / grid): at least one each
     const int64_t grid = min((int64_t)D.grid, units);
-    if (tid == 0) W.head->units = units, W.head->grid = grid;
+    if (tid == 0) head->units = units, head->grid = (int)grid, head->rmax = (int)widest;
+#pragma unroll
     for (int st = 0; st < 2; st++)
-        for (int e = 0; e < kPlanPer; e++)
+#pragma unroll
+        for (int e = 0; e < PER; e++)
             if (tun[st][e] > 0) {
                 const int64_t u0 = tu0[st][e], u1 = u0 + tun[st][e];
-                for (int64_t b = (u0 * grid + units - 1) / units; b < grid && units * b / grid < u1; b++)
-                    W.first[b] = tix[st][e];
+                if (cta >= 0) {
+                    const int64_t u = units * cta / grid;
+                    if (cta < grid && u >= u0 && u < u1) *first = tix[st][e];
+                } else {
+                    for (int64_t b = (u0 * grid + units - 1) / units; b < grid && units * b / grid < u1; b++)
+                        first[b] = tix[st][e];
+                }
             }
 }
 
+// One CTA plans for all.
+__global__ void __launch_bounds__(kPlanThreads) al_plan_kernel(AlArgs A, AlDims D, AlWs W) {
+    extern __shared__ int pl_smem[];  // [3][n_lanes]
+    __shared__ int64_t red[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    make_plan<kPlanThreads, kPlanPer>(A, D, pl_smem, pl_smem + A.n_lanes, pl_smem + 2 * A.n_lanes, red, W.head, W.first, -1,
+                                      W.tile_of, W.tiles, A.status);
+}
+
+// The plan as the other kernels see it: in the workspace, or in shared memory.
+struct AlPlan {
+    const AlPlanHead *head;
+    const int *first;  // of this CTA
+    const int *tile_of;
+    const AlTile *tiles;
+};
+
 // ------------------------------------------------------------------ the walk over a CTA's units
 struct Piece {
-    AlTile t;
+    const AlTile *t;  // (its fields are read where they are needed: registers are short)
     int kvh, hb, c0, c1;  // chunks c0 .. c1 - 1 of the tile for KV head kvh, head block hb
     int nrows, gs;        // rows, and rows per lane
     bool whole, head;     // all of its chunks; it is where the CTA's units start
@@ -277,39 +320,31 @@ struct Piece {
 
 struct Walker {
     int64_t u0, u, hi;
-    int ti;
-    AlTile t;
-    __device__ __forceinline__ void load(const AlWs &W) {
-        const int4 *p = reinterpret_cast<const int4 *>(W.tiles + ti);
-        int4 *o = reinterpret_cast<int4 *>(&t);
-#pragma unroll
-        for (int k = 0; k < 4; k++) o[k] = __ldcg(p + k);
-    }
-    __device__ __forceinline__ explicit Walker(const AlWs &W) {
-        const int64_t U = __ldcg(&W.head->units), G = __ldcg(&W.head->grid);
+    const AlTile *at;
+    __device__ __forceinline__ explicit Walker(const AlPlan &P) {
+        const int64_t U = P.head->units;
+        const int G = P.head->grid;
         u0 = u = hi = 0;
-        if (blockIdx.x < G) {
+        if ((int)blockIdx.x < G) {
             u0 = u = U * blockIdx.x / G;
             hi = U * (blockIdx.x + 1) / G;
-            ti = __ldcg(&W.first[blockIdx.x]);
-            load(W);
+            at = P.tiles + *P.first;
         }
     }
-    __device__ __forceinline__ bool next(Piece &p, const AlArgs &A, const AlWs &W, const AlDims &D) {
+    __device__ __forceinline__ bool next(Piece &p, const AlArgs &A, const AlDims &D) {
         if (u >= hi) return false;
-        while (u >= t.unit0 + (int64_t)t.nch * A.n_kv * D.HB) {
-            ti++;
-            load(W);
-        }
-        const int64_t r = u - t.unit0, sub = r / t.nch;
-        p.t = t;
-        p.kvh = (int)(sub / D.HB);
-        p.hb = (int)(sub - (int64_t)p.kvh * D.HB);
-        p.c0 = (int)(r - sub * t.nch);
-        p.c1 = (int)min((int64_t)t.nch, p.c0 + (hi - u));
+        while (u >= at->unit0 + (int64_t)at->nch * A.n_kv * D.HB) at++;
+        const int nch = at->nch;
+        const int64_t r = u - at->unit0;  // within a tile: nch n_kv HB units
+        const int64_t sub = (r >> 31) ? r / nch : (int64_t)((uint32_t)r / (uint32_t)nch);
+        p.t = at;
+        p.kvh = (int)sub / D.HB;
+        p.hb = (int)sub - p.kvh * D.HB;
+        p.c0 = (int)(r - sub * nch);
+        p.c1 = (int)min((int64_t)nch, p.c0 + (hi - u));
         p.gs = D.HB == 1 ? D.group : min(D.R, D.group - p.hb * D.R);
-        p.nrows = t.nl * p.gs;
-        p.whole = p.c0 == 0 && p.c1 == t.nch;
+        p.nrows = at->nl * p.gs;
+        p.whole = p.c0 == 0 && p.c1 == nch;
         p.head = u == u0;
         u += p.c1 - p.c0;
         return true;
@@ -323,15 +358,15 @@ struct ChunkView {
     int all_lo, all_hi;           // rows <= all_hi that are > all_lo or < sk are seen by every one
     bool edge;                    // not all of its keys are
     __device__ __forceinline__ ChunkView(const Piece &p, int c, const AlArgs &A) {
-        r0 = (c < p.t.nsink ? c : p.t.cfirst + c - p.t.nsink) * kChunk;
-        any_hi = (int)min((int64_t)p.t.pmax - p.t.base, (int64_t)p.t.lim - 1);
-        all_hi = (int)min((int64_t)p.t.pmin - p.t.base, (int64_t)p.t.lim - 1);
+        r0 = (c < p.t->nsink ? c : p.t->cfirst + c - p.t->nsink) * kChunk;
+        any_hi = (int)min((int64_t)p.t->pmax - p.t->base, (int64_t)p.t->lim - 1);
+        all_hi = (int)min((int64_t)p.t->pmin - p.t->base, (int64_t)p.t->lim - 1);
         any_lo = all_lo = -1;
         sk = 0;
         if (A.window) {
-            any_lo = (int)max((int64_t)-1, (int64_t)p.t.pmin - A.window - p.t.base);
-            all_lo = (int)max((int64_t)-1, (int64_t)p.t.pmax - A.window - p.t.base);
-            sk = max(0, A.sinks - p.t.base);
+            any_lo = (int)max((int64_t)-1, (int64_t)p.t->pmin - A.window - p.t->base);
+            all_lo = (int)max((int64_t)-1, (int64_t)p.t->pmax - A.window - p.t->base);
+            sk = max(0, A.sinks - p.t->base);
         }
         edge = !(r0 + kChunk - 1 <= all_hi && (r0 > all_lo || r0 + kChunk - 1 < sk));
     }
@@ -347,39 +382,53 @@ struct ChunkView {
 // NT: bf16 terms of a cached value (1: bf16 cache, 3: fp32 cache)
 template <int NT>
 struct AlCfg {
-    static constexpr int R = NT == 1 ? 64 : 32;     // rows of a tile
-    static constexpr int kSlots = NT == 1 ? 4 : 3;
+    static constexpr int R = NT == 1 ? 64 : 32;     // rows of a tile at most
+    static constexpr int kWg = R / 16;              // warpgroups, 16 rows each
     static constexpr int kTerm = 16384;             // 128 keys x 64 dims, or 64 keys x 128 dims, in bf16
     static constexpr int kSlot = NT * kTerm;
-    static constexpr int kQBlock = R * 128;         // one term of 64 dims of the rows
-    static constexpr int kQ = 4 * 3 * kQBlock;
-    static constexpr int kPPitch = 2 * R;           // a key's weights, one term
-    static constexpr int kPTerm = kChunk * kPPitch;
-    static constexpr int kP = 3 * kPTerm;
+    static constexpr int kMma = 4 * kWg;            // the warp that issues the MMAs; the producers follow it
     static constexpr int kProd = NT == 1 ? 1 : 8;   // producer warps
-    static constexpr int kThreads = 32 * (4 + 1 + kProd);
-    static constexpr uint32_t kCols = 4 * R;        // two S^T, two halves of O^T
+    static constexpr int kThreads = 32 * (kMma + 1 + kProd);
+    static constexpr uint32_t kCols = 8 * R;        // S^T main and small, twice; O^T (two halves of dims) twice
+    static constexpr uint32_t kSmall = 2 * R, kO = 4 * R;
+    static constexpr int kMaxSlots = NT == 1 ? 12 : 3;
 };
 
 template <int NT>
 struct AlCtl {
     using C = AlCfg<NT>;
-    uint64_t full[C::kSlots], empty[C::kSlots], fixed[C::kSlots];
-    uint64_t s_full[2], p_ready, pv_done, q_ready, drain;
+    uint64_t full[C::kMaxSlots], empty[C::kMaxSlots], fixed[C::kMaxSlots];
+    uint64_t s_full[2], p_ready, q_ready, pv_done, drain;
     int rowid[C::R];  // lane * n_heads + head
     int rowlo[C::R], rowhi[C::R];  // a row sees the keys <= rowhi that are > rowlo or first ones
+    int nan[C::R];    // it sees a value that is not finite and was replaced
     float mc[C::R], alpha[C::R];
     float red[4][C::R];
+    AlSelfPlan plan;
     uint32_t tmem;
     int abort;
 };
+constexpr int kAlSmem = 227 * 1024;  // all of an SM's: one CTA per SM
 
+// Shared memory: ring slots, then the rows' q (4 x 64 dims, three terms, rows
+// of 128 bytes), then the weights P (three terms of 128 keys' rows), then the
+// control block.  Rc: the widest tile's rows, rounded up to 16, 32 or 64.
 template <int NT>
-constexpr int al_smem() {
-    using C = AlCfg<NT>;
-    return 1024 + C::kSlots * C::kSlot + C::kQ + C::kP + (int)sizeof(AlCtl<NT>);
-}
-static_assert(al_smem<1>() <= 227 * 1024 && al_smem<3>() <= 227 * 1024, "shared memory of one CTA per SM");
+struct AlLayout {
+    int Rc, qblock, pitch, pterm, slots;
+    __device__ __forceinline__ AlLayout(int rmax, int hd) {
+        Rc = rmax <= 16 ? 16 : rmax <= 32 ? 32 : 64;
+        qblock = Rc * 128;
+        pitch = Rc == 64 ? 128 : 64;  // bytes of a key's weights, one term
+        pterm = kChunk * pitch;
+        const int left = kAlSmem - 1024 - (int)sizeof(AlCtl<NT>) - (hd + 63) / 64 * 3 * qblock - 3 * pterm;
+        slots = min(left / AlCfg<NT>::kSlot, AlCfg<NT>::kMaxSlots);
+    }
+    __device__ __forceinline__ int q() const { return slots * AlCfg<NT>::kSlot; }
+    __device__ __forceinline__ int p(int hd) const { return q() + (hd + 63) / 64 * 3 * qblock; }
+};
+static_assert(kAlSmem - 1024 - (int)sizeof(AlCtl<1>) - 4 * 3 * 64 * 128 - 3 * 128 * 128 >= 4 * 16384, "ring of four");
+static_assert(kAlSmem - 1024 - (int)sizeof(AlCtl<3>) - 4 * 3 * 32 * 128 - 3 * 128 * 64 >= 3 * 49152, "ring of three");
 
 // descriptor version 1; layout 2: 128-byte swizzle, 4: 64-byte
 __device__ __forceinline__ uint64_t al_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
@@ -430,30 +479,56 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Every lane's values of 32 columns -> lane l the reduction of column l over the warp.
+__device__ __forceinline__ uint4 lds128_a(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Every lane's values of 16 columns -> lane l the reduction of column l % 16 over the warp.
 template <bool MAX>
-__device__ __forceinline__ float al_reduce32(float (&v)[32], int lane) {
+__device__ __forceinline__ float al_reduce16(float (&v)[16], int lane) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
+    for (int off = 8; off > 0; off >>= 1)
 #pragma unroll
         for (int i = 0; i < off; i++) {
             const float send = (lane & off) ? v[i] : v[i + off], keep = (lane & off) ? v[i + off] : v[i];
             const float recv = __shfl_xor_sync(0xffffffffu, send, off);
             v[i] = MAX ? fmaxf(keep, recv) : __fadd_rn(keep, recv);
         }
-    return v[0];
+    const float o = __shfl_xor_sync(0xffffffffu, v[0], 16);
+    return MAX ? fmaxf(v[0], o) : __fadd_rn(v[0], o);
 }
 
-__device__ __forceinline__ void al_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool al_bar_or(bool v) {
+// barriers of one warpgroup
+__device__ __forceinline__ void al_bar(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory"); }
+__device__ __forceinline__ bool al_bar_or(int wg, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "r"(wg + 1)
         : "memory");
     return r != 0;
+}
+
+// 32 bytes if on, else zeros: both loads are in flight before either is used
+__device__ __forceinline__ void al_ld32(const float *p, bool on, uint4 &a, uint4 &b) {
+    a = b = make_uint4(0, 0, 0, 0);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %9, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%8];\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%4,%5,%6,%7}, [%8+16];\n\t}"
+        : "+r"(a.x), "+r"(a.y), "+r"(a.z), "+r"(a.w), "+r"(b.x), "+r"(b.y), "+r"(b.z), "+r"(b.w)
+        : "l"(p), "r"((uint32_t)on));
+}
+// eight values as three 16-byte groups of bf16 terms
+__device__ __forceinline__ void al_split8(const uint4 &a, const uint4 &b, uint4 &h, uint4 &m, uint4 &l) {
+    al_split2(__uint_as_float(a.x), __uint_as_float(a.y), h.x, m.x, l.x);
+    al_split2(__uint_as_float(a.z), __uint_as_float(a.w), h.y, m.y, l.y);
+    al_split2(__uint_as_float(b.x), __uint_as_float(b.y), h.z, m.z, l.z);
+    al_split2(__uint_as_float(b.z), __uint_as_float(b.w), h.w, m.w, l.w);
 }
 
 struct AlMaps {
@@ -467,15 +542,15 @@ struct SliceGen {
     Piece p;
     int n, i, sl;
     bool v, more;
-    __device__ __forceinline__ SliceGen(const AlArgs &A, const AlWs &W, const AlDims &D) : w(W) { piece(A, W, D); }
-    __device__ __forceinline__ void piece(const AlArgs &A, const AlWs &W, const AlDims &D) {
-        more = w.next(p, A, W, D);
+    __device__ __forceinline__ SliceGen(const AlArgs &A, const AlPlan &P, const AlDims &D) : w(P) { piece(A, D); }
+    __device__ __forceinline__ void piece(const AlArgs &A, const AlDims &D) {
+        more = w.next(p, A, D);
         n = p.c1 - p.c0;
         i = sl = 0;
         v = false;
     }
     __device__ __forceinline__ int chunk() const { return p.c0 + (v ? i - 1 : i); }
-    __device__ __forceinline__ void step(const AlArgs &A, const AlWs &W, const AlDims &D, int nK, int nV) {
+    __device__ __forceinline__ void step(const AlArgs &A, const AlDims &D, int nK, int nV) {
         if (++sl < (v ? nV : nK)) return;
         sl = 0;
         // step i: K of chunk i (if there is one), then V of chunk i - 1 (if there is one)
@@ -486,8 +561,17 @@ struct SliceGen {
         } else {
             i++;
             v = i >= n;
-            if (i > n) piece(A, W, D);
+            if (i > n) piece(A, D);
         }
+    }
+};
+
+// A place in the ring: slot and the parity of its round.
+struct RingPos {
+    int s = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void step(int slots) {
+        if (++s == slots) s = 0, round++;
     }
 };
 
@@ -498,57 +582,72 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     constexpr int R = C::R;
     extern __shared__ uint8_t al_raw[];
     uint8_t *const smem = al_raw + ((1024u - (smem_addr(al_raw) & 1023u)) & 1023u);  // the swizzled operands' alignment
-    uint8_t *const ring = smem, *const qs = ring + C::kSlots * C::kSlot, *const ps = qs + C::kQ;
-    AlCtl<NT> &S = *reinterpret_cast<AlCtl<NT> *>(ps + C::kP);
+    AlCtl<NT> &S = *reinterpret_cast<AlCtl<NT> *>(smem + (kAlSmem - 1024 - sizeof(AlCtl<NT>)) / 16 * 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hd = A.hd;
     const int nK = (hd + 63) / 64, nDH = (hd + 127) / 128, nV = 2 * nDH;
-    if (warp == 4) {
+    if (warp == C::kMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&S.tmem)),
                      "r"(C::kCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (tid == 0) {
-        for (int s = 0; s < C::kSlots; s++) {
+    if (tid == 32) {
+        for (int s = 0; s < C::kMaxSlots; s++) {
             mbar_init(&S.full[s], C::kProd);
             mbar_init(&S.empty[s], 1);
             mbar_init(&S.fixed[s], 128);
         }
         mbar_init(&S.s_full[0], 1);
         mbar_init(&S.s_full[1], 1);
-        mbar_init(&S.p_ready, 128);
+        // every warpgroup's warps arrive for every chunk and piece, with rows in it or not: no wait can then be
+        // two phases behind
+        mbar_init(&S.p_ready, 4 * C::kWg);
+        mbar_init(&S.q_ready, 4 * C::kWg);
         mbar_init(&S.pv_done, 1);
-        mbar_init(&S.q_ready, 128);
         mbar_init(&S.drain, 1);
         S.abort = 0;
         fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan, and what the kernels before wrote
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    AlPlan P{W.head, W.first + blockIdx.x, W.tile_of, W.tiles};
+    if (A.n_lanes <= kSelfPlan) {
+        AlSelfScratch &x = *reinterpret_cast<AlSelfScratch *>(smem);  // (the ring is not in use yet)
+        if (warp == 0) {
+            make_plan<32, kSelfPlan / 32>(A, D, x.pos, x.seq, x.pre, nullptr, &S.plan.head, &S.plan.first, blockIdx.x,
+                                          x.tile_of, S.plan.tiles, blockIdx.x == 0 ? A.status : nullptr);
+            fence_proxy_async_smem();
+        }
+        P = AlPlan{&S.plan.head, &S.plan.first, nullptr, S.plan.tiles};
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan, and what the kernels before it wrote
+    const AlLayout<NT> L(P.head->rmax, hd);
+    const int slots = L.slots;
+    uint8_t *const ring = smem, *const qs = ring + L.q(), *const ps = ring + L.p(hd);
 
-    if (warp >= 5) {
+    if (warp > C::kMma) {
         // ---------------------------------------------------------- producers
         if constexpr (NT == 1) {
             if (lane == 0) {
-                SliceGen sg(A, W, D);
+                SliceGen sg(A, P, D);
+                RingPos at;
                 int g = 0;
                 for (; sg.more; g++) {
-                    const int s = g % C::kSlots;
-                    if (g >= C::kSlots && !al_wait(&S.empty[s], (uint32_t)(g / C::kSlots - 1) & 1u, &S.abort)) {
+                    const int s = at.s;
+                    if (at.round && !al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort)) {
                         S.abort = 1;
                         raise_status(A.status, kStatusTimeout);
                         break;
                     }
                     const Piece &p = sg.p;
                     const ChunkView cv(p, sg.chunk(), A);
-                    const CUtensorMap *map = sg.v ? &maps.v[p.t.stream] : &maps.k[p.t.stream];
-                    const qlin_kv &kv = p.t.stream ? A.own : A.pre;
-                    const int z = kv.seq_stride ? p.t.slot : 0;
+                    const CUtensorMap *map = sg.v ? &maps.v[p.t->stream] : &maps.k[p.t->stream];
+                    const qlin_kv &kv = p.t->stream ? A.own : A.pre;
+                    const int z = kv.seq_stride ? p.t->slot : 0;
                     uint8_t *to = ring + s * C::kSlot;
                     // two boxes of 64 keys x 64 dims, those that nobody sees left out: K's are the two halves of
                     // the chunk, V's (of one half) the two halves of 128 dims
@@ -565,55 +664,49 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
 #pragma unroll
                     for (int b = 0; b < 2; b++)
                         if (on[b]) al_tma(to + b * 8192, map, x[b], y[b], z, &S.full[s]);
-                    sg.step(A, W, D, nK, nV);
+                    sg.step(A, D, nK, nV);
+                    at.step(slots);
                 }
-                if (S.abort)  // the copies in flight
-                    for (int k = max(0, g - C::kSlots); k < g; k++)
-                        mbar_wait(&S.full[k % C::kSlots], (uint32_t)(k / C::kSlots) & 1u);
+                if (*(volatile int *)&S.abort)  // the copies in flight
+                    for (int k = max(0, g - slots); k < g; k++)
+                        mbar_wait(&S.full[k % slots], (uint32_t)(k / slots) & 1u);
             }
         } else {
             // 32 rows of 8 dims at a time: thread t takes row t / 8, dims 8 (t % 8) ..; four such passes are a
             // slice's 128 rows (a V slice's rows 64 .. 127 are the second 64 dims of its 64 keys)
-            const int pt = tid - 160, pr = pt >> 3, pc = pt & 7;
-            float4 buf[2][8];
-            auto load = [&](SliceGen &sg, float4 (&o)[8]) {
+            const int pt = tid - 32 * (C::kMma + 1), pr = pt >> 3, pc = pt & 7;
+            uint4 buf[2][8];
+            auto load = [&](SliceGen &sg, uint4 (&o)[8]) {
                 const Piece &p = sg.p;
                 const ChunkView cv(p, sg.chunk(), A);
-                const qlin_kv &kv = p.t.stream ? A.own : A.pre;
-                const float *src = static_cast<const float *>(sg.v ? kv.v : kv.k) + (int64_t)p.t.slot * kv.seq_stride +
+                const qlin_kv &kv = p.t->stream ? A.own : A.pre;
+                const float *src = static_cast<const float *>(sg.v ? kv.v : kv.k) + (int64_t)p.t->slot * kv.seq_stride +
                                    p.kvh * hd + 8 * pc;
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const int r = e * 32 + pr;
                     const int key = cv.r0 + (sg.v ? (sg.sl / nDH) * 64 + (r & 63) : r);
                     const int d = sg.v ? (sg.sl % nDH) * 128 + (r >> 6) * 64 : sg.sl * 64;
-                    o[2 * e] = o[2 * e + 1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (d + 8 * pc < hd && cv.any(key)) {
-                        const float *a = src + (int64_t)key * kv.row_stride + d;
-                        const uint4 u = ld_stream_v4(a), w = ld_stream_v4(a + 4);
-                        o[2 * e] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                                               __uint_as_float(u.w));
-                        o[2 * e + 1] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
-                                                   __uint_as_float(w.w));
-                    }
+                    al_ld32(src + (int64_t)key * kv.row_stride + d, d + 8 * pc < hd && cv.any(key), o[2 * e], o[2 * e + 1]);
                 }
             };
-            SliceGen sg(A, W, D);
+            SliceGen sg(A, P, D);
+            RingPos at;
             bool have[2] = {false, false};
 #pragma unroll
             for (int k = 0; k < 2; k++)
                 if (sg.more) {
                     load(sg, buf[k]);
                     have[k] = true;
-                    sg.step(A, W, D, nK, nV);
+                    sg.step(A, D, nK, nV);
                 }
             bool ok = true;
-            for (int g = 0; ok && have[0]; g += 2) {
+            while (ok && have[0]) {
 #pragma unroll
                 for (int k = 0; k < 2; k++) {
                     if (!have[k]) break;
-                    const int gg = g + k, s = gg % C::kSlots;
-                    if (gg >= C::kSlots && !al_wait(&S.empty[s], (uint32_t)(gg / C::kSlots - 1) & 1u, &S.abort)) {
+                    const int s = at.s;
+                    if (at.round && !al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort)) {
                         S.abort = 1;
                         raise_status(A.status, kStatusTimeout);
                         ok = false;
@@ -623,41 +716,39 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         const int r = e * 32 + pr;
-                        const float4 a = buf[k][2 * e], b = buf[k][2 * e + 1];
                         uint4 h, m, l;
-                        al_split2(a.x, a.y, h.x, m.x, l.x);
-                        al_split2(a.z, a.w, h.y, m.y, l.y);
-                        al_split2(b.x, b.y, h.z, m.z, l.z);
-                        al_split2(b.z, b.w, h.w, m.w, l.w);
-                        const uint32_t at = to + (uint32_t)(r * 128 + ((pc ^ (r & 7)) << 4));
-                        sts128(at, h);
-                        sts128(at + C::kTerm, m);
-                        sts128(at + 2 * C::kTerm, l);
+                        al_split8(buf[k][2 * e], buf[k][2 * e + 1], h, m, l);
+                        const uint32_t a = to + (uint32_t)(r * 128 + ((pc ^ (r & 7)) << 4));
+                        sts128(a, h);
+                        sts128(a + C::kTerm, m);
+                        sts128(a + 2 * C::kTerm, l);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&S.full[s]);
+                    at.step(slots);
                     have[k] = sg.more;
                     if (sg.more) {
                         load(sg, buf[k]);
-                        sg.step(A, W, D, nK, nV);
+                        sg.step(A, D, nK, nV);
                     }
                 }
             }
         }
-    } else if (warp == 4) {
+    } else if (warp == C::kMma) {
         // ---------------------------------------------------------- the MMAs
         if (lane == 0) {
-            Walker w(W);
+            Walker w(P);
             Piece p;
-            int g = 0, it = 0;  // slices and chunks so far
-            uint32_t fixpar = 0;
+            RingPos at;
+            int it = 0, np = 0;   // chunks and pieces so far
+            uint32_t fixpar = 0;  // parities by slot
             bool ok = true;
             const uint32_t ring_a = smem_addr(ring), qs_a = smem_addr(qs), ps_a = smem_addr(ps);
-            constexpr uint32_t kPLayout = R == 64 ? 2u : 4u;
-            for (int np = 0; ok && w.next(p, A, W, D); np++) {
-                const int n = p.c1 - p.c0;
-                const uint32_t N = (uint32_t)(p.nrows + 15) / 16 * 16;
+            const uint32_t playout = L.pitch == 128 ? 2u : 4u;
+            for (; ok && w.next(p, A, D); np++) {
+                const int n = p.c1 - p.c0, wgs = (p.nrows + 15) / 16;
+                const uint32_t N = 16u * (uint32_t)wgs;
                 // fp32 accumulator, bf16 operands; S^T: both K-major, O^T: both with the keys as rows
                 const uint32_t ids = (1u << 4) | (1u << 7) | (1u << 10) | (N >> 3) << 17 | (128u >> 4) << 24;
                 const uint32_t idp = ids | (1u << 15) | (1u << 16);
@@ -665,19 +756,21 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 for (int i = 0; ok && i <= n; i++) {
                     if (i < n) {
                         const uint32_t d = tmem + (uint32_t)((it + i) & 1) * R;
-                        for (int sl = 0; sl < nK; sl++, g++) {
-                            const int s = g % C::kSlots;
-                            if (!(ok = al_wait(&S.full[s], (uint32_t)(g / C::kSlots) & 1u, &S.abort))) break;
+                        for (int sl = 0; sl < nK; sl++, at.step(slots)) {
+                            const int s = at.s;
+                            if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
                             tc_fence_after();
                             const int steps = min(64, hd - sl * 64) / 16;
+                            const uint32_t a0 = ring_a + s * C::kSlot, b0 = qs_a + sl * 3 * L.qblock;
                             for (int kk = 0; kk < steps; kk++)
 #pragma unroll
                                 for (int t = 0; t < NT; t++)
 #pragma unroll
                                     for (int u = 0; u < 3 - t; u++)
-                                        al_mma(d, al_desc(ring_a + s * C::kSlot + t * C::kTerm + 32 * kk, 16, 1024, 2),
-                                               al_desc(qs_a + (sl * 3 + u) * C::kQBlock + 32 * kk, 16, 1024, 2), ids,
-                                               sl > 0 || kk > 0 || t > 0 || u > 0);
+                                        // (each accumulator's first product: hi x hi, and hi x mid)
+                                        al_mma(d + (t + u ? C::kSmall : 0u), al_desc(a0 + t * C::kTerm + 32 * kk, 16, 1024, 2),
+                                               al_desc(b0 + u * L.qblock + 32 * kk, 16, 1024, 2), ids,
+                                               sl > 0 || kk > 0 || t > 0 || u > 1);
                             tc_commit(&S.empty[s]);
                         }
                         if (!ok) break;
@@ -686,24 +779,26 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     if (i >= 1) {
                         const ChunkView cv(p, p.c0 + i - 1, A);
                         if (!(ok = al_wait(&S.p_ready, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
-                        for (int vs = 0; vs < nV; vs++, g++) {
-                            const int s = g % C::kSlots, kh = vs / nDH, dh = vs % nDH;
-                            if (!(ok = al_wait(&S.full[s], (uint32_t)(g / C::kSlots) & 1u, &S.abort))) break;
+                        for (int vs = 0; vs < nV; vs++, at.step(slots)) {
+                            const int s = at.s, kh = vs / nDH, dh = vs % nDH;
+                            if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
                             if (cv.edge) {
                                 if (!(ok = al_wait(&S.fixed[s], (fixpar >> s) & 1u, &S.abort))) break;
                                 fixpar ^= 1u << s;
                             }
                             tc_fence_after();
-                            const uint32_t d = tmem + (uint32_t)(2 + dh) * R;
-                            for (int ks = 0; ks < 4; ks++)
+                            const uint32_t d = tmem + C::kO + (uint32_t)(((it + i - 1) & 1) * 2 + dh) * R;
+                            const uint32_t a0 = ring_a + s * C::kSlot, b0 = ps_a + kh * 64 * L.pitch;
+                            // the small products first: the accumulation rounds toward zero
+#pragma unroll
+                            for (int o = 2; o >= 0; o--)
 #pragma unroll
                                 for (int t = 0; t < NT; t++)
-#pragma unroll
-                                    for (int u = 0; u < 3 - t; u++)
-                                        al_mma(d, al_desc(ring_a + s * C::kSlot + t * C::kTerm + 2048 * ks, 8192, 1024, 2),
-                                               al_desc(ps_a + u * C::kPTerm + (kh * 64 + ks * 16) * C::kPPitch, 16,
-                                                       8 * C::kPPitch, kPLayout),
-                                               idp, i > 1 || kh > 0 || ks > 0 || t > 0 || u > 0);
+                                    if (o - t >= 0)
+                                        for (int ks = 0; ks < 4; ks++)
+                                            al_mma(d, al_desc(a0 + t * C::kTerm + 2048 * ks, 8192, 1024, 2),
+                                                   al_desc(b0 + (o - t) * L.pterm + ks * 16 * L.pitch, 16, 8 * L.pitch, playout),
+                                                   idp, kh > 0 || ks > 0 || t > 0 || o < 2);
                             tc_commit(&S.empty[s]);
                         }
                         if (!ok) break;
@@ -720,357 +815,386 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             }
         }
     } else {
-        // ---------------------------------------------------------- weights: thread t owns key t of a chunk
-        Walker w(W);
+        // ---------------------------------------------------------- weights and sums: warpgroup wg owns rows
+        // 16 wg .. 16 wg + 15, its thread t key t of a chunk, and of the outputs dims t and t + 128
+        const int wg = warp >> 2, t = tid & 127, r0 = 16 * wg;
+        Walker w(P);
         Piece p;
-        int g = 0, it = 0;
-        const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
+        int g = 0, it = 0;  // slices and chunks so far
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)r0;
         const float ninf = -__int_as_float(0x7f800000);
         bool ok = true;
-        while (ok && w.next(p, A, W, D)) {
-            const int n = p.c1 - p.c0, nr = (p.nrows + 15) / 16 * 16;
-            al_bar();  // the rows of the last piece are no longer needed
-            if (tid < nr) {
-                const int r = tid, ln = p.t.lane0 + r / p.gs;
+        while (ok && w.next(p, A, D)) {
+            const int n = p.c1 - p.c0;
+            if (r0 >= p.nrows) {  // (the first warpgroup always has rows)
+                if (lane == 0) mbar_arrive(&S.q_ready);
+                for (int i = 0; i < n && ok; i++, it++) {
+                    if (lane == 0) mbar_arrive(&S.p_ready);
+                    // (a second arrival must not meet the same phase)
+                    ok = al_wait(&S.pv_done, (uint32_t)it & 1u, &S.abort);
+                    __syncwarp();
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                continue;
+            }
+            al_bar(wg);  // the rows of the last piece are no longer needed
+            if (t < 16) {
+                const int r = r0 + t, ln = p.t->lane0 + r / p.gs;
                 const bool in = r < p.nrows;
-                const int64_t pl = in ? (int64_t)A.positions[ln] - p.t.base : -1;
-                S.rowid[r] = in ? ln * A.n_heads + p.kvh * D.group + p.hb * R + r % p.gs : -1;
-                S.rowhi[r] = (int)max((int64_t)-1, min(pl, (int64_t)p.t.lim - 1));
+                const int64_t pl = in ? (int64_t)A.positions[ln] - p.t->base : -1;
+                S.rowid[r] = in ? ln * A.n_heads + p.kvh * D.group + p.hb * D.R + r % p.gs : -1;
+                S.rowhi[r] = (int)max((int64_t)-1, min(pl, (int64_t)p.t->lim - 1));
                 S.rowlo[r] = A.window ? (int)max((int64_t)-1, pl - A.window) : -1;
                 S.mc[r] = kNoKey;
+                S.nan[r] = 0;
             }
-            al_bar();
+            al_bar(wg);
             // the rows' q as three bf16 terms, 64 dims after 64 dims, rows of 128 swizzled bytes
-            for (int e = tid; e < nr * (hd / 8); e += 128) {
-                const int r = e / (hd / 8), d8 = e - r * (hd / 8), id = S.rowid[r];
-                float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
-                if (id >= 0) {
-                    const float4 *src = reinterpret_cast<const float4 *>(A.q + (int64_t)id * hd + 8 * d8);
-                    a = __ldg(src), b = __ldg(src + 1);
-                }
-                uint4 h, m, l;
-                al_split2(a.x, a.y, h.x, m.x, l.x);
-                al_split2(a.z, a.w, h.y, m.y, l.y);
-                al_split2(b.x, b.y, h.z, m.z, l.z);
-                al_split2(b.z, b.w, h.w, m.w, l.w);
-                const uint32_t at = smem_addr(qs) + (uint32_t)((d8 >> 3) * 3 * C::kQBlock + r * 128 +
+            for (int e = t; e < 2 * hd; e += 128) {
+                const int r = r0 + e / (hd / 8), d8 = e % (hd / 8), id = S.rowid[r];
+                uint4 a, b, h, m, l;
+                al_ld32(A.q + (int64_t)max(id, 0) * hd + 8 * d8, id >= 0, a, b);
+                al_split8(a, b, h, m, l);
+                const uint32_t at = smem_addr(qs) + (uint32_t)((d8 >> 3) * 3 * L.qblock + r * 128 +
                                                                (((d8 & 7) ^ (r & 7)) << 4));
                 sts128(at, h);
-                sts128(at + C::kQBlock, m);
-                sts128(at + 2 * C::kQBlock, l);
+                sts128(at + L.qblock, m);
+                sts128(at + 2 * L.qblock, l);
             }
             fence_proxy_async_smem();
-            mbar_arrive(&S.q_ready);
-            float lsum[R];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.q_ready);
+            float lsum[16], acc[2][16];
 #pragma unroll
-            for (int r = 0; r < R; r++) lsum[r] = 0.0f;
+            for (int j = 0; j < 16; j++) lsum[j] = acc[0][j] = acc[1][j] = 0.0f;
+            // adds chunk c's products to the outputs
+            auto take = [&](int c) {
+                const uint32_t to = tl + C::kO + (uint32_t)((c & 1) * 2 * R);
+                uint32_t v[16];
+                tm_ld16(to, v);
+#pragma unroll
+                for (int j = 0; j < 16; j++) acc[0][j] = __fadd_rn(acc[0][j], __uint_as_float(v[j]));
+                if (nDH == 2) {
+                    tm_ld16(to + R, v);
+#pragma unroll
+                    for (int j = 0; j < 16; j++) acc[1][j] = __fadd_rn(acc[1][j], __uint_as_float(v[j]));
+                }
+            };
 
             for (int i = 0; i < n; i++, it++) {
                 const ChunkView cv(p, p.c0 + i, A);
-                const int key = cv.r0 + tid;
-                bool fail = !al_wait(&S.s_full[it & 1], (uint32_t)(it >> 1) & 1u, &S.abort);
+                const int key = cv.r0 + t;
+                const bool fail = !al_wait(&S.s_full[it & 1], (uint32_t)(it >> 1) & 1u, &S.abort);
                 __syncwarp();  // (the tensor-memory loads are for whole warps)
                 tc_fence_after();
-                const uint32_t ts = tl + (uint32_t)(it & 1) * R;
-                // whether this row of the tile sees this thread's key
-                auto sees = [&](int r) {
-                    return key <= S.rowhi[r] && (key > S.rowlo[r] || key < cv.sk);
-                };
+                float s[16];
+                {
+                    const uint32_t ts = tl + (uint32_t)(it & 1) * R;
+                    uint32_t a[16], b[16];
+                    tm_ld16_nw(ts, a);
+                    tm_ld16_nw(ts + C::kSmall, b);
+                    tm_wait_ld(a);
+                    tm_wait_ld(b);
+#pragma unroll
+                    for (int j = 0; j < 16; j++) s[j] = __fadd_rn(__uint_as_float(a[j]), __uint_as_float(b[j]));
+                }
+                // whether row r of the tile sees this thread's key
+                auto sees = [&](int r) { return key <= S.rowhi[r] && (key > S.rowlo[r] || key < cv.sk); };
+                if (cv.edge)
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        if (!sees(r0 + j)) s[j] = ninf;
                 bool big = i == 0;
-                if (i > 0) {
+                if (i > 0)
 #pragma unroll
-                    for (int b = 0; b < R / 16; b++)
-                        if (b * 16 < nr) {
-                            uint32_t v[16];
-                            tm_ld16(ts + 16 * b, v);
-#pragma unroll
-                            for (int j = 0; j < 16; j++) {
-                                const float x = __fmaf_rn(__uint_as_float(v[j]), D.c, -S.mc[16 * b + j]);
-                                if (!cv.edge || sees(16 * b + j)) big |= x > 8.0f;
-                            }
+                    for (int j = 0; j < 16; j++) big |= __fmaf_rn(s[j], D.c, -S.mc[r0 + j]) > 8.0f;
+                const bool update = al_bar_or(wg, big || fail);
+                if (update) {
+                    if (al_bar_or(wg, fail)) {
+                        if (fail) {
+                            S.abort = 1;
+                            raise_status(A.status, kStatusTimeout);
                         }
-                }
-                if (al_bar_or(fail)) {
-                    if (fail) {
-                        S.abort = 1;
-                        raise_status(A.status, kStatusTimeout);
+                        ok = false;
+                        break;
                     }
-                    ok = false;
-                    break;
-                }
-                if (al_bar_or(big)) {
                     // new maxima
+                    float m[16];
 #pragma unroll
-                    for (int b = 0; b < R / 32; b++)
-                        if (b * 32 < nr) {
-                            uint32_t v0[16], v1[16];
-                            float m[32];
-                            tm_ld16(ts + 32 * b, v0);
-                            tm_ld16(ts + 32 * b + 16, v1);
-#pragma unroll
-                            for (int j = 0; j < 16; j++) {
-                                const int r = 32 * b + j;
-                                m[j] = !cv.edge || sees(r) ? __uint_as_float(v0[j]) : ninf;
-                                m[j + 16] = r + 16 < nr && (!cv.edge || sees(r + 16)) ? __uint_as_float(v1[j]) : ninf;
-                            }
-                            const float top = al_reduce32<true>(m, lane);
-                            S.red[warp][32 * b + lane] = top;
-                        }
-                    al_bar();
-                    if (tid < nr) {
-                        const float m = fmaxf(fmaxf(S.red[0][tid], S.red[1][tid]), fmaxf(S.red[2][tid], S.red[3][tid]));
-                        const float old = S.mc[tid];
-                        const float mc = m > ninf ? fmaxf(__fmul_rn(m, D.c), old) : old;
-                        S.mc[tid] = mc;
-                        S.alpha[tid] = old == kNoKey ? 0.0f : al_ex2(__fsub_rn(old, mc));
+                    for (int j = 0; j < 16; j++) m[j] = s[j];
+                    const float top = al_reduce16<true>(m, lane);
+                    if (lane < 16) S.red[warp & 3][r0 + lane] = top;
+                    al_bar(wg);
+                    if (t < 16) {
+                        const int r = r0 + t;
+                        const float mx = fmaxf(fmaxf(S.red[0][r], S.red[1][r]), fmaxf(S.red[2][r], S.red[3][r]));
+                        const float old = S.mc[r], mc = mx > ninf ? fmaxf(__fmul_rn(mx, D.c), old) : old;
+                        S.mc[r] = mc;
+                        S.alpha[r] = old == kNoKey ? 0.0f : al_ex2(__fsub_rn(old, mc));
                     }
-                    al_bar();
-                    if (i > 0) {
+                    al_bar(wg);
 #pragma unroll
-                        for (int r = 0; r < R; r++)
-                            if (r < nr) lsum[r] = __fmul_rn(lsum[r], S.alpha[r]);
-                        // O^T: the products of the chunk before are in
-                        al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort);
-                        __syncwarp();
-                        tc_fence_after();
-                        for (int dh = 0; dh < nDH; dh++)
-                            for (int b = 0; b * 16 < nr; b++) {
-                                uint32_t v[16];
-                                const uint32_t to = tl + (uint32_t)((2 + dh) * R + 16 * b);
-                                tm_ld16(to, v);
-#pragma unroll
-                                for (int j = 0; j < 16; j++)
-                                    v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), S.alpha[16 * b + j]));
-                                tm_st16(to, v);
-                            }
-                        tm_wait_st();
-                    }
+                    for (int j = 0; j < 16; j++) lsum[j] = __fmul_rn(lsum[j], S.alpha[r0 + j]);
                 }
-                // the weights, as three bf16 terms, a key's rows side by side
+                // (a masked score stays minus infinity, the weight 0)
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    s[j] = al_ex2(__fmaf_rn(s[j], D.c, -S.mc[r0 + j]));
+                    lsum[j] = __fadd_rn(lsum[j], s[j]);
+                }
                 if (i > 0) al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort);  // P is read
                 __syncwarp();
-                const uint32_t prow = smem_addr(ps) + (uint32_t)(tid * C::kPPitch);
-                const uint32_t px = R == 64 ? (uint32_t)(tid & 7) : (uint32_t)((tid >> 1) & 3);
+                // the weights, as three bf16 terms, a key's rows side by side
+                {
+                    const uint32_t prow = smem_addr(ps) + (uint32_t)(t * L.pitch);
+                    const uint32_t px = L.pitch == 128 ? (uint32_t)(t & 7) : (uint32_t)((t >> 1) & 3);
 #pragma unroll
-                for (int b = 0; b < R / 16; b++)
-                    if (b * 16 < nr) {
-                        uint32_t v[16];
-                        tm_ld16(ts + 16 * b, v);
-                        float w16[16];
-#pragma unroll
-                        for (int j = 0; j < 16; j++) {
-                            const float x = __fmaf_rn(__uint_as_float(v[j]), D.c, -S.mc[16 * b + j]);
-                            w16[j] = !cv.edge || sees(16 * b + j) ? al_ex2(x) : 0.0f;
-                            lsum[16 * b + j] = __fadd_rn(lsum[16 * b + j], w16[j]);
-                        }
-#pragma unroll
-                        for (int q = 0; q < 2; q++) {
-                            uint4 h, m, l;
-                            al_split2(w16[8 * q], w16[8 * q + 1], h.x, m.x, l.x);
-                            al_split2(w16[8 * q + 2], w16[8 * q + 3], h.y, m.y, l.y);
-                            al_split2(w16[8 * q + 4], w16[8 * q + 5], h.z, m.z, l.z);
-                            al_split2(w16[8 * q + 6], w16[8 * q + 7], h.w, m.w, l.w);
-                            const uint32_t at = prow + ((((uint32_t)(2 * b + q)) ^ px) << 4);
-                            sts128(at, h);
-                            sts128(at + C::kPTerm, m);
-                            sts128(at + 2 * C::kPTerm, l);
-                        }
+                    for (int q = 0; q < 2; q++) {
+                        uint4 h, m, l;
+                        al_split2(s[8 * q], s[8 * q + 1], h.x, m.x, l.x);
+                        al_split2(s[8 * q + 2], s[8 * q + 3], h.y, m.y, l.y);
+                        al_split2(s[8 * q + 4], s[8 * q + 5], h.z, m.z, l.z);
+                        al_split2(s[8 * q + 6], s[8 * q + 7], h.w, m.w, l.w);
+                        const uint32_t at = prow + ((((uint32_t)(2 * wg + q)) ^ px) << 4);
+                        sts128(at, h);
+                        sts128(at + L.pterm, m);
+                        sts128(at + 2 * L.pterm, l);
                     }
+                }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(&S.p_ready);
-                if (cv.edge) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.p_ready);
+                if (wg == 0 && cv.edge) {
                     // the values of keys that not every row sees
                     const int gv = g + min(i + 2, n) * nK + i * nV;
                     const bool any = cv.any(key), all = cv.all(key);
-                    bool bad = false;
                     for (int vs = 0; vs < nV; vs++) {
-                        const int s = (gv + vs) % C::kSlots;
-                        al_wait(&S.full[s], (uint32_t)((gv + vs) / C::kSlots) & 1u, &S.abort);
-                        if (!all && (tid >> 6) == vs / nDH) {
-                            const uint32_t row = smem_addr(ring + s * C::kSlot) + (uint32_t)((tid & 63) * 128);
+                        const int sl = (gv + vs) % slots;
+                        al_wait(&S.full[sl], (uint32_t)((gv + vs) / slots) & 1u, &S.abort);
+                        if (!all && (t >> 6) == vs / nDH) {
+                            const uint32_t row = smem_addr(ring + sl * C::kSlot) + (uint32_t)((t & 63) * 128);
                             bool nf = !any;
-                            if (any)
+                            if (any) {
+#pragma unroll 4
                                 for (int q = 0; q < 16; q++) {
                                     const int d = (vs % nDH) * 128 + 8 * q;
                                     // a row of 64 dims is 8 groups of 16 bytes, swizzled by the row
-                                    const uint32_t at = row + (q >> 3) * 8192 + (((q & 7) ^ (tid & 7)) << 4);
                                     if (d < hd) {
-                                        uint4 v;
-                                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                                     : "r"(at));
+                                        const uint4 v = lds128_a(row + (q >> 3) * 8192 + (((q & 7) ^ (t & 7)) << 4));
                                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                                         for (int k = 0; k < 4; k++)
                                             nf |= (u[k] & 0x7f80u) == 0x7f80u || (u[k] & 0x7f800000u) == 0x7f800000u;
                                     }
                                 }
-                            if (nf) {
-                                bad |= any;
-                                for (int t = 0; t < NT; t++)
-                                    for (int q = 0; q < 16; q++)
-                                        sts128(row + t * C::kTerm + (q >> 3) * 8192 + ((q & 7) << 4), make_uint4(0, 0, 0, 0));
+                                if (nf)
+                                    for (int r = 0; r < p.nrows; r++)
+                                        if (sees(r)) S.nan[r] = 1;
                             }
+                            if (nf)
+                                for (int tt = 0; tt < NT; tt++)
+#pragma unroll 4
+                                    for (int q = 0; q < 16; q++)
+                                        sts128(row + tt * C::kTerm + (q >> 3) * 8192 + ((q & 7) << 4), make_uint4(0, 0, 0, 0));
                         }
                         fence_proxy_async_smem();
-                        mbar_arrive(&S.fixed[s]);
+                        mbar_arrive(&S.fixed[sl]);
                     }
-                    if (bad)
+                    __syncwarp();
+                }
+                if (i > 0) {
+                    tc_fence_after();
+                    take(it - 1);
+                    if (update)
 #pragma unroll
-                        for (int r = 0; r < R; r++)
-                            if (r < nr && sees(r)) lsum[r] = __int_as_float(0x7fc00000);
+                        for (int j = 0; j < 16; j++) {
+                            const float al = S.alpha[r0 + j];
+                            acc[0][j] = __fmul_rn(acc[0][j], al);
+                            acc[1][j] = __fmul_rn(acc[1][j], al);
+                        }
                 }
             }
             if (!ok) break;
             g += n * (nK + nV);
             // the sums over the keys
-#pragma unroll
-            for (int b = 0; b < R / 32; b++)
-                if (b * 32 < nr) {
-                    float v[32];
-#pragma unroll
-                    for (int j = 0; j < 32; j++) v[j] = lsum[32 * b + j];
-                    const float l = al_reduce32<false>(v, lane);
-                    S.red[warp][32 * b + lane] = l;
-                }
-            if (al_bar_or(!al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort))) {
+            const float l4 = al_reduce16<false>(lsum, lane);
+            if (lane < 16) S.red[warp & 3][r0 + lane] = l4;
+            if (al_bar_or(wg, !al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const bool direct = p.whole && D.streams == 1;
-            const int64_t prow0 = p.whole ? (int64_t)2 * D.grid * D.cap + (int64_t)p.t.stream * A.n_lanes * A.n_heads
+            const int64_t prow0 = p.whole ? (int64_t)2 * D.grid * D.cap + (int64_t)p.t->stream * A.n_lanes * A.n_heads
                                           : (int64_t)(2 * blockIdx.x + (p.head ? 0 : 1)) * D.cap;
-            if (tid < p.nrows) {
-                const float l = S.red[0][tid] + S.red[1][tid] + S.red[2][tid] + S.red[3][tid];
-                S.alpha[tid] = direct ? (l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l)) : 1.0f;
-                if (!direct) W.ml[prow0 + (p.whole ? S.rowid[tid] : tid)] = make_float2(S.mc[tid], l);
+            const int rows = min(16, p.nrows - r0);
+            if (t < rows) {
+                const int r = r0 + t;
+                float l = (S.red[0][r] + S.red[1][r]) + (S.red[2][r] + S.red[3][r]);
+                if (S.nan[r]) l = __int_as_float(0x7fc00000);
+                S.alpha[r] = direct ? (l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l)) : 1.0f;
+                if (!direct) W.ml[prow0 + (p.whole ? S.rowid[r] : r)] = make_float2(S.mc[r], l);
             }
-            al_bar();
-            for (int dh = 0; dh < nDH; dh++) {
-                const int d = dh * 128 + tid;
-                for (int b = 0; b * 16 < p.nrows; b++) {
-                    uint32_t v[16];
-                    tm_ld16(tl + (uint32_t)((2 + dh) * R + 16 * b), v);
-#pragma unroll
-                    for (int j = 0; j < 16; j++) {
-                        const int r = 16 * b + j;
-                        if (r < p.nrows && d < hd) {
-                            const int64_t id = S.rowid[r];
-                            float *o = direct ? A.out + id * hd : W.part + (prow0 + (p.whole ? id : r)) * hd;
-                            o[d] = __fmul_rn(__uint_as_float(v[j]), S.alpha[r]);
-                        }
-                    }
-                }
-            }
+            take(it - 1);
             tc_fence_before();
+            al_bar(wg);
+#pragma unroll
+            for (int j = 0; j < 16; j++)
+                if (j < rows) {
+                    const int r = r0 + j;
+                    const int64_t id = S.rowid[r];
+                    const float al = S.alpha[r];
+                    float *o = direct ? A.out + id * hd : W.part + (prow0 + (p.whole ? id : r)) * hd;
+                    if (t < hd) o[t] = __fmul_rn(acc[0][j], al);
+                    if (t + 128 < hd) o[t + 128] = __fmul_rn(acc[1][j], al);
+                }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4)
+    if (warp == C::kMma)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
 }
 
 // ------------------------------------------------------------------ merging partial tiles
 constexpr int kMergeThreads = 256;
 
-// One (lane, head) after the other: the pieces of its tiles by the weights
-// 2^(maximum - largest maximum); zeros where there are none.
+// The (lane, head)s in blocks of 256: first every thread finds out whether its
+// own is finished already, then the block takes the others one after the
+// other: the pieces of their tiles by the weights 2^(maximum - largest
+// maximum), zeros where there are none.  All but the partial sums themselves
+// is read while the kernel before still runs.
 __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDims D, AlWs W) {
     __shared__ float w[2 * kMaxCtas];
-    __shared__ int64_t row[2 * kMaxCtas];
     __shared__ float red[8];
     __shared__ float4 acc[kMergeThreads];
+    __shared__ int todo[kMergeThreads];
+    __shared__ int4 what[kMergeThreads][2];  // per stream: pieces, first CTA, row of its partial rows, its slot
+    __shared__ int count;
+    __shared__ AlSelfPlan plan;
+    __shared__ AlSelfScratch x;
     const int tid = threadIdx.x, warp = tid >> 5, lane_t = tid & 31, hd = A.hd;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t U = __ldcg(&W.head->units), G = __ldcg(&W.head->grid);
     const int total = A.n_lanes * A.n_heads;
-    for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
-        const int lane = idx / A.n_heads, h = idx - lane * A.n_heads;
-        const int kvh = h / D.group, hg = h - kvh * D.group, hb = hg / D.R;
-        int n = 0;
-        bool done = false;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    AlPlan P{W.head, nullptr, W.tile_of, W.tiles};
+    if (A.n_lanes <= kSelfPlan) {
+        if (warp == 0)
+            make_plan<32, kSelfPlan / 32>(A, D, x.pos, x.seq, x.pre, nullptr, &plan.head, &plan.first, kMaxCtas, x.tile_of,
+                                          plan.tiles, nullptr);
+        P = AlPlan{&plan.head, nullptr, x.tile_of, plan.tiles};
         __syncthreads();
-        for (int st = 2 - D.streams; st < 2; st++) {
-            const int ti = __ldcg(&W.tile_of[(int64_t)st * A.n_lanes + lane]);
-            if (ti < 0) continue;
-            const AlTile *t = W.tiles + ti;
-            const int nch = __ldcg(&t->nch);
-            if (nch == 0) continue;
-            const int gs = D.HB == 1 ? D.group : min(D.R, D.group - hb * D.R);
-            const int r = (lane - __ldcg(&t->lane0)) * gs + hg - hb * D.R;
-            const int64_t u0 = __ldcg(&t->unit0) + (int64_t)(kvh * D.HB + hb) * nch, u1 = u0 + nch;
-            const int b0 = (int)(((u0 + 1) * G - 1) / U), b1 = (int)((u1 * G - 1) / U);
-            if (b0 == b1 && D.streams == 1) {
-                done = true;
-                break;
+    }
+    const int64_t U = P.head->units, G = P.head->grid;
+    bool waited = false;
+    for (int base = blockIdx.x * D.merge; base < total; base += gridDim.x * D.merge) {
+        __syncthreads();
+        if (tid == 0) count = 0;
+        __syncthreads();
+        const int mine = base + tid;
+        if (tid < D.merge && mine < total) {
+            const int lane = mine / A.n_heads, h = mine - lane * A.n_heads;
+            const int kvh = h / D.group, hg = h - kvh * D.group, hb = hg / D.R;
+            bool done = false;
+            int4 y[2];
+#pragma unroll
+            for (int st = 0; st < 2; st++) {
+                y[st] = make_int4(0, 0, 0, 0);
+                if (st < 2 - D.streams) continue;
+                const int ti = P.tile_of[(int64_t)st * A.n_lanes + lane];
+                if (ti < 0) continue;
+                const AlTile *t = P.tiles + ti;
+                const int nch = t->nch;
+                if (nch == 0) continue;
+                const int gs = D.HB == 1 ? D.group : min(D.R, D.group - hb * D.R);
+                const int r = (lane - t->lane0) * gs + hg - hb * D.R;
+                const int64_t u0 = t->unit0 + (int64_t)(kvh * D.HB + hb) * nch, u1 = u0 + nch;
+                const int b0 = (int)(((u0 + 1) * G - 1) / U), b1 = (int)((u1 * G - 1) / U);
+                if (b0 == b1)
+                    done = D.streams == 1, y[st] = make_int4(1, -1, 0, 0);
+                else
+                    y[st] = make_int4(b1 - b0 + 1, b0, r, U * b0 / G >= u0 ? 0 : 1);
             }
-            for (int b = b0 + tid; b <= b1; b += kMergeThreads) {
-                const bool head = U * b / G >= u0;
-                row[n + b - b0] = b0 == b1 ? (int64_t)2 * D.grid * D.cap + (int64_t)st * total + idx
-                                           : (int64_t)(2 * b + (head ? 0 : 1)) * D.cap + r;
+            if (!done) {
+                const int k = atomicAdd(&count, 1);
+                todo[k] = mine;
+                what[k][0] = y[0], what[k][1] = y[1];
             }
-            n += b1 - b0 + 1;
         }
-        if (done) continue;
-        float *o = A.out + (int64_t)idx * hd;
-        if (n == 0) {
-            for (int d = tid; d < hd; d += kMergeThreads) o[d] = 0.0f;
-            continue;
+        __syncthreads();
+        if (!waited) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            waited = true;
         }
-        __syncthreads();
-        float m = kNoKey, l[2] = {0.0f, 0.0f}, mi[2];
-#pragma unroll
-        for (int k = 0; k < 2; k++)
-            if (tid + k * kMergeThreads < n) {
-                const float2 v = __ldcg(&W.ml[row[tid + k * kMergeThreads]]);
-                mi[k] = v.x, l[k] = v.y;
-                m = fmaxf(m, v.x);
+        for (int k = 0; k < count; k++) {
+            const int idx = todo[k];
+            const int4 a0 = what[k][0], a1 = what[k][1];
+            const int n = a0.x + a1.x;
+            float4 *o = reinterpret_cast<float4 *>(A.out + (int64_t)idx * hd);
+            if (n == 0) {
+                for (int d = tid; d < hd / 4; d += kMergeThreads) o[d] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                continue;
             }
-        m = warp_max(m);
-        if (lane_t == 0) red[warp] = m;
-        __syncthreads();
+            // the partial row of piece q: CTA b0's own slot, the first slot of the CTAs behind it
+            auto row = [&](int q) -> int64_t {
+                const int st = q < a0.x ? 0 : 1;
+                const int4 x = st ? a1 : a0;
+                const int b = st ? q - a0.x : q;
+                return x.y < 0 ? (int64_t)2 * D.grid * D.cap + (int64_t)st * total + idx
+                               : (int64_t)(2 * (x.y + b) + (b == 0 ? x.w : 0)) * D.cap + x.z;
+            };
+            __syncthreads();
+            float m = kNoKey, l[2] = {0.0f, 0.0f}, mi[2];
 #pragma unroll
-        for (int k = 0; k < 8; k++) m = fmaxf(m, red[k]);
-        float sum = 0.0f;
+            for (int e = 0; e < 2; e++)
+                if (tid + e * kMergeThreads < n) {
+                    const float2 v = __ldcg(&W.ml[row(tid + e * kMergeThreads)]);
+                    mi[e] = v.x, l[e] = v.y;
+                    m = fmaxf(m, v.x);
+                }
+            m = warp_max(m);
+            if (lane_t == 0) red[warp] = m;
+            __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 2; k++)
-            if (tid + k * kMergeThreads < n) {
-                const float x = mi[k] == kNoKey ? 0.0f : al_ex2(__fsub_rn(mi[k], m));
-                w[tid + k * kMergeThreads] = x;
-                sum += x * l[k];
-            }
-        sum = warp_psum(sum);
-        __syncthreads();
-        if (lane_t == 0) red[warp] = sum;
-        __syncthreads();
-        sum = 0.0f;
+            for (int e = 0; e < 8; e++) m = fmaxf(m, red[e]);
+            float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; k++) sum += red[k];
-        // thread: four dims, every `groups`-th piece
-        const int nv = hd / 4, groups = kMergeThreads / nv, gi = tid / nv, dv = tid - gi * nv;
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (gi < groups)
-#pragma unroll 4
-            for (int k = gi; k < n; k += groups) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(W.part + row[k] * hd) + dv);
-                const float x = w[k];
-                a.x += v.x * x, a.y += v.y * x, a.z += v.z * x, a.w += v.w * x;
+            for (int e = 0; e < 2; e++)
+                if (tid + e * kMergeThreads < n) {
+                    const float x = mi[e] == kNoKey ? 0.0f : al_ex2(__fsub_rn(mi[e], m));
+                    w[tid + e * kMergeThreads] = x;
+                    sum += x * l[e];
+                }
+            sum = warp_psum(sum);
+            __syncthreads();
+            if (lane_t == 0) red[warp] = sum;
+            __syncthreads();
+            sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; e++) sum += red[e];
+            // thread: four dims, every `groups`-th piece
+            const int nv = hd / 4, groups = kMergeThreads / nv, gi = tid / nv, dv = tid - gi * nv;
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (gi < groups)
+#pragma unroll 8
+                for (int q = gi; q < n; q += groups) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(W.part + row(q) * hd) + dv);
+                    const float x = w[q];
+                    a.x += v.x * x, a.y += v.y * x, a.z += v.z * x, a.w += v.w * x;
+                }
+            acc[tid] = a;
+            __syncthreads();
+            if (tid < nv) {
+                for (int e = 1; e < min(groups, n); e++) {
+                    const float4 v = acc[e * nv + tid];
+                    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+                }
+                const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+                o[tid] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
             }
-        acc[tid] = a;
-        __syncthreads();
-        if (tid < nv) {
-            for (int k = 1; k < min(groups, n); k++) {
-                const float4 v = acc[k * nv + tid];
-                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-            }
-            const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-            reinterpret_cast<float4 *>(o)[tid] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
         }
     }
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ host
@@ -1169,9 +1293,10 @@ qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t work
     D.cap = (int64_t)A.n_lanes * D.group < D.R ? A.n_lanes * D.group : D.R;
     D.streams = A.pre.k ? 2 : 1;
     D.grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+    D.merge = A.n_lanes <= kSelfPlan ? 1 : kMergeThreads;
     D.c = (float)(1.4426950408889634 / std::sqrt((double)A.hd));
     const void *kern = f32 ? (const void *)al_attn_kernel<3> : (const void *)al_attn_kernel<1>;
-    const size_t smem = f32 ? al_smem<3>() : al_smem<1>(), plan_smem = 3 * sizeof(int) * (size_t)A.n_lanes;
+    const size_t smem = kAlSmem, plan_smem = 3 * sizeof(int) * (size_t)A.n_lanes;
     QLIN_REQUIRE((int)smem <= max_smem_optin(), QLIN_ERR_UNSUPPORTED, "%s: shared memory", fn);
     blocks_per_sm(kern, smem);  // raises the dynamic shared-memory limit once
     blocks_per_sm((const void *)al_plan_kernel, plan_smem);
@@ -1184,15 +1309,16 @@ qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t work
         }
     cudaStream_t st = (cudaStream_t)stream;
     void *pargs[] = {(void *)&A, (void *)&D, (void *)&w};
-    if (qlin_status e = launch_pdl((const void *)al_plan_kernel, dim3(1), dim3(kPlanThreads), plan_smem, st, pargs,
-                                   "al_plan_kernel"))
-        return e;
+    if (A.n_lanes > kSelfPlan)
+        if (qlin_status e = launch_pdl((const void *)al_plan_kernel, dim3(1), dim3(kPlanThreads), plan_smem, st, pargs,
+                                       "al_plan_kernel"))
+            return e;
     void *args[] = {(void *)&maps, (void *)&A, (void *)&D, (void *)&w};
     if (qlin_status e = launch_pdl(kern, dim3(D.grid), dim3(f32 ? AlCfg<3>::kThreads : AlCfg<1>::kThreads), smem, st, args,
                                    "al_attn_kernel"))
         return e;
-    const int64_t total = (int64_t)A.n_lanes * A.n_heads;
-    return launch_pdl((const void *)al_merge_kernel, dim3((unsigned)(total < 8 * D.grid ? total : 8 * D.grid)),
+    const int64_t total = (int64_t)A.n_lanes * A.n_heads, blocks = (total + D.merge - 1) / D.merge;
+    return launch_pdl((const void *)al_merge_kernel, dim3((unsigned)(blocks < 8 * D.grid ? blocks : 8 * D.grid)),
                       dim3(kMergeThreads), 0, st, pargs, "al_merge_kernel");
 }
 
