@@ -170,6 +170,24 @@ def test_long_context(dev, kind):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("H,n_kv,hd", [(2, 2, 64), (4, 1, 256), (96, 2, 64)])
+def test_many_blocks_per_sm(dev, kind, H, n_kv, hd):
+    # each SM runs through many blocks of keys and several tiles: single tokens of 40 users at long contexts
+    # together with a chunk of a prompt (a sample of the lanes is compared)
+    S, R = 41, 8000
+    kv = Caches(dev, kind, S, R, n_kv, hd, 13, layers=1)
+    pos = [R - 1 - 37 * i for i in range(40)] + list(range(3000, 3300))
+    seqs = list(range(40)) + [40] * 300
+    for window, sinks in ((0, 0), (1500, 200)):
+        c = Call(dev, len(pos), H, n_kv, hd)
+        c.lanes(kv, _i32(pos, dev), _i32(seqs, dev), window, sinks)
+        got, q = c.result(), c.q.cpu().numpy()
+        for i in [0, 1, 17, 39, 40, 41, 100, 200, 338, 339]:
+            k, v = kv.host(seqs[i])
+            _close(got[i], _ref(q[i], k, v, pos[i], window, sinks, n_kv))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_unseen_rows_never_reach_the_outputs(dev, kind):
     import torch
 

@@ -9,7 +9,7 @@
 // zeros where no key is seen.
 //
 // One product for every use.  The rows of a tile are the query heads of one KV
-// head for up to 64 lanes (32 with fp32 caches) that read the same sequence:
+// head for up to 48 lanes (32 with fp32 caches) that read the same sequence:
 // the lanes of a prompt chunk, the beams of a prompt, or one lane alone.  The
 // keys and values are the large operand, so they take the tensor cores' 128
 // rows and the tile's rows the columns:
@@ -22,7 +22,9 @@
 // values enter as three bf16 terms x = hi + mid + lo (24 bits), a bf16 cache's
 // as they are; the products of terms whose orders add to at most two are
 // accumulated (three for a bf16 cache, six for an fp32 one; what is left out
-// is below 2^-24 of the product).
+// is below 2^-24 of the product).  The rows' terms stand side by side as the
+// columns of one product, in the order of their size, so that a cached term is
+// read once for all of them and each order has a sum of its own.
 //
 // A pass over the keys with a running maximum: the rows go to warpgroups, 16
 // each, and thread t of one owns key t of a 128-key chunk (a tensor-memory
@@ -31,8 +33,7 @@
 // otherwise weights relative to the maximum in use stay below 2^8 and nothing
 // needs rescaling.  The sums stay in each thread's registers until the end,
 // and so do the outputs: the tensor cores' accumulation rounds toward zero, so
-// they sum over one chunk only, and a score's main products (hi x hi) are
-// summed apart from the small ones.
+// they sum over one chunk only.
 //
 // Work is dealt out by 128-key chunks: every CTA (one per SM) takes an equal
 // run of the (tile, KV head, chunk) units, so a long sequence is split over
@@ -130,56 +131,42 @@ __device__ __forceinline__ float al_ex2(float x) {
 }
 
 // ------------------------------------------------------------------ the plan
-constexpr int kPlanThreads = 1024, kPlanPer = kMaxLanes / kPlanThreads;
-constexpr int kSelfPlan = 64;  // lanes up to which every CTA plans for itself, on one warp
+constexpr int kPlanThreads = 1024;
+constexpr int kSelfPlan = 64;  // lanes up to which every CTA plans for itself, a thread for each
 
 struct AlSelfPlan {  // in shared memory
     AlPlanHead head;
     AlTile tiles[2 * kSelfPlan];
     int first;
 };
+
+// a * b / c for 0 <= b < c
+__device__ __forceinline__ int64_t muldiv(int64_t a, int b, int c) {
+    const int64_t p = a * b;
+    return (p >> 32) ? p / c : (int64_t)((uint32_t)p / (uint32_t)c);
+}
+
+struct PlanRed {
+    int64_t sum[32];
+    int last[32];
+};
 struct AlSelfScratch {
     int tile_of[2 * kSelfPlan];
     int pos[kSelfPlan], seq[kSelfPlan], pre[kSelfPlan];
+    PlanRed red;
 };
 
-// Scans over T consecutive threads (a warp, or a whole block; all call them):
-// the reduction of the threads before this one, and of all.
-template <int T, bool MAX>
-__device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t init, int64_t *red, int64_t &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t in = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, in, off);
-        if (lane >= off) in = MAX ? max(in, o) : in + o;
-    }
-    int64_t ex = __shfl_up_sync(0xffffffffu, in, 1);
-    if (lane == 0) ex = init;
-    if (T == 32) {
-        total = __shfl_sync(0xffffffffu, in, 31);
-        return ex;
-    }
-    __syncthreads();
-    if (lane == 31) red[warp] = in;
-    __syncthreads();
-    total = init;
-    for (int w = 0; w < T / 32; w++) {
-        if (w == warp) ex = MAX ? max(ex, total) : ex + total;
-        total = MAX ? max(total, red[w]) : total + red[w];
-    }
-    return ex;
-}
-
 // Checks the lanes, cuts them into tiles and deals the units out.  T threads
-// (T == 32: one warp) with PER consecutive lanes each; spos (-1: no lane),
-// sseq, spre: [n_lanes] scratch.  first: the first tile of CTA `cta`, or of
-// every CTA if that is negative.
-template <int T, int PER>
-__device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int *spos, int *sseq, int *spre, int64_t *red,
+// of the block, the first ones, take T lanes at a time (barrier 1 among them);
+// spos (-1: no lane), sseq, spre: [n_lanes] scratch.  first: the first tile of
+// CTA `cta`, or of every CTA if that is negative.
+template <int T>
+__device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int *spos, int *sseq, int *spre, PlanRed &red,
                                           AlPlanHead *head, int *first, int cta, int *tile_of, AlTile *tiles_out,
                                           int32_t *status) {
-    const int tid = T == 32 ? (int)(threadIdx.x & 31) : (int)threadIdx.x, n = A.n_lanes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = A.n_lanes;
+    auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(T) : "memory"); };
+#pragma unroll 1
     for (int i = tid; i < n; i += T) {
         const int p = A.positions[i], s = A.seqs[i];
         int f = 0, P = 0;
@@ -196,109 +183,104 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
         sseq[i] = s;
         spre[i] = f;
     }
-    if (T == 32)
-        __syncwarp();
-    else
-        __syncthreads();
-    int64_t units = 0, tu0[2][PER], tun[2][PER];
-    int tiles = 0, rmax = 0, tix[2][PER];
-    const int i0 = tid * PER;
-#pragma unroll
-    for (int st = 0; st < 2; st++) {
-#pragma unroll
-        for (int e = 0; e < PER; e++) tun[st][e] = tu0[st][e] = 0, tix[st][e] = 0;
-        if (st == 0 && D.streams == 1) continue;
+    int64_t units = 0;
+    int tiles = 0, rmax = 0;
+#pragma unroll 1
+    for (int st = 2 - D.streams; st < 2; st++) {
         auto same = [&](int a, int b) { return spre[a] == spre[b] && (st == 0 || sseq[a] == sseq[b]); };
-        // where each lane's run of lanes of one sequence starts
-        int rs[PER], last = -1;
-#pragma unroll
-        for (int e = 0; e < PER; e++) {
-            const int i = i0 + e;
-            if (i < n && spos[i] >= 0 && (i == 0 || spos[i - 1] < 0 || !same(i, i - 1))) last = i;
-            rs[e] = last;
-        }
-        int64_t tot;
-        const int before = (int)plan_scan<T, true>(last, -1, red, tot);
-        int nt = 0;
-#pragma unroll
-        for (int e = 0; e < PER; e++) {
-            const int i = i0 + e;
-            if (rs[e] < 0) rs[e] = before;
-            rs[e] = i < n && spos[i] >= 0 ? (i - rs[e]) % D.LT : -1;  // the lane's place in its tile
-            nt += rs[e] == 0;
-        }
-        int64_t tot_t, tot_u, mine = 0;
-        int ti = tiles + (int)plan_scan<T, false>(nt, 0, red, tot_t);
-#pragma unroll
-        for (int e = 0; e < PER; e++) {
-            const int i = i0 + e;
-            if (rs[e] == 0) {
+        int run = -1;  // where the latest run of lanes of one sequence starts
+#pragma unroll 1
+        for (int base = 0; base < n; base += T) {
+            bar();
+            const int i = base + tid;
+            const bool valid = i < n && spos[i] >= 0;
+            const uint32_t starts =
+                __ballot_sync(0xffffffffu, valid && (i == 0 || spos[i - 1] < 0 || !same(i, i - 1)));
+            if (lane == 0) red.last[warp] = starts ? i + 31 - __clz(starts) : -1;
+            bar();
+            int rs = run;
+            for (int w = 0; w < warp; w++) rs = max(rs, red.last[w]);
+            for (int w = 0; w < T / 32; w++) run = max(run, red.last[w]);
+            const uint32_t upto = starts & (0xffffffffu >> (31 - lane));
+            if (upto) rs = i - lane + 31 - __clz(upto);
+            const bool start = valid && (i - rs) % D.LT == 0;
+            AlTile t;
+            int64_t tu = 0;
+            if (start) {
                 int nl = 0, pmin = INT_MAX, pmax = -1;
                 for (int j = i; j < n && nl < D.LT && spos[j] >= 0 && same(i, j); j++, nl++) {
                     pmin = min(pmin, spos[j]);
                     pmax = max(pmax, spos[j]);
                 }
+                // positions and rows are below 2^31, so differences fit
                 const int P = A.pre.k ? A.prefix_len[spre[i]] : 0;
-                const int64_t base = st == 0 ? 0 : P, lim = st == 0 ? P : A.own.rows;
-                const int64_t hi = min((int64_t)pmax - base, lim - 1);
-                const int64_t lo = A.window ? max((int64_t)0, (int64_t)pmin - A.window + 1 - base) : 0;
-                const int64_t sk = max((int64_t)0, min((int64_t)A.sinks - base, hi + 1));
-                const int64_t cf = lo / kChunk, main = lo <= hi ? hi / kChunk - cf + 1 : 0;
-                int64_t ns = A.window ? (sk + kChunk - 1) / kChunk : 0;
+                const int org = st == 0 ? 0 : P, lim = st == 0 ? P : A.own.rows;
+                const int hi = min(pmax - org, lim - 1);
+                const int lo = A.window && pmin - org >= A.window ? pmin - org - A.window + 1 : 0;
+                const int sk = A.window ? max(0, min(A.sinks - org, hi + 1)) : 0;
+                const int cf = lo / kChunk, main = lo <= hi ? hi / kChunk - cf + 1 : 0;
+                int ns = (sk + kChunk - 1) / kChunk;
                 if (main > 0) ns = min(ns, cf);
-                AlTile t;
-                t.unit0 = 0;
-                t.lane0 = i, t.nl = nl, t.stream = st, t.nch = (int)(ns + main), t.nsink = (int)ns, t.cfirst = (int)cf;
-                t.slot = st == 0 ? spre[i] : sseq[i], t.base = (int)base, t.lim = (int)lim;
+                t.lane0 = i, t.nl = nl, t.stream = st, t.nch = ns + main, t.nsink = ns, t.cfirst = cf;
+                t.slot = st == 0 ? spre[i] : sseq[i], t.base = org, t.lim = lim;
                 t.pmin = pmin, t.pmax = pmax, t.pad = 0;
-                tiles_out[ti] = t;
-                tix[st][e] = ti++;
-                tun[st][e] = (ns + main) * A.n_kv * D.HB;
-                mine += tun[st][e];
-                if (ns + main > 0) rmax = max(rmax, nl * min(D.group, D.R));
+                tu = (int64_t)t.nch * A.n_kv * D.HB;
+                if (t.nch > 0) rmax = max(rmax, nl * min(D.group, D.R));
             }
-            if (i < n) tile_of[(int64_t)st * n + i] = rs[e] >= 0 ? ti - 1 : -1;
-        }
-        int64_t u = units + plan_scan<T, false>(mine, 0, red, tot_u);
+            // tiles and units before this lane's, in one sum
+            const int64_t mine = ((int64_t)start << 48) | tu;
+            int64_t in = mine;
 #pragma unroll
-        for (int e = 0; e < PER; e++)
-            if (rs[e] == 0) {
-                tiles_out[tix[st][e]].unit0 = tu0[st][e] = u;
-                u += tun[st][e];
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, in, off);
+                if (lane >= off) in += o;
             }
-        tiles += (int)tot_t;
-        units += tot_u;
+            if (lane == 31) red.sum[warp] = in;
+            bar();
+            int64_t total = 0, before = in - mine;
+            for (int w = 0; w < T / 32; w++) {
+                if (w < warp) before += red.sum[w];
+                total += red.sum[w];
+            }
+            const int ti = tiles + (int)(before >> 48);
+            if (start) {
+                t.unit0 = units + (before & 0xffffffffffffll);
+                tiles_out[ti] = t;
+            }
+            if (i < n) tile_of[(int64_t)st * n + i] = valid ? ti - (start ? 0 : 1) : -1;
+            tiles += (int)(total >> 48);
+            units += total & 0xffffffffffffll;
+        }
     }
     if (D.streams == 1)
         for (int i = tid; i < n; i += T) tile_of[i] = -1;
-    int64_t widest;
-    plan_scan<T, true>(rmax, 0, red, widest);
+    rmax = __reduce_max_sync(0xffffffffu, rmax);
+    if (lane == 0) red.last[warp] = rmax;
+    bar();
+    for (int w = 0; w < T / 32; w++) rmax = max(rmax, red.last[w]);
     // CTA b takes the units [U b / grid, U (b + 1) / grid): at least one each
-    const int64_t grid = min((int64_t)D.grid, units);
-    if (tid == 0) head->units = units, head->grid = (int)grid, head->rmax = (int)widest;
-#pragma unroll
-    for (int st = 0; st < 2; st++)
-#pragma unroll
-        for (int e = 0; e < PER; e++)
-            if (tun[st][e] > 0) {
-                const int64_t u0 = tu0[st][e], u1 = u0 + tun[st][e];
-                if (cta >= 0) {
-                    const int64_t u = units * cta / grid;
-                    if (cta < grid && u >= u0 && u < u1) *first = tix[st][e];
-                } else {
-                    for (int64_t b = (u0 * grid + units - 1) / units; b < grid && units * b / grid < u1; b++)
-                        first[b] = tix[st][e];
-                }
-            }
+    const int grid = (int)min((int64_t)D.grid, units);
+    if (tid == 0) head->units = units, head->grid = grid, head->rmax = rmax;
+    const int64_t own = cta >= 0 && cta < grid ? muldiv(units, cta, grid) : -1;
+#pragma unroll 1
+    for (int i = tid; i < tiles; i += T) {
+        const int64_t u0 = tiles_out[i].unit0, u1 = u0 + (int64_t)tiles_out[i].nch * A.n_kv * D.HB;
+        if (cta >= 0) {
+            if (own >= u0 && own < u1) *first = i;
+        } else if (u0 < u1) {
+            for (int64_t b = (u0 * grid + units - 1) / units; b < grid && muldiv(units, (int)b, grid) < u1; b++)
+                first[b] = i;
+        }
+    }
 }
 
 // One CTA plans for all.
 __global__ void __launch_bounds__(kPlanThreads) al_plan_kernel(AlArgs A, AlDims D, AlWs W) {
     extern __shared__ int pl_smem[];  // [3][n_lanes]
-    __shared__ int64_t red[32];
+    __shared__ PlanRed red;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    make_plan<kPlanThreads, kPlanPer>(A, D, pl_smem, pl_smem + A.n_lanes, pl_smem + 2 * A.n_lanes, red, W.head, W.first, -1,
+    make_plan<kPlanThreads>(A, D, pl_smem, pl_smem + A.n_lanes, pl_smem + 2 * A.n_lanes, red, W.head, W.first, -1,
                                       W.tile_of, W.tiles, A.status);
 }
 
@@ -326,8 +308,8 @@ struct Walker {
         const int G = P.head->grid;
         u0 = u = hi = 0;
         if ((int)blockIdx.x < G) {
-            u0 = u = U * blockIdx.x / G;
-            hi = U * (blockIdx.x + 1) / G;
+            u0 = u = muldiv(U, (int)blockIdx.x, G);
+            hi = (int)blockIdx.x + 1 == G ? U : muldiv(U, (int)blockIdx.x + 1, G);
             at = P.tiles + *P.first;
         }
     }
@@ -359,17 +341,20 @@ struct ChunkView {
     bool edge;                    // not all of its keys are
     __device__ __forceinline__ ChunkView(const Piece &p, int c, const AlArgs &A) {
         r0 = (c < p.t->nsink ? c : p.t->cfirst + c - p.t->nsink) * kChunk;
-        any_hi = (int)min((int64_t)p.t->pmax - p.t->base, (int64_t)p.t->lim - 1);
-        all_hi = (int)min((int64_t)p.t->pmin - p.t->base, (int64_t)p.t->lim - 1);
+        const int pmin = p.t->pmin - p.t->base, pmax = p.t->pmax - p.t->base, last = p.t->lim - 1;
+        any_hi = min(pmax, last);
+        all_hi = min(pmin, last);
         any_lo = all_lo = -1;
         sk = 0;
         if (A.window) {
-            any_lo = (int)max((int64_t)-1, (int64_t)p.t->pmin - A.window - p.t->base);
-            all_lo = (int)max((int64_t)-1, (int64_t)p.t->pmax - A.window - p.t->base);
+            any_lo = pmin >= A.window ? pmin - A.window : -1;
+            all_lo = pmax >= A.window ? pmax - A.window : -1;
             sk = max(0, A.sinks - p.t->base);
         }
         edge = !(r0 + kChunk - 1 <= all_hi && (r0 > all_lo || r0 + kChunk - 1 < sk));
     }
+    // whether some row of the tile may not see one of the rows [a, b)
+    __device__ __forceinline__ bool edge_in(int a, int b) const { return !(b - 1 <= all_hi && (a > all_lo || b - 1 < sk)); }
     __device__ __forceinline__ bool any(int r) const { return r <= any_hi && (r > any_lo || r < sk); }
     __device__ __forceinline__ bool all(int r) const { return r <= all_hi && (r > all_lo || r < sk); }
     // whether some row of the tile may see one of the rows [a, b)
@@ -382,23 +367,23 @@ struct ChunkView {
 // NT: bf16 terms of a cached value (1: bf16 cache, 3: fp32 cache)
 template <int NT>
 struct AlCfg {
-    static constexpr int R = NT == 1 ? 64 : 32;     // rows of a tile at most
+    static constexpr int R = NT == 1 ? 48 : 32;     // rows of a tile at most
     static constexpr int kWg = R / 16;              // warpgroups, 16 rows each
     static constexpr int kTerm = 16384;             // 128 keys x 64 dims, or 64 keys x 128 dims, in bf16
     static constexpr int kSlot = NT * kTerm;
     static constexpr int kMma = 4 * kWg;            // the warp that issues the MMAs; the producers follow it
     static constexpr int kProd = NT == 1 ? 1 : 8;   // producer warps
     static constexpr int kThreads = 32 * (kMma + 1 + kProd);
-    static constexpr uint32_t kCols = 8 * R;        // S^T main and small, twice; O^T (two halves of dims) twice
-    static constexpr uint32_t kSmall = 2 * R, kO = 4 * R;
+    static constexpr uint32_t kCols = 512;          // S^T [3 R], then O^T's two halves of dims [3 R] each
+    static constexpr uint32_t kO = 3 * R;
     static constexpr int kMaxSlots = NT == 1 ? 12 : 3;
 };
 
 template <int NT>
 struct AlCtl {
     using C = AlCfg<NT>;
-    uint64_t full[C::kMaxSlots], empty[C::kMaxSlots], fixed[C::kMaxSlots];
-    uint64_t s_full[2], p_ready, q_ready, pv_done, drain;
+    uint64_t full[C::kMaxSlots], empty[C::kMaxSlots];
+    uint64_t s_full, s_free, p_ready, q_ready, pv_done, fix_go, fixed, drain;
     int rowid[C::R];  // lane * n_heads + head
     int rowlo[C::R], rowhi[C::R];  // a row sees the keys <= rowhi that are > rowlo or first ones
     int nan[C::R];    // it sees a value that is not finite and was replaced
@@ -410,38 +395,48 @@ struct AlCtl {
 };
 constexpr int kAlSmem = 227 * 1024;  // all of an SM's: one CTA per SM
 
-// Shared memory: ring slots, then the rows' q (4 x 64 dims, three terms, rows
-// of 128 bytes), then the weights P (three terms of 128 keys' rows), then the
-// control block.  Rc: the widest tile's rows, rounded up to 16, 32 or 64.
+// Shared memory: ring slots, then the rows' q (per 64 dims the three terms'
+// rows, of 128 swizzled bytes), then the weights P (the terms' rows in blocks
+// of 32, each [128 keys][64 swizzled bytes]), then the control block.  Rc: the
+// widest tile's rows, rounded up to 16s.
 template <int NT>
 struct AlLayout {
-    int Rc, qblock, pitch, pterm, slots;
+    int q, qslice, p, slots;
     __device__ __forceinline__ AlLayout(int rmax, int hd) {
-        Rc = rmax <= 16 ? 16 : rmax <= 32 ? 32 : 64;
-        qblock = Rc * 128;
-        pitch = Rc == 64 ? 128 : 64;  // bytes of a key's weights, one term
-        pterm = kChunk * pitch;
-        const int left = kAlSmem - 1024 - (int)sizeof(AlCtl<NT>) - (hd + 63) / 64 * 3 * qblock - 3 * pterm;
-        slots = min(left / AlCfg<NT>::kSlot, AlCfg<NT>::kMaxSlots);
+        const int Rc = max(16, (rmax + 15) / 16 * 16);
+        qslice = 3 * Rc * 128;
+        const int qb = (hd + 63) / 64 * qslice, pb = (3 * Rc + 31) / 32 * (kChunk * 64);
+        slots = min((kAlSmem - 1024 - (int)sizeof(AlCtl<NT>) - qb - pb) / AlCfg<NT>::kSlot, AlCfg<NT>::kMaxSlots);
+        q = slots * AlCfg<NT>::kSlot;
+        p = q + qb;
     }
-    __device__ __forceinline__ int q() const { return slots * AlCfg<NT>::kSlot; }
-    __device__ __forceinline__ int p(int hd) const { return q() + (hd + 63) / 64 * 3 * qblock; }
 };
-static_assert(kAlSmem - 1024 - (int)sizeof(AlCtl<1>) - 4 * 3 * 64 * 128 - 3 * 128 * 128 >= 4 * 16384, "ring of four");
+static_assert(kAlSmem - 1024 - (int)sizeof(AlCtl<1>) - 4 * 3 * 48 * 128 - 5 * 128 * 64 >= 6 * 16384, "ring of six");
 static_assert(kAlSmem - 1024 - (int)sizeof(AlCtl<3>) - 4 * 3 * 32 * 128 - 3 * 128 * 64 >= 3 * 49152, "ring of three");
 
-// descriptor version 1; layout 2: 128-byte swizzle, 4: 64-byte
-__device__ __forceinline__ uint64_t al_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
-           (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)layout << 61;
-}
-__device__ __forceinline__ void al_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// Shared-memory matrix descriptors as two words, so that a step inside an
+// operand is one 32-bit addition.  Low: address and leading byte offset (both
+// in 16 bytes); high: stride byte offset, version 1, layout (2: 128-byte
+// swizzle, 4: 64-byte).
+__device__ __forceinline__ uint32_t al_desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4) << 16; }
+__device__ __forceinline__ uint32_t al_desc_hi(uint32_t sbo, uint32_t layout) { return (sbo >> 4) | 1u << 14 | layout << 29; }
+__device__ __forceinline__ void al_mma(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                                       bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.u32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
+}
+// One thread of the (converged) warp, chosen so that the compiler knows it is
+// one: behind a test of the lane number it wraps every MMA, whose operands are
+// uniform registers, in a loop over lanes (about 100 cycles each).
+__device__ __forceinline__ bool al_elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ void al_tma(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(
@@ -485,6 +480,10 @@ __device__ __forceinline__ uint4 lds128_a(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+
 // Every lane's values of 16 columns -> lane l the reduction of column l % 16 over the warp.
 template <bool MAX>
 __device__ __forceinline__ float al_reduce16(float (&v)[16], int lane) {
@@ -521,6 +520,14 @@ __device__ __forceinline__ void al_ld32(const float *p, bool on, uint4 &a, uint4
         "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%8];\n\t"
         "@p ld.global.nc.L1::no_allocate.v4.u32 {%4,%5,%6,%7}, [%8+16];\n\t}"
         : "+r"(a.x), "+r"(a.y), "+r"(a.z), "+r"(a.w), "+r"(b.x), "+r"(b.y), "+r"(b.z), "+r"(b.w)
+        : "l"(p), "r"((uint32_t)on));
+}
+__device__ __forceinline__ void al_ld16(const float *p, bool on, uint4 &a) {
+    a = make_uint4(0, 0, 0, 0);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "+r"(a.x), "+r"(a.y), "+r"(a.z), "+r"(a.w)
         : "l"(p), "r"((uint32_t)on));
 }
 // eight values as three 16-byte groups of bf16 terms
@@ -596,15 +603,16 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         for (int s = 0; s < C::kMaxSlots; s++) {
             mbar_init(&S.full[s], C::kProd);
             mbar_init(&S.empty[s], 1);
-            mbar_init(&S.fixed[s], 128);
         }
-        mbar_init(&S.s_full[0], 1);
-        mbar_init(&S.s_full[1], 1);
+        mbar_init(&S.s_full, 1);
+        mbar_init(&S.s_free, 4 * C::kWg);
         // every warpgroup's warps arrive for every chunk and piece, with rows in it or not: no wait can then be
         // two phases behind
         mbar_init(&S.p_ready, 4 * C::kWg);
         mbar_init(&S.q_ready, 4 * C::kWg);
         mbar_init(&S.pv_done, 1);
+        mbar_init(&S.fix_go, 1);
+        mbar_init(&S.fixed, 4);
         mbar_init(&S.drain, 1);
         S.abort = 0;
         fence_mbar_init();
@@ -614,8 +622,8 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     AlPlan P{W.head, W.first + blockIdx.x, W.tile_of, W.tiles};
     if (A.n_lanes <= kSelfPlan) {
         AlSelfScratch &x = *reinterpret_cast<AlSelfScratch *>(smem);  // (the ring is not in use yet)
-        if (warp == 0) {
-            make_plan<32, kSelfPlan / 32>(A, D, x.pos, x.seq, x.pre, nullptr, &S.plan.head, &S.plan.first, blockIdx.x,
+        if (tid < kSelfPlan) {
+            make_plan<kSelfPlan>(A, D, x.pos, x.seq, x.pre, x.red, &S.plan.head, &S.plan.first, blockIdx.x,
                                           x.tile_of, S.plan.tiles, blockIdx.x == 0 ? A.status : nullptr);
             fence_proxy_async_smem();
         }
@@ -627,12 +635,12 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     const uint32_t tmem = S.tmem;
     const AlLayout<NT> L(P.head->rmax, hd);
     const int slots = L.slots;
-    uint8_t *const ring = smem, *const qs = ring + L.q(), *const ps = ring + L.p(hd);
+    uint8_t *const ring = smem, *const qs = ring + L.q, *const ps = ring + L.p;
 
     if (warp > C::kMma) {
         // ---------------------------------------------------------- producers
         if constexpr (NT == 1) {
-            if (lane == 0) {
+            if (al_elect()) {
                 SliceGen sg(A, P, D);
                 RingPos at;
                 int g = 0;
@@ -672,8 +680,9 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                         mbar_wait(&S.full[k % slots], (uint32_t)(k / slots) & 1u);
             }
         } else {
-            // 32 rows of 8 dims at a time: thread t takes row t / 8, dims 8 (t % 8) ..; four such passes are a
-            // slice's 128 rows (a V slice's rows 64 .. 127 are the second 64 dims of its 64 keys)
+            // 32 rows at a time: thread t takes row t / 8, dims 4 (t % 8) .. + 3 and the same 32 dims on (eight
+            // threads read 128 bytes of a row at once); four such passes are a slice's 128 rows (a V slice's rows
+            // 64 .. 127 are the second 64 dims of its 64 keys)
             const int pt = tid - 32 * (C::kMma + 1), pr = pt >> 3, pc = pt & 7;
             uint4 buf[2][8];
             auto load = [&](SliceGen &sg, uint4 (&o)[8]) {
@@ -681,13 +690,16 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 const ChunkView cv(p, sg.chunk(), A);
                 const qlin_kv &kv = p.t->stream ? A.own : A.pre;
                 const float *src = static_cast<const float *>(sg.v ? kv.v : kv.k) + (int64_t)p.t->slot * kv.seq_stride +
-                                   p.kvh * hd + 8 * pc;
+                                   p.kvh * hd + 4 * pc;
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const int r = e * 32 + pr;
                     const int key = cv.r0 + (sg.v ? (sg.sl / nDH) * 64 + (r & 63) : r);
                     const int d = sg.v ? (sg.sl % nDH) * 128 + (r >> 6) * 64 : sg.sl * 64;
-                    al_ld32(src + (int64_t)key * kv.row_stride + d, d + 8 * pc < hd && cv.any(key), o[2 * e], o[2 * e + 1]);
+                    const float *a = src + (int64_t)key * kv.row_stride + d;
+                    const bool any = cv.any(key);
+                    al_ld16(a, any && d + 4 * pc < hd, o[2 * e]);
+                    al_ld16(a + 32, any && d + 32 + 4 * pc < hd, o[2 * e + 1]);
                 }
             };
             SliceGen sg(A, P, D);
@@ -716,12 +728,17 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         const int r = e * 32 + pr;
-                        uint4 h, m, l;
-                        al_split8(buf[k][2 * e], buf[k][2 * e + 1], h, m, l);
-                        const uint32_t a = to + (uint32_t)(r * 128 + ((pc ^ (r & 7)) << 4));
-                        sts128(a, h);
-                        sts128(a + C::kTerm, m);
-                        sts128(a + 2 * C::kTerm, l);
+#pragma unroll
+                        for (int q = 0; q < 2; q++) {
+                            const uint4 v = buf[k][2 * e + q];
+                            uint2 h, m, l;
+                            al_split2(__uint_as_float(v.x), __uint_as_float(v.y), h.x, m.x, l.x);
+                            al_split2(__uint_as_float(v.z), __uint_as_float(v.w), h.y, m.y, l.y);
+                            const uint32_t a = to + (uint32_t)(r * 128 + (((4 * q + (pc >> 1)) ^ (r & 7)) << 4) + (pc & 1) * 8);
+                            sts64(a, h);
+                            sts64(a + C::kTerm, m);
+                            sts64(a + 2 * C::kTerm, l);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -737,44 +754,44 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         }
     } else if (warp == C::kMma) {
         // ---------------------------------------------------------- the MMAs
-        if (lane == 0) {
+        if (al_elect()) {
             Walker w(P);
             Piece p;
             RingPos at;
             int it = 0, np = 0;   // chunks and pieces so far
-            uint32_t fixpar = 0;  // parities by slot
+            uint32_t fixes = 0;   // slices of V handed to the first warpgroup so far
             bool ok = true;
             const uint32_t ring_a = smem_addr(ring), qs_a = smem_addr(qs), ps_a = smem_addr(ps);
-            const uint32_t playout = L.pitch == 128 ? 2u : 4u;
+            const uint32_t hi128 = al_desc_hi(1024, 2), hip = al_desc_hi(512, 4);
             for (; ok && w.next(p, A, D); np++) {
-                const int n = p.c1 - p.c0, wgs = (p.nrows + 15) / 16;
-                const uint32_t N = 16u * (uint32_t)wgs;
-                // fp32 accumulator, bf16 operands; S^T: both K-major, O^T: both with the keys as rows
-                const uint32_t ids = (1u << 4) | (1u << 7) | (1u << 10) | (N >> 3) << 17 | (128u >> 4) << 24;
+                const int n = p.c1 - p.c0;
+                const uint32_t nr = (uint32_t)(p.nrows + 15) / 16 * 16;
+                // fp32 accumulator, bf16 operands, N = the terms' rows; S^T: both operands K-major, O^T: both with
+                // the keys as rows.  Term t of a cached value meets the 3 - t first terms of the rows, whose columns
+                // start at the products' order t.
+                const uint32_t ids = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 4) << 24;
                 const uint32_t idp = ids | (1u << 15) | (1u << 16);
                 if (!(ok = al_wait(&S.q_ready, (uint32_t)np & 1u, &S.abort))) break;
                 for (int i = 0; ok && i <= n; i++) {
                     if (i < n) {
-                        const uint32_t d = tmem + (uint32_t)((it + i) & 1) * R;
+                        if (it + i > 0 && !(ok = al_wait(&S.s_free, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
                         for (int sl = 0; sl < nK; sl++, at.step(slots)) {
                             const int s = at.s;
                             if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
                             tc_fence_after();
                             const int steps = min(64, hd - sl * 64) / 16;
-                            const uint32_t a0 = ring_a + s * C::kSlot, b0 = qs_a + sl * 3 * L.qblock;
-                            for (int kk = 0; kk < steps; kk++)
+                            const uint32_t a0 = al_desc_lo(ring_a + s * C::kSlot, 16), b0 = al_desc_lo(qs_a + sl * L.qslice, 16);
 #pragma unroll
-                                for (int t = 0; t < NT; t++)
+                            for (int kk = 0; kk < 4; kk++)
+                                if (kk < steps)
 #pragma unroll
-                                    for (int u = 0; u < 3 - t; u++)
-                                        // (each accumulator's first product: hi x hi, and hi x mid)
-                                        al_mma(d + (t + u ? C::kSmall : 0u), al_desc(a0 + t * C::kTerm + 32 * kk, 16, 1024, 2),
-                                               al_desc(b0 + u * L.qblock + 32 * kk, 16, 1024, 2), ids,
-                                               sl > 0 || kk > 0 || t > 0 || u > 1);
+                                    for (int t = 0; t < NT; t++)
+                                        al_mma(tmem + t * nr, a0 + (uint32_t)(t * C::kTerm / 16 + 2 * kk), hi128, b0 + 2u * kk,
+                                               hi128, ids | ((3 - t) * nr >> 3) << 17, kk > 0 || t > 0 || sl > 0);
                             tc_commit(&S.empty[s]);
                         }
                         if (!ok) break;
-                        tc_commit(&S.s_full[(it + i) & 1]);
+                        tc_commit(&S.s_full);
                     }
                     if (i >= 1) {
                         const ChunkView cv(p, p.c0 + i - 1, A);
@@ -782,23 +799,21 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                         for (int vs = 0; vs < nV; vs++, at.step(slots)) {
                             const int s = at.s, kh = vs / nDH, dh = vs % nDH;
                             if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
-                            if (cv.edge) {
-                                if (!(ok = al_wait(&S.fixed[s], (fixpar >> s) & 1u, &S.abort))) break;
-                                fixpar ^= 1u << s;
+                            if (cv.edge_in(cv.r0 + 64 * kh, cv.r0 + 64 * kh + 64)) {
+                                mbar_arrive(&S.fix_go);
+                                if (!(ok = al_wait(&S.fixed, fixes & 1u, &S.abort))) break;
+                                fixes++;
                             }
                             tc_fence_after();
-                            const uint32_t d = tmem + C::kO + (uint32_t)(((it + i - 1) & 1) * 2 + dh) * R;
-                            const uint32_t a0 = ring_a + s * C::kSlot, b0 = ps_a + kh * 64 * L.pitch;
-                            // the small products first: the accumulation rounds toward zero
+                            const uint32_t d = tmem + C::kO + (uint32_t)dh * 3 * R;
+                            const uint32_t a0 = al_desc_lo(ring_a + s * C::kSlot, 8192);
+                            const uint32_t b0 = al_desc_lo(ps_a + kh * 64 * 64, kChunk * 64);
 #pragma unroll
-                            for (int o = 2; o >= 0; o--)
+                            for (int ks = 0; ks < 4; ks++)
 #pragma unroll
                                 for (int t = 0; t < NT; t++)
-                                    if (o - t >= 0)
-                                        for (int ks = 0; ks < 4; ks++)
-                                            al_mma(d, al_desc(a0 + t * C::kTerm + 2048 * ks, 8192, 1024, 2),
-                                                   al_desc(b0 + (o - t) * L.pterm + ks * 16 * L.pitch, 16, 8 * L.pitch, playout),
-                                                   idp, kh > 0 || ks > 0 || t > 0 || o < 2);
+                                    al_mma(d + t * nr, a0 + (uint32_t)(t * C::kTerm / 16 + 128 * ks), hi128, b0 + 64u * ks, hip,
+                                           idp | ((3 - t) * nr >> 3) << 17, ks > 0 || t > 0 || kh > 0);
                             tc_commit(&S.empty[s]);
                         }
                         if (!ok) break;
@@ -820,18 +835,20 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         const int wg = warp >> 2, t = tid & 127, r0 = 16 * wg;
         Walker w(P);
         Piece p;
-        int g = 0, it = 0;  // slices and chunks so far
+        int g = 0, it = 0;   // slices and chunks so far
+        uint32_t fixes = 0;  // slices of V looked through
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)r0;
         const float ninf = -__int_as_float(0x7f800000);
         bool ok = true;
         while (ok && w.next(p, A, D)) {
-            const int n = p.c1 - p.c0;
+            const int n = p.c1 - p.c0, nr = (p.nrows + 15) / 16 * 16;
             if (r0 >= p.nrows) {  // (the first warpgroup always has rows)
                 if (lane == 0) mbar_arrive(&S.q_ready);
                 for (int i = 0; i < n && ok; i++, it++) {
-                    if (lane == 0) mbar_arrive(&S.p_ready);
+                    ok = al_wait(&S.s_full, (uint32_t)it & 1u, &S.abort);
+                    if (lane == 0) mbar_arrive(&S.s_free), mbar_arrive(&S.p_ready);
                     // (a second arrival must not meet the same phase)
-                    ok = al_wait(&S.pv_done, (uint32_t)it & 1u, &S.abort);
+                    ok = ok && al_wait(&S.pv_done, (uint32_t)it & 1u, &S.abort);
                     __syncwarp();
                 }
                 ok = __all_sync(0xffffffffu, ok);
@@ -849,17 +866,17 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 S.nan[r] = 0;
             }
             al_bar(wg);
-            // the rows' q as three bf16 terms, 64 dims after 64 dims, rows of 128 swizzled bytes
+            // the rows' q as three bf16 terms
+#pragma unroll 2
             for (int e = t; e < 2 * hd; e += 128) {
-                const int r = r0 + e / (hd / 8), d8 = e % (hd / 8), id = S.rowid[r];
+                const int rr = e / (hd / 8), d8 = e - rr * (hd / 8), r = r0 + rr, id = S.rowid[r];
                 uint4 a, b, h, m, l;
                 al_ld32(A.q + (int64_t)max(id, 0) * hd + 8 * d8, id >= 0, a, b);
                 al_split8(a, b, h, m, l);
-                const uint32_t at = smem_addr(qs) + (uint32_t)((d8 >> 3) * 3 * L.qblock + r * 128 +
-                                                               (((d8 & 7) ^ (r & 7)) << 4));
+                const uint32_t at = smem_addr(qs) + (uint32_t)((d8 >> 3) * L.qslice + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
                 sts128(at, h);
-                sts128(at + L.qblock, m);
-                sts128(at + 2 * L.qblock, l);
+                sts128(at + nr * 128, m);
+                sts128(at + 2 * nr * 128, l);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -867,37 +884,43 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             float lsum[16], acc[2][16];
 #pragma unroll
             for (int j = 0; j < 16; j++) lsum[j] = acc[0][j] = acc[1][j] = 0.0f;
-            // adds chunk c's products to the outputs
-            auto take = [&](int c) {
-                const uint32_t to = tl + C::kO + (uint32_t)((c & 1) * 2 * R);
-                uint32_t v[16];
-                tm_ld16(to, v);
+            // 16 columns' terms of the products: (lo + mid) + hi
+            auto sum3 = [&](uint32_t at, float (&o)[16]) {
+                uint32_t h[16], m[16];
+                tm_ld16_nw(at + 2 * nr, h);
+                tm_ld16_nw(at + nr, m);
+                tm_wait_ld(h);
+                tm_wait_ld(m);
 #pragma unroll
-                for (int j = 0; j < 16; j++) acc[0][j] = __fadd_rn(acc[0][j], __uint_as_float(v[j]));
+                for (int j = 0; j < 16; j++) o[j] = __fadd_rn(__uint_as_float(h[j]), __uint_as_float(m[j]));
+                tm_ld16(at, h);
+#pragma unroll
+                for (int j = 0; j < 16; j++) o[j] = __fadd_rn(o[j], __uint_as_float(h[j]));
+            };
+            // adds a chunk's products to the outputs
+            auto take = [&]() {
+                float o[16];
+                sum3(tl + C::kO, o);
+#pragma unroll
+                for (int j = 0; j < 16; j++) acc[0][j] = __fadd_rn(acc[0][j], o[j]);
                 if (nDH == 2) {
-                    tm_ld16(to + R, v);
+                    sum3(tl + C::kO + 3 * R, o);
 #pragma unroll
-                    for (int j = 0; j < 16; j++) acc[1][j] = __fadd_rn(acc[1][j], __uint_as_float(v[j]));
+                    for (int j = 0; j < 16; j++) acc[1][j] = __fadd_rn(acc[1][j], o[j]);
                 }
             };
 
             for (int i = 0; i < n; i++, it++) {
                 const ChunkView cv(p, p.c0 + i, A);
                 const int key = cv.r0 + t;
-                const bool fail = !al_wait(&S.s_full[it & 1], (uint32_t)(it >> 1) & 1u, &S.abort);
+                const bool fail = !al_wait(&S.s_full, (uint32_t)it & 1u, &S.abort);
                 __syncwarp();  // (the tensor-memory loads are for whole warps)
                 tc_fence_after();
                 float s[16];
-                {
-                    const uint32_t ts = tl + (uint32_t)(it & 1) * R;
-                    uint32_t a[16], b[16];
-                    tm_ld16_nw(ts, a);
-                    tm_ld16_nw(ts + C::kSmall, b);
-                    tm_wait_ld(a);
-                    tm_wait_ld(b);
-#pragma unroll
-                    for (int j = 0; j < 16; j++) s[j] = __fadd_rn(__uint_as_float(a[j]), __uint_as_float(b[j]));
-                }
+                sum3(tl, s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.s_free);
                 // whether row r of the tile sees this thread's key
                 auto sees = [&](int r) { return key <= S.rowhi[r] && (key > S.rowlo[r] || key < cv.sk); };
                 if (cv.edge)
@@ -942,24 +965,36 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     s[j] = al_ex2(__fmaf_rn(s[j], D.c, -S.mc[r0 + j]));
                     lsum[j] = __fadd_rn(lsum[j], s[j]);
                 }
-                if (i > 0) al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort);  // P is read
-                __syncwarp();
+                if (i > 0) {  // the products of the chunk before: P is read, and O^T is there
+                    al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort);
+                    __syncwarp();
+                }
                 // the weights, as three bf16 terms, a key's rows side by side
-                {
-                    const uint32_t prow = smem_addr(ps) + (uint32_t)(t * L.pitch);
-                    const uint32_t px = L.pitch == 128 ? (uint32_t)(t & 7) : (uint32_t)((t >> 1) & 3);
 #pragma unroll
-                    for (int q = 0; q < 2; q++) {
-                        uint4 h, m, l;
-                        al_split2(s[8 * q], s[8 * q + 1], h.x, m.x, l.x);
-                        al_split2(s[8 * q + 2], s[8 * q + 3], h.y, m.y, l.y);
-                        al_split2(s[8 * q + 4], s[8 * q + 5], h.z, m.z, l.z);
-                        al_split2(s[8 * q + 6], s[8 * q + 7], h.w, m.w, l.w);
-                        const uint32_t at = prow + ((((uint32_t)(2 * wg + q)) ^ px) << 4);
-                        sts128(at, h);
-                        sts128(at + L.pterm, m);
-                        sts128(at + 2 * L.pterm, l);
+                for (int q = 0; q < 2; q++) {
+                    uint4 w3[3];
+                    al_split2(s[8 * q], s[8 * q + 1], w3[0].x, w3[1].x, w3[2].x);
+                    al_split2(s[8 * q + 2], s[8 * q + 3], w3[0].y, w3[1].y, w3[2].y);
+                    al_split2(s[8 * q + 4], s[8 * q + 5], w3[0].z, w3[1].z, w3[2].z);
+                    al_split2(s[8 * q + 6], s[8 * q + 7], w3[0].w, w3[1].w, w3[2].w);
+#pragma unroll
+                    for (int u = 0; u < 3; u++) {
+                        const int c = u * nr + r0 + 8 * q;
+                        sts128(smem_addr(ps) + (uint32_t)((c >> 5) * (kChunk * 64) + t * 64 +
+                                                          ((((c >> 3) & 3) ^ ((t >> 1) & 3)) << 4)),
+                               w3[u]);
                     }
+                }
+                if (i > 0) {
+                    tc_fence_after();
+                    take();
+                    if (update)
+#pragma unroll
+                        for (int j = 0; j < 16; j++) {
+                            const float al = S.alpha[r0 + j];
+                            acc[0][j] = __fmul_rn(acc[0][j], al);
+                            acc[1][j] = __fmul_rn(acc[1][j], al);
+                        }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -970,8 +1005,11 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     const int gv = g + min(i + 2, n) * nK + i * nV;
                     const bool any = cv.any(key), all = cv.all(key);
                     for (int vs = 0; vs < nV; vs++) {
-                        const int sl = (gv + vs) % slots;
-                        al_wait(&S.full[sl], (uint32_t)((gv + vs) / slots) & 1u, &S.abort);
+                        const int sl = (gv + vs) % slots, k0 = cv.r0 + 64 * (vs / nDH);
+                        if (!cv.edge_in(k0, k0 + 64)) continue;
+                        // its turn: the slice has landed and its product waits
+                        al_wait(&S.fix_go, fixes & 1u, &S.abort);
+                        fixes++;
                         if (!all && (t >> 6) == vs / nDH) {
                             const uint32_t row = smem_addr(ring + sl * C::kSlot) + (uint32_t)((t & 63) * 128);
                             bool nf = !any;
@@ -999,20 +1037,10 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                                         sts128(row + tt * C::kTerm + (q >> 3) * 8192 + ((q & 7) << 4), make_uint4(0, 0, 0, 0));
                         }
                         fence_proxy_async_smem();
-                        mbar_arrive(&S.fixed[sl]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&S.fixed);
                     }
                     __syncwarp();
-                }
-                if (i > 0) {
-                    tc_fence_after();
-                    take(it - 1);
-                    if (update)
-#pragma unroll
-                        for (int j = 0; j < 16; j++) {
-                            const float al = S.alpha[r0 + j];
-                            acc[0][j] = __fmul_rn(acc[0][j], al);
-                            acc[1][j] = __fmul_rn(acc[1][j], al);
-                        }
                 }
             }
             if (!ok) break;
@@ -1036,7 +1064,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 S.alpha[r] = direct ? (l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l)) : 1.0f;
                 if (!direct) W.ml[prow0 + (p.whole ? S.rowid[r] : r)] = make_float2(S.mc[r], l);
             }
-            take(it - 1);
+            take();
             tc_fence_before();
             al_bar(wg);
 #pragma unroll
@@ -1079,8 +1107,8 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     AlPlan P{W.head, nullptr, W.tile_of, W.tiles};
     if (A.n_lanes <= kSelfPlan) {
-        if (warp == 0)
-            make_plan<32, kSelfPlan / 32>(A, D, x.pos, x.seq, x.pre, nullptr, &plan.head, &plan.first, kMaxCtas, x.tile_of,
+        if (tid < kSelfPlan)
+            make_plan<kSelfPlan>(A, D, x.pos, x.seq, x.pre, x.red, &plan.head, &plan.first, kMaxCtas, x.tile_of,
                                           plan.tiles, nullptr);
         P = AlPlan{&plan.head, nullptr, x.tile_of, plan.tiles};
         __syncthreads();
@@ -1113,7 +1141,7 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
                 if (b0 == b1)
                     done = D.streams == 1, y[st] = make_int4(1, -1, 0, 0);
                 else
-                    y[st] = make_int4(b1 - b0 + 1, b0, r, U * b0 / G >= u0 ? 0 : 1);
+                    y[st] = make_int4(b1 - b0 + 1, b0, r, muldiv(U, b0, (int)G) >= u0 ? 0 : 1);
             }
             if (!done) {
                 const int k = atomicAdd(&count, 1);
@@ -1209,7 +1237,7 @@ AlWs carve(int n_lanes, int n_heads, int n_kv, int hd, char *base) {
         return p;
     };
     const int64_t group = n_heads / n_kv;
-    const int64_t rows = (int64_t)2 * kMaxCtas * (n_lanes * group < 64 ? n_lanes * group : 64) +
+    const int64_t rows = (int64_t)2 * kMaxCtas * (n_lanes * group < 48 ? n_lanes * group : 48) +
                          (int64_t)2 * n_lanes * n_heads;
     w.head = (AlPlanHead *)take(sizeof(AlPlanHead));
     w.first = (int *)take(sizeof(int) * kMaxCtas);
