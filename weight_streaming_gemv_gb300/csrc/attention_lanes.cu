@@ -70,6 +70,7 @@ constexpr int kMaxLanes = 4096;
 constexpr int kStatusBadLane = 1;
 constexpr int kMaxCtas = 160;  // the workspace holds two partial tiles for each
 constexpr int kChunk = 128;    // keys per unit (MMA M)
+constexpr int kSetup = 2;      // units that a tile's start is counted as (its rows' q, the first scores, the outputs)
 constexpr float kNoKey = -1e30f;  // the running maximum of a row that has seen no key
 
 struct AlArgs {
@@ -85,7 +86,7 @@ struct AlArgs {
 // (stream 0: prompts, stream 1: the lanes' own caches).  Its chunks of that
 // sequence's rows are 0 .. nsink - 1 and then cfirst, cfirst + 1, ...
 struct __align__(16) AlTile {
-    int64_t unit0;  // its first unit; units go (KV head, head block, chunk), chunk fastest
+    int64_t unit0;  // its first unit; units go (KV head, head block, kSetup and then the chunks)
     int lane0, nl, stream, nch, nsink, cfirst;
     int slot;        // sequence (or prompt) in the stream's caches
     int base;        // position of the sequence's row 0
@@ -146,6 +147,10 @@ __device__ __forceinline__ int64_t muldiv(int64_t a, int b, int c) {
     return (p >> 32) ? p / c : (int64_t)((uint32_t)p / (uint32_t)c);
 }
 
+__device__ __forceinline__ int64_t tile_units(int nch, const AlArgs &A, const AlDims &D) {
+    return nch ? (int64_t)(nch + kSetup) * A.n_kv * D.HB : 0;
+}
+
 struct PlanRed {
     int64_t sum[32];
     int last[32];
@@ -198,9 +203,10 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
                 __ballot_sync(0xffffffffu, valid && (i == 0 || spos[i - 1] < 0 || !same(i, i - 1)));
             if (lane == 0) red.last[warp] = starts ? i + 31 - __clz(starts) : -1;
             bar();
-            int rs = run;
-            for (int w = 0; w < warp; w++) rs = max(rs, red.last[w]);
-            for (int w = 0; w < T / 32; w++) run = max(run, red.last[w]);
+            const int lw = lane < T / 32 ? red.last[lane] : -1;
+            const int rs0 = max(run, __reduce_max_sync(0xffffffffu, lane < warp ? lw : -1));
+            run = max(run, __reduce_max_sync(0xffffffffu, lw));
+            int rs = rs0;
             const uint32_t upto = starts & (0xffffffffu >> (31 - lane));
             if (upto) rs = i - lane + 31 - __clz(upto);
             const bool start = valid && (i - rs) % D.LT == 0;
@@ -224,7 +230,7 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
                 t.lane0 = i, t.nl = nl, t.stream = st, t.nch = ns + main, t.nsink = ns, t.cfirst = cf;
                 t.slot = st == 0 ? spre[i] : sseq[i], t.base = org, t.lim = lim;
                 t.pmin = pmin, t.pmax = pmax, t.pad = 0;
-                tu = (int64_t)t.nch * A.n_kv * D.HB;
+                tu = tile_units(t.nch, A, D);
                 if (t.nch > 0) rmax = max(rmax, nl * min(D.group, D.R));
             }
             // tiles and units before this lane's, in one sum
@@ -237,11 +243,13 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
             }
             if (lane == 31) red.sum[warp] = in;
             bar();
-            int64_t total = 0, before = in - mine;
-            for (int w = 0; w < T / 32; w++) {
-                if (w < warp) before += red.sum[w];
-                total += red.sum[w];
+            int64_t total = lane < T / 32 ? red.sum[lane] : 0, before = lane < warp ? total : 0;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                total += __shfl_xor_sync(0xffffffffu, total, off);
+                before += __shfl_xor_sync(0xffffffffu, before, off);
             }
+            before += in - mine;
             const int ti = tiles + (int)(before >> 48);
             if (start) {
                 t.unit0 = units + (before & 0xffffffffffffll);
@@ -264,7 +272,7 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
     const int64_t own = cta >= 0 && cta < grid ? muldiv(units, cta, grid) : -1;
 #pragma unroll 1
     for (int i = tid; i < tiles; i += T) {
-        const int64_t u0 = tiles_out[i].unit0, u1 = u0 + (int64_t)tiles_out[i].nch * A.n_kv * D.HB;
+        const int64_t u0 = tiles_out[i].unit0, u1 = u0 + tile_units(tiles_out[i].nch, A, D);
         if (cta >= 0) {
             if (own >= u0 && own < u1) *first = i;
         } else if (u0 < u1) {
@@ -295,41 +303,58 @@ struct AlPlan {
 // ------------------------------------------------------------------ the walk over a CTA's units
 struct Piece {
     const AlTile *t;  // (its fields are read where they are needed: registers are short)
-    int kvh, hb, c0, c1;  // chunks c0 .. c1 - 1 of the tile for KV head kvh, head block hb
+    int kvh, hb, c0, c1;  // chunks c0 .. c1 - 1 of the tile for KV head kvh, head block hb,
+    int rot;              // taken from c0 + rot on, around
     int nrows, gs;        // rows, and rows per lane
-    bool whole, head;     // all of its chunks; it is where the CTA's units start
+    bool whole;           // all of its chunks
+    __device__ __forceinline__ int chunk(int i) const {
+        const int c = c0 + rot + i;
+        return c < c1 ? c : c - (c1 - c0);
+    }
 };
 
+// Tiles of one sequence read the same chunks.  So that they read them at the
+// same time, once from memory and then from L2, every CTA takes its chunks in
+// the order of their number modulo the units of a CTA.
 struct Walker {
-    int64_t u0, u, hi;
+    int64_t u, hi;
+    int turn;  // units of a CTA
     const AlTile *at;
+    Walker() = default;
     __device__ __forceinline__ explicit Walker(const AlPlan &P) {
         const int64_t U = P.head->units;
         const int G = P.head->grid;
-        u0 = u = hi = 0;
+        u = hi = 0;
+        turn = 1;
         if ((int)blockIdx.x < G) {
-            u0 = u = muldiv(U, (int)blockIdx.x, G);
+            turn = (int)min(muldiv(U + G - 1, 1, G), (int64_t)INT_MAX);
+            u = muldiv(U, (int)blockIdx.x, G);
             hi = (int)blockIdx.x + 1 == G ? U : muldiv(U, (int)blockIdx.x + 1, G);
             at = P.tiles + *P.first;
         }
     }
     __device__ __forceinline__ bool next(Piece &p, const AlArgs &A, const AlDims &D) {
-        if (u >= hi) return false;
-        while (u >= at->unit0 + (int64_t)at->nch * A.n_kv * D.HB) at++;
-        const int nch = at->nch;
-        const int64_t r = u - at->unit0;  // within a tile: nch n_kv HB units
-        const int64_t sub = (r >> 31) ? r / nch : (int64_t)((uint32_t)r / (uint32_t)nch);
-        p.t = at;
-        p.kvh = (int)sub / D.HB;
-        p.hb = (int)sub - p.kvh * D.HB;
-        p.c0 = (int)(r - sub * nch);
-        p.c1 = (int)min((int64_t)nch, p.c0 + (hi - u));
-        p.gs = D.HB == 1 ? D.group : min(D.R, D.group - p.hb * D.R);
-        p.nrows = at->nl * p.gs;
-        p.whole = p.c0 == 0 && p.c1 == nch;
-        p.head = u == u0;
-        u += p.c1 - p.c0;
-        return true;
+        while (u < hi) {
+            while (u >= at->unit0 + tile_units(at->nch, A, D)) at++;
+            const int nch = at->nch, per = nch + kSetup;
+            const int64_t r = u - at->unit0;
+            const int64_t sub = (r >> 31) ? r / per : (int64_t)((uint32_t)r / (uint32_t)per);
+            const int v0 = (int)(r - sub * per), v1 = (int)min((int64_t)per, v0 + (hi - u));
+            u += v1 - v0;
+            if (v1 <= kSetup) continue;  // the next CTA starts it
+            p.t = at;
+            p.kvh = (int)sub / D.HB;
+            p.hb = (int)sub - p.kvh * D.HB;
+            p.c0 = max(v0 - kSetup, 0);
+            p.c1 = v1 - kSetup;
+            const int over = p.c0 % turn;
+            p.rot = over && turn - over < p.c1 - p.c0 ? turn - over : 0;
+            p.gs = D.HB == 1 ? D.group : min(D.R, D.group - p.hb * D.R);
+            p.nrows = at->nl * p.gs;
+            p.whole = p.c0 == 0 && p.c1 == nch;
+            return true;
+        }
+        return false;
     }
 };
 
@@ -357,10 +382,6 @@ struct ChunkView {
     __device__ __forceinline__ bool edge_in(int a, int b) const { return !(b - 1 <= all_hi && (a > all_lo || b - 1 < sk)); }
     __device__ __forceinline__ bool any(int r) const { return r <= any_hi && (r > any_lo || r < sk); }
     __device__ __forceinline__ bool all(int r) const { return r <= all_hi && (r > all_lo || r < sk); }
-    // whether some row of the tile may see one of the rows [a, b)
-    __device__ __forceinline__ bool any_in(int a, int b) const {
-        return a <= any_hi && (b - 1 > any_lo || a < sk);
-    }
 };
 
 // ------------------------------------------------------------------ the product
@@ -371,13 +392,26 @@ struct AlCfg {
     static constexpr int kWg = R / 16;              // warpgroups, 16 rows each
     static constexpr int kTerm = 16384;             // 128 keys x 64 dims, or 64 keys x 128 dims, in bf16
     static constexpr int kSlot = NT * kTerm;
-    static constexpr int kMma = 4 * kWg;            // the warp that issues the MMAs; the producers follow it
     static constexpr int kProd = NT == 1 ? 1 : 8;   // producer warps
-    static constexpr int kThreads = 32 * (kMma + 1 + kProd);
+    // after the warpgroups: MMA warp and producer (bf16), or two warpgroups of producers and one whose first warp
+    // issues the MMAs (fp32; registers are dealt out by warpgroup)
+    static constexpr int kMma = NT == 1 ? 4 * kWg : 4 * kWg + kProd;
+    static constexpr int kProd0 = NT == 1 ? kMma + 1 : 4 * kWg;
+    static constexpr int kThreads = 32 * (NT == 1 ? 4 * kWg + 2 : 4 * kWg + kProd + 4);
     static constexpr uint32_t kCols = 512;          // S^T [3 R], then O^T's two halves of dims [3 R] each
     static constexpr uint32_t kO = 3 * R;
     static constexpr int kMaxSlots = NT == 1 ? 12 : 3;
 };
+
+// What a producer warp needs to load a slice of an fp32 cache.
+struct __align__(16) AlSlice {
+    const float *src;  // its first row and dim; null: no more slices
+    int64_t stride;    // floats between rows
+    int y0, any_lo, any_hi, sk;  // its first row; the rows that are seen
+    int v, dims;       // a slice of V; dims from src on
+    int64_t pad;
+};
+constexpr int kSliceRing = 4;
 
 template <int NT>
 struct AlCtl {
@@ -390,6 +424,8 @@ struct AlCtl {
     float mc[C::R], alpha[C::R];
     float red[4][C::R];
     AlSelfPlan plan;
+    AlSlice slice[kSliceRing];
+    uint64_t sl_full[kSliceRing], sl_empty[kSliceRing];
     uint32_t tmem;
     int abort;
 };
@@ -438,11 +474,11 @@ __device__ __forceinline__ bool al_elect() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
-__device__ __forceinline__ void al_tma(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+__device__ __forceinline__ void al_tma(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-            "r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -546,19 +582,33 @@ struct AlMaps {
 // ring: K of chunk 0, then for every chunk K of the next one and its own V.
 struct SliceGen {
     Walker w;
-    Piece p;
-    int n, i, sl;
+    int any_lo, any_hi, sk, nsink, cfirst, stream, slot, kvh;
+    int n, c1, first;  // chunks first, first + 1, ... (around at c1)
+    int i, sl, r0;     // r0: the chunk's first row
     bool v, more;
     __device__ __forceinline__ SliceGen(const AlArgs &A, const AlPlan &P, const AlDims &D) : w(P) { piece(A, D); }
     __device__ __forceinline__ void piece(const AlArgs &A, const AlDims &D) {
+        Piece p;
         more = w.next(p, A, D);
-        n = p.c1 - p.c0;
+        if (!more) return;
+        const ChunkView cv(p, 0, A);
+        any_lo = cv.any_lo, any_hi = cv.any_hi, sk = cv.sk;
+        nsink = p.t->nsink, cfirst = p.t->cfirst, stream = p.t->stream, slot = p.t->slot, kvh = p.kvh;
+        n = p.c1 - p.c0, c1 = p.c1, first = p.c0 + p.rot;
         i = sl = 0;
         v = false;
+        place();
     }
-    __device__ __forceinline__ int chunk() const { return p.c0 + (v ? i - 1 : i); }
-    __device__ __forceinline__ void step(const AlArgs &A, const AlDims &D, int nK, int nV) {
-        if (++sl < (v ? nV : nK)) return;
+    __device__ __forceinline__ void place() {
+        int c = first + (v ? i - 1 : i);
+        if (c >= c1) c -= n;
+        r0 = (c < nsink ? c : cfirst + c - nsink) * kChunk;
+    }
+    // whether some row of the tile may see one of the rows [a, b)
+    __device__ __forceinline__ bool any_in(int a, int b) const { return a <= any_hi && (b - 1 > any_lo || a < sk); }
+    // whether a new piece begins
+    __device__ __forceinline__ bool step(const AlArgs &A, const AlDims &D, int nK, int nV) {
+        if (++sl < (v ? nV : nK)) return false;
         sl = 0;
         // step i: K of chunk i (if there is one), then V of chunk i - 1 (if there is one)
         if (!v && i >= 1) {
@@ -568,8 +618,13 @@ struct SliceGen {
         } else {
             i++;
             v = i >= n;
-            if (i > n) piece(A, D);
+            if (i > n) {
+                piece(A, D);
+                return true;
+            }
         }
+        place();
+        return false;
     }
 };
 
@@ -610,6 +665,10 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         // two phases behind
         mbar_init(&S.p_ready, 4 * C::kWg);
         mbar_init(&S.q_ready, 4 * C::kWg);
+        for (int s = 0; s < kSliceRing; s++) {
+            mbar_init(&S.sl_full[s], 1);
+            mbar_init(&S.sl_empty[s], C::kProd);
+        }
         mbar_init(&S.pv_done, 1);
         mbar_init(&S.fix_go, 1);
         mbar_init(&S.fixed, 4);
@@ -637,43 +696,39 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     const int slots = L.slots;
     uint8_t *const ring = smem, *const qs = ring + L.q, *const ps = ring + L.p;
 
-    if (warp > C::kMma) {
+    if (warp >= C::kProd0 && warp < C::kProd0 + C::kProd) {
         // ---------------------------------------------------------- producers
         if constexpr (NT == 1) {
             if (al_elect()) {
                 SliceGen sg(A, P, D);
                 RingPos at;
                 int g = 0;
-                for (; sg.more; g++) {
-                    const int s = at.s;
-                    if (at.round && !al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort)) {
+                while (sg.more) {
+                    const CUtensorMap *mk = &maps.k[sg.stream], *mv = &maps.v[sg.stream];
+                    const int z = (sg.stream ? A.own : A.pre).seq_stride ? sg.slot : 0, x0 = sg.kvh * hd;
+                    bool ok = true;
+                    for (bool fresh = false; !fresh; g++) {
+                        const int s = at.s;
+                        if (at.round && !(ok = al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort))) break;
+                        // two boxes of 64 keys x 64 dims, those that nobody sees left out: K's are the two halves
+                        // of the chunk, V's (of one half) the two halves of 128 dims
+                        const uint32_t to = smem_addr(ring + s * C::kSlot), full = smem_addr(&S.full[s]);
+                        const int kh = nDH == 2 ? sg.sl >> 1 : sg.sl, dh = nDH == 2 ? sg.sl & 1 : 0;
+                        const int d0 = sg.v ? 128 * dh : 64 * sg.sl, y0 = sg.r0 + (sg.v ? 64 * kh : 0);
+                        const bool on0 = sg.any_in(y0, y0 + 64);
+                        const bool on1 = sg.v ? on0 && d0 + 64 < hd : sg.any_in(y0 + 64, y0 + 128);
+                        mbar_arrive_expect_tx(&S.full[s], 8192u * ((uint32_t)on0 + (uint32_t)on1));
+                        const CUtensorMap *map = sg.v ? mv : mk;
+                        if (on0) al_tma(to, map, x0 + d0, y0, z, full);
+                        if (on1) al_tma(to + 8192, map, x0 + d0 + (sg.v ? 64 : 0), y0 + (sg.v ? 0 : 64), z, full);
+                        fresh = sg.step(A, D, nK, nV);
+                        at.step(slots);
+                    }
+                    if (!ok) {
                         S.abort = 1;
                         raise_status(A.status, kStatusTimeout);
                         break;
                     }
-                    const Piece &p = sg.p;
-                    const ChunkView cv(p, sg.chunk(), A);
-                    const CUtensorMap *map = sg.v ? &maps.v[p.t->stream] : &maps.k[p.t->stream];
-                    const qlin_kv &kv = p.t->stream ? A.own : A.pre;
-                    const int z = kv.seq_stride ? p.t->slot : 0;
-                    uint8_t *to = ring + s * C::kSlot;
-                    // two boxes of 64 keys x 64 dims, those that nobody sees left out: K's are the two halves of
-                    // the chunk, V's (of one half) the two halves of 128 dims
-                    int x[2], y[2];
-                    bool on[2];
-#pragma unroll
-                    for (int b = 0; b < 2; b++) {
-                        const int d = sg.v ? (sg.sl % nDH) * 128 + b * 64 : sg.sl * 64;
-                        x[b] = p.kvh * hd + d;
-                        y[b] = cv.r0 + (sg.v ? sg.sl / nDH : b) * 64;
-                        on[b] = d < hd && cv.any_in(y[b], y[b] + 64);
-                    }
-                    mbar_arrive_expect_tx(&S.full[s], 8192u * ((uint32_t)on[0] + (uint32_t)on[1]));
-#pragma unroll
-                    for (int b = 0; b < 2; b++)
-                        if (on[b]) al_tma(to + b * 8192, map, x[b], y[b], z, &S.full[s]);
-                    sg.step(A, D, nK, nV);
-                    at.step(slots);
                 }
                 if (*(volatile int *)&S.abort)  // the copies in flight
                     for (int k = max(0, g - slots); k < g; k++)
@@ -683,36 +738,38 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             // 32 rows at a time: thread t takes row t / 8, dims 4 (t % 8) .. + 3 and the same 32 dims on (eight
             // threads read 128 bytes of a row at once); four such passes are a slice's 128 rows (a V slice's rows
             // 64 .. 127 are the second 64 dims of its 64 keys)
-            const int pt = tid - 32 * (C::kMma + 1), pr = pt >> 3, pc = pt & 7;
+            const int pt = tid - 32 * C::kProd0, pr = pt >> 3, pc = pt & 7;
             uint4 buf[2][8];
-            auto load = [&](SliceGen &sg, uint4 (&o)[8]) {
-                const Piece &p = sg.p;
-                const ChunkView cv(p, sg.chunk(), A);
-                const qlin_kv &kv = p.t->stream ? A.own : A.pre;
-                const float *src = static_cast<const float *>(sg.v ? kv.v : kv.k) + (int64_t)p.t->slot * kv.seq_stride +
-                                   p.kvh * hd + 4 * pc;
+            int ds = 0;
+            uint32_t dpar = 0;
+            bool ok = true, have[2];
+            // the next slice of the ring of descriptions; false when there is none
+            auto load = [&](uint4 (&o)[8]) -> bool {
+                if (!(ok = al_wait(&S.sl_full[ds], dpar, &S.abort))) return false;
+                const AlSlice &q = S.slice[ds];
+                const bool more = q.src != nullptr;
+                if (more) {
+                    const int key0 = q.y0 + pr, dims = q.dims - 4 * pc, v = q.v;
+                    const int64_t step = 32 * q.stride;
+                    const float *a = q.src + pr * q.stride + 4 * pc;
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int r = e * 32 + pr;
-                    const int key = cv.r0 + (sg.v ? (sg.sl / nDH) * 64 + (r & 63) : r);
-                    const int d = sg.v ? (sg.sl % nDH) * 128 + (r >> 6) * 64 : sg.sl * 64;
-                    const float *a = src + (int64_t)key * kv.row_stride + d;
-                    const bool any = cv.any(key);
-                    al_ld16(a, any && d + 4 * pc < hd, o[2 * e]);
-                    al_ld16(a + 32, any && d + 32 + 4 * pc < hd, o[2 * e + 1]);
+                    for (int e = 0; e < 4; e++) {
+                        // K: 32 rows on; V: the other half of its 64 rows, then 64 dims on
+                        const int key = key0 + (v ? (e & 1) * 32 : e * 32), d = v ? (e >> 1) * 64 : 0;
+                        const bool any = key <= q.any_hi && (key > q.any_lo || key < q.sk);
+                        al_ld16(a, any && d < dims, o[2 * e]);
+                        al_ld16(a + 32, any && d + 32 < dims, o[2 * e + 1]);
+                        a = v && e == 1 ? a - step + 64 : a + step;
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.sl_empty[ds]);
+                if (++ds == kSliceRing) ds = 0, dpar ^= 1u;
+                return more;
             };
-            SliceGen sg(A, P, D);
+            have[0] = load(buf[0]);
+            have[1] = have[0] && load(buf[1]);
             RingPos at;
-            bool have[2] = {false, false};
-#pragma unroll
-            for (int k = 0; k < 2; k++)
-                if (sg.more) {
-                    load(sg, buf[k]);
-                    have[k] = true;
-                    sg.step(A, D, nK, nV);
-                }
-            bool ok = true;
             while (ok && have[0]) {
 #pragma unroll
                 for (int k = 0; k < 2; k++) {
@@ -744,17 +801,43 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&S.full[s]);
                     at.step(slots);
-                    have[k] = sg.more;
-                    if (sg.more) {
-                        load(sg, buf[k]);
-                        sg.step(A, D, nK, nV);
-                    }
+                    have[k] = have[k ^ 1] && load(buf[k]);
                 }
             }
         }
-    } else if (warp == C::kMma) {
+    } else if (warp >= C::kMma) {
         // ---------------------------------------------------------- the MMAs
-        if (al_elect()) {
+        // 640 threads are launched with 96 registers (61440 in all): 128 x 56 here, 256 x 112 for the weights and
+        // 256 x 96 for the producers make 60416
+        if constexpr (NT == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (NT == 3 && warp == C::kMma + 1 && al_elect()) {
+            // ------------------------------------------------------ describes the slices to the producers
+            SliceGen sg(A, P, D);
+            bool ok = true;
+            for (int g = 0; ok; g++) {
+                const int ds = g % kSliceRing;
+                if (g >= kSliceRing) ok = al_wait(&S.sl_empty[ds], (uint32_t)(g / kSliceRing - 1) & 1u, &S.abort);
+                if (!ok) break;
+                AlSlice &q = S.slice[ds];
+                if (!sg.more) {
+                    q.src = nullptr;
+                    mbar_arrive(&S.sl_full[ds]);
+                    break;
+                }
+                const qlin_kv &kv = sg.stream ? A.own : A.pre;
+                const int kh = nDH == 2 ? sg.sl >> 1 : sg.sl, dh = nDH == 2 ? sg.sl & 1 : 0;
+                const int d0 = sg.v ? 128 * dh : 64 * sg.sl, y0 = sg.r0 + (sg.v ? 64 * kh : 0);
+                q.src = static_cast<const float *>(sg.v ? kv.v : kv.k) + (int64_t)sg.slot * kv.seq_stride + sg.kvh * hd +
+                      y0 * kv.row_stride + d0;
+                q.stride = kv.row_stride;
+                q.y0 = y0, q.any_lo = sg.any_lo, q.any_hi = sg.any_hi, q.sk = sg.sk;
+                q.v = sg.v, q.dims = hd - d0;
+                mbar_arrive(&S.sl_full[ds]);
+                sg.step(A, D, nK, nV);
+            }
+            if (!ok) S.abort = 1;
+        }
+        if (warp == C::kMma && al_elect()) {
             Walker w(P);
             Piece p;
             RingPos at;
@@ -794,7 +877,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                         tc_commit(&S.s_full);
                     }
                     if (i >= 1) {
-                        const ChunkView cv(p, p.c0 + i - 1, A);
+                        const ChunkView cv(p, p.chunk(i - 1), A);
                         if (!(ok = al_wait(&S.p_ready, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
                         for (int vs = 0; vs < nV; vs++, at.step(slots)) {
                             const int s = at.s, kh = vs / nDH, dh = vs % nDH;
@@ -832,6 +915,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     } else {
         // ---------------------------------------------------------- weights and sums: warpgroup wg owns rows
         // 16 wg .. 16 wg + 15, its thread t key t of a chunk, and of the outputs dims t and t + 128
+        if constexpr (NT == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         const int wg = warp >> 2, t = tid & 127, r0 = 16 * wg;
         Walker w(P);
         Piece p;
@@ -911,7 +995,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             };
 
             for (int i = 0; i < n; i++, it++) {
-                const ChunkView cv(p, p.c0 + i, A);
+                const ChunkView cv(p, p.chunk(i), A);
                 const int key = cv.r0 + t;
                 const bool fail = !al_wait(&S.s_full, (uint32_t)it & 1u, &S.abort);
                 __syncwarp();  // (the tensor-memory loads are for whole warps)
@@ -1055,7 +1139,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             tc_fence_after();
             const bool direct = p.whole && D.streams == 1;
             const int64_t prow0 = p.whole ? (int64_t)2 * D.grid * D.cap + (int64_t)p.t->stream * A.n_lanes * A.n_heads
-                                          : (int64_t)(2 * blockIdx.x + (p.head ? 0 : 1)) * D.cap;
+                                          : (int64_t)(2 * blockIdx.x + (p.c0 ? 0 : 1)) * D.cap;
             const int rows = min(16, p.nrows - r0);
             if (t < rows) {
                 const int r = r0 + t;
@@ -1088,9 +1172,8 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
 // ------------------------------------------------------------------ merging partial tiles
 constexpr int kMergeThreads = 256;
 
-// The (lane, head)s in blocks of 256: first every thread finds out whether its
-// own is finished already, then the block takes the others one after the
-// other: the pieces of their tiles by the weights 2^(maximum - largest
+// The (lane, head)s in blocks of up to 256: first every thread finds out
+// whether its own is finished already, then the block takes the others: the pieces of their tiles by the weights 2^(maximum - largest
 // maximum), zeros where there are none.  All but the partial sums themselves
 // is read while the kernel before still runs.
 __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDims D, AlWs W) {
@@ -1098,7 +1181,7 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
     __shared__ float red[8];
     __shared__ float4 acc[kMergeThreads];
     __shared__ int todo[kMergeThreads];
-    __shared__ int4 what[kMergeThreads][2];  // per stream: pieces, first CTA, row of its partial rows, its slot
+    __shared__ int4 what[kMergeThreads][2];  // per stream: pieces, first CTA, row of its partial rows
     __shared__ int count;
     __shared__ AlSelfPlan plan;
     __shared__ AlSelfScratch x;
@@ -1114,6 +1197,14 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
         __syncthreads();
     }
     const int64_t U = P.head->units, G = P.head->grid;
+    // the partial row of piece q: the second slot of the CTA that starts the tile, the first of the ones behind it
+    auto piece_row = [&](const int4 &a0, const int4 &a1, int q, int idx) -> int64_t {
+        const int st = q < a0.x ? 0 : 1;
+        const int4 x = st ? a1 : a0;
+        const int b = st ? q - a0.x : q;
+        return x.y < 0 ? (int64_t)2 * D.grid * D.cap + (int64_t)st * total + idx
+                       : (int64_t)(2 * (x.y + b) + (b == 0 ? 1 : 0)) * D.cap + x.z;
+    };
     bool waited = false;
     for (int base = blockIdx.x * D.merge; base < total; base += gridDim.x * D.merge) {
         __syncthreads();
@@ -1136,12 +1227,13 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
                 if (nch == 0) continue;
                 const int gs = D.HB == 1 ? D.group : min(D.R, D.group - hb * D.R);
                 const int r = (lane - t->lane0) * gs + hg - hb * D.R;
-                const int64_t u0 = t->unit0 + (int64_t)(kvh * D.HB + hb) * nch, u1 = u0 + nch;
+                // from the unit of its first chunk
+                const int64_t u1 = t->unit0 + (int64_t)(kvh * D.HB + hb + 1) * (nch + kSetup), u0 = u1 - nch;
                 const int b0 = (int)(((u0 + 1) * G - 1) / U), b1 = (int)((u1 * G - 1) / U);
                 if (b0 == b1)
                     done = D.streams == 1, y[st] = make_int4(1, -1, 0, 0);
                 else
-                    y[st] = make_int4(b1 - b0 + 1, b0, r, muldiv(U, b0, (int)G) >= u0 ? 0 : 1);
+                    y[st] = make_int4(b1 - b0 + 1, b0, r, 0);
             }
             if (!done) {
                 const int k = atomicAdd(&count, 1);
@@ -1154,29 +1246,54 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
             asm volatile("griddepcontrol.wait;" ::: "memory");
             waited = true;
         }
+        // up to 32 pieces: a warp each, a lane per piece for the weights, then four dims each
+        for (int k = warp; k < count; k += kMergeThreads / 32) {
+            const int idx = todo[k];
+            const int4 a0 = what[k][0], a1 = what[k][1];
+            const int n = a0.x + a1.x;
+            if (n > 32) continue;
+            float4 *o = reinterpret_cast<float4 *>(A.out + (int64_t)idx * hd);
+            int64_t row = 0;
+            float m = kNoKey, l = 0.0f;
+            if (lane_t < n) {
+                row = piece_row(a0, a1, lane_t, idx);
+                const float2 v = __ldcg(&W.ml[row]);
+                m = v.x, l = v.y;
+            }
+            const float top = warp_max(m);
+            const float x = m == kNoKey ? 0.0f : al_ex2(__fsub_rn(m, top));
+            const float sum = warp_psum(lane_t < n ? x * l : 0.0f);
+            const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+            float4 a[2] = {};
+#pragma unroll 4
+            for (int q = 0; q < n; q++) {
+                const float xq = __shfl_sync(0xffffffffu, x, q);
+                const float4 *src = reinterpret_cast<const float4 *>(W.part + __shfl_sync(0xffffffffu, row, q) * hd);
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                    if (lane_t + 32 * e < hd / 4) {
+                        const float4 v = __ldcg(src + lane_t + 32 * e);
+                        a[e].x += v.x * xq, a[e].y += v.y * xq, a[e].z += v.z * xq, a[e].w += v.w * xq;
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+                if (lane_t + 32 * e < hd / 4)
+                    o[lane_t + 32 * e] = make_float4(a[e].x * inv, a[e].y * inv, a[e].z * inv, a[e].w * inv);
+        }
+        // more: the whole block
         for (int k = 0; k < count; k++) {
             const int idx = todo[k];
             const int4 a0 = what[k][0], a1 = what[k][1];
             const int n = a0.x + a1.x;
+            if (n <= 32) continue;
             float4 *o = reinterpret_cast<float4 *>(A.out + (int64_t)idx * hd);
-            if (n == 0) {
-                for (int d = tid; d < hd / 4; d += kMergeThreads) o[d] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                continue;
-            }
-            // the partial row of piece q: CTA b0's own slot, the first slot of the CTAs behind it
-            auto row = [&](int q) -> int64_t {
-                const int st = q < a0.x ? 0 : 1;
-                const int4 x = st ? a1 : a0;
-                const int b = st ? q - a0.x : q;
-                return x.y < 0 ? (int64_t)2 * D.grid * D.cap + (int64_t)st * total + idx
-                               : (int64_t)(2 * (x.y + b) + (b == 0 ? x.w : 0)) * D.cap + x.z;
-            };
             __syncthreads();
             float m = kNoKey, l[2] = {0.0f, 0.0f}, mi[2];
 #pragma unroll
             for (int e = 0; e < 2; e++)
                 if (tid + e * kMergeThreads < n) {
-                    const float2 v = __ldcg(&W.ml[row(tid + e * kMergeThreads)]);
+                    const float2 v = __ldcg(&W.ml[piece_row(a0, a1, tid + e * kMergeThreads, idx)]);
                     mi[e] = v.x, l[e] = v.y;
                     m = fmaxf(m, v.x);
                 }
@@ -1206,7 +1323,7 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
             if (gi < groups)
 #pragma unroll 8
                 for (int q = gi; q < n; q += groups) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(W.part + row(q) * hd) + dv);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(W.part + piece_row(a0, a1, q, idx) * hd) + dv);
                     const float x = w[q];
                     a.x += v.x * x, a.y += v.y * x, a.z += v.z * x, a.w += v.w * x;
                 }
@@ -1321,7 +1438,7 @@ qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t work
     D.cap = (int64_t)A.n_lanes * D.group < D.R ? A.n_lanes * D.group : D.R;
     D.streams = A.pre.k ? 2 : 1;
     D.grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
-    D.merge = A.n_lanes <= kSelfPlan ? 1 : kMergeThreads;
+    D.merge = A.n_lanes <= kSelfPlan ? 1 : 32;
     D.c = (float)(1.4426950408889634 / std::sqrt((double)A.hd));
     const void *kern = f32 ? (const void *)al_attn_kernel<3> : (const void *)al_attn_kernel<1>;
     const size_t smem = kAlSmem, plan_smem = 3 * sizeof(int) * (size_t)A.n_lanes;
