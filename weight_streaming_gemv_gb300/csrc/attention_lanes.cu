@@ -87,14 +87,16 @@ struct AlArgs {
 // sequence's rows are 0 .. nsink - 1 and then cfirst, cfirst + 1, ...
 struct __align__(16) AlTile {
     int64_t unit0;  // its first unit; units go (KV head, head block, kSetup and then the chunks)
-    int lane0, nl, stream, nch, nsink, cfirst;
+    uint16_t lane0;
+    uint8_t nl, stream;
+    int nch, nsink, cfirst;
     int slot;        // sequence (or prompt) in the stream's caches
     int base;        // position of the sequence's row 0
     int lim;         // its rows
     int pmin, pmax;  // the lanes' positions
     int pad;
 };
-static_assert(sizeof(AlTile) == 64, "tiles are loaded 16 bytes at a time");
+static_assert(sizeof(AlTile) == 48 && kMaxLanes <= 65536, "tiles in shared memory");
 
 struct AlPlanHead {
     int64_t units;
@@ -157,19 +159,20 @@ struct PlanRed {
 };
 struct AlSelfScratch {
     int tile_of[2 * kSelfPlan];
-    int pos[kSelfPlan], seq[kSelfPlan], pre[kSelfPlan];
+    int lane[6 * kSelfPlan];
     PlanRed red;
 };
 
 // Checks the lanes, cuts them into tiles and deals the units out.  T threads
 // of the block, the first ones, take T lanes at a time (barrier 1 among them);
-// spos (-1: no lane), sseq, spre: [n_lanes] scratch.  first: the first tile of
-// CTA `cta`, or of every CTA if that is negative.
+// scratch: [6 n_lanes].  first: the first tile of CTA `cta`, or of every CTA
+// if that is negative.
 template <int T>
-__device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int *spos, int *sseq, int *spre, PlanRed &red,
-                                          AlPlanHead *head, int *first, int cta, int *tile_of, AlTile *tiles_out,
-                                          int32_t *status) {
+__device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int *scratch, PlanRed &red, AlPlanHead *head,
+                                          int *first, int cta, int *tile_of, AlTile *tiles_out, int32_t *status) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = A.n_lanes;
+    // per lane: position (-1: no lane), sequence, prompt; of the tile that starts at it: lanes, least and largest position
+    int *spos = scratch, *sseq = spos + n, *spre = sseq + n, *snl = spre + n, *smin = snl + n, *smax = smin + n;
     auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(T) : "memory"); };
 #pragma unroll 1
     for (int i = tid; i < n; i += T) {
@@ -195,6 +198,8 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
         auto same = [&](int a, int b) { return spre[a] == spre[b] && (st == 0 || sseq[a] == sseq[b]); };
         int run = -1;  // where the latest run of lanes of one sequence starts
 #pragma unroll 1
+        for (int i = tid; i < n; i += T) snl[i] = 0, smin[i] = INT_MAX, smax[i] = -1;
+#pragma unroll 1
         for (int base = 0; base < n; base += T) {
             bar();
             const int i = base + tid;
@@ -209,15 +214,25 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
             int rs = rs0;
             const uint32_t upto = starts & (0xffffffffu >> (31 - lane));
             if (upto) rs = i - lane + 31 - __clz(upto);
-            const bool start = valid && (i - rs) % D.LT == 0;
+            const int in_tile = valid ? (i - rs) % D.LT : 0;
+            const bool start = valid && in_tile == 0;
+            if (valid) {
+                atomicAdd(&snl[i - in_tile], 1);
+                atomicMin(&smin[i - in_tile], spos[i]);
+                atomicMax(&smax[i - in_tile], spos[i]);
+            }
+            // a tile may reach into the lanes of the next round: its first lane gathers it once those are through
+            // (the tile's lanes stand at most LT - 1 behind it)
+            bar();
             AlTile t;
             int64_t tu = 0;
             if (start) {
-                int nl = 0, pmin = INT_MAX, pmax = -1;
-                for (int j = i; j < n && nl < D.LT && spos[j] >= 0 && same(i, j); j++, nl++) {
-                    pmin = min(pmin, spos[j]);
-                    pmax = max(pmax, spos[j]);
+                for (int j = base + T; j < n && j < i + D.LT && spos[j] >= 0 && same(i, j); j++) {
+                    snl[i]++;
+                    smin[i] = min(smin[i], spos[j]);
+                    smax[i] = max(smax[i], spos[j]);
                 }
+                const int nl = snl[i], pmin = smin[i], pmax = smax[i];
                 // positions and rows are below 2^31, so differences fit
                 const int P = A.pre.k ? A.prefix_len[spre[i]] : 0;
                 const int org = st == 0 ? 0 : P, lim = st == 0 ? P : A.own.rows;
@@ -227,7 +242,7 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
                 const int cf = lo / kChunk, main = lo <= hi ? hi / kChunk - cf + 1 : 0;
                 int ns = (sk + kChunk - 1) / kChunk;
                 if (main > 0) ns = min(ns, cf);
-                t.lane0 = i, t.nl = nl, t.stream = st, t.nch = ns + main, t.nsink = ns, t.cfirst = cf;
+                t.lane0 = (uint16_t)i, t.nl = (uint8_t)nl, t.stream = (uint8_t)st, t.nch = ns + main, t.nsink = ns, t.cfirst = cf;
                 t.slot = st == 0 ? spre[i] : sseq[i], t.base = org, t.lim = lim;
                 t.pmin = pmin, t.pmax = pmax, t.pad = 0;
                 tu = tile_units(t.nch, A, D);
@@ -284,12 +299,11 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
 
 // One CTA plans for all.
 __global__ void __launch_bounds__(kPlanThreads) al_plan_kernel(AlArgs A, AlDims D, AlWs W) {
-    extern __shared__ int pl_smem[];  // [3][n_lanes]
+    extern __shared__ int pl_smem[];  // [6][n_lanes]
     __shared__ PlanRed red;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    make_plan<kPlanThreads>(A, D, pl_smem, pl_smem + A.n_lanes, pl_smem + 2 * A.n_lanes, red, W.head, W.first, -1,
-                                      W.tile_of, W.tiles, A.status);
+    make_plan<kPlanThreads>(A, D, pl_smem, red, W.head, W.first, -1, W.tile_of, W.tiles, A.status);
 }
 
 // The plan as the other kernels see it: in the workspace, or in shared memory.
@@ -300,27 +314,39 @@ struct AlPlan {
     const AlTile *tiles;
 };
 
-// ------------------------------------------------------------------ the walk over a CTA's units
-struct Piece {
-    const AlTile *t;  // (its fields are read where they are needed: registers are short)
-    int kvh, hb, c0, c1;  // chunks c0 .. c1 - 1 of the tile for KV head kvh, head block hb,
-    int rot;              // taken from c0 + rot on, around
-    int nrows, gs;        // rows, and rows per lane
-    bool whole;           // all of its chunks
-    __device__ __forceinline__ int chunk(int i) const {
-        const int c = c0 + rot + i;
-        return c < c1 ? c : c - (c1 - c0);
+// ------------------------------------------------------------------ the pieces of a CTA
+// A run of chunks of one tile for one KV head and head block, as one thread
+// hands it to the others.
+struct __align__(16) AlPiece {
+    int n;                 // its chunks; 0: there are no more pieces
+    int first, c1;         // they are first, first + 1, ... and from c1 on around
+    int nsink, cfirst;     // the tile's chunks as rows (AlTile)
+    int any_lo, any_hi, sk;  // rows that some row of the tile may see: > any_lo or < sk, and <= any_hi
+    int all_lo, all_hi;      // rows that all of them see: > all_lo or < sk, and <= all_hi
+    int stream, slot, kvh;
+    int nrows, gs;         // rows, and rows per lane
+    int lane0, head0;      // the first lane, and the first head
+    int base, lim;         // AlTile
+    int whole, begins;     // all of the tile's chunks; its first one
+
+    __device__ __forceinline__ int row0(int i) const {
+        int c = first + i;
+        if (c >= c1) c -= n;
+        return (c < nsink ? c : cfirst + c - nsink) * kChunk;
     }
+    // whether some row of the tile may see one of the rows [a, b), and whether some may not
+    __device__ __forceinline__ bool any_in(int a, int b) const { return a <= any_hi && (b - 1 > any_lo || a < sk); }
+    __device__ __forceinline__ bool edge_in(int a, int b) const { return !(b - 1 <= all_hi && (a > all_lo || b - 1 < sk)); }
 };
 
-// Tiles of one sequence read the same chunks.  So that they read them at the
-// same time, once from memory and then from L2, every CTA takes its chunks in
-// the order of their number modulo the units of a CTA.
+// Walks over a CTA's units and writes its pieces down.  Tiles of one sequence
+// read the same chunks.  So that they read them at the same time, once from
+// memory and then from L2, every CTA takes its chunks in the order of their
+// number modulo the units of a CTA.
 struct Walker {
     int64_t u, hi;
     int turn;  // units of a CTA
     const AlTile *at;
-    Walker() = default;
     __device__ __forceinline__ explicit Walker(const AlPlan &P) {
         const int64_t U = P.head->units;
         const int G = P.head->grid;
@@ -333,7 +359,7 @@ struct Walker {
             at = P.tiles + *P.first;
         }
     }
-    __device__ __forceinline__ bool next(Piece &p, const AlArgs &A, const AlDims &D) {
+    __device__ __forceinline__ void next(AlPiece &p, const AlArgs &A, const AlDims &D) {
         while (u < hi) {
             while (u >= at->unit0 + tile_units(at->nch, A, D)) at++;
             const int nch = at->nch, per = nch + kSetup;
@@ -342,46 +368,27 @@ struct Walker {
             const int v0 = (int)(r - sub * per), v1 = (int)min((int64_t)per, v0 + (hi - u));
             u += v1 - v0;
             if (v1 <= kSetup) continue;  // the next CTA starts it
-            p.t = at;
-            p.kvh = (int)sub / D.HB;
-            p.hb = (int)sub - p.kvh * D.HB;
-            p.c0 = max(v0 - kSetup, 0);
-            p.c1 = v1 - kSetup;
-            const int over = p.c0 % turn;
-            p.rot = over && turn - over < p.c1 - p.c0 ? turn - over : 0;
-            p.gs = D.HB == 1 ? D.group : min(D.R, D.group - p.hb * D.R);
+            const int kvh = D.HB == 1 ? (int)sub : (int)(sub / D.HB), hb = (int)sub - kvh * D.HB;
+            const int c0 = max(v0 - kSetup, 0), c1 = v1 - kSetup;
+            const int over = c0 % turn;
+            p.first = c0 + (over && turn - over < c1 - c0 ? turn - over : 0), p.c1 = c1;
+            p.nsink = at->nsink, p.cfirst = at->cfirst;
+            const int base = at->base, lim = at->lim, pmin = at->pmin - base, pmax = at->pmax - base;
+            p.any_hi = min(pmax, lim - 1), p.all_hi = min(pmin, lim - 1);
+            p.any_lo = A.window && pmin >= A.window ? pmin - A.window : -1;
+            p.all_lo = A.window && pmax >= A.window ? pmax - A.window : -1;
+            p.sk = A.window ? max(0, A.sinks - base) : 0;
+            p.stream = at->stream, p.slot = at->slot, p.kvh = kvh;
+            p.gs = D.HB == 1 ? D.group : min(D.R, D.group - hb * D.R);
             p.nrows = at->nl * p.gs;
-            p.whole = p.c0 == 0 && p.c1 == nch;
-            return true;
+            p.lane0 = at->lane0, p.head0 = kvh * D.group + hb * D.R;
+            p.base = base, p.lim = lim;
+            p.whole = c0 == 0 && c1 == nch, p.begins = c0 == 0;
+            p.n = c1 - c0;
+            return;
         }
-        return false;
+        p.n = 0;
     }
-};
-
-// The keys of chunk c of a piece, as rows of its sequence.
-struct ChunkView {
-    int r0;                       // its first row
-    int any_lo, any_hi, sk;       // rows > any_lo or < sk, and <= any_hi, may be seen by some row of the tile
-    int all_lo, all_hi;           // rows <= all_hi that are > all_lo or < sk are seen by every one
-    bool edge;                    // not all of its keys are
-    __device__ __forceinline__ ChunkView(const Piece &p, int c, const AlArgs &A) {
-        r0 = (c < p.t->nsink ? c : p.t->cfirst + c - p.t->nsink) * kChunk;
-        const int pmin = p.t->pmin - p.t->base, pmax = p.t->pmax - p.t->base, last = p.t->lim - 1;
-        any_hi = min(pmax, last);
-        all_hi = min(pmin, last);
-        any_lo = all_lo = -1;
-        sk = 0;
-        if (A.window) {
-            any_lo = pmin >= A.window ? pmin - A.window : -1;
-            all_lo = pmax >= A.window ? pmax - A.window : -1;
-            sk = max(0, A.sinks - p.t->base);
-        }
-        edge = !(r0 + kChunk - 1 <= all_hi && (r0 > all_lo || r0 + kChunk - 1 < sk));
-    }
-    // whether some row of the tile may not see one of the rows [a, b)
-    __device__ __forceinline__ bool edge_in(int a, int b) const { return !(b - 1 <= all_hi && (a > all_lo || b - 1 < sk)); }
-    __device__ __forceinline__ bool any(int r) const { return r <= any_hi && (r > any_lo || r < sk); }
-    __device__ __forceinline__ bool all(int r) const { return r <= all_hi && (r > all_lo || r < sk); }
 };
 
 // ------------------------------------------------------------------ the product
@@ -393,11 +400,12 @@ struct AlCfg {
     static constexpr int kTerm = 16384;             // 128 keys x 64 dims, or 64 keys x 128 dims, in bf16
     static constexpr int kSlot = NT * kTerm;
     static constexpr int kProd = NT == 1 ? 1 : 8;   // producer warps
-    // after the warpgroups: MMA warp and producer (bf16), or two warpgroups of producers and one whose first warp
-    // issues the MMAs (fp32; registers are dealt out by warpgroup)
-    static constexpr int kMma = NT == 1 ? 4 * kWg : 4 * kWg + kProd;
-    static constexpr int kProd0 = NT == 1 ? kMma + 1 : 4 * kWg;
-    static constexpr int kThreads = 32 * (NT == 1 ? 4 * kWg + 2 : 4 * kWg + kProd + 4);
+    // after the warpgroups, and the producers of an fp32 cache: a warp that issues the MMAs, one that describes the
+    // pieces, one that copies the slices of a bf16 cache or describes those of an fp32 cache to the producers, one idle
+    // (registers are dealt out by warpgroup)
+    static constexpr int kProd0 = 4 * kWg;
+    static constexpr int kMma = 4 * kWg + (NT == 1 ? 0 : kProd), kWalk = kMma + 1, kCopy = kMma + 2;
+    static constexpr int kThreads = 32 * (kMma + 4);
     static constexpr uint32_t kCols = 512;          // S^T [3 R], then O^T's two halves of dims [3 R] each
     static constexpr uint32_t kO = 3 * R;
     static constexpr int kMaxSlots = NT == 1 ? 12 : 3;
@@ -411,7 +419,7 @@ struct __align__(16) AlSlice {
     int v, dims;       // a slice of V; dims from src on
     int64_t pad;
 };
-constexpr int kSliceRing = 4;
+constexpr int kSliceRing = 4, kPieceRing = 2;
 
 template <int NT>
 struct AlCtl {
@@ -424,6 +432,9 @@ struct AlCtl {
     float mc[C::R], alpha[C::R];
     float red[4][C::R];
     AlSelfPlan plan;
+    AlPiece piece[kPieceRing];
+    uint64_t pc_full[kPieceRing], pc_empty[kPieceRing];
+    float *optr[C::R];  // a row's outputs
     AlSlice slice[kSliceRing];
     uint64_t sl_full[kSliceRing], sl_empty[kSliceRing];
     uint32_t tmem;
@@ -578,53 +589,29 @@ struct AlMaps {
     CUtensorMap k[2], v[2];  // stream 0 (prompts), stream 1 (own)
 };
 
-// The slices of a CTA's pieces in the order in which they pass through the
-// ring: K of chunk 0, then for every chunk K of the next one and its own V.
+// The slices of a piece in the order in which they pass through the ring: K of
+// chunk 0, then for every chunk K of the next one and its own V.
 struct SliceGen {
-    Walker w;
-    int any_lo, any_hi, sk, nsink, cfirst, stream, slot, kvh;
-    int n, c1, first;  // chunks first, first + 1, ... (around at c1)
-    int i, sl, r0;     // r0: the chunk's first row
-    bool v, more;
-    __device__ __forceinline__ SliceGen(const AlArgs &A, const AlPlan &P, const AlDims &D) : w(P) { piece(A, D); }
-    __device__ __forceinline__ void piece(const AlArgs &A, const AlDims &D) {
-        Piece p;
-        more = w.next(p, A, D);
-        if (!more) return;
-        const ChunkView cv(p, 0, A);
-        any_lo = cv.any_lo, any_hi = cv.any_hi, sk = cv.sk;
-        nsink = p.t->nsink, cfirst = p.t->cfirst, stream = p.t->stream, slot = p.t->slot, kvh = p.kvh;
-        n = p.c1 - p.c0, c1 = p.c1, first = p.c0 + p.rot;
-        i = sl = 0;
-        v = false;
-        place();
-    }
-    __device__ __forceinline__ void place() {
-        int c = first + (v ? i - 1 : i);
-        if (c >= c1) c -= n;
-        r0 = (c < nsink ? c : cfirst + c - nsink) * kChunk;
-    }
-    // whether some row of the tile may see one of the rows [a, b)
-    __device__ __forceinline__ bool any_in(int a, int b) const { return a <= any_hi && (b - 1 > any_lo || a < sk); }
-    // whether a new piece begins
-    __device__ __forceinline__ bool step(const AlArgs &A, const AlDims &D, int nK, int nV) {
-        if (++sl < (v ? nV : nK)) return false;
+    const AlPiece *p;
+    int i, sl, r0;  // r0: the chunk's first row
+    bool v;
+    __device__ __forceinline__ explicit SliceGen(const AlPiece *q) : p(q), i(0), sl(0), v(false) { r0 = p->row0(0); }
+    // false: that was the last one
+    __device__ __forceinline__ bool step(int nK, int nV) {
+        if (++sl < (v ? nV : nK)) return true;
         sl = 0;
         // step i: K of chunk i (if there is one), then V of chunk i - 1 (if there is one)
         if (!v && i >= 1) {
             v = true;
-        } else if (!v && n == 1) {
+        } else if (!v && p->n == 1) {
             v = true, i = 1;
         } else {
             i++;
-            v = i >= n;
-            if (i > n) {
-                piece(A, D);
-                return true;
-            }
+            v = i >= p->n;
+            if (i > p->n) return false;
         }
-        place();
-        return false;
+        r0 = p->row0(v ? i - 1 : i);
+        return true;
     }
 };
 
@@ -634,6 +621,21 @@ struct RingPos {
     uint32_t round = 0;
     __device__ __forceinline__ void step(int slots) {
         if (++s == slots) s = 0, round++;
+    }
+};
+
+// A reader's place in the ring of pieces.
+struct PieceRef {
+    int k = -1;
+    template <typename Ctl>
+    __device__ __forceinline__ const AlPiece *next(Ctl &S) {  // null: gave up
+        k++;
+        if (!al_wait(&S.pc_full[k % kPieceRing], (uint32_t)(k / kPieceRing) & 1u, &S.abort)) return nullptr;
+        return &S.piece[k % kPieceRing];
+    }
+    template <typename Ctl>
+    __device__ __forceinline__ void done(Ctl &S) {
+        mbar_arrive(&S.pc_empty[k % kPieceRing]);
     }
 };
 
@@ -669,6 +671,10 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             mbar_init(&S.sl_full[s], 1);
             mbar_init(&S.sl_empty[s], C::kProd);
         }
+        for (int s = 0; s < kPieceRing; s++) {
+            mbar_init(&S.pc_full[s], 1);
+            mbar_init(&S.pc_empty[s], 4 * C::kWg + 2);  // the warpgroups' warps, MMA and copy warp
+        }
         mbar_init(&S.pv_done, 1);
         mbar_init(&S.fix_go, 1);
         mbar_init(&S.fixed, 4);
@@ -682,7 +688,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     if (A.n_lanes <= kSelfPlan) {
         AlSelfScratch &x = *reinterpret_cast<AlSelfScratch *>(smem);  // (the ring is not in use yet)
         if (tid < kSelfPlan) {
-            make_plan<kSelfPlan>(A, D, x.pos, x.seq, x.pre, x.red, &S.plan.head, &S.plan.first, blockIdx.x,
+            make_plan<kSelfPlan>(A, D, x.lane, x.red, &S.plan.head, &S.plan.first, blockIdx.x,
                                           x.tile_of, S.plan.tiles, blockIdx.x == 0 ? A.status : nullptr);
             fence_proxy_async_smem();
         }
@@ -696,165 +702,193 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     const int slots = L.slots;
     uint8_t *const ring = smem, *const qs = ring + L.q, *const ps = ring + L.p;
 
-    if (warp >= C::kProd0 && warp < C::kProd0 + C::kProd) {
-        // ---------------------------------------------------------- producers
-        if constexpr (NT == 1) {
-            if (al_elect()) {
-                SliceGen sg(A, P, D);
-                RingPos at;
-                int g = 0;
-                while (sg.more) {
-                    const CUtensorMap *mk = &maps.k[sg.stream], *mv = &maps.v[sg.stream];
-                    const int z = (sg.stream ? A.own : A.pre).seq_stride ? sg.slot : 0, x0 = sg.kvh * hd;
-                    bool ok = true;
-                    for (bool fresh = false; !fresh; g++) {
-                        const int s = at.s;
-                        if (at.round && !(ok = al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort))) break;
-                        // two boxes of 64 keys x 64 dims, those that nobody sees left out: K's are the two halves
-                        // of the chunk, V's (of one half) the two halves of 128 dims
-                        const uint32_t to = smem_addr(ring + s * C::kSlot), full = smem_addr(&S.full[s]);
-                        const int kh = nDH == 2 ? sg.sl >> 1 : sg.sl, dh = nDH == 2 ? sg.sl & 1 : 0;
-                        const int d0 = sg.v ? 128 * dh : 64 * sg.sl, y0 = sg.r0 + (sg.v ? 64 * kh : 0);
-                        const bool on0 = sg.any_in(y0, y0 + 64);
-                        const bool on1 = sg.v ? on0 && d0 + 64 < hd : sg.any_in(y0 + 64, y0 + 128);
-                        mbar_arrive_expect_tx(&S.full[s], 8192u * ((uint32_t)on0 + (uint32_t)on1));
-                        const CUtensorMap *map = sg.v ? mv : mk;
-                        if (on0) al_tma(to, map, x0 + d0, y0, z, full);
-                        if (on1) al_tma(to + 8192, map, x0 + d0 + (sg.v ? 64 : 0), y0 + (sg.v ? 0 : 64), z, full);
-                        fresh = sg.step(A, D, nK, nV);
-                        at.step(slots);
-                    }
-                    if (!ok) {
-                        S.abort = 1;
-                        raise_status(A.status, kStatusTimeout);
-                        break;
-                    }
+    if (NT == 3 && warp >= C::kProd0 && warp < C::kProd0 + C::kProd) {
+        // ---------------------------------------------------------- producers of an fp32 cache's slices
+        // 32 rows at a time: thread t takes row t / 8, dims 4 (t % 8) .. + 3 and the same 32 dims on (eight
+        // threads read 128 bytes of a row at once); four such passes are a slice's 128 rows (a V slice's rows
+        // 64 .. 127 are the second 64 dims of its 64 keys)
+        const int pt = tid - 32 * C::kProd0, pr = pt >> 3, pc = pt & 7;
+        uint4 buf[2][8];
+        int ds = 0;
+        uint32_t dpar = 0;
+        bool ok = true, have[2];
+        // the next slice of the ring of descriptions; false when there is none
+        auto load = [&](uint4 (&o)[8]) -> bool {
+            if (!(ok = al_wait(&S.sl_full[ds], dpar, &S.abort))) return false;
+            const AlSlice &q = S.slice[ds];
+            const bool more = q.src != nullptr;
+            if (more) {
+                const int key0 = q.y0 + pr, dims = q.dims - 4 * pc, v = q.v;
+                const int64_t step = 32 * q.stride;
+                const float *a = q.src + pr * q.stride + 4 * pc;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    // K: 32 rows on; V: the other half of its 64 rows, then 64 dims on
+                    const int key = key0 + (v ? (e & 1) * 32 : e * 32), d = v ? (e >> 1) * 64 : 0;
+                    const bool any = key <= q.any_hi && (key > q.any_lo || key < q.sk);
+                    al_ld16(a, any && d < dims, o[2 * e]);
+                    al_ld16(a + 32, any && d + 32 < dims, o[2 * e + 1]);
+                    a = v && e == 1 ? a - step + 64 : a + step;
                 }
-                if (*(volatile int *)&S.abort)  // the copies in flight
-                    for (int k = max(0, g - slots); k < g; k++)
-                        mbar_wait(&S.full[k % slots], (uint32_t)(k / slots) & 1u);
             }
-        } else {
-            // 32 rows at a time: thread t takes row t / 8, dims 4 (t % 8) .. + 3 and the same 32 dims on (eight
-            // threads read 128 bytes of a row at once); four such passes are a slice's 128 rows (a V slice's rows
-            // 64 .. 127 are the second 64 dims of its 64 keys)
-            const int pt = tid - 32 * C::kProd0, pr = pt >> 3, pc = pt & 7;
-            uint4 buf[2][8];
-            int ds = 0;
-            uint32_t dpar = 0;
-            bool ok = true, have[2];
-            // the next slice of the ring of descriptions; false when there is none
-            auto load = [&](uint4 (&o)[8]) -> bool {
-                if (!(ok = al_wait(&S.sl_full[ds], dpar, &S.abort))) return false;
-                const AlSlice &q = S.slice[ds];
-                const bool more = q.src != nullptr;
-                if (more) {
-                    const int key0 = q.y0 + pr, dims = q.dims - 4 * pc, v = q.v;
-                    const int64_t step = 32 * q.stride;
-                    const float *a = q.src + pr * q.stride + 4 * pc;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.sl_empty[ds]);
+            if (++ds == kSliceRing) ds = 0, dpar ^= 1u;
+            return more;
+        };
+        have[0] = load(buf[0]);
+        have[1] = have[0] && load(buf[1]);
+        RingPos at;
+        while (ok && have[0]) {
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        // K: 32 rows on; V: the other half of its 64 rows, then 64 dims on
-                        const int key = key0 + (v ? (e & 1) * 32 : e * 32), d = v ? (e >> 1) * 64 : 0;
-                        const bool any = key <= q.any_hi && (key > q.any_lo || key < q.sk);
-                        al_ld16(a, any && d < dims, o[2 * e]);
-                        al_ld16(a + 32, any && d + 32 < dims, o[2 * e + 1]);
-                        a = v && e == 1 ? a - step + 64 : a + step;
+            for (int k = 0; k < 2; k++) {
+                if (!have[k]) break;
+                const int s = at.s;
+                if (at.round && !al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort)) {
+                    S.abort = 1;
+                    raise_status(A.status, kStatusTimeout);
+                    ok = false;
+                    break;
+                }
+                const uint32_t to = smem_addr(ring + s * C::kSlot);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int r = e * 32 + pr;
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+                        const uint4 v = buf[k][2 * e + q];
+                        uint2 h, m, l;
+                        al_split2(__uint_as_float(v.x), __uint_as_float(v.y), h.x, m.x, l.x);
+                        al_split2(__uint_as_float(v.z), __uint_as_float(v.w), h.y, m.y, l.y);
+                        const uint32_t a = to + (uint32_t)(r * 128 + (((4 * q + (pc >> 1)) ^ (r & 7)) << 4) + (pc & 1) * 8);
+                        sts64(a, h);
+                        sts64(a + C::kTerm, m);
+                        sts64(a + 2 * C::kTerm, l);
                     }
                 }
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&S.sl_empty[ds]);
-                if (++ds == kSliceRing) ds = 0, dpar ^= 1u;
-                return more;
-            };
-            have[0] = load(buf[0]);
-            have[1] = have[0] && load(buf[1]);
-            RingPos at;
-            while (ok && have[0]) {
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    if (!have[k]) break;
-                    const int s = at.s;
-                    if (at.round && !al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort)) {
-                        S.abort = 1;
-                        raise_status(A.status, kStatusTimeout);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t to = smem_addr(ring + s * C::kSlot);
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int r = e * 32 + pr;
-#pragma unroll
-                        for (int q = 0; q < 2; q++) {
-                            const uint4 v = buf[k][2 * e + q];
-                            uint2 h, m, l;
-                            al_split2(__uint_as_float(v.x), __uint_as_float(v.y), h.x, m.x, l.x);
-                            al_split2(__uint_as_float(v.z), __uint_as_float(v.w), h.y, m.y, l.y);
-                            const uint32_t a = to + (uint32_t)(r * 128 + (((4 * q + (pc >> 1)) ^ (r & 7)) << 4) + (pc & 1) * 8);
-                            sts64(a, h);
-                            sts64(a + C::kTerm, m);
-                            sts64(a + 2 * C::kTerm, l);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&S.full[s]);
-                    at.step(slots);
-                    have[k] = have[k ^ 1] && load(buf[k]);
-                }
+                if (lane == 0) mbar_arrive(&S.full[s]);
+                at.step(slots);
+                have[k] = have[k ^ 1] && load(buf[k]);
             }
         }
     } else if (warp >= C::kMma) {
-        // ---------------------------------------------------------- the MMAs
         // 640 threads are launched with 96 registers (61440 in all): 128 x 56 here, 256 x 112 for the weights and
         // 256 x 96 for the producers make 60416
         if constexpr (NT == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (NT == 3 && warp == C::kMma + 1 && al_elect()) {
-            // ------------------------------------------------------ describes the slices to the producers
-            SliceGen sg(A, P, D);
-            bool ok = true;
-            for (int g = 0; ok; g++) {
-                const int ds = g % kSliceRing;
-                if (g >= kSliceRing) ok = al_wait(&S.sl_empty[ds], (uint32_t)(g / kSliceRing - 1) & 1u, &S.abort);
-                if (!ok) break;
-                AlSlice &q = S.slice[ds];
-                if (!sg.more) {
-                    q.src = nullptr;
-                    mbar_arrive(&S.sl_full[ds]);
+        if (warp == C::kWalk && al_elect()) {
+            // ------------------------------------------------------ describes the pieces
+            Walker w(P);
+            for (int k = 0;; k++) {
+                const int r = k % kPieceRing;
+                if (k >= kPieceRing && !al_wait(&S.pc_empty[r], (uint32_t)(k / kPieceRing - 1) & 1u, &S.abort)) {
+                    S.abort = 1;
+                    raise_status(A.status, kStatusTimeout);
                     break;
                 }
-                const qlin_kv &kv = sg.stream ? A.own : A.pre;
-                const int kh = nDH == 2 ? sg.sl >> 1 : sg.sl, dh = nDH == 2 ? sg.sl & 1 : 0;
-                const int d0 = sg.v ? 128 * dh : 64 * sg.sl, y0 = sg.r0 + (sg.v ? 64 * kh : 0);
-                q.src = static_cast<const float *>(sg.v ? kv.v : kv.k) + (int64_t)sg.slot * kv.seq_stride + sg.kvh * hd +
-                      y0 * kv.row_stride + d0;
-                q.stride = kv.row_stride;
-                q.y0 = y0, q.any_lo = sg.any_lo, q.any_hi = sg.any_hi, q.sk = sg.sk;
-                q.v = sg.v, q.dims = hd - d0;
-                mbar_arrive(&S.sl_full[ds]);
-                sg.step(A, D, nK, nV);
+                w.next(S.piece[r], A, D);
+                const bool end = S.piece[r].n == 0;
+                mbar_arrive(&S.pc_full[r]);
+                if (end) break;
             }
-            if (!ok) S.abort = 1;
+        }
+        if (NT == 1 && warp == C::kCopy && al_elect()) {
+            // ------------------------------------------------------ copies the slices of a bf16 cache
+            PieceRef ref;
+            RingPos at;
+            int g = 0;
+            bool ok = true;
+            while (ok) {
+                const AlPiece *p = ref.next(S);
+                if (!(ok = p != nullptr) || p->n == 0) break;
+                SliceGen sg(p);
+                const CUtensorMap *mk = &maps.k[p->stream], *mv = &maps.v[p->stream];
+                const int z = (p->stream ? A.own : A.pre).seq_stride ? p->slot : 0, x0 = p->kvh * hd;
+                for (bool more = true; more; g++) {
+                    const int s = at.s;
+                    if (at.round && !(ok = al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort))) break;
+                    // two boxes of 64 keys x 64 dims, those that nobody sees left out: K's are the two halves of the
+                    // chunk, V's (of one half) the two halves of 128 dims
+                    const uint32_t to = smem_addr(ring + s * C::kSlot), full = smem_addr(&S.full[s]);
+                    const int kh = nDH == 2 ? sg.sl >> 1 : sg.sl, dh = nDH == 2 ? sg.sl & 1 : 0;
+                    const int d0 = sg.v ? 128 * dh : 64 * sg.sl, y0 = sg.r0 + (sg.v ? 64 * kh : 0);
+                    const bool on0 = p->any_in(y0, y0 + 64);
+                    const bool on1 = sg.v ? on0 && d0 + 64 < hd : p->any_in(y0 + 64, y0 + 128);
+                    mbar_arrive_expect_tx(&S.full[s], 8192u * ((uint32_t)on0 + (uint32_t)on1));
+                    const CUtensorMap *map = sg.v ? mv : mk;
+                    if (on0) al_tma(to, map, x0 + d0, y0, z, full);
+                    if (on1) al_tma(to + 8192, map, x0 + d0 + (sg.v ? 64 : 0), y0 + (sg.v ? 0 : 64), z, full);
+                    more = sg.step(nK, nV);
+                    at.step(slots);
+                }
+                ref.done(S);
+            }
+            if (!ok) {
+                S.abort = 1;
+                raise_status(A.status, kStatusTimeout);
+                for (int k = max(0, g - slots); k < g; k++)  // the copies in flight
+                    mbar_wait(&S.full[k % slots], (uint32_t)(k / slots) & 1u);
+            }
+        }
+        if (NT == 3 && warp == C::kCopy && al_elect()) {
+            // ------------------------------------------------------ describes the slices of an fp32 cache
+            PieceRef ref;
+            bool ok = true, end = false;
+            int g = 0;
+            while (ok && !end) {
+                const AlPiece *p = ref.next(S);
+                if (!(ok = p != nullptr)) break;
+                end = p->n == 0;
+                SliceGen sg(p);
+                const qlin_kv &kv = p->stream ? A.own : A.pre;
+                const int64_t off = (int64_t)p->slot * kv.seq_stride + p->kvh * hd;
+                for (bool more = true; more; g++) {
+                    const int ds = g % kSliceRing;
+                    if (g >= kSliceRing && !(ok = al_wait(&S.sl_empty[ds], (uint32_t)(g / kSliceRing - 1) & 1u, &S.abort)))
+                        break;
+                    AlSlice &q = S.slice[ds];
+                    q.src = nullptr;
+                    more = !end;
+                    if (!end) {
+                        const int kh = nDH == 2 ? sg.sl >> 1 : sg.sl, dh = nDH == 2 ? sg.sl & 1 : 0;
+                        const int d0 = sg.v ? 128 * dh : 64 * sg.sl, y0 = sg.r0 + (sg.v ? 64 * kh : 0);
+                        q.src = static_cast<const float *>(sg.v ? kv.v : kv.k) + off + y0 * kv.row_stride + d0;
+                        q.stride = kv.row_stride;
+                        q.y0 = y0, q.any_lo = p->any_lo, q.any_hi = p->any_hi, q.sk = p->sk;
+                        q.v = sg.v, q.dims = hd - d0;
+                        more = sg.step(nK, nV);
+                    }
+                    mbar_arrive(&S.sl_full[ds]);
+                }
+                if (ok) ref.done(S);
+            }
+            if (!ok) {
+                S.abort = 1;
+                raise_status(A.status, kStatusTimeout);
+            }
         }
         if (warp == C::kMma && al_elect()) {
-            Walker w(P);
-            Piece p;
+            // ------------------------------------------------------ the MMAs
+            PieceRef ref;
             RingPos at;
-            int it = 0, np = 0;   // chunks and pieces so far
+            int it = 0;           // chunks so far
             uint32_t fixes = 0;   // slices of V handed to the first warpgroup so far
             bool ok = true;
             const uint32_t ring_a = smem_addr(ring), qs_a = smem_addr(qs), ps_a = smem_addr(ps);
             const uint32_t hi128 = al_desc_hi(1024, 2), hip = al_desc_hi(512, 4);
-            for (; ok && w.next(p, A, D); np++) {
-                const int n = p.c1 - p.c0;
-                const uint32_t nr = (uint32_t)(p.nrows + 15) / 16 * 16;
+            while (ok) {
+                const AlPiece *p = ref.next(S);
+                if (!(ok = p != nullptr)) break;
+                const int n = p->n;
+                if (n == 0) break;
+                const uint32_t nr = (uint32_t)(p->nrows + 15) / 16 * 16;
                 // fp32 accumulator, bf16 operands, N = the terms' rows; S^T: both operands K-major, O^T: both with
                 // the keys as rows.  Term t of a cached value meets the 3 - t first terms of the rows, whose columns
                 // start at the products' order t.
                 const uint32_t ids = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 4) << 24;
                 const uint32_t idp = ids | (1u << 15) | (1u << 16);
-                if (!(ok = al_wait(&S.q_ready, (uint32_t)np & 1u, &S.abort))) break;
+                if (!(ok = al_wait(&S.q_ready, (uint32_t)ref.k & 1u, &S.abort))) break;
                 for (int i = 0; ok && i <= n; i++) {
                     if (i < n) {
                         if (it + i > 0 && !(ok = al_wait(&S.s_free, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
@@ -877,12 +911,12 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                         tc_commit(&S.s_full);
                     }
                     if (i >= 1) {
-                        const ChunkView cv(p, p.chunk(i - 1), A);
+                        const int cr = p->row0(i - 1);
                         if (!(ok = al_wait(&S.p_ready, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
                         for (int vs = 0; vs < nV; vs++, at.step(slots)) {
                             const int s = at.s, kh = vs / nDH, dh = vs % nDH;
                             if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
-                            if (cv.edge_in(cv.r0 + 64 * kh, cv.r0 + 64 * kh + 64)) {
+                            if (p->edge_in(cr + 64 * kh, cr + 64 * kh + 64)) {
                                 mbar_arrive(&S.fix_go);
                                 if (!(ok = al_wait(&S.fixed, fixes & 1u, &S.abort))) break;
                                 fixes++;
@@ -904,6 +938,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     }
                 }
                 it += n;
+                if (ok) ref.done(S);
             }
             if (!ok) {
                 S.abort = 1;
@@ -917,16 +952,23 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         // 16 wg .. 16 wg + 15, its thread t key t of a chunk, and of the outputs dims t and t + 128
         if constexpr (NT == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         const int wg = warp >> 2, t = tid & 127, r0 = 16 * wg;
-        Walker w(P);
-        Piece p;
+        PieceRef ref;
         int g = 0, it = 0;   // slices and chunks so far
         uint32_t fixes = 0;  // slices of V looked through
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)r0;
         const float ninf = -__int_as_float(0x7f800000);
         bool ok = true;
-        while (ok && w.next(p, A, D)) {
-            const int n = p.c1 - p.c0, nr = (p.nrows + 15) / 16 * 16;
-            if (r0 >= p.nrows) {  // (the first warpgroup always has rows)
+        while (ok) {
+            const AlPiece *p = ref.next(S);
+            __syncwarp();
+            if (p == nullptr) {
+                S.abort = 1;
+                raise_status(A.status, kStatusTimeout);
+            }
+            if (al_bar_or(wg, p == nullptr)) break;  // (and the rows of the last piece are no longer needed)
+            const int n = p->n, nrows = p->nrows, nr = (nrows + 15) / 16 * 16;
+            if (n == 0) break;
+            if (r0 >= nrows) {  // (the first warpgroup always has rows)
                 if (lane == 0) mbar_arrive(&S.q_ready);
                 for (int i = 0; i < n && ok; i++, it++) {
                     ok = al_wait(&S.s_full, (uint32_t)it & 1u, &S.abort);
@@ -935,23 +977,23 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     ok = ok && al_wait(&S.pv_done, (uint32_t)it & 1u, &S.abort);
                     __syncwarp();
                 }
-                ok = __all_sync(0xffffffffu, ok);
+                ok = !al_bar_or(wg, !ok);
+                if (lane == 0) ref.done(S);
                 continue;
             }
-            al_bar(wg);  // the rows of the last piece are no longer needed
             if (t < 16) {
-                const int r = r0 + t, ln = p.t->lane0 + r / p.gs;
-                const bool in = r < p.nrows;
-                const int64_t pl = in ? (int64_t)A.positions[ln] - p.t->base : -1;
-                S.rowid[r] = in ? ln * A.n_heads + p.kvh * D.group + p.hb * D.R + r % p.gs : -1;
-                S.rowhi[r] = (int)max((int64_t)-1, min(pl, (int64_t)p.t->lim - 1));
-                S.rowlo[r] = A.window ? (int)max((int64_t)-1, pl - A.window) : -1;
+                const int r = r0 + t, gs = p->gs, ln = p->lane0 + r / gs;
+                const bool in = r < nrows;
+                const int pl = in ? A.positions[ln] - p->base : -1;
+                S.rowid[r] = in ? ln * A.n_heads + p->head0 + r % gs : -1;
+                S.rowhi[r] = max(-1, min(pl, p->lim - 1));
+                S.rowlo[r] = A.window && pl >= A.window ? pl - A.window : -1;
                 S.mc[r] = kNoKey;
                 S.nan[r] = 0;
             }
             al_bar(wg);
             // the rows' q as three bf16 terms
-#pragma unroll 2
+#pragma unroll 4
             for (int e = t; e < 2 * hd; e += 128) {
                 const int rr = e / (hd / 8), d8 = e - rr * (hd / 8), r = r0 + rr, id = S.rowid[r];
                 uint4 a, b, h, m, l;
@@ -995,8 +1037,8 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             };
 
             for (int i = 0; i < n; i++, it++) {
-                const ChunkView cv(p, p.chunk(i), A);
-                const int key = cv.r0 + t;
+                const int cr = p->row0(i), sk = p->sk, key = cr + t;
+                const bool edge = p->edge_in(cr, cr + kChunk);
                 const bool fail = !al_wait(&S.s_full, (uint32_t)it & 1u, &S.abort);
                 __syncwarp();  // (the tensor-memory loads are for whole warps)
                 tc_fence_after();
@@ -1006,8 +1048,8 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.s_free);
                 // whether row r of the tile sees this thread's key
-                auto sees = [&](int r) { return key <= S.rowhi[r] && (key > S.rowlo[r] || key < cv.sk); };
-                if (cv.edge)
+                auto sees = [&](int r) { return key <= S.rowhi[r] && (key > S.rowlo[r] || key < sk); };
+                if (edge)
 #pragma unroll
                     for (int j = 0; j < 16; j++)
                         if (!sees(r0 + j)) s[j] = ninf;
@@ -1084,13 +1126,13 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.p_ready);
-                if (wg == 0 && cv.edge) {
+                if (wg == 0 && edge) {
                     // the values of keys that not every row sees
                     const int gv = g + min(i + 2, n) * nK + i * nV;
-                    const bool any = cv.any(key), all = cv.all(key);
+                    const bool any = p->any_in(key, key + 1), all = !p->edge_in(key, key + 1);
                     for (int vs = 0; vs < nV; vs++) {
-                        const int sl = (gv + vs) % slots, k0 = cv.r0 + 64 * (vs / nDH);
-                        if (!cv.edge_in(k0, k0 + 64)) continue;
+                        const int sl = (gv + vs) % slots, k0 = cr + 64 * (vs / nDH);
+                        if (!p->edge_in(k0, k0 + 64)) continue;
                         // its turn: the slice has landed and its product waits
                         al_wait(&S.fix_go, fixes & 1u, &S.abort);
                         fixes++;
@@ -1111,7 +1153,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                                     }
                                 }
                                 if (nf)
-                                    for (int r = 0; r < p.nrows; r++)
+                                    for (int r = 0; r < nrows; r++)
                                         if (sees(r)) S.nan[r] = 1;
                             }
                             if (nf)
@@ -1137,30 +1179,42 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 break;
             }
             tc_fence_after();
-            const bool direct = p.whole && D.streams == 1;
-            const int64_t prow0 = p.whole ? (int64_t)2 * D.grid * D.cap + (int64_t)p.t->stream * A.n_lanes * A.n_heads
-                                          : (int64_t)(2 * blockIdx.x + (p.c0 ? 0 : 1)) * D.cap;
-            const int rows = min(16, p.nrows - r0);
-            if (t < rows) {
+            const bool direct = p->whole && D.streams == 1;
+            const int rows = min(16, nrows - r0);
+            if (t < 16) {
                 const int r = r0 + t;
-                float l = (S.red[0][r] + S.red[1][r]) + (S.red[2][r] + S.red[3][r]);
-                if (S.nan[r]) l = __int_as_float(0x7fc00000);
-                S.alpha[r] = direct ? (l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l)) : 1.0f;
-                if (!direct) W.ml[prow0 + (p.whole ? S.rowid[r] : r)] = make_float2(S.mc[r], l);
+                float *o = nullptr;
+                if (t < rows) {
+                    float l = (S.red[0][r] + S.red[1][r]) + (S.red[2][r] + S.red[3][r]);
+                    if (S.nan[r]) l = __int_as_float(0x7fc00000);
+                    const int64_t id = S.rowid[r];
+                    if (direct) {
+                        o = A.out + id * hd;
+                        l = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+                    } else {
+                        const int64_t row = p->whole ? (int64_t)2 * D.grid * D.cap + (int64_t)p->stream * A.n_lanes * A.n_heads + id
+                                                     : (int64_t)(2 * blockIdx.x + p->begins) * D.cap + r;
+                        o = W.part + row * hd;
+                        W.ml[row] = make_float2(S.mc[r], l);
+                        l = 1.0f;
+                    }
+                    S.alpha[r] = l;
+                }
+                S.optr[r] = o;
             }
             take();
             tc_fence_before();
             al_bar(wg);
+            if (lane == 0) ref.done(S);
 #pragma unroll
-            for (int j = 0; j < 16; j++)
-                if (j < rows) {
-                    const int r = r0 + j;
-                    const int64_t id = S.rowid[r];
-                    const float al = S.alpha[r];
-                    float *o = direct ? A.out + id * hd : W.part + (prow0 + (p.whole ? id : r)) * hd;
+            for (int j = 0; j < 16; j++) {
+                float *o = S.optr[r0 + j];
+                if (o) {
+                    const float al = S.alpha[r0 + j];
                     if (t < hd) o[t] = __fmul_rn(acc[0][j], al);
                     if (t + 128 < hd) o[t + 128] = __fmul_rn(acc[1][j], al);
                 }
+            }
         }
     }
     tc_fence_before();
@@ -1191,8 +1245,7 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
     AlPlan P{W.head, nullptr, W.tile_of, W.tiles};
     if (A.n_lanes <= kSelfPlan) {
         if (tid < kSelfPlan)
-            make_plan<kSelfPlan>(A, D, x.pos, x.seq, x.pre, x.red, &plan.head, &plan.first, kMaxCtas, x.tile_of,
-                                          plan.tiles, nullptr);
+            make_plan<kSelfPlan>(A, D, x.lane, x.red, &plan.head, &plan.first, kMaxCtas, x.tile_of, plan.tiles, nullptr);
         P = AlPlan{&plan.head, nullptr, x.tile_of, plan.tiles};
         __syncthreads();
     }
@@ -1441,7 +1494,7 @@ qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t work
     D.merge = A.n_lanes <= kSelfPlan ? 1 : 32;
     D.c = (float)(1.4426950408889634 / std::sqrt((double)A.hd));
     const void *kern = f32 ? (const void *)al_attn_kernel<3> : (const void *)al_attn_kernel<1>;
-    const size_t smem = kAlSmem, plan_smem = 3 * sizeof(int) * (size_t)A.n_lanes;
+    const size_t smem = kAlSmem, plan_smem = 6 * sizeof(int) * (size_t)A.n_lanes;
     QLIN_REQUIRE((int)smem <= max_smem_optin(), QLIN_ERR_UNSUPPORTED, "%s: shared memory", fn);
     blocks_per_sm(kern, smem);  // raises the dynamic shared-memory limit once
     blocks_per_sm((const void *)al_plan_kernel, plan_smem);
