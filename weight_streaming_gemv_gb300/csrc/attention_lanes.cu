@@ -143,10 +143,12 @@ struct AlSelfPlan {  // in shared memory
     int first;
 };
 
-// a * b / c for 0 <= b < c
-__device__ __forceinline__ int64_t muldiv(int64_t a, int b, int c) {
-    const int64_t p = a * b;
-    return (p >> 32) ? p / c : (int64_t)((uint32_t)p / (uint32_t)c);
+// The first unit of CTA b of the `grid` that have work: units * b / grid (in 32
+// bits where that is enough: it stands at the head of every CTA's work).
+__device__ __forceinline__ int64_t unit_of(int64_t units, int b, int grid, const AlDims &D) {
+    if (units <= D.grid) return b;
+    const uint64_t p = (uint64_t)units * (uint32_t)b;
+    return (p >> 32) ? (int64_t)(p / (uint32_t)grid) : (int64_t)((uint32_t)p / (uint32_t)grid);
 }
 
 __device__ __forceinline__ int64_t tile_units(int nch, const AlArgs &A, const AlDims &D) {
@@ -208,10 +210,15 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
                 __ballot_sync(0xffffffffu, valid && (i == 0 || spos[i - 1] < 0 || !same(i, i - 1)));
             if (lane == 0) red.last[warp] = starts ? i + 31 - __clz(starts) : -1;
             bar();
-            const int lw = lane < T / 32 ? red.last[lane] : -1;
-            const int rs0 = max(run, __reduce_max_sync(0xffffffffu, lane < warp ? lw : -1));
-            run = max(run, __reduce_max_sync(0xffffffffu, lw));
-            int rs = rs0;
+            int rs = run;
+            if (T == 64) {
+                if (warp == 1) rs = max(rs, red.last[0]);
+                run = max(run, max(red.last[0], red.last[1]));
+            } else {
+                const int lw = lane < T / 32 ? red.last[lane] : -1;
+                rs = max(run, __reduce_max_sync(0xffffffffu, lane < warp ? lw : -1));
+                run = max(run, __reduce_max_sync(0xffffffffu, lw));
+            }
             const uint32_t upto = starts & (0xffffffffu >> (31 - lane));
             if (upto) rs = i - lane + 31 - __clz(upto);
             const int in_tile = valid ? (i - rs) % D.LT : 0;
@@ -258,11 +265,17 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
             }
             if (lane == 31) red.sum[warp] = in;
             bar();
-            int64_t total = lane < T / 32 ? red.sum[lane] : 0, before = lane < warp ? total : 0;
+            int64_t total, before;
+            if (T == 64) {
+                before = warp ? red.sum[0] : 0;
+                total = red.sum[0] + red.sum[1];
+            } else {
+                total = lane < T / 32 ? red.sum[lane] : 0, before = lane < warp ? total : 0;
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                total += __shfl_xor_sync(0xffffffffu, total, off);
-                before += __shfl_xor_sync(0xffffffffu, before, off);
+                for (int off = 16; off > 0; off >>= 1) {
+                    total += __shfl_xor_sync(0xffffffffu, total, off);
+                    before += __shfl_xor_sync(0xffffffffu, before, off);
+                }
             }
             before += in - mine;
             const int ti = tiles + (int)(before >> 48);
@@ -284,14 +297,14 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
     // CTA b takes the units [U b / grid, U (b + 1) / grid): at least one each
     const int grid = (int)min((int64_t)D.grid, units);
     if (tid == 0) head->units = units, head->grid = grid, head->rmax = rmax;
-    const int64_t own = cta >= 0 && cta < grid ? muldiv(units, cta, grid) : -1;
+    const int64_t own = cta >= 0 && cta < grid ? unit_of(units, cta, grid, D) : -1;
 #pragma unroll 1
     for (int i = tid; i < tiles; i += T) {
         const int64_t u0 = tiles_out[i].unit0, u1 = u0 + tile_units(tiles_out[i].nch, A, D);
         if (cta >= 0) {
             if (own >= u0 && own < u1) *first = i;
         } else if (u0 < u1) {
-            for (int64_t b = (u0 * grid + units - 1) / units; b < grid && muldiv(units, (int)b, grid) < u1; b++)
+            for (int64_t b = (u0 * grid + units - 1) / units; b < grid && unit_of(units, (int)b, grid, D) < u1; b++)
                 first[b] = i;
         }
     }
@@ -347,15 +360,15 @@ struct Walker {
     int64_t u, hi;
     int turn;  // units of a CTA
     const AlTile *at;
-    __device__ __forceinline__ explicit Walker(const AlPlan &P) {
+    __device__ __forceinline__ Walker(const AlPlan &P, const AlDims &D) {
         const int64_t U = P.head->units;
         const int G = P.head->grid;
         u = hi = 0;
         turn = 1;
         if ((int)blockIdx.x < G) {
-            turn = (int)min(muldiv(U + G - 1, 1, G), (int64_t)INT_MAX);
-            u = muldiv(U, (int)blockIdx.x, G);
-            hi = (int)blockIdx.x + 1 == G ? U : muldiv(U, (int)blockIdx.x + 1, G);
+            u = unit_of(U, (int)blockIdx.x, G, D);
+            hi = (int)blockIdx.x + 1 == G ? U : unit_of(U, (int)blockIdx.x + 1, G, D);
+            turn = (int)min(unit_of(U, 1, G, D) + 1, (int64_t)INT_MAX);
             at = P.tiles + *P.first;
         }
     }
@@ -364,13 +377,13 @@ struct Walker {
             while (u >= at->unit0 + tile_units(at->nch, A, D)) at++;
             const int nch = at->nch, per = nch + kSetup;
             const int64_t r = u - at->unit0;
-            const int64_t sub = (r >> 31) ? r / per : (int64_t)((uint32_t)r / (uint32_t)per);
+            const int64_t sub = r < per ? 0 : (r >> 31) ? r / per : (int64_t)((uint32_t)r / (uint32_t)per);
             const int v0 = (int)(r - sub * per), v1 = (int)min((int64_t)per, v0 + (hi - u));
             u += v1 - v0;
             if (v1 <= kSetup) continue;  // the next CTA starts it
             const int kvh = D.HB == 1 ? (int)sub : (int)(sub / D.HB), hb = (int)sub - kvh * D.HB;
             const int c0 = max(v0 - kSetup, 0), c1 = v1 - kSetup;
-            const int over = c0 % turn;
+            const int over = c0 < turn ? c0 : c0 % turn;
             p.first = c0 + (over && turn - over < c1 - c0 ? turn - over : 0), p.c1 = c1;
             p.nsink = at->nsink, p.cfirst = at->cfirst;
             const int base = at->base, lim = at->lim, pmin = at->pmin - base, pmax = at->pmax - base;
@@ -399,7 +412,7 @@ struct AlCfg {
     static constexpr int kWg = R / 16;              // warpgroups, 16 rows each
     static constexpr int kTerm = 16384;             // 128 keys x 64 dims, or 64 keys x 128 dims, in bf16
     static constexpr int kSlot = NT * kTerm;
-    static constexpr int kProd = NT == 1 ? 1 : 8;   // producer warps
+    static constexpr int kProd = NT == 1 ? 1 : 16;  // producer warps
     // after the warpgroups, and the producers of an fp32 cache: a warp that issues the MMAs, one that describes the
     // pieces, one that copies the slices of a bf16 cache or describes those of an fp32 cache to the producers, one idle
     // (registers are dealt out by warpgroup)
@@ -505,17 +518,17 @@ __device__ __forceinline__ bool al_wait(uint64_t *bar, uint32_t parity, int *abo
 }
 
 // Two values as three pairs of bf16 terms (the first value in the low half).
-__device__ __forceinline__ uint32_t al_pack(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
+// The terms are cut off, not rounded: 8 significant bits, the next 8 and the
+// last 8, so that the three add up to the value exactly, with no conversion
+// instruction (an infinity or NaN gives a NaN below itself).
 __device__ __forceinline__ void al_split2(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    hi = al_pack(a, b);
-    a = __fsub_rn(a, __uint_as_float(hi << 16)), b = __fsub_rn(b, __uint_as_float(hi & 0xffff0000u));
-    mid = al_pack(a, b);
-    a = __fsub_rn(a, __uint_as_float(mid << 16)), b = __fsub_rn(b, __uint_as_float(mid & 0xffff0000u));
-    lo = al_pack(a, b);
+    hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    a = __fsub_rn(a, __uint_as_float(__float_as_uint(a) & 0xffff0000u));
+    b = __fsub_rn(b, __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+    mid = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    a = __fsub_rn(a, __uint_as_float(__float_as_uint(a) & 0xffff0000u));
+    b = __fsub_rn(b, __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+    lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -590,30 +603,28 @@ struct AlMaps {
 };
 
 // The slices of a piece in the order in which they pass through the ring: K of
-// chunk 0, then for every chunk K of the next one and its own V.
-struct SliceGen {
-    const AlPiece *p;
-    int i, sl, r0;  // r0: the chunk's first row
-    bool v;
-    __device__ __forceinline__ explicit SliceGen(const AlPiece *q) : p(q), i(0), sl(0), v(false) { r0 = p->row0(0); }
-    // false: that was the last one
-    __device__ __forceinline__ bool step(int nK, int nV) {
-        if (++sl < (v ? nV : nK)) return true;
-        sl = 0;
-        // step i: K of chunk i (if there is one), then V of chunk i - 1 (if there is one)
-        if (!v && i >= 1) {
-            v = true;
-        } else if (!v && p->n == 1) {
-            v = true, i = 1;
-        } else {
-            i++;
-            v = i >= p->n;
-            if (i > p->n) return false;
-        }
-        r0 = p->row0(v ? i - 1 : i);
-        return true;
+// chunk 0, then for every chunk K of the next one and its own V.  f(v, row,
+// dim): a slice of V or K from that row and dim on; it returns false to stop.
+// (One thread runs this among busy warps: what a piece's slices share is in
+// registers.)
+template <typename F>
+__device__ __forceinline__ bool for_slices(const AlPiece &p, int nK, int nDH, F f) {
+    const int n = p.n, c1 = p.c1, nsink = p.nsink, skip = p.cfirst - nsink;
+    int c = p.first, prev = 0;
+    for (int i = 0; i <= n; i++) {
+        const int row = (c < nsink ? c : c + skip) * kChunk;
+        if (++c == c1) c -= n;
+        if (i < n)
+            for (int sl = 0; sl < nK; sl++)
+                if (!f(false, row, 64 * sl)) return false;
+        if (i >= 1)
+            for (int kh = 0; kh < 2; kh++)
+                for (int dh = 0; dh < nDH; dh++)
+                    if (!f(true, prev + 64 * kh, 128 * dh)) return false;
+        prev = row;
     }
-};
+    return true;
+}
 
 // A place in the ring: slot and the parity of its round.
 struct RingPos {
@@ -704,31 +715,33 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
 
     if (NT == 3 && warp >= C::kProd0 && warp < C::kProd0 + C::kProd) {
         // ---------------------------------------------------------- producers of an fp32 cache's slices
-        // 32 rows at a time: thread t takes row t / 8, dims 4 (t % 8) .. + 3 and the same 32 dims on (eight
-        // threads read 128 bytes of a row at once); four such passes are a slice's 128 rows (a V slice's rows
-        // 64 .. 127 are the second 64 dims of its 64 keys)
-        const int pt = tid - 32 * C::kProd0, pr = pt >> 3, pc = pt & 7;
-        uint4 buf[2][8];
+        if constexpr (NT == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // 64 rows at a time: eight threads take dims 4 pc .. + 3 of a row and the same 32 dims on (they read 128 bytes
+        // of it at once); two such passes are a slice's 128 rows (a V slice's rows 64 .. 127 are the second 64 dims of
+        // its 64 keys)
+        // (a warp's four rows are 0, 4, 1, 5 or 2, 6, 3, 7 of eight: their swizzled halves fill all banks)
+        const int pw = warp - C::kProd0, pj = lane >> 3, pc = lane & 7;
+        const int pr = (pw >> 1) * 8 + (pw & 1) * 2 + (pj & 1) * 4 + (pj >> 1);
+        uint4 buf[2][4];
         int ds = 0;
         uint32_t dpar = 0;
         bool ok = true, have[2];
         // the next slice of the ring of descriptions; false when there is none
-        auto load = [&](uint4 (&o)[8]) -> bool {
+        auto load = [&](uint4 (&o)[4]) -> bool {
             if (!(ok = al_wait(&S.sl_full[ds], dpar, &S.abort))) return false;
             const AlSlice &q = S.slice[ds];
             const bool more = q.src != nullptr;
             if (more) {
                 const int key0 = q.y0 + pr, dims = q.dims - 4 * pc, v = q.v;
-                const int64_t step = 32 * q.stride;
                 const float *a = q.src + pr * q.stride + 4 * pc;
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    // K: 32 rows on; V: the other half of its 64 rows, then 64 dims on
-                    const int key = key0 + (v ? (e & 1) * 32 : e * 32), d = v ? (e >> 1) * 64 : 0;
+                for (int e = 0; e < 2; e++) {
+                    // K: 64 rows on; V: 64 dims on
+                    const int key = key0 + (v ? 0 : e * 64), d = v ? e * 64 : 0;
                     const bool any = key <= q.any_hi && (key > q.any_lo || key < q.sk);
                     al_ld16(a, any && d < dims, o[2 * e]);
                     al_ld16(a + 32, any && d + 32 < dims, o[2 * e + 1]);
-                    a = v && e == 1 ? a - step + 64 : a + step;
+                    a += v ? 64 : 64 * q.stride;
                 }
             }
             __syncwarp();
@@ -752,8 +765,8 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 }
                 const uint32_t to = smem_addr(ring + s * C::kSlot);
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int r = e * 32 + pr;
+                for (int e = 0; e < 2; e++) {
+                    const int r = e * 64 + pr;
 #pragma unroll
                     for (int q = 0; q < 2; q++) {
                         const uint4 v = buf[k][2 * e + q];
@@ -774,12 +787,12 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             }
         }
     } else if (warp >= C::kMma) {
-        // 640 threads are launched with 96 registers (61440 in all): 128 x 56 here, 256 x 112 for the weights and
-        // 256 x 96 for the producers make 60416
-        if constexpr (NT == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // 896 threads are launched with 72 registers (64512 in all): 128 x 40 here, 256 x 104 for the weights and
+        // 512 x 64 for the producers are as many
+        if constexpr (NT == 3) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == C::kWalk && al_elect()) {
             // ------------------------------------------------------ describes the pieces
-            Walker w(P);
+            Walker w(P, D);
             for (int k = 0;; k++) {
                 const int r = k % kPieceRing;
                 if (k >= kPieceRing && !al_wait(&S.pc_empty[r], (uint32_t)(k / kPieceRing - 1) & 1u, &S.abort)) {
@@ -802,27 +815,25 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             while (ok) {
                 const AlPiece *p = ref.next(S);
                 if (!(ok = p != nullptr) || p->n == 0) break;
-                SliceGen sg(p);
                 const CUtensorMap *mk = &maps.k[p->stream], *mv = &maps.v[p->stream];
                 const int z = (p->stream ? A.own : A.pre).seq_stride ? p->slot : 0, x0 = p->kvh * hd;
-                for (bool more = true; more; g++) {
+                const int any_lo = p->any_lo, any_hi = p->any_hi, sk = p->sk;
+                // two boxes of 64 keys x 64 dims, those that nobody sees left out: K's are the two halves of the
+                // chunk, V's (of one half) the two halves of 128 dims
+                ok = for_slices(*p, nK, nDH, [&](bool v, int row, int dim) {
                     const int s = at.s;
-                    if (at.round && !(ok = al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort))) break;
-                    // two boxes of 64 keys x 64 dims, those that nobody sees left out: K's are the two halves of the
-                    // chunk, V's (of one half) the two halves of 128 dims
+                    if (at.round && !al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort)) return false;
                     const uint32_t to = smem_addr(ring + s * C::kSlot), full = smem_addr(&S.full[s]);
-                    const int kh = nDH == 2 ? sg.sl >> 1 : sg.sl, dh = nDH == 2 ? sg.sl & 1 : 0;
-                    const int d0 = sg.v ? 128 * dh : 64 * sg.sl, y0 = sg.r0 + (sg.v ? 64 * kh : 0);
-                    const bool on0 = p->any_in(y0, y0 + 64);
-                    const bool on1 = sg.v ? on0 && d0 + 64 < hd : p->any_in(y0 + 64, y0 + 128);
+                    auto any_in = [&](int a, int b) { return a <= any_hi && (b - 1 > any_lo || a < sk); };
+                    const bool on0 = any_in(row, row + 64), on1 = v ? on0 && dim + 64 < hd : any_in(row + 64, row + 128);
                     mbar_arrive_expect_tx(&S.full[s], 8192u * ((uint32_t)on0 + (uint32_t)on1));
-                    const CUtensorMap *map = sg.v ? mv : mk;
-                    if (on0) al_tma(to, map, x0 + d0, y0, z, full);
-                    if (on1) al_tma(to + 8192, map, x0 + d0 + (sg.v ? 64 : 0), y0 + (sg.v ? 0 : 64), z, full);
-                    more = sg.step(nK, nV);
+                    if (on0) al_tma(to, v ? mv : mk, x0 + dim, row, z, full);
+                    if (on1) al_tma(to + 8192, v ? mv : mk, x0 + dim + (v ? 64 : 0), row + (v ? 0 : 64), z, full);
                     at.step(slots);
-                }
-                ref.done(S);
+                    g++;
+                    return true;
+                });
+                if (ok) ref.done(S);
             }
             if (!ok) {
                 S.abort = 1;
@@ -834,33 +845,42 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         if (NT == 3 && warp == C::kCopy && al_elect()) {
             // ------------------------------------------------------ describes the slices of an fp32 cache
             PieceRef ref;
-            bool ok = true, end = false;
-            int g = 0;
-            while (ok && !end) {
+            int ds = 0;
+            uint32_t dround = 0;
+            bool ok = true;
+            // the next entry of the ring of descriptions; null: gave up
+            auto entry = [&]() -> AlSlice * {
+                return dround && !al_wait(&S.sl_empty[ds], (dround - 1) & 1u, &S.abort) ? nullptr : &S.slice[ds];
+            };
+            auto publish = [&]() {
+                mbar_arrive(&S.sl_full[ds]);
+                if (++ds == kSliceRing) ds = 0, dround++;
+            };
+            while (ok) {
                 const AlPiece *p = ref.next(S);
                 if (!(ok = p != nullptr)) break;
-                end = p->n == 0;
-                SliceGen sg(p);
-                const qlin_kv &kv = p->stream ? A.own : A.pre;
-                const int64_t off = (int64_t)p->slot * kv.seq_stride + p->kvh * hd;
-                for (bool more = true; more; g++) {
-                    const int ds = g % kSliceRing;
-                    if (g >= kSliceRing && !(ok = al_wait(&S.sl_empty[ds], (uint32_t)(g / kSliceRing - 1) & 1u, &S.abort)))
-                        break;
-                    AlSlice &q = S.slice[ds];
-                    q.src = nullptr;
-                    more = !end;
-                    if (!end) {
-                        const int kh = nDH == 2 ? sg.sl >> 1 : sg.sl, dh = nDH == 2 ? sg.sl & 1 : 0;
-                        const int d0 = sg.v ? 128 * dh : 64 * sg.sl, y0 = sg.r0 + (sg.v ? 64 * kh : 0);
-                        q.src = static_cast<const float *>(sg.v ? kv.v : kv.k) + off + y0 * kv.row_stride + d0;
-                        q.stride = kv.row_stride;
-                        q.y0 = y0, q.any_lo = p->any_lo, q.any_hi = p->any_hi, q.sk = p->sk;
-                        q.v = sg.v, q.dims = hd - d0;
-                        more = sg.step(nK, nV);
+                if (p->n == 0) {
+                    AlSlice *q = entry();
+                    if ((ok = q != nullptr)) {
+                        q->src = nullptr;
+                        publish();
                     }
-                    mbar_arrive(&S.sl_full[ds]);
+                    break;
                 }
+                const qlin_kv &kv = p->stream ? A.own : A.pre;
+                const int64_t off = (int64_t)p->slot * kv.seq_stride + p->kvh * hd, stride = kv.row_stride;
+                const float *ksrc = static_cast<const float *>(kv.k) + off, *vsrc = static_cast<const float *>(kv.v) + off;
+                const int any_lo = p->any_lo, any_hi = p->any_hi, sk = p->sk;
+                ok = for_slices(*p, nK, nDH, [&](bool v, int row, int dim) {
+                    AlSlice *q = entry();
+                    if (!q) return false;
+                    q->src = (v ? vsrc : ksrc) + row * stride + dim;
+                    q->stride = stride;
+                    q->y0 = row, q->any_lo = any_lo, q->any_hi = any_hi, q->sk = sk;
+                    q->v = v, q->dims = hd - dim;
+                    publish();
+                    return true;
+                });
                 if (ok) ref.done(S);
             }
             if (!ok) {
@@ -950,7 +970,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     } else {
         // ---------------------------------------------------------- weights and sums: warpgroup wg owns rows
         // 16 wg .. 16 wg + 15, its thread t key t of a chunk, and of the outputs dims t and t + 128
-        if constexpr (NT == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+        if constexpr (NT == 3) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int wg = warp >> 2, t = tid & 127, r0 = 16 * wg;
         PieceRef ref;
         int g = 0, it = 0;   // slices and chunks so far
@@ -988,16 +1008,16 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 S.rowid[r] = in ? ln * A.n_heads + p->head0 + r % gs : -1;
                 S.rowhi[r] = max(-1, min(pl, p->lim - 1));
                 S.rowlo[r] = A.window && pl >= A.window ? pl - A.window : -1;
-                S.mc[r] = kNoKey;
+                S.mc[r] = in ? kNoKey : -ninf;  // (what lies in the place of a row that is not there gets no weight)
                 S.nan[r] = 0;
             }
             al_bar(wg);
             // the rows' q as three bf16 terms
 #pragma unroll 4
-            for (int e = t; e < 2 * hd; e += 128) {
-                const int rr = e / (hd / 8), d8 = e - rr * (hd / 8), r = r0 + rr, id = S.rowid[r];
+            for (int e = t; e < min(16, nrows - r0) * (hd / 8); e += 128) {
+                const int rr = e / (hd / 8), d8 = e - rr * (hd / 8), r = r0 + rr;
                 uint4 a, b, h, m, l;
-                al_ld32(A.q + (int64_t)max(id, 0) * hd + 8 * d8, id >= 0, a, b);
+                al_ld32(A.q + (int64_t)S.rowid[r] * hd + 8 * d8, true, a, b);
                 al_split8(a, b, h, m, l);
                 const uint32_t at = smem_addr(qs) + (uint32_t)((d8 >> 3) * L.qslice + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
                 sts128(at, h);
