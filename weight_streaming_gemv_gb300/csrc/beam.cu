@@ -8,12 +8,16 @@
 // end token.  The n largest of a group come out in descending order, ties to
 // the lower b * vocab + v.
 //
-// Two launches.  beam_slice_kernel reads every logit once: a CTA holds one
-// slice of one beam's row in registers, forms the slice's part of the sum and
-// finds its n largest logits (inside a beam the order of the candidates is the
-// order of the logits).  beam_merge_kernel, one CTA per group, adds the sums
-// up and merges the slices' sorted lists.  Bound by the logits' bytes from a
-// few rows on; below that by the two launches.
+// Two launches.  beam_slice_kernel reads every logit once: a CTA walks a slice
+// of one beam's row, a few thousand values in registers at a time with the next
+// ones in flight, sums the exponentials and keeps the values that can be among
+// the slice's n largest logits (inside a beam the order of the candidates is
+// the order of the logits).  What can be is told by a threshold: the largest
+// values of a warp's threads, in order; n of the block's values are no smaller
+// than the least of its warps' ceil(n / 8)-th.  beam_merge_kernel, one CTA per
+// group, adds the sums up and takes the n best of the slices' sorted lists,
+// again by a threshold (on the lists' heads) first.  Bound by the logits' bytes
+// from a few dozen rows on, below that by the two launches.
 //
 // Two beams' candidates can lie closer together than fp32 resolves, so lse
 // and the candidates are held in fp64.  The sum's parts are exact to scale: a
@@ -41,9 +45,9 @@ constexpr int kMaxBeams = 64;
 constexpr int kMaxOut = 128;
 
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 256;
+constexpr int kSelThreads = 256, kSelPerSm = 3;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBuf = 1024;  // candidates of a slice ranked in shared memory
+constexpr int kSelBuf = 1024;  // candidates of a slice in shared memory
 
 // fp32 as an unsigned whole number in the same order
 __device__ __forceinline__ uint32_t ord32(float v) {
@@ -94,177 +98,299 @@ __device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *fi
     return !(finished && finished[row]) && scores[row] > -__int_as_float(0x7f800000);
 }
 
-// grid (S, rows).  Thread t holds VPT values of the slice [slice, slice + 256
-// VPT): 16-byte groups t, t + 256, ... with VEC (rows 16-byte aligned), single
+// A slice's candidates so far, in shared memory.
+struct SelBuf {
+    uint64_t key[kSelBuf];
+    int count;
+};
+
+// The place of key `mine` (and `tie`, smaller first) among c keys: the number
+// of larger ones.  The high words tell nearly all of them apart.
+template <typename Tie>
+__device__ __forceinline__ int place_of(uint64_t mine, Tie tie, const uint64_t *key, const Tie *ties, int c) {
+    const uint32_t hi = (uint32_t)(mine >> 32);
+    const uint32_t *his = reinterpret_cast<const uint32_t *>(key) + 1;
+    int r = 0, eq = 0;
+#pragma unroll 8
+    for (int q = 0; q < c; q++) {
+        const uint32_t h = his[2 * q];
+        r += h > hi;
+        eq += h == hi;
+    }
+    if (eq > 1)
+        for (int q = 0; q < c; q++) {
+            const uint64_t k = key[q];
+            if ((uint32_t)(k >> 32) == hi && (k > mine || (k == mine && ties[q] < tie))) r++;
+        }
+    return r;
+}
+
+// The n largest of the c (<= kSelBuf) keys of b to out, in descending order
+// (keys are unique).
+__device__ __forceinline__ void sel_rank(const SelBuf &b, int c, int n, uint64_t *out) {
+    for (int i = threadIdx.x; i < c; i += kSelThreads) {
+        const uint64_t key = b.key[i];
+        const int r = place_of<uint64_t>(key, 0, b.key, b.key, c);
+        if (r < n) out[r] = key;
+    }
+}
+
+// grid (S, rows): slice blockIdx.x of a row is the values from blockIdx.x * len
+// on, `len` of them (a multiple of 4), taken in tiles of 256 VPT: thread t
+// holds 16-byte groups t, t + 256, ... with VEC (rows 16-byte aligned), single
 // values t, t + 256, ... without.
 template <int VPT, bool VEC>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     beam_slice_kernel(const float *__restrict__ logits, int64_t row_stride, const float *__restrict__ scores,
-                      const uint8_t *__restrict__ finished, int V, int n, SelPart *part, uint64_t *cand) {
+                      const uint8_t *__restrict__ finished, int V, int len, int n, SelPart *part, uint64_t *cand) {
+    constexpr int kTile = kSelThreads * VPT;
     __shared__ float wmax[kSelWarps];
-    __shared__ double wsum[kSelWarps];
+    __shared__ float2 wsum[kSelWarps];
     __shared__ uint32_t wkth[kSelWarps];
-    __shared__ int count;
-    __shared__ uint64_t buf[kSelBuf];
+    __shared__ SelBuf buf;
+    __shared__ uint64_t best[kMaxOut];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = blockIdx.y, S = gridDim.x, sl = blockIdx.x;
+    const int row = blockIdx.y, S = gridDim.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!beam_live(scores, finished, row)) return;  // (the merge skips its parts)
     const float ninf = -__int_as_float(0x7f800000);
-    const int v0 = sl * (kSelThreads * VPT);
+    const int v0 = blockIdx.x * len, v1 = min(v0 + len, V);
     const float *x = logits + (int64_t)row * row_stride;
-    float v[VPT];
-    auto index = [&](int j) { return VEC ? v0 + ((j >> 2) * kSelThreads + tid) * 4 + (j & 3) : v0 + j * kSelThreads + tid; };
-    if (tid == 0) count = 0;
-    if constexpr (VEC) {
+    auto index = [&](int j) { return VEC ? ((j >> 2) * kSelThreads + tid) * 4 + (j & 3) : j * kSelThreads + tid; };
+    auto load = [&](int at, float (&v)[VPT]) {
+        // (the loads of a whole tile are predicated, not branched to: none is waited for before the next is out)
+        const bool whole = at + kTile <= v1;
+        if (!whole)
 #pragma unroll
-        for (int j = 0; j < VPT; j += 4) {
-            const int i = index(j);
-            float4 f = make_float4(ninf, ninf, ninf, ninf);
-            if (i + 3 < V) {
-                f = __ldcs(reinterpret_cast<const float4 *>(x + i));
-            } else {
-                if (i < V) f.x = x[i];
-                if (i + 1 < V) f.y = x[i + 1];
-                if (i + 2 < V) f.z = x[i + 2];
+            for (int j = 0; j < VPT; j++) {
+                const int i = at + index(j);
+                v[j] = i < v1 ? x[i] : ninf;
             }
-            v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
-        }
-    } else {
 #pragma unroll
-        for (int j = 0; j < VPT; j++) {
-            const int i = index(j);
-            v[j] = i < V ? __ldcs(x + i) : ninf;
+        for (int j = 0; j < VPT; j += VEC ? 4 : 1) {
+            if constexpr (VEC)
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+                    : "+f"(v[j]), "+f"(v[j + 1]), "+f"(v[j + 2]), "+f"(v[j + 3])
+                    : "l"(x + at + index(j)), "r"((uint32_t)whole));
+            else
+                asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.cs.f32 %0, [%1];\n\t}"
+                             : "+f"(v[j])
+                             : "l"(x + at + index(j)), "r"((uint32_t)whole));
         }
-    }
-    float tmax = ninf;
-#pragma unroll
-    for (int j = 0; j < VPT; j++) tmax = fmaxf(tmax, v[j]);
-    // the k-th largest of the warp's thread maxima, k = ceil(n / warps): at
-    // least n values of the slice are no smaller than the least of the warps'
-    uint32_t mine = ord32(tmax), kth = 0, wtop = 0;
+    };
+    float v[VPT], nx[VPT];
+    float m, sum;  // this thread's largest value and its sum times 2^e
+    int e, c;
+    uint32_t thr;  // n values of the slice so far are no smaller (minus infinity is no candidate)
     const int k = (n + kSelWarps - 1) / kSelWarps;  // at most 16
-    for (int r = 0; r < k; r++) {
-        kth = __reduce_max_sync(0xffffffffu, mine);
-        if (r == 0) wtop = kth;
-        const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
-        if (lane == __ffs(who) - 1) mine = 0;
-    }
-    if (lane == 0) wmax[warp] = unord32(wtop), wkth[warp] = kth;
-    __syncthreads();
-    float m = wmax[0];
-    uint32_t thr = wkth[0];
+    // Once without looking at the buffer after every tile; where that let it
+    // overflow (many equal values) once more, carefully.
+    for (bool careful = false;; careful = true) {
+        load(v0, v);
+        if (tid == 0) buf.count = 0;
+        m = ninf, sum = 0.0f, e = -(1 << 28);
+        thr = kOrdNegInf + 1;
+        bool over = false;
+        int tile = 0;
+        for (int at = v0; at < v1 && !over; at += kTile, tile++) {
+            if (at + kTile < v1) load(at + kTile, nx);
+            float tmax = ninf;
 #pragma unroll
-    for (int w = 1; w < kSelWarps; w++) m = fmaxf(m, wmax[w]), thr = min(thr, wkth[w]);
-    const bool wide = sel_wide(m);
-    const float ef = sel_exp(m);
-    float s = 0.0f;
-    bool bad = false;  // NaN or +infinity: the beam's sum becomes NaN
-#pragma unroll
-    for (int j = 0; j < VPT; j++) {
-        // x log2(e) - e with log2(e) in two parts: the rounding of one would
-        // be the same for a whole beam
-        const float y = wide ? __fmul_rn(__fsub_rn(v[j], m), kLog2eHi)
-                             : __fmaf_rn(v[j], kLog2eLo, __fmaf_rn(v[j], kLog2eHi, -ef));
-        s += v[j] > ninf ? ex2_approx(y) : 0.0f;
-        bad |= !(v[j] < -ninf);
-    }
-    double d = bad ? (double)__int_as_float(0x7fc00000) : (double)s;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-    if (lane == 0) wsum[warp] = d;
-    // the values no smaller than the threshold
-    if (thr < kOrdNegInf + 1) thr = kOrdNegInf + 1;
-#pragma unroll
-    for (int j = 0; j < VPT; j++) {
-        const uint32_t o = ord32(v[j]);
-        if (o >= thr && v[j] == v[j]) {
-            const int at = atomicAdd(&count, 1);
-            if (at < kSelBuf) buf[at] = cand_key(v[j], (uint32_t)index(j));
-        }
-    }
-    __syncthreads();
-    int c = count;
-    if (c > kSelBuf) {
-        // many equal values: the n-th largest key bit by bit, then the n keys
-        // no smaller (keys are unique)
-        uint64_t t = 0;
-        for (int bit = 63; bit >= 0; bit--) {
-            const uint64_t tt = t | (1ull << bit);
-            int nn = 0;
-#pragma unroll
-            for (int j = 0; j < VPT; j++) nn += v[j] == v[j] && cand_key(v[j], (uint32_t)index(j)) >= tt;
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) nn += __shfl_xor_sync(0xffffffffu, nn, off);
-            __syncthreads();
-            if (lane == 0) wkth[warp] = (uint32_t)nn;
-            __syncthreads();
-            nn = 0;
-#pragma unroll
-            for (int w = 0; w < kSelWarps; w++) nn += (int)wkth[w];
-            if (nn >= n) t = tt;
-        }
-        if (tid == 0) count = 0;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < VPT; j++) {
-            const uint64_t key = cand_key(v[j], (uint32_t)index(j));
-            if (v[j] == v[j] && key >= t) {
-                const int at = atomicAdd(&count, 1);
-                if (at < kSelBuf) buf[at] = key;
+            for (int j = 0; j < VPT; j++) tmax = fmaxf(tmax, v[j]);
+            if (tmax > m) {
+                m = tmax;
+                // a whole-number scale at or above the largest term's exponent
+                const int ne = (int)fminf(fmaxf(sel_exp(m), -1e8f), 1e8f);
+                if (ne > e) sum *= pow2i(max(e - ne, -126)), e = ne;
             }
+            const float ef = (float)e;
+#pragma unroll
+            for (int j = 0; j < VPT; j++) {
+                // x log2(e) - e with log2(e) in two parts: the rounding of one
+                // would be the same for a whole beam (NaN stays in the sum, plus
+                // infinity makes it infinite, nothing else does)
+                sum += ex2_approx(__fmaf_rn(v[j], kLog2eLo, __fmaf_rn(v[j], kLog2eHi, -ef)));
+            }
+            // a threshold for the first two tiles and every fourth: it has settled by then
+            if (careful || tile < 2 || tile % 4 == 0) {
+                // the k-th largest of the warp's thread maxima
+                uint32_t mine = ord32(tmax), kth = 0;
+                for (int r = 0; r < k; r++) {
+                    kth = __reduce_max_sync(0xffffffffu, mine);
+                    const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
+                    if (lane == __ffs(who) - 1) mine = 0;
+                }
+                if (lane == 0) wkth[warp] = kth;
+                __syncthreads();
+                uint32_t tk = wkth[0];
+#pragma unroll
+                for (int w = 1; w < kSelWarps; w++) tk = min(tk, wkth[w]);
+                thr = max(thr, tk);
+                c = buf.count;
+                __syncthreads();
+                over = c > kSelBuf;
+                if (!over && c > kSelBuf / 2) {  // keep the n best
+                    sel_rank(buf, c, n, best);
+                    __syncthreads();
+                    c = min(c, n);
+                    for (int i = tid; i < c; i += kSelThreads) buf.key[i] = best[i];
+                    if (tid == 0) buf.count = c;
+                    __syncthreads();
+                }
+            }
+            const float low = unord32(thr);
+            if (tmax >= low && !over)  // (NaN is not)
+#pragma unroll
+                for (int j = 0; j < VPT; j++)
+                    if (v[j] >= low) {
+                        const int p = atomicAdd(&buf.count, 1);
+                        if (p < kSelBuf) buf.key[p] = cand_key(v[j], (uint32_t)(at + index(j)));
+                    }
+            if (careful) {
+                __syncthreads();
+                if (buf.count > kSelBuf) {
+                    // the tile's n-th largest key bit by bit, then the n keys no smaller
+                    uint64_t t = 0;
+                    for (int bit = 63; bit >= 0; bit--) {
+                        const uint64_t tt = t | (1ull << bit);
+                        int nn = 0;
+#pragma unroll
+                        for (int j = 0; j < VPT; j++)
+                            nn += v[j] == v[j] && cand_key(v[j], (uint32_t)(at + index(j))) >= tt;
+                        nn = (int)__reduce_add_sync(0xffffffffu, (unsigned)nn);
+                        __syncthreads();
+                        if (lane == 0) wkth[warp] = (uint32_t)nn;
+                        __syncthreads();
+                        nn = 0;
+#pragma unroll
+                        for (int w = 0; w < kSelWarps; w++) nn += (int)wkth[w];
+                        if (nn >= n) t = tt;
+                    }
+                    __syncthreads();
+                    if (tid == 0) buf.count = c;
+                    __syncthreads();
+#pragma unroll
+                    for (int j = 0; j < VPT; j++) {
+                        const uint64_t key = cand_key(v[j], (uint32_t)(at + index(j)));
+                        if (v[j] == v[j] && key >= t) buf.key[atomicAdd(&buf.count, 1)] = key;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; j++) v[j] = nx[j];
         }
         __syncthreads();
-        c = min(count, kSelBuf);
+        c = buf.count;
+        __syncthreads();
+        if (careful || (!over && c <= kSelBuf)) break;
     }
-    const int64_t ps = (int64_t)row * S + sl;
+    // the ones below the last threshold are out
+    {
+        uint64_t keep[kSelBuf / kSelThreads];
+#pragma unroll
+        for (int u = 0; u < kSelBuf / kSelThreads; u++)
+            keep[u] = tid + u * kSelThreads < c ? buf.key[tid + u * kSelThreads] : 0;
+        __syncthreads();
+        if (tid == 0) buf.count = 0;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kSelBuf / kSelThreads; u++)
+            if ((uint32_t)(keep[u] >> 32) >= thr) buf.key[atomicAdd(&buf.count, 1)] = keep[u];
+    }
+    // the block's largest value, and the sum on its scale (no thread's is above it)
+    float top = warp_max(m);
+    if (lane == 0) wmax[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelWarps; w++) top = fmaxf(top, wmax[w]);
+    float d;
+    if (sel_wide(top)) {
+        // logits beyond 2^24 (or none at all): once more, relative to the largest
+        d = 0.0f;
+        for (int i = v0 + tid; i < v1; i += kSelThreads)
+            if (x[i] > ninf) d += ex2_approx(__fmul_rn(__fsub_rn(x[i], top), kLog2eHi));
+    } else {
+        d = __fmul_rn(sum, pow2i(max(e - (int)sel_exp(top), -126)));
+    }
+    if (!(sum < -ninf)) d = __int_as_float(0x7fc00000);  // the beam's sum becomes NaN
+    // the threads' sums with the rounding of every addition kept (fp64 costs 16 cycles per instruction and warp here)
+    auto add = [](float &h, float &l, float oh, float ol) {
+        const float t = __fadd_rn(h, oh), z = __fsub_rn(t, h);
+        l = __fadd_rn(__fadd_rn(l, ol), __fadd_rn(__fsub_rn(h, __fsub_rn(t, z)), __fsub_rn(oh, z)));
+        h = t;
+    };
+    float dl = 0.0f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        add(d, dl, __shfl_xor_sync(0xffffffffu, d, off), __shfl_xor_sync(0xffffffffu, dl, off));
+    if (lane == 0) wsum[warp] = make_float2(d, dl);
+    __syncthreads();
+    c = buf.count;
+    const int64_t ps = (int64_t)row * S + blockIdx.x;
     if (tid == 0) {
         SelPart p;
-        p.sum = 0.0;
 #pragma unroll
-        for (int w = 0; w < kSelWarps; w++) p.sum += wsum[w];
-        p.m = m;
+        for (int w = 1; w < kSelWarps; w++) add(d, dl, wsum[w].x, wsum[w].y);
+        p.sum = (double)d + (double)dl;
+        p.m = top;
         p.count = min(c, n);
         part[ps] = p;
     }
-    // a key's place is the number of larger ones
-    for (int i = tid; i < c; i += kSelThreads) {
-        const uint64_t key = buf[i];
-        int r = 0;
-        for (int q = 0; q < c; q++) r += buf[q] > key;
-        if (r < n) cand[ps * n + r] = key;
-    }
+    sel_rank(buf, c, n, cand + ps * n);
 }
 
-constexpr int kMergeThreads = 512;
-constexpr int kOnly = 255;  // above kMaxOut
+constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeLists = 1024;  // beams * slices at most (sel_slices)
+constexpr int kMergeBuf = 2048;    // candidates ranked in shared memory
 
 __device__ __forceinline__ bool better(double c, int64_t at, double bc, int64_t bat) {
     return c > bc || (c == bc && at < bat);
 }
+// fp64 as an unsigned whole number in the same order, above 0 for all but NaN
+__device__ __forceinline__ uint64_t ord64(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double unord64(uint64_t k) {
+    return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
+}
+__device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+    return (uint64_t)hi << 32 | lo;
+}
 
-// One CTA per group: lse of every live beam, then n rounds of taking the best
-// head of the beams' sorted lists (S lists per live beam, one entry for a
-// finished one).
+struct MergeSmem {
+    double lse[kMaxBeams];  // the log of a beam's sum, less top
+    float top[kMaxBeams];   // its largest logit
+    uint64_t key[kMergeBuf];
+    int64_t at[kMergeBuf];
+    uint64_t kth[kMergeWarps], sharp;
+    double wc[kMergeWarps];
+    int64_t wat[kMergeWarps];
+    int wlist[kMergeWarps];
+    int count, passing;
+    uint16_t list[kMergeLists];
+    uint8_t next[kMergeLists];  // the next entry of each list
+};
+
+// One CTA per group: lse of every live beam, then the n best of the beams'
+// sorted lists (S lists per live beam, one entry for a finished one).
 __global__ void __launch_bounds__(kMergeThreads)
     beam_merge_kernel(const SelPart *__restrict__ part, const uint64_t *__restrict__ cand,
                       const float *__restrict__ scores, const uint8_t *__restrict__ finished, int eos, int beams, int V,
                       int S, int n, float *out_scores, int32_t *parents, int32_t *tokens) {
-    __shared__ double lse[kMaxBeams];  // the log of a beam's sum, less top
-    __shared__ float top[kMaxBeams];   // its largest logit
-    __shared__ double wc[kMergeThreads / 32];
-    __shared__ int64_t wat[kMergeThreads / 32];
-    __shared__ int wlist[kMergeThreads / 32];
-    __shared__ int won;
-    extern __shared__ uint8_t heads[];  // [beams * S]: the next entry of each list (kOnly: the beam itself)
+    extern __shared__ __align__(16) uint8_t mg_raw[];
+    MergeSmem &M = *reinterpret_cast<MergeSmem *>(mg_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const float ninf = -__int_as_float(0x7f800000);
     const double dninf = (double)ninf;
-    for (int b = warp; b < beams; b += kMergeThreads / 32) {
+    for (int b = warp; b < beams; b += kMergeWarps) {
         const int row = g * beams + b;
         double l = 0.0;
         float big = ninf;
@@ -272,7 +398,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             const SelPart *p = part + (int64_t)row * S;
             for (int i = lane; i < S; i += 32) big = fmaxf(big, __ldcg(&p[i].m));
             big = warp_max(big);
-            const double M = (double)big, E = (double)sel_exp(big);
+            const double top = (double)big, E = (double)sel_exp(big);
             const double ln2 = 0.69314718055994530942;
             double s = 0.0;
             for (int i = lane; i < S; i += 32) {
@@ -282,68 +408,128 @@ __global__ void __launch_bounds__(kMergeThreads)
                     const int sh = sel_wide(mi) ? -1000 : max((int)(sel_exp(mi) - (float)E), -1000);
                     s += si * __hiloint2double((sh + 1023) << 20, 0);
                 } else if (mi > ninf) {
-                    s += si * exp((sel_wide(mi) ? (double)mi : (double)sel_exp(mi) * ln2) - M);
+                    s += si * exp((sel_wide(mi) ? (double)mi : (double)sel_exp(mi) * ln2) - top);
                 } else {
                     s += si;  // 0, or NaN
                 }
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            l = log(s) + (sel_wide(big) ? 0.0 : E * ln2 - M);
+            l = s;
         }
-        if (lane == 0) lse[b] = l, top[b] = big;
+        if (lane == 0) M.lse[b] = l, M.top[b] = big;
     }
-    const int lists = beams * S;
-    for (int i = tid; i < lists; i += kMergeThreads) {
-        const int row = g * beams + i / S;
-        // a list that has nothing starts behind its end
-        heads[i] = beam_live(scores, finished, row) ? 0 : (finished && finished[row] && i % S == 0) ? kOnly : n;
+    if (tid == 0) M.count = 0;
+    __syncthreads();
+    if (tid < beams) {  // (one warp or two: an fp64 logarithm is a hundred instructions of 16 cycles)
+        const float big = M.top[tid];
+        M.lse[tid] = log(M.lse[tid]) + (sel_wide(big) ? 0.0 : (double)sel_exp(big) * 0.69314718055994530942 - (double)big);
     }
     __syncthreads();
-    // the head of list i
-    auto head = [&](int i, double &c, int64_t &at) {
-        const int b = i / S, row = g * beams + b, h = heads[i];
-        c = dninf, at = INT64_MAX;
-        if (h == kOnly) {
+    const int lists = beams * S;
+    // entry h of list i, its place beam << 32 | word; false where there is none (NaN: nothing of this beam)
+    auto entry = [&](int i, int h, double &c, int64_t &at) -> bool {
+        const int b = i / S, row = g * beams + b;
+        c = dninf;
+        if (finished && finished[row]) {
+            if (h > 0 || i % S) return false;
             c = (double)scores[row];
-            at = (int64_t)b * V + eos;
-        } else if (h < n && h < __ldcg(&part[(int64_t)row * S + i % S].count)) {
+            at = (int64_t)b << 32 | (uint32_t)eos;
+        } else {
+            if (!(scores[row] > ninf) || h >= n || h >= __ldcg(&part[(int64_t)row * S + i % S].count)) return false;
             const uint64_t k = __ldcg(&cand[((int64_t)row * S + i % S) * n + h]);
-            c = (double)scores[row] + (((double)unord32((uint32_t)(k >> 32)) - (double)top[b]) - lse[b]);
-            at = (int64_t)b * V + (uint32_t)~(uint32_t)k;
+            c = (double)scores[row] + (((double)unord32((uint32_t)(k >> 32)) - (double)M.top[b]) - M.lse[b]);
+            at = (int64_t)b << 32 | (uint32_t)~(uint32_t)k;
         }
-        if (!(c > dninf)) c = dninf, at = INT64_MAX;  // NaN: nothing of this beam
+        return c > dninf;
     };
-    double mc = dninf;
-    int64_t mat = INT64_MAX;
-    int mlist = -1;
-    auto rescan = [&]() {
-        mc = dninf, mat = INT64_MAX, mlist = -1;
-        for (int i = tid; i < lists; i += kMergeThreads) {
-            double c;
-            int64_t at;
-            head(i, c, at);
-            if (better(c, at, mc, mat)) mc = c, mat = at, mlist = i;
-        }
-    };
-    rescan();
-    for (int r = 0; r < n; r++) {
-        double c = mc;
-        int64_t at = mat;
-        int li = mlist;
+    // The lists are dealt out to the warps evenly.  With the q-th entries of
+    // ceil(n / (warps q)) lists in every warp no smaller than a threshold, n
+    // candidates are not.
+    const int W = min(kMergeWarps, lists), q = (n + lists - 1) / lists, k = (n + W * q - 1) / (W * q);
+    uint64_t mine = 0, head[kMergeLists / kMergeThreads];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            const double oc = __shfl_xor_sync(0xffffffffu, c, off);
-            const int64_t oat = __shfl_xor_sync(0xffffffffu, at, off);
-            const int ol = __shfl_xor_sync(0xffffffffu, li, off);
-            if (better(oc, oat, c, at)) c = oc, at = oat, li = ol;
+    for (int u = 0; u < kMergeLists / kMergeThreads; u++) {
+        const int i = u * kMergeThreads + lane * kMergeWarps + warp;
+        double c;
+        int64_t at;
+        head[u] = i < lists && entry(i, q - 1, c, at) ? ord64(c) : 0;
+        mine = max(mine, head[u]);
+    }
+    uint64_t kth = 0;
+    for (int r = 0; r < k; r++) {
+        kth = warp_max64(mine);
+        const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
+        if (lane == __ffs(who) - 1) mine = 0;
+    }
+    if (lane == 0) M.kth[warp] = kth;
+    __syncthreads();
+    uint64_t thr = M.kth[0];
+    for (int w = 1; w < W; w++) thr = min(thr, M.kth[w]);
+    // sharper: the ceil(n / q)-th of the heads that pass (beams differ: a warp may hold poor ones only)
+#pragma unroll
+    for (int u = 0; u < kMergeLists / kMergeThreads; u++)
+        if (head[u] && head[u] >= thr) M.key[atomicAdd(&M.count, 1)] = head[u];
+    if (tid == 0) M.sharp = 0;
+    __syncthreads();
+    const int heads = M.count, want = (n + q - 1) / q;
+    for (int i = tid; i < heads; i += kMergeThreads) {
+        const uint64_t key = M.key[i];
+        int above = 0, same = 0;
+#pragma unroll 8
+        for (int j = 0; j < heads; j++) above += M.key[j] > key, same += M.key[j] == key;
+        if (above < want && above + same >= want) M.sharp = key;  // (all that write it write the same)
+    }
+    __syncthreads();
+    thr = max(thr, M.sharp);
+    // the lists whose head passes, then all of their entries at once
+    if (tid == 0) M.count = M.passing = 0;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMergeLists / kMergeThreads; u++) {
+        const int i = u * kMergeThreads + lane * kMergeWarps + warp;
+        if (i < lists && (q > 1 || (head[u] && head[u] >= thr))) M.list[atomicAdd(&M.passing, 1)] = (uint16_t)i;
+    }
+    __syncthreads();
+    const int pairs = M.passing * n;
+    for (int i = tid; i < pairs; i += kMergeThreads) {
+        double c;
+        int64_t at;
+        const int l = i / n;
+        if (entry(M.list[l], i - l * n, c, at) && ord64(c) >= thr) {
+            const int p = atomicAdd(&M.count, 1);
+            if (p < kMergeBuf) M.key[p] = ord64(c), M.at[p] = at;
         }
-        if (lane == 0) wc[warp] = c, wat[warp] = at, wlist[warp] = li;
+    }
+    __syncthreads();
+    const int total = M.count;
+    auto write = [&](int r, double c, int64_t at) {
+        const int64_t o = (int64_t)g * n + r;
+        out_scores[o] = (float)c;
+        parents[o] = (int)(at >> 32);
+        tokens[o] = (int)(uint32_t)at;
+    };
+    int found = min(total, n);
+    if (total <= kMergeBuf) {
+        for (int i = tid; i < total; i += kMergeThreads) {
+            const uint64_t key = M.key[i];
+            const int64_t at = M.at[i];
+            const int r = place_of<int64_t>(key, at, M.key, M.at, total);
+            if (r < n) write(r, unord64(key), at);
+        }
+    } else {
+        // too many equal candidates: n rounds of taking the best head of the lists
+        for (int i = tid; i < lists; i += kMergeThreads) M.next[i] = 0;
         __syncthreads();
-        if (warp == 0) {
-            c = lane < kMergeThreads / 32 ? wc[lane] : dninf;
-            at = lane < kMergeThreads / 32 ? wat[lane] : INT64_MAX;
-            li = lane < kMergeThreads / 32 ? wlist[lane] : -1;
+        for (int r = 0; r < n; r++) {
+            double c = dninf;
+            int64_t at = INT64_MAX;
+            int li = -1;
+            for (int i = tid; i < lists; i += kMergeThreads) {
+                double ec;
+                int64_t eat;
+                if (entry(i, M.next[i], ec, eat) && better(ec, eat, c, at)) c = ec, at = eat, li = i;
+            }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) {
                 const double oc = __shfl_xor_sync(0xffffffffu, c, off);
@@ -351,18 +537,21 @@ __global__ void __launch_bounds__(kMergeThreads)
                 const int ol = __shfl_xor_sync(0xffffffffu, li, off);
                 if (better(oc, oat, c, at)) c = oc, at = oat, li = ol;
             }
-            if (lane == 0) {
-                const bool none = at == INT64_MAX;
-                const int64_t o = (int64_t)g * n + r;
-                out_scores[o] = none ? ninf : (float)c;
-                parents[o] = none ? -1 : (int)(at / V);
-                tokens[o] = none ? -1 : (int)(at % V);
-                won = none ? -1 : li;
-                if (!none) heads[li] = heads[li] == kOnly ? n : heads[li] + 1;
+            if (lane == 0) M.wc[warp] = c, M.wat[warp] = at, M.wlist[warp] = li;
+            __syncthreads();
+            if (tid == 0) {
+                for (int w = 1; w < kMergeWarps; w++)
+                    if (better(M.wc[w], M.wat[w], c, at)) c = M.wc[w], at = M.wat[w], li = M.wlist[w];
+                write(r, c, at);  // (there are more than n)
+                M.next[li]++;
             }
+            __syncthreads();
         }
-        __syncthreads();
-        if (won == mlist && won >= 0) rescan();
+    }
+    for (int r = found + tid; r < n; r += kMergeThreads) {
+        const int64_t o = (int64_t)g * n + r;
+        out_scores[o] = ninf;
+        parents[o] = tokens[o] = -1;
     }
 }
 
@@ -504,17 +693,19 @@ __global__ void __launch_bounds__(32) beam_reorder_kernel(RoArgs A) {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// Values per thread of a slice: the largest slice that still gives two CTAs
-// per SM, so that a few rows are read by all SMs.
-int sel_vpt(int rows, int V) {
-    for (int vpt : {32, 16, 8})
-        if ((int64_t)rows * ((V + kSelThreads * vpt - 1) / (kSelThreads * vpt)) >= 2 * 152) return vpt;
-    return 4;
+// Slices of a row: one wave of CTAs over all rows, but a thousand values each.
+constexpr int kSelCtas = kSelPerSm * 152;
+int sel_len(int rows, int V) {
+    int S = kSelCtas / rows;
+    if (S > (V + 1023) / 1024) S = (V + 1023) / 1024;
+    if (S < 1) S = 1;
+    return ((V + S - 1) / S + 3) / 4 * 4;
 }
 int sel_slices(int rows, int V) {
-    const int per = kSelThreads * sel_vpt(rows, V);
-    return (V + per - 1) / per;
+    const int len = sel_len(rows, V);
+    return (V + len - 1) / len;
 }
+static_assert(kSelCtas + kMaxBeams <= kMergeLists, "a group's lists");
 
 template <int VPT>
 const void *slice_kernel(bool vec) {
@@ -563,22 +754,17 @@ qlin_status qlin_beam_select(const float *logits, int64_t row_stride, const floa
     QLIN_REQUIRE(workspace_bytes >= w.bytes, QLIN_ERR_INVALID_ARG, "qlin_beam_select: workspace %zu < %zu bytes",
                  workspace_bytes, w.bytes);
     const bool vec = aligned16(logits) && row_stride % 4 == 0;
-    const void *k = nullptr;
-    switch (sel_vpt(rows, vocab)) {
-        case 32: k = slice_kernel<32>(vec); break;
-        case 16: k = slice_kernel<16>(vec); break;
-        case 8: k = slice_kernel<8>(vec); break;
-        default: k = slice_kernel<4>(vec); break;
-    }
+    const int len = sel_len(rows, vocab);
+    const void *k = len <= 1024 ? slice_kernel<4>(vec) : len <= 2048 ? slice_kernel<8>(vec) : slice_kernel<16>(vec);
     void *a0[] = {(void *)&logits, (void *)&row_stride, (void *)&scores, (void *)&finished, (void *)&vocab,
-                  (void *)&n_out, (void *)&w.part, (void *)&w.cand};
+                  (void *)&len, (void *)&n_out, (void *)&w.part, (void *)&w.cand};
     if (qlin_status st = launch_pdl(k, dim3(S, rows), dim3(kSelThreads), 0, (cudaStream_t)stream, a0,
                                     "beam_slice_kernel"))
         return st;
     void *a1[] = {(void *)&w.part, (void *)&w.cand, (void *)&scores, (void *)&finished, (void *)&eos, (void *)&beams,
                   (void *)&vocab, (void *)&S, (void *)&n_out, (void *)&out_scores, (void *)&parents, (void *)&tokens};
-    const size_t smem = (size_t)beams * S;
-    if (smem > 40 * 1024) blocks_per_sm((const void *)beam_merge_kernel, smem);  // raises the limit once
+    const size_t smem = sizeof(MergeSmem);
+    blocks_per_sm((const void *)beam_merge_kernel, smem);  // raises the dynamic shared-memory limit once
     return launch_pdl((const void *)beam_merge_kernel, dim3(n_groups), dim3(kMergeThreads), smem, (cudaStream_t)stream,
                       a1, "beam_merge_kernel");
 }
