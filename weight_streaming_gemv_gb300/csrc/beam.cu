@@ -105,9 +105,10 @@ struct SelBuf {
 };
 
 // The place of key `mine` (and `tie`, smaller first) among c keys: the number
-// of larger ones.  The high words tell nearly all of them apart.
+// of larger ones (self: it is among them).  The high words tell nearly all of
+// them apart.
 template <typename Tie>
-__device__ __forceinline__ int place_of(uint64_t mine, Tie tie, const uint64_t *key, const Tie *ties, int c) {
+__device__ __forceinline__ int place_of(uint64_t mine, Tie tie, bool self, const uint64_t *key, const Tie *ties, int c) {
     const uint32_t hi = (uint32_t)(mine >> 32);
     const uint32_t *his = reinterpret_cast<const uint32_t *>(key) + 1;
     int r = 0, eq = 0;
@@ -117,10 +118,10 @@ __device__ __forceinline__ int place_of(uint64_t mine, Tie tie, const uint64_t *
         r += h > hi;
         eq += h == hi;
     }
-    if (eq > 1)
+    if (eq > (int)self)
         for (int q = 0; q < c; q++) {
             const uint64_t k = key[q];
-            if ((uint32_t)(k >> 32) == hi && (k > mine || (k == mine && ties[q] < tie))) r++;
+            if ((uint32_t)(k >> 32) == hi && (k > mine || (k == mine && ties[q] < tie))) r++;  // (not itself)
         }
     return r;
 }
@@ -130,7 +131,7 @@ __device__ __forceinline__ int place_of(uint64_t mine, Tie tie, const uint64_t *
 __device__ __forceinline__ void sel_rank(const SelBuf &b, int c, int n, uint64_t *out) {
     for (int i = threadIdx.x; i < c; i += kSelThreads) {
         const uint64_t key = b.key[i];
-        const int r = place_of<uint64_t>(key, 0, b.key, b.key, c);
+        const int r = place_of<uint64_t>(key, 0, true, b.key, b.key, c);
         if (r < n) out[r] = key;
     }
 }
@@ -213,29 +214,36 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
                 // infinity makes it infinite, nothing else does)
                 sum += ex2_approx(__fmaf_rn(v[j], kLog2eLo, __fmaf_rn(v[j], kLog2eHi, -ef)));
             }
-            // a threshold for the first two tiles and every fourth: it has settled by then
-            if (careful || tile < 2 || tile % 4 == 0) {
-                // the k-th largest of the warp's thread maxima
-                uint32_t mine = ord32(tmax), kth = 0;
-                for (int r = 0; r < k; r++) {
-                    kth = __reduce_max_sync(0xffffffffu, mine);
-                    const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
-                    if (lane == __ffs(who) - 1) mine = 0;
+            // the threshold: from the first two tiles' thread maxima, then the n-th of what they left in the buffer, and
+            // again every eighth tile
+            const bool maxima = careful || tile < 2, rank = tile == 2 || tile % 8 == 7;
+            if (maxima || rank) {
+                if (maxima) {
+                    // the k-th largest of the warp's thread maxima
+                    uint32_t mine = ord32(tmax), kth = 0;
+                    for (int r = 0; r < k; r++) {
+                        kth = __reduce_max_sync(0xffffffffu, mine);
+                        const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
+                        if (lane == __ffs(who) - 1) mine = 0;
+                    }
+                    if (lane == 0) wkth[warp] = kth;
                 }
-                if (lane == 0) wkth[warp] = kth;
                 __syncthreads();
-                uint32_t tk = wkth[0];
+                if (maxima) {
+                    uint32_t tk = wkth[0];
 #pragma unroll
-                for (int w = 1; w < kSelWarps; w++) tk = min(tk, wkth[w]);
-                thr = max(thr, tk);
+                    for (int w = 1; w < kSelWarps; w++) tk = min(tk, wkth[w]);
+                    thr = max(thr, tk);
+                }
                 c = buf.count;
                 __syncthreads();
                 over = c > kSelBuf;
-                if (!over && c > kSelBuf / 2) {  // keep the n best
+                if (!over && (c > kSelBuf / 2 || (rank && c >= n))) {  // keep the n best
                     sel_rank(buf, c, n, best);
                     __syncthreads();
                     c = min(c, n);
                     for (int i = tid; i < c; i += kSelThreads) buf.key[i] = best[i];
+                    if (c == n) thr = max(thr, (uint32_t)(best[n - 1] >> 32));
                     if (tid == 0) buf.count = c;
                     __syncthreads();
                 }
@@ -365,6 +373,8 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 struct MergeSmem {
     double lse[kMaxBeams];  // the log of a beam's sum, less top
     float top[kMaxBeams];   // its largest logit
+    float base[kMaxBeams];  // its score
+    int kind[kMaxBeams];    // 0: dead, 1: live, 2: finished
     uint64_t key[kMergeBuf];
     int64_t at[kMergeBuf];
     uint64_t kth[kMergeWarps], sharp;
@@ -417,7 +427,11 @@ __global__ void __launch_bounds__(kMergeThreads)
             for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
             l = s;
         }
-        if (lane == 0) M.lse[b] = l, M.top[b] = big;
+        if (lane == 0) {
+            M.lse[b] = l, M.top[b] = big;
+            M.base[b] = scores[row];
+            M.kind[b] = finished && finished[row] ? 2 : scores[row] > ninf ? 1 : 0;
+        }
     }
     if (tid == 0) M.count = 0;
     __syncthreads();
@@ -429,17 +443,18 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int lists = beams * S;
     // entry h of list i, its place beam << 32 | word; false where there is none (NaN: nothing of this beam)
     auto entry = [&](int i, int h, double &c, int64_t &at) -> bool {
-        const int b = i / S, row = g * beams + b;
+        const int b = i / S, kind = M.kind[b];
         c = dninf;
-        if (finished && finished[row]) {
-            if (h > 0 || i % S) return false;
-            c = (double)scores[row];
-            at = (int64_t)b << 32 | (uint32_t)eos;
-        } else {
-            if (!(scores[row] > ninf) || h >= n || h >= __ldcg(&part[(int64_t)row * S + i % S].count)) return false;
-            const uint64_t k = __ldcg(&cand[((int64_t)row * S + i % S) * n + h]);
-            c = (double)scores[row] + (((double)unord32((uint32_t)(k >> 32)) - (double)M.top[b]) - M.lse[b]);
+        if (kind == 1 && h < n) {
+            const int64_t l = (int64_t)(g * beams + b) * S + (i - b * S);
+            const int count = __ldcg(&part[l].count);
+            const uint64_t k = __ldcg(&cand[l * n + h]);
+            if (h >= count) return false;
+            c = (double)M.base[b] + (((double)unord32((uint32_t)(k >> 32)) - (double)M.top[b]) - M.lse[b]);
             at = (int64_t)b << 32 | (uint32_t)~(uint32_t)k;
+        } else if (kind == 2 && h == 0 && i == b * S) {
+            c = (double)M.base[b];
+            at = (int64_t)b << 32 | (uint32_t)eos;
         }
         return c > dninf;
     };
@@ -511,11 +526,20 @@ __global__ void __launch_bounds__(kMergeThreads)
     };
     int found = min(total, n);
     if (total <= kMergeBuf) {
-        for (int i = tid; i < total; i += kMergeThreads) {
-            const uint64_t key = M.key[i];
-            const int64_t at = M.at[i];
-            const int r = place_of<int64_t>(key, at, M.key, M.at, total);
-            if (r < n) write(r, unord64(key), at);
+        // four threads count for a candidate
+        for (int i0 = 0; i0 < total; i0 += kMergeThreads / 4) {
+            const int i = i0 + (tid >> 2), part4 = tid & 3, per = (total + 3) / 4;
+            const int j0 = min(part4 * per, total), j1 = min(j0 + per, total);
+            uint64_t key = 0;
+            int64_t at = 0;
+            int r = 0;
+            if (i < total) {
+                key = M.key[i], at = M.at[i];
+                r = place_of<int64_t>(key, at, i >= j0 && i < j1, M.key + j0, M.at + j0, j1 - j0);
+            }
+            r += __shfl_xor_sync(0xffffffffu, r, 1);
+            r += __shfl_xor_sync(0xffffffffu, r, 2);
+            if (i < total && part4 == 0 && r < n) write(r, unord64(key), at);
         }
     } else {
         // too many equal candidates: n rounds of taking the best head of the lists
@@ -755,7 +779,7 @@ qlin_status qlin_beam_select(const float *logits, int64_t row_stride, const floa
                  workspace_bytes, w.bytes);
     const bool vec = aligned16(logits) && row_stride % 4 == 0;
     const int len = sel_len(rows, vocab);
-    const void *k = len <= 1024 ? slice_kernel<4>(vec) : len <= 2048 ? slice_kernel<8>(vec) : slice_kernel<16>(vec);
+    const void *k = len <= 1024 ? slice_kernel<4>(vec) : len <= 4096 ? slice_kernel<8>(vec) : slice_kernel<16>(vec);
     void *a0[] = {(void *)&logits, (void *)&row_stride, (void *)&scores, (void *)&finished, (void *)&vocab,
                   (void *)&len, (void *)&n_out, (void *)&w.part, (void *)&w.cand};
     if (qlin_status st = launch_pdl(k, dim3(S, rows), dim3(kSelThreads), 0, (cudaStream_t)stream, a0,
