@@ -548,12 +548,11 @@ typedef struct {
  * whose sequence or position is out of range gets zeros too and sets bit 0 of
  * *status_word (device int32, may be NULL; bit 1: a bounded device wait gave
  * up; nothing clears it).  Rows that a lane does not see never reach its
- * outputs, whatever they hold; NaN or an infinity in a q, k or v that it sees
- * makes its outputs NaN (of the heads concerned).
+ * outputs, whatever they hold; a NaN or an infinity in its q or in a k or v
+ * that it sees can make all its outputs NaN (of the heads concerned).
  * fp32 accuracy with either cache type: the products run on the tensor cores
  * on bf16 terms that carry all 24 significant bits, with fp32 accumulation,
- * and the softmax is in fp32; |x| above the largest bf16 (about 3.39e38)
- * counts as an infinity.
+ * and the softmax is in fp32.
  * workspace: device, 16-byte aligned, qlin_attention_lanes_workspace_size
  * bytes (0 for sizes out of range), owned by the caller, any content; calls
  * sharing it must not overlap on the GPU.  The call issues a fixed sequence of
@@ -577,6 +576,31 @@ qlin_status qlin_attention_prefix(const float *q, const qlin_kv *prefix, const i
                                   const int32_t *seqs, int n_lanes, int n_heads, int n_kv, int head_dim, int window,
                                   int sinks, float *out, int32_t *status_word, void *workspace,
                                   size_t workspace_bytes, qlin_stream_t stream);
+
+/* decode_lanes_t158 for lanes that share prompts kept once: the beams of a
+ * search, or many answers to one prompt.  prompts->kv holds the prompts' keys
+ * and values in the layout of decode_lanes_t158's caches, device fp32
+ * [n_prompts][n_layers][2][rows][kv_dim] (with rows = max_pos it is such a
+ * cache: prompts are read in by decode_lanes_t158 itself), len[f] (device
+ * int32 [n_prompts]) their lengths.  Lane i continues prompt prefix_of[i]
+ * (NULL: prompt 0) at positions[i] >= len[prefix_of[i]]; its k and v go to row
+ * positions[i] - len of sequence seqs[i] of kv_caches, device fp32
+ * [n_seqs][n_layers][2][own_rows][kv_dim].  The attention is
+ * qlin_attention_prefix's (a prompt is read once for all its lanes), so a
+ * lane's results are those of decode_lanes_t158 to fp32 accuracy in the
+ * attention, not bit for bit.  Everything else, decode_lanes_t158_status
+ * included, as decode_lanes_t158; the workspace has
+ * decode_lanes_t158_prefix_workspace_size bytes. */
+typedef struct {
+    const float *kv;
+    const int32_t *len;
+    int32_t n_prompts, rows;
+} t158_prompts;
+qlin_status decode_lanes_t158_prefix_workspace_size(const t158_model *m, int max_lanes, size_t *bytes);
+qlin_status decode_lanes_t158_prefix(const t158_model *m, const t158_prompts *prompts, const int32_t *prefix_of,
+                                     float *kv_caches, int own_rows, int n_seqs, int n_lanes, const int32_t *tokens,
+                                     const int32_t *positions, const int32_t *seqs, float *logits, int32_t *next,
+                                     void *workspace, size_t workspace_bytes, int max_lanes, qlin_stream_t stream);
 
 /* Beam search's selection.  Group g has `beams` beams with running scores
  * scores[g][b] and logits row g * beams + b (device fp32, rows row_stride

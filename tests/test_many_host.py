@@ -128,3 +128,32 @@ def test_kv_cache_describes_tensors():
         qlin.kv_cache(x[0, 0, 0], x[0, 0, 1])
     with pytest.raises(ValueError):
         qlin.kv_cache(x[:, 0, 0].half(), x[:, 0, 1].half())
+
+
+def test_prefix_step_refuses():
+    import ctypes as ct
+
+    L, m, n = qlin.lib(), qlin.T158ModelC(), ct.c_size_t()
+    assert L.decode_lanes_t158_prefix_workspace_size(ct.byref(m), 4, ct.byref(n)) == 1  # an empty model
+    m.n_layers, m.dim, m.n_heads, m.n_kv_heads, m.head_dim = 1, 64, 2, 1, 32
+    m.ffn, m.vocab, m.max_pos = 96, 100, 64
+    for j in range(qlin.T158_NMAT):
+        m.w[j], m.pitch[j] = 4096, 32
+    for f in ("scales", "g_attn", "g_ffn", "g_final", "emb", "rope_cos", "rope_sin"):
+        setattr(m, f, 4096)
+    assert L.decode_lanes_t158_prefix_workspace_size(ct.byref(m), 4, ct.byref(n)) == 0 and n.value > 0
+    assert L.decode_lanes_t158_prefix_workspace_size(ct.byref(m), 0, ct.byref(n)) == 1
+    p = qlin.T158PromptsC()
+
+    def call(**kw):
+        for k, v in dict(kv=4096, len=4096, n_prompts=1, rows=64).items():
+            setattr(p, k, kw.pop(k, v))
+        a = dict(of=None, kvs=4096, own=8, n_seqs=2, n_lanes=2, tok=16, pos=16, seq=16, lg=None, nx=16, ws=4096,
+                 wsb=n.value, mx=4)
+        a.update(kw)
+        return L.decode_lanes_t158_prefix(ct.byref(m), ct.byref(p), *a.values(), None)
+
+    assert call(kv=None) == 1 and call(len=None) == 1 and call(n_prompts=0) == 1 and call(rows=0) == 1
+    assert call(own=0) == 1 and call(kv=8) == 1 and call(len=6) == 1 and call(of=2) == 1 and call(kvs=None) == 1
+    assert call(wsb=64) == 1 and call(n_lanes=5) == 1 and call(ws=8) == 1
+    assert "decode_lanes_t158" in L.qlin_last_error().decode()

@@ -64,15 +64,27 @@ __global__ void lanes_embed_kernel(const uint16_t *__restrict__ emb, int vocab, 
     if (!ok && threadIdx.x == 0) atomicOr(status, kLaneStatusBad);
 }
 
-// per lane: rotate q and k at the lane's position, write k and v to its cache row
+// per lane: rotate q and k at the lane's position, write k and v to its cache
+// row: its position, less its prompt's length where prompts are kept apart
+// (pre_len; lane i behind prompt pre_of[i], or 0)
 __global__ void lanes_rope_kv_kernel(float *q, const float *k, const float *v, float *kv, const int32_t *pos,
-                                     const int32_t *seq, int n_seqs, int layer, int L, int max_pos,
+                                     const int32_t *seq, int n_seqs, int layer, int L, int max_pos, int rows,
+                                     const int32_t *pre_len, const int32_t *pre_of, int n_pre, int pre_rows,
                                      const float *__restrict__ cos_t, const float *__restrict__ sin_t, int nh,
                                      int nkv, int hd, int32_t *status) {
     extern __shared__ float kr[];  // [nkv*hd]
     const int i = blockIdx.x;
     const int p = pos[i], s = seq[i];
-    if (!lane_ok(p, s, max_pos, n_seqs)) {
+    const int f = pre_len && pre_of ? pre_of[i] : 0;
+    bool ok = lane_ok(p, s, max_pos, n_seqs);
+    int row = p;
+    if (pre_len) {
+        ok = ok && f >= 0 && f < n_pre;
+        const int len = ok ? pre_len[f] : 0;
+        row = p - len;
+        ok = ok && len >= 0 && len <= pre_rows && row >= 0 && row < rows;  // (nothing is written into a prompt)
+    }
+    if (!ok) {
         if (threadIdx.x == 0) atomicOr(status, kLaneStatusBad);
         return;
     }
@@ -84,9 +96,9 @@ __global__ void lanes_rope_kv_kernel(float *q, const float *k, const float *v, f
     __syncthreads();
     rope_rotate(kr, nkv, hd, c, sn, whole_block());
     __syncthreads();
-    float *kc = kv + (((int64_t)s * L + layer) * 2 + 0) * max_pos * kvd;
-    float *vc = kc + (int64_t)max_pos * kvd;
-    const int64_t off = (int64_t)p * kvd;
+    float *kc = kv + (((int64_t)s * L + layer) * 2 + 0) * rows * kvd;
+    float *vc = kc + (int64_t)rows * kvd;
+    const int64_t off = (int64_t)row * kvd;
     for (int e = threadIdx.x; e < kvd; e += blockDim.x) {
         kc[off + e] = kr[e];
         vc[off + e] = v[(int64_t)i * kvd + e];
@@ -529,10 +541,11 @@ struct LanesWs {
     float *h, *xn, *xs, *q, *k, *v, *att, *y, *g, *u, *attn;
     int8_t *xq;
     void *lm, *tiles;  // tiles: fp16 activation tiles of the tensor-core linears
-    size_t lm_bytes, bytes;
+    void *pre;         // the attention's, where prompts are kept apart
+    size_t lm_bytes, pre_bytes, bytes;
 };
 
-LanesWs carve_lanes(const t158_model *m, int max_lanes, char *base) {
+LanesWs carve_lanes(const t158_model *m, int max_lanes, char *base, bool prompts) {
     LanesWs w{};
     size_t off = 0;
     auto take = [&](size_t b) {
@@ -555,10 +568,12 @@ LanesWs carve_lanes(const t158_model *m, int max_lanes, char *base) {
     w.y = (float *)take(4 * M * d);
     w.g = (float *)take(4 * M * f);
     w.u = (float *)take(4 * M * f);
-    w.attn = (float *)take(4 * M * m->n_heads * (size_t)attn_chunks(m->max_pos) * (2 + m->head_dim));
+    w.attn = (float *)take(prompts ? 0 : 4 * M * m->n_heads * (size_t)attn_chunks(m->max_pos) * (2 + m->head_dim));
     w.lm_bytes = qlin_lm_head_lanes_workspace_size(m->vocab, m->dim);
     w.lm = take(w.lm_bytes);
     w.tiles = take(max_lanes >= kLanesTensorMin ? t158_tc_workspace_bytes(max_lanes, (int)big) : 0);
+    w.pre_bytes = prompts ? qlin_attention_lanes_workspace_size(max_lanes, m->n_heads, m->n_kv_heads, m->head_dim) : 0;
+    w.pre = take(w.pre_bytes);
     w.bytes = off;
     return w;
 }
@@ -600,27 +615,13 @@ qlin_status check_lanes_model(const t158_model *m) {
     return QLIN_OK;
 }
 
-}  // namespace
-}  // namespace qlin
-
-using namespace qlin;
-
-extern "C" {
-
-qlin_status decode_lanes_t158_workspace_size(const t158_model *m, int max_lanes, size_t *bytes) {
-    qlin::clear_error();
-    qlin_status st = check_lanes_model(m);
-    if (st) return st;
-    QLIN_REQUIRE(bytes && max_lanes >= 1 && max_lanes <= 4096, QLIN_ERR_INVALID_ARG,
-                 "decode_lanes_t158_workspace_size: max_lanes %d outside 1..4096", max_lanes);
-    *bytes = carve_lanes(m, max_lanes, nullptr).bytes;
-    return QLIN_OK;
-}
-
-qlin_status decode_lanes_t158(const t158_model *m, float *kv_caches, int n_seqs, int n_lanes, const int32_t *tokens,
-                              const int32_t *positions, const int32_t *seqs, float *logits, int32_t *next,
-                              void *workspace, size_t workspace_bytes, int max_lanes, qlin_stream_t stream) {
-    qlin::clear_error();
+// One step over lanes.  prompts null: every sequence has its whole cache,
+// max_pos rows; else the prompts' rows are in prompts->kv and kv_caches holds
+// own_rows rows of what follows them.
+qlin_status lanes_step(const t158_model *m, const t158_prompts *prompts, const int32_t *prefix_of, float *kv_caches,
+                       int own_rows, int n_seqs, int n_lanes, const int32_t *tokens, const int32_t *positions,
+                       const int32_t *seqs, float *logits, int32_t *next, void *workspace, size_t workspace_bytes,
+                       int max_lanes, qlin_stream_t stream) {
     qlin_status st = check_lanes_model(m);
     if (st) return st;
     QLIN_REQUIRE(kv_caches && tokens && positions && seqs && next && workspace, QLIN_ERR_INVALID_ARG,
@@ -629,7 +630,7 @@ qlin_status decode_lanes_t158(const t158_model *m, float *kv_caches, int n_seqs,
                  "decode_lanes_t158: n_seqs %d, n_lanes %d, max_lanes %d", n_seqs, n_lanes, max_lanes);
     QLIN_REQUIRE(aligned16(workspace) && aligned16(kv_caches), QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158: workspace or kv_caches not 16-byte aligned");
-    const LanesWs w = carve_lanes(m, max_lanes, (char *)workspace);
+    const LanesWs w = carve_lanes(m, max_lanes, (char *)workspace, prompts != nullptr);
     QLIN_REQUIRE(workspace_bytes >= w.bytes, QLIN_ERR_INVALID_ARG, "decode_lanes_t158: workspace %zu < %zu bytes",
                  workspace_bytes, w.bytes);
     cudaStream_t s = (cudaStream_t)stream;
@@ -702,29 +703,45 @@ qlin_status decode_lanes_t158(const t158_model *m, float *kv_caches, int n_seqs,
             if ((st = lin_group(l, 0, 3, qkv))) return st;
         }
         lanes_rope_kv_kernel<<<M, 256, (size_t)kvd * sizeof(float), s>>>(
-            w.q, w.k, w.v, kv_caches, positions, seqs, n_seqs, l, L, m->max_pos, m->rope_cos, m->rope_sin, nh, nkv,
-            hd, w.status);
+            w.q, w.k, w.v, kv_caches, positions, seqs, n_seqs, l, L, m->max_pos, own_rows,
+            prompts ? prompts->len : nullptr, prefix_of, prompts ? prompts->n_prompts : 0, prompts ? prompts->rows : 0,
+            m->rope_cos, m->rope_sin, nh, nkv, hd, w.status);
         QLIN_LAUNCHED("lanes_rope_kv_kernel");
-        if (attn_k) {
-            void *args[] = {(void *)&w.q, (void *)&kv_caches, (void *)&positions, (void *)&seqs, (void *)&n_seqs,
-                            (void *)&l, (void *)&L, (void *)&m->max_pos, (void *)&m->n_heads, (void *)&m->n_kv_heads,
-                            (void *)&M, (void *)&w.attn, (void *)&ncmax, (void *)&w.status};
-            QLIN_CUDA(cudaLaunchKernel(attn_k, dim3(attn_grid), dim3(kAttnThreads), args, attn_k_smem, s));
-            QLIN_LAUNCHED("lanes_attn_kernel");
+        if (prompts) {
+            auto layer = [&](const float *kv, int rows, int n) {
+                qlin_kv c{};
+                c.k = kv + (int64_t)2 * l * rows * kvd;
+                c.v = kv + (int64_t)(2 * l + 1) * rows * kvd;
+                c.seq_stride = (int64_t)2 * L * rows * kvd, c.row_stride = kvd;
+                c.n_seqs = n, c.rows = rows, c.type = QLIN_KV_F32;
+                return c;
+            };
+            const qlin_kv pre = layer(prompts->kv, prompts->rows, prompts->n_prompts), own = layer(kv_caches, own_rows, n_seqs);
+            if ((st = qlin_attention_prefix(w.q, &pre, prompts->len, prefix_of, &own, positions, seqs, M, nh, nkv, hd, 0, 0,
+                                            w.att, w.status, w.pre, w.pre_bytes, stream)))
+                return st;
         } else {
-            lanes_attn_chunk_kernel<<<dim3(ncmax, nkv, M), attn_threads, attn_smem, s>>>(w.q, kv_caches, positions, seqs, n_seqs,
-                                                                                 l, L, m->max_pos, nh, nkv, hd, w.attn,
-                                                                                 ncmax);
-            QLIN_LAUNCHED("lanes_attn_chunk_kernel");
-        }
-        if (merge_smem) {
-            lanes_attn_merge_smem_kernel<<<dim3(nh, M), 256, merge_smem, s>>>(w.attn, ncmax, positions, seqs, n_seqs,
-                                                                            m->max_pos, nh, hd, w.att);
-            QLIN_LAUNCHED("lanes_attn_merge_smem_kernel");
-        } else {
-            lanes_attn_merge_kernel<<<dim3(nh, M), 256, (size_t)next_pow2(ncmax) * sizeof(float), s>>>(
-                w.attn, ncmax, positions, seqs, n_seqs, m->max_pos, nh, hd, w.att);
-            QLIN_LAUNCHED("lanes_attn_merge_kernel");
+            if (attn_k) {
+                void *args[] = {(void *)&w.q, (void *)&kv_caches, (void *)&positions, (void *)&seqs, (void *)&n_seqs,
+                                (void *)&l, (void *)&L, (void *)&m->max_pos, (void *)&m->n_heads, (void *)&m->n_kv_heads,
+                                (void *)&M, (void *)&w.attn, (void *)&ncmax, (void *)&w.status};
+                QLIN_CUDA(cudaLaunchKernel(attn_k, dim3(attn_grid), dim3(kAttnThreads), args, attn_k_smem, s));
+                QLIN_LAUNCHED("lanes_attn_kernel");
+            } else {
+                lanes_attn_chunk_kernel<<<dim3(ncmax, nkv, M), attn_threads, attn_smem, s>>>(w.q, kv_caches, positions, seqs, n_seqs,
+                                                                                     l, L, m->max_pos, nh, nkv, hd, w.attn,
+                                                                                     ncmax);
+                QLIN_LAUNCHED("lanes_attn_chunk_kernel");
+            }
+            if (merge_smem) {
+                lanes_attn_merge_smem_kernel<<<dim3(nh, M), 256, merge_smem, s>>>(w.attn, ncmax, positions, seqs, n_seqs,
+                                                                                m->max_pos, nh, hd, w.att);
+                QLIN_LAUNCHED("lanes_attn_merge_smem_kernel");
+            } else {
+                lanes_attn_merge_kernel<<<dim3(nh, M), 256, (size_t)next_pow2(ncmax) * sizeof(float), s>>>(
+                    w.attn, ncmax, positions, seqs, n_seqs, m->max_pos, nh, hd, w.att);
+                QLIN_LAUNCHED("lanes_attn_merge_kernel");
+            }
         }
         if ((st = quant_i8_tiles(w.att, codes, w.xs, M, qd, tiles, s)) || (st = lin_group(l, 3, 1, &w.y))) return st;
         if ((st = norm_quant_tiles(w.h, w.y, m->g_ffn + (int64_t)l * d, m->eps, codes, w.xs, M, d, tiles, s))) return st;
@@ -740,6 +757,57 @@ qlin_status decode_lanes_t158(const t158_model *m, float *kv_caches, int n_seqs,
     // the output layer for all lanes in one pass over the table (tensor cores)
     if ((st = qlin_lm_head_lanes(m->emb, w.xn, m->vocab, d, M, logits, next, w.lm, w.lm_bytes, stream))) return st;
     return QLIN_OK;
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" {
+
+qlin_status decode_lanes_t158_workspace_size(const t158_model *m, int max_lanes, size_t *bytes) {
+    qlin::clear_error();
+    qlin_status st = check_lanes_model(m);
+    if (st) return st;
+    QLIN_REQUIRE(bytes && max_lanes >= 1 && max_lanes <= 4096, QLIN_ERR_INVALID_ARG,
+                 "decode_lanes_t158_workspace_size: max_lanes %d outside 1..4096", max_lanes);
+    *bytes = carve_lanes(m, max_lanes, nullptr, false).bytes;
+    return QLIN_OK;
+}
+
+qlin_status decode_lanes_t158(const t158_model *m, float *kv_caches, int n_seqs, int n_lanes, const int32_t *tokens,
+                              const int32_t *positions, const int32_t *seqs, float *logits, int32_t *next,
+                              void *workspace, size_t workspace_bytes, int max_lanes, qlin_stream_t stream) {
+    qlin::clear_error();
+    if (qlin_status st = check_lanes_model(m)) return st;
+    return lanes_step(m, nullptr, nullptr, kv_caches, m->max_pos, n_seqs, n_lanes, tokens, positions, seqs, logits, next,
+                      workspace, workspace_bytes, max_lanes, stream);
+}
+
+qlin_status decode_lanes_t158_prefix_workspace_size(const t158_model *m, int max_lanes, size_t *bytes) {
+    qlin::clear_error();
+    if (qlin_status st = check_lanes_model(m)) return st;
+    QLIN_REQUIRE(bytes && max_lanes >= 1 && max_lanes <= 4096, QLIN_ERR_INVALID_ARG,
+                 "decode_lanes_t158_prefix_workspace_size: max_lanes %d outside 1..4096", max_lanes);
+    *bytes = carve_lanes(m, max_lanes, nullptr, true).bytes;
+    return QLIN_OK;
+}
+
+qlin_status decode_lanes_t158_prefix(const t158_model *m, const t158_prompts *prompts, const int32_t *prefix_of,
+                                     float *kv_caches, int own_rows, int n_seqs, int n_lanes, const int32_t *tokens,
+                                     const int32_t *positions, const int32_t *seqs, float *logits, int32_t *next,
+                                     void *workspace, size_t workspace_bytes, int max_lanes, qlin_stream_t stream) {
+    qlin::clear_error();
+    if (qlin_status st = check_lanes_model(m)) return st;
+    QLIN_REQUIRE(prompts && prompts->kv && prompts->len, QLIN_ERR_INVALID_ARG, "decode_lanes_t158_prefix: null pointer");
+    QLIN_REQUIRE(prompts->n_prompts >= 1 && prompts->rows >= 1 && own_rows >= 1, QLIN_ERR_INVALID_ARG,
+                 "decode_lanes_t158_prefix: %d prompts of %d rows, %d rows of a lane's own", (int)prompts->n_prompts,
+                 (int)prompts->rows, own_rows);
+    QLIN_REQUIRE(aligned16(prompts->kv) && aligned4(prompts->len) && aligned4(prefix_of), QLIN_ERR_INVALID_ARG,
+                 "decode_lanes_t158_prefix: misaligned prompts");
+    return lanes_step(m, prompts, prefix_of, kv_caches, own_rows, n_seqs, n_lanes, tokens, positions, seqs, logits, next,
+                      workspace, workspace_bytes, max_lanes, stream);
 }
 
 int decode_lanes_t158_launches(const t158_model *m, int n_lanes) {

@@ -134,3 +134,84 @@ class T158Decoder:
 
     def check_lanes_status(self, stream=None):
         qlin.decode_lanes_t158_status(self.lanes_workspace, stream)
+
+    # ---------------------------------------------------------------- beam search
+    def prepare_beams(self, beams: int, own_rows: int, eos: int | None = None):
+        """A search over ``beams`` beams for each of the ``n_seqs`` prompts of ``prepare_lanes``, whose caches hold the
+        prompts (read in by ``step_lanes``, the last token included); every beam's cache holds the ``own_rows`` rows
+        that follow, so a search goes up to own_rows + 1 tokens.  eos: the token that ends a beam (None: none does).
+        The calls of a search run on torch's current stream."""
+        cfg, dev = self.cfg, self.emb.device
+        G, B = self.n_seqs, beams
+        i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
+        self.beams, self.own_rows, self.eos = B, own_rows, eos
+        self.kv_beams = torch.zeros((G * B, cfg.n_layers, 2, own_rows, cfg.kv_dim), dtype=torch.float32, device=dev)
+        self.prompt_len, self.beam_rows = i32(G), i32(G)
+        self.beam_prompt = torch.arange(G, dtype=torch.int32, device=dev).repeat_interleave(B)
+        self.beam_seq = torch.arange(G * B, dtype=torch.int32, device=dev)
+        self.beam_pos, self.beam_next = i32(G * B), i32(G * B)
+        self.beam_tokens, self.beam_parents = i32(G, B), i32(G, B)
+        # a beam's tokens so far, rows of 16-byte multiples: they follow the selection as the caches do
+        self.beam_history = i32(G * B, 1, 1, (own_rows + 4) // 4 * 4)
+        self.beam_scores = torch.empty((2, G, B), dtype=torch.float32, device=dev)
+        self.beam_done = torch.zeros((G, B), dtype=torch.uint8, device=dev)
+        self.beam_logits = torch.empty((G * B, cfg.vocab), dtype=torch.float32, device=dev)
+        self.select_ws_bytes = qlin.qlin_beam_select_workspace_size(G, B, cfg.vocab, B)
+        self.select_ws = torch.empty(self.select_ws_bytes, dtype=torch.uint8, device=dev)
+        self.beams_ws_bytes = qlin.decode_lanes_t158_prefix_workspace_size(self.model, G * B)
+        self.beams_ws = torch.zeros(self.beams_ws_bytes, dtype=torch.uint8, device=dev)
+        p = qlin.T158PromptsC()
+        p.kv, p.len = self.kv_lanes.data_ptr(), self.prompt_len.data_ptr()
+        p.n_prompts, p.rows = G, cfg.max_pos
+        self.prompts = p
+
+    def start_beams(self, prompt_len, logits):
+        """The beams' first tokens: ``logits`` [n_seqs][vocab] are those of each prompt's last token, ``prompt_len``
+        (int32 tensor or list) the prompts' lengths."""
+        G, B, V = self.n_seqs, self.beams, self.cfg.vocab
+        self.prompt_len.copy_(torch.as_tensor(prompt_len, dtype=torch.int32))
+        self.beam_rows.zero_()
+        self.beam_done.zero_()
+        self.beam_t = 0
+        self.beam_scores[0].fill_(float("-inf"))  # the beams are still one: only the first counts
+        self.beam_scores[0][:, 0] = 0.0
+        self.beam_logits.view(G, B, V)[:, 0].copy_(logits)
+        self._select()
+
+    def step_beams(self):
+        """One token further: a forward step of every beam, the selection, and the beams' caches after it."""
+        G, B = self.n_seqs, self.beams
+        if self.beam_t > self.own_rows:
+            raise ValueError(f"step_beams: the beams' caches hold {self.own_rows} rows")
+        torch.add(self.prompt_len[self.beam_prompt], self.beam_t - 1, out=self.beam_pos)
+        qlin.decode_lanes_t158_prefix(self.model, self.prompts, self.beam_prompt, self.kv_beams, self.own_rows, G * B,
+                                      G * B, self.beam_tokens, self.beam_pos, self.beam_seq, self.beam_logits,
+                                      self.beam_next, self.beams_ws, self.beams_ws_bytes, G * B)
+        self._select()
+
+    def _select(self):
+        G, B, V = self.n_seqs, self.beams, self.cfg.vocab
+        a, b = self.beam_t & 1, 1 - (self.beam_t & 1)
+        done, eos = (None, 0) if self.eos is None else (self.beam_done, self.eos)
+        qlin.qlin_beam_select(self.beam_logits, V, self.beam_scores[a], done, eos, G, B, V, B, self.beam_scores[b],
+                              self.beam_parents, self.beam_tokens, self.select_ws, self.select_ws_bytes)
+        self.beam_rows.fill_(self.beam_t)  # rows of the caches in use: the first tokens came from the prompt
+        x, h = self.kv_beams, self.beam_history
+        qlin.qlin_beam_reorder(x, x.stride(0) * 4, x.stride(2) * 4, 2 * self.cfg.n_layers, self.cfg.kv_dim * 4,
+                               self.own_rows, self.beam_parents, self.beam_rows, G, B)
+        qlin.qlin_beam_reorder(h, h.stride(0) * 4, h.stride(0) * 4, 1, h.stride(0) * 4, 1, self.beam_parents, None, G, B)
+        if self.eos is not None:
+            parents = self.beam_parents.long().clamp_min(0)
+            self.beam_done.copy_(torch.gather(self.beam_done, 1, parents) | (self.beam_tokens == self.eos))
+        # (a place that found no candidate goes on with word 0 and a score of minus infinity)
+        self.beam_tokens.clamp_(min=0)
+        h[:, 0, 0, self.beam_t] = self.beam_tokens.view(-1)
+        self.beam_t += 1
+
+    def beam_results(self):
+        """(tokens [n_seqs][beams][steps], scores [n_seqs][beams]), the best beam of a prompt first."""
+        return (self.beam_history[:, 0, 0, : self.beam_t].view(self.n_seqs, self.beams, -1),
+                self.beam_scores[self.beam_t & 1])
+
+    def check_beams_status(self, stream=None):
+        qlin.decode_lanes_t158_status(self.beams_ws, stream)

@@ -63,6 +63,14 @@ class QlinKvC(ctypes.Structure):
 
 KV_F32, KV_BF16 = 0, 1
 
+
+class T158PromptsC(ctypes.Structure):
+    """Mirror of ``t158_prompts``."""
+
+    _fields_ = [("kv", ctypes.c_void_p), ("len", ctypes.c_void_p), ("n_prompts", ctypes.c_int32),
+                ("rows", ctypes.c_int32)]
+
+
 _P, _I, _I64, _F, _D, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double,
                              ctypes.c_size_t)
 _ST = ctypes.c_int
@@ -126,6 +134,9 @@ SIGNATURES = {
     "qlin_attention_lanes": ([_P, ctypes.POINTER(QlinKvC), _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P], _ST),
     "qlin_attention_prefix": ([_P, ctypes.POINTER(QlinKvC), _P, _P, ctypes.POINTER(QlinKvC), _P, _P, _I, _I, _I, _I,
                                _I, _I, _P, _P, _P, _SZ, _P], _ST),
+    "decode_lanes_t158_prefix_workspace_size": ([ctypes.POINTER(T158ModelC), _I, ctypes.POINTER(_SZ)], _ST),
+    "decode_lanes_t158_prefix": ([ctypes.POINTER(T158ModelC), ctypes.POINTER(T158PromptsC), _P, _P, _I, _I, _I, _P, _P,
+                                  _P, _P, _P, _P, _SZ, _I, _P], _ST),
     "qlin_beam_select_workspace_size": ([_I, _I, _I, _I], _SZ),
     "qlin_beam_select": ([_P, _I64, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P], _ST),
     "qlin_beam_reorder": ([_P, _I64, _I64, _I, _I64, _I, _P, _P, _I, _I, _P, _P], _ST),
@@ -475,6 +486,22 @@ def qlin_attention_prefix(q, prefix: QlinKvC, prefix_len, prefix_of, kv: QlinKvC
         _ptr(q), ctypes.byref(prefix), _ptr(prefix_len), _ptr(prefix_of), ctypes.byref(kv), _ptr(positions),
         _ptr(seqs), n_lanes, n_heads, n_kv, head_dim, window, sinks, _ptr(out), _ptr(status_word), _ptr(workspace),
         workspace_bytes, _stream(stream)))
+
+
+def decode_lanes_t158_prefix_workspace_size(model: T158ModelC, max_lanes: int) -> int:
+    n = ctypes.c_size_t()
+    _check("decode_lanes_t158_prefix_workspace_size",
+           lib().decode_lanes_t158_prefix_workspace_size(ctypes.byref(model), max_lanes, ctypes.byref(n)))
+    return n.value
+
+
+def decode_lanes_t158_prefix(model: T158ModelC, prompts: T158PromptsC, prefix_of, kv_caches, own_rows, n_seqs, n_lanes,
+                             tokens, positions, seqs, logits, next_tokens, workspace, workspace_bytes, max_lanes,
+                             stream=None):
+    _check("decode_lanes_t158_prefix", lib().decode_lanes_t158_prefix(
+        ctypes.byref(model), ctypes.byref(prompts), _ptr(prefix_of), _ptr(kv_caches), own_rows, n_seqs, n_lanes,
+        _ptr(tokens), _ptr(positions), _ptr(seqs), _ptr(logits), _ptr(next_tokens), _ptr(workspace), workspace_bytes,
+        max_lanes, _stream(stream)))
 
 
 def qlin_beam_select_workspace_size(n_groups, beams, vocab, n_out) -> int:
