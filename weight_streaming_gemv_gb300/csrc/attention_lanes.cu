@@ -412,12 +412,14 @@ struct AlCfg {
     static constexpr int kWg = R / 16;              // warpgroups, 16 rows each
     static constexpr int kTerm = 16384;             // 128 keys x 64 dims, or 64 keys x 128 dims, in bf16
     static constexpr int kSlot = NT * kTerm;
-    static constexpr int kProd = NT == 1 ? 1 : 16;  // producer warps
+    static constexpr int kProd = NT == 1 ? 2 : 16;  // producer warps (arrivals of a slot)
     // after the warpgroups, and the producers of an fp32 cache: a warp that issues the MMAs, one that describes the
-    // pieces, one that copies the slices of a bf16 cache or describes those of an fp32 cache to the producers, one idle
-    // (registers are dealt out by warpgroup)
+    // pieces, two that copy the slices of a bf16 cache (half a slice each: one thread issues a copy in some 200 cycles,
+    // 500 with all that goes with a slice) or one that describes those of an fp32 cache to the producers (registers are
+    // dealt out by warpgroup)
     static constexpr int kProd0 = 4 * kWg;
     static constexpr int kMma = 4 * kWg + (NT == 1 ? 0 : kProd), kWalk = kMma + 1, kCopy = kMma + 2;
+    static constexpr int kCopies = NT == 1 ? 2 : 1;
     static constexpr int kThreads = 32 * (kMma + 4);
     static constexpr uint32_t kCols = 512;          // S^T [3 R], then O^T's two halves of dims [3 R] each
     static constexpr uint32_t kO = 3 * R;
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         }
         for (int s = 0; s < kPieceRing; s++) {
             mbar_init(&S.pc_full[s], 1);
-            mbar_init(&S.pc_empty[s], 4 * C::kWg + 2);  // the warpgroups' warps, MMA and copy warp
+            mbar_init(&S.pc_empty[s], 4 * C::kWg + 1 + C::kCopies);  // the warpgroups' warps, MMA and copy warps
         }
         mbar_init(&S.pv_done, 1);
         mbar_init(&S.fix_go, 1);
@@ -806,7 +808,8 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 if (end) break;
             }
         }
-        if (NT == 1 && warp == C::kCopy && al_elect()) {
+        if (NT == 1 && warp >= C::kCopy && al_elect()) {
+            const int half = warp - C::kCopy;
             // ------------------------------------------------------ copies the slices of a bf16 cache
             PieceRef ref;
             RingPos at;
@@ -818,17 +821,15 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 const CUtensorMap *mk = &maps.k[p->stream], *mv = &maps.v[p->stream];
                 const int z = (p->stream ? A.own : A.pre).seq_stride ? p->slot : 0, x0 = p->kvh * hd;
                 const int any_lo = p->any_lo, any_hi = p->any_hi, sk = p->sk;
-                // two boxes of 64 keys x 64 dims, those that nobody sees left out: K's are the two halves of the
-                // chunk, V's (of one half) the two halves of 128 dims
+                // a box of 64 keys x 64 dims, left out if nobody sees it: K's are the halves of the chunk, V's (of half
+                // a chunk) the halves of 128 dims
                 ok = for_slices(*p, nK, nDH, [&](bool v, int row, int dim) {
-                    const int s = at.s;
+                    const int s = at.s, y = row + (v ? 0 : 64 * half), x = dim + (v ? 64 * half : 0);
                     if (at.round && !al_wait(&S.empty[s], (at.round - 1) & 1u, &S.abort)) return false;
-                    const uint32_t to = smem_addr(ring + s * C::kSlot), full = smem_addr(&S.full[s]);
-                    auto any_in = [&](int a, int b) { return a <= any_hi && (b - 1 > any_lo || a < sk); };
-                    const bool on0 = any_in(row, row + 64), on1 = v ? on0 && dim + 64 < hd : any_in(row + 64, row + 128);
-                    mbar_arrive_expect_tx(&S.full[s], 8192u * ((uint32_t)on0 + (uint32_t)on1));
-                    if (on0) al_tma(to, v ? mv : mk, x0 + dim, row, z, full);
-                    if (on1) al_tma(to + 8192, v ? mv : mk, x0 + dim + (v ? 64 : 0), row + (v ? 0 : 64), z, full);
+                    const bool on = x < hd && y <= any_hi && (y + 63 > any_lo || y < sk);
+                    mbar_arrive_expect_tx(&S.full[s], on ? 8192u : 0u);
+                    if (on)
+                        al_tma(smem_addr(ring + s * C::kSlot) + 8192u * half, v ? mv : mk, x0 + x, y, z, smem_addr(&S.full[s]));
                     at.step(slots);
                     g++;
                     return true;
@@ -895,7 +896,9 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             int it = 0;           // chunks so far
             uint32_t fixes = 0;   // slices of V handed to the first warpgroup so far
             bool ok = true;
-            const uint32_t ring_a = smem_addr(ring), qs_a = smem_addr(qs), ps_a = smem_addr(ps);
+            const uint32_t qs_a = smem_addr(qs), ps_a = smem_addr(ps);
+            // (K slices have no leading byte offset to speak of, V's 64-dim blocks are 8 KB apart)
+            const uint32_t ring_d = al_desc_lo(smem_addr(ring), 16), vlbo = ((8192u - 16u) >> 4) << 16;
             const uint32_t hi128 = al_desc_hi(1024, 2), hip = al_desc_hi(512, 4);
             while (ok) {
                 const AlPiece *p = ref.next(S);
@@ -906,56 +909,70 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 // fp32 accumulator, bf16 operands, N = the terms' rows; S^T: both operands K-major, O^T: both with
                 // the keys as rows.  Term t of a cached value meets the 3 - t first terms of the rows, whose columns
                 // start at the products' order t.
-                const uint32_t ids = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 4) << 24;
-                const uint32_t idp = ids | (1u << 15) | (1u << 16);
+                uint32_t ids[NT], idp[NT];
+#pragma unroll
+                for (int t = 0; t < NT; t++) {
+                    ids[t] = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 4) << 24 | ((3 - t) * nr >> 3) << 17;
+                    idp[t] = ids[t] | (1u << 15) | (1u << 16);
+                }
                 if (!(ok = al_wait(&S.q_ready, (uint32_t)ref.k & 1u, &S.abort))) break;
+                const int c1 = p->c1, nsink = p->nsink, skip = p->cfirst - nsink;
+                int c = p->first;
+                bool edge[2] = {false, false};  // of the chunk whose products are next
                 for (int i = 0; ok && i <= n; i++) {
                     if (i < n) {
                         if (it + i > 0 && !(ok = al_wait(&S.s_free, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
-                        for (int sl = 0; sl < nK; sl++, at.step(slots)) {
+                        uint32_t b0 = al_desc_lo(qs_a, 16);
+                        for (int sl = 0; sl < nK; sl++, at.step(slots), b0 += (uint32_t)L.qslice >> 4) {
                             const int s = at.s;
                             if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
                             tc_fence_after();
-                            const int steps = min(64, hd - sl * 64) / 16;
-                            const uint32_t a0 = al_desc_lo(ring_a + s * C::kSlot, 16), b0 = al_desc_lo(qs_a + sl * L.qslice, 16);
+                            const int dims = hd - sl * 64;
+                            const uint32_t a0 = ring_d + (uint32_t)s * (C::kSlot / 16);
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)
-                                if (kk < steps)
+                                if (16 * kk < dims)
 #pragma unroll
                                     for (int t = 0; t < NT; t++)
                                         al_mma(tmem + t * nr, a0 + (uint32_t)(t * C::kTerm / 16 + 2 * kk), hi128, b0 + 2u * kk,
-                                               hi128, ids | ((3 - t) * nr >> 3) << 17, kk > 0 || t > 0 || sl > 0);
+                                               hi128, ids[t], kk > 0 || t > 0 || sl > 0);
                             tc_commit(&S.empty[s]);
                         }
                         if (!ok) break;
                         tc_commit(&S.s_full);
                     }
                     if (i >= 1) {
-                        const int cr = p->row0(i - 1);
                         if (!(ok = al_wait(&S.p_ready, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
-                        for (int vs = 0; vs < nV; vs++, at.step(slots)) {
-                            const int s = at.s, kh = vs / nDH, dh = vs % nDH;
-                            if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
-                            if (p->edge_in(cr + 64 * kh, cr + 64 * kh + 64)) {
-                                mbar_arrive(&S.fix_go);
-                                if (!(ok = al_wait(&S.fixed, fixes & 1u, &S.abort))) break;
-                                fixes++;
-                            }
-                            tc_fence_after();
-                            const uint32_t d = tmem + C::kO + (uint32_t)dh * 3 * R;
-                            const uint32_t a0 = al_desc_lo(ring_a + s * C::kSlot, 8192);
+#pragma unroll
+                        for (int kh = 0; kh < 2; kh++) {
                             const uint32_t b0 = al_desc_lo(ps_a + kh * 64 * 64, kChunk * 64);
+                            uint32_t d = tmem + C::kO;
+                            for (int dh = 0; ok && dh < nDH; dh++, at.step(slots), d += 3 * R) {
+                                const int s = at.s;
+                                if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
+                                if (edge[kh]) {
+                                    mbar_arrive(&S.fix_go);
+                                    if (!(ok = al_wait(&S.fixed, fixes & 1u, &S.abort))) break;
+                                    fixes++;
+                                }
+                                tc_fence_after();
+                                const uint32_t a0 = ring_d + (uint32_t)s * (C::kSlot / 16) + vlbo;
 #pragma unroll
-                            for (int ks = 0; ks < 4; ks++)
+                                for (int ks = 0; ks < 4; ks++)
 #pragma unroll
-                                for (int t = 0; t < NT; t++)
-                                    al_mma(d + t * nr, a0 + (uint32_t)(t * C::kTerm / 16 + 128 * ks), hi128, b0 + 64u * ks, hip,
-                                           idp | ((3 - t) * nr >> 3) << 17, ks > 0 || t > 0 || kh > 0);
-                            tc_commit(&S.empty[s]);
+                                    for (int t = 0; t < NT; t++)
+                                        al_mma(d + t * nr, a0 + (uint32_t)(t * C::kTerm / 16 + 128 * ks), hi128, b0 + 64u * ks,
+                                               hip, idp[t], ks > 0 || t > 0 || kh > 0);
+                                tc_commit(&S.empty[s]);
+                            }
                         }
                         if (!ok) break;
                         tc_commit(&S.pv_done);
                     }
+                    const int row = (c < nsink ? c : c + skip) * kChunk;  // of chunk i
+                    if (++c == c1) c -= n;
+                    edge[0] = p->edge_in(row, row + 64);
+                    edge[1] = p->edge_in(row + 64, row + 128);
                 }
                 it += n;
                 if (ok) ref.done(S);
