@@ -109,16 +109,31 @@ class Call:
         return got[: self.n]
 
 
+def _times(kind, n, rows, H, n_kv, hd, window, sinks):
+    """How often n lanes have to be given for the call to be too much work for the kernel of little work (by the
+    multiply-adds that it goes by, 300 M at most)."""
+    keys = min(rows, window + sinks) if window else rows
+    per = 32 if kind == "f32" else 64
+    gh = 1 if H == n_kv else 2 if H <= 2 * n_kv else 4 if H <= 4 * n_kv else 8
+    fma = -(-keys // per) * per * n * n_kv * -(-(H // n_kv) // gh) * gh * hd * 2
+    return min(int(300e6 // fma) + 1, 4096 // n)
+
+
 def _check_lanes(dev, kind, n_seqs, rows, H, n_kv, hd, pos, seqs, window, sinks, seed=0, status=0):
+    """The lanes once, and given over and over until the other kernel takes them (as many as there can be)."""
     kv = Caches(dev, kind, n_seqs, rows, n_kv, hd, seed)
-    c = Call(dev, len(pos), H, n_kv, hd, seed + 1)
-    c.lanes(kv, _i32(pos, dev), _i32(seqs, dev), window, sinks)
-    got, q = c.result(status), c.q.cpu().numpy()
-    ref = np.zeros_like(got, dtype=np.float64)
-    for i, (p, s) in enumerate(zip(pos, seqs)):
-        if 0 <= p < rows and 0 <= s < n_seqs:
-            ref[i] = _ref(q[i], *kv.host(s), p, window, sinks, n_kv)
-    _close(got, ref)
+    n, ref = len(pos), None
+    for times in sorted({1, _times(kind, n, rows, H, n_kv, hd, window, sinks)}):
+        c = Call(dev, n * times, H, n_kv, hd, seed + 1)
+        c.q.copy_(c.q[:n].repeat(times, 1, 1))
+        c.lanes(kv, _i32(np.tile(np.int64(pos), times), dev), _i32(np.tile(np.int64(seqs), times), dev), window, sinks)
+        got, q = c.result(status), c.q.cpu().numpy()
+        if ref is None:
+            ref = np.zeros((n, H, hd))
+            for i, (p, s) in enumerate(zip(pos, seqs)):
+                if 0 <= p < rows and 0 <= s < n_seqs:
+                    ref[i] = _ref(q[i], *kv.host(s), p, window, sinks, n_kv)
+        _close(got, np.tile(ref, (times, 1, 1)))
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
@@ -170,6 +185,26 @@ def test_long_context(dev, kind):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_runs_of_lanes_past_a_thousand(dev, kind):
+    # one prompt's chunk of 2100 lanes, and lanes of few sequences that return to each of them (a sample is compared)
+    S, R, H, n_kv, hd = 7, 2200, 4, 1, 64
+    kv = Caches(dev, kind, S, R, n_kv, hd, 14, layers=1)
+    rng = np.random.default_rng(15)
+    runs = rng.integers(0, S, 4000)
+    for pos, seqs in ((list(range(60, 2160)), [3] * 2100),
+                      (rng.integers(-1, R, 4000).tolist(), np.repeat(runs, rng.integers(1, 5, 4000))[:4000].tolist())):
+        c = Call(dev, len(pos), H, n_kv, hd)
+        c.lanes(kv, _i32(pos, dev), _i32(seqs, dev), 300, 5)
+        got, q = c.result(), c.q.cpu().numpy()
+        host = [kv.host(s) for s in range(S)]
+        for i in list(range(1000, 1060)) + list(range(2030, 2060)) + rng.integers(0, len(pos), 60).tolist():
+            if pos[i] >= 0:
+                _close(got[i], _ref(q[i], *host[seqs[i]], pos[i], 300, 5, n_kv))
+            else:
+                assert (got[i] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("H,n_kv,hd", [(2, 2, 64), (4, 1, 256), (96, 2, 64)])
 def test_many_blocks_per_sm(dev, kind, H, n_kv, hd):
     # each SM runs through many blocks of keys and several tiles: single tokens of 40 users at long contexts
@@ -187,13 +222,14 @@ def test_many_blocks_per_sm(dev, kind, H, n_kv, hd):
             _close(got[i], _ref(q[i], k, v, pos[i], window, sinks, n_kv))
 
 
+@pytest.mark.parametrize("times", [1, 40])  # (40: too much work for the kernel of little work)
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
-def test_unseen_rows_never_reach_the_outputs(dev, kind):
+def test_unseen_rows_never_reach_the_outputs(dev, kind, times):
     import torch
 
     S, R, H, n_kv, hd, W, sinks = 3, 300, 4, 2, 64, 50, 3
-    pos = [170, 20] + list(range(100, 164))
-    seqs = [0, 1] + [2] * 64
+    pos = ([170, 20] + list(range(100, 164))) * times
+    seqs = ([0, 1] + [2] * 64) * times
     for bad in (float("nan"), float("inf"), -float("inf"), 3.4e38):
         kv = Caches(dev, kind, S, R, n_kv, hd, 3)
         clean = [kv.host(s) for s in range(S)]
@@ -206,8 +242,11 @@ def test_unseen_rows_never_reach_the_outputs(dev, kind):
         c = Call(dev, len(pos), H, n_kv, hd)
         c.lanes(kv, _i32(pos, dev), _i32(seqs, dev), W, sinks)
         got, q = c.result(), c.q.cpu().numpy()
-        _close(got, np.stack([_ref(q[i], *clean[s], p, W, sinks, n_kv) for i, (p, s) in enumerate(zip(pos, seqs))]))
+        if bad != bad:
+            want = np.stack([_ref(q[i], *clean[s], p, W, sinks, n_kv) for i, (p, s) in enumerate(zip(pos, seqs))])
+        _close(got, want)
     # a row that some lanes of a chunk see and others do not: NaN for those that see it, and only those
+    clean_ref = [_ref(q[i], *clean[s], p, W, sinks, n_kv) for i, (p, s) in enumerate(zip(pos, seqs))]
     for which in range(2):
         kv = Caches(dev, kind, S, R, n_kv, hd, 3)
         (kv.k, kv.v)[which][2, 130, :hd] = float("nan")  # KV head 0 alone
@@ -217,7 +256,7 @@ def test_unseen_rows_never_reach_the_outputs(dev, kind):
         got, q = c.out.cpu().numpy()[: len(pos)], c.q.cpu().numpy()
         for i, (p, s) in enumerate(zip(pos, seqs)):
             sees = s == 2 and 130 <= p < 130 + W
-            ref = _ref(q[i], *clean[s], p, W, sinks, n_kv)
+            ref = clean_ref[i]
             _close(got[i, H // 2:], ref[H // 2:])
             if sees:
                 assert np.isnan(got[i, : H // 2]).all(axis=-1 if which == 0 else None).all() or which == 1
@@ -272,15 +311,19 @@ def test_shared_prompt(dev, kind, B, H, n_kv, hd, P):
     pos = [P + o for o in own]
     if P > 5:
         pos[0] = P - 5  # a lane that is still inside the prompt
-    c = Call(dev, B, H, n_kv, hd)
-    c.prefix(pre, _i32([P], dev), None, kv, _i32(pos, dev), _i32(np.arange(B), dev))
-    got, q = c.result(), c.q.cpu().numpy()
     pk, pv = pre.host(0)
-    ref = []
-    for i in range(B):
-        k, v = kv.host(i)
-        ref.append(_ref(q[i], np.concatenate([pk[:P], k]), np.concatenate([pv[:P], v]), pos[i], 0, 0, n_kv))
-    _close(got, np.stack(ref))
+    ref = None
+    for times in sorted({1, _times(kind, B, max(P, 1) + R, H, n_kv, hd, 0, 0)}):
+        c = Call(dev, B * times, H, n_kv, hd)
+        c.q.copy_(c.q[:B].repeat(times, 1, 1))
+        c.prefix(pre, _i32([P], dev), None, kv, _i32(np.tile(pos, times), dev), _i32(np.tile(np.arange(B), times), dev))
+        got, q = c.result(), c.q.cpu().numpy()
+        if ref is None:
+            ref = []
+            for i in range(B):
+                k, v = kv.host(i)
+                ref.append(_ref(q[i], np.concatenate([pk[:P], k]), np.concatenate([pv[:P], v]), pos[i], 0, 0, n_kv))
+        _close(got, np.tile(np.stack(ref), (times, 1, 1)))
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
@@ -294,15 +337,20 @@ def test_several_prompts(dev, kind, window, sinks):
     seqs = [0, 1, 2, 3, 4, 5, 6, 7, 8, 7] + [4] * 30
     own = [0, 9, 63, 40, 5, 3, 63, 20, 33, 21] + list(range(6, 36))
     pos = [plens[f] + o for f, o in zip(pof, own)]
-    c = Call(dev, len(pos), 6, 2, 64)
-    c.prefix(pre, _i32(plens, dev), _i32(pof, dev), kv, _i32(pos, dev), _i32(seqs, dev), window, sinks)
-    got, q = c.result(), c.q.cpu().numpy()
-    ref = []
-    for i, (f, s, p) in enumerate(zip(pof, seqs, pos)):
-        (pk, pv), (k, v) = pre.host(f), kv.host(s)
-        n = plens[f]
-        ref.append(_ref(q[i], np.concatenate([pk[:n], k]), np.concatenate([pv[:n], v]), p, window, sinks, 2))
-    _close(got, np.stack(ref))
+    N, ref = len(pos), None
+    for times in sorted({1, _times(kind, N, 160 + 64, 6, 2, 64, window, sinks)}):
+        tile = lambda x: _i32(np.tile(x, times), dev)
+        c = Call(dev, N * times, 6, 2, 64)
+        c.q.copy_(c.q[:N].repeat(times, 1, 1))
+        c.prefix(pre, _i32(plens, dev), tile(pof), kv, tile(pos), tile(seqs), window, sinks)
+        got, q = c.result(), c.q.cpu().numpy()
+        if ref is None:
+            ref = []
+            for i, (f, s, p) in enumerate(zip(pof, seqs, pos)):
+                (pk, pv), (k, v) = pre.host(f), kv.host(s)
+                n = plens[f]
+                ref.append(_ref(q[i], np.concatenate([pk[:n], k]), np.concatenate([pv[:n], v]), p, window, sinks, 2))
+        _close(got, np.tile(np.stack(ref), (times, 1, 1)))
 
 
 def test_offsets_past_32_bits(dev):

@@ -228,18 +228,17 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
                 atomicMin(&smin[i - in_tile], spos[i]);
                 atomicMax(&smax[i - in_tile], spos[i]);
             }
-            // a tile may reach into the lanes of the next round: its first lane gathers it once those are through
-            // (the tile's lanes stand at most LT - 1 behind it)
+            // (a tile that reaches the end of this round's lanes may go on in the next: its first lane looks)
             bar();
             AlTile t;
             int64_t tu = 0;
             if (start) {
-                for (int j = base + T; j < n && j < i + D.LT && spos[j] >= 0 && same(i, j); j++) {
-                    snl[i]++;
-                    smin[i] = min(smin[i], spos[j]);
-                    smax[i] = max(smax[i], spos[j]);
-                }
-                const int nl = snl[i], pmin = smin[i], pmax = smax[i];
+                int nl = snl[i], pmin = smin[i], pmax = smax[i];
+                if (i + nl == base + T)
+                    for (int j = base + T; j < n && j < i + D.LT && spos[j] >= 0 && same(i, j); j++, nl++) {
+                        pmin = min(pmin, spos[j]);
+                        pmax = max(pmax, spos[j]);
+                    }
                 // positions and rows are below 2^31, so differences fit
                 const int P = A.pre.k ? A.prefix_len[spre[i]] : 0;
                 const int org = st == 0 ? 0 : P, lim = st == 0 ? P : A.own.rows;
@@ -1432,10 +1431,251 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ------------------------------------------------------------------ little work
+// A few lanes over short stretches are over before the product kernel's plan,
+// pieces and rings are set up.  Here every CTA takes one lane, up to GH query
+// heads of one KV head and kKeys of the keys that the lane sees, counted
+// without gaps (first tokens, then the window): it copies their k and v rows
+// into shared memory, all of them at once, and computes in fp32 on the CUDA
+// cores.  Nothing is shared between lanes.  The CTA s of a (lane, head)
+// leaves partial sums for al_few_merge_kernel, or the result if it is alone.
+constexpr int kFewThreads = 256, kFewMaxSplits = 1024, kFewRows = 16384;
+constexpr int kFewDims = 64;  // dims of a head per merging CTA
+
+template <typename T>
+struct FewCfg {
+    static constexpr int kKeys = sizeof(T) == 4 ? 32 : 64;       // 32 KB of k and of v rows at most
+    static constexpr int kParts = kFewThreads / kKeys;           // threads that share a key's dot products
+    static constexpr int kVec = 16 / (int)sizeof(T);             // values of 16 bytes
+};
+
+// What lane i sees: keys j < sk and lo <= j <= p (sk <= lo), `count` of them; -1 if it is none.
+struct FewLane {
+    int count, sk, lo, len, seq, pre;
+    bool bad;
+    __device__ __forceinline__ FewLane(const AlArgs &A, int i) {
+        const int p = A.positions[i];
+        seq = A.seqs[i];
+        pre = 0, len = 0;
+        bool ok = seq >= 0 && seq < A.own.n_seqs;
+        if (A.pre.k) {
+            pre = A.prefix_of ? A.prefix_of[i] : 0;
+            ok = ok && pre >= 0 && pre < A.pre.n_seqs;
+            len = ok ? A.prefix_len[pre] : 0;
+            ok = ok && len >= 0 && len <= A.pre.rows;
+        }
+        ok = ok && p - len < A.own.rows;
+        bad = p >= 0 && !ok;
+        lo = A.window && p >= A.window ? p - A.window + 1 : 0;
+        sk = min(A.sinks, lo);
+        count = p >= 0 && ok ? sk + p + 1 - lo : 0;
+    }
+};
+
+__device__ __forceinline__ void few_unpack(const uint4 &u, float (&f)[4]) {
+    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void few_unpack(const uint4 &u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; k++) f[2 * k] = __uint_as_float(w[k] << 16), f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+}
+
+// grid (splits, KV heads x blocks of GH query heads, lanes)
+template <typename T, int GH>
+__global__ void __launch_bounds__(kFewThreads) al_few_kernel(AlArgs A, AlDims D, float2 *ml, float *part, int splits) {
+    using C = FewCfg<T>;
+    constexpr int K = C::kKeys, V = C::kVec;
+    extern __shared__ __align__(16) uint8_t few_smem[];
+    __shared__ __align__(16) float qs[GH][256];
+    __shared__ __align__(16) float ws[K][GH];
+    const int tid = threadIdx.x, hd = A.hd, pitch = hd * (int)sizeof(T) + 16;
+    const int s = blockIdx.x, blocks = (D.group + GH - 1) / GH, kvh = blockIdx.y / blocks, h0 = (blockIdx.y % blocks) * GH;
+    const int lane_i = blockIdx.z, heads = min(GH, D.group - h0), head0 = kvh * D.group + h0;
+    uint8_t *ks = few_smem, *vs = few_smem + K * pitch;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const FewLane L(A, lane_i);
+    if (L.bad && s == 0 && blockIdx.y == 0 && tid == 0) raise_status(A.status, kStatusBadLane);
+    const int n = min(K, L.count - s * K);  // this CTA's keys
+    if (n <= 0) {
+        if (s == 0)
+            for (int e = tid; e < heads * hd; e += kFewThreads) A.out[((int64_t)lane_i * A.n_heads + head0) * hd + e] = 0.0f;
+        return;
+    }
+    const int per = hd / V;  // 16-byte groups of a row
+    for (int e = tid; e < n * per; e += kFewThreads) {
+        const int r = e / per, c = e - r * per, x = s * K + r, j = x < L.sk ? x : L.lo + x - L.sk;
+        const bool in = j < L.len;
+        const qlin_kv &kv = in ? A.pre : A.own;
+        const int64_t off = (int64_t)(in ? L.pre : L.seq) * kv.seq_stride + (int64_t)(in ? j : j - L.len) * kv.row_stride +
+                            kvh * hd + c * V;
+        cp_async16(ks + r * pitch + c * 16, static_cast<const T *>(kv.k) + off, 16);
+        cp_async16(vs + r * pitch + c * 16, static_cast<const T *>(kv.v) + off, 16);
+    }
+    cp_async_commit();
+    for (int e = tid; e < GH * hd; e += kFewThreads) {
+        const int h = e / hd;
+        qs[h][e - h * hd] = h < heads ? A.q[((int64_t)lane_i * A.n_heads + head0) * hd + e] : 0.0f;
+    }
+    cp_async_wait_pending<0>();
+    __syncthreads();
+    // scores: kParts threads share a key, 16 bytes of its row in turn
+    const int key = tid / C::kParts, pt = tid % C::kParts;
+    float sc[GH];
+#pragma unroll
+    for (int h = 0; h < GH; h++) sc[h] = 0.0f;
+    if (key < n)
+        for (int c = pt; c < per; c += C::kParts) {
+            float k[V];
+            few_unpack(lds128(ks + key * pitch + c * 16), k);
+#pragma unroll
+            for (int h = 0; h < GH; h++)
+#pragma unroll
+                for (int v = 0; v < V; v += 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(&qs[h][c * V + v]);
+                    sc[h] = __fmaf_rn(q.x, k[v], sc[h]);
+                    sc[h] = __fmaf_rn(q.y, k[v + 1], sc[h]);
+                    sc[h] = __fmaf_rn(q.z, k[v + 2], sc[h]);
+                    sc[h] = __fmaf_rn(q.w, k[v + 3], sc[h]);
+                }
+        }
+#pragma unroll
+    for (int off = 1; off < C::kParts; off <<= 1)
+#pragma unroll
+        for (int h = 0; h < GH; h++) sc[h] = __fadd_rn(sc[h], __shfl_xor_sync(0xffffffffu, sc[h], off));
+    if (pt == 0)
+#pragma unroll
+        for (int h = 0; h < GH; h++) ws[key][h] = key < n ? __fmul_rn(sc[h], D.c) : -__int_as_float(0x7f800000);
+    __syncthreads();
+    // weights: a warp per head
+    const int warp = tid >> 5, lane = tid & 31;
+    const bool alone = L.count <= K;
+    const int64_t row0 = ((int64_t)lane_i * A.n_heads + head0) * splits + s;  // head h: row0 + h splits
+    __shared__ float inv[GH];
+    if (warp < GH) {
+        float x[K / 32], m = -__int_as_float(0x7f800000), l = 0.0f;
+#pragma unroll
+        for (int u = 0; u < K / 32; u++) x[u] = ws[lane + 32 * u][warp], m = fmaxf(m, x[u]);
+        m = warp_max(m);
+        if (!(m > -__int_as_float(0x7f800000))) m = 0.0f;  // (scores of minus infinity or NaN alone)
+#pragma unroll
+        for (int u = 0; u < K / 32; u++) {
+            x[u] = al_ex2(__fsub_rn(x[u], m));
+            l += x[u];
+            ws[lane + 32 * u][warp] = x[u];
+        }
+        l = warp_psum(l);
+        if (lane == 0) {
+            inv[warp] = alone ? __fdiv_rn(1.0f, l) : 1.0f;
+            if (!alone && warp < heads) ml[row0 + (int64_t)warp * splits] = make_float2(m, l);
+        }
+    }
+    __syncthreads();
+    // outputs: four dims of every `groups`-th key per thread, then the sum over the groups
+    const int nv = hd / 4, groups = kFewThreads / nv, gi = tid / nv, d = (tid - gi * nv) * 4;
+    float4 o[GH];
+#pragma unroll
+    for (int h = 0; h < GH; h++) o[h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (gi < groups)
+#pragma unroll 4
+        for (int j = gi; j < n; j += groups) {
+            float4 v;
+            if constexpr (sizeof(T) == 4) {
+                v = *reinterpret_cast<const float4 *>(vs + j * pitch + d * 4);
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2 *>(vs + j * pitch + d * 2);
+                v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                                __uint_as_float(u.y & 0xffff0000u));
+            }
+#pragma unroll
+            for (int h = 0; h < GH; h++) {
+                const float w = ws[j][h];
+                o[h].x = __fmaf_rn(w, v.x, o[h].x), o[h].y = __fmaf_rn(w, v.y, o[h].y);
+                o[h].z = __fmaf_rn(w, v.z, o[h].z), o[h].w = __fmaf_rn(w, v.w, o[h].w);
+            }
+        }
+    __syncthreads();  // the k rows' place takes the groups' sums: [groups][GH][hd], at most 32 KB
+    float *red = reinterpret_cast<float *>(few_smem);
+    if (gi < groups)
+#pragma unroll
+        for (int h = 0; h < GH; h++) *reinterpret_cast<float4 *>(red + (gi * GH + h) * hd + d) = o[h];
+    __syncthreads();
+    for (int e = tid; e < heads * nv; e += kFewThreads) {
+        const int h = e / nv, dd = (e - h * nv) * 4;
+        float4 a = *reinterpret_cast<const float4 *>(red + h * hd + dd);
+        for (int u = 1; u < groups; u++) {
+            const float4 b = *reinterpret_cast<const float4 *>(red + (u * GH + h) * hd + dd);
+            a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+        }
+        const float f = inv[h];
+        float *to = alone ? A.out + ((int64_t)lane_i * A.n_heads + head0 + h) * hd : part + (row0 + (int64_t)h * splits) * hd;
+        *reinterpret_cast<float4 *>(to + dd) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+    }
+}
+
+// grid (heads, lanes, dims / kFewDims): the partial sums of one (lane, head) by
+// the weights 2^(maximum - largest maximum).
+__global__ void __launch_bounds__(kFewThreads) al_few_merge_kernel(AlArgs A, const float2 *ml, const float *part, int splits,
+                                                                 int keys) {
+    __shared__ float w[kFewMaxSplits];
+    __shared__ float red[8];
+    __shared__ float4 acc[kFewThreads];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = A.hd;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (the lanes' places were there before the kernel before began)
+    const FewLane L(A, blockIdx.y);
+    const int n = (L.count + keys - 1) / keys;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n <= 1) return;  // done already
+    const int64_t id = (int64_t)blockIdx.y * A.n_heads + blockIdx.x, row0 = id * splits;
+    float m = -__int_as_float(0x7f800000);
+    for (int k = tid; k < n; k += kFewThreads) m = fmaxf(m, __ldcg(&ml[row0 + k]).x);
+    m = warp_max(m);
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; k++) m = fmaxf(m, red[k]);
+    __syncthreads();
+    float l = 0.0f;
+    for (int k = tid; k < n; k += kFewThreads) {
+        const float2 v = __ldcg(&ml[row0 + k]);
+        w[k] = al_ex2(__fsub_rn(v.x, m));
+        l += w[k] * v.y;
+    }
+    l = warp_psum(l);
+    if (lane == 0) red[warp] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; k++) l += red[k];
+    constexpr int nv = kFewDims / 4, groups = kFewThreads / nv;
+    const int gi = tid / nv, dv = blockIdx.z * nv + tid % nv;  // four dims, every 16th piece
+    const bool in = dv < hd / 4;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (in)
+#pragma unroll 8
+        for (int k = gi; k < n; k += groups) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + (row0 + k) * hd) + dv);
+            const float x = w[k];
+            a.x += v.x * x, a.y += v.y * x, a.z += v.z * x, a.w += v.w * x;
+        }
+    acc[tid] = a;
+    __syncthreads();
+    if (tid < nv && in) {
+        for (int k = 1; k < min(groups, n); k++) {
+            const float4 v = acc[k * nv + tid];
+            a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+        }
+        const float inv = __fdiv_rn(1.0f, l);
+        reinterpret_cast<float4 *>(A.out + id * hd)[dv] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    }
+}
+
 // ------------------------------------------------------------------ host
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
-AlWs carve(int n_lanes, int n_heads, int n_kv, int hd, char *base) {
+AlWs carve(int n_lanes, int n_heads, int n_kv, int hd, char *base, int64_t *n_rows = nullptr) {
     AlWs w{};
     size_t off = 0;
     auto take = [&](size_t b) {
@@ -1444,8 +1684,9 @@ AlWs carve(int n_lanes, int n_heads, int n_kv, int hd, char *base) {
         return p;
     };
     const int64_t group = n_heads / n_kv;
-    const int64_t rows = (int64_t)2 * kMaxCtas * (n_lanes * group < 48 ? n_lanes * group : 48) +
-                         (int64_t)2 * n_lanes * n_heads;
+    int64_t rows = (int64_t)2 * kMaxCtas * (n_lanes * group < 48 ? n_lanes * group : 48) + (int64_t)2 * n_lanes * n_heads;
+    if (rows < kFewRows) rows = kFewRows;
+    if (n_rows) *n_rows = rows;
     w.head = (AlPlanHead *)take(sizeof(AlPlanHead));
     w.first = (int *)take(sizeof(int) * kMaxCtas);
     w.tile_of = (int *)take(sizeof(int) * 2 * (size_t)n_lanes);
@@ -1477,6 +1718,62 @@ qlin_status kv_map(const void *p, const qlin_kv &c, int kvd, CUtensorMap *out) {
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     QLIN_REQUIRE(r == CUDA_SUCCESS, QLIN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return QLIN_OK;
+}
+
+// The keys that a lane can see at most, and the splits they make.
+int64_t few_splits(const AlArgs &A, bool f32) {
+    int64_t keys = (int64_t)A.own.rows + (A.pre.k ? A.pre.rows : 0);
+    if (A.window && (int64_t)A.window + A.sinks < keys) keys = (int64_t)A.window + A.sinks;
+    const int per = f32 ? FewCfg<float>::kKeys : FewCfg<uint16_t>::kKeys;
+    return (keys + per - 1) / per;
+}
+int few_heads(const AlDims &D) { return D.group <= 1 ? 1 : D.group <= 2 ? 2 : D.group <= 4 ? 4 : 8; }
+
+// Whether the call is little work, by the caches' sizes (the positions are on
+// the device): the multiply-adds of all its CTAs at most, with every lane and
+// block of GH heads counted for itself.  Measured with every position of the
+// caches in use, us per call here / by the product kernel: fp32, 4 query heads
+// on one KV head of 256: one lane of 512 7.4 / 16.7, 64 of 2048 (268 MB, 268 M
+// multiply-adds) 55.8 / 68.7; 8 on each of two of 128: 16 of 512 (34 M) 11.3 /
+// 23.3, 16 of 2048 (134 M) 28.6 / 31.2; bf16, 4 on one of 256: 16 of 2048 (67
+// M) 14.2 / 20.5, 64 of 2048 (268 M) 41.2 / 27.3; 8 on each of two of 128: 16
+// of 512 (34 M) 12.7 / 15.8, 16 of 2048 (134 M) 21.9 / 18.6; one on each of
+// four of 64: 64 of 2048 (67 M) 34.9 / 45.5.
+bool few_fits(const AlArgs &A, const AlDims &D, bool f32, int64_t rows) {
+    const int64_t s = few_splits(A, f32);
+    const int gh = few_heads(D);
+    const double fma = (double)s * (f32 ? FewCfg<float>::kKeys : FewCfg<uint16_t>::kKeys) * A.n_lanes * A.n_kv *
+                       ((D.group + gh - 1) / gh) * gh * A.hd * 2;
+    return s <= kFewMaxSplits && s * A.n_lanes * A.n_heads <= rows && fma <= (!f32 ? 90e6 : gh < 8 ? 300e6 : 140e6);
+}
+
+template <typename T, int GH>
+qlin_status launch_few(const AlArgs &A, const AlDims &D, const AlWs &w, int splits, cudaStream_t st) {
+    const void *kern = (const void *)al_few_kernel<T, GH>;
+    const size_t rowbytes = (size_t)2 * FewCfg<T>::kKeys * (A.hd * sizeof(T) + 16);
+    const size_t sums = (size_t)(kFewThreads / (A.hd / 4)) * GH * A.hd * sizeof(float);
+    const size_t smem = rowbytes > sums ? rowbytes : sums;
+    blocks_per_sm(kern, smem);  // raises the dynamic shared-memory limit once
+    void *args[] = {(void *)&A, (void *)&D, (void *)&w.ml, (void *)&w.part, (void *)&splits};
+    return launch_pdl(kern, dim3(splits, A.n_kv * ((D.group + GH - 1) / GH), A.n_lanes), dim3(kFewThreads), smem, st, args,
+                      "al_few_kernel");
+}
+template <typename T>
+qlin_status launch_few(const AlArgs &A, const AlDims &D, const AlWs &w, int splits, cudaStream_t st) {
+    switch (few_heads(D)) {
+        case 1: return launch_few<T, 1>(A, D, w, splits, st);
+        case 2: return launch_few<T, 2>(A, D, w, splits, st);
+        case 4: return launch_few<T, 4>(A, D, w, splits, st);
+        default: return launch_few<T, 8>(A, D, w, splits, st);
+    }
+}
+qlin_status attend_few(const AlArgs &A, const AlDims &D, const AlWs &w, bool f32, cudaStream_t st) {
+    const int splits = (int)few_splits(A, f32), keys = f32 ? FewCfg<float>::kKeys : FewCfg<uint16_t>::kKeys;
+    if (qlin_status e = f32 ? launch_few<float>(A, D, w, splits, st) : launch_few<uint16_t>(A, D, w, splits, st)) return e;
+    if (splits == 1) return QLIN_OK;
+    void *args[] = {(void *)&A, (void *)&w.ml, (void *)&w.part, (void *)&splits, (void *)&keys};
+    return launch_pdl((const void *)al_few_merge_kernel, dim3(A.n_heads, A.n_lanes, (A.hd + kFewDims - 1) / kFewDims),
+                      dim3(kFewThreads), 0, st, args, "al_few_merge_kernel");
 }
 
 qlin_status check_kv(const char *fn, const char *what, const qlin_kv *c, int n_kv, int hd) {
@@ -1516,7 +1813,8 @@ qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t work
     QLIN_REQUIRE(aligned4(A.positions) && aligned4(A.seqs) && aligned4(A.prefix_len) && aligned4(A.prefix_of) &&
                      aligned4(A.status),
                  QLIN_ERR_INVALID_ARG, "%s: pointer not 4-byte aligned", fn);
-    const AlWs w = carve(A.n_lanes, A.n_heads, A.n_kv, A.hd, (char *)workspace);
+    int64_t rows;
+    const AlWs w = carve(A.n_lanes, A.n_heads, A.n_kv, A.hd, (char *)workspace, &rows);
     QLIN_REQUIRE(workspace_bytes >= w.bytes, QLIN_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", fn, workspace_bytes,
                  w.bytes);
     const bool f32 = A.own.type == QLIN_KV_F32;
@@ -1530,6 +1828,7 @@ qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t work
     D.grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
     D.merge = A.n_lanes <= kSelfPlan ? 1 : 32;
     D.c = (float)(1.4426950408889634 / std::sqrt((double)A.hd));
+    if (few_fits(A, D, f32, rows)) return attend_few(A, D, w, f32, (cudaStream_t)stream);
     const void *kern = f32 ? (const void *)al_attn_kernel<3> : (const void *)al_attn_kernel<1>;
     const size_t smem = kAlSmem, plan_smem = 6 * sizeof(int) * (size_t)A.n_lanes;
     QLIN_REQUIRE((int)smem <= max_smem_optin(), QLIN_ERR_UNSUPPORTED, "%s: shared memory", fn);
