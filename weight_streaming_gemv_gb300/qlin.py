@@ -183,6 +183,10 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
+        c = torch._C
+        # (torch.cuda.current_stream() makes an object: 3 us of a 13 us call on a Grace core, this 0.2)
+        if hasattr(c, "_cuda_getCurrentRawStream") and torch.cuda.is_initialized():
+            return c._cuda_getCurrentRawStream(c._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
