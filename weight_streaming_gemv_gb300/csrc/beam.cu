@@ -63,10 +63,11 @@ __device__ __forceinline__ uint64_t cand_key(float v, uint32_t idx) { return ((u
 constexpr uint32_t kOrdNegInf = 0x007fffffu;  // ord32(-inf); anything above it is a candidate
 
 struct SelPart {  // a slice's part of its beam's sum of exponentials
-    double sum;  // times 2^sel_exp(m), or times exp(m) where sel_wide(m)
-    float m;     // the slice's largest logit
-    int count;   // candidates listed
+    float sum, lo;  // sum + lo, times 2^sel_exp(m), or times exp(m) where sel_wide(m)
+    float m;        // the slice's largest logit
+    int count;      // candidates listed
 };
+static_assert(sizeof(SelPart) == 16, "read as one vector");
 constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.9259629911266175e-8f;
 __device__ __forceinline__ bool sel_wide(float m) { return !(fabsf(m) <= 16777216.0f); }
 __device__ __forceinline__ float sel_exp(float m) { return ceilf(__fmul_rn(m, kLog2eHi)); }
@@ -98,6 +99,20 @@ __device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *fi
     return !(finished && finished[row]) && scores[row] > -__int_as_float(0x7f800000);
 }
 
+// Two floats as one number of twice the digits: h + l += oh + ol, with the
+// rounding of h + oh kept in l (fp64 costs 16 cycles per instruction and warp
+// here, and stalls what depends on it for longer).
+__device__ __forceinline__ void pair_add(float &h, float &l, float oh, float ol) {
+    const float t = __fadd_rn(h, oh), z = __fsub_rn(t, h);
+    l = __fadd_rn(__fadd_rn(l, ol), __fadd_rn(__fsub_rn(h, __fsub_rn(t, z)), __fsub_rn(oh, z)));
+    h = t;
+}
+__device__ __forceinline__ void pair_warp_sum(float &h, float &l) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        pair_add(h, l, __shfl_xor_sync(0xffffffffu, h, off), __shfl_xor_sync(0xffffffffu, l, off));
+}
+
 // A slice's candidates so far, in shared memory.
 struct SelBuf {
     uint64_t key[kSelBuf];
@@ -127,13 +142,45 @@ __device__ __forceinline__ int place_of(uint64_t mine, Tie tie, bool self, const
 }
 
 // The n largest of the c (<= kSelBuf) keys of b to out, in descending order
-// (keys are unique).
+// (keys are unique); four threads count for a key.
 __device__ __forceinline__ void sel_rank(const SelBuf &b, int c, int n, uint64_t *out) {
-    for (int i = threadIdx.x; i < c; i += kSelThreads) {
-        const uint64_t key = b.key[i];
-        const int r = place_of<uint64_t>(key, 0, true, b.key, b.key, c);
-        if (r < n) out[r] = key;
+    const int part = threadIdx.x & 3, per = (c + 3) / 4, j0 = min(part * per, c), j1 = min(j0 + per, c);
+    for (int i0 = 0; i0 < c; i0 += kSelThreads / 4) {
+        const int i = i0 + ((int)threadIdx.x >> 2);
+        uint64_t key = 0;
+        int r = 0;
+        if (i < c) {
+            key = b.key[i];
+            r = place_of<uint64_t>(key, 0, i >= j0 && i < j1, b.key + j0, b.key, j1 - j0);
+        }
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        if (i < c && part == 0 && r < n) out[r] = key;
     }
+}
+
+// A value that n of the block's threads' `mine` are no smaller than: with
+// k = ceil(n / warps) and j = ceil(n / k), the j-th largest of the warps' k-th
+// largest.  To be called by all warps, with a barrier behind it before wkth
+// is written again.
+__device__ __forceinline__ void sel_kth(uint32_t mine, int k, uint32_t *wkth) {
+    const int lane = threadIdx.x & 31;
+    uint32_t kth = 0;
+    for (int r = 0; r < k; r++) {
+        kth = __reduce_max_sync(0xffffffffu, mine);
+        const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
+        if (lane == __ffs(who) - 1) mine = 0;
+    }
+    if (lane == 0) wkth[threadIdx.x >> 5] = kth;
+}
+__device__ __forceinline__ uint32_t sel_threshold(const uint32_t *wkth, int j) {
+    const int own = threadIdx.x & (kSelWarps - 1);
+    const uint32_t mine = wkth[own];
+    int above = 0;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; w++) above += wkth[w] > mine || (wkth[w] == mine && w < own);
+    const uint32_t who = __ballot_sync(0xffffffffu, above == j - 1);
+    return __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
 }
 
 // grid (S, rows): slice blockIdx.x of a row is the values from blockIdx.x * len
@@ -148,7 +195,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     __shared__ float wmax[kSelWarps];
     __shared__ float2 wsum[kSelWarps];
     __shared__ uint32_t wkth[kSelWarps];
-    __shared__ SelBuf buf;
+    __shared__ SelBuf buf, last;
     __shared__ uint64_t best[kMaxOut];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.y, S = gridDim.x;
@@ -185,7 +232,8 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     float m, sum;  // this thread's largest value and its sum times 2^e
     int e, c;
     uint32_t thr;  // n values of the slice so far are no smaller (minus infinity is no candidate)
-    const int k = (n + kSelWarps - 1) / kSelWarps;  // at most 16
+    const int k = (n + kSelWarps - 1) / kSelWarps, jw = (n + k - 1) / k;  // k at most 16
+    if (tid == 0) last.count = 0;
     // Once without looking at the buffer after every tile; where that let it
     // overflow (many equal values) once more, carefully.
     for (bool careful = false;; careful = true) {
@@ -214,31 +262,16 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
                 // infinity makes it infinite, nothing else does)
                 sum += ex2_approx(__fmaf_rn(v[j], kLog2eLo, __fmaf_rn(v[j], kLog2eHi, -ef)));
             }
-            // the threshold: from the first two tiles' thread maxima, then the n-th of what they left in the buffer, and
-            // again every eighth tile
-            const bool maxima = careful || tile < 2, rank = tile == 2 || tile % 8 == 7;
-            if (maxima || rank) {
-                if (maxima) {
-                    // the k-th largest of the warp's thread maxima
-                    uint32_t mine = ord32(tmax), kth = 0;
-                    for (int r = 0; r < k; r++) {
-                        kth = __reduce_max_sync(0xffffffffu, mine);
-                        const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
-                        if (lane == __ffs(who) - 1) mine = 0;
-                    }
-                    if (lane == 0) wkth[warp] = kth;
-                }
+            // the threshold: from the threads' maxima so far, after tiles 1, 2, 4, 8, ... (a tile's share of the values
+            // is halved from one to the next, so each part of the slice leaves about as many candidates)
+            if (careful || (tile & (tile + 1)) == 0) {
+                sel_kth(ord32(m), k, wkth);
                 __syncthreads();
-                if (maxima) {
-                    uint32_t tk = wkth[0];
-#pragma unroll
-                    for (int w = 1; w < kSelWarps; w++) tk = min(tk, wkth[w]);
-                    thr = max(thr, tk);
-                }
+                thr = max(thr, sel_threshold(wkth, jw));
                 c = buf.count;
                 __syncthreads();
                 over = c > kSelBuf;
-                if (!over && (c > kSelBuf / 2 || (rank && c >= n))) {  // keep the n best
+                if (!over && c > kSelBuf / 2) {  // keep the n best
                     sel_rank(buf, c, n, best);
                     __syncthreads();
                     c = min(c, n);
@@ -249,13 +282,18 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
                 }
             }
             const float low = unord32(thr);
-            if (tmax >= low && !over)  // (NaN is not)
+            if (tmax >= low && !over) {  // (NaN is not)
+                int p = 0;
+#pragma unroll
+                for (int j = 0; j < VPT; j++) p += v[j] >= low;
+                p = atomicAdd(&buf.count, p);
 #pragma unroll
                 for (int j = 0; j < VPT; j++)
                     if (v[j] >= low) {
-                        const int p = atomicAdd(&buf.count, 1);
                         if (p < kSelBuf) buf.key[p] = cand_key(v[j], (uint32_t)(at + index(j)));
+                        p++;
                     }
+            }
             if (careful) {
                 __syncthreads();
                 if (buf.count > kSelBuf) {
@@ -289,30 +327,24 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
 #pragma unroll
             for (int j = 0; j < VPT; j++) v[j] = nx[j];
         }
+        sel_kth(ord32(m), k, wkth);
+        const float wtop = warp_max(m);
+        if (lane == 0) wmax[warp] = wtop;
         __syncthreads();
         c = buf.count;
-        __syncthreads();
         if (careful || (!over && c <= kSelBuf)) break;
+        __syncthreads();
     }
     // the ones below the last threshold are out
-    {
-        uint64_t keep[kSelBuf / kSelThreads];
-#pragma unroll
-        for (int u = 0; u < kSelBuf / kSelThreads; u++)
-            keep[u] = tid + u * kSelThreads < c ? buf.key[tid + u * kSelThreads] : 0;
-        __syncthreads();
-        if (tid == 0) buf.count = 0;
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kSelBuf / kSelThreads; u++)
-            if ((uint32_t)(keep[u] >> 32) >= thr) buf.key[atomicAdd(&buf.count, 1)] = keep[u];
+    thr = max(thr, sel_threshold(wkth, jw));
+    for (int i = tid; i < c; i += kSelThreads) {
+        const uint64_t key = buf.key[i];
+        if ((uint32_t)(key >> 32) >= thr) last.key[atomicAdd(&last.count, 1)] = key;
     }
     // the block's largest value, and the sum on its scale (no thread's is above it)
-    float top = warp_max(m);
-    if (lane == 0) wmax[warp] = top;
-    __syncthreads();
+    float top = wmax[0];
 #pragma unroll
-    for (int w = 0; w < kSelWarps; w++) top = fmaxf(top, wmax[w]);
+    for (int w = 1; w < kSelWarps; w++) top = fmaxf(top, wmax[w]);
     float d;
     if (sel_wide(top)) {
         // logits beyond 2^24 (or none at all): once more, relative to the largest
@@ -323,39 +355,25 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
         d = __fmul_rn(sum, pow2i(max(e - (int)sel_exp(top), -126)));
     }
     if (!(sum < -ninf)) d = __int_as_float(0x7fc00000);  // the beam's sum becomes NaN
-    // the threads' sums with the rounding of every addition kept (fp64 costs 16 cycles per instruction and warp here)
-    auto add = [](float &h, float &l, float oh, float ol) {
-        const float t = __fadd_rn(h, oh), z = __fsub_rn(t, h);
-        l = __fadd_rn(__fadd_rn(l, ol), __fadd_rn(__fsub_rn(h, __fsub_rn(t, z)), __fsub_rn(oh, z)));
-        h = t;
-    };
+    // the threads' sums as pairs
     float dl = 0.0f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        add(d, dl, __shfl_xor_sync(0xffffffffu, d, off), __shfl_xor_sync(0xffffffffu, dl, off));
+    pair_warp_sum(d, dl);
     if (lane == 0) wsum[warp] = make_float2(d, dl);
     __syncthreads();
-    c = buf.count;
+    c = last.count;
     const int64_t ps = (int64_t)row * S + blockIdx.x;
     if (tid == 0) {
-        SelPart p;
 #pragma unroll
-        for (int w = 1; w < kSelWarps; w++) add(d, dl, wsum[w].x, wsum[w].y);
-        p.sum = (double)d + (double)dl;
-        p.m = top;
-        p.count = min(c, n);
-        part[ps] = p;
+        for (int w = 1; w < kSelWarps; w++) pair_add(d, dl, wsum[w].x, wsum[w].y);
+        part[ps] = SelPart{d, dl, top, min(c, n)};
     }
-    sel_rank(buf, c, n, cand + ps * n);
+    sel_rank(last, c, n, cand + ps * n);
 }
 
 constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeLists = 1024;  // beams * slices at most (sel_slices)
 constexpr int kMergeBuf = 2048;    // candidates ranked in shared memory
+constexpr int kMergeStage = 4096;  // listed candidates read at once
 
-__device__ __forceinline__ bool better(double c, int64_t at, double bc, int64_t bat) {
-    return c > bc || (c == bc && at < bat);
-}
 // fp64 as an unsigned whole number in the same order, above 0 for all but NaN
 __device__ __forceinline__ uint64_t ord64(double v) {
     const uint64_t u = (uint64_t)__double_as_longlong(v);
@@ -370,108 +388,171 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
     return (uint64_t)hi << 32 | lo;
 }
 
+// log s to about 1e-12, from s = 2^k f with f in [2/3, 4/3] and log f =
+// 2 (w + w^3 / 3 + w^5 / 5 + ...), w = (f - 1) / (f + 1): |w| <= 1/5, so the
+// first term left out is below 1e-12 of the sum.  (The sums it is taken of are
+// good to 1e-7 of their largest term.)  s is 0, positive or NaN.
+__device__ __forceinline__ double log_of_sum(double s) {
+    if (!(s > 0.0)) return s == 0.0 ? -(double)__int_as_float(0x7f800000) : s;
+    int k = (__double2hiint(s) >> 20) - 1023;
+    double f = s * __hiloint2double((1023 - k) << 20, 0);
+    if (f > 4.0 / 3.0) f *= 0.5, k++;
+    const double num = f - 1.0, den = f + 1.0;
+    const double r = (double)(1.0f / (float)den), w = num * fma(r, fma(-den, r, 1.0), r);
+    const double z = w * w, z2 = z * z, z4 = z2 * z2;
+    const double p = fma(z4, fma(z2, fma(z, 1.0 / 15.0, 1.0 / 13.0), fma(z, 1.0 / 11.0, 1.0 / 9.0)),
+                         fma(z2, fma(z, 1.0 / 7.0, 1.0 / 5.0), fma(z, 1.0 / 3.0, 1.0)));
+    return fma((double)k, 0.69314718055994530942, 2.0 * w * p);
+}
+
 struct MergeSmem {
-    double lse[kMaxBeams];  // the log of a beam's sum, less top
-    float top[kMaxBeams];   // its largest logit
+    double sum[kMaxBeams];  // of a beam's exponentials
+    double lse[kMaxBeams];  // its log, less top
+    float2 lse2[kMaxBeams];  // that as a pair
+    float top[kMaxBeams];   // the beam's largest logit
     float base[kMaxBeams];  // its score
     int kind[kMaxBeams];    // 0: dead, 1: live, 2: finished
-    uint64_t key[kMergeBuf];
-    int64_t at[kMergeBuf];
-    uint64_t kth[kMergeWarps], sharp;
-    double wc[kMergeWarps];
+    int wild;               // a live beam's numbers are beyond what pairs of floats hold
+    int count, passing;
+    uint64_t sharp;
+    uint64_t kth[kMergeWarps], wkey[kMergeWarps];
     int64_t wat[kMergeWarps];
     int wlist[kMergeWarps];
-    int count, passing;
-    uint16_t list[kMergeLists];
-    uint8_t next[kMergeLists];  // the next entry of each list
+    SelPart part[kMergeThreads];
+    uint64_t key[kMergeBuf];
+    int64_t at[kMergeBuf];
+    uint64_t stage[kMergeStage];
+    uint16_t list[kMergeThreads];
+    uint8_t next[kMergeThreads];  // the next entry of each list
 };
 
 // One CTA per group: lse of every live beam, then the n best of the beams'
-// sorted lists (S lists per live beam, one entry for a finished one).
+// sorted lists (S lists per live beam, one entry for a finished one).  What it
+// reads is on its way at once; candidates are pairs of floats (48 bits), or
+// fp64 where a beam's numbers are too large for that, and compared as whole
+// numbers in the same order.
 __global__ void __launch_bounds__(kMergeThreads)
     beam_merge_kernel(const SelPart *__restrict__ part, const uint64_t *__restrict__ cand,
-                      const float *__restrict__ scores, const uint8_t *__restrict__ finished, int eos, int beams, int V,
+                      const float *__restrict__ scores, const uint8_t *__restrict__ finished, int eos, int beams,
                       int S, int n, float *out_scores, int32_t *parents, int32_t *tokens) {
     extern __shared__ __align__(16) uint8_t mg_raw[];
     MergeSmem &M = *reinterpret_cast<MergeSmem *>(mg_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = blockIdx.x;
+    const int g = blockIdx.x, lists = beams * S;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const float ninf = -__int_as_float(0x7f800000);
-    const double dninf = (double)ninf;
+    part += (int64_t)g * lists;
+    cand += (int64_t)g * lists * n;
+    const bool staged = lists * n <= kMergeStage;
+    {
+        // (a dead or finished beam's parts and a list's end hold anything: read, and not used)
+        uint64_t w[kMergeStage / kMergeThreads];
+        if (staged)
+#pragma unroll
+            for (int u = 0; u < kMergeStage / kMergeThreads; u++)
+                if (u * kMergeThreads + tid < lists * n) w[u] = __ldcg(&cand[u * kMergeThreads + tid]);
+        if (tid < lists) {
+            const int4 p = __ldcg((const int4 *)&part[tid]);
+            M.part[tid] = SelPart{__int_as_float(p.x), __int_as_float(p.y), __int_as_float(p.z), p.w};
+        }
+        if (tid < beams) {
+            const float score = scores[g * beams + tid];
+            M.base[tid] = score;
+            M.kind[tid] = finished && finished[g * beams + tid] ? 2 : score > ninf ? 1 : 0;
+        }
+        if (tid == 0) M.count = M.wild = 0, M.sharp = 0;
+        if (staged)
+#pragma unroll
+            for (int u = 0; u < kMergeStage / kMergeThreads; u++)
+                if (u * kMergeThreads + tid < lists * n) M.stage[u * kMergeThreads + tid] = w[u];
+    }
+    __syncthreads();
     for (int b = warp; b < beams; b += kMergeWarps) {
-        const int row = g * beams + b;
-        double l = 0.0;
+        if (M.kind[b] != 1) continue;
+        const SelPart *p = M.part + b * S;
         float big = ninf;
-        if (beam_live(scores, finished, row)) {
-            const SelPart *p = part + (int64_t)row * S;
-            for (int i = lane; i < S; i += 32) big = fmaxf(big, __ldcg(&p[i].m));
-            big = warp_max(big);
-            const double top = (double)big, E = (double)sel_exp(big);
-            const double ln2 = 0.69314718055994530942;
-            double s = 0.0;
+        for (int i = lane; i < S; i += 32) big = fmaxf(big, p[i].m);
+        big = warp_max(big);
+        double sum;
+        if (!sel_wide(big)) {
+            float h = 0.0f, l = 0.0f;
             for (int i = lane; i < S; i += 32) {
-                const float mi = __ldcg(&p[i].m);
-                const double si = __ldcg(&p[i].sum);
-                if (!sel_wide(big)) {  // (a wide slice is below every other one here: nothing, or NaN)
-                    const int sh = sel_wide(mi) ? -1000 : max((int)(sel_exp(mi) - (float)E), -1000);
-                    s += si * __hiloint2double((sh + 1023) << 20, 0);
-                } else if (mi > ninf) {
-                    s += si * exp((sel_wide(mi) ? (double)mi : (double)sel_exp(mi) * ln2) - top);
-                } else {
-                    s += si;  // 0, or NaN
-                }
+                // (a wide slice is far below the others here: nothing, or NaN)
+                const float sh = sel_wide(p[i].m) ? ninf : sel_exp(p[i].m) - sel_exp(big);
+                const float f = sh >= -126.0f ? pow2i((int)sh) : 0.0f;
+                pair_add(h, l, __fmul_rn(p[i].sum, f), __fmul_rn(p[i].lo, f));
+            }
+            pair_warp_sum(h, l);
+            sum = (double)h + (double)l;
+        } else {
+            sum = 0.0;
+            for (int i = lane; i < S; i += 32) {
+                const float mi = p[i].m;
+                const double si = (double)p[i].sum + (double)p[i].lo;  // (0, or NaN, where there is no logit)
+                sum += mi > ninf ? si * exp((sel_wide(mi) ? (double)mi : (double)sel_exp(mi) * 0.69314718055994530942) -
+                                            (double)big)
+                                 : si;
             }
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            l = s;
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         }
-        if (lane == 0) {
-            M.lse[b] = l, M.top[b] = big;
-            M.base[b] = scores[row];
-            M.kind[b] = finished && finished[row] ? 2 : scores[row] > ninf ? 1 : 0;
-        }
+        if (lane == 0) M.sum[b] = sum, M.top[b] = big;
     }
-    if (tid == 0) M.count = 0;
     __syncthreads();
-    if (tid < beams) {  // (one warp or two: an fp64 logarithm is a hundred instructions of 16 cycles)
+    if (tid < beams && M.kind[tid] == 1) {  // (one warp or two)
         const float big = M.top[tid];
-        M.lse[tid] = log(M.lse[tid]) + (sel_wide(big) ? 0.0 : (double)sel_exp(big) * 0.69314718055994530942 - (double)big);
+        const bool wide = sel_wide(big);
+        const double l = log_of_sum(M.sum[tid]) + (wide ? 0.0 : (double)sel_exp(big) * 0.69314718055994530942 - (double)big);
+        const float hi = (float)l;
+        M.lse[tid] = l;
+        M.lse2[tid] = make_float2(hi, (float)(l - (double)hi));
+        if (wide || !(fabsf(M.base[tid]) <= 1e30f)) M.wild = 1;
     }
     __syncthreads();
-    const int lists = beams * S;
-    // entry h of list i, its place beam << 32 | word; false where there is none (NaN: nothing of this beam)
-    auto entry = [&](int i, int h, double &c, int64_t &at) -> bool {
+    const bool wild = M.wild;
+    // entry h of list i as a whole number in the order of the candidates (0: there is none; NaN gives nothing of this
+    // beam), and its place beam << 32 | word
+    auto entry = [&](int i, int h, uint64_t &key, int64_t &at) -> bool {
         const int b = i / S, kind = M.kind[b];
-        c = dninf;
-        if (kind == 1 && h < n) {
-            const int64_t l = (int64_t)(g * beams + b) * S + (i - b * S);
-            const int count = __ldcg(&part[l].count);
-            const uint64_t k = __ldcg(&cand[l * n + h]);
-            if (h >= count) return false;
-            c = (double)M.base[b] + (((double)unord32((uint32_t)(k >> 32)) - (double)M.top[b]) - M.lse[b]);
+        key = 0;
+        if (kind == 1) {
+            if (h >= M.part[i].count) return false;
+            const uint64_t k = staged ? M.stage[i * n + h] : __ldcg(&cand[(int64_t)i * n + h]);
+            const float x = unord32((uint32_t)(k >> 32));
             at = (int64_t)b << 32 | (uint32_t)~(uint32_t)k;
+            if (wild) {
+                const double c = (double)M.base[b] + (((double)x - (double)M.top[b]) - M.lse[b]);
+                if (c > (double)ninf) key = ord64(c);
+            } else {
+                float c = x, l = 0.0f;
+                pair_add(c, l, -M.top[b], 0.0f);
+                pair_add(c, l, -M.lse2[b].x, -M.lse2[b].y);
+                pair_add(c, l, M.base[b], 0.0f);
+                // the nearest float and the rest of it (+ 0: no negative zeros)
+                float hi = l, lo = 0.0f;
+                pair_add(hi, lo, c, 0.0f);
+                if (fabsf(lo) < fabsf(hi) * 0x1p-53f) lo = 0.0f;  // (candidates near the type's lowest value are equal)
+                if (hi > ninf) key = (uint64_t)ord32(__fadd_rn(hi, 0.0f)) << 32 | ord32(__fadd_rn(lo, 0.0f));
+            }
         } else if (kind == 2 && h == 0 && i == b * S) {
-            c = (double)M.base[b];
+            const float c = __fadd_rn(M.base[b], 0.0f);
             at = (int64_t)b << 32 | (uint32_t)eos;
+            if (c > ninf) key = wild ? ord64((double)c) : (uint64_t)ord32(c) << 32 | ord32(0.0f);
         }
-        return c > dninf;
+        return key != 0;
     };
     // The lists are dealt out to the warps evenly.  With the q-th entries of
     // ceil(n / (warps q)) lists in every warp no smaller than a threshold, n
     // candidates are not.
     const int W = min(kMergeWarps, lists), q = (n + lists - 1) / lists, k = (n + W * q - 1) / (W * q);
-    uint64_t mine = 0, head[kMergeLists / kMergeThreads];
-#pragma unroll
-    for (int u = 0; u < kMergeLists / kMergeThreads; u++) {
-        const int i = u * kMergeThreads + lane * kMergeWarps + warp;
-        double c;
+    const int mylist = lane * kMergeWarps + warp;
+    uint64_t head = 0;
+    {
         int64_t at;
-        head[u] = i < lists && entry(i, q - 1, c, at) ? ord64(c) : 0;
-        mine = max(mine, head[u]);
+        if (mylist < lists) entry(mylist, q - 1, head, at);
     }
-    uint64_t kth = 0;
+    uint64_t mine = head, kth = 0;
     for (int r = 0; r < k; r++) {
         kth = warp_max64(mine);
         const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
@@ -479,57 +560,56 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
     if (lane == 0) M.kth[warp] = kth;
     __syncthreads();
-    uint64_t thr = M.kth[0];
-    for (int w = 1; w < W; w++) thr = min(thr, M.kth[w]);
-    // sharper: the ceil(n / q)-th of the heads that pass (beams differ: a warp may hold poor ones only)
-#pragma unroll
-    for (int u = 0; u < kMergeLists / kMergeThreads; u++)
-        if (head[u] && head[u] >= thr) M.key[atomicAdd(&M.count, 1)] = head[u];
-    if (tid == 0) M.sharp = 0;
+    uint64_t thr = ~warp_max64(lane < W ? ~M.kth[lane] : 0);
+    // sharper: the ceil(n / q)-th of the heads that pass (beams differ: a warp may hold poor ones only); eight threads
+    // count for a head
+    if (head && head >= thr) M.key[atomicAdd(&M.count, 1)] = head;
     __syncthreads();
     const int heads = M.count, want = (n + q - 1) / q;
-    for (int i = tid; i < heads; i += kMergeThreads) {
-        const uint64_t key = M.key[i];
+    for (int i0 = 0; i0 < heads; i0 += kMergeThreads / 8) {
+        const int i = i0 + (tid >> 3);
+        const uint64_t key = i < heads ? M.key[i] : 0;
         int above = 0, same = 0;
-#pragma unroll 8
-        for (int j = 0; j < heads; j++) above += M.key[j] > key, same += M.key[j] == key;
-        if (above < want && above + same >= want) M.sharp = key;  // (all that write it write the same)
+#pragma unroll 4
+        for (int j = tid & 7; j < heads; j += 8) above += M.key[j] > key, same += M.key[j] == key;
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) {
+            above += __shfl_xor_sync(0xffffffffu, above, off);
+            same += __shfl_xor_sync(0xffffffffu, same, off);
+        }
+        if (i < heads && above < want && above + same >= want) M.sharp = key;  // (all that write it write the same)
     }
     __syncthreads();
     thr = max(thr, M.sharp);
     // the lists whose head passes, then all of their entries at once
     if (tid == 0) M.count = M.passing = 0;
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kMergeLists / kMergeThreads; u++) {
-        const int i = u * kMergeThreads + lane * kMergeWarps + warp;
-        if (i < lists && (q > 1 || (head[u] && head[u] >= thr))) M.list[atomicAdd(&M.passing, 1)] = (uint16_t)i;
-    }
+    if (mylist < lists && (q > 1 || (head && head >= thr))) M.list[atomicAdd(&M.passing, 1)] = (uint16_t)mylist;
     __syncthreads();
     const int pairs = M.passing * n;
     for (int i = tid; i < pairs; i += kMergeThreads) {
-        double c;
+        uint64_t key;
         int64_t at;
         const int l = i / n;
-        if (entry(M.list[l], i - l * n, c, at) && ord64(c) >= thr) {
+        if (entry(M.list[l], i - l * n, key, at) && key >= thr) {
             const int p = atomicAdd(&M.count, 1);
-            if (p < kMergeBuf) M.key[p] = ord64(c), M.at[p] = at;
+            if (p < kMergeBuf) M.key[p] = key, M.at[p] = at;
         }
     }
     __syncthreads();
     const int total = M.count;
-    auto write = [&](int r, double c, int64_t at) {
+    auto write = [&](int r, uint64_t key, int64_t at) {
         const int64_t o = (int64_t)g * n + r;
-        out_scores[o] = (float)c;
+        out_scores[o] = wild ? (float)unord64(key) : unord32((uint32_t)(key >> 32));
         parents[o] = (int)(at >> 32);
         tokens[o] = (int)(uint32_t)at;
     };
-    int found = min(total, n);
+    const int found = min(total, n);
     if (total <= kMergeBuf) {
         // four threads count for a candidate
+        const int part4 = tid & 3, per = (total + 3) / 4, j0 = min(part4 * per, total), j1 = min(j0 + per, total);
         for (int i0 = 0; i0 < total; i0 += kMergeThreads / 4) {
-            const int i = i0 + (tid >> 2), part4 = tid & 3, per = (total + 3) / 4;
-            const int j0 = min(part4 * per, total), j1 = min(j0 + per, total);
+            const int i = i0 + (tid >> 2);
             uint64_t key = 0;
             int64_t at = 0;
             int r = 0;
@@ -539,34 +619,33 @@ __global__ void __launch_bounds__(kMergeThreads)
             }
             r += __shfl_xor_sync(0xffffffffu, r, 1);
             r += __shfl_xor_sync(0xffffffffu, r, 2);
-            if (i < total && part4 == 0 && r < n) write(r, unord64(key), at);
+            if (i < total && part4 == 0 && r < n) write(r, key, at);
         }
     } else {
         // too many equal candidates: n rounds of taking the best head of the lists
-        for (int i = tid; i < lists; i += kMergeThreads) M.next[i] = 0;
+        if (tid < lists) M.next[tid] = 0;
         __syncthreads();
+        auto better = [](uint64_t key, int64_t at, uint64_t bkey, int64_t bat) {
+            return key > bkey || (key == bkey && at < bat);
+        };
         for (int r = 0; r < n; r++) {
-            double c = dninf;
+            uint64_t key = 0;
             int64_t at = INT64_MAX;
-            int li = -1;
-            for (int i = tid; i < lists; i += kMergeThreads) {
-                double ec;
-                int64_t eat;
-                if (entry(i, M.next[i], ec, eat) && better(ec, eat, c, at)) c = ec, at = eat, li = i;
-            }
+            if (!(tid < lists && entry(tid, M.next[tid], key, at))) key = 0, at = INT64_MAX;
+            int li = tid;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) {
-                const double oc = __shfl_xor_sync(0xffffffffu, c, off);
+                const uint64_t ok = __shfl_xor_sync(0xffffffffu, key, off);
                 const int64_t oat = __shfl_xor_sync(0xffffffffu, at, off);
                 const int ol = __shfl_xor_sync(0xffffffffu, li, off);
-                if (better(oc, oat, c, at)) c = oc, at = oat, li = ol;
+                if (better(ok, oat, key, at)) key = ok, at = oat, li = ol;
             }
-            if (lane == 0) M.wc[warp] = c, M.wat[warp] = at, M.wlist[warp] = li;
+            if (lane == 0) M.wkey[warp] = key, M.wat[warp] = at, M.wlist[warp] = li;
             __syncthreads();
             if (tid == 0) {
                 for (int w = 1; w < kMergeWarps; w++)
-                    if (better(M.wc[w], M.wat[w], c, at)) c = M.wc[w], at = M.wat[w], li = M.wlist[w];
-                write(r, c, at);  // (there are more than n)
+                    if (better(M.wkey[w], M.wat[w], key, at)) key = M.wkey[w], at = M.wat[w], li = M.wlist[w];
+                write(r, key, at);  // (there are more than n)
                 M.next[li]++;
             }
             __syncthreads();
@@ -729,7 +808,7 @@ int sel_slices(int rows, int V) {
     const int len = sel_len(rows, V);
     return (V + len - 1) / len;
 }
-static_assert(kSelCtas + kMaxBeams <= kMergeLists, "a group's lists");
+static_assert(kSelCtas <= kMergeThreads && kMaxBeams <= kMergeThreads, "a thread for each of a group's lists");
 
 template <int VPT>
 const void *slice_kernel(bool vec) {
@@ -786,7 +865,7 @@ qlin_status qlin_beam_select(const float *logits, int64_t row_stride, const floa
                                     "beam_slice_kernel"))
         return st;
     void *a1[] = {(void *)&w.part, (void *)&w.cand, (void *)&scores, (void *)&finished, (void *)&eos, (void *)&beams,
-                  (void *)&vocab, (void *)&S, (void *)&n_out, (void *)&out_scores, (void *)&parents, (void *)&tokens};
+                  (void *)&S, (void *)&n_out, (void *)&out_scores, (void *)&parents, (void *)&tokens};
     const size_t smem = sizeof(MergeSmem);
     blocks_per_sm((const void *)beam_merge_kernel, smem);  // raises the dynamic shared-memory limit once
     return launch_pdl((const void *)beam_merge_kernel, dim3(n_groups), dim3(kMergeThreads), smem, (cudaStream_t)stream,
