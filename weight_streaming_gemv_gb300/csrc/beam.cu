@@ -68,6 +68,7 @@ struct SelPart {  // a slice's part of its beam's sum of exponentials
     int count;      // candidates listed
 };
 static_assert(sizeof(SelPart) == 16, "read as one vector");
+constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654323148236e-9f;
 constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.9259629911266175e-8f;
 __device__ __forceinline__ bool sel_wide(float m) { return !(fabsf(m) <= 16777216.0f); }
 __device__ __forceinline__ float sel_exp(float m) { return ceilf(__fmul_rn(m, kLog2eHi)); }
@@ -245,9 +246,12 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
         int tile = 0;
         for (int at = v0; at < v1 && !over; at += kTile, tile++) {
             if (at + kTile < v1) load(at + kTile, nx);
-            float tmax = ninf;
+            float tmax = ninf, gmax[VPT / 4];
 #pragma unroll
-            for (int j = 0; j < VPT; j++) tmax = fmaxf(tmax, v[j]);
+            for (int u = 0; u < VPT / 4; u++) {
+                gmax[u] = fmaxf(fmaxf(v[4 * u], v[4 * u + 1]), fmaxf(v[4 * u + 2], v[4 * u + 3]));
+                tmax = fmaxf(tmax, gmax[u]);
+            }
             if (tmax > m) {
                 m = tmax;
                 // a whole-number scale at or above the largest term's exponent
@@ -282,18 +286,21 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
                 }
             }
             const float low = unord32(thr);
-            if (tmax >= low && !over) {  // (NaN is not)
-                int p = 0;
+            if (tmax >= low && !over)  // (NaN is not)
 #pragma unroll
-                for (int j = 0; j < VPT; j++) p += v[j] >= low;
-                p = atomicAdd(&buf.count, p);
+                for (int u = 0; u < VPT / 4; u++)  // (a warp passes over the fours that none of its threads has one in)
+                    if (gmax[u] >= low) {
+                        int p = 0;
 #pragma unroll
-                for (int j = 0; j < VPT; j++)
-                    if (v[j] >= low) {
-                        if (p < kSelBuf) buf.key[p] = cand_key(v[j], (uint32_t)(at + index(j)));
-                        p++;
+                        for (int j = 4 * u; j < 4 * u + 4; j++) p += v[j] >= low;
+                        p = atomicAdd(&buf.count, p);
+#pragma unroll
+                        for (int j = 4 * u; j < 4 * u + 4; j++)
+                            if (v[j] >= low) {
+                                if (p < kSelBuf) buf.key[p] = cand_key(v[j], (uint32_t)(at + index(j)));
+                                p++;
+                            }
                     }
-            }
             if (careful) {
                 __syncthreads();
                 if (buf.count > kSelBuf) {
@@ -388,27 +395,35 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
     return (uint64_t)hi << 32 | lo;
 }
 
-// log s to about 1e-12, from s = 2^k f with f in [2/3, 4/3] and log f =
-// 2 (w + w^3 / 3 + w^5 / 5 + ...), w = (f - 1) / (f + 1): |w| <= 1/5, so the
-// first term left out is below 1e-12 of the sum.  (The sums it is taken of are
-// good to 1e-7 of their largest term.)  s is 0, positive or NaN.
-__device__ __forceinline__ double log_of_sum(double s) {
-    if (!(s > 0.0)) return s == 0.0 ? -(double)__int_as_float(0x7f800000) : s;
-    int k = (__double2hiint(s) >> 20) - 1023;
-    double f = s * __hiloint2double((1023 - k) << 20, 0);
-    if (f > 4.0 / 3.0) f *= 0.5, k++;
-    const double num = f - 1.0, den = f + 1.0;
-    const double r = (double)(1.0f / (float)den), w = num * fma(r, fma(-den, r, 1.0), r);
-    const double z = w * w, z2 = z * z, z4 = z2 * z2;
-    const double p = fma(z4, fma(z2, fma(z, 1.0 / 15.0, 1.0 / 13.0), fma(z, 1.0 / 11.0, 1.0 / 9.0)),
-                         fma(z2, fma(z, 1.0 / 7.0, 1.0 / 5.0), fma(z, 1.0 / 3.0, 1.0)));
-    return fma((double)k, 0.69314718055994530942, 2.0 * w * p);
+// log (h + l) as a pair, to about 1e-9 (the sums it is taken of are good to
+// 1e-7 of their largest term): h + l = 2^k f with f in [2/3, 4/3] and log f =
+// 2 (w + w^3 / 3 + w^5 / 5 + ...), w = (f - 1) / (f + 1).  |w| <= 1/5: the
+// first term left out is below 1e-9, and behind w itself, which is a pair, one
+// float's digits do.  h is 0, positive or NaN.
+__device__ __forceinline__ float2 log_of_sum(float h, float l) {
+    if (!(h > 0.0f)) return make_float2(h == 0.0f ? -__int_as_float(0x7f800000) : h, 0.0f);
+    int k = (int)(__float_as_uint(h) >> 23) - 127;
+    float sc = pow2i(-k);
+    if (__fmul_rn(h, sc) > 1.3333334f) sc = __fmul_rn(sc, 0.5f), k++;
+    const float f = __fmul_rn(h, sc), fl = __fmul_rn(l, sc);
+    const float nh = __fsub_rn(f, 1.0f);  // (exact)
+    float dh = f, dl = fl;
+    pair_add(dh, dl, 1.0f, 0.0f);
+    const float w = __fdiv_rn(nh, dh);
+    const float wl = __fdividef(__fmaf_rn(-w, dl, __fadd_rn(__fmaf_rn(-w, dh, nh), fl)), dh);
+    const float z = __fmul_rn(w, w);
+    float t = 1.0f / 13;
+#pragma unroll
+    for (int c = 11; c >= 3; c -= 2) t = __fmaf_rn(z, t, 1.0f / (float)c);
+    t = __fmul_rn(z, t);
+    float rh = 2.0f * w, rl = 2.0f * __fmaf_rn(w, t, wl);
+    const float kf = (float)k, ph = __fmul_rn(kf, kLn2Hi);
+    pair_add(rh, rl, ph, __fmaf_rn(kf, kLn2Lo, __fmaf_rn(kf, kLn2Hi, -ph)));
+    return make_float2(rh, rl);
 }
 
 struct MergeSmem {
-    double sum[kMaxBeams];  // of a beam's exponentials
-    double lse[kMaxBeams];  // its log, less top
-    float2 lse2[kMaxBeams];  // that as a pair
+    float2 lse[kMaxBeams];  // a beam's sum of exponentials, then its log less top
     float top[kMaxBeams];   // the beam's largest logit
     float base[kMaxBeams];  // its score
     int kind[kMaxBeams];    // 0: dead, 1: live, 2: finished
@@ -422,9 +437,51 @@ struct MergeSmem {
     uint64_t key[kMergeBuf];
     int64_t at[kMergeBuf];
     uint64_t stage[kMergeStage];
+    uint64_t heads[kMergeThreads + 32];  // (an odd stride between a warp's)
     uint16_t list[kMergeThreads];
+    uint8_t beam[kMergeThreads];  // of each list
     uint8_t next[kMergeThreads];  // the next entry of each list
 };
+
+// Entry h of list i as a whole number in the order of the candidates (key 0:
+// there is none; NaN gives nothing of this beam), and its place beam << 32 |
+// word.  One copy of the code: the kernel runs once through little data, and
+// fetching instructions is much of its time.
+struct MergeEntry {
+    uint64_t key;
+    int64_t at;
+};
+__device__ __noinline__ MergeEntry merge_entry(const MergeSmem &M, const uint64_t *list, int i, int h, int eos) {
+    MergeEntry e{0, 0};
+    const int b = M.beam[i], kind = M.kind[b];
+    const float ninf = -__int_as_float(0x7f800000);
+    if (kind == 1) {
+        if (h >= M.part[i].count) return e;
+        const uint64_t k = list[h];
+        const float x = unord32((uint32_t)(k >> 32)), top = M.top[b], base = M.base[b];
+        const float2 lse = M.lse[b];
+        e.at = (int64_t)b << 32 | (uint32_t)~(uint32_t)k;
+        if (M.wild) {
+            const double c = (double)base + (((double)x - (double)top) - ((double)lse.x + (double)lse.y));
+            if (c > (double)ninf) e.key = ord64(c);
+        } else {
+            float c = x, l = 0.0f;
+            pair_add(c, l, -top, 0.0f);
+            pair_add(c, l, -lse.x, -lse.y);
+            pair_add(c, l, base, 0.0f);
+            // the nearest float and the rest of it (+ 0: no negative zeros)
+            float hi = l, lo = 0.0f;
+            pair_add(hi, lo, c, 0.0f);
+            if (fabsf(lo) < fabsf(hi) * 0x1p-53f) lo = 0.0f;  // (candidates near the type's lowest value are equal)
+            if (hi > ninf) e.key = (uint64_t)ord32(__fadd_rn(hi, 0.0f)) << 32 | ord32(__fadd_rn(lo, 0.0f));
+        }
+    } else if (kind == 2 && h == 0 && (i == 0 || M.beam[i - 1] != b)) {
+        const float c = __fadd_rn(M.base[b], 0.0f);
+        e.at = (int64_t)b << 32 | (uint32_t)eos;
+        if (c > ninf) e.key = M.wild ? ord64((double)c) : (uint64_t)ord32(c) << 32 | ord32(0.0f);
+    }
+    return e;
+}
 
 // One CTA per group: lse of every live beam, then the n best of the beams'
 // sorted lists (S lists per live beam, one entry for a finished one).  What it
@@ -456,6 +513,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             const int4 p = __ldcg((const int4 *)&part[tid]);
             M.part[tid] = SelPart{__int_as_float(p.x), __int_as_float(p.y), __int_as_float(p.z), p.w};
         }
+        if (tid < lists) M.beam[tid] = (uint8_t)(tid / S);
         if (tid < beams) {
             const float score = scores[g * beams + tid];
             M.base[tid] = score;
@@ -473,85 +531,58 @@ __global__ void __launch_bounds__(kMergeThreads)
         const SelPart *p = M.part + b * S;
         float big = ninf;
         for (int i = lane; i < S; i += 32) big = fmaxf(big, p[i].m);
-        big = warp_max(big);
-        double sum;
+        big = unord32(__reduce_max_sync(0xffffffffu, ord32(big)));
+        float h = 0.0f, l = 0.0f;
         if (!sel_wide(big)) {
-            float h = 0.0f, l = 0.0f;
             for (int i = lane; i < S; i += 32) {
                 // (a wide slice is far below the others here: nothing, or NaN)
                 const float sh = sel_wide(p[i].m) ? ninf : sel_exp(p[i].m) - sel_exp(big);
                 const float f = sh >= -126.0f ? pow2i((int)sh) : 0.0f;
                 pair_add(h, l, __fmul_rn(p[i].sum, f), __fmul_rn(p[i].lo, f));
             }
-            pair_warp_sum(h, l);
-            sum = (double)h + (double)l;
         } else {
-            sum = 0.0;
             for (int i = lane; i < S; i += 32) {
-                const float mi = p[i].m;
-                const double si = (double)p[i].sum + (double)p[i].lo;  // (0, or NaN, where there is no logit)
-                sum += mi > ninf ? si * exp((sel_wide(mi) ? (double)mi : (double)sel_exp(mi) * 0.69314718055994530942) -
-                                            (double)big)
-                                 : si;
+                // (0, or NaN, where there is no logit)
+                const double mi = (double)p[i].m, si = (double)p[i].sum + (double)p[i].lo;
+                const double v = p[i].m > ninf
+                                     ? si * exp((sel_wide(p[i].m) ? mi : (double)sel_exp(p[i].m) * 0.69314718055994530942) -
+                                                (double)big)
+                                     : si;
+                pair_add(h, l, (float)v, (float)(v - (double)(float)v));
             }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         }
-        if (lane == 0) M.sum[b] = sum, M.top[b] = big;
+        pair_warp_sum(h, l);
+        if (lane == 0) {
+            float hi = l, lo = 0.0f;
+            pair_add(hi, lo, h, 0.0f);
+            M.lse[b] = make_float2(hi, lo), M.top[b] = big;
+        }
     }
     __syncthreads();
     if (tid < beams && M.kind[tid] == 1) {  // (one warp or two)
         const float big = M.top[tid];
+        float2 l = log_of_sum(M.lse[tid].x, M.lse[tid].y);
         const bool wide = sel_wide(big);
-        const double l = log_of_sum(M.sum[tid]) + (wide ? 0.0 : (double)sel_exp(big) * 0.69314718055994530942 - (double)big);
-        const float hi = (float)l;
+        if (!wide) {
+            const float e = sel_exp(big), p = __fmul_rn(e, kLn2Hi);
+            pair_add(l.x, l.y, p, __fmaf_rn(e, kLn2Lo, __fmaf_rn(e, kLn2Hi, -p)));
+            pair_add(l.x, l.y, -big, 0.0f);
+        }
         M.lse[tid] = l;
-        M.lse2[tid] = make_float2(hi, (float)(l - (double)hi));
         if (wide || !(fabsf(M.base[tid]) <= 1e30f)) M.wild = 1;
     }
     __syncthreads();
-    const bool wild = M.wild;
-    // entry h of list i as a whole number in the order of the candidates (0: there is none; NaN gives nothing of this
-    // beam), and its place beam << 32 | word
-    auto entry = [&](int i, int h, uint64_t &key, int64_t &at) -> bool {
-        const int b = i / S, kind = M.kind[b];
-        key = 0;
-        if (kind == 1) {
-            if (h >= M.part[i].count) return false;
-            const uint64_t k = staged ? M.stage[i * n + h] : __ldcg(&cand[(int64_t)i * n + h]);
-            const float x = unord32((uint32_t)(k >> 32));
-            at = (int64_t)b << 32 | (uint32_t)~(uint32_t)k;
-            if (wild) {
-                const double c = (double)M.base[b] + (((double)x - (double)M.top[b]) - M.lse[b]);
-                if (c > (double)ninf) key = ord64(c);
-            } else {
-                float c = x, l = 0.0f;
-                pair_add(c, l, -M.top[b], 0.0f);
-                pair_add(c, l, -M.lse2[b].x, -M.lse2[b].y);
-                pair_add(c, l, M.base[b], 0.0f);
-                // the nearest float and the rest of it (+ 0: no negative zeros)
-                float hi = l, lo = 0.0f;
-                pair_add(hi, lo, c, 0.0f);
-                if (fabsf(lo) < fabsf(hi) * 0x1p-53f) lo = 0.0f;  // (candidates near the type's lowest value are equal)
-                if (hi > ninf) key = (uint64_t)ord32(__fadd_rn(hi, 0.0f)) << 32 | ord32(__fadd_rn(lo, 0.0f));
-            }
-        } else if (kind == 2 && h == 0 && i == b * S) {
-            const float c = __fadd_rn(M.base[b], 0.0f);
-            at = (int64_t)b << 32 | (uint32_t)eos;
-            if (c > ninf) key = wild ? ord64((double)c) : (uint64_t)ord32(c) << 32 | ord32(0.0f);
-        }
-        return key != 0;
+    auto entry = [&](int i, int h) {
+        return merge_entry(M, staged ? M.stage + i * n : cand + (int64_t)i * n, i, h, eos);
     };
     // The lists are dealt out to the warps evenly.  With the q-th entries of
     // ceil(n / (warps q)) lists in every warp no smaller than a threshold, n
     // candidates are not.
     const int W = min(kMergeWarps, lists), q = (n + lists - 1) / lists, k = (n + W * q - 1) / (W * q);
     const int mylist = lane * kMergeWarps + warp;
-    uint64_t head = 0;
-    {
-        int64_t at;
-        if (mylist < lists) entry(mylist, q - 1, head, at);
-    }
+    M.heads[tid + tid / kMergeWarps] = tid < lists ? entry(tid, q - 1).key : 0;
+    __syncthreads();
+    const uint64_t head = M.heads[mylist + lane];
     uint64_t mine = head, kth = 0;
     for (int r = 0; r < k; r++) {
         kth = warp_max64(mine);
@@ -588,19 +619,18 @@ __global__ void __launch_bounds__(kMergeThreads)
     __syncthreads();
     const int pairs = M.passing * n;
     for (int i = tid; i < pairs; i += kMergeThreads) {
-        uint64_t key;
-        int64_t at;
         const int l = i / n;
-        if (entry(M.list[l], i - l * n, key, at) && key >= thr) {
+        const MergeEntry e = entry(M.list[l], i - l * n);
+        if (e.key && e.key >= thr) {
             const int p = atomicAdd(&M.count, 1);
-            if (p < kMergeBuf) M.key[p] = key, M.at[p] = at;
+            if (p < kMergeBuf) M.key[p] = e.key, M.at[p] = e.at;
         }
     }
     __syncthreads();
     const int total = M.count;
     auto write = [&](int r, uint64_t key, int64_t at) {
         const int64_t o = (int64_t)g * n + r;
-        out_scores[o] = wild ? (float)unord64(key) : unord32((uint32_t)(key >> 32));
+        out_scores[o] = M.wild ? (float)unord64(key) : unord32((uint32_t)(key >> 32));
         parents[o] = (int)(at >> 32);
         tokens[o] = (int)(uint32_t)at;
     };
@@ -629,9 +659,9 @@ __global__ void __launch_bounds__(kMergeThreads)
             return key > bkey || (key == bkey && at < bat);
         };
         for (int r = 0; r < n; r++) {
-            uint64_t key = 0;
-            int64_t at = INT64_MAX;
-            if (!(tid < lists && entry(tid, M.next[tid], key, at))) key = 0, at = INT64_MAX;
+            const MergeEntry e = tid < lists ? entry(tid, M.next[tid]) : MergeEntry{0, 0};
+            uint64_t key = e.key;
+            int64_t at = key ? e.at : INT64_MAX;
             int li = tid;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) {
