@@ -96,6 +96,24 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// two at once
+__device__ __forceinline__ uint64_t bits2(float2 v) {
+    return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x);
+}
+__device__ __forceinline__ float2 floats2(uint64_t b) {
+    return make_float2(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return floats2(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return floats2(d);
+}
+
 __device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *finished, int row) {
     return !(finished && finished[row]) && scores[row] > -__int_as_float(0x7f800000);
 }
@@ -162,8 +180,8 @@ __device__ __forceinline__ void sel_rank(const SelBuf &b, int c, int n, uint64_t
 
 // A value that n of the block's threads' `mine` are no smaller than: with
 // k = ceil(n / warps) and j = ceil(n / k), the j-th largest of the warps' k-th
-// largest.  To be called by all warps, with a barrier behind it before wkth
-// is written again.
+// largest.  A warp's k-th largest only grows, so any of its
+// published values will do (one of an earlier walk over the slice would too).
 __device__ __forceinline__ void sel_kth(uint32_t mine, int k, uint32_t *wkth) {
     const int lane = threadIdx.x & 31;
     uint32_t kth = 0;
@@ -172,14 +190,18 @@ __device__ __forceinline__ void sel_kth(uint32_t mine, int k, uint32_t *wkth) {
         const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
         if (lane == __ffs(who) - 1) mine = 0;
     }
-    if (lane == 0) wkth[threadIdx.x >> 5] = kth;
+    if (lane == 0) *(volatile uint32_t *)&wkth[threadIdx.x >> 5] = kth;
 }
 __device__ __forceinline__ uint32_t sel_threshold(const uint32_t *wkth, int j) {
     const int own = threadIdx.x & (kSelWarps - 1);
-    const uint32_t mine = wkth[own];
+    // (other warps may be writing: each value is read once)
+    const uint32_t mine = *(volatile const uint32_t *)&wkth[own];
     int above = 0;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; w++) above += wkth[w] > mine || (wkth[w] == mine && w < own);
+    for (int w = 0; w < kSelWarps; w++) {
+        const uint32_t other = __shfl_sync(0xffffffffu, mine, w);
+        above += other > mine || (other == mine && w < own);
+    }
     const uint32_t who = __ballot_sync(0xffffffffu, above == j - 1);
     return __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
 }
@@ -234,6 +256,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     int e, c;
     uint32_t thr;  // n values of the slice so far are no smaller (minus infinity is no candidate)
     const int k = (n + kSelWarps - 1) / kSelWarps, jw = (n + k - 1) / k;  // k at most 16
+    const bool many = n > 32;
     if (tid == 0) last.count = 0;
     // Once without looking at the buffer after every tile; where that let it
     // overflow (many equal values) once more, carefully.
@@ -258,18 +281,24 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
                 const int ne = (int)fminf(fmaxf(sel_exp(m), -1e8f), 1e8f);
                 if (ne > e) sum *= pow2i(max(e - ne, -126)), e = ne;
             }
-            const float ef = (float)e;
+            // x log2(e) - e with log2(e) in two parts: the rounding of one would be the same for a whole beam (NaN
+            // stays in the sum, plus infinity makes it infinite, nothing else does)
+            const float2 ef = make_float2(-(float)e, -(float)e);
+            float2 acc = make_float2(sum, 0.0f);
 #pragma unroll
-            for (int j = 0; j < VPT; j++) {
-                // x log2(e) - e with log2(e) in two parts: the rounding of one
-                // would be the same for a whole beam (NaN stays in the sum, plus
-                // infinity makes it infinite, nothing else does)
-                sum += ex2_approx(__fmaf_rn(v[j], kLog2eLo, __fmaf_rn(v[j], kLog2eHi, -ef)));
+            for (int j = 0; j < VPT; j += 2) {
+                const float2 y = fma2(make_float2(v[j], v[j + 1]), make_float2(kLog2eLo, kLog2eLo),
+                                      fma2(make_float2(v[j], v[j + 1]), make_float2(kLog2eHi, kLog2eHi), ef));
+                acc = add2(acc, make_float2(ex2_approx(y.x), ex2_approx(y.y)));
             }
+            sum = __fadd_rn(acc.x, acc.y);
             // the threshold: from the threads' maxima so far, after tiles 1, 2, 4, 8, ... (a tile's share of the values
-            // is halved from one to the next, so each part of the slice leaves about as many candidates)
-            if (careful || (tile & (tile + 1)) == 0) {
-                sel_kth(ord32(m), k, wkth);
+            // is halved from one to the next, so each part of the slice leaves about as many candidates).  What a warp
+            // last published holds from then on, so without many candidates only the first tile needs a barrier, and
+            // the tile behind each takes in what the other warps published late.
+            const bool publish = careful || (tile & (tile + 1)) == 0;
+            if (publish) sel_kth(ord32(m), k, wkth);
+            if (publish && (careful || tile == 0 || many)) {
                 __syncthreads();
                 thr = max(thr, sel_threshold(wkth, jw));
                 c = buf.count;
@@ -284,6 +313,8 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
                     if (tid == 0) buf.count = c;
                     __syncthreads();
                 }
+            } else if (publish || (tile & (tile - 1)) == 0) {
+                thr = max(thr, sel_threshold(wkth, jw));
             }
             const float low = unord32(thr);
             if (tmax >= low && !over)  // (NaN is not)
