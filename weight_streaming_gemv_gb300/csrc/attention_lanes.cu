@@ -70,7 +70,6 @@ constexpr int kMaxLanes = 4096;
 constexpr int kStatusBadLane = 1;
 constexpr int kMaxCtas = 160;  // the workspace holds two partial tiles for each
 constexpr int kChunk = 128;    // keys per unit (MMA M)
-constexpr int kSetup = 2;      // units that a tile's start is counted as (its rows' q, the first scores, the outputs)
 constexpr float kNoKey = -1e30f;  // the running maximum of a row that has seen no key
 
 struct AlArgs {
@@ -86,7 +85,7 @@ struct AlArgs {
 // (stream 0: prompts, stream 1: the lanes' own caches).  Its chunks of that
 // sequence's rows are 0 .. nsink - 1 and then cfirst, cfirst + 1, ...
 struct __align__(16) AlTile {
-    int64_t unit0;  // its first unit; units go (KV head, head block, kSetup and then the chunks)
+    int64_t unit0;  // its first unit; units go (KV head, head block, AlDims::setup and then the chunks)
     uint16_t lane0;
     uint8_t nl, stream;
     int nch, nsink, cfirst;
@@ -124,6 +123,7 @@ struct AlDims {
     int streams;  // 1: own caches only, 2
     int grid;
     int merge;  // (lane, head)s per block of the merging kernel
+    int setup;  // units that a tile's start is counted as (its rows' q, the first scores, the outputs)
     float c;    // log2(e) / sqrt(hd)
 };
 
@@ -152,7 +152,7 @@ __device__ __forceinline__ int64_t unit_of(int64_t units, int b, int grid, const
 }
 
 __device__ __forceinline__ int64_t tile_units(int nch, const AlArgs &A, const AlDims &D) {
-    return nch ? (int64_t)(nch + kSetup) * A.n_kv * D.HB : 0;
+    return nch ? (int64_t)(nch + D.setup) * A.n_kv * D.HB : 0;
 }
 
 struct PlanRed {
@@ -374,14 +374,14 @@ struct Walker {
     __device__ __forceinline__ void next(AlPiece &p, const AlArgs &A, const AlDims &D) {
         while (u < hi) {
             while (u >= at->unit0 + tile_units(at->nch, A, D)) at++;
-            const int nch = at->nch, per = nch + kSetup;
+            const int nch = at->nch, per = nch + D.setup;
             const int64_t r = u - at->unit0;
             const int64_t sub = r < per ? 0 : (r >> 31) ? r / per : (int64_t)((uint32_t)r / (uint32_t)per);
             const int v0 = (int)(r - sub * per), v1 = (int)min((int64_t)per, v0 + (hi - u));
             u += v1 - v0;
-            if (v1 <= kSetup) continue;  // the next CTA starts it
+            if (v1 <= D.setup) continue;  // the next CTA starts it
             const int kvh = D.HB == 1 ? (int)sub : (int)(sub / D.HB), hb = (int)sub - kvh * D.HB;
-            const int c0 = max(v0 - kSetup, 0), c1 = v1 - kSetup;
+            const int c0 = max(v0 - D.setup, 0), c1 = v1 - D.setup;
             const int over = c0 < turn ? c0 : c0 % turn;
             p.first = c0 + (over && turn - over < c1 - c0 ? turn - over : 0), p.c1 = c1;
             p.nsink = at->nsink, p.cfirst = at->cfirst;
@@ -507,15 +507,41 @@ __device__ __forceinline__ void al_tma(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 
+__device__ __forceinline__ void al_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// whether the phase is over by now
+__device__ __forceinline__ bool al_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait that also ends when another role gave up.
-__device__ __forceinline__ bool al_wait(uint64_t *bar, uint32_t parity, int *abort) {
-    if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool al_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool al_wait_at(uint32_t bar, uint32_t parity, int *abort) {
+    if (al_try(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (uint32_t i = 0; i < (1u << 26); i++) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (al_try(bar, parity)) return true;
         if ((i & 63u) == 63u && (*(volatile int *)abort || global_ns() - t0 > kWaitLimitNs)) return false;
     }
     return false;
+}
+__device__ __forceinline__ bool al_wait(uint64_t *bar, uint32_t parity, int *abort) {
+    return al_wait_at(smem_addr(bar), parity, abort);
 }
 
 // Two values as three pairs of bf16 terms (the first value in the low half).
@@ -890,15 +916,30 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         }
         if (warp == C::kMma && al_elect()) {
             // ------------------------------------------------------ the MMAs
+            // One thread paces a chunk.  What it needs is in registers, whether the next slice has landed is asked while
+            // the products of this one are issued (the answer takes 70 cycles), and a chunk is one run of instructions:
+            // a jump back takes 200 cycles here, the other warps having pushed its target out of the instruction cache.
             PieceRef ref;
-            RingPos at;
             int it = 0;           // chunks so far
             uint32_t fixes = 0;   // slices of V handed to the first warpgroup so far
             bool ok = true;
             const uint32_t qs_a = smem_addr(qs), ps_a = smem_addr(ps);
             // (K slices have no leading byte offset to speak of, V's 64-dim blocks are 8 KB apart)
             const uint32_t ring_d = al_desc_lo(smem_addr(ring), 16), vlbo = ((8192u - 16u) >> 4) << 16;
-            const uint32_t hi128 = al_desc_hi(1024, 2), hip = al_desc_hi(512, 4);
+            const uint32_t hi128 = al_desc_hi(1024, 2), hip = al_desc_hi(512, 4), qstep = (uint32_t)L.qslice >> 4;
+            const uint32_t full0 = smem_addr(&S.full[0]), empty0 = smem_addr(&S.empty[0]) - full0;
+            const uint32_t end = full0 + 8u * slots, s_free = smem_addr(&S.s_free), p_ready = smem_addr(&S.p_ready);
+            uint32_t full = full0, par = 0, slot_d = ring_d;  // the next slice: its barrier, its phase, its place
+            bool landed = false;                              // it has
+            // the barrier to commit to when the slice's products are issued; on to the next one
+            auto step = [&]() {
+                const uint32_t done = full + empty0;
+                full += 8, slot_d += C::kSlot / 16;
+                if (full == end) full = full0, slot_d = ring_d, par ^= 1u;
+                landed = al_test(full, par);
+                return done;
+            };
+            auto arrived = [&]() { return landed || al_wait_at(full, par, &S.abort); };
             while (ok) {
                 const AlPiece *p = ref.next(S);
                 if (!(ok = p != nullptr)) break;
@@ -914,64 +955,70 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     ids[t] = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 4) << 24 | ((3 - t) * nr >> 3) << 17;
                     idp[t] = ids[t] | (1u << 15) | (1u << 16);
                 }
-                if (!(ok = al_wait(&S.q_ready, (uint32_t)ref.k & 1u, &S.abort))) break;
                 const int c1 = p->c1, nsink = p->nsink, skip = p->cfirst - nsink;
+                const int all_lo = p->all_lo, all_hi = p->all_hi, sk = p->sk;
                 int c = p->first;
-                bool edge[2] = {false, false};  // of the chunk whose products are next
+                uint32_t edge = 0, edge_next = 0;  // bit kh: of half kh of the chunk whose products are next; of the one behind
+                if (!(ok = al_wait(&S.q_ready, (uint32_t)ref.k & 1u, &S.abort))) break;
                 for (int i = 0; ok && i <= n; i++) {
                     if (i < n) {
-                        if (it + i > 0 && !(ok = al_wait(&S.s_free, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
+                        const bool free = it + i == 0 || al_test(s_free, (uint32_t)(it + i - 1) & 1u);
+                        // (of chunk i, while that is on its way)
+                        const int row = (c < nsink ? c : c + skip) * kChunk;
+                        if (++c == c1) c -= n;
+                        auto edge_in = [&](int a, int b) { return !(b <= all_hi && (a > all_lo || b < sk)); };
+                        edge = edge_next;
+                        edge_next = (uint32_t)edge_in(row, row + 63) | (uint32_t)edge_in(row + 64, row + 127) << 1;
+                        if (!free && !(ok = al_wait_at(s_free, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
                         uint32_t b0 = al_desc_lo(qs_a, 16);
-                        for (int sl = 0; sl < nK; sl++, at.step(slots), b0 += (uint32_t)L.qslice >> 4) {
-                            const int s = at.s;
-                            if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
+#pragma unroll
+                        for (int sl = 0; sl < 4; sl++, b0 += qstep) {
+                            const int dims = hd - 64 * sl;
+                            if (dims <= 0 || !(ok = arrived())) break;
                             tc_fence_after();
-                            const int dims = hd - sl * 64;
-                            const uint32_t a0 = ring_d + (uint32_t)s * (C::kSlot / 16);
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)
                                 if (16 * kk < dims)
 #pragma unroll
                                     for (int t = 0; t < NT; t++)
-                                        al_mma(tmem + t * nr, a0 + (uint32_t)(t * C::kTerm / 16 + 2 * kk), hi128, b0 + 2u * kk,
+                                        al_mma(tmem + t * nr, slot_d + (uint32_t)(t * C::kTerm / 16 + 2 * kk), hi128, b0 + 2u * kk,
                                                hi128, ids[t], kk > 0 || t > 0 || sl > 0);
-                            tc_commit(&S.empty[s]);
+                            al_commit(step());
                         }
                         if (!ok) break;
                         tc_commit(&S.s_full);
+                    } else {
+                        edge = edge_next;
                     }
                     if (i >= 1) {
-                        if (!(ok = al_wait(&S.p_ready, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
+                        if (!(ok = al_wait_at(p_ready, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
 #pragma unroll
                         for (int kh = 0; kh < 2; kh++) {
                             const uint32_t b0 = al_desc_lo(ps_a + kh * 64 * 64, kChunk * 64);
                             uint32_t d = tmem + C::kO;
-                            for (int dh = 0; ok && dh < nDH; dh++, at.step(slots), d += 3 * R) {
-                                const int s = at.s;
-                                if (!(ok = al_wait(&S.full[s], at.round & 1u, &S.abort))) break;
-                                if (edge[kh]) {
+#pragma unroll
+                            for (int dh = 0; dh < 2; dh++, d += 3 * R) {
+                                if (dh >= nDH || !(ok = arrived())) break;
+                                if (edge >> kh & 1u) {
                                     mbar_arrive(&S.fix_go);
                                     if (!(ok = al_wait(&S.fixed, fixes & 1u, &S.abort))) break;
                                     fixes++;
                                 }
                                 tc_fence_after();
-                                const uint32_t a0 = ring_d + (uint32_t)s * (C::kSlot / 16) + vlbo;
+                                const uint32_t a0 = slot_d + vlbo;
 #pragma unroll
                                 for (int ks = 0; ks < 4; ks++)
 #pragma unroll
                                     for (int t = 0; t < NT; t++)
                                         al_mma(d + t * nr, a0 + (uint32_t)(t * C::kTerm / 16 + 128 * ks), hi128, b0 + 64u * ks,
                                                hip, idp[t], ks > 0 || t > 0 || kh > 0);
-                                tc_commit(&S.empty[s]);
+                                al_commit(step());
                             }
+                            if (!ok) break;
                         }
                         if (!ok) break;
                         tc_commit(&S.pv_done);
                     }
-                    const int row = (c < nsink ? c : c + skip) * kChunk;  // of chunk i
-                    if (++c == c1) c -= n;
-                    edge[0] = p->edge_in(row, row + 64);
-                    edge[1] = p->edge_in(row + 64, row + 128);
                 }
                 it += n;
                 if (ok) ref.done(S);
@@ -1317,7 +1364,7 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
                 const int gs = D.HB == 1 ? D.group : min(D.R, D.group - hb * D.R);
                 const int r = (lane - t->lane0) * gs + hg - hb * D.R;
                 // from the unit of its first chunk
-                const int64_t u1 = t->unit0 + (int64_t)(kvh * D.HB + hb + 1) * (nch + kSetup), u0 = u1 - nch;
+                const int64_t u1 = t->unit0 + (int64_t)(kvh * D.HB + hb + 1) * (nch + D.setup), u0 = u1 - nch;
                 const int b0 = (int)(((u0 + 1) * G - 1) / U), b1 = (int)((u1 * G - 1) / U);
                 if (b0 == b1)
                     done = D.streams == 1, y[st] = make_int4(1, -1, 0, 0);
@@ -1827,6 +1874,8 @@ qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t work
     D.streams = A.pre.k ? 2 : 1;
     D.grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
     D.merge = A.n_lanes <= kSelfPlan ? 1 : 32;
+    // (measured: tiles of 2 to 33 chunks of 128 keys in bf16 want 3 to 5, the longer chunks of fp32 caches 2)
+    D.setup = f32 ? 2 : 4;
     D.c = (float)(1.4426950408889634 / std::sqrt((double)A.hd));
     if (few_fits(A, D, f32, rows)) return attend_few(A, D, w, f32, (cudaStream_t)stream);
     const void *kern = f32 ? (const void *)al_attn_kernel<3> : (const void *)al_attn_kernel<1>;
