@@ -1243,7 +1243,8 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                                 for (int tt = 0; tt < NT; tt++)
 #pragma unroll 4
                                     for (int q = 0; q < 16; q++)
-                                        sts128(row + tt * C::kTerm + (q >> 3) * 8192 + ((q & 7) << 4), make_uint4(0, 0, 0, 0));
+                                        sts128(row + tt * C::kTerm + (q >> 3) * 8192 + (((q & 7) ^ (t & 7)) << 4),
+                                               make_uint4(0, 0, 0, 0));
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
