@@ -422,7 +422,7 @@ struct AlCfg {
     static constexpr int kThreads = 32 * (kMma + 4);
     static constexpr uint32_t kCols = 512;          // S^T [3 R], then O^T's two halves of dims [3 R] each
     static constexpr uint32_t kO = 3 * R;
-    static constexpr int kMaxSlots = NT == 1 ? 12 : 3;
+    static constexpr int kMaxSlots = NT == 1 ? 12 : 3;  // (bf16: at least six, more than a chunk's four slices of V)
 };
 
 // What a producer warp needs to load a slice of an fp32 cache.
@@ -677,6 +677,29 @@ struct PieceRef {
     }
 };
 
+// 64 dims of one key's values in a slice (row: their 128 swizzled bytes, of the slice's t-th key), a key that not every
+// row sees: zeros where no row does, or where one is not finite; then the rows that see it are marked.
+template <int NT>
+__device__ __forceinline__ void al_look(AlCtl<NT> &S, const AlPiece &p, int key, uint32_t row, int t, int dims) {
+    if (p.any_in(key, key + 1)) {
+        uint32_t bad = 0;
+#pragma unroll 4
+        for (int q = 0; q < 8; q++)
+            if (8 * q < dims) {
+                const uint4 v = lds128_a(row + ((q ^ (t & 7)) << 4));
+                // an exponent of all ones runs over into the sign's place
+                bad |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                       ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+            }
+        if (!(bad & 0x80008000u)) return;
+        for (int r = 0; r < p.nrows; r++)
+            if (key <= S.rowhi[r] && (key > S.rowlo[r] || key < p.sk)) S.nan[r] = 1;
+    }
+    for (int tt = 0; tt < NT; tt++)
+#pragma unroll 4
+        for (int q = 0; q < 8; q++) sts128(row + tt * AlCfg<NT>::kTerm + ((q ^ (t & 7)) << 4), make_uint4(0, 0, 0, 0));
+}
+
 template <int NT>
 __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     al_attn_kernel(const __grid_constant__ AlMaps maps, AlArgs A, AlDims D, AlWs W) {
@@ -921,7 +944,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             // a jump back takes 200 cycles here, the other warps having pushed its target out of the instruction cache.
             PieceRef ref;
             int it = 0;           // chunks so far
-            uint32_t fixes = 0;   // slices of V handed to the first warpgroup so far
+            uint32_t fixes = 0;   // slices of V of an fp32 cache handed to the first warpgroup so far
             bool ok = true;
             const uint32_t qs_a = smem_addr(qs), ps_a = smem_addr(ps);
             // (K slices have no leading byte offset to speak of, V's 64-dim blocks are 8 KB apart)
@@ -955,21 +978,16 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     ids[t] = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 4) << 24 | ((3 - t) * nr >> 3) << 17;
                     idp[t] = ids[t] | (1u << 15) | (1u << 16);
                 }
-                const int c1 = p->c1, nsink = p->nsink, skip = p->cfirst - nsink;
-                const int all_lo = p->all_lo, all_hi = p->all_hi, sk = p->sk;
-                int c = p->first;
                 uint32_t edge = 0, edge_next = 0;  // bit kh: of half kh of the chunk whose products are next; of the one behind
                 if (!(ok = al_wait(&S.q_ready, (uint32_t)ref.k & 1u, &S.abort))) break;
                 for (int i = 0; ok && i <= n; i++) {
                     if (i < n) {
-                        const bool free = it + i == 0 || al_test(s_free, (uint32_t)(it + i - 1) & 1u);
-                        // (of chunk i, while that is on its way)
-                        const int row = (c < nsink ? c : c + skip) * kChunk;
-                        if (++c == c1) c -= n;
-                        auto edge_in = [&](int a, int b) { return !(b <= all_hi && (a > all_lo || b < sk)); };
-                        edge = edge_next;
-                        edge_next = (uint32_t)edge_in(row, row + 63) | (uint32_t)edge_in(row + 64, row + 127) << 1;
-                        if (!free && !(ok = al_wait_at(s_free, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
+                        if (it + i > 0 && !(ok = al_wait_at(s_free, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
+                        if (NT == 3) {
+                            const int row = p->row0(i);
+                            edge = edge_next;
+                            edge_next = (uint32_t)p->edge_in(row, row + 64) | (uint32_t)p->edge_in(row + 64, row + 128) << 1;
+                        }
                         uint32_t b0 = al_desc_lo(qs_a, 16);
 #pragma unroll
                         for (int sl = 0; sl < 4; sl++, b0 += qstep) {
@@ -999,7 +1017,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
 #pragma unroll
                             for (int dh = 0; dh < 2; dh++, d += 3 * R) {
                                 if (dh >= nDH || !(ok = arrived())) break;
-                                if (edge >> kh & 1u) {
+                                if (NT == 3 && (edge >> kh & 1u)) {
                                     mbar_arrive(&S.fix_go);
                                     if (!(ok = al_wait(&S.fixed, fixes & 1u, &S.abort))) break;
                                     fixes++;
@@ -1037,7 +1055,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         const int wg = warp >> 2, t = tid & 127, r0 = 16 * wg;
         PieceRef ref;
         int g = 0, it = 0;   // slices and chunks so far
-        uint32_t fixes = 0;  // slices of V looked through
+        uint32_t fixes = 0;  // slices of V of an fp32 cache looked through
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)r0;
         const float ninf = -__int_as_float(0x7f800000);
         bool ok = true;
@@ -1061,6 +1079,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     __syncwarp();
                 }
                 ok = !al_bar_or(wg, !ok);
+                g += n * (nK + nV);
                 if (lane == 0) ref.done(S);
                 continue;
             }
@@ -1205,47 +1224,38 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                             acc[1][j] = __fmul_rn(acc[1][j], al);
                         }
                 }
+                if (NT == 1 && edge) {
+                    // Values of keys that not every row sees: the weight of a hidden one is zero, but zero times an
+                    // infinity or NaN is not.  The slices are dealt out to the warpgroups, half a key's values to a
+                    // thread.  (With the scores of the next chunk there, what lay in these slots before is read, and
+                    // what lies in them now stays until the weights are ready: the barriers' phases are the next ones.)
+                    if (i + 1 < n) al_wait(&S.s_full, (uint32_t)(it + 1) & 1u, &S.abort);
+                    const int gv = g + min(i + 2, n) * nK + i * nV;
+                    for (int vs = wg; vs < nV; vs += (nrows + 15) / 16) {
+                        const int sl = (gv + vs) % slots, k0 = cr + 64 * (vs / nDH), y = k0 + (t & 63);
+                        if (!p->edge_in(k0, k0 + 64)) continue;
+                        al_wait(&S.full[sl], (uint32_t)((gv + vs) / slots) & 1u, &S.abort);
+                        if (p->edge_in(y, y + 1))
+                            al_look<NT>(S, *p, y, smem_addr(ring + sl * C::kSlot) + (uint32_t)((t >> 6) * 8192 + (t & 63) * 128),
+                                        t, hd - (vs % nDH) * 128 - (t >> 6) * 64);
+                    }
+                }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.p_ready);
-                if (wg == 0 && edge) {
-                    // the values of keys that not every row sees
+                if (NT == 3 && wg == 0 && edge) {
+                    // the same slice by slice, as each has landed and its product waits (the ring of an fp32 cache may
+                    // be shorter than a chunk's slices of V)
                     const int gv = g + min(i + 2, n) * nK + i * nV;
-                    const bool any = p->any_in(key, key + 1), all = !p->edge_in(key, key + 1);
                     for (int vs = 0; vs < nV; vs++) {
-                        const int sl = (gv + vs) % slots, k0 = cr + 64 * (vs / nDH);
+                        const int sl = (gv + vs) % slots, k0 = cr + 64 * (vs / nDH), y = k0 + (t & 63);
                         if (!p->edge_in(k0, k0 + 64)) continue;
-                        // its turn: the slice has landed and its product waits
                         al_wait(&S.fix_go, fixes & 1u, &S.abort);
                         fixes++;
-                        if (!all && (t >> 6) == vs / nDH) {
-                            const uint32_t row = smem_addr(ring + sl * C::kSlot) + (uint32_t)((t & 63) * 128);
-                            bool nf = !any;
-                            if (any) {
-#pragma unroll 4
-                                for (int q = 0; q < 16; q++) {
-                                    const int d = (vs % nDH) * 128 + 8 * q;
-                                    // a row of 64 dims is 8 groups of 16 bytes, swizzled by the row
-                                    if (d < hd) {
-                                        const uint4 v = lds128_a(row + (q >> 3) * 8192 + (((q & 7) ^ (t & 7)) << 4));
-                                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                        for (int k = 0; k < 4; k++)
-                                            nf |= (u[k] & 0x7f80u) == 0x7f80u || (u[k] & 0x7f800000u) == 0x7f800000u;
-                                    }
-                                }
-                                if (nf)
-                                    for (int r = 0; r < nrows; r++)
-                                        if (sees(r)) S.nan[r] = 1;
-                            }
-                            if (nf)
-                                for (int tt = 0; tt < NT; tt++)
-#pragma unroll 4
-                                    for (int q = 0; q < 16; q++)
-                                        sts128(row + tt * C::kTerm + (q >> 3) * 8192 + (((q & 7) ^ (t & 7)) << 4),
-                                               make_uint4(0, 0, 0, 0));
-                        }
+                        if (p->edge_in(y, y + 1))
+                            al_look<NT>(S, *p, y, smem_addr(ring + sl * C::kSlot) + (uint32_t)((t >> 6) * 8192 + (t & 63) * 128),
+                                        t, hd - (vs % nDH) * 128 - (t >> 6) * 64);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&S.fixed);
