@@ -1884,7 +1884,7 @@ qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t work
     D.cap = (int64_t)A.n_lanes * D.group < D.R ? A.n_lanes * D.group : D.R;
     D.streams = A.pre.k ? 2 : 1;
     D.grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
-    D.merge = A.n_lanes <= kSelfPlan ? 1 : 32;
+    D.merge = A.n_lanes <= kSelfPlan ? 1 : 16;
     // (measured: tiles of 2 to 33 chunks of 128 keys in bf16 want 3 to 5, the longer chunks of fp32 caches 2)
     D.setup = f32 ? 2 : 4;
     D.c = (float)(1.4426950408889634 / std::sqrt((double)A.hd));
