@@ -9,8 +9,8 @@
 // zeros where no key is seen.
 //
 // One product for every use.  The rows of a tile are the query heads of one KV
-// head for up to 48 lanes (32 with fp32 caches) that read the same sequence:
-// the lanes of a prompt chunk, the beams of a prompt, or one lane alone.  The
+// head for the lanes that read the same sequence, 48 rows at most (32 with fp32
+// caches): lanes of a prompt chunk, beams of a prompt, or one lane alone.  The
 // keys and values are the large operand, so they take the tensor cores' 128
 // rows and the tile's rows the columns:
 //   S^T [128 keys][rows]      = K [keys][dims] . Q^T
@@ -40,19 +40,39 @@
 // many SMs and many short ones are packed, whatever the lengths, which are
 // read on the device.  A tile that lies in one CTA is finished there; the
 // others leave partial sums that a second kernel merges.  Up to 64 lanes every
-// CTA plans for itself (one warp, a lane or two per thread); from there a
-// kernel of one CTA plans once for all.
+// CTA plans for itself (two warps, a thread per lane); from there a kernel of
+// one CTA plans once for all (15 us at 4096 lanes).  A tile's start (the rows'
+// q, the first scores and maxima, the outputs) takes as long as four chunks of a
+// bf16 cache or two of an fp32 one and is dealt out as that many.  Tiles of one
+// sequence read the same chunks; each CTA takes its own in the order of their
+// number modulo a CTA's units, so that they are read from memory once.
 //
 // Keys and values go through a ring of 16 KB slots (x 3 terms for an fp32
 // cache): 128 keys x 64 dims of K, 64 keys x 128 dims of V.  The shared memory
 // that the plan's widest tile leaves is ring.  A bf16 cache's are tensor
-// copies (TMA, 128-byte swizzle) straight from the cache; an fp32 cache's are
-// loaded, split and stored by eight warps.
+// copies (TMA, 128-byte swizzle) straight from the cache, issued by two warps;
+// an fp32 cache's are loaded, split and stored by 16 warps.
 //
 // Rows that nobody in the tile may see (behind the last position, before the
 // window) are set to zero before their product, and a value that only some
 // rows of a tile may see is replaced by zero where it is not finite, with the
 // sums of the rows that do see it made NaN: 0 x NaN would reach the others.
+//
+// What bounds it, at 256 dims and 4 query heads on one KV head in bf16 (us of a
+// call in a graph; GB300):
+//   64 lanes of their own, 4100 keys each: 57 (270 MB: 4.7 TB/s, 71% of a
+//     measured copy; without any product 43: the tiles' starts are the rest);
+//   64 lanes behind one prompt of 131072: 102.  Each 128-key chunk takes 4000
+//     cycles: 2640 for the products' columns at the full rate, the rest
+//     hand-overs between the thread that issues them and the warpgroups (with a
+//     quarter of the products and no copies it is 93).  Caches are read once
+//     (147 MB), the tensor pipe is busy half of the time;
+//   two chunks of 2048 lanes, a window of 1024: 86, of which 15 plan and 6
+//     merge; a tile has 10 chunks, 3 of them with keys that some rows do not
+//     see (5000 cycles and more), and a start;
+// and 16 lanes of 32768 keys on fp32 caches, 8 heads on each of two KV heads of
+// 128: 200 (836 MB, 4.2 TB/s: 62% of a measured copy; the producers' splitting).
+// Few keys per lane take another kernel, below.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -1497,6 +1517,8 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
 // into shared memory, all of them at once, and computes in fp32 on the CUDA
 // cores.  Nothing is shared between lanes.  The CTA s of a (lane, head)
 // leaves partial sums for al_few_merge_kernel, or the result if it is alone.
+// One lane of 516 keys (4 heads, 256 dims, fp32: 1.06 MB) takes 7.3 us, two
+// launches and two trips to memory; the product kernel 16.7.
 constexpr int kFewThreads = 256, kFewMaxSplits = 1024, kFewRows = 16384;
 constexpr int kFewDims = 64;  // dims of a head per merging CTA
 
@@ -1791,12 +1813,12 @@ int few_heads(const AlDims &D) { return D.group <= 1 ? 1 : D.group <= 2 ? 2 : D.
 // the device): the multiply-adds of all its CTAs at most, with every lane and
 // block of GH heads counted for itself.  Measured with every position of the
 // caches in use, us per call here / by the product kernel: fp32, 4 query heads
-// on one KV head of 256: one lane of 512 7.4 / 16.7, 64 of 2048 (268 MB, 268 M
-// multiply-adds) 55.8 / 68.7; 8 on each of two of 128: 16 of 512 (34 M) 11.3 /
-// 23.3, 16 of 2048 (134 M) 28.6 / 31.2; bf16, 4 on one of 256: 16 of 2048 (67
-// M) 14.2 / 20.5, 64 of 2048 (268 M) 41.2 / 27.3; 8 on each of two of 128: 16
-// of 512 (34 M) 12.7 / 15.8, 16 of 2048 (134 M) 21.9 / 18.6; one on each of
-// four of 64: 64 of 2048 (67 M) 34.9 / 45.5.
+// on one KV head of 256: one lane of 512 7.3 / 16.7, 64 of 2048 (268 MB, 268 M
+// multiply-adds) 56.1 / 63.9; 8 on each of two of 128: 16 of 512 (34 M) 11.4 /
+// 20.5, 16 of 2048 (134 M) 28.7 / 29.0; bf16, 4 on one of 256: 16 of 2048 (67
+// M) 14.0 / 18.9, 64 of 2048 (268 M) 41.4 / 27.4; 8 on each of two of 128: 16
+// of 512 (34 M) 12.9 / 15.3, 16 of 2048 (134 M) 21.8 / 17.9; one on each of
+// four of 64: 64 of 2048 (67 M) 34.8 / 41.4.
 bool few_fits(const AlArgs &A, const AlDims &D, bool f32, int64_t rows) {
     const int64_t s = few_splits(A, f32);
     const int gh = few_heads(D);
