@@ -138,6 +138,46 @@ def test_beam_of_lowest_values_only(dev):
     np.testing.assert_allclose(out, np.full((1, 5), -1 - np.log(1000)), rtol=1e-6)
 
 
+def test_logarithm_of_every_count(dev):
+    # Group g: g + 1 equally likely words against a finished beam whose score is fp32's nearest to their offer.  The
+    # sum is exact, so which comes first tells the logarithm's error.  Its series leaves out less than 1e-11; behind w
+    # (|w| <= 1/5, kept in two floats) the rest, at most 2 w^3 / 3 (1 + ...) < 6e-3, is rounded some six times at
+    # 2^-24 each: 2.2e-9.
+    G = 1500
+    x = np.full((G, 2, G), -np.inf, np.float32)
+    for g in range(G):
+        x[g, 0, : g + 1] = 0
+    lse = np.log(np.arange(1, G + 1, dtype=np.float64))
+    score = (-lse).astype(np.float32)
+    s = np.zeros((G, 2), np.float32)
+    s[:, 1] = score
+    fin = np.zeros((G, 2), np.uint8)
+    fin[:, 1] = 1
+    out, par, tok = _select(dev, x, s, 1, fin, 7)
+    gap = score.astype(np.float64) + lse
+    sure = np.abs(gap) > 3e-9
+    assert sure.mean() > 0.8
+    np.testing.assert_array_equal(par[sure, 0], gap[sure] > 0)
+    assert par[0, 0] == 0  # a tie
+    np.testing.assert_allclose(out[:, 0], score, rtol=2.0 ** -23)
+
+
+def test_large_scores_and_logits(dev):
+    rng = np.random.default_rng(12)
+    # a beam's score swallows its words' differences: the words in the order of their logits
+    x = rng.normal(0, 3, (1, 3, 5000)).astype(np.float32)
+    for big in (np.float32(3e34), np.float32(np.inf)):
+        s, p, t = _select(dev, x, np.float32([[-1, big, -2]]), 6)
+        assert (p == 1).all() and (s == big).all()
+        np.testing.assert_array_equal(t[0], np.argsort(-x[0, 1], kind="stable")[:6])
+    # logits beyond 2^24: the sum is taken relative to the largest
+    x = (3e7 + 2 * np.stack([rng.permutation(4000) for _ in range(2)])).astype(np.float32)[None]
+    x[0, 1] -= 2e7
+    _check(dev, x, np.float32([[-0.5, -1.25]]), 9)
+    x[0, 0] = -x[0, 0]
+    _check(dev, x, np.float32([[-0.5, -1.25]]), 9)
+
+
 def test_nan_and_infinity(dev):
     rng = np.random.default_rng(8)
     x = rng.normal(0, 3, (1, 4, 9000)).astype(np.float32)
@@ -156,6 +196,14 @@ def test_ties_go_to_the_lowest_beam_then_word(dev, V):
     _check(dev, x, np.zeros((1, 3), np.float32), 70, need_gap=False)
     x = np.round(np.random.default_rng(9).normal(0, 1, (2, 2, V))).astype(np.float32)  # many equal values
     _check(dev, x, np.float32([[0, -1], [-1, -1]]), 100, need_gap=False)
+
+
+def test_zeros_of_either_sign_are_equal(dev):
+    x = np.full((1, 2, 4000), -1, np.float32)
+    x[:, :, 100:1900:3] = 0.0
+    x[:, :, 101:1900:3] = -0.0
+    _check(dev, x, np.zeros((1, 2), np.float32), 12, need_gap=False)
+    _check(dev, x, np.float32([[0, -1]]), 128, need_gap=False)
 
 
 def test_sorted_logits(dev):

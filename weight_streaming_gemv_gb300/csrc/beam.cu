@@ -67,8 +67,10 @@ __device__ __forceinline__ uint32_t ord32(float v) {
 __device__ __forceinline__ float unord32(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
-// larger value first, then the lower index
-__device__ __forceinline__ uint64_t cand_key(float v, uint32_t idx) { return ((uint64_t)ord32(v) << 32) | (uint32_t)~idx; }
+// larger value first, then the lower index (+ 0: no negative zeros)
+__device__ __forceinline__ uint64_t cand_key(float v, uint32_t idx) {
+    return ((uint64_t)ord32(__fadd_rn(v, 0.0f)) << 32) | (uint32_t)~idx;
+}
 
 constexpr uint32_t kOrdNegInf = 0x007fffffu;  // ord32(-inf); anything above it is a candidate
 
@@ -465,6 +467,7 @@ __device__ __forceinline__ float2 log_of_sum(float h, float l) {
 
 struct MergeSmem {
     float2 lse[kMaxBeams];  // a beam's sum of exponentials, then its log less top
+    float2 shift[kMaxBeams];  // its score less that log
     float top[kMaxBeams];   // the beam's largest logit
     float base[kMaxBeams];  // its score
     int kind[kMaxBeams];    // 0: dead, 1: live, 2: finished
@@ -485,9 +488,9 @@ struct MergeSmem {
 };
 
 // Entry h of list i as a whole number in the order of the candidates (key 0:
-// there is none; NaN gives nothing of this beam), and its place beam << 32 |
-// word.  One copy of the code: the kernel runs once through little data, and
-// fetching instructions is much of its time.
+// there is none; NaN gives nothing of this beam), and what settles equal ones:
+// the beam, the logit (the larger first: offers are only equal as rounded) and
+// the word, in 6, 32 and 24 bits.
 struct MergeEntry {
     uint64_t key;
     int64_t at;
@@ -501,15 +504,15 @@ __device__ __noinline__ MergeEntry merge_entry(const MergeSmem &M, const uint64_
         const uint64_t k = list[h];
         const float x = unord32((uint32_t)(k >> 32)), top = M.top[b], base = M.base[b];
         const float2 lse = M.lse[b];
-        e.at = (int64_t)b << 32 | (uint32_t)~(uint32_t)k;
+        e.at = (int64_t)b << 56 | (int64_t)(uint32_t)~(uint32_t)(k >> 32) << 24 | (uint32_t)~(uint32_t)k;
         if (M.wild) {
             const double c = (double)base + (((double)x - (double)top) - ((double)lse.x + (double)lse.y));
             if (c > (double)ninf) e.key = ord64(c);
         } else {
+            // (one rounding, of the low part: a beam's candidates keep the order of its logits)
+            const float2 shift = M.shift[b];
             float c = x, l = 0.0f;
-            pair_add(c, l, -top, 0.0f);
-            pair_add(c, l, -lse.x, -lse.y);
-            pair_add(c, l, base, 0.0f);
+            pair_add(c, l, shift.x, shift.y);
             // the nearest float and the rest of it (+ 0: no negative zeros)
             float hi = l, lo = 0.0f;
             pair_add(hi, lo, c, 0.0f);
@@ -518,7 +521,7 @@ __device__ __noinline__ MergeEntry merge_entry(const MergeSmem &M, const uint64_
         }
     } else if (kind == 2 && h == 0 && (i == 0 || M.beam[i - 1] != b)) {
         const float c = __fadd_rn(M.base[b], 0.0f);
-        e.at = (int64_t)b << 32 | (uint32_t)eos;
+        e.at = (int64_t)b << 56 | (uint32_t)eos;
         if (c > ninf) e.key = M.wild ? ord64((double)c) : (uint64_t)ord32(c) << 32 | ord32(0.0f);
     }
     return e;
@@ -610,6 +613,13 @@ __global__ void __launch_bounds__(kMergeThreads)
             pair_add(l.x, l.y, -big, 0.0f);
         }
         M.lse[tid] = l;
+        // what a candidate is above its logit: score - lse
+        l.x = -l.x, l.y = -l.y;
+        pair_add(l.x, l.y, -big, 0.0f);
+        pair_add(l.x, l.y, M.base[tid], 0.0f);
+        float hi = l.y, lo = 0.0f;
+        pair_add(hi, lo, l.x, 0.0f);
+        M.shift[tid] = make_float2(hi, lo);
         if (wide || !(fabsf(M.base[tid]) <= 1e30f)) M.wild = 1;
     }
     __syncthreads();
@@ -672,8 +682,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     auto write = [&](int r, uint64_t key, int64_t at) {
         const int64_t o = (int64_t)g * n + r;
         out_scores[o] = M.wild ? (float)unord64(key) : unord32((uint32_t)(key >> 32));
-        parents[o] = (int)(at >> 32);
-        tokens[o] = (int)(uint32_t)at;
+        parents[o] = (int)(at >> 56);
+        tokens[o] = (int)(at & 0xffffff);
     };
     const int found = min(total, n);
     if (total <= kMergeBuf) {
