@@ -79,7 +79,7 @@
 
 #include <cmath>
 
-#include "common.cuh"
+#include "launch.cuh"
 #include "stream.cuh"
 #include "tcgen05.cuh"
 

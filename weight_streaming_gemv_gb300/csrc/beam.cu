@@ -44,7 +44,7 @@
 // and beams that stay cost nothing.  64 beams of 13 MB in four groups (1.22 GB
 // read and written): 194 us, 6.3 TB/s, 94% of a measured copy; four beams of 2.7
 // MB, three of them moved (10.6 MB, from L2): 4.2 us.
-#include "common.cuh"
+#include "launch.cuh"
 #include "stream.cuh"
 #include "tcgen05.cuh"
 
