@@ -374,6 +374,34 @@ def test_offsets_past_32_bits(dev):
     _close(got, np.stack([_ref(q[i], f(k, s), f(v, s), p, 0, 0, 1) for i, (p, s) in enumerate([(299, 1), (150, 0)])]))
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [6, 640])
+def test_sequences_inside_rows(dev, kind, n):
+    # row r of every sequence side by side: seq_stride below row_stride, and k and v interleaved (640 lanes are too
+    # much for the kernel of little work)
+    import torch
+
+    from weight_streaming_gemv_gb300 import qlin
+
+    S, R, H, n_kv, hd = 5, 700, 4, 2, 128
+    g = torch.Generator(device=dev).manual_seed(21)
+    t = torch.randn((R, S, 2, n_kv * hd), generator=g, device=dev).to(torch.float32 if kind == "f32" else torch.bfloat16)
+    k, v = t[:, :, 0].permute(1, 0, 2), t[:, :, 1].permute(1, 0, 2)
+
+    class View:
+        c = qlin.kv_cache(k, v)
+
+    rng = np.random.default_rng(22)
+    pos, seqs = rng.integers(0, R, n), np.sort(rng.integers(0, S, n))
+    c = Call(dev, n, H, n_kv, hd)
+    c.lanes(View, _i32(pos, dev), _i32(seqs, dev), 300, 3)
+    got, q = c.result(), c.q.cpu().numpy()
+    f = lambda x: x.float().cpu().numpy().reshape(R, n_kv, hd)
+    host = [(f(k[s]), f(v[s])) for s in range(S)]
+    for i in list(range(6)) + rng.integers(0, n, 40).tolist():
+        _close(got[i], _ref(q[i], *host[seqs[i]], pos[i], 300, 3, n_kv))
+
+
 def test_captured_and_on_another_stream(dev):
     import torch
 

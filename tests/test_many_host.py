@@ -155,5 +155,6 @@ def test_prefix_step_refuses():
 
     assert call(kv=None) == 1 and call(len=None) == 1 and call(n_prompts=0) == 1 and call(rows=0) == 1
     assert call(own=0) == 1 and call(kv=8) == 1 and call(len=6) == 1 and call(of=2) == 1 and call(kvs=None) == 1
+    assert call(rows=2 ** 30 + 1) == 2 and call(own=2 ** 30 + 1) == 2  # (more than the attention takes)
     assert call(wsb=64) == 1 and call(n_lanes=5) == 1 and call(ws=8) == 1
     assert "decode_lanes_t158" in L.qlin_last_error().decode()

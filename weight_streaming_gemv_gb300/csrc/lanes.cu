@@ -804,6 +804,12 @@ qlin_status decode_lanes_t158_prefix(const t158_model *m, const t158_prompts *pr
     QLIN_REQUIRE(prompts->n_prompts >= 1 && prompts->rows >= 1 && own_rows >= 1, QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158_prefix: %d prompts of %d rows, %d rows of a lane's own", (int)prompts->n_prompts,
                  (int)prompts->rows, own_rows);
+    // (what the attention takes: refused here, before anything is written)
+    const int most = prompts->rows > own_rows ? prompts->rows : own_rows;
+    QLIN_REQUIRE(most <= 1 << 30 && m->n_heads <= 65535 &&
+                     (double)2 * m->n_layers * most * m->n_kv_heads * m->head_dim * 4 < (double)((int64_t)1 << 40),
+                 QLIN_ERR_UNSUPPORTED, "decode_lanes_t158_prefix: %d rows of a prompt, %d of a lane's own",
+                 (int)prompts->rows, own_rows);
     QLIN_REQUIRE(aligned16(prompts->kv) && aligned4(prompts->len) && aligned4(prefix_of), QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158_prefix: misaligned prompts");
     return lanes_step(m, prompts, prefix_of, kv_caches, own_rows, n_seqs, n_lanes, tokens, positions, seqs, logits, next,
