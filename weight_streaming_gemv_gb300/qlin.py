@@ -19,6 +19,7 @@ from .build import LIB
 T158_NMAT = 7
 _lock = threading.Lock()
 _lib = None
+_raw_stream = None  # torch's functions behind _stream, once CUDA is in use
 
 
 class QlinError(RuntimeError):
@@ -146,6 +147,8 @@ SIGNATURES = {
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB):
@@ -171,23 +174,31 @@ def _check(fn: str, s: int):
 
 def _ptr(t):
     """Device/host address of a torch tensor or numpy array; ints pass through; None is NULL."""
+    address = getattr(t, "data_ptr", None)
+    if address is not None:
+        return address()
     if t is None:
         return None
-    if isinstance(t, int):
-        return t
     if isinstance(t, np.ndarray):
         return t.ctypes.data
-    return t.data_ptr()
+    if isinstance(t, int):
+        return t
+    raise TypeError(f"not a tensor, an array or an address: {type(t).__name__}")
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        c = torch._C
-        # (torch.cuda.current_stream() makes an object: 3 us of a 13 us call on a Grace core, this 0.2)
-        if hasattr(c, "_cuda_getCurrentRawStream") and torch.cuda.is_initialized():
-            return c._cuda_getCurrentRawStream(c._cuda_getDevice())
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            current = torch.cuda.current_stream().cuda_stream  # (and CUDA is initialised from here on)
+            c = torch._C
+            # (current_stream() makes an object: 3 us of a 13 us call on a Grace core, this 0.2)
+            if not (hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice")):
+                return current
+            _raw_stream = c._cuda_getCurrentRawStream, c._cuda_getDevice
+        handle, device = _raw_stream
+        return handle(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
