@@ -375,6 +375,22 @@ def test_offsets_past_32_bits(dev):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("H,n_kv,hd", [(4, 1, 256), (3, 3, 16), (10, 1, 64), (2, 1, 80)])
+@pytest.mark.parametrize("rows", [33, 65, 100, 300, 516, 640, 641, 1000, 1281])
+def test_little_work_in_any_number_of_pieces(dev, kind, rows, H, n_kv, hd):
+    # 1 to 41 pieces of a lane's keys: alone, as clusters of 2 to 16, with a merging launch; a short lane leaves most
+    # of its pieces empty, a padding lane all
+    kv = Caches(dev, kind, 2, rows, n_kv, hd, rows)
+    pos, seqs = [rows - 1, 0, rows // 2, -1], [0, 1, 1, 0]
+    c = Call(dev, 4, H, n_kv, hd, rows)
+    c.lanes(kv, _i32(pos, dev), _i32(seqs, dev))
+    got, q = c.result(), c.q.cpu().numpy()
+    for i in range(3):
+        _close(got[i], _ref(q[i], *kv.host(seqs[i]), pos[i], 0, 0, n_kv))
+    assert (got[3] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("n", [6, 640])
 def test_sequences_inside_rows(dev, kind, n):
     # row r of every sequence side by side: seq_stride below row_stride, and k and v interleaved (640 lanes are too

@@ -1516,15 +1516,18 @@ __global__ void __launch_bounds__(kMergeThreads) al_merge_kernel(AlArgs A, AlDim
 // without gaps (first tokens, then the window): it copies their k and v rows
 // into shared memory, all of them at once, and computes in fp32 on the CUDA
 // cores.  Nothing is shared between lanes.  The CTA s of a (lane, head)
-// leaves partial sums for al_few_merge_kernel, or the result if it is alone.
-// One lane of 516 keys (4 heads, 256 dims, fp32: 1.06 MB) takes 7.3 us, two
-// launches and two trips to memory; the product kernel 16.7.
+// leaves partial sums for al_few_merge_kernel, or the result if it is alone;
+// few enough CTAs are a cluster, which merges through its shared memory.  One
+// lane of 516 keys (4 heads, 256 dims, fp32: 1.06 MB) takes 6.8 us as a cluster
+// of 16, 7.3 with a merging launch, and 16.7 in the product kernel: a launch, a
+// trip to memory, and the chain from a key's dot product to the sum.
 constexpr int kFewThreads = 256, kFewMaxSplits = 1024, kFewRows = 16384;
 constexpr int kFewDims = 64;  // dims of a head per merging CTA
 
-template <typename T>
+// CL: the CTAs of a (lane, head) are one cluster and merge among themselves
+template <typename T, bool CL = false>
 struct FewCfg {
-    static constexpr int kKeys = sizeof(T) == 4 ? 32 : 64;       // 32 KB of k and of v rows at most
+    static constexpr int kKeys = (sizeof(T) == 4 ? 32 : 64) * (CL ? 2 : 1);  // 32 KB of k and of v rows at most, 64 of a cluster's
     static constexpr int kParts = kFewThreads / kKeys;           // threads that share a key's dot products
     static constexpr int kVec = 16 / (int)sizeof(T);             // values of 16 bytes
 };
@@ -1561,24 +1564,26 @@ __device__ __forceinline__ void few_unpack(const uint4 &u, float (&f)[8]) {
     for (int k = 0; k < 4; k++) f[2 * k] = __uint_as_float(w[k] << 16), f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
 }
 
-// grid (splits, KV heads x blocks of GH query heads, lanes)
-template <typename T, int GH>
-__global__ void __launch_bounds__(kFewThreads) al_few_kernel(AlArgs A, AlDims D, float2 *ml, float *part, int splits) {
-    using C = FewCfg<T>;
-    constexpr int K = C::kKeys, V = C::kVec;
+// grid (splits, KV heads x blocks of GH query heads, lanes); K: keys of a CTA
+template <typename T, int GH, bool CL>
+__global__ void __launch_bounds__(kFewThreads)
+    al_few_kernel(AlArgs A, AlDims D, float2 *ml, float *part, int splits, int K) {
+    using C = FewCfg<T, CL>;
+    constexpr int KM = C::kKeys, V = C::kVec;
     extern __shared__ __align__(16) uint8_t few_smem[];
     __shared__ __align__(16) float qs[GH][256];
-    __shared__ __align__(16) float ws[K][GH];
+    __shared__ __align__(16) float ws[KM][GH];
+    __shared__ float4 stat[GH];  // a cluster's: the largest score and the sum of the weights here
     const int tid = threadIdx.x, hd = A.hd, pitch = hd * (int)sizeof(T) + 16;
     const int s = blockIdx.x, blocks = (D.group + GH - 1) / GH, kvh = blockIdx.y / blocks, h0 = (blockIdx.y % blocks) * GH;
     const int lane_i = blockIdx.z, heads = min(GH, D.group - h0), head0 = kvh * D.group + h0;
-    uint8_t *ks = few_smem, *vs = few_smem + K * pitch;
+    uint8_t *ks = few_smem, *vs = few_smem + (CL ? K : KM) * pitch;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const FewLane L(A, lane_i);
     if (L.bad && s == 0 && blockIdx.y == 0 && tid == 0) raise_status(A.status, kStatusBadLane);
     const int n = min(K, L.count - s * K);  // this CTA's keys
-    if (n <= 0) {
+    if (CL ? L.count <= 0 : n <= 0) {
         if (s == 0)
             for (int e = tid; e < heads * hd; e += kFewThreads) A.out[((int64_t)lane_i * A.n_heads + head0) * hd + e] = 0.0f;
         return;
@@ -1594,6 +1599,7 @@ __global__ void __launch_bounds__(kFewThreads) al_few_kernel(AlArgs A, AlDims D,
         cp_async16(vs + r * pitch + c * 16, static_cast<const T *>(kv.v) + off, 16);
     }
     cp_async_commit();
+    if (CL && tid < GH) stat[tid] = make_float4(-__int_as_float(0x7f800000), 0.0f, 0.0f, 0.0f);  // (no key)
     for (int e = tid; e < GH * hd; e += kFewThreads) {
         const int h = e / hd;
         qs[h][e - h * hd] = h < heads ? A.q[((int64_t)lane_i * A.n_heads + head0) * hd + e] : 0.0f;
@@ -1630,17 +1636,17 @@ __global__ void __launch_bounds__(kFewThreads) al_few_kernel(AlArgs A, AlDims D,
     __syncthreads();
     // weights: a warp per head
     const int warp = tid >> 5, lane = tid & 31;
-    const bool alone = L.count <= K;
+    const bool alone = !CL && L.count <= K;
     const int64_t row0 = ((int64_t)lane_i * A.n_heads + head0) * splits + s;  // head h: row0 + h splits
     __shared__ float inv[GH];
-    if (warp < GH) {
-        float x[K / 32], m = -__int_as_float(0x7f800000), l = 0.0f;
+    if (warp < GH && n > 0) {
+        float x[KM / 32], m = -__int_as_float(0x7f800000), l = 0.0f;
 #pragma unroll
-        for (int u = 0; u < K / 32; u++) x[u] = ws[lane + 32 * u][warp], m = fmaxf(m, x[u]);
+        for (int u = 0; u < KM / 32; u++) x[u] = ws[lane + 32 * u][warp], m = fmaxf(m, x[u]);
         m = warp_max(m);
         if (!(m > -__int_as_float(0x7f800000))) m = 0.0f;  // (scores of minus infinity or NaN alone)
 #pragma unroll
-        for (int u = 0; u < K / 32; u++) {
+        for (int u = 0; u < KM / 32; u++) {
             x[u] = al_ex2(__fsub_rn(x[u], m));
             l += x[u];
             ws[lane + 32 * u][warp] = x[u];
@@ -1648,7 +1654,10 @@ __global__ void __launch_bounds__(kFewThreads) al_few_kernel(AlArgs A, AlDims D,
         l = warp_psum(l);
         if (lane == 0) {
             inv[warp] = alone ? __fdiv_rn(1.0f, l) : 1.0f;
-            if (!alone && warp < heads) ml[row0 + (int64_t)warp * splits] = make_float2(m, l);
+            if (CL)
+                stat[warp] = make_float4(m, l, 0.0f, 0.0f);
+            else if (!alone && warp < heads)
+                ml[row0 + (int64_t)warp * splits] = make_float2(m, l);
         }
     }
     __syncthreads();
@@ -1688,9 +1697,43 @@ __global__ void __launch_bounds__(kFewThreads) al_few_kernel(AlArgs A, AlDims D,
             const float4 b = *reinterpret_cast<const float4 *>(red + (u * GH + h) * hd + dd);
             a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
         }
+        if constexpr (CL) {
+            *reinterpret_cast<float4 *>(red + h * hd + dd) = a;
+            continue;
+        }
         const float f = inv[h];
         float *to = alone ? A.out + ((int64_t)lane_i * A.n_heads + head0 + h) * hd : part + (row0 + (int64_t)h * splits) * hd;
         *reinterpret_cast<float4 *>(to + dd) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+    }
+    if constexpr (CL) {
+        // the cluster's CTAs share the outputs out: as many threads to four dims as there are CTAs (2, 4, 8 or 16), one
+        // for each one's sums
+        cluster_sync();
+        const int lg = splits <= 2 ? 1 : splits <= 4 ? 2 : splits <= 8 ? 3 : 4, r = tid & ((1 << lg) - 1);
+        const int items = heads * nv, share = (items + splits - 1) / splits;
+        for (int i0 = 0; i0 < share; i0 += kFewThreads >> lg) {
+            const int at = i0 + (tid >> lg), i = s * share + at, h = min(i, items - 1) / nv, dd = (i - h * nv) * 4;
+            const bool on = at < share && i < items;
+            float4 st = make_float4(-__int_as_float(0x7f800000), 0.0f, 0.0f, 0.0f), v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (on && r < splits) st = ld_peer_f4(&stat[h], (uint32_t)r);
+            const bool some = st.x > -__int_as_float(0x7f800000);
+            if (some) v = ld_peer_f4(red + h * hd + dd, (uint32_t)r);
+            float m = st.x;
+            for (int off = 1 << lg >> 1; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            const float w = some ? al_ex2(__fsub_rn(st.x, m)) : 0.0f;
+            float l = w * st.y;
+            v.x *= w, v.y *= w, v.z *= w, v.w *= w;
+            for (int off = 1 << lg >> 1; off > 0; off >>= 1) {
+                l += __shfl_xor_sync(0xffffffffu, l, off);
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, off), v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+                v.z += __shfl_xor_sync(0xffffffffu, v.z, off), v.w += __shfl_xor_sync(0xffffffffu, v.w, off);
+            }
+            const float f = __fdiv_rn(1.0f, l);
+            if (on && r == 0)
+                *reinterpret_cast<float4 *>(A.out + ((int64_t)lane_i * A.n_heads + head0 + h) * hd + dd) =
+                    make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+        }
+        cluster_sync();  // nobody leaves while its sums are read
     }
 }
 
@@ -1801,9 +1844,12 @@ qlin_status kv_map(const void *p, const qlin_kv &c, int kvd, CUtensorMap *out) {
 }
 
 // The keys that a lane can see at most, and the splits they make.
+int64_t few_keys(const AlArgs &A) {
+    const int64_t keys = (int64_t)A.own.rows + (A.pre.k ? A.pre.rows : 0);
+    return A.window && (int64_t)A.window + A.sinks < keys ? (int64_t)A.window + A.sinks : keys;
+}
 int64_t few_splits(const AlArgs &A, bool f32) {
-    int64_t keys = (int64_t)A.own.rows + (A.pre.k ? A.pre.rows : 0);
-    if (A.window && (int64_t)A.window + A.sinks < keys) keys = (int64_t)A.window + A.sinks;
+    const int64_t keys = few_keys(A);
     const int per = f32 ? FewCfg<float>::kKeys : FewCfg<uint16_t>::kKeys;
     return (keys + per - 1) / per;
 }
@@ -1813,7 +1859,7 @@ int few_heads(const AlDims &D) { return D.group <= 1 ? 1 : D.group <= 2 ? 2 : D.
 // the device): the multiply-adds of all its CTAs at most, with every lane and
 // block of GH heads counted for itself.  Measured with every position of the
 // caches in use, us per call here / by the product kernel: fp32, 4 query heads
-// on one KV head of 256: one lane of 512 7.3 / 16.7, 64 of 2048 (268 MB, 268 M
+// on one KV head of 256: one lane of 512 6.8 / 16.7, 64 of 2048 (268 MB, 268 M
 // multiply-adds) 56.1 / 63.9; 8 on each of two of 128: 16 of 512 (34 M) 11.4 /
 // 20.5, 16 of 2048 (134 M) 28.7 / 29.0; bf16, 4 on one of 256: 16 of 2048 (67
 // M) 14.0 / 18.9, 64 of 2048 (268 M) 41.4 / 27.4; 8 on each of two of 128: 16
@@ -1827,29 +1873,49 @@ bool few_fits(const AlArgs &A, const AlDims &D, bool f32, int64_t rows) {
     return s <= kFewMaxSplits && s * A.n_lanes * A.n_heads <= rows && fma <= (!f32 ? 90e6 : gh < 8 ? 300e6 : 140e6);
 }
 
-template <typename T, int GH>
-qlin_status launch_few(const AlArgs &A, const AlDims &D, const AlWs &w, int splits, cudaStream_t st) {
-    const void *kern = (const void *)al_few_kernel<T, GH>;
-    const size_t rowbytes = (size_t)2 * FewCfg<T>::kKeys * (A.hd * sizeof(T) + 16);
+// CTAs of a cluster for keys that make `splits` CTAs; 0: no cluster.
+constexpr int kFewCluster = 16;
+int few_cluster(int splits) {
+    return splits > 1 && splits <= kFewCluster * 5 / 4 ? (splits < kFewCluster ? splits : kFewCluster) : 0;
+}
+constexpr qlin_status kNoCluster = (qlin_status)-1;
+
+template <typename T, int GH, bool CL>
+qlin_status launch_few(const AlArgs &A, const AlDims &D, const AlWs &w, int splits, int keys, cudaStream_t st) {
+    const void *kern = (const void *)al_few_kernel<T, GH, CL>;
+    const size_t rowbytes = (size_t)2 * keys * (A.hd * sizeof(T) + 16);
     const size_t sums = (size_t)(kFewThreads / (A.hd / 4)) * GH * A.hd * sizeof(float);
     const size_t smem = rowbytes > sums ? rowbytes : sums;
     blocks_per_sm(kern, smem);  // raises the dynamic shared-memory limit once
-    void *args[] = {(void *)&A, (void *)&D, (void *)&w.ml, (void *)&w.part, (void *)&splits};
-    return launch_pdl(kern, dim3(splits, A.n_kv * ((D.group + GH - 1) / GH), A.n_lanes), dim3(kFewThreads), smem, st, args,
-                      "al_few_kernel");
+    void *args[] = {(void *)&A, (void *)&D, (void *)&w.ml, (void *)&w.part, (void *)&splits, (void *)&keys};
+    const dim3 grid(splits, A.n_kv * ((D.group + GH - 1) / GH), A.n_lanes);
+    if (CL && max_clusters(kern, smem, kFewThreads, splits) < (int64_t)grid.y * grid.z) return kNoCluster;
+    return launch_pdl(kern, grid, dim3(kFewThreads), smem, st, args, "al_few_kernel", CL ? splits : 0);
 }
-template <typename T>
-qlin_status launch_few(const AlArgs &A, const AlDims &D, const AlWs &w, int splits, cudaStream_t st) {
+template <typename T, bool CL>
+qlin_status launch_few(const AlArgs &A, const AlDims &D, const AlWs &w, int splits, int keys, cudaStream_t st) {
     switch (few_heads(D)) {
-        case 1: return launch_few<T, 1>(A, D, w, splits, st);
-        case 2: return launch_few<T, 2>(A, D, w, splits, st);
-        case 4: return launch_few<T, 4>(A, D, w, splits, st);
-        default: return launch_few<T, 8>(A, D, w, splits, st);
+        case 1: return launch_few<T, 1, CL>(A, D, w, splits, keys, st);
+        case 2: return launch_few<T, 2, CL>(A, D, w, splits, keys, st);
+        case 4: return launch_few<T, 4, CL>(A, D, w, splits, keys, st);
+        default: return launch_few<T, 8, CL>(A, D, w, splits, keys, st);
     }
 }
 qlin_status attend_few(const AlArgs &A, const AlDims &D, const AlWs &w, bool f32, cudaStream_t st) {
     const int splits = (int)few_splits(A, f32), keys = f32 ? FewCfg<float>::kKeys : FewCfg<uint16_t>::kKeys;
-    if (qlin_status e = f32 ? launch_few<float>(A, D, w, splits, st) : launch_few<uint16_t>(A, D, w, splits, st)) return e;
+    // One launch if the CTAs of every (lane, head block) can be a cluster and no cluster has to wait for another's SMs.
+    // us per call with a cluster / with two launches: fp32, 4 query heads on one KV head of 256: one lane of 512 6.8 /
+    // 7.5, four 7.0 / 8.6, 16 of 200 8.6 / 9.5; one on each of four of 64: one lane of 512 4.4 / 5.8; bf16: one lane of
+    // 1024 7.2 / 8.2, eight of 512 7.8 / 11.1.  With more keys to a CTA than a quarter above its own number it does not
+    // pay (fp32, one lane of 1024 in 16 CTAs: 8.7 / 7.4).
+    if (const int c = few_cluster(splits)) {
+        const int share = (int)((few_keys(A) + c - 1) / c);
+        const qlin_status e = f32 ? launch_few<float, true>(A, D, w, c, share, st) : launch_few<uint16_t, true>(A, D, w, c, share, st);
+        if (e != kNoCluster) return e;
+    }
+    if (qlin_status e = f32 ? launch_few<float, false>(A, D, w, splits, keys, st)
+                            : launch_few<uint16_t, false>(A, D, w, splits, keys, st))
+        return e;
     if (splits == 1) return QLIN_OK;
     void *args[] = {(void *)&A, (void *)&w.ml, (void *)&w.part, (void *)&splits, (void *)&keys};
     return launch_pdl((const void *)al_few_merge_kernel, dim3(A.n_heads, A.n_lanes, (A.hd + kFewDims - 1) / kFewDims),

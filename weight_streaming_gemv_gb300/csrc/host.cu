@@ -8,7 +8,7 @@
 #include <tuple>
 #include <vector>
 
-#include "common.cuh"
+#include "launch.cuh"
 
 namespace qlin {
 
@@ -77,6 +77,35 @@ int blocks_per_sm(const void *kern, size_t smem) {
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 256, smem) != cudaSuccess || n < 1) n = 1;
     g_occ[key] = n;
+    return n;
+}
+
+int max_clusters(const void *kern, size_t smem, int threads, int cluster) {
+    static std::mutex mu;
+    static std::map<std::tuple<const void *, int, size_t, int, int>, int> known;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const auto key = std::make_tuple(kern, dev, smem, threads, cluster);
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        auto it = known.find(key);
+        if (it != known.end()) return it->second;
+    }
+    blocks_per_sm(kern, smem);
+    int n = 0;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)cluster), cfg.blockDim = dim3((unsigned)threads), cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr, cfg.numAttrs = 1;
+    if ((cluster > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    std::lock_guard<std::mutex> lk(mu);
+    known[key] = n;
     return n;
 }
 
