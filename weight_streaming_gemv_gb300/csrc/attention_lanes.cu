@@ -71,7 +71,9 @@
 //     merge; a tile has 10 chunks, 3 of them with keys that some rows do not
 //     see (5000 cycles and more), and a start;
 // and 16 lanes of 32768 keys on fp32 caches, 8 heads on each of two KV heads of
-// 128: 200 (836 MB, 4.2 TB/s: 62% of a measured copy; the producers' splitting).
+// 128: 197 (836 MB, 4.2 TB/s: 63% of a measured copy; the producers wait for
+// their loads two thirds of the time, with the 64 KB in flight that their
+// registers hold, and split and store for a sixth).
 // Few keys per lane take another kernel, below.
 #include <cuda.h>
 #include <cudaTypedefs.h>
