@@ -250,7 +250,7 @@ __device__ __forceinline__ void make_plan(const AlArgs &A, const AlDims &D, int 
                 atomicMin(&smin[i - in_tile], spos[i]);
                 atomicMax(&smax[i - in_tile], spos[i]);
             }
-            // (a tile that reaches the end of this round's lanes may go on in the next: its first lane looks)
+            // (a tile that reaches the last of these lanes may go on behind them: its first lane looks)
             bar();
             AlTile t;
             int64_t tu = 0;
@@ -802,19 +802,18 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
         auto load = [&](uint4 (&o)[4]) -> bool {
             if (!(ok = al_wait(&S.sl_full[ds], dpar, &S.abort))) return false;
             const AlSlice &q = S.slice[ds];
+            // (no branch around the loads: the registers would be waited for behind it)
             const bool more = q.src != nullptr;
-            if (more) {
-                const int key0 = q.y0 + pr, dims = q.dims - 4 * pc, v = q.v;
-                const float *a = q.src + pr * q.stride + 4 * pc;
+            const int key0 = q.y0 + pr, dims = q.dims - 4 * pc, v = q.v;
+            const float *a = q.src + pr * q.stride + 4 * pc;
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    // K: 64 rows on; V: 64 dims on
-                    const int key = key0 + (v ? 0 : e * 64), d = v ? e * 64 : 0;
-                    const bool any = key <= q.any_hi && (key > q.any_lo || key < q.sk);
-                    al_ld16(a, any && d < dims, o[2 * e]);
-                    al_ld16(a + 32, any && d + 32 < dims, o[2 * e + 1]);
-                    a += v ? 64 : 64 * q.stride;
-                }
+            for (int e = 0; e < 2; e++) {
+                // K: 64 rows on; V: 64 dims on
+                const int key = key0 + (v ? 0 : e * 64), d = v ? e * 64 : 0;
+                const bool any = more && key <= q.any_hi && (key > q.any_lo || key < q.sk);
+                al_ld16(a, any && d < dims, o[2 * e]);
+                al_ld16(a + 32, any && d + 32 < dims, o[2 * e + 1]);
+                a += v ? 64 : 64 * q.stride;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.sl_empty[ds]);
