@@ -1866,12 +1866,30 @@ int few_heads(const AlDims &D) { return D.group <= 1 ? 1 : D.group <= 2 ? 2 : D.
 // M) 14.0 / 18.9, 64 of 2048 (268 M) 41.4 / 27.4; 8 on each of two of 128: 16
 // of 512 (34 M) 12.9 / 15.3, 16 of 2048 (134 M) 21.8 / 17.9; one on each of
 // four of 64: 64 of 2048 (67 M) 34.8 / 41.4.
+//
+// Where lanes share a sequence or a prompt (at least two to each, by the
+// caches' sizes), the product kernel reads its rows once and this one once per
+// lane, so the rows' bytes count too, some 256 more for a row's handling,
+// against a product kernel that takes longer for more tiles.  fp32, 32 beams of
+// one prompt: two heads on each of four KV heads of 128, 1250 rows (168 MB) 44.6
+// / 30.1, 300 rows (44 MB) 16.9 / 26.4; on three of 64, 2500 rows (124 MB) 50.6
+// / 24.9; 32 on each of six prompts of 300 (98 MB, 576 tiles) 39.3 / 64.7; four
+// on one of 256, 620 rows (43 MB) 18.5 / 25.6, 2500 (166 MB) 43.9 / 34.1; bf16,
+// two on each of four of 128, 1250 (84 MB) 26.2 / 21.5, 620 (43 MB) 16.6 / 21.5;
+// a chunk of 64 lanes, window 512, fp32, two on each of four of 128: 38.1 / 21.6.
 bool few_fits(const AlArgs &A, const AlDims &D, bool f32, int64_t rows) {
     const int64_t s = few_splits(A, f32);
     const int gh = few_heads(D);
     const double fma = (double)s * (f32 ? FewCfg<float>::kKeys : FewCfg<uint16_t>::kKeys) * A.n_lanes * A.n_kv *
                        ((D.group + gh - 1) / gh) * gh * A.hd * 2;
-    return s <= kFewMaxSplits && s * A.n_lanes * A.n_heads <= rows && fma <= (!f32 ? 90e6 : gh < 8 ? 300e6 : 140e6);
+    if (s > kFewMaxSplits || s * A.n_lanes * A.n_heads > rows || fma > (!f32 ? 90e6 : gh < 8 ? 300e6 : 140e6)) return false;
+    const qlin_kv &from = A.pre.k ? A.pre : A.own;
+    if (A.n_lanes < 2 * (int64_t)from.n_seqs) return true;
+    // several lanes to a sequence
+    const double bytes = (double)A.n_lanes * A.n_kv * ((D.group + gh - 1) / gh) * few_keys(A) *
+                         (A.hd * 2 * (f32 ? 4 : 2) + 256);
+    const double tiles = (double)A.n_kv * (A.pre.k ? A.n_lanes : (A.n_lanes + D.LT - 1) / D.LT);
+    return bytes <= (f32 ? 106e6 : 90e6) + 0.3e6 * tiles && !(f32 && gh == 8 && fma > 100e6);
 }
 
 // CTAs of a cluster for keys that make `splits` CTAs; 0: no cluster.
