@@ -178,6 +178,29 @@ def test_large_scores_and_logits(dev):
     _check(dev, x, np.float32([[-0.5, -1.25]]), 9)
 
 
+def test_logits_beyond_the_scales_range(dev):
+    # Finite logits of any size: behind 2^24 the sum is taken relative to the largest, and a whole-number scale has no
+    # room for them from 7e7 on.  The beams' scores make the large one win.
+    rng = np.random.default_rng(13)
+    V = 40000  # (several slices)
+    s = np.float32([[-0.5, -1.25]])
+    small = rng.normal(0, 3, V).astype(np.float32)
+    for big, step in ((7e7, 8), (1e8, 8), (-1e8, 8), (-7e7, 8), (2e12, 131072)):  # (steps are fp32's there)
+        x = np.stack([(big + step * rng.permutation(V)).astype(np.float32), small])[None]
+        _check(dev, x, s, 9)
+    for big in (6.9e7, 7e7, 1e8, 3e38, np.finfo(np.float32).max, np.finfo(np.float32).min):
+        x = np.stack([np.full(V, big, np.float32), small])[None]
+        _check(dev, x, s, 20, need_gap=False)        # all of its words are equal
+        x[0, 0] = small
+        x[0, 0, [7, 11, 30000]] = big                # in slices of ordinary ones, and beside slices without
+        _check(dev, x, s, 6, need_gap=False)
+        for bad in (np.nan, np.inf):                 # in the slice of the large ones, and in another
+            for at in (8, 39000):
+                y = x.copy()
+                y[0, 0, at] = bad
+                _check(dev, y, s, 6, need_gap=False)
+
+
 def test_nan_and_infinity(dev):
     rng = np.random.default_rng(8)
     x = rng.normal(0, 3, (1, 4, 9000)).astype(np.float32)

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
                 if (ne > e) sum *= pow2i(max(e - ne, -126)), e = ne;
             }
             // x log2(e) - e with log2(e) in two parts: the rounding of one would be the same for a whole beam (NaN
-            // stays in the sum, plus infinity makes it infinite, nothing else does)
+            // stays in the sum; where a logit is beyond 2^24 the sum is made again)
             const float2 ef = make_float2(-(float)e, -(float)e);
             float2 acc = make_float2(sum, 0.0f);
 #pragma unroll
@@ -398,13 +398,16 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     float d;
     if (sel_wide(top)) {
         // logits beyond 2^24 (or none at all): once more, relative to the largest
+        // (a NaN is no smaller than anything and stays in the sum, plus infinity less itself is one; the first sum says
+        // nothing here: its scale ends at 1e8)
         d = 0.0f;
-        for (int i = v0 + tid; i < v1; i += kSelThreads)
-            if (x[i] > ninf) d += ex2_approx(__fmul_rn(__fsub_rn(x[i], top), kLog2eHi));
+        for (int i = v0 + tid; i < v1; i += kSelThreads) {
+            const float xi = x[i];
+            if (!(xi == ninf)) d += ex2_approx(__fmul_rn(__fsub_rn(xi, top), kLog2eHi));
+        }
     } else {
         d = __fmul_rn(sum, pow2i(max(e - (int)sel_exp(top), -126)));
     }
-    if (!(sum < -ninf)) d = __int_as_float(0x7fc00000);  // the beam's sum becomes NaN
     // the threads' sums as pairs
     float dl = 0.0f;
     pair_warp_sum(d, dl);
