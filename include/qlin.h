@@ -562,6 +562,15 @@ qlin_status qlin_attention_lanes(const float *q, const qlin_kv *kv, const int32_
                                  int n_lanes, int n_heads, int n_kv, int head_dim, int window, int sinks, float *out,
                                  int32_t *status_word, void *workspace, size_t workspace_bytes, qlin_stream_t stream);
 
+/* Which of two ways such a call goes, by its sizes alone (the positions are on
+ * the device): 1: on the tensor cores, where lanes that stand next to each
+ * other share the reads of their sequence or prompt; 0: little work, every lane
+ * for itself; below 0: a call of these sizes is refused with the status that is
+ * its negative (qlin_last_error).  prefix is NULL for qlin_attention_lanes, else
+ * as qlin_attention_prefix takes it. */
+int qlin_attention_on_tensor_cores(const qlin_kv *prefix, const qlin_kv *kv, int n_lanes, int n_heads, int n_kv,
+                                   int head_dim, int window, int sinks);
+
 /* The same for lanes that share prompts kept once.  Lane i continues prompt
  * prefix_of[i] (device int32 [n_lanes], NULL: prompt 0 for every lane), whose
  * first prefix_len[f] rows (device int32 [prefix->n_seqs]) are the keys and

@@ -62,6 +62,26 @@ def test_prefix_refuses():
     assert "not 4-byte aligned" in qlin.lib().qlin_last_error().decode()
 
 
+def test_attention_on_tensor_cores():
+    f = lambda kv, *a, prefix=None: qlin.qlin_attention_on_tensor_cores(prefix, kv, *a)
+    assert not f(_kv(), 2, 4, 1, 256, 0, 0)
+    assert not f(_kv(rows=30000), 2, 4, 1, 256, 500, 4)
+    for t in (0, 1):  # (more rows than the kernel for little work takes, whatever the lanes)
+        assert f(_kv(rows=66000, type=t), 1, 1, 1, 16, 0, 0)
+        assert f(_kv(rows=8, type=t), 1, 1, 1, 16, 0, 0, prefix=_kv(rows=66000, type=t))
+        assert f(_kv(rows=4096, n_seqs=64, type=t), 4096, 4, 1, 256, 0, 0)
+    for a, status in [((0, 4, 1, 256, 0, 0), 1), ((4097, 4, 1, 256, 0, 0), 2), ((2, 3, 2, 64, 0, 0), 1),
+                      ((2, 4, 1, 24, 0, 0), 2), ((2, 4, 1, 256, -1, 0), 1), ((2, 4, 1, 256, 0, -1), 1)]:
+        with pytest.raises(qlin.QlinError) as e:
+            f(_kv(), *a)
+        assert e.value.status == status
+    for kv, prefix in ((_kv(k=None), None), (_kv(rows=0), None), (_kv(), _kv(row_stride=252)), (_kv(), _kv(type=1))):
+        with pytest.raises(qlin.QlinError) as e:
+            f(kv, 2, 4, 1, 256, 0, 0, prefix=prefix)
+        assert e.value.status == 1
+    assert qlin.lib().qlin_attention_on_tensor_cores(None, None, 2, 4, 1, 256, 0, 0) == -1
+
+
 def test_attention_workspace_size():
     f = qlin.qlin_attention_lanes_workspace_size
     assert f(1, 4, 1, 256) > 0 and f(4096, 4, 1, 256) >= f(64, 4, 1, 256) >= f(1, 4, 1, 256)

@@ -1959,29 +1959,17 @@ qlin_status check_kv(const char *fn, const char *what, const qlin_kv *c, int n_k
     return QLIN_OK;
 }
 
+qlin_status same_types(const char *fn, const qlin_kv *prefix, const qlin_kv *kv) {
+    QLIN_REQUIRE(!prefix || prefix->type == kv->type, QLIN_ERR_INVALID_ARG, "%s: the caches' types differ", fn);
+    return QLIN_OK;
+}
+
 bool sizes_ok(int n_lanes, int n_heads, int n_kv, int hd) {
     return n_lanes >= 1 && n_lanes <= kMaxLanes && n_kv >= 1 && n_heads >= n_kv && n_heads % n_kv == 0 &&
            n_heads <= 65535 && hd >= 16 && hd <= 256 && hd % 16 == 0;
 }
 
-qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t workspace_bytes, qlin_stream_t stream) {
-    QLIN_REQUIRE(A.q && A.positions && A.seqs && A.out && workspace, QLIN_ERR_INVALID_ARG, "%s: null pointer", fn);
-    QLIN_REQUIRE(A.n_lanes >= 1 && A.n_heads >= 1 && A.n_kv >= 1 && A.n_heads % A.n_kv == 0 && A.window >= 0 &&
-                     A.sinks >= 0,
-                 QLIN_ERR_INVALID_ARG, "%s: n_lanes %d, n_heads %d, n_kv %d, window %d, sinks %d", fn, A.n_lanes,
-                 A.n_heads, A.n_kv, A.window, A.sinks);
-    QLIN_REQUIRE(sizes_ok(A.n_lanes, A.n_heads, A.n_kv, A.hd), QLIN_ERR_UNSUPPORTED,
-                 "%s: head_dim %d is not a multiple of 16 in 16..256, or more than %d lanes (%d) or 65535 heads", fn, A.hd,
-                 kMaxLanes, A.n_lanes);
-    QLIN_REQUIRE(aligned16(A.q) && aligned16(A.out) && aligned16(workspace), QLIN_ERR_INVALID_ARG,
-                 "%s: q, out and workspace are 16-byte aligned", fn);
-    QLIN_REQUIRE(aligned4(A.positions) && aligned4(A.seqs) && aligned4(A.prefix_len) && aligned4(A.prefix_of) &&
-                     aligned4(A.status),
-                 QLIN_ERR_INVALID_ARG, "%s: pointer not 4-byte aligned", fn);
-    int64_t rows;
-    const AlWs w = carve(A.n_lanes, A.n_heads, A.n_kv, A.hd, (char *)workspace, &rows);
-    QLIN_REQUIRE(workspace_bytes >= w.bytes, QLIN_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", fn, workspace_bytes,
-                 w.bytes);
+AlDims al_dims(const AlArgs &A) {
     const bool f32 = A.own.type == QLIN_KV_F32;
     AlDims D{};
     D.group = A.n_heads / A.n_kv;
@@ -1995,6 +1983,34 @@ qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t work
     // (measured: tiles of 2 to 33 chunks of 128 keys in bf16 want 3 to 5, the longer chunks of fp32 caches 2)
     D.setup = f32 ? 2 : 4;
     D.c = (float)(1.4426950408889634 / std::sqrt((double)A.hd));
+    return D;
+}
+
+qlin_status check_sizes(const char *fn, const AlArgs &A) {
+    QLIN_REQUIRE(A.n_lanes >= 1 && A.n_heads >= 1 && A.n_kv >= 1 && A.n_heads % A.n_kv == 0 && A.window >= 0 &&
+                     A.sinks >= 0,
+                 QLIN_ERR_INVALID_ARG, "%s: n_lanes %d, n_heads %d, n_kv %d, window %d, sinks %d", fn, A.n_lanes,
+                 A.n_heads, A.n_kv, A.window, A.sinks);
+    QLIN_REQUIRE(sizes_ok(A.n_lanes, A.n_heads, A.n_kv, A.hd), QLIN_ERR_UNSUPPORTED,
+                 "%s: head_dim %d is not a multiple of 16 in 16..256, or more than %d lanes (%d) or 65535 heads", fn, A.hd,
+                 kMaxLanes, A.n_lanes);
+    return QLIN_OK;
+}
+
+qlin_status attend(const char *fn, const AlArgs &A, void *workspace, size_t workspace_bytes, qlin_stream_t stream) {
+    QLIN_REQUIRE(A.q && A.positions && A.seqs && A.out && workspace, QLIN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (qlin_status e = check_sizes(fn, A)) return e;
+    QLIN_REQUIRE(aligned16(A.q) && aligned16(A.out) && aligned16(workspace), QLIN_ERR_INVALID_ARG,
+                 "%s: q, out and workspace are 16-byte aligned", fn);
+    QLIN_REQUIRE(aligned4(A.positions) && aligned4(A.seqs) && aligned4(A.prefix_len) && aligned4(A.prefix_of) &&
+                     aligned4(A.status),
+                 QLIN_ERR_INVALID_ARG, "%s: pointer not 4-byte aligned", fn);
+    int64_t rows;
+    const AlWs w = carve(A.n_lanes, A.n_heads, A.n_kv, A.hd, (char *)workspace, &rows);
+    QLIN_REQUIRE(workspace_bytes >= w.bytes, QLIN_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", fn, workspace_bytes,
+                 w.bytes);
+    const bool f32 = A.own.type == QLIN_KV_F32;
+    const AlDims D = al_dims(A);
     if (few_fits(A, D, f32, rows)) return attend_few(A, D, w, f32, (cudaStream_t)stream);
     const void *kern = f32 ? (const void *)al_attn_kernel<3> : (const void *)al_attn_kernel<1>;
     const size_t smem = kAlSmem, plan_smem = 6 * sizeof(int) * (size_t)A.n_lanes;
@@ -2034,6 +2050,24 @@ size_t qlin_attention_lanes_workspace_size(int n_lanes, int n_heads, int n_kv, i
     return sizes_ok(n_lanes, n_heads, n_kv, head_dim) ? carve(n_lanes, n_heads, n_kv, head_dim, nullptr).bytes : 0;
 }
 
+int qlin_attention_on_tensor_cores(const qlin_kv *prefix, const qlin_kv *kv, int n_lanes, int n_heads, int n_kv,
+                                   int head_dim, int window, int sinks) {
+    qlin::clear_error();
+    const char *fn = "qlin_attention_on_tensor_cores";
+    if (prefix)
+        if (qlin_status st = check_kv(fn, "prefix", prefix, n_kv, head_dim)) return -(int)st;
+    if (qlin_status st = check_kv(fn, "kv", kv, n_kv, head_dim)) return -(int)st;
+    if (qlin_status st = same_types(fn, prefix, kv)) return -(int)st;
+    AlArgs A{};
+    A.own = *kv;
+    if (prefix) A.pre = *prefix;
+    A.n_lanes = n_lanes, A.n_heads = n_heads, A.n_kv = n_kv, A.hd = head_dim, A.window = window, A.sinks = sinks;
+    if (qlin_status st = check_sizes(fn, A)) return -(int)st;
+    int64_t rows;
+    carve(n_lanes, n_heads, n_kv, head_dim, nullptr, &rows);
+    return few_fits(A, al_dims(A), kv->type == QLIN_KV_F32, rows) ? 0 : 1;
+}
+
 qlin_status qlin_attention_lanes(const float *q, const qlin_kv *kv, const int32_t *positions, const int32_t *seqs,
                                  int n_lanes, int n_heads, int n_kv, int head_dim, int window, int sinks, float *out,
                                  int32_t *status_word, void *workspace, size_t workspace_bytes, qlin_stream_t stream) {
@@ -2052,7 +2086,7 @@ qlin_status qlin_attention_prefix(const float *q, const qlin_kv *prefix, const i
     qlin::clear_error();
     if (qlin_status st = check_kv("qlin_attention_prefix", "prefix", prefix, n_kv, head_dim)) return st;
     if (qlin_status st = check_kv("qlin_attention_prefix", "kv", kv, n_kv, head_dim)) return st;
-    QLIN_REQUIRE(prefix->type == kv->type, QLIN_ERR_INVALID_ARG, "qlin_attention_prefix: the caches' types differ");
+    if (qlin_status st = same_types("qlin_attention_prefix", prefix, kv)) return st;
     QLIN_REQUIRE(prefix_len, QLIN_ERR_INVALID_ARG, "qlin_attention_prefix: null pointer");
     AlArgs A{q, *kv, *prefix, positions, seqs, prefix_len, prefix_of, n_lanes, n_heads, n_kv, head_dim, window, sinks,
              out, status_word};

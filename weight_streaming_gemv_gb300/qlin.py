@@ -132,6 +132,7 @@ SIGNATURES = {
     "decode_lanes_t158_status": ([_P, _P], _ST),
     "decode_step_t158_sketch_status": ([ctypes.POINTER(T158ModelC), ctypes.POINTER(T158SketchC), _P, _P], _ST),
     "qlin_attention_lanes_workspace_size": ([_I, _I, _I, _I], _SZ),
+    "qlin_attention_on_tensor_cores": ([ctypes.POINTER(QlinKvC), ctypes.POINTER(QlinKvC), _I, _I, _I, _I, _I, _I], _I),
     "qlin_attention_lanes": ([_P, ctypes.POINTER(QlinKvC), _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P], _ST),
     "qlin_attention_prefix": ([_P, ctypes.POINTER(QlinKvC), _P, _P, ctypes.POINTER(QlinKvC), _P, _P, _I, _I, _I, _I,
                                _I, _I, _P, _P, _P, _SZ, _P], _ST),
@@ -486,6 +487,14 @@ def kv_cache(k, v) -> QlinKvC:
 
 def qlin_attention_lanes_workspace_size(n_lanes, n_heads, n_kv, head_dim) -> int:
     return int(lib().qlin_attention_lanes_workspace_size(n_lanes, n_heads, n_kv, head_dim))
+
+
+def qlin_attention_on_tensor_cores(prefix, kv: QlinKvC, n_lanes, n_heads, n_kv, head_dim, window, sinks) -> bool:
+    r = lib().qlin_attention_on_tensor_cores(None if prefix is None else ctypes.byref(prefix), ctypes.byref(kv), n_lanes,
+                                             n_heads, n_kv, head_dim, window, sinks)
+    if r < 0:
+        _check("qlin_attention_on_tensor_cores", -r)
+    return bool(r)
 
 
 def qlin_attention_lanes(q, kv: QlinKvC, positions, seqs, n_lanes, n_heads, n_kv, head_dim, window, sinks, out,
