@@ -257,3 +257,29 @@ def test_same_inputs_same_bits(dev, kind, lanes):
         c.out[: c.n] = 1.0
         c.lanes(kv, pos, seqs)
         np.testing.assert_array_equal(c.result(), first)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("lanes", [3, 80])
+def test_scores_of_any_size(dev, kind, lanes):
+    # Finite scores far below those of real models: equal ones give the mean of the values, a larger one takes all, in
+    # whole and in split tiles.  (Equal scores are equal bits: what is left is the mean's error, a few 2^-24 of the values'
+    # 2-norm, within TOL.)
+    import torch
+
+    used, H, hd = 1000, 2, 64
+    kv = Long(dev, kind, 3, used, 1, hd, 15)
+    kv.k[0, :used] = -1e16
+    kv.k[1, :used] = -1e17
+    kv.k[1, 400] = 0.0
+    kv.k[2, :used] = -2e17
+    kv.k[2, 300:302] = -1e17
+    c = Call(dev, lanes, H, 1, hd)
+    _on_tensor_cores(c, kv)
+    c.q[:] = 1e16
+    c.q[:, 1] = 3e18
+    seqs = np.arange(lanes) % 3
+    c.lanes(kv, _i32([used - 1] * lanes, dev), _i32(seqs, dev))
+    got, host = c.result(), [kv.host(s)[1][:, 0].astype(np.float64) for s in range(3)]
+    want = [host[0].mean(0), host[1][400], host[2][300:302].mean(0)]
+    _close(got, np.stack([np.broadcast_to(want[s], (H, hd)) for s in seqs]))

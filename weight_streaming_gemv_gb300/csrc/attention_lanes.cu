@@ -26,7 +26,10 @@
 // columns of one product, in the order of their size, so that a cached term is
 // read once for all of them and each order has a sum of its own.
 //
-// A pass over the keys with a running maximum: the rows go to warpgroups, 16
+// A pass over the keys with a running maximum: q is multiplied by log2(e) /
+// sqrt(head_dim) before it is cut into terms, so a weight is 2^(score - maximum)
+// with one subtraction, which is exact for scores near the maximum however large
+// they are.  The rows go to warpgroups, 16
 // each, and thread t of one owns key t of a 128-key chunk (a tensor-memory
 // lane).  The maximum of a row is over threads, so it is only taken when some
 // score exceeds the one in use by 2^8 (and for a tile's first chunk):
@@ -92,7 +95,7 @@ constexpr int kMaxLanes = 4096;
 constexpr int kStatusBadLane = 1;
 constexpr int kMaxCtas = 160;  // the workspace holds two partial tiles for each
 constexpr int kChunk = 128;    // keys per unit (MMA M)
-constexpr float kNoKey = -1e30f;  // the running maximum of a row that has seen no key
+constexpr float kNoKey = -3.402823466e38f;  // the running maximum of a row that has seen no key: no score is below it
 
 struct AlArgs {
     const float *q;
@@ -1115,12 +1118,14 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 S.nan[r] = 0;
             }
             al_bar(wg);
-            // the rows' q as three bf16 terms
+            // the rows' q, with the softmax's scale, as three bf16 terms
 #pragma unroll 4
             for (int e = t; e < min(16, nrows - r0) * (hd / 8); e += 128) {
                 const int rr = e / (hd / 8), d8 = e - rr * (hd / 8), r = r0 + rr;
                 uint4 a, b, h, m, l;
                 al_ld32(A.q + (int64_t)S.rowid[r] * hd + 8 * d8, true, a, b);
+                auto scale = [&](uint32_t &u) { u = __float_as_uint(__fmul_rn(__uint_as_float(u), D.c)); };
+                scale(a.x), scale(a.y), scale(a.z), scale(a.w), scale(b.x), scale(b.y), scale(b.z), scale(b.w);
                 al_split8(a, b, h, m, l);
                 const uint32_t at = smem_addr(qs) + (uint32_t)((d8 >> 3) * L.qslice + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
                 sts128(at, h);
@@ -1179,7 +1184,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 bool big = i == 0;
                 if (i > 0)
 #pragma unroll
-                    for (int j = 0; j < 16; j++) big |= __fmaf_rn(s[j], D.c, -S.mc[r0 + j]) > 8.0f;
+                    for (int j = 0; j < 16; j++) big |= __fsub_rn(s[j], S.mc[r0 + j]) > 8.0f;
                 const bool update = al_bar_or(wg, big || fail);
                 if (update) {
                     if (al_bar_or(wg, fail)) {
@@ -1200,7 +1205,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     if (t < 16) {
                         const int r = r0 + t;
                         const float mx = fmaxf(fmaxf(S.red[0][r], S.red[1][r]), fmaxf(S.red[2][r], S.red[3][r]));
-                        const float old = S.mc[r], mc = mx > ninf ? fmaxf(__fmul_rn(mx, D.c), old) : old;
+                        const float old = S.mc[r], mc = mx > ninf ? fmaxf(mx, old) : old;
                         S.mc[r] = mc;
                         S.alpha[r] = old == kNoKey ? 0.0f : al_ex2(__fsub_rn(old, mc));
                     }
@@ -1211,7 +1216,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                 // (a masked score stays minus infinity, the weight 0)
 #pragma unroll
                 for (int j = 0; j < 16; j++) {
-                    s[j] = al_ex2(__fmaf_rn(s[j], D.c, -S.mc[r0 + j]));
+                    s[j] = al_ex2(__fsub_rn(s[j], S.mc[r0 + j]));
                     lsum[j] = __fadd_rn(lsum[j], s[j]);
                 }
                 if (i > 0) {  // the products of the chunk before: P is read, and O^T is there
