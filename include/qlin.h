@@ -549,7 +549,8 @@ typedef struct {
  * *status_word (device int32, may be NULL; bit 1: a bounded device wait gave
  * up; nothing clears it).  Rows that a lane does not see never reach its
  * outputs, whatever they hold; a NaN or an infinity in its q or in a k or v
- * that it sees can make all its outputs NaN (of the heads concerned).
+ * that it sees can make all its outputs NaN (of the heads concerned).  A score
+ * below fp32's range has no weight; a lane with no other gets zeros or NaN.
  * fp32 accuracy with either cache type: the products run on the tensor cores
  * on bf16 terms that carry all 24 significant bits, with fp32 accumulation,
  * and the softmax is in fp32.

@@ -391,6 +391,27 @@ def test_little_work_in_any_number_of_pieces(dev, kind, rows, H, n_kv, hd):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [30, 100, 600, 2000])  # alone, a cluster, and pieces that a second kernel joins
+def test_scores_below_the_types_range(dev, kind, rows):
+    # The first fifth of the keys have scores that fp32 cannot hold (-8e40): no weight.  The others' are equal, and far
+    # below zero: the mean of their values.
+    import torch
+
+    H, hd, n = 2, 64, rows // 5
+    kv = Caches(dev, kind, 2, rows, 1, hd, 31)
+    kv.k[0] = -3e-19
+    kv.k[0, :n] = -1e20
+    c = Call(dev, 2, H, 1, hd)
+    c.q[:] = 1e20
+    c.q[1] = 0.0
+    c.lanes(kv, _i32([rows - 1, rows - 1], dev), _i32([0, 1], dev))
+    got = c.result()
+    v, w = kv.host(0)[1].astype(np.float64), kv.host(1)[1].astype(np.float64)
+    _close(got[0], np.broadcast_to(v[n:, 0].mean(0), (H, hd)))
+    _close(got[1], np.broadcast_to(w[:, 0].mean(0), (H, hd)))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("n", [6, 640])
 def test_sequences_inside_rows(dev, kind, n):
     # row r of every sequence side by side: seq_stride below row_stride, and k and v interleaved (640 lanes are too

@@ -1650,7 +1650,8 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
         for (int u = 0; u < KM / 32; u++) x[u] = ws[lane + 32 * u][warp], m = fmaxf(m, x[u]);
         m = warp_max(m);
-        if (!(m > -__int_as_float(0x7f800000))) m = 0.0f;  // (scores of minus infinity or NaN alone)
+        const bool some = m > -__int_as_float(0x7f800000);
+        if (!some) m = 0.0f;  // (scores of minus infinity or NaN alone)
 #pragma unroll
         for (int u = 0; u < KM / 32; u++) {
             x[u] = al_ex2(__fsub_rn(x[u], m));
@@ -1658,6 +1659,8 @@ __global__ void __launch_bounds__(kFewThreads)
             ws[lane + 32 * u][warp] = x[u];
         }
         l = warp_psum(l);
+        // (scores beyond fp32's range have no weight, and no say in what the other pieces are relative to)
+        if (!some && l == 0.0f) m = -__int_as_float(0x7f800000);
         if (lane == 0) {
             inv[warp] = alone ? __fdiv_rn(1.0f, l) : 1.0f;
             if (CL)
