@@ -283,3 +283,33 @@ def test_scores_of_any_size(dev, kind, lanes):
     got, host = c.result(), [kv.host(s)[1][:, 0].astype(np.float64) for s in range(3)]
     want = [host[0].mean(0), host[1][400], host[2][300:302].mean(0)]
     _close(got, np.stack([np.broadcast_to(want[s], (H, hd)) for s in seqs]))
+
+
+@pytest.mark.parametrize("pattern", [0x3F80FFFF, 0x3F80C0FF, 0x3F80BF80, 0x3F817FFF])
+def test_products_of_an_fp32_cache(dev, pattern):
+    # Products that all have one sign and lose the most where operands are cut into bf16 terms: keys whose every value
+    # has the pattern's mantissa against keys of bf16 values, which lose nothing, in scores of about 32 and 46.
+    #
+    # Tolerance: what is left out of a product, 2 * mid * lo with mid < 2^-7 and lo <= 2^-16 of the leading bit (where mid
+    # is rounded to nearest), is at most 2^-22: 46 * 2^-22 = 1.1e-5 in the difference of two scores.  Each score is
+    # rounded to fp32 once when its terms are added, 46 * 2^-24 = 2.8e-6 at most, twice.  exp2 has 2^-22 for each key.
+    # An output here is (a e^x - b) / (a e^x + b), x the difference's error: half of it.  (1.1e-5 + 5.6e-6 + 4.8e-7) / 2
+    # = 8.6e-6; where mid is 2^-7 (the first pattern) lo is 2^-23 and the first part is nothing: 3.1e-6.
+    import torch
+
+    used, hd = 900, 256
+    kv = Long(dev, "f32", 1, used, 1, hd, 16)
+    x = torch.tensor([pattern], dtype=torch.int32, device=dev).view(torch.float32)
+    kv.k[0, :used] = 1.015625
+    kv.k[0, 1:used:2] = x
+    kv.v[0, :used] = -1.0
+    kv.v[0, 1:used:2] = 1.0
+    c = Call(dev, 1, 2, 1, hd)
+    _on_tensor_cores(c, kv)
+    c.q[0, 0] = 2 * x
+    c.q[0, 1] = (x.double() * (16 / np.log2(np.e) / 4)).float()  # (with the softmax's scale in it: the pattern again)
+    c.lanes(kv, _i32([used - 1], dev), _i32([0], dev))
+    got, q = c.result(), c.q.cpu().numpy()
+    ref = _ref(q[0], *kv.host(0), used - 1, 0, 0, 1)
+    e = np.abs(got[0] - ref).max(-1)
+    assert (e <= (3.2e-6 if pattern == 0x3F80FFFF else 8.6e-6)).all(), e

@@ -21,8 +21,10 @@
 // fp32 accuracy from bf16 operands: q, the weights P and an fp32 cache's
 // values enter as three bf16 terms x = hi + mid + lo (24 bits), a bf16 cache's
 // as they are; the products of terms whose orders add to at most two are
-// accumulated (three for a bf16 cache, six for an fp32 one; what is left out
-// is below 2^-24 of the product).  The rows' terms stand side by side as the
+// accumulated: three for a bf16 cache, which are all there are, six for an fp32
+// one, where mid lo + lo mid + lo lo is left out.  With mid at most 2^-7 and lo
+// at most 2^-16 of a value's leading bit that is at most 2^-22 of the product, of
+// either sign, and some 2^-26 on average.  The rows' terms stand side by side as the
 // columns of one product, in the order of their size, so that a cached term is
 // read once for all of them and each order has a sum of its own.
 //
@@ -570,16 +572,19 @@ __device__ __forceinline__ bool al_wait(uint64_t *bar, uint32_t parity, int *abo
 }
 
 // Two values as three pairs of bf16 terms (the first value in the low half).
-// The terms are cut off, not rounded: 8 significant bits, the next 8 and the
-// last 8, so that the three add up to the value exactly, with no conversion
-// instruction (an infinity or NaN gives a NaN below itself).
+// The first term is cut off, so that the largest values stay finite, the second
+// rounded to nearest: what is left then has either sign, is at most 2^-16 of the
+// value's leading bit and fits the third, and the three add up to the value
+// exactly (an infinity or NaN gives a NaN below itself).  With the second term
+// cut off as well the products that are left out (al_attn_kernel) would all have
+// the sign of those that are not, and be twice as large.
 __device__ __forceinline__ void al_split2(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
     hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
     a = __fsub_rn(a, __uint_as_float(__float_as_uint(a) & 0xffff0000u));
     b = __fsub_rn(b, __uint_as_float(__float_as_uint(b) & 0xffff0000u));
-    mid = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-    a = __fsub_rn(a, __uint_as_float(__float_as_uint(a) & 0xffff0000u));
-    b = __fsub_rn(b, __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(mid) : "f"(b), "f"(a));
+    a = __fsub_rn(a, __uint_as_float(mid << 16));
+    b = __fsub_rn(b, __uint_as_float(mid & 0xffff0000u));
     lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
