@@ -155,6 +155,7 @@ class T158Decoder:
         self.beam_history = i32(G * B, 1, 1, (own_rows + 4) // 4 * 4)
         self.beam_scores = torch.empty((2, G, B), dtype=torch.float32, device=dev)
         self.beam_done = torch.zeros((G, B), dtype=torch.uint8, device=dev)
+        self.beam_status = i32(1)  # of the reordering
         self.beam_logits = torch.empty((G * B, cfg.vocab), dtype=torch.float32, device=dev)
         self.select_ws_bytes = qlin.qlin_beam_select_workspace_size(G, B, cfg.vocab, B)
         self.select_ws = torch.empty(self.select_ws_bytes, dtype=torch.uint8, device=dev)
@@ -198,8 +199,9 @@ class T158Decoder:
         self.beam_rows.fill_(self.beam_t)  # rows of the caches in use: the first tokens came from the prompt
         x, h = self.kv_beams, self.beam_history
         qlin.qlin_beam_reorder(x, x.stride(0) * 4, x.stride(2) * 4, 2 * self.cfg.n_layers, self.cfg.kv_dim * 4,
-                               self.own_rows, self.beam_parents, self.beam_rows, G, B)
-        qlin.qlin_beam_reorder(h, h.stride(0) * 4, h.stride(0) * 4, 1, h.stride(0) * 4, 1, self.beam_parents, None, G, B)
+                               self.own_rows, self.beam_parents, self.beam_rows, G, B, self.beam_status)
+        qlin.qlin_beam_reorder(h, h.stride(0) * 4, h.stride(0) * 4, 1, h.stride(0) * 4, 1, self.beam_parents, None, G, B,
+                               self.beam_status)
         if self.eos is not None:
             parents = self.beam_parents.long().clamp_min(0)
             self.beam_done.copy_(torch.gather(self.beam_done, 1, parents) | (self.beam_tokens == self.eos))
@@ -214,4 +216,10 @@ class T158Decoder:
                 self.beam_scores[self.beam_t & 1])
 
     def check_beams_status(self, stream=None):
+        """Raises what the forward steps or the reordering reported since the last check (a wait that gave up there
+        leaves some of the beams' states moved and others not), and clears it."""
         qlin.decode_lanes_t158_status(self.beams_ws, stream)
+        if self.beam_status.item():
+            self.beam_status.zero_()
+            raise qlin.QlinError("qlin_beam_reorder", qlin.ERR_TIMEOUT, "a bounded wait gave up: the beams' states are "
+                                 "partly moved")

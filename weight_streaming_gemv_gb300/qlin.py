@@ -17,6 +17,7 @@ import numpy as np
 from .build import LIB
 
 T158_NMAT = 7
+ERR_TIMEOUT = 5  # QLIN_ERR_TIMEOUT
 _lock = threading.Lock()
 _lib = None
 _raw_stream = None  # torch's functions behind _stream, once CUDA is in use
