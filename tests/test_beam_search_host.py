@@ -61,3 +61,24 @@ def test_the_reorderings_status_is_kept_and_raised(search):
     assert e.value.status == 5 and "qlin_beam_reorder" in str(e.value)
     d.check_beams_status()
     assert calls["reorder"] == 6 and calls["steps"] == 2 and calls["selects"] == 3
+
+
+def test_steps_past_the_models_positions_are_refused(search):
+    d, calls = search
+    d.start_beams([3, MAX_POS - 2], torch.zeros((N_SEQS, VOCAB)))
+    d.step_beams()  # positions 3 and 14: the first token's
+    d.step_beams()  # 4 and 15, the last there is
+    with pytest.raises(ValueError):
+        d.step_beams()
+    assert calls["steps"] == 2 and d.beam_t == 3
+    d.start_beams(torch.tensor([3, 5]), torch.zeros((N_SEQS, VOCAB)))  # (another search: as long as its caches are)
+    for _ in range(OWN):
+        d.step_beams()
+    with pytest.raises(ValueError):
+        d.step_beams()
+    for bad in ([3, MAX_POS + 1], [-1, 3]):
+        with pytest.raises(ValueError):
+            d.start_beams(bad, torch.zeros((N_SEQS, VOCAB)))
+    d.start_beams([3, MAX_POS], torch.zeros((N_SEQS, VOCAB)))  # (the first tokens need no position behind the prompt)
+    with pytest.raises(ValueError):
+        d.step_beams()

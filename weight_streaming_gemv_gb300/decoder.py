@@ -168,9 +168,14 @@ class T158Decoder:
 
     def start_beams(self, prompt_len, logits):
         """The beams' first tokens: ``logits`` [n_seqs][vocab] are those of each prompt's last token, ``prompt_len``
-        (int32 tensor or list) the prompts' lengths."""
+        (int32 tensor or list) the prompts' lengths.  Lengths on the host are checked, and step_beams refuses a step past
+        the model's max_pos; where they are on the device, check_beams_status tells."""
         G, B, V = self.n_seqs, self.beams, self.cfg.vocab
-        self.prompt_len.copy_(torch.as_tensor(prompt_len, dtype=torch.int32))
+        lens = torch.as_tensor(prompt_len, dtype=torch.int32)
+        self.longest = 0 if lens.is_cuda else int(lens.max())
+        if self.longest > self.cfg.max_pos or (not lens.is_cuda and int(lens.min()) < 0):
+            raise ValueError(f"start_beams: prompts of {lens.tolist()} positions, caches of {self.cfg.max_pos}")
+        self.prompt_len.copy_(lens)
         self.beam_rows.zero_()
         self.beam_done.zero_()
         self.beam_t = 0
@@ -184,6 +189,9 @@ class T158Decoder:
         G, B = self.n_seqs, self.beams
         if self.beam_t > self.own_rows:
             raise ValueError(f"step_beams: the beams' caches hold {self.own_rows} rows")
+        if self.longest + self.beam_t > self.cfg.max_pos:
+            raise ValueError(f"step_beams: {self.beam_t} tokens behind a prompt of {self.longest}, and the model has "
+                             f"{self.cfg.max_pos} positions")
         torch.add(self.prompt_len[self.beam_prompt], self.beam_t - 1, out=self.beam_pos)
         qlin.decode_lanes_t158_prefix(self.model, self.prompts, self.beam_prompt, self.kv_beams, self.own_rows, G * B,
                                       G * B, self.beam_tokens, self.beam_pos, self.beam_seq, self.beam_logits,
