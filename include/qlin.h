@@ -555,9 +555,10 @@ typedef struct {
  * on bf16 terms that carry all 24 significant bits, with fp32 accumulation,
  * and the softmax is in fp32.
  * workspace: device, 16-byte aligned, qlin_attention_lanes_workspace_size
- * bytes (0 for sizes out of range), owned by the caller, any content; calls
- * sharing it must not overlap on the GPU.  The call issues a fixed sequence of
- * kernels with no host synchronisation and can be captured. */
+ * bytes (0 for sizes out of range; 17 MB at least at 256 dims), owned by the
+ * caller, any content; calls sharing it must not overlap on the GPU.  The call
+ * issues a fixed sequence of kernels with no host synchronisation and can be
+ * captured. */
 size_t qlin_attention_lanes_workspace_size(int n_lanes, int n_heads, int n_kv, int head_dim);
 qlin_status qlin_attention_lanes(const float *q, const qlin_kv *kv, const int32_t *positions, const int32_t *seqs,
                                  int n_lanes, int n_heads, int n_kv, int head_dim, int window, int sinks, float *out,

@@ -24,21 +24,20 @@
 // accumulated: three for a bf16 cache, which are all there are, six for an fp32
 // one, where mid lo + lo mid + lo lo is left out.  With mid at most 2^-7 and lo
 // at most 2^-16 of a value's leading bit that is at most 2^-22 of the product, of
-// either sign, and some 2^-26 on average.  The rows' terms stand side by side as the
-// columns of one product, in the order of their size, so that a cached term is
-// read once for all of them and each order has a sum of its own.
+// either sign, and some 2^-26 on average.  The rows' terms stand side by side as
+// the columns of one product, in the order of their size, so that a cached term
+// is read once for all of them and each order has a sum of its own.
 //
 // A pass over the keys with a running maximum: q is multiplied by log2(e) /
 // sqrt(head_dim) before it is cut into terms, so a weight is 2^(score - maximum)
 // with one subtraction, which is exact for scores near the maximum however large
-// they are.  The rows go to warpgroups, 16
-// each, and thread t of one owns key t of a 128-key chunk (a tensor-memory
-// lane).  The maximum of a row is over threads, so it is only taken when some
-// score exceeds the one in use by 2^8 (and for a tile's first chunk):
-// otherwise weights relative to the maximum in use stay below 2^8 and nothing
-// needs rescaling.  The sums stay in each thread's registers until the end,
-// and so do the outputs: the tensor cores' accumulation rounds toward zero, so
-// they sum over one chunk only.
+// they are.  The rows go to warpgroups, 16 each, and thread t of one owns key t
+// of a 128-key chunk (a tensor-memory lane).  The maximum of a row is over
+// threads, so it is only taken when some score exceeds the one in use by 8 (and
+// for a tile's first chunk): otherwise weights relative to the maximum in use
+// stay below 2^8 and nothing needs rescaling.  The sums stay in each thread's
+// registers until the end, and so do the outputs: the tensor cores' accumulation
+// rounds toward zero, so they sum over one chunk only.
 //
 // Work is dealt out by 128-key chunks: every CTA (one per SM) takes an equal
 // run of the (tile, KV head, chunk) units, so a long sequence is split over
@@ -72,13 +71,18 @@
 //     hand-overs between the thread that issues them and the warpgroups (with a
 //     quarter of the products and no copies it is 93).  Caches are read once
 //     (147 MB), the tensor pipe is busy half of the time;
-//   two chunks of 2048 lanes, a window of 1024: 86, of which 15 plan and 6
-//     merge; a tile has 10 chunks, 3 of them with keys that some rows do not
-//     see (5000 cycles and more), and a start;
+//   two chunks of 2048 lanes, a window of 1024: 89 (98 to 102 where the inputs
+//     change from call to call), of which 15 plan and 6 merge; a tile has 10
+//     chunks, 3 of them with keys that some rows do not see (5000 cycles and
+//     more), and a start;
 // and 16 lanes of 32768 keys on fp32 caches, 8 heads on each of two KV heads of
-// 128: 197 (836 MB, 4.2 TB/s: 63% of a measured copy; the producers wait for
+// 128: 192 (836 MB, 4.4 TB/s: 65% of a measured copy; the producers wait for
 // their loads two thirds of the time, with the 64 KB in flight that their
-// registers hold, and split and store for a sixth).
+// registers hold, and split and store for a sixth; at these 16 rows of 128 dims
+// 46 KB of shared memory are left over, as the ring's slots are 48).  On fp32
+// caches two chunks of 512 lanes, a window of 1024, 4 heads on one of 256, take
+// 87 (floor 11: six products of 3.6 GFLOP), 32 lanes behind one prompt of 32768,
+// 4 heads on each of two of 128, 80 (floor 13, the same).
 // Few keys per lane take another kernel, below.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -1888,8 +1892,15 @@ int few_heads(const AlDims &D) { return D.group <= 1 ? 1 : D.group <= 2 ? 2 : D.
 // / 30.1, 300 rows (44 MB) 16.9 / 26.4; on three of 64, 2500 rows (124 MB) 50.6
 // / 24.9; 32 on each of six prompts of 300 (98 MB, 576 tiles) 39.3 / 64.7; four
 // on one of 256, 620 rows (43 MB) 18.5 / 25.6, 2500 (166 MB) 43.9 / 34.1; bf16,
-// two on each of four of 128, 1250 (84 MB) 26.2 / 21.5, 620 (43 MB) 16.6 / 21.5;
-// a chunk of 64 lanes, window 512, fp32, two on each of four of 128: 38.1 / 21.6.
+// two on each of four of 128, 1250 (84 MB) 26.2 / 21.5 (just inside the limit, so
+// it goes the slower way), 620 (43 MB) 16.6 / 21.5; a chunk of 64 lanes, window
+// 512, fp32, two on each of four of 128: 38.1 / 21.6.
+//
+// Caches larger than what is seen count as if all of them were: 16 lanes at
+// position 500 (fp32, 8 on each of two of 128) take 13.2 us in caches of 512 rows
+// and 20.8 in caches of 32768, by the product kernel; four beams behind a prompt
+// of 300 (4 on one of 256) 7.4 where the prompts' cache has 300 rows and 21.6 at
+// 32768.
 bool few_fits(const AlArgs &A, const AlDims &D, bool f32, int64_t rows) {
     const int64_t s = few_splits(A, f32);
     const int gh = few_heads(D);

@@ -18,12 +18,20 @@
 // of the slices' sorted lists, again by a threshold (on the lists' heads)
 // first.
 //
-// 4 beams of 262144 words (4.2 MB): 10.3 us; the slices' two tiles each and
+// 4 beams of 262144 words (4.2 MB): 10.1 us; the slices' two tiles each and
 // the merge are 4 us each, chains of a few dozen steps.  8 groups of 8 beams (59
-// MB): 24 us from L2, 26 from memory (2.2 TB/s, a third of a measured copy): the
-// slices take 18, bound by their instructions (300 per warp and 512 values,
-// half of the issue slots; a ring in shared memory with two tiles on their way
-// gave 0.5 us here and cost 1 us on the small case, prefetching to L2 nothing).
+// MB): 24 us from L2, 26 from memory (2.2 TB/s, a third of a measured copy).  The
+// slices take 18 of them, and nothing is full: half of the issue slots (330
+// instructions per warp and 512 values), a third of the memory's rate, the warps
+// mostly waiting for their next values (a ring in shared memory with two tiles on
+// their way gave 0.5 us here and cost 1 us on the small case, prefetching to L2
+// nothing).  Slices are dealt out over all rows: those of dead and finished beams
+// end at once, and the others get no more for it.
+//
+// Masks of minus infinity cost nothing (64 rows with 40 words left: 19 to 26 us).
+// With finite ones, the type's lowest value or -1e4, every masked word of a slice
+// without n others is a candidate as good as the next: the buffer overflows, the
+// slice is walked again with care, and the same 64 rows take 450 to 870 us.
 //
 // Two beams' candidates can lie closer together than fp32 resolves, so lse
 // and the candidates are held as pairs of floats (48 bits; fp64 instructions
