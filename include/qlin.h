@@ -624,7 +624,8 @@ qlin_status decode_lanes_t158_prefix(const t158_model *m, const t158_prompts *pr
  * infinity (a beam with that score, a word with that logit) are not taken;
  * where a group has fewer than n_out others, the rest of its lists is minus
  * infinity, -1 and -1.  A beam whose logits hold a NaN or plus infinity offers
- * nothing.  Offers are formed and compared in 46 bits or more (a beam's words
+ * nothing.  The logarithm of a beam's sum is good to 1e-6, however many words
+ * are alike; offers are formed and compared in 46 bits or more (a beam's words
  * come in the order of their logits, also where its score is so large that
  * their offers are equal); out_scores may be scores of the next call, but not
  * of this one.  beams: 1..64, n_out: 1..128, vocab:

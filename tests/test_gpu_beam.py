@@ -162,6 +162,33 @@ def test_logarithm_of_every_count(dev):
     np.testing.assert_allclose(out[:, 0], score, rtol=2.0 ** -23)
 
 
+@pytest.mark.parametrize("levels", [1, 2])
+def test_sums_of_equal_logits(dev, levels):
+    # So many rows that each is one slice, of equal words (or of two levels, 4 apart): every term rounds the same way.
+    # An offer is score - log V (with two levels log(V / 2 (1 + e^-4)) for the upper half's words).  Its error: 8 roundings
+    # of a tile's sum, the exponential's 2^-22, an argument's 2^-24 of at most 6, and the result's own, 2^-24 of 12:
+    # 2^-21 + 2^-22 + 2^-21.4 + 2^-20.4 = 1.8e-6.
+    import torch
+
+    from weight_streaming_gemv_gb300 import qlin
+
+    G, V = 460, 100000
+    x = torch.linspace(-3, 3, G, device=dev)[:, None].repeat(1, V)
+    if levels == 2:
+        x[:, 1::2] -= 4
+    sc, out = torch.zeros((G, 1), device=dev), torch.empty((G, 2), device=dev)
+    par, tok = (torch.empty((G, 2), dtype=torch.int32, device=dev) for _ in range(2))
+    nb = qlin.qlin_beam_select_workspace_size(G, 1, V, 2)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    qlin.qlin_beam_select(x, V, sc, None, 0, G, 1, V, 2, out, par, tok, ws, nb)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(par.cpu().numpy(), np.zeros((G, 2)))
+    np.testing.assert_array_equal(tok.cpu().numpy(), np.tile([0, levels], (G, 1)))
+    d = x.double()
+    want = -(torch.log(torch.exp(d - d[:, :1]).sum(1))).cpu().numpy()
+    assert np.abs(out.cpu().numpy() - want[:, None]).max() <= 1.8e-6
+
+
 def test_large_scores_and_logits(dev):
     rng = np.random.default_rng(12)
     # a beam's score swallows its words' differences: the words in the order of their logits

@@ -41,8 +41,9 @@
 // largest logit, so slices are brought to one scale by powers of two.  (Logits
 // beyond 2^24, where masks of the type's lowest value lie, take the slice's
 // largest logit itself as the scale.)  Each term is one fp32 exp2 (relative error
-// about 2^-22, independent from term to term), summed in fp32 over a thread's
-// values and in pairs from there.
+// about 2^-22); the terms of a thread's tile, 16 at most, are summed in fp32 (2^-21
+// at most) and pairs from there, since equal terms all round the same way and a
+// longer sum would be off the more the longer it is.
 //
 // Reordering.  new[b] = old[parent[b]] for every beam that does not keep its
 // place, in place: a CTA brings the same stretch of every beam that is wanted
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
         }
     };
     float v[VPT], nx[VPT];
-    float m, sum;  // this thread's largest value and its sum times 2^e
+    float m, sum, rest;  // this thread's largest value and its sum (sum + rest) times 2^e
     int e, c;
     uint32_t thr;  // n values of the slice so far are no smaller (minus infinity is no candidate)
     const int k = (n + kSelWarps - 1) / kSelWarps, jw = (n + k - 1) / k;  // k at most 16
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     for (bool careful = false;; careful = true) {
         load(v0, v);
         if (tid == 0) buf.count = 0;
-        m = ninf, sum = 0.0f, e = -(1 << 28);
+        m = ninf, sum = rest = 0.0f, e = -(1 << 28);
         thr = kOrdNegInf + 1;
         bool over = false;
         int tile = 0;
@@ -299,19 +300,22 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
                 m = tmax;
                 // a whole-number scale at or above the largest term's exponent
                 const int ne = (int)fminf(fmaxf(sel_exp(m), -1e8f), 1e8f);
-                if (ne > e) sum *= pow2i(max(e - ne, -126)), e = ne;
+                if (ne > e) {
+                    const float f = pow2i(max(e - ne, -126));
+                    sum *= f, rest *= f, e = ne;
+                }
             }
             // x log2(e) - e with log2(e) in two parts: the rounding of one would be the same for a whole beam (NaN
             // stays in the sum; where a logit is beyond 2^24 the sum is made again)
             const float2 ef = make_float2(-(float)e, -(float)e);
-            float2 acc = make_float2(sum, 0.0f);
+            float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int j = 0; j < VPT; j += 2) {
                 const float2 y = fma2(make_float2(v[j], v[j + 1]), make_float2(kLog2eLo, kLog2eLo),
                                       fma2(make_float2(v[j], v[j + 1]), make_float2(kLog2eHi, kLog2eHi), ef));
                 acc = add2(acc, make_float2(ex2_approx(y.x), ex2_approx(y.y)));
             }
-            sum = __fadd_rn(acc.x, acc.y);
+            pair_add(sum, rest, __fadd_rn(acc.x, acc.y), 0.0f);
             // the threshold: from the threads' maxima so far, after tiles 1, 2, 4, 8, ... (a tile's share of the values
             // is halved from one to the next, so each part of the slice leaves about as many candidates).  What a warp
             // last published holds from then on, so without many candidates only the first tile needs a barrier, and
@@ -403,21 +407,20 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     float top = wmax[0];
 #pragma unroll
     for (int w = 1; w < kSelWarps; w++) top = fmaxf(top, wmax[w]);
-    float d;
+    float d, dl;
     if (sel_wide(top)) {
         // logits beyond 2^24 (or none at all): once more, relative to the largest
         // (a NaN is no smaller than anything and stays in the sum, plus infinity less itself is one; the first sum says
         // nothing here: its scale ends at 1e8)
-        d = 0.0f;
+        d = dl = 0.0f;
         for (int i = v0 + tid; i < v1; i += kSelThreads) {
             const float xi = x[i];
-            if (!(xi == ninf)) d += ex2_approx(__fmul_rn(__fsub_rn(xi, top), kLog2eHi));
+            if (!(xi == ninf)) pair_add(d, dl, ex2_approx(__fmul_rn(__fsub_rn(xi, top), kLog2eHi)), 0.0f);
         }
     } else {
-        d = __fmul_rn(sum, pow2i(max(e - (int)sel_exp(top), -126)));
+        const float f = pow2i(max(e - (int)sel_exp(top), -126));
+        d = __fmul_rn(sum, f), dl = __fmul_rn(rest, f);
     }
-    // the threads' sums as pairs
-    float dl = 0.0f;
     pair_warp_sum(d, dl);
     if (lane == 0) wsum[warp] = make_float2(d, dl);
     __syncthreads();
