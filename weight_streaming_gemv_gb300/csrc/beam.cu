@@ -453,7 +453,7 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 }
 
 // log (h + l) as a pair, to about 1e-9 (the sums it is taken of are good to
-// 1e-7 of their largest term): h + l = 2^k f with f in [2/3, 4/3] and log f =
+// 7e-7): h + l = 2^k f with f in [2/3, 4/3] and log f =
 // 2 (w + w^3 / 3 + w^5 / 5 + ...), w = (f - 1) / (f + 1).  |w| <= 1/5: the
 // first term left out is below 1e-9, and behind w itself, which is a pair, one
 // float's digits do.  h is 0, positive or NaN.
