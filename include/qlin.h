@@ -654,6 +654,88 @@ qlin_status qlin_beam_reorder(void *cache, int64_t seq_stride, int64_t plane_str
                               int max_rows, const int32_t *parents, const int32_t *n_rows, int n_groups, int beams,
                               int32_t *status_word, qlin_stream_t stream);
 
+/* ========================================================================
+ * Long conversations in a small cache: keys and values in 4 bits on pages, the
+ * attention over them, and sampling.  They have no counterpart on the pages
+ * that the parts above cite.
+ *
+ * The cache.  Sequence s's position p lies in row p % page_rows of page
+ * table[s * table_stride + p / page_rows] of a pool of n_pages pages that all
+ * sequences draw from (a page may stand in several sequences' tables: a prompt
+ * kept once).  k and v hold the codes, uint8
+ * [n_pages][n_kv][page_rows][head_dim/2], k_scale and v_scale the scales,
+ * uint8 [n_pages][n_kv][page_rows][head_dim/32].  32 consecutive dims x of a
+ * head share a scale s, which is (8 + m) 2^(e-24) in the byte 8 e + m (2^-21
+ * .. 1920): the least that is at least max|x| / 7 (fp32 division), or the
+ * largest.  A code is rint(x / s) (fp32 division, ties to even), cut to -7 ..
+ * 7, stored as code + 8.  The codes of dims 8w .. 8w+7 are the little-endian
+ * 32-bit word w of a row: dim 8w + 2i in its bits 4i .. 4i+3, dim 8w + 2i + 1
+ * in its bits 16+4i .. 19+4i.  Every content of a page stands for finite
+ * values, so pages need no clearing.
+ * page_rows: 16, 32, 64, 128 or 256.  head_dim: 64, 128 or 256.  k, v, k_scale,
+ * v_scale: device, 16-byte aligned; table: device int32 [n_seqs][table_stride],
+ * table_stride >= max_pages, 4-byte aligned.  max_pages * page_rows is at most
+ * 2^30, n_pages * n_kv * page_rows below 2^31.  Entries of the table behind a
+ * sequence's last page, or before its window, are never read.
+ *
+ * Lanes are as above: lane i is the token at positions[i] of sequence seqs[i];
+ * a negative position is padding.  A lane whose sequence, position or page is
+ * out of range sets bit 0 of *status_word (device int32, may be NULL; nothing
+ * clears it).
+ * ====================================================================== */
+typedef struct {
+    void *k, *v, *k_scale, *v_scale;
+    const int32_t *table;
+    int64_t table_stride;
+    int32_t n_pages, page_rows, n_seqs, max_pages;
+} qlin_kv4;
+
+/* Appends the lanes' keys and values to the cache, rotated on the way: dims i
+ * and i + head_dim/2 of a query or key turn by the angle of the lane's position
+ * (rows of cos_t and sin_t, device fp32 [rope_rows][head_dim/2] as
+ * t158_rope_table makes them; both NULL: no rotation).  Rotation in fp32,
+ * products rounded then added, as qlin_rope_kv_append.
+ * k, v: device fp32, lane i's rows [n_kv][head_dim] at k + i * kv_stride; q:
+ * device fp32, lane i's rows [n_heads][head_dim] at q + i * q_stride; q_out:
+ * device fp32 [n_lanes][n_heads][head_dim], the rotated queries; it may be q
+ * itself where q_stride is n_heads * head_dim, else it does not overlap.  q and
+ * q_out may both be NULL.  Strides in floats, multiples of 4, of any size from a
+ * row on (so that q, k and v can be parts of one row).  Two lanes at the same
+ * position of one sequence, or whose pages are the same, race.
+ * A lane that is padding or out of range (a position of rope_rows or more
+ * counts) appends nothing and its queries come out as zeros.  A NaN is stored as
+ * 0, an infinity as the largest value of its sign; either sets bit 2 of
+ * *status_word.  n_lanes: 1..65536. */
+qlin_status qlin_kv4_append(const qlin_kv4 *kv, const float *k, const float *v, int64_t kv_stride, const float *q,
+                            int64_t q_stride, float *q_out, const float *cos_t, const float *sin_t, int rope_rows,
+                            const int32_t *positions, const int32_t *seqs, int n_lanes, int n_heads, int n_kv,
+                            int head_dim, int32_t *status_word, qlin_stream_t stream);
+
+/* The rows of the lanes' positions as the values that the cache holds: k_out
+ * and v_out, device fp32 [n_lanes][n_kv][head_dim], either may be NULL; zeros
+ * for a lane that is padding or out of range.  (Moves a sequence to an fp32
+ * cache, or shows what the 4 bits made of it.)  n_lanes: 1..2^20. */
+qlin_status qlin_kv4_read(const qlin_kv4 *kv, const int32_t *positions, const int32_t *seqs, int n_lanes, int n_kv,
+                          int head_dim, float *k_out, float *v_out, int32_t *status_word, qlin_stream_t stream);
+
+/* qlin_attention_lanes over such a cache: lane i, at position p, sees the keys
+ * at positions j <= p with j > p - window or j < sinks (window 0: every j <=
+ * p), its own row in the cache already.  q, out: device fp32
+ * [n_lanes][n_heads][head_dim], 16-byte aligned, not overlapping.  Lanes that
+ * are padding or out of range get zeros.  Keys whose page is out of range count
+ * as not seen and set bit 0 of *status_word (bit 1: a bounded device wait gave
+ * up).  A NaN or an infinity in a lane's q can make the outputs of its heads
+ * NaN; a score below fp32's range has no weight.  fp32 accuracy for the values
+ * that the cache holds.  n_lanes: 1..4096.
+ * workspace: device, 16-byte aligned, qlin_attention_kv4_workspace_size bytes
+ * (0 for sizes out of range), owned by the caller, any content; calls sharing
+ * it must not overlap on the GPU.  The call issues a fixed sequence of kernels
+ * with no host synchronisation and can be captured. */
+size_t qlin_attention_kv4_workspace_size(int n_lanes, int n_heads, int n_kv, int head_dim);
+qlin_status qlin_attention_kv4(const float *q, const qlin_kv4 *kv, const int32_t *positions, const int32_t *seqs,
+                               int n_lanes, int n_heads, int n_kv, int head_dim, int window, int sinks, float *out,
+                               int32_t *status_word, void *workspace, size_t workspace_bytes, qlin_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

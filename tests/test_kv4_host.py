@@ -1,0 +1,141 @@
+"""Refusals of the paged 4-bit cache's operators (no GPU: every call fails, or sizes its workspace, on the host before
+anything is launched), and the numpy form of the cache that the GPU tests go by."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import kv4_ref as ref
+
+qlin = pytest.importorskip("weight_streaming_gemv_gb300.qlin")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from weight_streaming_gemv_gb300 import build
+
+    build.build()
+
+
+def _kv(**kw):
+    c = qlin.QlinKv4C()
+    c.k, c.v, c.k_scale, c.v_scale, c.table = 4096, 8192, 16384, 32768, 64
+    c.table_stride, c.n_pages, c.page_rows, c.n_seqs, c.max_pages = 8, 16, 64, 2, 8
+    for n, v in kw.items():
+        setattr(c, n, v)
+    return c
+
+
+BAD_KV = [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(k_scale=None), 1), (dict(v_scale=None), 1), (dict(table=None), 1),
+    (dict(k=4104), 1), (dict(v=8200), 1), (dict(k_scale=16392), 1), (dict(v_scale=32776), 1), (dict(table=66), 1),
+    (dict(n_pages=0), 1), (dict(n_seqs=0), 1), (dict(max_pages=0), 1), (dict(table_stride=7), 1),
+    (dict(page_rows=8), 2), (dict(page_rows=48), 2), (dict(page_rows=512), 2), (dict(page_rows=0), 2),
+    (dict(n_pages=1 << 30), 2), (dict(max_pages=1 << 28, table_stride=1 << 28), 2),
+]
+
+
+def _append(**kw):
+    a = dict(kv=_kv(), k=16, v=32, kv_stride=256, q=48, q_stride=1024, q_out=64, cos=80, sin=96, rope_rows=128,
+             positions=4, seqs=8, n_lanes=2, n_heads=4, n_kv=1, head_dim=256, status=None)
+    a.update(kw)
+    kv = ctypes.byref(a["kv"]) if a["kv"] is not None else None
+    return qlin.lib().qlin_kv4_append(kv, a["k"], a["v"], a["kv_stride"], a["q"], a["q_stride"], a["q_out"], a["cos"],
+                                      a["sin"], a["rope_rows"], a["positions"], a["seqs"], a["n_lanes"], a["n_heads"],
+                                      a["n_kv"], a["head_dim"], a["status"], None)
+
+
+@pytest.mark.parametrize("bad,status", [(dict(kv=_kv(**b)), s) for b, s in BAD_KV] + [
+    (dict(kv=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(q=None), 1), (dict(q_out=None), 1),
+    (dict(cos=None), 1), (dict(sin=None), 1), (dict(positions=None), 1), (dict(seqs=None), 1),
+    (dict(k=20), 1), (dict(v=40), 1), (dict(q=52), 1), (dict(q_out=72), 1), (dict(cos=88), 1), (dict(sin=100), 1),
+    (dict(positions=6), 1), (dict(seqs=9), 1), (dict(status=3), 1),
+    (dict(n_lanes=0), 1), (dict(n_lanes=65537), 2), (dict(n_heads=0), 1), (dict(n_kv=0), 1), (dict(rope_rows=0), 1),
+    (dict(kv_stride=252), 1), (dict(kv_stride=258), 1), (dict(q_stride=1020), 1), (dict(q_stride=1026), 1),
+    (dict(q_out=48, q_stride=1028), 1), (dict(head_dim=32), 2), (dict(head_dim=96), 2), (dict(head_dim=512), 2),
+])
+def test_append_refuses(bad, status):
+    assert _append(**bad) == status
+    assert qlin.lib().qlin_last_error().decode().startswith("qlin_kv4_append")
+
+
+def _read(**kw):
+    a = dict(kv=_kv(), positions=4, seqs=8, n_lanes=2, n_kv=1, head_dim=256, k=16, v=32, status=None)
+    a.update(kw)
+    kv = ctypes.byref(a["kv"]) if a["kv"] is not None else None
+    return qlin.lib().qlin_kv4_read(kv, a["positions"], a["seqs"], a["n_lanes"], a["n_kv"], a["head_dim"], a["k"], a["v"],
+                                    a["status"], None)
+
+
+@pytest.mark.parametrize("bad,status", [(dict(kv=_kv(**b)), s) for b, s in BAD_KV] + [
+    (dict(kv=None), 1), (dict(positions=None), 1), (dict(seqs=None), 1), (dict(k=20), 1), (dict(v=40), 1),
+    (dict(positions=6), 1), (dict(seqs=9), 1), (dict(status=3), 1), (dict(n_lanes=0), 1),
+    (dict(n_lanes=(1 << 20) + 1), 2), (dict(n_kv=0), 1), (dict(head_dim=16), 2),
+])
+def test_read_refuses(bad, status):
+    assert _read(**bad) == status
+    assert qlin.lib().qlin_last_error().decode().startswith("qlin_kv4_read")
+
+
+def _attend(**kw):
+    a = dict(q=16, kv=_kv(), positions=32, seqs=48, n_lanes=2, n_heads=4, n_kv=1, head_dim=256, window=0, sinks=0,
+             out=64, status=None, ws=80, bytes=1 << 40)
+    a.update(kw)
+    kv = ctypes.byref(a["kv"]) if a["kv"] is not None else None
+    return qlin.lib().qlin_attention_kv4(a["q"], kv, a["positions"], a["seqs"], a["n_lanes"], a["n_heads"], a["n_kv"],
+                                         a["head_dim"], a["window"], a["sinks"], a["out"], a["status"], a["ws"],
+                                         a["bytes"], None)
+
+
+@pytest.mark.parametrize("bad,status", [(dict(kv=_kv(**b)), s) for b, s in BAD_KV] + [
+    (dict(q=None), 1), (dict(kv=None), 1), (dict(positions=None), 1), (dict(seqs=None), 1), (dict(out=None), 1),
+    (dict(ws=None), 1), (dict(bytes=16), 1), (dict(q=24), 1), (dict(out=72), 1), (dict(ws=88), 1),
+    (dict(positions=33), 1), (dict(seqs=49), 1), (dict(status=50), 1),
+    (dict(n_lanes=0), 1), (dict(n_lanes=4097), 2), (dict(n_heads=3, n_kv=2), 1), (dict(n_kv=0), 1), (dict(n_heads=0), 1),
+    (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(head_dim=32), 2), (dict(head_dim=512), 2),
+])
+def test_attention_refuses(bad, status):
+    assert _attend(**bad) == status
+    assert qlin.lib().qlin_last_error().decode().startswith("qlin_attention_kv4")
+
+
+def test_workspace_sizes():
+    size = qlin.qlin_attention_kv4_workspace_size
+    assert size(1, 4, 1, 256) > 0 and size(4096, 32, 4, 128) > 0
+    for bad in ((0, 4, 1, 256), (4097, 4, 1, 256), (1, 3, 2, 256), (1, 4, 0, 256), (1, 4, 1, 48), (1, 0, 1, 64)):
+        assert size(*bad) == 0
+
+
+def test_binding_checks_tensors():
+    torch = pytest.importorskip("torch")
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    k, sc, t = u8(3, 2, 16, 64), u8(3, 2, 16, 4), torch.zeros((5, 2), dtype=torch.int32)
+    c = qlin.kv4_cache(k, k.clone(), sc, sc.clone(), t)
+    assert (c.n_pages, c.page_rows, c.n_seqs, c.max_pages, c.table_stride) == (3, 16, 5, 2, 2)
+    assert qlin.kv4_cache(k, k, sc, sc, torch.zeros((5, 8), dtype=torch.int32)[:, :2]).table_stride == 8
+    for bad in ((k, k, sc, u8(3, 2, 16, 2), t), (k, u8(3, 2, 16, 32), sc, sc, t), (k, k, u8(3, 1, 16, 4), sc, t),
+                (k, k, sc, sc, t.long()), (k, k, sc, sc, t[0]), (k[:, :, ::2], k, sc, sc, t), (k.float(), k, sc, sc, t),
+                (k, k, sc, sc, torch.zeros((2, 5), dtype=torch.int32).t())):
+        with pytest.raises(ValueError):
+            qlin.kv4_cache(*bad)
+
+
+def test_reference_format():
+    """the numpy cache: every byte's scale, rounding, packing there and back"""
+    assert SCALE_BITS(np.arange(256)).tolist() == ref.SCALES.tolist()
+    x = np.zeros((1, 64), np.float32)
+    x[0, :32] = np.linspace(-7, 7, 32)
+    x[0, 40] = 7 * 1.0625  # between the scales 1 and 1.125
+    code, b = ref.quantise(x)
+    assert ref.SCALES[b].tolist() == [[1.0, 1.125]] and code[0, 40] == round(7 * 1.0625 / 1.125)
+    assert code[0, 0] == -7 and code[0, 31] == 7 and (code[0, 32:40] == 0).all()
+    rng = np.random.default_rng(0)
+    c = rng.integers(-8, 8, (5, 128))
+    s = rng.integers(0, 256, (5, 4)).astype(np.uint8)
+    assert np.array_equal(ref.values(ref.pack(c), s), c * np.repeat(ref.SCALES[s], 32, -1))
+    assert ref.pack(np.array([[-8, -8, 7] + [-8] * 5])).tolist() == [[0xF0, 0, 0, 0]]
+
+
+def SCALE_BITS(b):
+    """an fp32 number's exponent and first three bits of mantissa, less a bias"""
+    return ((b + (106 << 3)) << 20).astype(np.uint32).view(np.float32).astype(np.float64)

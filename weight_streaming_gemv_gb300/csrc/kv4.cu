@@ -1,0 +1,220 @@
+// Appending keys and values to the paged cache of 4 bits a value, with the
+// position's rotation applied on the way (qlin_kv4_append), and reading rows
+// back as the values that they stand for (qlin_kv4_read).
+//
+// A head's row x of a lane at position p turns as
+//   x'[i] = x[i] cos_p[i] - x[i+h] sin_p[i],  x'[i+h] = x[i] sin_p[i] + x[i+h] cos_p[i],  h = head_dim / 2
+// and every 32 dims of a key or value are rounded to codes of one scale s, the
+// least number (8 + m) 2^(e-24) that is at least max|x'| / 7.
+//
+// Everything is read once and written once, so memory bounds it, and a launch
+// where there is little.  A thread takes four dims i .. i+3 and their partners
+// i+h .. i+h+3, so that a rotation needs no other thread and may be in place;
+// the eight threads of four low dims each are the 32 of one scale, as are their
+// eight partners, and two neighbours' codes make a word.
+#include "kv4.cuh"
+#include "launch.cuh"
+#include "stream.cuh"
+
+namespace qlin {
+namespace {
+
+constexpr int kKv4Threads = 256;
+constexpr int kKv4MaxLanes = 65536, kKv4MaxRead = 1 << 20;
+
+struct AppendArgs {
+    qlin_kv4 kv;
+    const float *k, *v, *q;
+    int64_t kv_stride, q_stride;
+    float *q_out;
+    const float *cos_t, *sin_t;
+    int rope_rows;
+    const int32_t *positions, *seqs;
+    int n_lanes, n_heads, n_kv, hd;
+    int32_t *status;
+};
+
+// Four dims as codes: bits 0 .. 15 of the low and of the high halves' nibbles
+// that these four have in their word (the first four dims of the word in the
+// low byte of each half; the other thread's are shifted by 8).
+__device__ __forceinline__ uint32_t code4(const float (&x)[4], float s) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        float r = rintf(__fdiv_rn(x[j], s));
+        r = fminf(fmaxf(r, -7.0f), 7.0f);
+        const uint32_t c = x[j] != x[j] ? 8u : (uint32_t)((int)r + 8);
+        w |= c << (4 * (j >> 1) + 16 * (j & 1));
+    }
+    return w;
+}
+
+__device__ __forceinline__ float top8(const float (&x)[4]) {
+    // (fmaxf passes over a NaN)
+    float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    return m == m ? m : 0.0f;
+}
+
+__device__ __forceinline__ bool finite4(const float (&x)[4]) {
+    bool ok = true;
+#pragma unroll
+    for (int j = 0; j < 4; j++) ok = ok && fabsf(x[j]) < __int_as_float(0x7f800000);
+    return ok;
+}
+
+// per: threads to a head's row.  The rows of a lane: the queries', then the
+// keys', then the values'.
+__global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const __grid_constant__ AppendArgs A) {
+    const int per = A.hd / 8, heads = A.q ? A.n_heads : 0, rows = heads + 2 * A.n_kv;
+    const int64_t at = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x, total = (int64_t)A.n_lanes * rows * per;
+    const bool on = at < total;
+    const int64_t item = (on ? at : 0) / per;
+    const int j = (int)(at % per), lane = (int)(item / rows), row = (int)(item % rows);
+    const int what = row < heads ? 0 : row < heads + A.n_kv ? 1 : 2;  // query, key, value
+    const int head = what == 0 ? row : row - heads - (what - 1) * A.n_kv;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int p = A.positions[lane];
+    const bool turned = A.cos_t && what < 2;
+    int64_t place = kv4_row(A.kv, A.n_kv, p, A.seqs[lane]);
+    if (place >= 0 && A.cos_t && p >= A.rope_rows) place = -2;
+    if (on && place == -2 && row == 0 && j == 0) raise_status(A.status, kStatusKv4Lane);
+    const bool live = on && place >= 0;
+    float lo[4] = {}, hi[4] = {};
+    if (live) {
+        const float *src = what == 0 ? A.q + lane * A.q_stride : (what == 1 ? A.k : A.v) + lane * A.kv_stride;
+        src += head * A.hd + 4 * j;
+        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + A.hd / 2);
+        lo[0] = a.x, lo[1] = a.y, lo[2] = a.z, lo[3] = a.w, hi[0] = b.x, hi[1] = b.y, hi[2] = b.z, hi[3] = b.w;
+        if (turned) {
+            const int64_t o = (int64_t)p * (A.hd / 2) + 4 * j;
+            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(A.cos_t + o));
+            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(A.sin_t + o));
+            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float x = lo[e], y = hi[e];
+                lo[e] = __fsub_rn(__fmul_rn(x, c[e]), __fmul_rn(y, s[e]));
+                hi[e] = __fadd_rn(__fmul_rn(x, s[e]), __fmul_rn(y, c[e]));
+            }
+        }
+    }
+    if (on && what == 0) {
+        float *to = A.q_out + ((int64_t)lane * A.n_heads + head) * A.hd + 4 * j;
+        *reinterpret_cast<float4 *>(to) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<float4 *>(to + A.hd / 2) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    }
+    // (whole warps from here on: a row's threads are 8, 16 or 32 of one warp)
+    const uint32_t bl = kv4_scale_byte(__fdiv_rn(top8(lo), 7.0f)), bh = kv4_scale_byte(__fdiv_rn(top8(hi), 7.0f));
+    const uint32_t l = code4(lo, kv4_scale(bl)), h = code4(hi, kv4_scale(bh));
+    // the even thread writes the low dims' word, the odd one the high dims'
+    const bool odd = j & 1;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? l : h, 1);
+    const uint32_t word = odd ? other | h << 8 : l | other << 8;
+    if (live && what > 0) {
+        const int64_t r = place + (int64_t)head * A.kv.page_rows;
+        uint8_t *code = static_cast<uint8_t *>(what == 1 ? A.kv.k : A.kv.v) + r * (A.hd / 2);
+        uint8_t *sc = static_cast<uint8_t *>(what == 1 ? A.kv.k_scale : A.kv.v_scale) + r * (A.hd / kKv4Group);
+        *reinterpret_cast<uint32_t *>(code + (odd ? A.hd / 4 : 0) + (j >> 1) * 4) = word;
+        if ((j & 7) < 2) sc[(odd ? A.hd / 64 : 0) + (j >> 3)] = (uint8_t)(odd ? bh : bl);
+        if (!finite4(lo) || !finite4(hi)) raise_status(A.status, kStatusKv4NotFinite);
+    }
+}
+
+struct ReadArgs {
+    qlin_kv4 kv;
+    const int32_t *positions, *seqs;
+    int n_lanes, n_kv, hd;
+    float *k_out, *v_out;
+    int32_t *status;
+};
+
+// a thread: a word of eight codes
+__global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const __grid_constant__ ReadArgs A) {
+    const int per = A.hd / 8;
+    const int64_t at = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x;
+    if (at >= (int64_t)A.n_lanes * 2 * A.n_kv * per) return;
+    const int w = (int)(at % per), head = (int)(at / per % A.n_kv), which = (int)(at / per / A.n_kv % 2);
+    const int lane = (int)(at / per / A.n_kv / 2);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t place = kv4_row(A.kv, A.n_kv, A.positions[lane], A.seqs[lane]);
+    if (place == -2 && which == 0 && head == 0 && w == 0) raise_status(A.status, kStatusKv4Lane);
+    float *to = which ? A.v_out : A.k_out;
+    if (!to) return;
+    float x[8] = {};
+    if (place >= 0) {
+        const int64_t r = place + (int64_t)head * A.kv.page_rows;
+        const uint32_t word = *reinterpret_cast<const uint32_t *>(
+            static_cast<const uint8_t *>(which ? A.kv.v : A.kv.k) + r * (A.hd / 2) + 4 * w);
+        const float s = kv4_scale(static_cast<const uint8_t *>(which ? A.kv.v_scale : A.kv.k_scale)[r * (A.hd / kKv4Group) + w / 4]);
+#pragma unroll
+        for (int d = 0; d < 8; d++) x[d] = __fmul_rn((float)((int)(word >> (4 * (d >> 1) + 16 * (d & 1)) & 15u) - 8), s);
+    }
+    to += ((int64_t)lane * A.n_kv + head) * A.hd + 8 * w;
+    *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" {
+
+qlin_status qlin_kv4_append(const qlin_kv4 *kv, const float *k, const float *v, int64_t kv_stride, const float *q,
+                            int64_t q_stride, float *q_out, const float *cos_t, const float *sin_t, int rope_rows,
+                            const int32_t *positions, const int32_t *seqs, int n_lanes, int n_heads, int n_kv,
+                            int head_dim, int32_t *status_word, qlin_stream_t stream) {
+    qlin::clear_error();
+    const char *fn = "qlin_kv4_append";
+    if (qlin_status st = check_kv4(fn, kv, n_kv, head_dim)) return st;
+    QLIN_REQUIRE(k && v && positions && seqs && !q == !q_out && !cos_t == !sin_t, QLIN_ERR_INVALID_ARG,
+                 "%s: null pointer (q and q_out, cos_t and sin_t go together)", fn);
+    QLIN_REQUIRE(n_lanes >= 1 && (!q || n_heads >= 1) && (!cos_t || rope_rows >= 1), QLIN_ERR_INVALID_ARG,
+                 "%s: n_lanes %d, n_heads %d, rope_rows %d", fn, n_lanes, n_heads, rope_rows);
+    QLIN_REQUIRE(n_lanes <= kKv4MaxLanes && (!q || n_heads <= 65535) && n_kv <= 65535, QLIN_ERR_UNSUPPORTED,
+                 "%s: more than %d lanes (%d) or 65535 heads", fn, kKv4MaxLanes, n_lanes);
+    QLIN_REQUIRE(aligned16(k) && aligned16(v) && aligned16(q) && aligned16(q_out) && aligned16(cos_t) && aligned16(sin_t) &&
+                     aligned4(positions) && aligned4(seqs) && aligned4(status_word),
+                 QLIN_ERR_INVALID_ARG, "%s: a pointer is not 16-byte aligned (positions, seqs, status_word: 4)", fn);
+    const int64_t most = (int64_t)1 << 40;
+    QLIN_REQUIRE(kv_stride >= (int64_t)n_kv * head_dim && kv_stride % 4 == 0 && kv_stride < most &&
+                     (!q || (q_stride >= (int64_t)n_heads * head_dim && q_stride % 4 == 0 && q_stride < most)),
+                 QLIN_ERR_INVALID_ARG, "%s: kv_stride %lld, q_stride %lld: a lane's rows at least, multiples of 4", fn,
+                 (long long)kv_stride, (long long)q_stride);
+    QLIN_REQUIRE(!q || q != q_out || q_stride == (int64_t)n_heads * head_dim, QLIN_ERR_INVALID_ARG,
+                 "%s: in place with a q_stride of %lld", fn, (long long)q_stride);
+    AppendArgs A{*kv, k, v, q, kv_stride, q_stride, q_out, cos_t, sin_t, rope_rows, positions, seqs, n_lanes, n_heads,
+                 n_kv, head_dim, status_word};
+    const int64_t threads = (int64_t)n_lanes * ((q ? n_heads : 0) + 2 * n_kv) * (head_dim / 8);
+    const int64_t blocks = (threads + kKv4Threads - 1) / kKv4Threads;
+    QLIN_REQUIRE(blocks < (int64_t)1 << 31, QLIN_ERR_UNSUPPORTED, "%s: too many rows", fn);
+    void *args[] = {(void *)&A};
+    return launch_pdl((const void *)kv4_append_kernel, dim3((unsigned)blocks), dim3(kKv4Threads), 0, (cudaStream_t)stream,
+                      args, "kv4_append_kernel");
+}
+
+qlin_status qlin_kv4_read(const qlin_kv4 *kv, const int32_t *positions, const int32_t *seqs, int n_lanes, int n_kv,
+                          int head_dim, float *k_out, float *v_out, int32_t *status_word, qlin_stream_t stream) {
+    qlin::clear_error();
+    const char *fn = "qlin_kv4_read";
+    if (qlin_status st = check_kv4(fn, kv, n_kv, head_dim)) return st;
+    QLIN_REQUIRE(positions && seqs, QLIN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    QLIN_REQUIRE(n_lanes >= 1, QLIN_ERR_INVALID_ARG, "%s: n_lanes %d", fn, n_lanes);
+    QLIN_REQUIRE(n_lanes <= kKv4MaxRead && n_kv <= 65535, QLIN_ERR_UNSUPPORTED, "%s: more than %d lanes (%d) or 65535 heads",
+                 fn, kKv4MaxRead, n_lanes);
+    QLIN_REQUIRE(aligned16(k_out) && aligned16(v_out) && aligned4(positions) && aligned4(seqs) && aligned4(status_word),
+                 QLIN_ERR_INVALID_ARG, "%s: a pointer is not 16-byte aligned (positions, seqs, status_word: 4)", fn);
+    ReadArgs A{*kv, positions, seqs, n_lanes, n_kv, head_dim, k_out, v_out, status_word};
+    const int64_t blocks = ((int64_t)n_lanes * 2 * n_kv * (head_dim / 8) + kKv4Threads - 1) / kKv4Threads;
+    QLIN_REQUIRE(blocks < (int64_t)1 << 31, QLIN_ERR_UNSUPPORTED, "%s: too many rows", fn);
+    void *args[] = {(void *)&A};
+    return launch_pdl((const void *)kv4_read_kernel, dim3((unsigned)blocks), dim3(kKv4Threads), 0, (cudaStream_t)stream, args,
+                      "kv4_read_kernel");
+}
+
+}  // extern "C"

@@ -66,6 +66,17 @@ class QlinKvC(ctypes.Structure):
 KV_F32, KV_BF16 = 0, 1
 
 
+class QlinKv4C(ctypes.Structure):
+    """Mirror of ``qlin_kv4``."""
+
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("n_pages", ctypes.c_int32), ("page_rows", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+    ]
+
+
 class T158PromptsC(ctypes.Structure):
     """Mirror of ``t158_prompts``."""
 
@@ -143,6 +154,11 @@ SIGNATURES = {
     "qlin_beam_select_workspace_size": ([_I, _I, _I, _I], _SZ),
     "qlin_beam_select": ([_P, _I64, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P], _ST),
     "qlin_beam_reorder": ([_P, _I64, _I64, _I, _I64, _I, _P, _P, _I, _I, _P, _P], _ST),
+    "qlin_kv4_append": ([ctypes.POINTER(QlinKv4C), _P, _P, _I64, _P, _I64, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P,
+                         _P], _ST),
+    "qlin_kv4_read": ([ctypes.POINTER(QlinKv4C), _P, _P, _I, _I, _I, _P, _P, _P, _P], _ST),
+    "qlin_attention_kv4_workspace_size": ([_I, _I, _I, _I], _SZ),
+    "qlin_attention_kv4": ([_P, ctypes.POINTER(QlinKv4C), _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P], _ST),
 }
 
 
@@ -545,3 +561,47 @@ def qlin_beam_reorder(cache, seq_stride, plane_stride, n_planes, row_bytes, max_
     _check("qlin_beam_reorder", lib().qlin_beam_reorder(
         _ptr(cache), seq_stride, plane_stride, n_planes, row_bytes, max_rows, _ptr(parents), _ptr(n_rows), n_groups,
         beams, _ptr(status_word), _stream(stream)))
+
+
+def kv4_cache(k, v, k_scale, v_scale, table) -> QlinKv4C:
+    """The ``qlin_kv4`` of four contiguous uint8 tensors, codes [n_pages][n_kv][page_rows][head_dim / 2] and scales
+    [n_pages][n_kv][page_rows][head_dim / 32], and an int32 table [n_seqs][pages of a sequence] (any stride between
+    its rows), which the caller keeps."""
+    for t in (k, v, k_scale, v_scale):
+        if t.dim() != 4 or str(t.dtype) != "torch.uint8" or not t.is_contiguous() or t.shape[:3] != k.shape[:3]:
+            raise ValueError("kv4_cache: codes and scales are contiguous uint8 tensors [n_pages][n_kv][page_rows][...]")
+    if v.shape != k.shape or k.shape[3] != 16 * k_scale.shape[3] or v_scale.shape != k_scale.shape:
+        raise ValueError(f"kv4_cache: codes {tuple(k.shape)}, {tuple(v.shape)} and scales {tuple(k_scale.shape)}, "
+                         f"{tuple(v_scale.shape)}")
+    if table.dim() != 2 or str(table.dtype) != "torch.int32" or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("kv4_cache: the table is int32 [n_seqs][pages], its rows contiguous")
+    c = QlinKv4C()
+    c.k, c.v, c.k_scale, c.v_scale = k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
+    c.table, c.table_stride = table.data_ptr(), max(table.stride(0), table.shape[1])
+    c.n_pages, c.page_rows = k.shape[0], k.shape[2]
+    c.n_seqs, c.max_pages = table.shape
+    return c
+
+
+def qlin_kv4_append(kv: QlinKv4C, k, v, kv_stride, q, q_stride, q_out, cos_t, sin_t, rope_rows, positions, seqs,
+                    n_lanes, n_heads, n_kv, head_dim, status_word=None, stream=None):
+    _check("qlin_kv4_append", lib().qlin_kv4_append(
+        ctypes.byref(kv), _ptr(k), _ptr(v), kv_stride, _ptr(q), q_stride, _ptr(q_out), _ptr(cos_t), _ptr(sin_t),
+        rope_rows, _ptr(positions), _ptr(seqs), n_lanes, n_heads, n_kv, head_dim, _ptr(status_word), _stream(stream)))
+
+
+def qlin_kv4_read(kv: QlinKv4C, positions, seqs, n_lanes, n_kv, head_dim, k_out, v_out, status_word=None, stream=None):
+    _check("qlin_kv4_read", lib().qlin_kv4_read(
+        ctypes.byref(kv), _ptr(positions), _ptr(seqs), n_lanes, n_kv, head_dim, _ptr(k_out), _ptr(v_out),
+        _ptr(status_word), _stream(stream)))
+
+
+def qlin_attention_kv4_workspace_size(n_lanes, n_heads, n_kv, head_dim) -> int:
+    return int(lib().qlin_attention_kv4_workspace_size(n_lanes, n_heads, n_kv, head_dim))
+
+
+def qlin_attention_kv4(q, kv: QlinKv4C, positions, seqs, n_lanes, n_heads, n_kv, head_dim, window, sinks, out,
+                       status_word, workspace, workspace_bytes, stream=None):
+    _check("qlin_attention_kv4", lib().qlin_attention_kv4(
+        _ptr(q), ctypes.byref(kv), _ptr(positions), _ptr(seqs), n_lanes, n_heads, n_kv, head_dim, window, sinks,
+        _ptr(out), _ptr(status_word), _ptr(workspace), workspace_bytes, _stream(stream)))
