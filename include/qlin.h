@@ -736,6 +736,33 @@ qlin_status qlin_attention_kv4(const float *q, const qlin_kv4 *kv, const int32_t
                                int n_lanes, int n_heads, int n_kv, int head_dim, int window, int sinks, float *out,
                                int32_t *status_word, void *workspace, size_t workspace_bytes, qlin_stream_t stream);
 
+/* Draws the next tokens.  Row r of logits (device fp32, rows row_stride floats
+ * apart) has vocab words of weight w_v = exp((logits[v] - largest) / T), T =
+ * temperature[r].  The words in descending order of their logits (ties: the
+ * lower word first) are cut three times: behind the top_k[r]-th (0 or less, or
+ * vocab and more: not at all); then behind the first at which the running sum
+ * of the weights reaches top_p[r] times the sum over what top-k left (1 or
+ * more: not at all; the first word always stays); then where w_v is below
+ * min_p[r] (0 or less: not at all; above 1 counts as 1).  The token is the first
+ * word, by number, at which the running sum of the weights left exceeds u[r]
+ * times their sum (u: given random numbers in [0, 1); from 1 on the last word
+ * with a weight).  T <= 0 takes the first of the largest logits, as
+ * qlin_lm_head_argmax.  temperature, top_k, top_p and min_p: device [n_rows], or
+ * NULL for 1, 0, 1 and 0 everywhere.
+ * tokens: device int32 [n_rows]; probs: device fp32 [n_rows], the token's share
+ * of the weights left, or NULL; kept: device int32 [n_rows], how many words were
+ * left, or NULL.  Words of minus infinity are never taken nor counted.  A row
+ * that holds a NaN or plus infinity or nothing but minus infinity, or whose
+ * temperature is a NaN, gives -1, 0 and 0.
+ * Weights are whole numbers of 2^-44 of the largest's (of 2^-(62 - b) where
+ * vocab takes b > 18 bits), good to about 2^-38 of themselves, and their sums
+ * exact: the same inputs give the same tokens.
+ * n_rows: 1..65535; vocab: up to 2^24.  Pointers 4-byte aligned (logits 16-byte
+ * aligned with row_stride % 4 == 0 are read fastest). */
+qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u, const float *temperature,
+                        const int32_t *top_k, const float *top_p, const float *min_p, int n_rows, int vocab,
+                        int32_t *tokens, float *probs, int32_t *kept, qlin_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

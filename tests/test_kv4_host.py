@@ -139,3 +139,21 @@ def test_reference_format():
 def SCALE_BITS(b):
     """an fp32 number's exponent and first three bits of mantissa, less a bias"""
     return ((b + (106 << 3)) << 20).astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def _sample(**kw):
+    a = dict(logits=16, stride=100, u=4, t=8, k=12, p=20, m=24, rows=2, vocab=100, tokens=28, probs=32, kept=36)
+    a.update(kw)
+    return qlin.lib().qlin_sample(a["logits"], a["stride"], a["u"], a["t"], a["k"], a["p"], a["m"], a["rows"], a["vocab"],
+                                  a["tokens"], a["probs"], a["kept"], None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(logits=None), 1), (dict(u=None), 1), (dict(tokens=None), 1), (dict(rows=0), 1), (dict(vocab=0), 1),
+    (dict(stride=99), 1), (dict(rows=65536), 2), (dict(vocab=(1 << 24) + 1, stride=1 << 25), 2), (dict(stride=1 << 40), 2),
+    (dict(logits=18), 1), (dict(u=5), 1), (dict(t=9), 1), (dict(k=13), 1), (dict(p=21), 1), (dict(m=26), 1),
+    (dict(tokens=29), 1), (dict(probs=33), 1), (dict(kept=37), 1),
+])
+def test_sample_refuses(bad, status):
+    assert _sample(**bad) == status
+    assert qlin.lib().qlin_last_error().decode().startswith("qlin_sample")

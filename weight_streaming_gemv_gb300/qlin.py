@@ -157,6 +157,7 @@ SIGNATURES = {
     "qlin_kv4_append": ([ctypes.POINTER(QlinKv4C), _P, _P, _I64, _P, _I64, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P,
                          _P], _ST),
     "qlin_kv4_read": ([ctypes.POINTER(QlinKv4C), _P, _P, _I, _I, _I, _P, _P, _P, _P], _ST),
+    "qlin_sample": ([_P, _I64, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P], _ST),
     "qlin_attention_kv4_workspace_size": ([_I, _I, _I, _I], _SZ),
     "qlin_attention_kv4": ([_P, ctypes.POINTER(QlinKv4C), _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P], _ST),
 }
@@ -605,3 +606,10 @@ def qlin_attention_kv4(q, kv: QlinKv4C, positions, seqs, n_lanes, n_heads, n_kv,
     _check("qlin_attention_kv4", lib().qlin_attention_kv4(
         _ptr(q), ctypes.byref(kv), _ptr(positions), _ptr(seqs), n_lanes, n_heads, n_kv, head_dim, window, sinks,
         _ptr(out), _ptr(status_word), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qlin_sample(logits, row_stride, u, temperature, top_k, top_p, min_p, n_rows, vocab, tokens, probs=None, kept=None,
+                stream=None):
+    _check("qlin_sample", lib().qlin_sample(
+        _ptr(logits), row_stride, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), n_rows, vocab,
+        _ptr(tokens), _ptr(probs), _ptr(kept), _stream(stream)))
