@@ -672,8 +672,8 @@ qlin_status qlin_beam_reorder(void *cache, int64_t seq_stride, int64_t plane_str
  * 32-bit word w of a row: dim 8w + 2i in its bits 4i .. 4i+3, dim 8w + 2i + 1
  * in its bits 16+4i .. 19+4i.  Every content of a page stands for finite
  * values, so pages need no clearing.
- * page_rows: 16, 32, 64, 128 or 256.  head_dim: 64, 128 or 256.  k, v, k_scale,
- * v_scale: device, 16-byte aligned; table: device int32 [n_seqs][table_stride],
+ * page_rows: 16, 32, 64, 128 or 256.  head_dim: 64, 128 or 256.  k and v:
+ * device, 32-byte aligned, k_scale and v_scale 16-byte; table: device int32 [n_seqs][table_stride],
  * table_stride >= max_pages, 4-byte aligned.  max_pages * page_rows is at most
  * 2^30, n_pages * n_kv * page_rows below 2^31.  Entries of the table behind a
  * sequence's last page, or before its window, are never read.
@@ -735,6 +735,12 @@ size_t qlin_attention_kv4_workspace_size(int n_lanes, int n_heads, int n_kv, int
 qlin_status qlin_attention_kv4(const float *q, const qlin_kv4 *kv, const int32_t *positions, const int32_t *seqs,
                                int n_lanes, int n_heads, int n_kv, int head_dim, int window, int sinks, float *out,
                                int32_t *status_word, void *workspace, size_t workspace_bytes, qlin_stream_t stream);
+
+/* Which of two ways such a call goes, by its sizes alone: 1: on the tensor
+ * cores; 0: little work, on the CUDA cores; below 0: a call of these sizes is
+ * refused with the status that is its negative (qlin_last_error). */
+int qlin_attention_kv4_on_tensor_cores(const qlin_kv4 *kv, int n_lanes, int n_heads, int n_kv, int head_dim, int window,
+                                       int sinks);
 
 /* Draws the next tokens.  Row r of logits (device fp32, rows row_stride floats
  * apart) has vocab words of weight w_v = exp((logits[v] - largest) / T), T =

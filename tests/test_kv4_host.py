@@ -28,7 +28,7 @@ def _kv(**kw):
 
 BAD_KV = [
     (dict(k=None), 1), (dict(v=None), 1), (dict(k_scale=None), 1), (dict(v_scale=None), 1), (dict(table=None), 1),
-    (dict(k=4104), 1), (dict(v=8200), 1), (dict(k_scale=16392), 1), (dict(v_scale=32776), 1), (dict(table=66), 1),
+    (dict(k=4112), 1), (dict(v=8208), 1), (dict(k_scale=16392), 1), (dict(v_scale=32776), 1), (dict(table=66), 1),
     (dict(n_pages=0), 1), (dict(n_seqs=0), 1), (dict(max_pages=0), 1), (dict(table_stride=7), 1),
     (dict(page_rows=8), 2), (dict(page_rows=48), 2), (dict(page_rows=512), 2), (dict(page_rows=0), 2),
     (dict(n_pages=1 << 30), 2), (dict(max_pages=1 << 28, table_stride=1 << 28), 2),
@@ -97,6 +97,17 @@ def _attend(**kw):
 def test_attention_refuses(bad, status):
     assert _attend(**bad) == status
     assert qlin.lib().qlin_last_error().decode().startswith("qlin_attention_kv4")
+
+
+def test_which_way():
+    """little work goes to the CUDA cores, more of any kind to the tensor cores"""
+    on = qlin.qlin_attention_kv4_on_tensor_cores
+    kv = _kv(max_pages=512, table_stride=512)
+    assert not on(kv, 1, 4, 1, 256, 512, 4) and on(kv, 64, 4, 1, 256, 0, 0) and on(kv, 512, 4, 1, 256, 512, 0)
+    with pytest.raises(qlin.QlinError):
+        on(kv, 0, 4, 1, 256, 0, 0)
+    with pytest.raises(qlin.QlinError):
+        on(_kv(page_rows=24), 1, 4, 1, 256, 0, 0)
 
 
 def test_workspace_sizes():

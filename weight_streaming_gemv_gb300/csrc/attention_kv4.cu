@@ -15,15 +15,12 @@
 // second kernel joins by the weights 2^(maximum - largest maximum).
 #include <cmath>
 
+#include "attention_lanes.cuh"
 #include "kv4.cuh"
-#include "launch.cuh"
-#include "stream.cuh"
-#include "tcgen05.cuh"
 
 namespace qlin {
 namespace {
 
-constexpr int kMaxLanes = 4096;
 constexpr int kThreads = 256;
 constexpr int kKeys = 64;          // keys of a step
 constexpr int kParts = kThreads / kKeys;
@@ -41,11 +38,6 @@ struct Kv4Args {
     float c;    // log2(e) / sqrt(hd)
 };
 
-__device__ __forceinline__ float kv4_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 constexpr float kInf = __builtin_huge_valf();
 
 // What lane i sees: keys j < sk and lo <= j <= p (sk <= lo), `count` of them; 0 if it is none.
@@ -169,11 +161,11 @@ __global__ void __launch_bounds__(kThreads) kv4_few_kernel(const __grid_constant
             const float a = ws[lane][warp], b = ws[lane + 32][warp], old = sm[warp];
             const float top = fmaxf(old, warp_max(fmaxf(a, b)));
             const float base = top > -kInf ? top : 0.0f;  // (nothing seen yet)
-            const float ea = kv4_ex2(__fsub_rn(a, base)), eb = kv4_ex2(__fsub_rn(b, base));
+            const float ea = al_ex2(__fsub_rn(a, base)), eb = al_ex2(__fsub_rn(b, base));
             const float sum = warp_psum(__fadd_rn(ea, eb));
             ws[lane][warp] = ea, ws[lane + 32][warp] = eb;
             if (lane == 0) {
-                const float f = old > -kInf ? kv4_ex2(__fsub_rn(old, base)) : 0.0f;
+                const float f = old > -kInf ? al_ex2(__fsub_rn(old, base)) : 0.0f;
                 sl[warp] = __fmaf_rn(sl[warp], f, sum);
                 sm[warp] = top, sa[warp] = f;
             }
@@ -248,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) kv4_few_merge_kernel(const __grid_co
     float l = 0.0f;
     for (int k = tid; k < n; k += kThreads) {
         const float2 v = __ldcg(&ml[row0 + k]);
-        w[k] = kv4_ex2(__fsub_rn(v.x, m));
+        w[k] = al_ex2(__fsub_rn(v.x, m));
         l += w[k] * v.y;
     }
     l = warp_psum(l);
@@ -278,35 +270,639 @@ __global__ void __launch_bounds__(kThreads) kv4_few_merge_kernel(const __grid_co
     }
 }
 
-// ------------------------------------------------------------------ host
-size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+// ------------------------------------------------------------------ the product
+constexpr int kR = 32;                // rows of a tile at most
+constexpr int kProd = 16;             // producer warps, in groups of four
+constexpr int kProd0 = 8;             // behind two warpgroups of the weights
+constexpr int kMma = kProd0 + kProd;  // the warp that issues the MMAs; then the ones that describe pieces and steps
+constexpr int kWalk = kMma + 1, kSteps = kMma + 2;
+constexpr int kTcThreads = 32 * (kMma + 4);
+constexpr int kVSlot = 16384;         // 64 keys x 128 dims
+constexpr int kMaxVSlots = 10, kKSlots = 8;
+constexpr int kStepRing = 4, kBadRing = 64;
+// tensor memory: S^T twice [2 kR], O^T's two halves of dims [2 kR] each, slices of K (128 keys x 64 dims)
+constexpr uint32_t kTmS = 0, kTmO = 4 * kR, kTmK = 8 * kR, kTmCols = 512;
+static_assert(kTmK + 32 * kKSlots <= kTmCols, "tensor memory");
+constexpr float kStale = 4.0f;        // how far a score may exceed the maximum in use
+constexpr float kUp = 2048.0f;        // weights are multiplied by this: below 2^15, and steps of 2^-35 of the largest
 
+// What the producers need to load a step's slices: chunk i's keys and chunk
+// i-1's values of a piece.
+struct __align__(16) KvStep {
+    int krow[8], vrow[8];        // per page of the chunk: the pool's row of its first key, -1: nothing to read
+    int kbase, vbase;            // the chunks' first keys; below 0: none
+    int any_lo, any_hi, sk;      // the keys that some row sees
+    int more;                    // 0: there are no more steps
+    int pad[2];
+};
+
+struct KvCtl {
+    uint64_t kfull[kKSlots], kempty[kKSlots], vfull[kMaxVSlots], vempty[kMaxVSlots];
+    uint64_t s_full[2], s_free[2], p_ready, q_ready, pv_done, drain;
+    uint64_t st_full[kStepRing], st_empty[kStepRing], pc_full[kPieceRing], pc_empty[kPieceRing];
+    KvStep step[kStepRing];
+    uint32_t bad[kBadRing];   // per chunk: pages that are out of range
+    int rowid[kR];            // lane * n_heads + head
+    int rowlo[kR], rowhi[kR]; // a row sees the keys <= rowhi that are > rowlo or first ones
+    float mc[kR], alpha[kR], qf[kR];
+    float red[4][kR];
+    float *optr[kR];
+    AlSelfPlan plan;
+    AlPiece piece[kPieceRing];
+    uint32_t tmem;
+    int abort;
+};
+
+struct KvLayout {  // in shared memory: the ring of V, the rows' q (per 64 dims the two terms' rows), the weights P
+    int q, qslice, p, slots;
+    __device__ __forceinline__ KvLayout(int rmax, int hd) {
+        const int Rc = rmax <= 16 ? 16 : 32;
+        qslice = 2 * Rc * 128;
+        const int qb = hd / 64 * qslice, pb = kChunk * 64 * (Rc / 16);
+        slots = min((kAlSmem - 1024 - (int)sizeof(KvCtl) - qb - pb) / kVSlot, kMaxVSlots);
+        q = slots * kVSlot;
+        p = q + qb;
+    }
+};
+static_assert(kAlSmem - 1024 - (int)sizeof(KvCtl) - 4 * 2 * 32 * 128 - 2 * kChunk * 64 >= 9 * kVSlot, "ring of nine");
+
+// D (tensor memory) (+)= A (tensor memory) x B (shared memory)
+__device__ __forceinline__ void kv_mma_ta(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {  // a in the low half
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+// two values as two pairs of fp16 terms: hi + lo is 22 bits of them, and steps of 2^-25 at least
+__device__ __forceinline__ void kv_split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = f16x2(a, b);
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    lo = f16x2(__fsub_rn(a, h.x), __fsub_rn(b, h.y));
+}
+// 32 bytes of codes and two scale bytes if on, else zeros
+__device__ __forceinline__ void kv_ld(const uint8_t *code, const uint8_t *scale, bool on, uint32_t (&w)[8], uint32_t &s) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) w[i] = 0;
+    uint16_t h = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %11, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%9];\n\t"
+        "@p ld.global.nc.b16 %8, [%10];\n\t}"
+        : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]), "+r"(w[4]), "+r"(w[5]), "+r"(w[6]), "+r"(w[7]), "+h"(h)
+        : "l"(code), "l"(scale), "r"((uint32_t)on));
+    s = h;
+}
+
+// Walks over the steps' slices that are one producer group's: of a step's K
+// and then V slices every fourth, counted on from step to step.
+struct KvSlices {
+    int st = 0, x = 0, cnt = 0;   // the step's place in the ring, the next slice in it, slices before it
+    uint32_t par = 0;
+    int kn = 0, vn = 0;           // K and V slices before the step
+    bool open = false;
+};
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+    kv4_attn_kernel(const __grid_constant__ AlArgs A, const __grid_constant__ AlDims D, const __grid_constant__ AlWs W,
+                    const __grid_constant__ qlin_kv4 kv) {
+    extern __shared__ uint8_t kv_raw[];
+    uint8_t *const smem = kv_raw + ((1024u - (smem_addr(kv_raw) & 1023u)) & 1023u);  // the swizzled operands' alignment
+    KvCtl &S = *reinterpret_cast<KvCtl *>(smem + (kAlSmem - 1024 - sizeof(KvCtl)) / 16 * 16);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hd = A.hd, nK = hd / 64, nDH = (hd + 127) / 128, nV = 2 * nDH;
+    if (warp == kMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&S.tmem)),
+                     "r"(kTmCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 32) {
+        for (int s = 0; s < kKSlots; s++) mbar_init(&S.kfull[s], 4), mbar_init(&S.kempty[s], 1);
+        for (int s = 0; s < kMaxVSlots; s++) mbar_init(&S.vfull[s], 4), mbar_init(&S.vempty[s], 1);
+        for (int s = 0; s < 2; s++) mbar_init(&S.s_full[s], 1), mbar_init(&S.s_free[s], 8);
+        mbar_init(&S.p_ready, 8), mbar_init(&S.q_ready, 8), mbar_init(&S.pv_done, 1), mbar_init(&S.drain, 1);
+        for (int s = 0; s < kStepRing; s++) mbar_init(&S.st_full[s], 1), mbar_init(&S.st_empty[s], kProd);
+        for (int s = 0; s < kPieceRing; s++) mbar_init(&S.pc_full[s], 1), mbar_init(&S.pc_empty[s], 8 + 2);
+        S.abort = 0;
+        fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan, and what the kernels before wrote
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    AlPlan P{W.head, W.first + blockIdx.x, W.tile_of, W.tiles};
+    if (A.n_lanes <= kSelfPlan) {
+        AlSelfScratch &x = *reinterpret_cast<AlSelfScratch *>(smem);  // (the ring is not in use yet)
+        if (tid < kSelfPlan) {
+            make_plan<kSelfPlan>(A, D, x.lane, x.red, &S.plan.head, &S.plan.first, blockIdx.x, x.tile_of, S.plan.tiles,
+                                 blockIdx.x == 0 ? A.status : nullptr);
+            fence_proxy_async_smem();
+        }
+        P = AlPlan{&S.plan.head, &S.plan.first, nullptr, S.plan.tiles};
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    const KvLayout L(P.head->rmax, hd);
+    const int slots = L.slots;
+    uint8_t *const ring = smem, *const qs = ring + L.q, *const ps = ring + L.p;
+    auto give_up = [&]() {
+        S.abort = 1;
+        raise_status(A.status, kStatusTimeout);
+    };
+
+    if (warp >= kProd0 && warp < kMma) {
+        // ---------------------------------------------------------- producers: a slice of K or V per group of four warps,
+        // 64 dims of a key per thread, three slices in registers on their way
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        const int pg = (warp - kProd0) >> 2, t = tid & 127;
+        const int lp = kv.page_rows >= kChunk ? 7 : 31 - __clz(kv.page_rows);
+        KvSlices c;
+        constexpr int kDepth = 3;
+        uint32_t w[kDepth][8], sc[kDepth];
+        int meta[kDepth];  // slice number * 2 + kind (0 K, 1 V); below 0: none
+        bool ok = true, more = true;
+        int have = 0;  // slices in registers
+        // The group's next slice, if its step is described by now or there is nothing else to do: the steps of the pieces
+        // to come may wait for slices that are still in registers here.
+        auto load = [&](uint32_t (&o)[8], uint32_t &s, int &m) {
+            m = -1;
+            while (more) {
+                KvStep &q = S.step[c.st];
+                if (!c.open) {
+                    if (have && !__all_sync(0xffffffffu, al_test(smem_addr(&S.st_full[c.st]), c.par))) return;
+                    if (!(ok = al_wait(&S.st_full[c.st], c.par, &S.abort)) || !q.more) {
+                        more = false;
+                        break;
+                    }
+                    c.open = true;
+                    c.x = (pg - c.cnt) & 3;
+                }
+                const int nk = q.kbase >= 0 ? nK : 0, nv = q.vbase >= 0 ? nV : 0;
+                if (c.x < nk + nv) {
+                    const bool v = c.x >= nk;
+                    const int e = v ? c.x - nk : c.x;
+                    // K: key t, dims 64 e ..; V: key t & 63 of half e / nDH, 64 dims of the 128 from 128 (e % nDH) on
+                    const int r = v ? (e / nDH) * 64 + (t & 63) : t, d = v ? (e % nDH) * 128 + (t >> 6) * 64 : 64 * e;
+                    const int key = (v ? q.vbase : q.kbase) + r, row0 = (v ? q.vrow : q.krow)[r >> lp];
+                    const int64_t row = row0 + (r & ((1 << lp) - 1));
+                    const bool on = row0 >= 0 && d < hd && key <= q.any_hi && (key > q.any_lo || key < q.sk);
+                    kv_ld(static_cast<const uint8_t *>(v ? kv.v : kv.k) + row * (hd / 2) + d / 2,
+                          static_cast<const uint8_t *>(v ? kv.v_scale : kv.k_scale) + row * (hd / 32) + d / 32, on, o, s);
+                    m = (v ? c.vn + e : c.kn + e) * 2 + v;
+                    c.x += 4;
+                    have++;
+                    return;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.st_empty[c.st]);
+                c.cnt += nk + nv, c.kn += nk, c.vn += nv;
+                c.open = false;
+                if (++c.st == kStepRing) c.st = 0, c.par ^= 1u;
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < kDepth; k++) load(w[k], sc[k], meta[k]);
+        while (ok && have) {
+#pragma unroll
+            for (int k = 0; k < kDepth; k++) {
+                if (meta[k] < 0) {
+                    load(w[k], sc[k], meta[k]);
+                    continue;
+                }
+                const int n = meta[k] >> 1;
+                const bool v = meta[k] & 1;
+                const int slot = v ? n % slots : n % kKSlots, round = v ? n / slots : n / kKSlots;
+                if (round && !al_wait(v ? &S.vempty[slot] : &S.kempty[slot], (uint32_t)(round - 1) & 1u, &S.abort)) {
+                    ok = false;
+                    break;
+                }
+                __half2 s0, m0, s1, m1;
+                kv4_scale2(sc[k] & 255u, s0, m0);
+                kv4_scale2(sc[k] >> 8, s1, m1);
+                if (v) {
+                    const uint32_t to = smem_addr(ring + slot * kVSlot) + (uint32_t)((t >> 6) * 8192 + (t & 63) * 128);
+                    if (nDH * 128 == hd || t < 64)
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            uint32_t o[4];
+                            kv4_decode8(w[k][i], i < 4 ? s0 : s1, i < 4 ? m0 : m1, o);
+                            sts128(to + (uint32_t)((i ^ (t & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                        }
+                    fence_proxy_async_smem();
+                } else {
+                    __syncwarp();
+                    tc_fence_after();  // (the products that read what lay there)
+                    const uint32_t to = tmem + kTmK + 32u * (uint32_t)slot + ((uint32_t)(32 * (warp & 3)) << 16);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            uint32_t x[4];
+                            kv4_decode8(w[k][4 * h + i], h ? s1 : s0, h ? m1 : m0, x);
+                            o[4 * i] = x[0], o[4 * i + 1] = x[1], o[4 * i + 2] = x[2], o[4 * i + 3] = x[3];
+                        }
+                        tm_st16(to + 16u * h, o);
+                    }
+                    tm_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v ? &S.vfull[slot] : &S.kfull[slot]);
+                have--;
+                load(w[k], sc[k], meta[k]);
+            }
+        }
+        if (!ok) give_up();
+    } else if (warp >= kMma) {
+        // 896 threads are launched with 72 registers (64512 in all): 128 x 40 here, 256 x 104 for the weights and
+        // 512 x 64 for the producers are as many
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == kWalk && al_elect()) {
+            // ------------------------------------------------------ describes the pieces
+            Walker w(P, D);
+            for (int k = 0;; k++) {
+                const int r = k % kPieceRing;
+                if (k >= kPieceRing && !al_wait(&S.pc_empty[r], (uint32_t)(k / kPieceRing - 1) & 1u, &S.abort)) {
+                    give_up();
+                    break;
+                }
+                w.next(S.piece[r], A, D);
+                const bool end = S.piece[r].n == 0;
+                mbar_arrive(&S.pc_full[r]);
+                if (end) break;
+            }
+        }
+        if (warp == kSteps) {
+            // ------------------------------------------------------ describes the steps: a lane per page of a chunk, four
+            // chunks' pages looked up at a time
+            PieceRef ref;
+            int st = 0, it = 0;  // the next step's place, chunks so far
+            uint32_t round = 0;
+            bool ok = true;
+            const int lp = 31 - __clz(kv.page_rows), per = max(1, kChunk >> lp), e = lane & 7;
+            auto entry = [&]() { return !round || al_wait(&S.st_empty[st], (round - 1) & 1u, &S.abort); };
+            auto publish = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.st_full[st]);
+                if (++st == kStepRing) st = 0, round++;
+            };
+            while (ok) {
+                const AlPiece *p = ref.next(S);
+                if (!(ok = __all_sync(0xffffffffu, p != nullptr))) break;
+                const int n = p->n;
+                if (n == 0) {
+                    if ((ok = __all_sync(0xffffffffu, entry()))) {
+                        if (lane == 0) S.step[st].more = 0;
+                        publish();
+                    }
+                    break;
+                }
+                const int any_lo = p->any_lo, any_hi = p->any_hi, sk = p->sk, kvh = p->kvh;
+                const int32_t *table = kv.table + (int64_t)p->slot * kv.table_stride;
+                int row4 = -1, prev = -1, base = -1;  // of this lane's page: in the four chunks, in the chunk before; its first key
+                for (int i = 0; i <= n; i++) {
+                    if (i < n && (i & 3) == 0) {
+                        const int c = i + (lane >> 3), b = c < n ? p->row0(c) : 0, k0 = b + (e << lp);
+                        row4 = -1;
+                        bool miss = false;
+                        if (c < n && e < per && p->any_in(k0, k0 + min(kChunk, 1 << lp))) {
+                            const int page = k0 >> lp, id = __ldg(table + page);
+                            miss = id < 0 || id >= kv.n_pages;
+                            if (!miss) row4 = ((id * A.n_kv + kvh) << lp) + (k0 & ((1 << lp) - 1));
+                        }
+                        const uint32_t bad = __ballot_sync(0xffffffffu, miss);
+                        if (bad && lane == 0) raise_status(A.status, kStatusBadLane);
+                        if (e == 0 && c < n) S.bad[(it + c) % kBadRing] = bad >> (lane & 24) & 255u;
+                    }
+                    const int row = i < n ? __shfl_sync(0xffffffffu, row4, (i & 3) * 8 + e) : -1;
+                    const int kb = i < n ? p->row0(i) : -1;
+                    if (!(ok = __all_sync(0xffffffffu, entry()))) break;
+                    KvStep &q = S.step[st];
+                    if (lane < 8) q.krow[lane] = row, q.vrow[lane] = prev;
+                    if (lane == 0) q.kbase = kb, q.vbase = base, q.any_lo = any_lo, q.any_hi = any_hi, q.sk = sk, q.more = 1;
+                    publish();
+                    prev = row, base = kb;
+                }
+                it += n;
+                if (ok && lane == 0) ref.done(S);
+            }
+            if (!ok) give_up();
+        }
+        if (warp == kMma && al_elect()) {
+            // ------------------------------------------------------ the MMAs
+            PieceRef ref;
+            int it = 0, kn = 0, vn = 0;  // chunks, slices of K and of V so far
+            bool ok = true;
+            const uint32_t qs_a = smem_addr(qs), ps_a = smem_addr(ps), qstep = (uint32_t)L.qslice >> 4;
+            const uint32_t ring_d = al_desc_lo(smem_addr(ring), 8192);
+            const uint32_t hi128 = al_desc_hi(1024, 2), hip = al_desc_hi(512, 4);
+            while (ok) {
+                const AlPiece *p = ref.next(S);
+                if (!(ok = p != nullptr)) break;
+                const int n = p->n;
+                if (n == 0) break;
+                const uint32_t nr = (uint32_t)(p->nrows + 15) / 16 * 16;
+                // fp32 accumulator, fp16 operands, N = the two terms' rows; S^T: q K-major, O^T: both with the keys as rows
+                const uint32_t ids = (1u << 4) | (128u >> 4) << 24 | (2 * nr >> 3) << 17, idp = ids | (1u << 15) | (1u << 16);
+                if (!(ok = al_wait(&S.q_ready, (uint32_t)ref.k & 1u, &S.abort))) break;
+                for (int i = 0; ok && i <= n; i++) {
+                    if (i < n) {
+                        const int g = it + i;
+                        if (g >= 2 && !(ok = al_wait(&S.s_free[g & 1], (uint32_t)((g >> 1) - 1) & 1u, &S.abort))) break;
+                        const uint32_t d = tmem + kTmS + (uint32_t)(g & 1) * 2 * kR;
+                        uint32_t b0 = al_desc_lo(qs_a, 16);
+                        for (int sl = 0; sl < nK; sl++, b0 += qstep, kn++) {
+                            const int slot = kn % kKSlots;
+                            if (!(ok = al_wait(&S.kfull[slot], (uint32_t)(kn / kKSlots) & 1u, &S.abort))) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < 4; kk++)
+                                kv_mma_ta(d, tmem + kTmK + 32u * (uint32_t)slot + 8u * kk, b0 + 2u * kk, hi128, ids, kk > 0 || sl > 0);
+                            tc_commit(&S.kempty[slot]);
+                        }
+                        if (!ok) break;
+                        tc_commit(&S.s_full[g & 1]);
+                    }
+                    if (i >= 1) {
+                        if (!(ok = al_wait(&S.p_ready, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
+                        for (int vs = 0; vs < nV; vs++, vn++) {
+                            const int slot = vn % slots, kh = vs / nDH, dh = vs - kh * nDH;
+                            if (!(ok = al_wait(&S.vfull[slot], (uint32_t)(vn / slots) & 1u, &S.abort))) break;
+                            tc_fence_after();
+                            const uint32_t a0 = ring_d + (uint32_t)(slot * (kVSlot / 16));
+                            const uint32_t b0 = al_desc_lo(ps_a + kh * 64 * 64, kChunk * 64);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ks++)
+                                al_mma(tmem + kTmO + (uint32_t)dh * 2 * kR, a0 + 128u * ks, hi128, b0 + 64u * ks, hip, idp,
+                                       ks > 0 || kh > 0);
+                            tc_commit(&S.vempty[slot]);
+                        }
+                        if (!ok) break;
+                        tc_commit(&S.pv_done);
+                    }
+                }
+                it += n;
+                if (ok) ref.done(S);
+            }
+            if (!ok) {
+                give_up();
+                tc_commit(&S.drain);  // the MMAs in flight
+                mbar_wait(&S.drain, 0);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- weights and sums: warpgroup wg owns rows
+        // 16 wg .. 16 wg + 15, its thread t key t of a chunk, and of the outputs dims t and t + 128
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int wg = warp >> 2, t = tid & 127, r0 = 16 * wg;
+        PieceRef ref;
+        int it = 0;  // chunks so far
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)r0;
+        const int lp = kv.page_rows >= kChunk ? 7 : 31 - __clz(kv.page_rows);
+        bool ok = true;
+        while (ok) {
+            const AlPiece *p = ref.next(S);
+            __syncwarp();
+            if (p == nullptr) give_up();
+            if (al_bar_or(wg, p == nullptr)) break;  // (and the rows of the last piece are no longer needed)
+            const int n = p->n, nrows = p->nrows, nr = (nrows + 15) / 16 * 16;
+            if (n == 0) break;
+            if (r0 >= nrows) {  // (the first warpgroup always has rows)
+                if (lane == 0) mbar_arrive(&S.q_ready);
+                for (int i = 0; i < n && ok; i++, it++) {
+                    ok = al_wait(&S.s_full[it & 1], (uint32_t)(it >> 1) & 1u, &S.abort);
+                    if (lane == 0) mbar_arrive(&S.s_free[it & 1]), mbar_arrive(&S.p_ready);
+                    // (a second arrival must not meet the same phase)
+                    ok = ok && al_wait(&S.pv_done, (uint32_t)it & 1u, &S.abort);
+                    __syncwarp();
+                }
+                ok = !al_bar_or(wg, !ok);
+                if (lane == 0) ref.done(S);
+                continue;
+            }
+            if (t < 16) {
+                const int r = r0 + t, gs = p->gs, ln = p->lane0 + r / gs;
+                const bool in = r < nrows;
+                const int pl = in ? A.positions[ln] - p->base : -1;
+                S.rowid[r] = in ? ln * A.n_heads + p->head0 + r % gs : -1;
+                S.rowhi[r] = max(-1, min(pl, p->lim - 1));
+                S.rowlo[r] = A.window && pl >= A.window ? pl - A.window : -1;
+                S.mc[r] = in ? kNoKey : kInf;  // (what lies in the place of a row that is not there gets no weight)
+            }
+            al_bar(wg);
+            // the rows' q with the softmax's scale, multiplied by a power of two that brings the largest value of the row
+            // to 2^13 .. 2^14, as two fp16 terms
+            const int per = hd / 8;  // threads to a row
+            for (int e = t; e < 16 * per; e += 128) {
+                const int rr = e / per, d8 = e - rr * per, r = r0 + rr;
+                const bool in = r < nrows;
+                uint4 a, b;
+                al_ld32(A.q + (in ? (int64_t)S.rowid[r] * hd + 8 * d8 : 0), in, a, b);
+                float x[8] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
+                              __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; k++) x[k] = __fmul_rn(x[k], D.c), top = fmaxf(top, fabsf(x[k]));
+                for (int off = 1; off < per; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                const int k2 = top < kInf ? min(126, 140 - (int)(__float_as_uint(top) >> 23)) : 0;
+                const float f = __uint_as_float((uint32_t)(k2 + 127) << 23);
+                if (d8 == 0) S.qf[r] = __uint_as_float((uint32_t)(127 - k2) << 23);
+#pragma unroll
+                for (int k = 0; k < 8; k++) x[k] = __fmul_rn(x[k], f);
+                uint4 h, l;
+                kv_split2(x[0], x[1], h.x, l.x), kv_split2(x[2], x[3], h.y, l.y);
+                kv_split2(x[4], x[5], h.z, l.z), kv_split2(x[6], x[7], h.w, l.w);
+                if (r < nr) {
+                    const uint32_t at = smem_addr(qs) + (uint32_t)((d8 >> 3) * L.qslice + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
+                    sts128(at, h);
+                    sts128(at + nr * 128, l);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.q_ready);
+            al_bar(wg);  // (the rows' factors)
+            float lsum[16], acc[2][16];
+#pragma unroll
+            for (int j = 0; j < 16; j++) lsum[j] = acc[0][j] = acc[1][j] = 0.0f;
+            // 16 columns' terms of the products
+            auto sum2 = [&](uint32_t at, float (&o)[16]) {
+                uint32_t h[16], l[16];
+                tm_ld16_nw(at, h);
+                tm_ld16_nw(at + nr, l);
+                tm_wait_ld(h);
+                tm_wait_ld(l);
+#pragma unroll
+                for (int j = 0; j < 16; j++) o[j] = __fadd_rn(__uint_as_float(h[j]), __uint_as_float(l[j]));
+            };
+            // adds a chunk's products to the outputs
+            auto take = [&]() {
+                float o[16];
+                sum2(tl + kTmO, o);
+#pragma unroll
+                for (int j = 0; j < 16; j++) acc[0][j] = __fadd_rn(acc[0][j], o[j]);
+                if (nDH == 2) {
+                    sum2(tl + kTmO + 2 * kR, o);
+#pragma unroll
+                    for (int j = 0; j < 16; j++) acc[1][j] = __fadd_rn(acc[1][j], o[j]);
+                }
+            };
+
+            for (int i = 0; i < n; i++, it++) {
+                const int cr = p->row0(i), sk = p->sk, key = cr + t;
+                const bool fail = !al_wait(&S.s_full[it & 1], (uint32_t)(it >> 1) & 1u, &S.abort);
+                __syncwarp();  // (the tensor-memory loads are for whole warps)
+                tc_fence_after();
+                const uint32_t bad = S.bad[it % kBadRing];
+                const bool edge = p->edge_in(cr, cr + kChunk) || bad;
+                float s[16];
+                sum2(tl + kTmS + (uint32_t)(it & 1) * 2 * kR, s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.s_free[it & 1]);
+#pragma unroll
+                for (int j = 0; j < 16; j++) s[j] = __fmul_rn(s[j], S.qf[r0 + j]);
+                // whether row r of the tile sees this thread's key
+                const bool there = !(bad >> (t >> lp) & 1u);
+                auto sees = [&](int r) { return there && key <= S.rowhi[r] && (key > S.rowlo[r] || key < sk); };
+                if (edge)
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        if (!sees(r0 + j)) s[j] = -kInf;
+                bool big = i == 0;
+                if (i > 0)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) big |= __fsub_rn(s[j], S.mc[r0 + j]) > kStale;
+                const bool update = al_bar_or(wg, big || fail);
+                if (update) {
+                    if (al_bar_or(wg, fail)) {
+                        if (fail) give_up();
+                        ok = false;
+                        break;
+                    }
+                    // new maxima
+                    float m[16];
+#pragma unroll
+                    for (int j = 0; j < 16; j++) m[j] = s[j];
+                    const float top = al_reduce16<true>(m, lane);
+                    if (lane < 16) S.red[warp & 3][r0 + lane] = top;
+                    al_bar(wg);
+                    if (t < 16) {
+                        const int r = r0 + t;
+                        const float mx = fmaxf(fmaxf(S.red[0][r], S.red[1][r]), fmaxf(S.red[2][r], S.red[3][r]));
+                        const float old = S.mc[r], mc = mx > -kInf ? fmaxf(mx, old) : old;
+                        S.mc[r] = mc;
+                        S.alpha[r] = old == kNoKey ? 0.0f : al_ex2(__fsub_rn(old, mc));
+                    }
+                    al_bar(wg);
+#pragma unroll
+                    for (int j = 0; j < 16; j++) lsum[j] = __fmul_rn(lsum[j], S.alpha[r0 + j]);
+                }
+                // (a masked score stays minus infinity, the weight 0)
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    s[j] = __fmul_rn(al_ex2(__fsub_rn(s[j], S.mc[r0 + j])), kUp);
+                    lsum[j] = __fadd_rn(lsum[j], s[j]);
+                }
+                if (i > 0) {  // the products of the chunk before: P is read, and O^T is there
+                    al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort);
+                    __syncwarp();
+                }
+                // the weights, as two fp16 terms, a key's rows side by side
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    uint4 w2[2];
+                    kv_split2(s[8 * q], s[8 * q + 1], w2[0].x, w2[1].x);
+                    kv_split2(s[8 * q + 2], s[8 * q + 3], w2[0].y, w2[1].y);
+                    kv_split2(s[8 * q + 4], s[8 * q + 5], w2[0].z, w2[1].z);
+                    kv_split2(s[8 * q + 6], s[8 * q + 7], w2[0].w, w2[1].w);
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        const int c = u * nr + r0 + 8 * q;
+                        sts128(smem_addr(ps) + (uint32_t)((c >> 5) * (kChunk * 64) + t * 64 + ((((c >> 3) & 3) ^ ((t >> 1) & 3)) << 4)),
+                               w2[u]);
+                    }
+                }
+                if (i > 0) {
+                    tc_fence_after();
+                    take();
+                    if (update)
+#pragma unroll
+                        for (int j = 0; j < 16; j++) {
+                            const float al = S.alpha[r0 + j];
+                            acc[0][j] = __fmul_rn(acc[0][j], al);
+                            acc[1][j] = __fmul_rn(acc[1][j], al);
+                        }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.p_ready);
+            }
+            if (!ok) break;
+            // the sums over the keys
+            const float l4 = al_reduce16<false>(lsum, lane);
+            if (lane < 16) S.red[warp & 3][r0 + lane] = l4;
+            if (al_bar_or(wg, !al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (t < 16) {
+                const int r = r0 + t;
+                float *o = nullptr;
+                if (r < nrows) {
+                    float l = (S.red[0][r] + S.red[1][r]) + (S.red[2][r] + S.red[3][r]);
+                    const int64_t id = S.rowid[r];
+                    if (p->whole) {
+                        o = A.out + id * hd;
+                        l = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+                    } else {
+                        const int64_t row = (int64_t)(2 * blockIdx.x + p->begins) * D.cap + r;
+                        o = W.part + row * hd;
+                        W.ml[row] = make_float2(S.mc[r], l);
+                        l = 1.0f;
+                    }
+                    S.alpha[r] = l;
+                }
+                S.optr[r] = o;
+            }
+            take();
+            tc_fence_before();
+            al_bar(wg);
+            if (lane == 0) ref.done(S);
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                float *o = S.optr[r0 + j];
+                if (o) {
+                    const float al = S.alpha[r0 + j];
+                    if (t < hd) o[t] = __fmul_rn(acc[0][j], al);
+                    if (t + 128 < hd) o[t + 128] = __fmul_rn(acc[1][j], al);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMma)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmCols) : "memory");
+}
+
+// ------------------------------------------------------------------ host
 int few_heads(int group) { return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8; }
 
 bool sizes_ok(int n_lanes, int n_heads, int n_kv, int hd) {
     return n_lanes >= 1 && n_lanes <= kMaxLanes && n_kv >= 1 && n_heads >= n_kv && n_heads % n_kv == 0 &&
            n_heads <= 65535 && (hd == 64 || hd == 128 || hd == 256);
-}
-
-struct Kv4Ws {
-    float2 *ml;
-    float *part;
-    int splits;  // at most
-    size_t bytes;
-};
-
-// CTAs of about four to an SM, whatever the lanes
-Kv4Ws carve(int n_lanes, int n_heads, int n_kv, int hd, char *base) {
-    Kv4Ws w{};
-    const int group = n_heads / n_kv, gh = few_heads(group), blocks = n_kv * ((group + gh - 1) / gh);
-    const int64_t ctas = (int64_t)n_lanes * blocks;
-    w.splits = (int)(ctas >= 1024 ? 1 : 1024 / ctas);
-    const size_t rows = (size_t)w.splits * n_lanes * n_heads;
-    w.ml = (float2 *)base;
-    w.bytes = align256(rows * sizeof(float2));
-    w.part = (float *)(base ? base + w.bytes : nullptr);
-    w.bytes += align256(rows * hd * sizeof(float));
-    return w;
 }
 
 template <int HD>
@@ -319,10 +915,34 @@ const void *few_kernel(int gh) {
     }
 }
 
-qlin_status attend_few(const Kv4Args &A, const Kv4Ws &w, cudaStream_t st) {
+// The keys that a lane can see at most.
+int64_t most_keys(const Kv4Args &A) {
     const int64_t rows = (int64_t)A.kv.max_pages * A.kv.page_rows;
-    const int64_t keys = A.window && (int64_t)A.window + A.sinks < rows ? (int64_t)A.window + A.sinks : rows;
-    int64_t span = (keys + w.splits - 1) / w.splits;
+    return A.window && (int64_t)A.window + A.sinks < rows ? (int64_t)A.window + A.sinks : rows;
+}
+
+bool few_fits(const Kv4Args &A) {
+    return (double)most_keys(A) * A.n_lanes * A.n_heads * A.hd * 2 <= 40e6;
+}
+
+// The checks of a call's sizes, and what they make of its arguments.
+qlin_status describe(const char *fn, const qlin_kv4 *kv, int n_lanes, int n_heads, int n_kv, int hd, int window, int sinks,
+                     Kv4Args &A) {
+    if (qlin_status st = check_kv4(fn, kv, n_kv, hd)) return st;
+    QLIN_REQUIRE(n_lanes >= 1 && n_heads >= 1 && n_heads % n_kv == 0 && window >= 0 && sinks >= 0, QLIN_ERR_INVALID_ARG,
+                 "%s: n_lanes %d, n_heads %d, n_kv %d, window %d, sinks %d", fn, n_lanes, n_heads, n_kv, window, sinks);
+    QLIN_REQUIRE(sizes_ok(n_lanes, n_heads, n_kv, hd), QLIN_ERR_UNSUPPORTED, "%s: more than %d lanes (%d) or 65535 heads", fn,
+                 kMaxLanes, n_lanes);
+    A.kv = *kv, A.n_lanes = n_lanes, A.n_heads = n_heads, A.n_kv = n_kv, A.hd = hd, A.window = window, A.sinks = sinks;
+    A.group = n_heads / n_kv;
+    A.c = (float)(1.4426950408889634 / std::sqrt((double)hd));
+    return QLIN_OK;
+}
+
+qlin_status attend_few(const Kv4Args &A, const AlWs &w, int64_t rows, cudaStream_t st) {
+    const int64_t keys = most_keys(A);
+    int64_t span = (keys + kMaxSplits - 1) / kMaxSplits;
+    while ((keys + span - 1) / span * A.n_lanes * A.n_heads > rows) span *= 2;
     span = (span + kKeys - 1) / kKeys * kKeys;
     int splits = (int)((keys + span - 1) / span), ispan = (int)span;
     const int gh = few_heads(A.group);
@@ -336,6 +956,38 @@ qlin_status attend_few(const Kv4Args &A, const Kv4Ws &w, cudaStream_t st) {
                       st, args, "kv4_few_merge_kernel");
 }
 
+qlin_status attend_tc(const Kv4Args &K, const AlWs &w, cudaStream_t st) {
+    AlArgs A{};
+    A.q = K.q, A.positions = K.positions, A.seqs = K.seqs, A.out = K.out, A.status = K.status;
+    A.n_lanes = K.n_lanes, A.n_heads = K.n_heads, A.n_kv = K.n_kv, A.hd = K.hd, A.window = K.window, A.sinks = K.sinks;
+    A.own.n_seqs = K.kv.n_seqs, A.own.rows = K.kv.max_pages * K.kv.page_rows;  // (what the plan goes by)
+    AlDims D{};
+    D.group = K.group, D.R = kR;
+    D.LT = D.group < D.R ? D.R / D.group : 1;
+    D.HB = (D.group + D.R - 1) / D.R;
+    D.cap = (int64_t)A.n_lanes * D.group < D.R ? A.n_lanes * D.group : D.R;
+    D.streams = 1;
+    D.grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+    D.merge = A.n_lanes <= kSelfPlan ? 1 : 16;
+    D.setup = 4;
+    D.c = K.c;
+    const void *kern = (const void *)kv4_attn_kernel;
+    const size_t plan_smem = 6 * sizeof(int) * (size_t)A.n_lanes;
+    QLIN_REQUIRE(kAlSmem <= max_smem_optin(), QLIN_ERR_UNSUPPORTED, "qlin_attention_kv4: shared memory");
+    blocks_per_sm(kern, kAlSmem);  // raises the dynamic shared-memory limit once
+    blocks_per_sm((const void *)al_plan_kernel, plan_smem);
+    void *pargs[] = {(void *)&A, (void *)&D, (void *)&w};
+    if (A.n_lanes > kSelfPlan)
+        if (qlin_status e = launch_pdl((const void *)al_plan_kernel, dim3(1), dim3(kPlanThreads), plan_smem, st, pargs,
+                                       "al_plan_kernel"))
+            return e;
+    void *args[] = {(void *)&A, (void *)&D, (void *)&w, (void *)&K.kv};
+    if (qlin_status e = launch_pdl(kern, dim3(D.grid), dim3(kTcThreads), kAlSmem, st, args, "kv4_attn_kernel")) return e;
+    const int64_t total = (int64_t)A.n_lanes * A.n_heads, blocks = (total + D.merge - 1) / D.merge;
+    return launch_pdl((const void *)al_merge_kernel, dim3((unsigned)(blocks < 8 * D.grid ? blocks : 8 * D.grid)),
+                      dim3(kMergeThreads), 0, st, pargs, "al_merge_kernel");
+}
+
 }  // namespace
 }  // namespace qlin
 
@@ -347,26 +999,32 @@ size_t qlin_attention_kv4_workspace_size(int n_lanes, int n_heads, int n_kv, int
     return sizes_ok(n_lanes, n_heads, n_kv, head_dim) ? carve(n_lanes, n_heads, n_kv, head_dim, nullptr).bytes : 0;
 }
 
+int qlin_attention_kv4_on_tensor_cores(const qlin_kv4 *kv, int n_lanes, int n_heads, int n_kv, int head_dim, int window,
+                                       int sinks) {
+    qlin::clear_error();
+    const char *fn = "qlin_attention_kv4_on_tensor_cores";
+    Kv4Args A{};
+    if (qlin_status st = describe(fn, kv, n_lanes, n_heads, n_kv, head_dim, window, sinks, A)) return -(int)st;
+    return few_fits(A) ? 0 : 1;
+}
+
 qlin_status qlin_attention_kv4(const float *q, const qlin_kv4 *kv, const int32_t *positions, const int32_t *seqs,
                                int n_lanes, int n_heads, int n_kv, int head_dim, int window, int sinks, float *out,
                                int32_t *status_word, void *workspace, size_t workspace_bytes, qlin_stream_t stream) {
     qlin::clear_error();
     const char *fn = "qlin_attention_kv4";
-    if (qlin_status st = check_kv4(fn, kv, n_kv, head_dim)) return st;
+    Kv4Args A{};
+    if (qlin_status st = describe(fn, kv, n_lanes, n_heads, n_kv, head_dim, window, sinks, A)) return st;
     QLIN_REQUIRE(q && positions && seqs && out && workspace, QLIN_ERR_INVALID_ARG, "%s: null pointer", fn);
-    QLIN_REQUIRE(n_lanes >= 1 && n_heads >= 1 && n_heads % n_kv == 0 && window >= 0 && sinks >= 0, QLIN_ERR_INVALID_ARG,
-                 "%s: n_lanes %d, n_heads %d, n_kv %d, window %d, sinks %d", fn, n_lanes, n_heads, n_kv, window, sinks);
-    QLIN_REQUIRE(sizes_ok(n_lanes, n_heads, n_kv, head_dim), QLIN_ERR_UNSUPPORTED, "%s: more than %d lanes (%d) or 65535 heads",
-                 fn, kMaxLanes, n_lanes);
     QLIN_REQUIRE(aligned16(q) && aligned16(out) && aligned16(workspace) && aligned4(positions) && aligned4(seqs) &&
                      aligned4(status_word),
                  QLIN_ERR_INVALID_ARG, "%s: q, out and workspace are 16-byte aligned (positions, seqs, status_word: 4)", fn);
-    const Kv4Ws w = carve(n_lanes, n_heads, n_kv, head_dim, (char *)workspace);
+    int64_t rows;
+    const AlWs w = carve(n_lanes, n_heads, n_kv, head_dim, (char *)workspace, &rows);
     QLIN_REQUIRE(workspace_bytes >= w.bytes, QLIN_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", fn, workspace_bytes,
                  w.bytes);
-    Kv4Args A{q, *kv, positions, seqs, n_lanes, n_heads, n_kv, head_dim, window, sinks, out, status_word, n_heads / n_kv,
-              (float)(1.4426950408889634 / std::sqrt((double)head_dim))};
-    return attend_few(A, w, (cudaStream_t)stream);
+    A.q = q, A.positions = positions, A.seqs = seqs, A.out = out, A.status = status_word;
+    return few_fits(A) ? attend_few(A, w, rows, (cudaStream_t)stream) : attend_tc(A, w, (cudaStream_t)stream);
 }
 
 }  // extern "C"

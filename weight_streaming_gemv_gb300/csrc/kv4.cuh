@@ -49,8 +49,9 @@ __device__ __forceinline__ void kv4_scale2(uint32_t b, __half2 &s, __half2 &m24)
 
 inline qlin_status check_kv4(const char *fn, const qlin_kv4 *c, int n_kv, int head_dim) {
     QLIN_REQUIRE(c && c->k && c->v && c->k_scale && c->v_scale && c->table, QLIN_ERR_INVALID_ARG, "%s: kv: null pointer", fn);
-    QLIN_REQUIRE(aligned16(c->k) && aligned16(c->v) && aligned16(c->k_scale) && aligned16(c->v_scale) && aligned4(c->table),
-                 QLIN_ERR_INVALID_ARG, "%s: kv: codes and scales are 16-byte aligned, the table 4-byte", fn);
+    QLIN_REQUIRE((((uintptr_t)c->k | (uintptr_t)c->v) & 31u) == 0 && aligned16(c->k_scale) && aligned16(c->v_scale) &&
+                     aligned4(c->table),
+                 QLIN_ERR_INVALID_ARG, "%s: kv: codes are 32-byte aligned, scales 16-byte, the table 4-byte", fn);
     QLIN_REQUIRE(c->n_pages >= 1 && c->n_seqs >= 1 && c->max_pages >= 1 && n_kv >= 1, QLIN_ERR_INVALID_ARG,
                  "%s: kv: %d pages, %d sequences of %d pages, %d KV heads", fn, (int)c->n_pages, (int)c->n_seqs,
                  (int)c->max_pages, n_kv);

@@ -159,6 +159,7 @@ SIGNATURES = {
     "qlin_kv4_read": ([ctypes.POINTER(QlinKv4C), _P, _P, _I, _I, _I, _P, _P, _P, _P], _ST),
     "qlin_sample": ([_P, _I64, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P], _ST),
     "qlin_attention_kv4_workspace_size": ([_I, _I, _I, _I], _SZ),
+    "qlin_attention_kv4_on_tensor_cores": ([ctypes.POINTER(QlinKv4C), _I, _I, _I, _I, _I, _I], _I),
     "qlin_attention_kv4": ([_P, ctypes.POINTER(QlinKv4C), _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P], _ST),
 }
 
@@ -599,6 +600,13 @@ def qlin_kv4_read(kv: QlinKv4C, positions, seqs, n_lanes, n_kv, head_dim, k_out,
 
 def qlin_attention_kv4_workspace_size(n_lanes, n_heads, n_kv, head_dim) -> int:
     return int(lib().qlin_attention_kv4_workspace_size(n_lanes, n_heads, n_kv, head_dim))
+
+
+def qlin_attention_kv4_on_tensor_cores(kv: QlinKv4C, n_lanes, n_heads, n_kv, head_dim, window, sinks) -> bool:
+    r = lib().qlin_attention_kv4_on_tensor_cores(ctypes.byref(kv), n_lanes, n_heads, n_kv, head_dim, window, sinks)
+    if r < 0:
+        _check("qlin_attention_kv4_on_tensor_cores", -r)
+    return bool(r)
 
 
 def qlin_attention_kv4(q, kv: QlinKv4C, positions, seqs, n_lanes, n_heads, n_kv, head_dim, window, sinks, out,
