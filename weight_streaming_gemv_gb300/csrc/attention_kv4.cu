@@ -13,6 +13,9 @@
 // their codes and scales into shared memory, scores and weighted values in
 // fp32 on the CUDA cores.  The runs of one lane leave partial sums that a
 // second kernel joins by the weights 2^(maximum - largest maximum).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <cmath>
 
 #include "attention_lanes.cuh"
@@ -274,57 +277,72 @@ __global__ void __launch_bounds__(kThreads) kv4_few_merge_kernel(const __grid_co
 constexpr int kR = 32;                // rows of a tile at most
 constexpr int kProd = 16;             // producer warps, in groups of four
 constexpr int kProd0 = 8;             // behind two warpgroups of the weights
-constexpr int kMma = kProd0 + kProd;  // the warp that issues the MMAs; then the ones that describe pieces and steps
-constexpr int kWalk = kMma + 1, kSteps = kMma + 2;
+constexpr int kMma = kProd0 + kProd;  // the warp that issues the MMAs; then the ones that describe pieces and copy
+constexpr int kWalk = kMma + 1, kCopy = kMma + 2;
 constexpr int kTcThreads = 32 * (kMma + 4);
 constexpr int kVSlot = 16384;         // 64 keys x 128 dims
-constexpr int kMaxVSlots = 10, kKSlots = 8;
-constexpr int kStepRing = 4, kBadRing = 64;
-// tensor memory: S^T twice [2 kR], O^T's two halves of dims [2 kR] each, slices of K (128 keys x 64 dims)
+constexpr int kVSlots = 6, kKSlots = 8;
+constexpr int kMaxStages = 4;         // chunks of codes of K, and of V
+constexpr int kBadRing = 64;
+// tensor memory: S^T twice [2 kR], O^T [4 kR], slices of K (128 keys x 64 dims)
 constexpr uint32_t kTmS = 0, kTmO = 4 * kR, kTmK = 8 * kR, kTmCols = 512;
 static_assert(kTmK + 32 * kKSlots <= kTmCols, "tensor memory");
 constexpr float kStale = 4.0f;        // how far a score may exceed the maximum in use
 constexpr float kUp = 2048.0f;        // weights are multiplied by this: below 2^15, and steps of 2^-35 of the largest
 
-// What the producers need to load a step's slices: chunk i's keys and chunk
-// i-1's values of a piece.
-struct __align__(16) KvStep {
-    int krow[8], vrow[8];        // per page of the chunk: the pool's row of its first key, -1: nothing to read
-    int kbase, vbase;            // the chunks' first keys; below 0: none
-    int any_lo, any_hi, sk;      // the keys that some row sees
-    int more;                    // 0: there are no more steps
-    int pad[2];
+struct KvMaps {
+    CUtensorMap k, v;
+};
+
+template <int HD>
+struct KvCfg {
+    static constexpr int nK = HD / 64;               // slices of 64 dims of a chunk's K
+    static constexpr int nDH = (HD + 127) / 128, nV = 2 * nDH;  // slices of 64 keys x 128 dims of V
+    static constexpr int kCodes = kChunk * HD / 2, kScales = kChunk * HD / 32, kStage = kCodes + kScales;
+    // The producer groups' slices of every chunk: with 256 dims one of K and one of V each, else groups 0 (and 1, with
+    // 128) K's, groups 2 and 3 V's
+    static constexpr bool kBoth = HD == 256;
+    static constexpr int kKWarps = 4 * nK, kVWarps = 4 * nV;  // warps that read a chunk's codes
 };
 
 struct KvCtl {
-    uint64_t kfull[kKSlots], kempty[kKSlots], vfull[kMaxVSlots], vempty[kMaxVSlots];
-    uint64_t s_full[2], s_free[2], p_ready, q_ready, pv_done, drain;
-    uint64_t st_full[kStepRing], st_empty[kStepRing], pc_full[kPieceRing], pc_empty[kPieceRing];
-    KvStep step[kStepRing];
+    uint64_t kfull[kKSlots], kempty[kKSlots], vfull[kVSlots], vempty[kVSlots];
+    uint64_t kst_full[kMaxStages], kst_empty[kMaxStages], vst_full[kMaxStages], vst_empty[kMaxStages];
+    uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready, drain;
+    uint64_t pc_full[kPieceRing], pc_empty[kPieceRing];
     uint32_t bad[kBadRing];   // per chunk: pages that are out of range
     int rowid[kR];            // lane * n_heads + head
     int rowlo[kR], rowhi[kR]; // a row sees the keys <= rowhi that are > rowlo or first ones
-    float mc[kR], alpha[kR], qf[kR];
+    float qf[kR];             // what a row's scores are multiplied by
+    float mc[kR], sum[kR], alpha[kR];  // of a warpgroup's 16 rows each
     float red[4][kR];
     float *optr[kR];
     AlSelfPlan plan;
     AlPiece piece[kPieceRing];
+    int chunks;               // all of them, once that is known
     uint32_t tmem;
     int abort;
 };
 
-struct KvLayout {  // in shared memory: the ring of V, the rows' q (per 64 dims the two terms' rows), the weights P
-    int q, qslice, p, slots;
-    __device__ __forceinline__ KvLayout(int rmax, int hd) {
-        const int Rc = rmax <= 16 ? 16 : 32;
-        qslice = 2 * Rc * 128;
-        const int qb = hd / 64 * qslice, pb = kChunk * 64 * (Rc / 16);
-        slots = min((kAlSmem - 1024 - (int)sizeof(KvCtl) - qb - pb) / kVSlot, kMaxVSlots);
-        q = slots * kVSlot;
-        p = q + qb;
+// In shared memory: the ring of V, the rows' q (per 64 dims the two terms'
+// rows), the weights P, the stages' codes (K's, V's), their scales.
+template <int HD>
+struct KvLayout {
+    using C = KvCfg<HD>;
+    int q, qslice, p, codes, scales, nks, nvs;
+    __device__ __forceinline__ KvLayout(int rmax) {
+        qslice = 2 * (rmax <= 16 ? 16 : 32) * 128;
+        q = kVSlots * kVSlot;
+        p = q + C::nK * qslice;
+        codes = p + 2 * kChunk * 64;
+        const int n = min((kAlSmem - 1024 - (int)sizeof(KvCtl) - 16 - codes) / C::kStage, 2 * kMaxStages);
+        nks = (n + 1) / 2, nvs = n / 2;
+        scales = codes + n * C::kCodes;
     }
 };
-static_assert(kAlSmem - 1024 - (int)sizeof(KvCtl) - 4 * 2 * 32 * 128 - 2 * kChunk * 64 >= 9 * kVSlot, "ring of nine");
+static_assert(kAlSmem - 1024 - (int)sizeof(KvCtl) - 16 - kVSlots * kVSlot - 4 * 2 * 32 * 128 - 2 * kChunk * 64 >=
+                  4 * KvCfg<256>::kStage,
+              "two stages of K and two of V");
 
 // D (tensor memory) (+)= A (tensor memory) x B (shared memory)
 __device__ __forceinline__ void kv_mma_ta(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc, bool acc) {
@@ -334,6 +352,13 @@ __device__ __forceinline__ void kv_mma_ta(uint32_t d, uint32_t a, uint32_t blo, 
         "mov.b64 b, {%2, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
         "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void kv_tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ uint32_t f16x2(float a, float b) {  // a in the low half
@@ -347,37 +372,33 @@ __device__ __forceinline__ void kv_split2(float a, float b, uint32_t &hi, uint32
     const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
     lo = f16x2(__fsub_rn(a, h.x), __fsub_rn(b, h.y));
 }
-// 32 bytes of codes and two scale bytes if on, else zeros
-__device__ __forceinline__ void kv_ld(const uint8_t *code, const uint8_t *scale, bool on, uint32_t (&w)[8], uint32_t &s) {
-#pragma unroll
-    for (int i = 0; i < 8; i++) w[i] = 0;
-    uint16_t h = 0;
+// a barrier of both warpgroups of the weights, and whether v holds anywhere
+__device__ __forceinline__ bool kv_bar_or(bool v) {
+    uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %11, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%9];\n\t"
-        "@p ld.global.nc.b16 %8, [%10];\n\t}"
-        : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]), "+r"(w[4]), "+r"(w[5]), "+r"(w[6]), "+r"(w[7]), "+h"(h)
-        : "l"(code), "l"(scale), "r"((uint32_t)on));
-    s = h;
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 3, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
 }
 
-// Walks over the steps' slices that are one producer group's: of a step's K
-// and then V slices every fourth, counted on from step to step.
-struct KvSlices {
-    int st = 0, x = 0, cnt = 0;   // the step's place in the ring, the next slice in it, slices before it
-    uint32_t par = 0;
-    int kn = 0, vn = 0;           // K and V slices before the step
-    bool open = false;
-};
+// A wait of a whole warp: its lanes go on, or give up, together.
+__device__ __forceinline__ bool kv_wait_all(uint64_t *bar, uint32_t parity, int *abort) {
+    return __all_sync(0xffffffffu, al_wait(bar, parity, abort));
+}
 
+template <int HD>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    kv4_attn_kernel(const __grid_constant__ AlArgs A, const __grid_constant__ AlDims D, const __grid_constant__ AlWs W,
-                    const __grid_constant__ qlin_kv4 kv) {
+    kv4_attn_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ AlArgs A, const __grid_constant__ AlDims D,
+                    const __grid_constant__ AlWs W, const __grid_constant__ qlin_kv4 kv) {
+    using C = KvCfg<HD>;
+    constexpr int nK = C::nK, nDH = C::nDH, nV = C::nV;
     extern __shared__ uint8_t kv_raw[];
     uint8_t *const smem = kv_raw + ((1024u - (smem_addr(kv_raw) & 1023u)) & 1023u);  // the swizzled operands' alignment
     KvCtl &S = *reinterpret_cast<KvCtl *>(smem + (kAlSmem - 1024 - sizeof(KvCtl)) / 16 * 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hd = A.hd, nK = hd / 64, nDH = (hd + 127) / 128, nV = 2 * nDH;
     if (warp == kMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&S.tmem)),
                      "r"(kTmCols)
@@ -386,11 +407,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (tid == 32) {
         for (int s = 0; s < kKSlots; s++) mbar_init(&S.kfull[s], 4), mbar_init(&S.kempty[s], 1);
-        for (int s = 0; s < kMaxVSlots; s++) mbar_init(&S.vfull[s], 4), mbar_init(&S.vempty[s], 1);
-        for (int s = 0; s < 2; s++) mbar_init(&S.s_full[s], 1), mbar_init(&S.s_free[s], 8);
-        mbar_init(&S.p_ready, 8), mbar_init(&S.q_ready, 8), mbar_init(&S.pv_done, 1), mbar_init(&S.drain, 1);
-        for (int s = 0; s < kStepRing; s++) mbar_init(&S.st_full[s], 1), mbar_init(&S.st_empty[s], kProd);
+        for (int s = 0; s < kVSlots; s++) mbar_init(&S.vfull[s], 4), mbar_init(&S.vempty[s], 1);
+        for (int s = 0; s < kMaxStages; s++) {
+            mbar_init(&S.kst_full[s], 1), mbar_init(&S.kst_empty[s], C::kKWarps);
+            mbar_init(&S.vst_full[s], 1), mbar_init(&S.vst_empty[s], C::kVWarps);
+        }
+        // (a chunk's weights come from both warpgroups, a warp's first lane arriving, or from one, its first two)
+        for (int s = 0; s < 2; s++)
+            mbar_init(&S.s_full[s], 1), mbar_init(&S.s_free[s], 8), mbar_init(&S.p_ready[s], 8), mbar_init(&S.pv_done[s], 1);
+        mbar_init(&S.q_ready, 8), mbar_init(&S.drain, 1);
         for (int s = 0; s < kPieceRing; s++) mbar_init(&S.pc_full[s], 1), mbar_init(&S.pc_empty[s], 8 + 2);
+        S.chunks = INT_MAX;
         S.abort = 0;
         fence_mbar_init();
     }
@@ -410,9 +437,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    const KvLayout L(P.head->rmax, hd);
-    const int slots = L.slots;
+    const KvLayout<HD> L(P.head->rmax);
     uint8_t *const ring = smem, *const qs = ring + L.q, *const ps = ring + L.p;
+    uint8_t *const codes = ring + L.codes, *const scales = ring + L.scales;  // K's stages, then V's
     auto give_up = [&]() {
         S.abort = 1;
         raise_status(A.status, kStatusTimeout);
@@ -420,106 +447,99 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (warp >= kProd0 && warp < kMma) {
         // ---------------------------------------------------------- producers: a slice of K or V per group of four warps,
-        // 64 dims of a key per thread, three slices in registers on their way
+        // 64 dims of a key per thread
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         const int pg = (warp - kProd0) >> 2, t = tid & 127;
-        const int lp = kv.page_rows >= kChunk ? 7 : 31 - __clz(kv.page_rows);
-        KvSlices c;
-        constexpr int kDepth = 3;
-        uint32_t w[kDepth][8], sc[kDepth];
-        int meta[kDepth];  // slice number * 2 + kind (0 K, 1 V); below 0: none
-        bool ok = true, more = true;
-        int have = 0;  // slices in registers
-        // The group's next slice, if its step is described by now or there is nothing else to do: the steps of the pieces
-        // to come may wait for slices that are still in registers here.
-        auto load = [&](uint32_t (&o)[8], uint32_t &s, int &m) {
-            m = -1;
-            while (more) {
-                KvStep &q = S.step[c.st];
-                if (!c.open) {
-                    if (have && !__all_sync(0xffffffffu, al_test(smem_addr(&S.st_full[c.st]), c.par))) return;
-                    if (!(ok = al_wait(&S.st_full[c.st], c.par, &S.abort)) || !q.more) {
-                        more = false;
-                        break;
-                    }
-                    c.open = true;
-                    c.x = (pg - c.cnt) & 3;
-                }
-                const int nk = q.kbase >= 0 ? nK : 0, nv = q.vbase >= 0 ? nV : 0;
-                if (c.x < nk + nv) {
-                    const bool v = c.x >= nk;
-                    const int e = v ? c.x - nk : c.x;
-                    // K: key t, dims 64 e ..; V: key t & 63 of half e / nDH, 64 dims of the 128 from 128 (e % nDH) on
-                    const int r = v ? (e / nDH) * 64 + (t & 63) : t, d = v ? (e % nDH) * 128 + (t >> 6) * 64 : 64 * e;
-                    const int key = (v ? q.vbase : q.kbase) + r, row0 = (v ? q.vrow : q.krow)[r >> lp];
-                    const int64_t row = row0 + (r & ((1 << lp) - 1));
-                    const bool on = row0 >= 0 && d < hd && key <= q.any_hi && (key > q.any_lo || key < q.sk);
-                    kv_ld(static_cast<const uint8_t *>(v ? kv.v : kv.k) + row * (hd / 2) + d / 2,
-                          static_cast<const uint8_t *>(v ? kv.v_scale : kv.k_scale) + row * (hd / 32) + d / 32, on, o, s);
-                    m = (v ? c.vn + e : c.kn + e) * 2 + v;
-                    c.x += 4;
-                    have++;
-                    return;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.st_empty[c.st]);
-                c.cnt += nk + nv, c.kn += nk, c.vn += nv;
-                c.open = false;
-                if (++c.st == kStepRing) c.st = 0, c.par ^= 1u;
-            }
+        const bool does_k = C::kBoth || pg < nK, does_v = C::kBoth || pg >= 2;
+        const int ev = C::kBoth ? pg : pg - 2, kh = ev / nDH, dh = ev % nDH;  // (a slice of V: half the keys, 128 dims)
+        const bool v_dims = nDH * 128 == HD || t < 64;
+        auto place = [&](int row, int group) {  // of a group of 32 dims in a stage (the copies' swizzle)
+            const int x = HD == 256 ? row & 7 : HD == 128 ? (row >> 1) & 3 : (row >> 2) & 1;
+            return (uint32_t)(row * (HD / 2) + ((group ^ x) << 4));
         };
-#pragma unroll
-        for (int k = 0; k < kDepth; k++) load(w[k], sc[k], meta[k]);
-        while (ok && have) {
-#pragma unroll
-            for (int k = 0; k < kDepth; k++) {
-                if (meta[k] < 0) {
-                    load(w[k], sc[k], meta[k]);
-                    continue;
-                }
-                const int n = meta[k] >> 1;
-                const bool v = meta[k] & 1;
-                const int slot = v ? n % slots : n % kKSlots, round = v ? n / slots : n / kKSlots;
-                if (round && !al_wait(v ? &S.vempty[slot] : &S.kempty[slot], (uint32_t)(round - 1) & 1u, &S.abort)) {
-                    ok = false;
-                    break;
-                }
-                __half2 s0, m0, s1, m1;
-                kv4_scale2(sc[k] & 255u, s0, m0);
-                kv4_scale2(sc[k] >> 8, s1, m1);
-                if (v) {
-                    const uint32_t to = smem_addr(ring + slot * kVSlot) + (uint32_t)((t >> 6) * 8192 + (t & 63) * 128);
-                    if (nDH * 128 == hd || t < 64)
-#pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            uint32_t o[4];
-                            kv4_decode8(w[k][i], i < 4 ? s0 : s1, i < 4 ? m0 : m1, o);
-                            sts128(to + (uint32_t)((i ^ (t & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
-                        }
-                    fence_proxy_async_smem();
-                } else {
+        // where this thread's codes and scales lie in a stage of K and of V
+        const int vrow = 64 * kh + (t & 63), vg = 4 * dh + 2 * (t >> 6);
+        const uint32_t k0 = place(t, 2 * pg), k1 = place(t, 2 * pg + 1), ks = (uint32_t)(t * (HD / 32) + 2 * pg);
+        const uint32_t v0 = place(vrow, vg), v1 = place(vrow, vg + 1), vs = (uint32_t)(vrow * (HD / 32) + vg);
+        const uint32_t to_v = smem_addr(ring) + (uint32_t)((t >> 6) * 8192 + (t & 63) * 128);
+        const uint32_t to_k = tmem + kTmK + ((uint32_t)(32 * (warp & 3)) << 16);
+        int kst = 0, vst = 0;
+        uint32_t kpar = 0, vpar = 0;
+        int vslot = ev;
+        uint32_t vround = 0;
+        bool ok = true;
+        for (int c = 0; ok && (does_k || does_v); c++) {
+            bool end = false;
+            if (does_k) {
+                if (!(ok = kv_wait_all(&S.kst_full[kst], kpar, &S.abort))) break;
+                end = c >= *(volatile int *)&S.chunks;
+                if (!end) {
+                    const uint8_t *from = codes + kst * C::kCodes;
+                    const uint4 a = lds128(from + k0), b = lds128(from + k1);
+                    const uint32_t sc = *reinterpret_cast<const uint16_t *>(scales + kst * C::kScales + ks);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.kst_empty[kst]);
+                    if (++kst == L.nks) kst = 0, kpar ^= 1u;
+                    const int kn = c * nK + pg, slot = kn % kKSlots, round = kn / kKSlots;
+                    if (round && !(ok = kv_wait_all(&S.kempty[slot], (uint32_t)(round - 1) & 1u, &S.abort))) break;
                     __syncwarp();
                     tc_fence_after();  // (the products that read what lay there)
-                    const uint32_t to = tmem + kTmK + 32u * (uint32_t)slot + ((uint32_t)(32 * (warp & 3)) << 16);
+                    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
+                        __half2 s2, m2;
+                        kv4_scale2(h ? sc >> 8 : sc & 255u, s2, m2);
                         uint32_t o[16];
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
                             uint32_t x[4];
-                            kv4_decode8(w[k][4 * h + i], h ? s1 : s0, h ? m1 : m0, x);
+                            kv4_decode8(w[4 * h + i], s2, m2, x);
                             o[4 * i] = x[0], o[4 * i + 1] = x[1], o[4 * i + 2] = x[2], o[4 * i + 3] = x[3];
                         }
-                        tm_st16(to + 16u * h, o);
+                        tm_st16(to_k + 32u * (uint32_t)slot + 16u * h, o);
                     }
                     tm_wait_st();
                     tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.kfull[slot]);
+                }
+            }
+            if (does_v && (!does_k || c > 0)) {
+                if (!(ok = kv_wait_all(&S.vst_full[vst], vpar, &S.abort))) break;
+                if (!does_k && (end = c >= *(volatile int *)&S.chunks)) break;
+                uint4 a, b;
+                uint32_t sc = 0;
+                if (v_dims) {
+                    const uint8_t *from = codes + (L.nks + vst) * C::kCodes;
+                    a = lds128(from + v0), b = lds128(from + v1);
+                    sc = *reinterpret_cast<const uint16_t *>(scales + (L.nks + vst) * C::kScales + vs);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(v ? &S.vfull[slot] : &S.kfull[slot]);
-                have--;
-                load(w[k], sc[k], meta[k]);
+                if (lane == 0) mbar_arrive(&S.vst_empty[vst]);
+                if (++vst == L.nvs) vst = 0, vpar ^= 1u;
+                if (vround && !(ok = kv_wait_all(&S.vempty[vslot], (vround - 1) & 1u, &S.abort))) break;
+                if (v_dims) {
+                    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        __half2 s2, m2;
+                        kv4_scale2(h ? sc >> 8 : sc & 255u, s2, m2);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            uint32_t o[4];
+                            kv4_decode8(w[4 * h + i], s2, m2, o);
+                            sts128(to_v + (uint32_t)(vslot * kVSlot + (((4 * h + i) ^ (t & 7)) << 4)),
+                                   make_uint4(o[0], o[1], o[2], o[3]));
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.vfull[vslot]);
+                vslot += nV;
+                if (vslot >= kVSlots) vslot -= kVSlots, vround++;
             }
+            if (end) break;
         }
         if (!ok) give_up();
     } else if (warp >= kMma) {
@@ -541,113 +561,149 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (end) break;
             }
         }
-        if (warp == kSteps) {
-            // ------------------------------------------------------ describes the steps: a lane per page of a chunk, four
-            // chunks' pages looked up at a time
+        if (warp == kCopy) {
+            // ------------------------------------------------------ copies the chunks' codes and scales: a lane per page of
+            // a chunk, four chunks' pages looked up at a time
             PieceRef ref;
-            int st = 0, it = 0;  // the next step's place, chunks so far
-            uint32_t round = 0;
+            int it = 0, kst = 0, vst = 0;  // chunks so far, the next stages
+            uint32_t kround = 0, vround = 0;
+            int ks_n = 0, vs_n = 0;        // stages filled
             bool ok = true;
-            const int lp = 31 - __clz(kv.page_rows), per = max(1, kChunk >> lp), e = lane & 7;
-            auto entry = [&]() { return !round || al_wait(&S.st_empty[st], (round - 1) & 1u, &S.abort); };
-            auto publish = [&]() {
+            const int lp = 31 - __clz(kv.page_rows), per = max(1, kChunk >> lp), e = lane & 7, rows = min(kChunk, kv.page_rows);
+            // a chunk whose pages lie at the rows `row` of the pool (lanes 0 .. 7; -1: nothing to read)
+            auto fill = [&](bool v, int row) -> bool {
+                int &st = v ? vst : kst;
+                uint32_t &round = v ? vround : kround;
+                uint64_t *const full = v ? &S.vst_full[st] : &S.kst_full[st];
+                if (round && !kv_wait_all(v ? &S.vst_empty[st] : &S.kst_empty[st], (round - 1) & 1u, &S.abort))
+                    return false;
+                const bool on = lane < per && row >= 0;
+                const int pages = __popc(__ballot_sync(0xffffffffu, on));
+                if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(pages * rows * (HD / 2 + HD / 32)));
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&S.st_full[st]);
-                if (++st == kStepRing) st = 0, round++;
+                if (on) {
+                    const int s = (v ? L.nks : 0) + st;
+                    kv_tma_2d(smem_addr(codes + s * C::kCodes + lane * rows * (HD / 2)), v ? &maps.v : &maps.k, 0, row,
+                              smem_addr(full));
+                    bulk_g2s_l2(scales + s * C::kScales + lane * rows * (HD / 32),
+                                static_cast<const uint8_t *>(v ? kv.v_scale : kv.k_scale) + (int64_t)row * (HD / 32),
+                                (uint32_t)(rows * (HD / 32)), full);
+                }
+                __syncwarp();
+                if (++st == (v ? L.nvs : L.nks)) st = 0, round++;
+                (v ? vs_n : ks_n)++;
+                return true;
             };
             while (ok) {
                 const AlPiece *p = ref.next(S);
                 if (!(ok = __all_sync(0xffffffffu, p != nullptr))) break;
                 const int n = p->n;
                 if (n == 0) {
-                    if ((ok = __all_sync(0xffffffffu, entry()))) {
-                        if (lane == 0) S.step[st].more = 0;
-                        publish();
-                    }
+                    if (lane == 0) *(volatile int *)&S.chunks = it;
+                    ok = fill(false, -1) && fill(true, -1);  // (empty ones, behind the last)
                     break;
                 }
-                const int any_lo = p->any_lo, any_hi = p->any_hi, sk = p->sk, kvh = p->kvh;
+                const int kvh = p->kvh;
                 const int32_t *table = kv.table + (int64_t)p->slot * kv.table_stride;
-                int row4 = -1, prev = -1, base = -1;  // of this lane's page: in the four chunks, in the chunk before; its first key
-                for (int i = 0; i <= n; i++) {
+                int row4 = -1, prev = -1;  // of this lane's page: in the four chunks, in the chunk before
+                for (int i = 0; i <= n && ok; i++) {
                     if (i < n && (i & 3) == 0) {
                         const int c = i + (lane >> 3), b = c < n ? p->row0(c) : 0, k0 = b + (e << lp);
                         row4 = -1;
                         bool miss = false;
-                        if (c < n && e < per && p->any_in(k0, k0 + min(kChunk, 1 << lp))) {
-                            const int page = k0 >> lp, id = __ldg(table + page);
+                        if (c < n && e < per && p->any_in(k0, k0 + rows)) {
+                            const int id = __ldg(table + (k0 >> lp));
                             miss = id < 0 || id >= kv.n_pages;
                             if (!miss) row4 = ((id * A.n_kv + kvh) << lp) + (k0 & ((1 << lp) - 1));
                         }
                         const uint32_t bad = __ballot_sync(0xffffffffu, miss);
                         if (bad && lane == 0) raise_status(A.status, kStatusBadLane);
                         if (e == 0 && c < n) S.bad[(it + c) % kBadRing] = bad >> (lane & 24) & 255u;
+                        __syncwarp();
                     }
-                    const int row = i < n ? __shfl_sync(0xffffffffu, row4, (i & 3) * 8 + e) : -1;
-                    const int kb = i < n ? p->row0(i) : -1;
-                    if (!(ok = __all_sync(0xffffffffu, entry()))) break;
-                    KvStep &q = S.step[st];
-                    if (lane < 8) q.krow[lane] = row, q.vrow[lane] = prev;
-                    if (lane == 0) q.kbase = kb, q.vbase = base, q.any_lo = any_lo, q.any_hi = any_hi, q.sk = sk, q.more = 1;
-                    publish();
-                    prev = row, base = kb;
+                    const int row = __shfl_sync(0xffffffffu, row4, (i & 3) * 8 + e);
+                    if (i < n) ok = fill(false, row);
+                    if (ok && i > 0) ok = fill(true, prev);
+                    prev = row;
                 }
                 it += n;
                 if (ok && lane == 0) ref.done(S);
             }
-            if (!ok) give_up();
+            if (!ok) {
+                give_up();
+                // the copies in flight
+                for (int k = max(0, ks_n - L.nks); k < ks_n; k++) mbar_wait(&S.kst_full[k % L.nks], (uint32_t)(k / L.nks) & 1u);
+                for (int k = max(0, vs_n - L.nvs); k < vs_n; k++) mbar_wait(&S.vst_full[k % L.nvs], (uint32_t)(k / L.nvs) & 1u);
+            }
         }
         if (warp == kMma && al_elect()) {
             // ------------------------------------------------------ the MMAs
+            // One thread paces a chunk: what it needs is in registers, and whether the next slice has landed is asked while
+            // the products of this one are issued.
             PieceRef ref;
-            int it = 0, kn = 0, vn = 0;  // chunks, slices of K and of V so far
+            int it = 0;  // chunks so far
             bool ok = true;
             const uint32_t qs_a = smem_addr(qs), ps_a = smem_addr(ps), qstep = (uint32_t)L.qslice >> 4;
             const uint32_t ring_d = al_desc_lo(smem_addr(ring), 8192);
             const uint32_t hi128 = al_desc_hi(1024, 2), hip = al_desc_hi(512, 4);
+            int kslot = 0, vslot = 0;
+            uint32_t kpar = 0, vpar = 0;
+            bool klanded = false, vlanded = false;
             while (ok) {
                 const AlPiece *p = ref.next(S);
                 if (!(ok = p != nullptr)) break;
                 const int n = p->n;
                 if (n == 0) break;
-                const uint32_t nr = (uint32_t)(p->nrows + 15) / 16 * 16;
+                const uint32_t nr = p->nrows <= 16 ? 16 : 32;
+                // 16 rows: the warpgroups take chunks in turn, each with weights and outputs of its own, and the scores are
+                // two chunks ahead of the outputs; more: one chunk ahead
+                const int lead = nr == 16 ? 2 : 1;
                 // fp32 accumulator, fp16 operands, N = the two terms' rows; S^T: q K-major, O^T: both with the keys as rows
                 const uint32_t ids = (1u << 4) | (128u >> 4) << 24 | (2 * nr >> 3) << 17, idp = ids | (1u << 15) | (1u << 16);
                 if (!(ok = al_wait(&S.q_ready, (uint32_t)ref.k & 1u, &S.abort))) break;
-                for (int i = 0; ok && i <= n; i++) {
+                for (int i = 0; i < n + lead; i++) {
                     if (i < n) {
                         const int g = it + i;
                         if (g >= 2 && !(ok = al_wait(&S.s_free[g & 1], (uint32_t)((g >> 1) - 1) & 1u, &S.abort))) break;
                         const uint32_t d = tmem + kTmS + (uint32_t)(g & 1) * 2 * kR;
-                        uint32_t b0 = al_desc_lo(qs_a, 16);
-                        for (int sl = 0; sl < nK; sl++, b0 += qstep, kn++) {
-                            const int slot = kn % kKSlots;
-                            if (!(ok = al_wait(&S.kfull[slot], (uint32_t)(kn / kKSlots) & 1u, &S.abort))) break;
+                        const uint32_t b0 = al_desc_lo(qs_a, 16);
+#pragma unroll
+                        for (int sl = 0; sl < nK; sl++) {
+                            if (!klanded && !(ok = al_wait(&S.kfull[kslot], kpar, &S.abort))) break;
                             tc_fence_after();
+                            const uint32_t a = tmem + kTmK + 32u * (uint32_t)kslot;
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)
-                                kv_mma_ta(d, tmem + kTmK + 32u * (uint32_t)slot + 8u * kk, b0 + 2u * kk, hi128, ids, kk > 0 || sl > 0);
-                            tc_commit(&S.kempty[slot]);
+                                kv_mma_ta(d, a + 8u * kk, b0 + qstep * sl + 2u * kk, hi128, ids, kk > 0 || sl > 0);
+                            tc_commit(&S.kempty[kslot]);
+                            if (++kslot == kKSlots) kslot = 0, kpar ^= 1u;
+                            klanded = al_test(smem_addr(&S.kfull[kslot]), kpar);
                         }
                         if (!ok) break;
                         tc_commit(&S.s_full[g & 1]);
                     }
-                    if (i >= 1) {
-                        if (!(ok = al_wait(&S.p_ready, (uint32_t)(it + i - 1) & 1u, &S.abort))) break;
-                        for (int vs = 0; vs < nV; vs++, vn++) {
-                            const int slot = vn % slots, kh = vs / nDH, dh = vs - kh * nDH;
-                            if (!(ok = al_wait(&S.vfull[slot], (uint32_t)(vn / slots) & 1u, &S.abort))) break;
-                            tc_fence_after();
-                            const uint32_t a0 = ring_d + (uint32_t)(slot * (kVSlot / 16));
-                            const uint32_t b0 = al_desc_lo(ps_a + kh * 64 * 64, kChunk * 64);
+                    if (i >= lead) {
+                        const int g = it + i - lead;
+                        if (!(ok = al_wait(&S.p_ready[g & 1], (uint32_t)(g >> 1) & 1u, &S.abort))) break;
+                        const uint32_t d = tmem + kTmO + (lead == 2 ? (uint32_t)(g & 1) * 64u : 0u);
+                        const uint32_t pa = ps_a + (lead == 2 ? (uint32_t)(g & 1) * (kChunk * 64) : 0u);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ks++)
-                                al_mma(tmem + kTmO + (uint32_t)dh * 2 * kR, a0 + 128u * ks, hi128, b0 + 64u * ks, hip, idp,
-                                       ks > 0 || kh > 0);
-                            tc_commit(&S.vempty[slot]);
+                        for (int vs = 0; vs < nV; vs++) {
+                            const int kh = vs / nDH, dh = vs % nDH;
+                            if (!vlanded && !(ok = al_wait(&S.vfull[vslot], vpar, &S.abort))) break;
+                            tc_fence_after();
+                            const uint32_t a0 = ring_d + (uint32_t)(vslot * (kVSlot / 16));
+                            const uint32_t b0 = al_desc_lo(pa + kh * 64 * 64, kChunk * 64);
+#pragma unroll
+                            for (int k4 = 0; k4 < 4; k4++)
+                                al_mma(d + (uint32_t)dh * 2 * nr, a0 + 128u * k4, hi128, b0 + 64u * k4, hip, idp,
+                                       k4 > 0 || kh > 0);
+                            tc_commit(&S.vempty[vslot]);
+                            if (++vslot == kVSlots) vslot = 0, vpar ^= 1u;
+                            vlanded = al_test(smem_addr(&S.vfull[vslot]), vpar);
                         }
                         if (!ok) break;
-                        tc_commit(&S.pv_done);
+                        tc_commit(&S.pv_done[g & 1]);
                     }
                 }
                 it += n;
@@ -660,58 +716,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     } else {
-        // ---------------------------------------------------------- weights and sums: warpgroup wg owns rows
-        // 16 wg .. 16 wg + 15, its thread t key t of a chunk, and of the outputs dims t and t + 128
+        // ---------------------------------------------------------- weights and sums: thread t of a warpgroup owns key t of a
+        // chunk, and of the outputs dims t and t + 128.  Up to 16 rows the warpgroups take the chunks in turn and add up at
+        // the end; more, and warpgroup wg owns rows 16 wg .. 16 wg + 15 of every chunk.
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        const int wg = warp >> 2, t = tid & 127, r0 = 16 * wg;
+        const int wg = warp >> 2, t = tid & 127, own = 16 * wg;  // own: this warpgroup's place in what both have 16 of
         PieceRef ref;
         int it = 0;  // chunks so far
-        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)r0;
         const int lp = kv.page_rows >= kChunk ? 7 : 31 - __clz(kv.page_rows);
         bool ok = true;
-        while (ok) {
+        while (true) {
             const AlPiece *p = ref.next(S);
             __syncwarp();
             if (p == nullptr) give_up();
-            if (al_bar_or(wg, p == nullptr)) break;  // (and the rows of the last piece are no longer needed)
-            const int n = p->n, nrows = p->nrows, nr = (nrows + 15) / 16 * 16;
+            if (kv_bar_or(p == nullptr || !ok)) break;  // (and the rows of the last piece are no longer needed)
+            const int n = p->n, nrows = p->nrows, nr = nrows <= 16 ? 16 : 32;
             if (n == 0) break;
-            if (r0 >= nrows) {  // (the first warpgroup always has rows)
-                if (lane == 0) mbar_arrive(&S.q_ready);
-                for (int i = 0; i < n && ok; i++, it++) {
-                    ok = al_wait(&S.s_full[it & 1], (uint32_t)(it >> 1) & 1u, &S.abort);
-                    if (lane == 0) mbar_arrive(&S.s_free[it & 1]), mbar_arrive(&S.p_ready);
-                    // (a second arrival must not meet the same phase)
-                    ok = ok && al_wait(&S.pv_done, (uint32_t)it & 1u, &S.abort);
-                    __syncwarp();
-                }
-                ok = !al_bar_or(wg, !ok);
-                if (lane == 0) ref.done(S);
-                continue;
-            }
+            const bool turns = nr == 16;
+            const int r0 = turns ? 0 : own;
             if (t < 16) {
                 const int r = r0 + t, gs = p->gs, ln = p->lane0 + r / gs;
                 const bool in = r < nrows;
                 const int pl = in ? A.positions[ln] - p->base : -1;
-                S.rowid[r] = in ? ln * A.n_heads + p->head0 + r % gs : -1;
+                S.rowid[r] = in ? ln * A.n_heads + p->head0 + r % gs : -1;  // (in turns: both write the same)
                 S.rowhi[r] = max(-1, min(pl, p->lim - 1));
                 S.rowlo[r] = A.window && pl >= A.window ? pl - A.window : -1;
-                S.mc[r] = in ? kNoKey : kInf;  // (what lies in the place of a row that is not there gets no weight)
+                S.mc[own + t] = in ? kNoKey : kInf;  // (what lies in the place of a row that is not there gets no weight)
             }
-            al_bar(wg);
+            kv_bar_or(false);
             // the rows' q with the softmax's scale, multiplied by a power of two that brings the largest value of the row
             // to 2^13 .. 2^14, as two fp16 terms
-            const int per = hd / 8;  // threads to a row
-            for (int e = t; e < 16 * per; e += 128) {
-                const int rr = e / per, d8 = e - rr * per, r = r0 + rr;
+            constexpr int per = HD / 8;  // threads to a row
+#pragma unroll 2
+            for (int e = tid; e < nr * per; e += 256) {
+                const int r = e / per, d8 = e % per;
                 const bool in = r < nrows;
                 uint4 a, b;
-                al_ld32(A.q + (in ? (int64_t)S.rowid[r] * hd + 8 * d8 : 0), in, a, b);
+                al_ld32(A.q + (in ? (int64_t)S.rowid[r] * HD + 8 * d8 : 0), in, a, b);
                 float x[8] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
                               __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
                 float top = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 8; k++) x[k] = __fmul_rn(x[k], D.c), top = fmaxf(top, fabsf(x[k]));
+#pragma unroll
                 for (int off = 1; off < per; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                 const int k2 = top < kInf ? min(126, 140 - (int)(__float_as_uint(top) >> 23)) : 0;
                 const float f = __uint_as_float((uint32_t)(k2 + 127) << 23);
@@ -721,19 +768,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 uint4 h, l;
                 kv_split2(x[0], x[1], h.x, l.x), kv_split2(x[2], x[3], h.y, l.y);
                 kv_split2(x[4], x[5], h.z, l.z), kv_split2(x[6], x[7], h.w, l.w);
-                if (r < nr) {
-                    const uint32_t at = smem_addr(qs) + (uint32_t)((d8 >> 3) * L.qslice + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
-                    sts128(at, h);
-                    sts128(at + nr * 128, l);
-                }
+                const uint32_t at = smem_addr(qs) + (uint32_t)((d8 >> 3) * L.qslice + r * 128 + (((d8 & 7) ^ (r & 7)) << 4));
+                sts128(at, h);
+                sts128(at + nr * 128, l);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.q_ready);
-            al_bar(wg);  // (the rows' factors)
-            float lsum[16], acc[2][16];
+            kv_bar_or(false);  // (the rows' factors)
+            const int arrivals = turns ? 2 : 1;
+            const uint32_t half = 2 * nr;  // columns of O^T's second half of dims behind the first
+            const uint32_t lanes_at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+            const uint32_t at_o = lanes_at + kTmO + (turns ? 64u * wg : (uint32_t)r0);
+            const uint32_t at_p = smem_addr(ps) + (turns ? (uint32_t)wg * (kChunk * 64) : 0u) + (uint32_t)t * 64;
+            float lsum[16], acc[nDH][16];
 #pragma unroll
-            for (int j = 0; j < 16; j++) lsum[j] = acc[0][j] = acc[1][j] = 0.0f;
+            for (int j = 0; j < 16; j++) {
+                lsum[j] = 0.0f;
+#pragma unroll
+                for (int h = 0; h < nDH; h++) acc[h][j] = 0.0f;
+            }
             // 16 columns' terms of the products
             auto sum2 = [&](uint32_t at, float (&o)[16]) {
                 uint32_t h[16], l[16];
@@ -746,29 +800,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             // adds a chunk's products to the outputs
             auto take = [&]() {
-                float o[16];
-                sum2(tl + kTmO, o);
 #pragma unroll
-                for (int j = 0; j < 16; j++) acc[0][j] = __fadd_rn(acc[0][j], o[j]);
-                if (nDH == 2) {
-                    sum2(tl + kTmO + 2 * kR, o);
+                for (int h = 0; h < nDH; h++) {
+                    float o[16];
+                    sum2(at_o + h * half, o);
 #pragma unroll
-                    for (int j = 0; j < 16; j++) acc[1][j] = __fadd_rn(acc[1][j], o[j]);
+                    for (int j = 0; j < 16; j++) acc[h][j] = __fadd_rn(acc[h][j], o[j]);
                 }
             };
 
-            for (int i = 0; i < n; i++, it++) {
-                const int cr = p->row0(i), sk = p->sk, key = cr + t;
-                const bool fail = !al_wait(&S.s_full[it & 1], (uint32_t)(it >> 1) & 1u, &S.abort);
+            const int step = turns ? 2 : 1, i0 = turns ? (it ^ wg) & 1 : 0;  // this warpgroup's chunks
+            int last = -1;  // the last one
+            for (int i = i0; i < n; i += step) {
+                const int g = it + i, cr = p->row0(i), sk = p->sk, key = cr + t;
+                const bool fail = !al_wait(&S.s_full[g & 1], (uint32_t)(g >> 1) & 1u, &S.abort);
                 __syncwarp();  // (the tensor-memory loads are for whole warps)
                 tc_fence_after();
-                const uint32_t bad = S.bad[it % kBadRing];
+                const uint32_t bad = S.bad[g % kBadRing];
                 const bool edge = p->edge_in(cr, cr + kChunk) || bad;
                 float s[16];
-                sum2(tl + kTmS + (uint32_t)(it & 1) * 2 * kR, s);
+                sum2(lanes_at + kTmS + (uint32_t)(g & 1) * 2 * kR + (uint32_t)r0, s);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&S.s_free[it & 1]);
+                if (lane < arrivals) mbar_arrive(&S.s_free[g & 1]);
 #pragma unroll
                 for (int j = 0; j < 16; j++) s[j] = __fmul_rn(s[j], S.qf[r0 + j]);
                 // whether row r of the tile sees this thread's key
@@ -778,10 +832,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; j++)
                         if (!sees(r0 + j)) s[j] = -kInf;
-                bool big = i == 0;
-                if (i > 0)
+                bool big = last < 0;
+                if (last >= 0)
 #pragma unroll
-                    for (int j = 0; j < 16; j++) big |= __fsub_rn(s[j], S.mc[r0 + j]) > kStale;
+                    for (int j = 0; j < 16; j++) big |= __fsub_rn(s[j], S.mc[own + j]) > kStale;
                 const bool update = al_bar_or(wg, big || fail);
                 if (update) {
                     if (al_bar_or(wg, fail)) {
@@ -794,10 +848,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; j++) m[j] = s[j];
                     const float top = al_reduce16<true>(m, lane);
-                    if (lane < 16) S.red[warp & 3][r0 + lane] = top;
+                    if (lane < 16) S.red[warp & 3][own + lane] = top;
                     al_bar(wg);
                     if (t < 16) {
-                        const int r = r0 + t;
+                        const int r = own + t;
                         const float mx = fmaxf(fmaxf(S.red[0][r], S.red[1][r]), fmaxf(S.red[2][r], S.red[3][r]));
                         const float old = S.mc[r], mc = mx > -kInf ? fmaxf(mx, old) : old;
                         S.mc[r] = mc;
@@ -805,16 +859,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     al_bar(wg);
 #pragma unroll
-                    for (int j = 0; j < 16; j++) lsum[j] = __fmul_rn(lsum[j], S.alpha[r0 + j]);
+                    for (int j = 0; j < 16; j++) lsum[j] = __fmul_rn(lsum[j], S.alpha[own + j]);
                 }
                 // (a masked score stays minus infinity, the weight 0)
 #pragma unroll
                 for (int j = 0; j < 16; j++) {
-                    s[j] = __fmul_rn(al_ex2(__fsub_rn(s[j], S.mc[r0 + j])), kUp);
+                    s[j] = __fmul_rn(al_ex2(__fsub_rn(s[j], S.mc[own + j])), kUp);
                     lsum[j] = __fadd_rn(lsum[j], s[j]);
                 }
-                if (i > 0) {  // the products of the chunk before: P is read, and O^T is there
-                    al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort);
+                if (last >= 0) {  // the products of the chunk before: P is read, and O^T is there
+                    al_wait(&S.pv_done[last & 1], (uint32_t)(last >> 1) & 1u, &S.abort);
                     __syncwarp();
                 }
                 // the weights, as two fp16 terms, a key's rows side by side
@@ -828,65 +882,103 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int u = 0; u < 2; u++) {
                         const int c = u * nr + r0 + 8 * q;
-                        sts128(smem_addr(ps) + (uint32_t)((c >> 5) * (kChunk * 64) + t * 64 + ((((c >> 3) & 3) ^ ((t >> 1) & 3)) << 4)),
-                               w2[u]);
+                        sts128(at_p + (uint32_t)((c >> 5) * (kChunk * 64) + ((((c >> 3) & 3) ^ ((t >> 1) & 3)) << 4)), w2[u]);
                     }
                 }
-                if (i > 0) {
+                if (last >= 0) {
                     tc_fence_after();
                     take();
                     if (update)
 #pragma unroll
                         for (int j = 0; j < 16; j++) {
-                            const float al = S.alpha[r0 + j];
-                            acc[0][j] = __fmul_rn(acc[0][j], al);
-                            acc[1][j] = __fmul_rn(acc[1][j], al);
+                            const float al = S.alpha[own + j];
+#pragma unroll
+                            for (int h = 0; h < nDH; h++) acc[h][j] = __fmul_rn(acc[h][j], al);
                         }
                 }
+                last = g;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&S.p_ready);
+                if (lane < arrivals) mbar_arrive(&S.p_ready[g & 1]);
             }
-            if (!ok) break;
+            it += n;
+            if (ok && last >= 0) {
+                ok = al_wait(&S.pv_done[last & 1], (uint32_t)(last >> 1) & 1u, &S.abort);
+                __syncwarp();
+                tc_fence_after();
+                take();
+                tc_fence_before();
+            }
             // the sums over the keys
             const float l4 = al_reduce16<false>(lsum, lane);
-            if (lane < 16) S.red[warp & 3][r0 + lane] = l4;
-            if (al_bar_or(wg, !al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort))) {
-                ok = false;
-                break;
+            if (lane < 16) S.red[warp & 3][own + lane] = l4;
+            if (kv_bar_or(!ok)) break;  // (the weights' place is free as well)
+            if (t < 16) {
+                const int r = own + t;
+                S.sum[r] = (S.red[0][r] + S.red[1][r]) + (S.red[2][r] + S.red[3][r]);
             }
-            tc_fence_after();
+            // in turns: the warpgroups' halves of the rows change places, [half of dims][8 rows][128] in the weights' place
+            float *const other = reinterpret_cast<float *>(ps) + (wg ^ 1) * 1024 * nDH, *const mine = reinterpret_cast<float *>(ps) + wg * 1024 * nDH;
+            if (turns)
+#pragma unroll
+                for (int h = 0; h < nDH; h++)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) other[(h * 8 + j) * 128 + t] = wg ? acc[h][j] : acc[h][8 + j];
+            kv_bar_or(false);
             if (t < 16) {
                 const int r = r0 + t;
                 float *o = nullptr;
+                float f0 = 1.0f, f1 = 0.0f;  // the factors of this warpgroup's sums and of the other's
                 if (r < nrows) {
-                    float l = (S.red[0][r] + S.red[1][r]) + (S.red[2][r] + S.red[3][r]);
+                    float l = S.sum[own + t], mc = S.mc[own + t];
+                    if (turns) {
+                        const float m1 = S.mc[(own ^ 16) + t], m = fmaxf(mc, m1);
+                        f0 = mc == kNoKey ? 0.0f : al_ex2(__fsub_rn(mc, m));
+                        f1 = m1 == kNoKey ? 0.0f : al_ex2(__fsub_rn(m1, m));
+                        l = f0 * l + f1 * S.sum[(own ^ 16) + t];
+                        mc = m;
+                    }
                     const int64_t id = S.rowid[r];
+                    float inv = 1.0f;
                     if (p->whole) {
-                        o = A.out + id * hd;
-                        l = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+                        o = A.out + id * HD;
+                        inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
                     } else {
                         const int64_t row = (int64_t)(2 * blockIdx.x + p->begins) * D.cap + r;
-                        o = W.part + row * hd;
-                        W.ml[row] = make_float2(S.mc[r], l);
-                        l = 1.0f;
+                        o = W.part + row * HD;
+                        if (!turns || wg == 0) W.ml[row] = make_float2(mc, l);
                     }
-                    S.alpha[r] = l;
+                    f0 *= inv, f1 *= inv;
                 }
-                S.optr[r] = o;
+                S.optr[own + t] = o;
+                S.alpha[own + t] = f0;
+                S.red[0][own + t] = f1;
             }
-            take();
-            tc_fence_before();
             al_bar(wg);
             if (lane == 0) ref.done(S);
+            if (turns) {
 #pragma unroll
-            for (int j = 0; j < 16; j++) {
-                float *o = S.optr[r0 + j];
-                if (o) {
-                    const float al = S.alpha[r0 + j];
-                    if (t < hd) o[t] = __fmul_rn(acc[0][j], al);
-                    if (t + 128 < hd) o[t + 128] = __fmul_rn(acc[1][j], al);
+                for (int j = 0; j < 8; j++) {
+                    float *o = S.optr[own + 8 * wg + j];
+                    if (o) {
+                        const float f0 = S.alpha[own + 8 * wg + j], f1 = S.red[0][own + 8 * wg + j];
+#pragma unroll
+                        for (int h = 0; h < nDH; h++)
+                            if (HD >= 128 || t < HD)
+                                o[t + 128 * h] = __fmaf_rn(wg ? acc[h][8 + j] : acc[h][j], f0, __fmul_rn(mine[(h * 8 + j) * 128 + t], f1));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    float *o = S.optr[own + j];
+                    if (o) {
+                        const float f0 = S.alpha[own + j];
+#pragma unroll
+                        for (int h = 0; h < nDH; h++)
+                            if (HD >= 128 || t < HD) o[t + 128 * h] = __fmul_rn(acc[h][j], f0);
+                    }
                 }
             }
         }
@@ -956,6 +1048,30 @@ qlin_status attend_few(const Kv4Args &A, const AlWs &w, int64_t rows, cudaStream
                       st, args, "kv4_few_merge_kernel");
 }
 
+// The tensor map of a pool's codes: its rows, boxes of a page or 128 of its
+// rows, swizzled so that the 16 bytes of eight rows on end meet all banks.
+qlin_status codes_map(const void *p, const qlin_kv4 &c, int n_kv, int hd, CUtensorMap *out) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)fn;
+    }();
+    QLIN_REQUIRE(encode, QLIN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t gdim[2] = {(cuuint64_t)hd / 2, (cuuint64_t)c.n_pages * n_kv * c.page_rows}, gstride[1] = {(cuuint64_t)hd / 2};
+    const cuuint32_t box[2] = {(cuuint32_t)hd / 2, (cuuint32_t)(c.page_rows < kChunk ? c.page_rows : kChunk)}, estride[2] = {1, 1};
+    const CUtensorMapSwizzle swizzle = hd == 256   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                       : hd == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                   : CU_TENSOR_MAP_SWIZZLE_32B;
+    const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), gdim, gstride, box, estride,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    QLIN_REQUIRE(r == CUDA_SUCCESS, QLIN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return QLIN_OK;
+}
+
 qlin_status attend_tc(const Kv4Args &K, const AlWs &w, cudaStream_t st) {
     AlArgs A{};
     A.q = K.q, A.positions = K.positions, A.seqs = K.seqs, A.out = K.out, A.status = K.status;
@@ -971,7 +1087,9 @@ qlin_status attend_tc(const Kv4Args &K, const AlWs &w, cudaStream_t st) {
     D.merge = A.n_lanes <= kSelfPlan ? 1 : 16;
     D.setup = 4;
     D.c = K.c;
-    const void *kern = (const void *)kv4_attn_kernel;
+    const void *kern = A.hd == 64    ? (const void *)kv4_attn_kernel<64>
+                       : A.hd == 128 ? (const void *)kv4_attn_kernel<128>
+                                     : (const void *)kv4_attn_kernel<256>;
     const size_t plan_smem = 6 * sizeof(int) * (size_t)A.n_lanes;
     QLIN_REQUIRE(kAlSmem <= max_smem_optin(), QLIN_ERR_UNSUPPORTED, "qlin_attention_kv4: shared memory");
     blocks_per_sm(kern, kAlSmem);  // raises the dynamic shared-memory limit once
@@ -981,7 +1099,10 @@ qlin_status attend_tc(const Kv4Args &K, const AlWs &w, cudaStream_t st) {
         if (qlin_status e = launch_pdl((const void *)al_plan_kernel, dim3(1), dim3(kPlanThreads), plan_smem, st, pargs,
                                        "al_plan_kernel"))
             return e;
-    void *args[] = {(void *)&A, (void *)&D, (void *)&w, (void *)&K.kv};
+    KvMaps maps;
+    if (qlin_status e = codes_map(K.kv.k, K.kv, A.n_kv, A.hd, &maps.k)) return e;
+    if (qlin_status e = codes_map(K.kv.v, K.kv, A.n_kv, A.hd, &maps.v)) return e;
+    void *args[] = {(void *)&maps, (void *)&A, (void *)&D, (void *)&w, (void *)&K.kv};
     if (qlin_status e = launch_pdl(kern, dim3(D.grid), dim3(kTcThreads), kAlSmem, st, args, "kv4_attn_kernel")) return e;
     const int64_t total = (int64_t)A.n_lanes * A.n_heads, blocks = (total + D.merge - 1) / D.merge;
     return launch_pdl((const void *)al_merge_kernel, dim3((unsigned)(blocks < 8 * D.grid ? blocks : 8 * D.grid)),
