@@ -280,13 +280,12 @@ constexpr int kProd0 = 8;             // behind two warpgroups of the weights
 constexpr int kMma = kProd0 + kProd;  // the warp that issues the MMAs; then the ones that describe pieces and copy
 constexpr int kWalk = kMma + 1, kCopy = kMma + 2;
 constexpr int kTcThreads = 32 * (kMma + 4);
-constexpr int kVSlot = 16384;         // 64 keys x 128 dims
-constexpr int kVSlots = 6, kKSlots = 8;
+constexpr int kVSlot = 16384;         // 64 keys x 128 dims of V
+constexpr int kVRing = 6 * kVSlot;    // half chunks
 constexpr int kMaxStages = 4;         // chunks of codes of K, and of V
 constexpr int kBadRing = 64;
-// tensor memory: S^T twice [2 kR], O^T [4 kR], slices of K (128 keys x 64 dims)
+// tensor memory: S^T twice [2 kR], O^T [4 kR], K of two chunks
 constexpr uint32_t kTmS = 0, kTmO = 4 * kR, kTmK = 8 * kR, kTmCols = 512;
-static_assert(kTmK + 32 * kKSlots <= kTmCols, "tensor memory");
 constexpr float kStale = 4.0f;        // how far a score may exceed the maximum in use
 constexpr float kUp = 2048.0f;        // weights are multiplied by this: below 2^15, and steps of 2^-35 of the largest
 
@@ -303,10 +302,13 @@ struct KvCfg {
     // 128) K's, groups 2 and 3 V's
     static constexpr bool kBoth = HD == 256;
     static constexpr int kKWarps = 4 * nK, kVWarps = 4 * nV;  // warps that read a chunk's codes
+    static constexpr int kHalf = nDH * kVSlot, kHalves = kVRing / kHalf;  // half a chunk of V in the ring, and how many
+    static constexpr uint32_t kKCols = 32 * nK;               // tensor memory columns of a chunk's K
+    static_assert(kTmK + 2 * kKCols <= kTmCols, "tensor memory");
 };
 
 struct KvCtl {
-    uint64_t kfull[kKSlots], kempty[kKSlots], vfull[kVSlots], vempty[kVSlots];
+    uint64_t kfull[2], kempty[2], vfull[6], vempty[6];
     uint64_t kst_full[kMaxStages], kst_empty[kMaxStages], vst_full[kMaxStages], vst_empty[kMaxStages];
     uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready, drain;
     uint64_t pc_full[kPieceRing], pc_empty[kPieceRing];
@@ -332,7 +334,7 @@ struct KvLayout {
     int q, qslice, p, codes, scales, nks, nvs;
     __device__ __forceinline__ KvLayout(int rmax) {
         qslice = 2 * (rmax <= 16 ? 16 : 32) * 128;
-        q = kVSlots * kVSlot;
+        q = kVRing;
         p = q + C::nK * qslice;
         codes = p + 2 * kChunk * 64;
         const int n = min((kAlSmem - 1024 - (int)sizeof(KvCtl) - 16 - codes) / C::kStage, 2 * kMaxStages);
@@ -340,7 +342,7 @@ struct KvLayout {
         scales = codes + n * C::kCodes;
     }
 };
-static_assert(kAlSmem - 1024 - (int)sizeof(KvCtl) - 16 - kVSlots * kVSlot - 4 * 2 * 32 * 128 - 2 * kChunk * 64 >=
+static_assert(kAlSmem - 1024 - (int)sizeof(KvCtl) - 16 - kVRing - 4 * 2 * 32 * 128 - 2 * kChunk * 64 >=
                   4 * KvCfg<256>::kStage,
               "two stages of K and two of V");
 
@@ -406,8 +408,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 32) {
-        for (int s = 0; s < kKSlots; s++) mbar_init(&S.kfull[s], 4), mbar_init(&S.kempty[s], 1);
-        for (int s = 0; s < kVSlots; s++) mbar_init(&S.vfull[s], 4), mbar_init(&S.vempty[s], 1);
+        for (int s = 0; s < 2; s++) mbar_init(&S.kfull[s], C::kKWarps), mbar_init(&S.kempty[s], 1);
+        for (int s = 0; s < C::kHalves; s++) mbar_init(&S.vfull[s], C::kVWarps / 2), mbar_init(&S.vempty[s], 1);
         for (int s = 0; s < kMaxStages; s++) {
             mbar_init(&S.kst_full[s], 1), mbar_init(&S.kst_empty[s], C::kKWarps);
             mbar_init(&S.vst_full[s], 1), mbar_init(&S.vst_empty[s], C::kVWarps);
@@ -461,11 +463,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int vrow = 64 * kh + (t & 63), vg = 4 * dh + 2 * (t >> 6);
         const uint32_t k0 = place(t, 2 * pg), k1 = place(t, 2 * pg + 1), ks = (uint32_t)(t * (HD / 32) + 2 * pg);
         const uint32_t v0 = place(vrow, vg), v1 = place(vrow, vg + 1), vs = (uint32_t)(vrow * (HD / 32) + vg);
-        const uint32_t to_v = smem_addr(ring) + (uint32_t)((t >> 6) * 8192 + (t & 63) * 128);
-        const uint32_t to_k = tmem + kTmK + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t to_v = smem_addr(ring) + (uint32_t)(dh * kVSlot + (t >> 6) * 8192 + (t & 63) * 128);
+        const uint32_t to_k = tmem + kTmK + 32u * (uint32_t)pg + ((uint32_t)(32 * (warp & 3)) << 16);
         int kst = 0, vst = 0;
         uint32_t kpar = 0, vpar = 0;
-        int vslot = ev;
+        int vslot = kh;
         uint32_t vround = 0;
         bool ok = true;
         for (int c = 0; ok && (does_k || does_v); c++) {
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&S.kst_empty[kst]);
                     if (++kst == L.nks) kst = 0, kpar ^= 1u;
-                    const int kn = c * nK + pg, slot = kn % kKSlots, round = kn / kKSlots;
+                    const int slot = c & 1, round = c >> 1;
                     if (round && !(ok = kv_wait_all(&S.kempty[slot], (uint32_t)(round - 1) & 1u, &S.abort))) break;
                     __syncwarp();
                     tc_fence_after();  // (the products that read what lay there)
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             kv4_decode8(w[4 * h + i], s2, m2, x);
                             o[4 * i] = x[0], o[4 * i + 1] = x[1], o[4 * i + 2] = x[2], o[4 * i + 3] = x[3];
                         }
-                        tm_st16(to_k + 32u * (uint32_t)slot + 16u * h, o);
+                        tm_st16(to_k + C::kKCols * (uint32_t)slot + 16u * h, o);
                     }
                     tm_wait_st();
                     tc_fence_before();
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int i = 0; i < 4; i++) {
                             uint32_t o[4];
                             kv4_decode8(w[4 * h + i], s2, m2, o);
-                            sts128(to_v + (uint32_t)(vslot * kVSlot + (((4 * h + i) ^ (t & 7)) << 4)),
+                            sts128(to_v + (uint32_t)(vslot * C::kHalf + (((4 * h + i) ^ (t & 7)) << 4)),
                                    make_uint4(o[0], o[1], o[2], o[3]));
                         }
                     }
@@ -536,8 +538,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.vfull[vslot]);
-                vslot += nV;
-                if (vslot >= kVSlots) vslot -= kVSlots, vround++;
+                vslot += 2;
+                if (vslot >= C::kHalves) vslot -= C::kHalves, vround++;
             }
             if (end) break;
         }
@@ -638,69 +640,58 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (warp == kMma && al_elect()) {
             // ------------------------------------------------------ the MMAs
-            // One thread paces a chunk: what it needs is in registers, and whether the next slice has landed is asked while
-            // the products of this one are issued.
             PieceRef ref;
             int it = 0;  // chunks so far
             bool ok = true;
             const uint32_t qs_a = smem_addr(qs), ps_a = smem_addr(ps), qstep = (uint32_t)L.qslice >> 4;
             const uint32_t ring_d = al_desc_lo(smem_addr(ring), 8192);
             const uint32_t hi128 = al_desc_hi(1024, 2), hip = al_desc_hi(512, 4);
-            int kslot = 0, vslot = 0;
-            uint32_t kpar = 0, vpar = 0;
-            bool klanded = false, vlanded = false;
+            int vslot = 0;
+            uint32_t vpar = 0;
             while (ok) {
                 const AlPiece *p = ref.next(S);
                 if (!(ok = p != nullptr)) break;
                 const int n = p->n;
                 if (n == 0) break;
                 const uint32_t nr = p->nrows <= 16 ? 16 : 32;
-                // 16 rows: the warpgroups take chunks in turn, each with weights and outputs of its own, and the scores are
-                // two chunks ahead of the outputs; more: one chunk ahead
-                const int lead = nr == 16 ? 2 : 1;
+                const bool turns = nr == 16;  // the warpgroups take chunks in turn, each with weights and outputs of its own
                 // fp32 accumulator, fp16 operands, N = the two terms' rows; S^T: q K-major, O^T: both with the keys as rows
                 const uint32_t ids = (1u << 4) | (128u >> 4) << 24 | (2 * nr >> 3) << 17, idp = ids | (1u << 15) | (1u << 16);
                 if (!(ok = al_wait(&S.q_ready, (uint32_t)ref.k & 1u, &S.abort))) break;
-                for (int i = 0; i < n + lead; i++) {
+                for (int i = 0; i <= n; i++) {
                     if (i < n) {
                         const int g = it + i;
                         if (g >= 2 && !(ok = al_wait(&S.s_free[g & 1], (uint32_t)((g >> 1) - 1) & 1u, &S.abort))) break;
                         const uint32_t d = tmem + kTmS + (uint32_t)(g & 1) * 2 * kR;
                         const uint32_t b0 = al_desc_lo(qs_a, 16);
+                        if (!(ok = al_wait(&S.kfull[g & 1], (uint32_t)(g >> 1) & 1u, &S.abort))) break;
+                        tc_fence_after();
+                        const uint32_t a = tmem + kTmK + C::kKCols * (uint32_t)(g & 1);
 #pragma unroll
-                        for (int sl = 0; sl < nK; sl++) {
-                            if (!klanded && !(ok = al_wait(&S.kfull[kslot], kpar, &S.abort))) break;
-                            tc_fence_after();
-                            const uint32_t a = tmem + kTmK + 32u * (uint32_t)kslot;
-#pragma unroll
-                            for (int kk = 0; kk < 4; kk++)
-                                kv_mma_ta(d, a + 8u * kk, b0 + qstep * sl + 2u * kk, hi128, ids, kk > 0 || sl > 0);
-                            tc_commit(&S.kempty[kslot]);
-                            if (++kslot == kKSlots) kslot = 0, kpar ^= 1u;
-                            klanded = al_test(smem_addr(&S.kfull[kslot]), kpar);
-                        }
-                        if (!ok) break;
+                        for (int kk = 0; kk < 4 * nK; kk++)
+                            kv_mma_ta(d, a + 8u * kk, b0 + qstep * (kk / 4) + 2u * (kk % 4), hi128, ids, kk > 0);
+                        tc_commit(&S.kempty[g & 1]);
                         tc_commit(&S.s_full[g & 1]);
                     }
-                    if (i >= lead) {
-                        const int g = it + i - lead;
+                    if (i >= 1) {
+                        const int g = it + i - 1;
                         if (!(ok = al_wait(&S.p_ready[g & 1], (uint32_t)(g >> 1) & 1u, &S.abort))) break;
-                        const uint32_t d = tmem + kTmO + (lead == 2 ? (uint32_t)(g & 1) * 64u : 0u);
-                        const uint32_t pa = ps_a + (lead == 2 ? (uint32_t)(g & 1) * (kChunk * 64) : 0u);
+                        const uint32_t d = tmem + kTmO + (turns ? (uint32_t)(g & 1) * 64u : 0u);
+                        const uint32_t pa = ps_a + (turns ? (uint32_t)(g & 1) * (kChunk * 64) : 0u);
 #pragma unroll
-                        for (int vs = 0; vs < nV; vs++) {
-                            const int kh = vs / nDH, dh = vs % nDH;
-                            if (!vlanded && !(ok = al_wait(&S.vfull[vslot], vpar, &S.abort))) break;
+                        for (int kh = 0; kh < 2; kh++) {
+                            if (!(ok = al_wait(&S.vfull[vslot], vpar, &S.abort))) break;
                             tc_fence_after();
-                            const uint32_t a0 = ring_d + (uint32_t)(vslot * (kVSlot / 16));
+                            const uint32_t a0 = ring_d + (uint32_t)(vslot * (C::kHalf / 16));
                             const uint32_t b0 = al_desc_lo(pa + kh * 64 * 64, kChunk * 64);
 #pragma unroll
-                            for (int k4 = 0; k4 < 4; k4++)
-                                al_mma(d + (uint32_t)dh * 2 * nr, a0 + 128u * k4, hi128, b0 + 64u * k4, hip, idp,
-                                       k4 > 0 || kh > 0);
+                            for (int dh = 0; dh < nDH; dh++)
+#pragma unroll
+                                for (int k4 = 0; k4 < 4; k4++)
+                                    al_mma(d + (uint32_t)dh * 2 * nr, a0 + (uint32_t)(dh * (kVSlot / 16)) + 128u * k4, hi128,
+                                           b0 + 64u * k4, hip, idp, k4 > 0 || kh > 0);
                             tc_commit(&S.vempty[vslot]);
-                            if (++vslot == kVSlots) vslot = 0, vpar ^= 1u;
-                            vlanded = al_test(smem_addr(&S.vfull[vslot]), vpar);
+                            if (++vslot == C::kHalves) vslot = 0, vpar ^= 1u;
                         }
                         if (!ok) break;
                         tc_commit(&S.pv_done[g & 1]);
@@ -823,8 +814,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane < arrivals) mbar_arrive(&S.s_free[g & 1]);
-#pragma unroll
-                for (int j = 0; j < 16; j++) s[j] = __fmul_rn(s[j], S.qf[r0 + j]);
                 // whether row r of the tile sees this thread's key
                 const bool there = !(bad >> (t >> lp) & 1u);
                 auto sees = [&](int r) { return there && key <= S.rowhi[r] && (key > S.rowlo[r] || key < sk); };
@@ -833,9 +822,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int j = 0; j < 16; j++)
                         if (!sees(r0 + j)) s[j] = -kInf;
                 bool big = last < 0;
+                // (a power of two times a score is exact: one rounding)
+                auto over = [&](int j) { return __fmaf_rn(s[j], S.qf[r0 + j], -S.mc[own + j]); };
+                float e[16];
                 if (last >= 0)
 #pragma unroll
-                    for (int j = 0; j < 16; j++) big |= __fsub_rn(s[j], S.mc[own + j]) > kStale;
+                    for (int j = 0; j < 16; j++) e[j] = over(j), big |= e[j] > kStale;
                 const bool update = al_bar_or(wg, big || fail);
                 if (update) {
                     if (al_bar_or(wg, fail)) {
@@ -846,7 +838,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // new maxima
                     float m[16];
 #pragma unroll
-                    for (int j = 0; j < 16; j++) m[j] = s[j];
+                    for (int j = 0; j < 16; j++) m[j] = __fmul_rn(s[j], S.qf[r0 + j]);
                     const float top = al_reduce16<true>(m, lane);
                     if (lane < 16) S.red[warp & 3][own + lane] = top;
                     al_bar(wg);
@@ -859,12 +851,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     al_bar(wg);
 #pragma unroll
-                    for (int j = 0; j < 16; j++) lsum[j] = __fmul_rn(lsum[j], S.alpha[own + j]);
+                    for (int j = 0; j < 16; j++) lsum[j] = __fmul_rn(lsum[j], S.alpha[own + j]), e[j] = over(j);
                 }
                 // (a masked score stays minus infinity, the weight 0)
 #pragma unroll
                 for (int j = 0; j < 16; j++) {
-                    s[j] = __fmul_rn(al_ex2(__fsub_rn(s[j], S.mc[own + j])), kUp);
+                    s[j] = __fmul_rn(al_ex2(e[j]), kUp);
                     lsum[j] = __fadd_rn(lsum[j], s[j]);
                 }
                 if (last >= 0) {  // the products of the chunk before: P is read, and O^T is there
