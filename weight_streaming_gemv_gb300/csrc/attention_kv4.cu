@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     kv4_attn_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ AlArgs A, const __grid_constant__ AlDims D,
                     const __grid_constant__ AlWs W, const __grid_constant__ qlin_kv4 kv) {
     using C = KvCfg<HD>;
-    constexpr int nK = C::nK, nDH = C::nDH, nV = C::nV;
+    constexpr int nK = C::nK, nDH = C::nDH;
     extern __shared__ uint8_t kv_raw[];
     uint8_t *const smem = kv_raw + ((1024u - (smem_addr(kv_raw) & 1023u)) & 1023u);  // the swizzled operands' alignment
     KvCtl &S = *reinterpret_cast<KvCtl *>(smem + (kAlSmem - 1024 - sizeof(KvCtl)) / 16 * 16);

@@ -17,10 +17,16 @@
 // warp hold and hand over by shuffles, and a series of four terms.
 //
 // One cluster of CTAs per row, whose shared memory holds the row: it is read
-// once.  A cut is found with a histogram of 2048 bins over y (counts for
-// top-k, weights for top-p; a CTA sums a share of the bins over the cluster's),
-// then among the words of one bin, which go to a list in the first CTA.  Where
-// few words are left the first CTA does the rest alone.
+// once.  A histogram of 2048 bins over y counts the words and adds up an eighth
+// of a bin's width each lies above its border, which gives a bin's weight to
+// about 10^-4; a CTA sums a share of the bins over the cluster's.  So top-k's
+// border is known to a bin and top-p's to one or two.  Their words go to a list
+// in the first CTA, which sorts it, while every thread adds up the exact weights
+// of the words before them (and of all) in registers; the border is then a place
+// in the list.  Where all words up to the border fit the list the first CTA does
+// the rest alone.  Where a list does not hold the border (many equal logits, a
+// top_p next to 1) a histogram of exact weights, and more of them over the bits
+// of the logits of one bin, narrow it down.
 #include <cmath>
 
 #include "launch.cuh"
@@ -33,8 +39,8 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048, kLocalBins = 512;
-constexpr int kList = 1536;
+constexpr int kBins = 2048;
+constexpr int kList = 1024;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxVocab = 1 << 24;
 constexpr float kInf = __builtin_huge_valf();
@@ -42,6 +48,8 @@ constexpr float kPart = 32.0f;               // units of y to a factor of two
 constexpr float kNoWeight = 46.0f * kPart;   // y from which a weight is 0
 constexpr float kMagic = 12582912.0f;        // 1.5 * 2^23: adding it rounds to a whole number
 constexpr int kMagicBits = 0x4B400000;
+constexpr float kBinsPer = 1.375f;           // bins to a unit of y
+constexpr float kNear = 1e-4f;               // how far the bins' weights may be off, as a part of the sum
 
 struct SampleArgs {
     const float *logits;
@@ -66,16 +74,17 @@ struct Shared {
             uint32_t count[kBins];
         } hist;
         struct {
+            u64 word[kList];  // key << 32 | ~number, so that the larger one comes first
             u64 mass[kList];
-            uint32_t key[kList], idx[kList];
         } list;
     };
-    u64 lmass[kLocalBins];  // the first CTA's own histograms
+    uint32_t mine[kList];   // the CTA's own words in the list
     u64 scan[kWarps];
-    u64 pub[2];             // what the CTAs tell each other, in turn
-    u64 peer[kMaxCluster];
+    u64 certain[kWarps];    // weights before the list's words
+    u64 pub[2][2];          // what the CTAs tell each other, in turn
+    u64 peer[2][kMaxCluster];
     u64 found[4];           // what a search ends with
-    uint32_t n_list;
+    uint32_t n_list, n_mine;
     double thr;             // the least logit that min-p keeps, less the largest
     float ch, cl;
 };
@@ -102,29 +111,29 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // key_of(-inf)
 
+__device__ __forceinline__ uint32_t peer_addr(const void *local, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
+    return a;
+}
 template <typename T>
 __device__ __forceinline__ T ld_peer(const T *local, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
     if constexpr (sizeof(T) == 8) {
         u64 v;
-        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer_addr(local, rank)) : "memory");
         return (T)v;
     } else {
         uint32_t v;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_addr(local, rank)) : "memory");
         return (T)v;
     }
 }
-__device__ __forceinline__ void st_peer(uint32_t *local, uint32_t rank, uint32_t v) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+__device__ __forceinline__ void st_peer(u64 *local, uint32_t rank, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_addr(local, rank)), "l"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t add_peer(uint32_t *local, uint32_t rank, uint32_t v) {
-    uint32_t a, old;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
-    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(peer_addr(local, rank)), "r"(v) : "memory");
     return old;
 }
 
@@ -171,7 +180,7 @@ struct Row {
     __device__ __forceinline__ bool keeps(uint32_t k, uint32_t i) const { return k > kt || (k == kt && i <= it); }
     __device__ __forceinline__ float y_of(float x) const { return __fmul_rn(__fsub_rn(M, x), ch); }
     __device__ __forceinline__ int bin_of(float y) const {
-        return y < kNoWeight ? __float_as_int(__fmaf_rn(y, 1.375f, kMagic)) - kMagicBits : kBins - 1;
+        return y < kNoWeight ? __float_as_int(__fmaf_rn(y, kBinsPer, kMagic)) - kMagicBits : kBins - 1;
     }
     // A word's weight; all lanes of the warp at once.
     __device__ __forceinline__ u64 weight(float x, bool on) const {
@@ -204,7 +213,7 @@ struct Row {
     // once (words that are not there are minus infinity)
     template <typename F>
     __device__ __forceinline__ void words_of_warp(F f) const {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = (A.slice + 128 * kWarps - 1) / (128 * kWarps) * 128;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = run_length();
         const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
         for (int b = r0; b < r1; b += 128) {
             const int i = b + 4 * lane;
@@ -225,11 +234,12 @@ struct Row {
         return v;
     }
 
-    // thread 0's v of every CTA of the cluster, in S.peer
-    __device__ __forceinline__ void tell(u64 v) {
-        if (threadIdx.x == 0) S.pub[turn & 1] = v;
+    // thread 0's numbers of every CTA of the cluster, in S.peer
+    __device__ __forceinline__ void tell(u64 v, u64 w = 0) {
+        if (threadIdx.x == 0) S.pub[turn & 1][0] = v, S.pub[turn & 1][1] = w;
         cluster_sync();
-        if (threadIdx.x < A.cluster) S.peer[threadIdx.x] = ld_peer(&S.pub[turn & 1], threadIdx.x);
+        if (threadIdx.x < 2 * A.cluster)
+            S.peer[threadIdx.x & 1][threadIdx.x >> 1] = ld_peer(&S.pub[turn & 1][threadIdx.x & 1], threadIdx.x >> 1);
         turn++;
         __syncthreads();
     }
@@ -256,33 +266,27 @@ struct Row {
         return w + in - v;
     }
 
-    // The first word, by number, at which the running sum of f(logit, number) exceeds want(sum over all).  f is called
-    // by whole warps.  On every CTA: S.found = {number, its f, the sum, the words with one} of the CTA that has it in
-    // owner's shared memory; the sum's owner is returned, or -1 if the sum is 0.
+    __device__ __forceinline__ int run_length() const { return (A.slice + 128 * kWarps - 1) / (128 * kWarps) * 128; }
+    // The first word, by number, at which the running sum of f(logit, number) exceeds want(sum over all), f called by
+    // whole warps.  sums: each warp's sum of its words, in S.scan; count: words to add up beside.  Returns the CTA in
+    // whose S.found the word's number and its f are, or -1 if the sum is 0.
     template <typename F, typename W>
-    __device__ __forceinline__ int search(F f, W want, u64 &sum) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        u64 mine = 0;
-        words_of_warp([&](float x, uint32_t i) { mine += f(x, i); });
-        mine = warp_sum(mine);
-        __syncthreads();
-        if (lane == 0) S.scan[warp] = mine;
-        __syncthreads();
+    __device__ __forceinline__ int find(F f, W want, u64 &sum, u64 &count) {
         u64 all = 0;
         for (int k = 0; k < kWarps; k++) all += S.scan[k];
-        tell(all);
-        sum = 0;
-        for (int k = 0; k < A.cluster; k++) sum += S.peer[k];
+        tell(all, count);
+        sum = count = 0;
+        for (int k = 0; k < A.cluster; k++) sum += S.peer[0][k], count += S.peer[1][k];
         if (sum == 0) return -1;
         const u64 target = want(sum);
         u64 low = 0;
         int owner = 0;
-        while (owner < A.cluster - 1 && low + S.peer[owner] <= target) low += S.peer[owner++];
+        while (owner < A.cluster - 1 && low + S.peer[0][owner] <= target) low += S.peer[0][owner++];
         if (owner == rank) {
             int w = 0;
             while (w < kWarps - 1 && low + S.scan[w] <= target) low += S.scan[w++];
             // the run of warp w, a stretch of words per thread
-            const int run = (A.slice + 128 * kWarps - 1) / (128 * kWarps) * 128, r0 = min(n, w * run), r1 = min(n, r0 + run);
+            const int run = run_length(), r0 = min(n, w * run), r1 = min(n, r0 + run);
             const int per = (r1 - r0 + kThreads - 1) / kThreads, a = r0 + (int)threadIdx.x * per;
             u64 v = 0, total;
             for (int k = 0; k < per; k++) {
@@ -304,6 +308,22 @@ struct Row {
         }
         return owner;
     }
+    // the same, the sums made first; c: whether a word counts
+    template <typename F, typename G, typename W>
+    __device__ __forceinline__ int search(F f, G c, W want, u64 &sum, u64 &count) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        u64 mine = 0, total;
+        uint32_t many = 0;
+        words_of_warp([&](float x, uint32_t i) { mine += f(x, i), many += c(x, i); });
+        mine = warp_sum(mine);
+        many = __reduce_add_sync(0xffffffffu, many);
+        before(lane == 0 ? (u64)many : 0, total);
+        __syncthreads();
+        if (lane == 0) S.scan[warp] = mine;
+        __syncthreads();
+        count = total;
+        return find(f, want, sum, count);
+    }
 
     // ---------------------------------------------------------------- a cut, by the whole cluster
     struct Cut {
@@ -314,162 +334,237 @@ struct Row {
     // A histogram is filled: the bin at which the running sum reaches want(total) (by weights, or by counts).
     template <bool MASS, typename W>
     __device__ __forceinline__ Cut find_bin(W want) {
-        const int tid = threadIdx.x, C = A.cluster, per = (kBins + C - 1) / C, b0 = rank * per;
-        const int mine = max(0, min(per, kBins - b0)), each = (mine + kThreads - 1) / kThreads;  // bins of a thread: 4 at most
+        const int tid = threadIdx.x, C = A.cluster, per = kBins / C, b0 = rank * per;
+        // bins of a thread (four at most), or threads to a bin, each for some of the CTAs
+        const int each = max(1, per / kThreads), share = max(1, kThreads / per), sub = tid & (share - 1);
         cluster_sync();
-        u64 m[4] = {}, c[4] = {}, ms = 0, cs = 0;
+        u64 m[4], c[4], ms = 0, cs = 0;
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            const int b = b0 + tid * each + k;
-            if (k >= each || tid * each + k >= mine) continue;
-            for (int r = 0; r < C; r++) {
+            m[k] = c[k] = 0;
+            if (k >= each) continue;
+            const int b = b0 + tid / share * each + k;
+#pragma unroll 4
+            for (int r = sub; r < C; r += share) {
                 if (MASS) m[k] += ld_peer(&S.hist.mass[b], (uint32_t)r);
                 c[k] += ld_peer(&S.hist.count[b], (uint32_t)r);
             }
+            for (int off = 1; off < share; off <<= 1) {
+                if (MASS) m[k] += __shfl_xor_sync(0xffffffffu, m[k], off);
+                c[k] += __shfl_xor_sync(0xffffffffu, c[k], off);
+            }
+            if (sub) m[k] = c[k] = 0;
             ms += m[k], cs += c[k];
         }
         u64 mt = 0, ct;
         u64 mb = MASS ? before(ms, mt) : 0;
         u64 cb = before(cs, ct);
-        // the CTAs' sums
+        tell(MASS ? mt : ct, ct);
         Cut r;
-        u64 mlow = 0, clow = 0;
         r.total = 0;
-        if (MASS) {
-            tell(mt);
-            for (int k = 0; k < C; k++) {
-                if (k < rank) mlow += S.peer[k];
-                r.total += S.peer[k];
-            }
-            __syncthreads();
-        }
-        tell(ct);
-        u64 call = 0;
         for (int k = 0; k < C; k++) {
-            if (k < rank) clow += S.peer[k];
-            call += S.peer[k];
+            if (k < rank) mb += S.peer[0][k], cb += S.peer[1][k];
+            r.total += S.peer[0][k];
         }
-        if (!MASS) r.total = call;
         const u64 target = want(r.total);
-        mb += mlow, cb += clow;
         if (tid < 4) S.found[tid] = 0;
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < 4; k++) {
             const u64 a = MASS ? mb : cb, v = MASS ? m[k] : c[k];
             if (a < target && target <= a + v)
-                S.found[0] = (u64)(b0 + tid * each + k) + 1, S.found[1] = a, S.found[2] = cb, S.found[3] = c[k];
+                S.found[0] = (u64)(b0 + tid / share * each + k) + 1, S.found[1] = a, S.found[2] = cb, S.found[3] = c[k];
             mb += m[k], cb += c[k];
         }
         cluster_sync();
-        // (one CTA has it; the others' are zeros)
-        u64 x[4] = {0, 0, 0, 0};
+        // (one CTA has it, the others' are zeros; found is not written again before the next meeting of the CTAs)
+        int owner = 0;
         for (int k = 0; k < C; k++)
-            if (ld_peer(&S.found[0], (uint32_t)k))
-                for (int e = 0; e < 4; e++) x[e] = ld_peer(&S.found[e], (uint32_t)k);
-        r.bin = (int)x[0] - 1, r.above = x[1], r.above_n = x[2], r.in_n = x[3];
-        cluster_sync();  // (before anyone writes found or the histogram again)
+            if (ld_peer(&S.found[0], (uint32_t)k)) owner = k;
+        r.bin = (int)ld_peer(&S.found[0], (uint32_t)owner) - 1, r.above = ld_peer(&S.found[1], (uint32_t)owner);
+        r.above_n = ld_peer(&S.found[2], (uint32_t)owner), r.in_n = ld_peer(&S.found[3], (uint32_t)owner);
         return r;
     }
+    // The bins of the words as they are counted by count_by_y: lo and hi, between which top-k's border (k > 0) or top-p's
+    // must be, and the words up to hi and between.  A count is exact, a weight an estimate.
+    struct Border {
+        int lo, hi;
+        uint32_t upto, between;
+    };
+    __device__ __forceinline__ Border find_border(u64 k, float p) {
+        const int tid = threadIdx.x, C = A.cluster, per = kBins / C, b0 = rank * per;
+        const int each = max(1, per / kThreads), share = max(1, kThreads / per), sub = tid & (share - 1);
+        cluster_sync();
+        u64 c[4], cs = 0;
+        float m[4], ms = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            m[q] = 0.0f, c[q] = 0;
+            if (q >= each) continue;
+            const int b = b0 + tid / share * each + q;
+            uint32_t n = 0, f = 0;
+#pragma unroll 4
+            for (int r = sub; r < C; r += share) {
+                const u64 v = ld_peer(&S.hist.mass[b], (uint32_t)r);
+                n += (uint32_t)(v >> 32), f += (uint32_t)v;
+            }
+            for (int off = 1; off < share; off <<= 1)
+                n += __shfl_xor_sync(0xffffffffu, n, off), f += __shfl_xor_sync(0xffffffffu, f, off);
+            if (sub || !n) continue;
+            c[q] = n, cs += n;
+            // (the words' mean y: they lie (f + 1/2) / 8 of a bin above its lower border on average)
+            if (b < kBins - 1)
+                m[q] = (float)n * exp2f(-((float)b - 0.5f + (__fdiv_rn((float)f, (float)n) + 0.5f) * 0.125f) / (kBinsPer * kPart));
+            ms += m[q];
+        }
+        u64 ct;
+        u64 cb = before(cs, ct);
+        // weights as whole numbers of 2^-20 of the largest, so that every CTA adds up the same
+        u64 mt, m64[4], mo = 0;
+#pragma unroll
+        for (int q = 0; q < 4; q++) m64[q] = (u64)(m[q] * 1048576.0f), mo += m64[q];
+        u64 mb = before(mo, mt);
+        tell(mt, ct);
+        u64 mall = 0, call = 0;
+        for (int q = 0; q < C; q++) {
+            if (q < rank) mb += S.peer[0][q], cb += S.peer[1][q];
+            mall += S.peer[0][q], call += S.peer[1][q];
+        }
+        k = min(k, call);
+        const float want = p * (float)mall, off = kNear * (float)mall + 1.0f;
+        const u64 lo_t = k ? k : (u64)fmaxf(want - off, 1.0f), hi_t = k ? k : min(mall, (u64)(want + off));
+        if (tid < 4) S.found[tid] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const u64 a = k ? cb : mb, v = k ? c[q] : m64[q];
+            const int b = b0 + tid / share * each + q;
+            if (a < lo_t && lo_t <= a + v) S.found[0] = (u64)b + 1, S.found[1] = cb;
+            if (a < hi_t && hi_t <= a + v) S.found[2] = (u64)b + 1, S.found[3] = cb + c[q];
+            mb += m64[q], cb += c[q];
+        }
+        cluster_sync();
+        Border r{0, 0, 0, 0};
+        u64 under = 0, upto = 0;
+        for (int q = 0; q < C; q++) {
+            const u64 l = ld_peer(&S.found[0], (uint32_t)q), h = ld_peer(&S.found[2], (uint32_t)q);
+            if (l) r.lo = (int)l - 1, under = ld_peer(&S.found[1], (uint32_t)q);
+            if (h) r.hi = (int)h - 1, upto = ld_peer(&S.found[3], (uint32_t)q);
+        }
+        r.upto = (uint32_t)upto, r.between = (uint32_t)(upto - under);
+        return r;
+    }
+    template <bool MASS>
     __device__ __forceinline__ void clear_hist() {
         __syncthreads();
-        for (int b = threadIdx.x; b < kBins; b += kThreads) S.hist.mass[b] = 0, S.hist.count[b] = 0;
+        for (int b = threadIdx.x; b < kBins; b += kThreads) {
+            S.hist.mass[b] = 0;
+            if (MASS) S.hist.count[b] = 0;
+        }
         __syncthreads();
     }
-    // the words that are kept so far, by y
-    template <bool MASS>
-    __device__ __forceinline__ void fill_by_y() {
-        clear_hist();
+    // the kept words by y: a bin's count (high half), and eighths of a bin (low half)
+    __device__ __forceinline__ void count_by_y() {
+        clear_hist<false>();
         uint32_t rest = 0;
+        uint32_t *const half = reinterpret_cast<uint32_t *>(S.hist.mass);
         words_of_warp([&](float x, uint32_t i) {
-            const bool on = keeps(key_of(x), i);
-            const u64 w = MASS ? weight(x, on) : 0;
-            const int b = bin_of(y_of(x));
-            if (!on) return;
-            if (b == kBins - 1) {
+            if (!keeps(key_of(x), i)) return;
+            const float y = y_of(x);
+            if (!(y < kNoWeight)) {
                 rest++;  // (those of no weight, which may be most)
                 return;
             }
-            if (MASS) atomicAdd(&S.hist.mass[b], w);
+            const float z = __fmul_rn(y, kBinsPer);
+            const int b = bin_of(y);
+            atomicAdd(&half[2 * b], (uint32_t)min(7.0f, fmaxf(0.0f, 8.0f * (z - (float)b + 0.5f))));
+            atomicAdd(&half[2 * b + 1], 1u);
+        });
+        rest = __reduce_add_sync(0xffffffffu, rest);
+        if ((threadIdx.x & 31) == 0 && rest) atomicAdd(&half[2 * kBins - 1], rest);
+    }
+    // the kept words' exact weights by y
+    __device__ __forceinline__ void weigh_by_y() {
+        clear_hist<true>();
+        uint32_t rest = 0;
+        words_of_warp([&](float x, uint32_t i) {
+            const bool on = keeps(key_of(x), i);
+            const u64 w = weight(x, on);
+            const int b = bin_of(y_of(x));
+            if (!on) return;
+            if (b == kBins - 1) {
+                rest++;
+                return;
+            }
+            atomicAdd(&S.hist.mass[b], w);
             atomicAdd(&S.hist.count[b], 1u);
         });
         rest = __reduce_add_sync(0xffffffffu, rest);
         if ((threadIdx.x & 31) == 0 && rest) atomicAdd(&S.hist.count[kBins - 1], rest);
     }
-    // the kept words that sel(key, y) takes to the first CTA's list
-    template <typename F>
-    __device__ __forceinline__ void gather(F sel) {
-        if (threadIdx.x == 0 && rank == 0) S.n_list = 0;
+    // The kept words that sel(key, logit) takes to the first CTA's list; also(logit, taken, kept) for every word.  Call
+    // it behind a meeting of the CTAs.
+    template <typename F, typename G>
+    __device__ __forceinline__ void gather(F sel, G also) {
+        if (threadIdx.x == 0) S.n_list = S.n_mine = 0;
         cluster_sync();
         words_of_warp([&](float x, uint32_t i) {
             const uint32_t k = key_of(x);
-            if (!keeps(k, i) || !sel(k, x)) return;
-            const uint32_t at = add_peer(&S.n_list, 0, 1);
-            if (at < kList) st_peer(&S.list.key[at], 0, k), st_peer(&S.list.idx[at], 0, i);
+            const bool on = keeps(k, i), take = on && sel(k, x);
+            also(x, take, on);
+            if (!take) return;
+            const uint32_t at = add_peer(&S.n_list, 0, 1), own = atomicAdd(&S.n_mine, 1u);
+            if (at < kList) st_peer(&S.list.word[at], 0, (u64)k << 32 | (uint32_t)~i);
+            if (own < kList) S.mine[own] = i;
         });
         cluster_sync();
     }
 
-    // ---------------------------------------------------------------- the first CTA alone
-    // Of the n list entries with on(e): the key at which the running sum of val(e), from the largest key down, reaches
-    // target (0 < target <= the sum); above: the sum of the entries with larger keys.
-    template <typename K, typename V, typename O>
-    __device__ __forceinline__ uint32_t local_cut(int n, K key, V val, O on, u64 target, u64 &above) {
+    // ---------------------------------------------------------------- the first CTA's list
+    // The first P words (a power of two) sorted, the largest first.  A warp's 32 pairs of a step up to 32 words apart lie
+    // in 64 words of its own.
+    __device__ __forceinline__ void sort(u64 *w, int P) const {
         const int tid = threadIdx.x;
-        uint32_t hi = 0xffffffffu;
-        int s = 23;  // bins of 2^s keys from hi down
-        above = 0;
-        for (;;) {
-            __syncthreads();
-            S.lmass[tid] = 0;
-            __syncthreads();
-            for (int e = tid; e < n; e += kThreads) {
-                const uint32_t d = hi - key(e);
-                if (on(e) && key(e) <= hi && (d >> s) < kLocalBins) atomicAdd(&S.lmass[d >> s], val(e));
+        for (int k = 2; k <= P; k <<= 1)
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                if (j >= 32 || (k == 2))
+                    __syncthreads();
+                else
+                    __syncwarp();
+                if (tid < P / 2) {
+                    const int a = ((tid & ~(j - 1)) << 1) | (tid & (j - 1)), b = a | j;
+                    const u64 x = w[a], y = w[b];
+                    if ((x < y) == ((a & k) == 0)) w[a] = y, w[b] = x;
+                }
             }
-            __syncthreads();
-            const u64 v = S.lmass[tid];
-            u64 total;
-            const u64 b = above + before(v, total);
-            if (b < target && target <= b + v) S.found[0] = (u64)tid, S.found[1] = b;
-            __syncthreads();
-            hi -= (uint32_t)S.found[0] << s;
-            above = S.found[1];
-            if (s == 0) return hi;
-            s = s > 9 ? s - 9 : 0;
-        }
-    }
-    // Cuts the list's kept words behind the first `target` of the sum, by counts or weights: kt and it.
-    template <bool MASS>
-    __device__ __forceinline__ void cut_list(int n, u64 target) {
-        u64 above;
-        const uint32_t k = local_cut(
-            n, [&](int e) { return S.list.key[e]; }, [&](int e) { return MASS ? S.list.mass[e] : (u64)1; },
-            [&](int e) { return keeps(S.list.key[e], S.list.idx[e]); }, target, above);
-        // of the words with this key, the first ones that reach the target
-        u64 a2;
-        const uint32_t last = local_cut(
-            n, [&](int e) { return ~S.list.idx[e]; }, [&](int e) { return MASS ? S.list.mass[e] : (u64)1; },
-            [&](int e) { return S.list.key[e] == k && keeps(k, S.list.idx[e]); }, target - above, a2);
         __syncthreads();
-        kt = k, it = ~last;
     }
-    __device__ __forceinline__ u64 sum_list(int n, uint32_t &count) {
-        u64 v = 0, total, many;
-        u64 c = 0;
-        for (int e = threadIdx.x; e < n; e += kThreads)
-            if (keeps(S.list.key[e], S.list.idx[e])) v += S.list.mass[e], c++;
-        before(v, total);
-        before(c, many);
-        count = (uint32_t)many;
+    __device__ __forceinline__ static int pow2_of(int n) { return n <= 2 ? 2 : 1 << (32 - __clz(n - 1)); }
+    // The first n words of the list sorted; returns n.
+    __device__ __forceinline__ int sort_list() {
+        const int n = (int)min(S.n_list, (uint32_t)kList), P = pow2_of(n);
+        __syncthreads();
+        for (int e = n + threadIdx.x; e < P; e += kThreads) S.list.word[e] = 0;  // (behind every word)
+        sort(S.list.word, P);
+        return n;
+    }
+    // The weights of the sorted list's first `n` words, and the sums up to and with each, in S.list.mass.
+    __device__ __forceinline__ u64 sums_of_list(int n) {
+        const int e = 2 * threadIdx.x;
+        u64 w[2], total;
+#pragma unroll
+        for (int q = 0; q < 2; q++) w[q] = weight(e + q < n ? of_key((uint32_t)(S.list.word[e + q] >> 32)) : -kInf, e + q < n);
+        const u64 at = before(w[0] + w[1], total);
+        S.list.mass[e] = at + w[0], S.list.mass[e + 1] = at + w[0] + w[1];
+        __syncthreads();
         return total;
     }
-    __device__ __forceinline__ void weigh_list(int n) {
-        for (int e = threadIdx.x; e - (int)(threadIdx.x & 31) < n; e += kThreads) {
-            const u64 w = weight(e < n ? of_key(S.list.key[e]) : -kInf, e < n);
-            if (e < n) S.list.mass[e] = w;
-        }
-        __syncthreads();
+    // how many of the list's first n sums are below target
+    __device__ __forceinline__ int below(int n, u64 target) {
+        const int e = 2 * threadIdx.x;
+        u64 total;
+        before((u64)((e < n && S.list.mass[e] < target) + (e + 1 < n && S.list.mass[e + 1] < target)), total);
+        return (int)total;
     }
 
     // ---------------------------------------------------------------- the parts of a row
@@ -482,6 +577,18 @@ struct Row {
         const uint32_t k = key_of(fminf(x, M));
         if (k > kt) kt = k, it = 0xffffffffu;
     }
+    // kt and it from the place in the first CTA's list behind which it is cut, on every CTA; a place below 0: not there
+    __device__ __forceinline__ bool cut_at(int place) {
+        if (rank == 0 && threadIdx.x == 0) {
+            const u64 w = place >= 0 ? S.list.word[place] : 0;
+            S.found[2] = w >> 32, S.found[3] = (uint32_t)~w;
+        }
+        cluster_sync();
+        const uint32_t k = (uint32_t)ld_peer(&S.found[2], 0), i = (uint32_t)ld_peer(&S.found[3], 0);
+        if (!k) return false;
+        kt = k, it = i;
+        return true;
+    }
     // In a bin of `in_n` kept words (those that sel takes), the cut where the running sum reaches target.
     template <bool MASS, typename F>
     __device__ __forceinline__ void cut_in_bin(F sel, u64 in_n, u64 target) {
@@ -490,7 +597,7 @@ struct Row {
         auto in = [&](uint32_t k, float x) { return sel(k, x) && (known == 0 || (k >> (32 - known)) == prefix); };
         while (in_n > kList && known < 32) {
             const int bits = known == 22 ? 10 : 11, sh = 32 - known - bits;
-            clear_hist();
+            clear_hist<true>();
             words_of_warp([&](float x, uint32_t i) {
                 const uint32_t k = key_of(x);
                 const bool on = keeps(k, i) && in(k, x);
@@ -505,62 +612,82 @@ struct Row {
             prefix = prefix << bits | (uint32_t)((1 << bits) - 1 - c.bin), known += bits;
         }
         if (in_n > kList) {  // one logit, many words: the target's word by its number
-            u64 sum;
+            u64 sum, many;
             const int owner = search([&](float x, uint32_t i) -> u64 {
                 const uint32_t k = key_of(x);
                 const bool on = keeps(k, i) && in(k, x);
                 return MASS ? weight(x, on) : (u64)on;
-            }, [&](u64) { return target - 1; }, sum);
+            }, [](float, uint32_t) { return 0u; }, [&](u64) { return target - 1; }, sum, many);
             cluster_sync();
-            const uint32_t last = (uint32_t)ld_peer(&S.found[0], (uint32_t)owner);
+            kt = prefix, it = (uint32_t)ld_peer(&S.found[0], (uint32_t)owner);
             cluster_sync();
-            kt = prefix, it = last;
             return;
         }
-        gather(in);
+        gather(in, [](float, bool, bool) {});
+        int place = -1;
         if (rank == 0) {
-            const int n = (int)min(S.n_list, (uint32_t)kList);
-            if (MASS) weigh_list(n);
-            cut_list<MASS>(n, target);
-            if (threadIdx.x == 0) S.found[2] = kt, S.found[3] = it;
+            const int n = sort_list();
+            if (MASS) sums_of_list(n);
+            place = MASS ? below(n, target) : (int)target - 1;
         }
-        cluster_sync();
-        kt = (uint32_t)ld_peer(&S.found[2], 0), it = (uint32_t)ld_peer(&S.found[3], 0);
-        cluster_sync();
+        cut_at(place);
     }
     __device__ __forceinline__ void write(int row, int64_t token, u64 mass, u64 sum, uint32_t kept) {
         A.tokens[row] = (int32_t)token;
         if (A.probs) A.probs[row] = sum ? (float)((double)mass / (double)sum) : 0.0f;
         if (A.kept) A.kept[row] = (int32_t)kept;
     }
-    // The first CTA's list holds every word that is left and maybe more: the rest of the row.
-    __device__ __forceinline__ void finish_list(int row, u64 k, float p, u64 p_target, float min_p, float u) {
-        const int n = (int)min(S.n_list, (uint32_t)kList);
-        weigh_list(n);
-        uint32_t count;
-        if (k) cut_list<false>(n, k);
+    // The first CTA's list holds top-k's k words (or all there are) and maybe more: the rest of the row.
+    __device__ __forceinline__ void finish_list(int row, u64 k, float p, float min_p, float u) {
+        int n = sort_list();
+        if (k < (u64)n) n = (int)k;
+        u64 total = sums_of_list(n);
+        bool exact;
         if (p < 1.0f) {
-            if (!p_target) {
-                bool exact;
-                const u64 t = times(sum_list(n, count), p, exact);
-                p_target = max((u64)1, t + !exact);
-            }
-            cut_list<true>(n, p_target);
+            const u64 t = times(total, p, exact);
+            n = min(n, below(n, max((u64)1, t + !exact)) + 1);
         }
         cut_min_p(min_p);
-        const u64 sum = sum_list(n, count);
-        bool exact;
-        const u64 target = min(times(sum, u, exact), sum - 1);
-        u64 above;
-        const uint32_t idx = ~local_cut(
-            n, [&](int e) { return ~S.list.idx[e]; }, [&](int e) { return S.list.mass[e]; },
-            [&](int e) { return keeps(S.list.key[e], S.list.idx[e]); }, target + 1, above);
-        for (int e = threadIdx.x; e < n; e += kThreads)
-            if (S.list.idx[e] == idx) write(row, idx, S.list.mass[e], sum, count);
+        if (min_p > 0.0f) {
+            u64 many;
+            const int e = 2 * threadIdx.x;
+            auto kept = [&](int q) {
+                const u64 w = q < n ? S.list.word[q] : 0;
+                return q < n && keeps((uint32_t)(w >> 32), (uint32_t)~w);
+            };
+            before((u64)(kept(e) + kept(e + 1)), many);
+            n = (int)many;
+        }
+        const u64 sum = S.list.mass[n - 1], target = min(times(sum, u, exact), sum - 1);
+        // the words that are left in the order of their numbers: ~number << 32 | place
+        const int P = pow2_of(n), e = 2 * threadIdx.x;
+        u64 *const order = S.list.word;
+        u64 o[2] = {0, 0};
+#pragma unroll
+        for (int q = 0; q < 2; q++)
+            if (e + q < n) o[q] = S.list.word[e + q] << 32 | (uint32_t)(e + q);
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 2; q++)
+            if (e + q < P) order[e + q] = o[q];
+        sort(order, P);
+        u64 w[2] = {0, 0};
+#pragma unroll
+        for (int q = 0; q < 2; q++)
+            if (e + q < n) {
+                const int at = (int)(uint32_t)order[e + q];
+                w[q] = S.list.mass[at] - (at ? S.list.mass[at - 1] : 0);
+            }
+        u64 at = before(w[0] + w[1], total);
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            if (at <= target && target < at + w[q]) write(row, (uint32_t)~(uint32_t)(order[e + q] >> 32), w[q], sum, (uint32_t)n);
+            at += w[q];
+        }
     }
 };
 
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleArgs A) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs A) {
     extern __shared__ __align__(16) float words[];
     __shared__ Shared S;
     __shared__ float red[kWarps];
@@ -619,7 +746,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     Row R{A, S, words, from, rank, n, first, 0.0f, S.ch, S.cl, pow.x, pow.y, kKeyNegInf + 1, 0xffffffffu};
     R.tell((u64)key_of(top));
     uint32_t best = 0;
-    for (int e = 0; e < A.cluster; e++) best = max(best, (uint32_t)S.peer[e]);
+    for (int e = 0; e < A.cluster; e++) best = max(best, (uint32_t)S.peer[0][e]);
     R.M = of_key(best);
     const float M = R.M;
     if (!(M < kInf) || !(M > -kInf) || !(T == T)) {  // a NaN or plus infinity, or no word at all
@@ -627,57 +754,111 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         cluster_sync();
         return;
     }
-    u64 sum = 0;
+    u64 sum = 0, many = 0;
+    bool exact;
+    auto drawn = [&](u64 total) { return min(times(total, u, exact), total - 1); };
+    auto none = [](float, uint32_t) { return 0u; };
     if (!(T > 0.0f)) {  // the first of the largest
-        const int owner = R.search([&](float x, uint32_t) { return (u64)(x == M); }, [](u64) { return (u64)0; }, sum);
+        const int owner = R.search([&](float x, uint32_t) { return (u64)(x == M); }, none, [](u64) { return (u64)0; }, sum, many);
         if (owner == rank && tid == 0) R.write(row, (int64_t)S.found[0], 1, 1, 1);
         cluster_sync();
         return;
     }
     const bool by_k = k > 0 && k < A.vocab, by_p = p < 1.0f;
-    u64 k_left = 0;
     if (by_k) {
-        R.fill_by_y<false>();
-        const Row::Cut c = R.find_bin<false>([&](u64 total) { return min((u64)k, total); });
-        k_left = min((u64)k, c.total);
-        if (c.above_n + c.in_n <= kList) {
-            R.gather([&](uint32_t, float x) { return R.bin_of(R.y_of(x)) <= c.bin; });
-            if (rank == 0) R.finish_list(row, k_left, p, 0, min_p, u);
+        R.count_by_y();
+        const Row::Border c = R.find_border((u64)k, 0.0f);
+        auto bin = [&](float x) { return R.bin_of(R.y_of(x)); };
+        if (c.upto <= kList) {
+            R.gather([&](uint32_t, float x) { return bin(x) <= c.hi; }, [](float, bool, bool) {});
+            if (rank == 0) R.finish_list(row, (u64)k, p, min_p, u);
             return;
         }
-        R.cut_in_bin<false>([&](uint32_t, float x) { return R.bin_of(R.y_of(x)) == c.bin; }, c.in_n, k_left - c.above);
+        // (fewer words than k: all of them stay)
+        const u64 above = c.upto - c.between;
+        if (c.upto >= k) R.cut_in_bin<false>([&](uint32_t, float x) { return bin(x) == c.hi; }, c.between, (u64)k - above);
     }
+    auto keeps = [&](float x, uint32_t i) { return (uint32_t)R.keeps(key_of(x), i); };
+    auto weigh = [&](float x, uint32_t i) { return R.weight(x, R.keeps(key_of(x), i)); };
+    bool summed = false;  // S.scan holds the warps' sums of what is left, many the CTA's words
     if (by_p) {
-        R.fill_by_y<true>();
-        u64 target = 0;
-        const Row::Cut c = R.find_bin<true>([&](u64 total) {
-            bool exact;
-            const u64 t = times(total, p, exact);
-            return target = max((u64)1, t + !exact);
-        });
-        if (c.above_n + c.in_n <= kList) {
-            R.gather([&](uint32_t, float x) { return R.bin_of(R.y_of(x)) <= c.bin; });
-            if (rank == 0) R.finish_list(row, 0, p, target, min_p, u);
-            return;
+        R.count_by_y();
+        const Row::Border c = R.find_border(0, p);
+        bool done = false;
+        if (c.between <= kList) {
+            // the exact weights of the words before the list's, and of all
+            u64 before = 0, all = 0, total, ahead;
+            uint32_t ahead_n = 0;
+            R.gather([&](uint32_t, float x) {
+                const int b = R.bin_of(R.y_of(x));
+                return b >= c.lo && b <= c.hi;
+            }, [&](float x, bool take, bool on) {
+                const u64 w = R.weight(x, on);
+                const bool in = on && !take && R.bin_of(R.y_of(x)) < c.lo;
+                all += w;
+                if (in) before += w, ahead_n++;
+            });
+            before = warp_sum(before);
+            if (lane == 0) S.certain[warp] = before;
+            ahead_n = __reduce_add_sync(0xffffffffu, ahead_n);
+            u64 counted;
+            R.before(all, total);
+            R.before(lane == 0 ? (u64)ahead_n : 0, counted);
+            u64 own = 0;
+            for (int e = 0; e < kWarps; e++) own += S.certain[e];
+            R.tell(total, own);
+            total = ahead = 0;
+            for (int e = 0; e < A.cluster; e++) total += S.peer[0][e], ahead += S.peer[1][e];
+            const u64 t = times(total, p, exact), target = max((u64)1, t + !exact);
+            int place = -1;
+            if (rank == 0) {
+                const int m = R.sort_list();
+                const u64 in_list = R.sums_of_list(m);
+                if (ahead < target && target <= ahead + in_list) place = R.below(m, target - ahead);
+            }
+            done = R.cut_at(place);
+            if (done) {
+                // the warps' sums of what is left: the words before, and those of the CTA's own in the list
+                const float floor_x = min_p > 0.0f ? (float)((double)M + S.thr) : -kInf;
+                summed = !(min_p > 0.0f) || !(R.y_of(floor_x) < ((float)c.hi + 1.0f) / kBinsPer);
+                if (summed) {
+                    const int run = R.run_length(), own_n = (int)S.n_mine;
+                    __syncthreads();
+                    if (tid < kWarps) S.scan[tid] = S.certain[tid];
+                    __syncthreads();
+                    u64 left = 0;
+                    for (int e = tid; e - lane < own_n; e += kThreads) {
+                        const uint32_t i = e < own_n ? S.mine[e] : 0;
+                        const int at = (int)(i - (uint32_t)first);
+                        const float x = e < own_n ? (at < A.cached ? words[at] : __ldg(from + at)) : -kInf;
+                        const bool on = e < own_n && R.keeps(key_of(x), i);
+                        const u64 w = R.weight(x, on);
+                        if (on) atomicAdd(&S.scan[at / run], w), left++;
+                    }
+                    u64 in_list;
+                    // (before() uses S.scan)
+                    __syncthreads();
+                    const u64 mine = tid < kWarps ? S.scan[tid] : 0;
+                    R.before(left, in_list);
+                    __syncthreads();
+                    if (tid < kWarps) S.scan[tid] = mine;
+                    __syncthreads();
+                    many = counted + in_list;
+                }
+            }
         }
-        R.cut_in_bin<true>([&](uint32_t, float x) { return R.bin_of(R.y_of(x)) == c.bin; }, c.in_n, target - c.above);
+        if (!done) {
+            R.weigh_by_y();
+            u64 target = 0;
+            const Row::Cut b = R.find_bin<true>([&](u64 total) {
+                const u64 t = times(total, p, exact);
+                return target = max((u64)1, t + !exact);
+            });
+            R.cut_in_bin<true>([&](uint32_t, float x) { return R.bin_of(R.y_of(x)) == b.bin; }, b.in_n, target - b.above);
+        }
     }
     R.cut_min_p(min_p);
-    uint32_t mine = 0;
-    const int owner = R.search(
-        [&](float x, uint32_t i) { return R.weight(x, R.keeps(key_of(x), i)); },
-        [&](u64 total) {
-            bool exact;
-            return min(times(total, u, exact), total - 1);
-        },
-        sum);
-    R.words_of_warp([&](float x, uint32_t i) { mine += R.keeps(key_of(x), i); });
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    u64 many;
-    R.before(lane == 0 ? (u64)mine : 0, many);
-    R.tell(many);
-    many = 0;
-    for (int e = 0; e < A.cluster; e++) many += S.peer[e];
+    const int owner = summed ? R.find(weigh, drawn, sum, many) : R.search(weigh, keeps, drawn, sum, many);
     if (owner == rank && tid == 0) R.write(row, (int64_t)S.found[0], S.found[1], sum, (uint32_t)many);
     cluster_sync();  // nobody leaves while its numbers are read
 }
