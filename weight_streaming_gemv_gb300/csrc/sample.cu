@@ -42,6 +42,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 1024;
 constexpr int kMaxCluster = 16;
+constexpr int kPacked = 16384;  // a CTA's words up to which a bin's numbers share 32 bits
 constexpr int kMaxVocab = 1 << 24;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kPart = 32.0f;               // units of y to a factor of two
@@ -81,9 +82,9 @@ struct Shared {
     uint32_t mine[kList];   // the CTA's own words in the list
     u64 scan[kWarps];
     u64 certain[kWarps];    // weights before the list's words
-    u64 pub[2][2];          // what the CTAs tell each other, in turn
-    u64 peer[2][kMaxCluster];
-    u64 found[4];           // what a search ends with
+    u64 peer[2][2][kMaxCluster];  // what the CTAs tell each other, in turn
+    u64 found[4];           // what a search in this CTA ends with
+    u64 result[4];          // and what some CTA's ended with
     uint32_t n_list, n_mine;
     double thr;             // the least logit that min-p keeps, less the largest
     float ch, cl;
@@ -234,14 +235,19 @@ struct Row {
         return v;
     }
 
-    // thread 0's numbers of every CTA of the cluster, in S.peer
+    // The CTAs tell each other two numbers (the same in all of a CTA's threads): told(0, r) and told(1, r) are CTA r's.
+    // Nobody reads another's memory afterwards.  (A CTA is at most one such meeting ahead: two places in turn.)
     __device__ __forceinline__ void tell(u64 v, u64 w = 0) {
-        if (threadIdx.x == 0) S.pub[turn & 1][0] = v, S.pub[turn & 1][1] = w;
-        cluster_sync();
-        if (threadIdx.x < 2 * A.cluster)
-            S.peer[threadIdx.x & 1][threadIdx.x >> 1] = ld_peer(&S.pub[turn & 1][threadIdx.x & 1], threadIdx.x >> 1);
         turn++;
-        __syncthreads();
+        if (threadIdx.x < 2 * A.cluster)
+            st_peer(&S.peer[turn & 1][threadIdx.x & 1][rank], threadIdx.x >> 1, threadIdx.x & 1 ? w : v);
+        cluster_sync();
+    }
+    __device__ __forceinline__ u64 told(int what, int r) const { return S.peer[turn & 1][what][r]; }
+    // words q .. q + many - 1 of found, where this CTA has them, become result's on every CTA (behind the next meeting)
+    __device__ __forceinline__ void give(bool has, int q, int many) {
+        for (int e = threadIdx.x; e < many * A.cluster; e += kThreads)
+            if (has) st_peer(&S.result[q + e % many], e / many, S.found[q + e % many]);
     }
     // the sums of v over the threads before this one, and over all
     __device__ __forceinline__ u64 before(u64 v, u64 &total) {
@@ -276,12 +282,12 @@ struct Row {
         for (int k = 0; k < kWarps; k++) all += S.scan[k];
         tell(all, count);
         sum = count = 0;
-        for (int k = 0; k < A.cluster; k++) sum += S.peer[0][k], count += S.peer[1][k];
+        for (int k = 0; k < A.cluster; k++) sum += told(0, k), count += told(1, k);
         if (sum == 0) return -1;
         const u64 target = want(sum);
         u64 low = 0;
         int owner = 0;
-        while (owner < A.cluster - 1 && low + S.peer[0][owner] <= target) low += S.peer[0][owner++];
+        while (owner < A.cluster - 1 && low + told(0, owner) <= target) low += told(0, owner++);
         if (owner == rank) {
             int w = 0;
             while (w < kWarps - 1 && low + S.scan[w] <= target) low += S.scan[w++];
@@ -363,8 +369,8 @@ struct Row {
         Cut r;
         r.total = 0;
         for (int k = 0; k < C; k++) {
-            if (k < rank) mb += S.peer[0][k], cb += S.peer[1][k];
-            r.total += S.peer[0][k];
+            if (k < rank) mb += told(0, k), cb += told(1, k);
+            r.total += told(0, k);
         }
         const u64 target = want(r.total);
         if (tid < 4) S.found[tid] = 0;
@@ -376,13 +382,11 @@ struct Row {
                 S.found[0] = (u64)(b0 + tid / share * each + k) + 1, S.found[1] = a, S.found[2] = cb, S.found[3] = c[k];
             mb += m[k], cb += c[k];
         }
+        __syncthreads();
+        give(S.found[0] != 0, 0, 4);
+        if (tid == 0) S.n_list = S.n_mine = 0;
         cluster_sync();
-        // (one CTA has it, the others' are zeros; found is not written again before the next meeting of the CTAs)
-        int owner = 0;
-        for (int k = 0; k < C; k++)
-            if (ld_peer(&S.found[0], (uint32_t)k)) owner = k;
-        r.bin = (int)ld_peer(&S.found[0], (uint32_t)owner) - 1, r.above = ld_peer(&S.found[1], (uint32_t)owner);
-        r.above_n = ld_peer(&S.found[2], (uint32_t)owner), r.in_n = ld_peer(&S.found[3], (uint32_t)owner);
+        r.bin = (int)S.result[0] - 1, r.above = S.result[1], r.above_n = S.result[2], r.in_n = S.result[3];
         return r;
     }
     // The bins of the words as they are counted by count_by_y: lo and hi, between which top-k's border (k > 0) or top-p's
@@ -405,8 +409,13 @@ struct Row {
             uint32_t n = 0, f = 0;
 #pragma unroll 4
             for (int r = sub; r < C; r += share) {
-                const u64 v = ld_peer(&S.hist.mass[b], (uint32_t)r);
-                n += (uint32_t)(v >> 32), f += (uint32_t)v;
+                if (A.slice <= kPacked) {
+                    const uint32_t v = ld_peer(&S.hist.count[b], (uint32_t)r);
+                    n += v >> 17, f += v & 0x1ffffu;
+                } else {
+                    const u64 v = ld_peer(&S.hist.mass[b], (uint32_t)r);
+                    n += (uint32_t)(v >> 32), f += (uint32_t)v;
+                }
             }
             for (int off = 1; off < share; off <<= 1)
                 n += __shfl_xor_sync(0xffffffffu, n, off), f += __shfl_xor_sync(0xffffffffu, f, off);
@@ -427,8 +436,8 @@ struct Row {
         tell(mt, ct);
         u64 mall = 0, call = 0;
         for (int q = 0; q < C; q++) {
-            if (q < rank) mb += S.peer[0][q], cb += S.peer[1][q];
-            mall += S.peer[0][q], call += S.peer[1][q];
+            if (q < rank) mb += told(0, q), cb += told(1, q);
+            mall += told(0, q), call += told(1, q);
         }
         k = min(k, call);
         const float want = p * (float)mall, off = kNear * (float)mall + 1.0f;
@@ -443,29 +452,29 @@ struct Row {
             if (a < hi_t && hi_t <= a + v) S.found[2] = (u64)b + 1, S.found[3] = cb + c[q];
             mb += m64[q], cb += c[q];
         }
+        __syncthreads();
+        give(S.found[0] != 0, 0, 2);
+        give(S.found[2] != 0, 2, 2);
+        if (tid == 0) S.n_list = S.n_mine = 0;
         cluster_sync();
-        Border r{0, 0, 0, 0};
-        u64 under = 0, upto = 0;
-        for (int q = 0; q < C; q++) {
-            const u64 l = ld_peer(&S.found[0], (uint32_t)q), h = ld_peer(&S.found[2], (uint32_t)q);
-            if (l) r.lo = (int)l - 1, under = ld_peer(&S.found[1], (uint32_t)q);
-            if (h) r.hi = (int)h - 1, upto = ld_peer(&S.found[3], (uint32_t)q);
-        }
-        r.upto = (uint32_t)upto, r.between = (uint32_t)(upto - under);
+        Border r{(int)S.result[0] - 1, (int)S.result[2] - 1, 0, 0};
+        r.upto = (uint32_t)S.result[3], r.between = (uint32_t)(S.result[3] - S.result[1]);
         return r;
     }
-    template <bool MASS>
+    template <bool MASS, bool COUNT>
     __device__ __forceinline__ void clear_hist() {
         __syncthreads();
         for (int b = threadIdx.x; b < kBins; b += kThreads) {
-            S.hist.mass[b] = 0;
-            if (MASS) S.hist.count[b] = 0;
+            if (MASS) S.hist.mass[b] = 0;
+            if (COUNT) S.hist.count[b] = 0;
         }
         __syncthreads();
     }
-    // the kept words by y: a bin's count (high half), and eighths of a bin (low half)
+    // The kept words by y: a bin's count and eighths of a bin, in 15 and 17 bits of a word where the CTA's words cannot
+    // exceed those, else in 32 each.
+    template <bool PACKED>
     __device__ __forceinline__ void count_by_y() {
-        clear_hist<false>();
+        clear_hist<!PACKED, PACKED>();
         uint32_t rest = 0;
         uint32_t *const half = reinterpret_cast<uint32_t *>(S.hist.mass);
         words_of_warp([&](float x, uint32_t i) {
@@ -477,15 +486,31 @@ struct Row {
             }
             const float z = __fmul_rn(y, kBinsPer);
             const int b = bin_of(y);
-            atomicAdd(&half[2 * b], (uint32_t)min(7.0f, fmaxf(0.0f, 8.0f * (z - (float)b + 0.5f))));
-            atomicAdd(&half[2 * b + 1], 1u);
+            const uint32_t f = (uint32_t)min(7.0f, fmaxf(0.0f, 8.0f * (z - (float)b + 0.5f)));
+            if (PACKED) {
+                atomicAdd(&S.hist.count[b], (1u << 17) + f);
+            } else {
+                atomicAdd(&half[2 * b], f);
+                atomicAdd(&half[2 * b + 1], 1u);
+            }
         });
         rest = __reduce_add_sync(0xffffffffu, rest);
-        if ((threadIdx.x & 31) == 0 && rest) atomicAdd(&half[2 * kBins - 1], rest);
+        if ((threadIdx.x & 31) == 0 && rest) {
+            if (PACKED)
+                atomicAdd(&S.hist.count[kBins - 1], rest << 17);
+            else
+                atomicAdd(&half[2 * kBins - 1], rest);
+        }
+    }
+    __device__ __forceinline__ void count_by_y() {
+        if (A.slice <= kPacked)
+            count_by_y<true>();
+        else
+            count_by_y<false>();
     }
     // the kept words' exact weights by y
     __device__ __forceinline__ void weigh_by_y() {
-        clear_hist<true>();
+        clear_hist<true, true>();
         uint32_t rest = 0;
         words_of_warp([&](float x, uint32_t i) {
             const bool on = keeps(key_of(x), i);
@@ -502,12 +527,10 @@ struct Row {
         rest = __reduce_add_sync(0xffffffffu, rest);
         if ((threadIdx.x & 31) == 0 && rest) atomicAdd(&S.hist.count[kBins - 1], rest);
     }
-    // The kept words that sel(key, logit) takes to the first CTA's list; also(logit, taken, kept) for every word.  Call
-    // it behind a meeting of the CTAs.
+    // The kept words that sel(key, logit) takes to the first CTA's list; also(logit, taken, kept) for every word.
+    // (find_bin and find_border leave the list empty, and the histogram's place free.)
     template <typename F, typename G>
     __device__ __forceinline__ void gather(F sel, G also) {
-        if (threadIdx.x == 0) S.n_list = S.n_mine = 0;
-        cluster_sync();
         words_of_warp([&](float x, uint32_t i) {
             const uint32_t k = key_of(x);
             const bool on = keeps(k, i), take = on && sel(k, x);
@@ -579,12 +602,16 @@ struct Row {
     }
     // kt and it from the place in the first CTA's list behind which it is cut, on every CTA; a place below 0: not there
     __device__ __forceinline__ bool cut_at(int place) {
-        if (rank == 0 && threadIdx.x == 0) {
-            const u64 w = place >= 0 ? S.list.word[place] : 0;
-            S.found[2] = w >> 32, S.found[3] = (uint32_t)~w;
+        if (rank == 0) {
+            if (threadIdx.x == 0) {
+                const u64 w = place >= 0 ? S.list.word[place] : 0;
+                S.found[0] = w >> 32, S.found[1] = (uint32_t)~w;
+            }
+            __syncthreads();
+            give(true, 0, 2);
         }
         cluster_sync();
-        const uint32_t k = (uint32_t)ld_peer(&S.found[2], 0), i = (uint32_t)ld_peer(&S.found[3], 0);
+        const uint32_t k = (uint32_t)S.result[0], i = (uint32_t)S.result[1];
         if (!k) return false;
         kt = k, it = i;
         return true;
@@ -597,7 +624,7 @@ struct Row {
         auto in = [&](uint32_t k, float x) { return sel(k, x) && (known == 0 || (k >> (32 - known)) == prefix); };
         while (in_n > kList && known < 32) {
             const int bits = known == 22 ? 10 : 11, sh = 32 - known - bits;
-            clear_hist<true>();
+            clear_hist<true, true>();
             words_of_warp([&](float x, uint32_t i) {
                 const uint32_t k = key_of(x);
                 const bool on = keeps(k, i) && in(k, x);
@@ -618,9 +645,9 @@ struct Row {
                 const bool on = keeps(k, i) && in(k, x);
                 return MASS ? weight(x, on) : (u64)on;
             }, [](float, uint32_t) { return 0u; }, [&](u64) { return target - 1; }, sum, many);
+            give(owner == rank, 0, 1);
             cluster_sync();
-            kt = prefix, it = (uint32_t)ld_peer(&S.found[0], (uint32_t)owner);
-            cluster_sync();
+            kt = prefix, it = (uint32_t)S.result[0];
             return;
         }
         gather(in, [](float, bool, bool) {});
@@ -694,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster_rank(), row = blockIdx.x / A.cluster, first = rank * A.slice;
     const int n = max(0, min(A.slice, A.vocab - first));
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (this CTA is there)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const float *from = A.logits + (int64_t)row * A.row_stride + first;
@@ -744,14 +772,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < kWarps; e++) top = fmaxf(top, red[e]);
     Row R{A, S, words, from, rank, n, first, 0.0f, S.ch, S.cl, pow.x, pow.y, kKeyNegInf + 1, 0xffffffffu};
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // (all are: their memory may be written)
     R.tell((u64)key_of(top));
     uint32_t best = 0;
-    for (int e = 0; e < A.cluster; e++) best = max(best, (uint32_t)S.peer[0][e]);
+    for (int e = 0; e < A.cluster; e++) best = max(best, (uint32_t)R.told(0, e));
     R.M = of_key(best);
     const float M = R.M;
     if (!(M < kInf) || !(M > -kInf) || !(T == T)) {  // a NaN or plus infinity, or no word at all
         if (rank == 0 && tid == 0) R.write(row, -1, 0, 0, 0);
-        cluster_sync();
         return;
     }
     u64 sum = 0, many = 0;
@@ -761,7 +789,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (!(T > 0.0f)) {  // the first of the largest
         const int owner = R.search([&](float x, uint32_t) { return (u64)(x == M); }, none, [](u64) { return (u64)0; }, sum, many);
         if (owner == rank && tid == 0) R.write(row, (int64_t)S.found[0], 1, 1, 1);
-        cluster_sync();
         return;
     }
     const bool by_k = k > 0 && k < A.vocab, by_p = p < 1.0f;
@@ -808,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             for (int e = 0; e < kWarps; e++) own += S.certain[e];
             R.tell(total, own);
             total = ahead = 0;
-            for (int e = 0; e < A.cluster; e++) total += S.peer[0][e], ahead += S.peer[1][e];
+            for (int e = 0; e < A.cluster; e++) total += R.told(0, e), ahead += R.told(1, e);
             const u64 t = times(total, p, exact), target = max((u64)1, t + !exact);
             int place = -1;
             if (rank == 0) {
@@ -860,7 +887,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     R.cut_min_p(min_p);
     const int owner = summed ? R.find(weigh, drawn, sum, many) : R.search(weigh, keeps, drawn, sum, many);
     if (owner == rank && tid == 0) R.write(row, (int64_t)S.found[0], S.found[1], sum, (uint32_t)many);
-    cluster_sync();  // nobody leaves while its numbers are read
 }
 
 }  // namespace
