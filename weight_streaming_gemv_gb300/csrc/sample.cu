@@ -42,6 +42,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 1024;
 constexpr int kMaxCluster = 16;
+constexpr int kCached = 16384;  // words of a CTA in shared memory, so that an SM has room for two CTAs
 constexpr int kPacked = 16384;  // a CTA's words up to which a bin's numbers share 32 bits
 constexpr int kMaxVocab = 1 << 24;
 constexpr float kInf = __builtin_huge_valf();
@@ -166,6 +167,33 @@ __device__ __forceinline__ u64 times(u64 a, float b, bool &exact) {
     return hi << (64 - sh) | lo >> sh;
 }
 
+// Two floats in a register pair, and operations on both at once.
+__device__ __forceinline__ u64 f2(float a, float b) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 of_f2(u64 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 struct Row {
     const SampleArgs &A;
     Shared &S;
@@ -179,54 +207,91 @@ struct Row {
     int turn = 0;
 
     __device__ __forceinline__ bool keeps(uint32_t k, uint32_t i) const { return k > kt || (k == kt && i <= it); }
+    // (the lowest finite number may be a word's, and the cut among its equals)
+    __device__ __forceinline__ bool is_cut() const { return kt != kKeyNegInf + 1 || it != 0xffffffffu; }
     __device__ __forceinline__ float y_of(float x) const { return __fmul_rn(__fsub_rn(M, x), ch); }
     __device__ __forceinline__ int bin_of(float y) const {
         return y < kNoWeight ? __float_as_int(__fmaf_rn(y, kBinsPer, kMagic)) - kMagicBits : kBins - 1;
     }
-    // A word's weight; all lanes of the warp at once.
-    __device__ __forceinline__ u64 weight(float x, bool on) const {
-        const float s = __fsub_rn(M, x), bb = __fsub_rn(s, M);
-        const float e = __fsub_rn(__fsub_rn(M, __fsub_rn(s, bb)), __fadd_rn(x, bb));
-        const float yh = __fmul_rn(s, ch);
-        on = on && yh < kNoWeight;
-        const float t = __fadd_rn(yh, kMagic), f = __fsub_rn(yh, __fsub_rn(t, kMagic));  // -1/2 .. 1/2, exact
-        const int n = __float_as_int(t) - kMagicBits;
-        const float yl = __fmaf_rn(e, ch, __fmaf_rn(s, cl, __fmaf_rn(s, ch, -yh)));
-        // z = (f + yl) log(2) / 32 as a pair
-        const float zh = __fmul_rn(f, kL), zl = __fmaf_rn(yl, kL, __fmaf_rn(f, kLl, __fmaf_rn(f, kL, -zh)));
+    // The weights of two words and their y; all lanes of the warp at once.
+    __device__ __forceinline__ void weigh2(float x0, float x1, u64 (&w)[2], float (&y)[2]) const {
+        const u64 x = f2(x0, x1), m = f2(M, M), mm = f2(-M, -M), one = f2(-1.0f, -1.0f), h = f2(ch, ch);
+        const u64 s = fma2(x, one, m), bb = add2(s, mm);
+        const u64 e = fma2(add2(x, bb), one, fma2(fma2(bb, one, s), one, m));  // M - x is s + e
+        const u64 yh = mul2(s, h), ny = fma2(s, f2(-ch, -ch), yh);             // (s ch is yh - ny)
+        const u64 yl = fma2(ny, one, fma2(s, f2(cl, cl), mul2(e, h)));
+        const u64 t = add2(yh, f2(kMagic, kMagic)), f = fma2(add2(t, f2(-kMagic, -kMagic)), one, yh);  // -1/2 .. 1/2, exact
+        // z = (f + yl) log(2) / 32 is zh - nzl
+        const u64 zh = mul2(f, f2(kL, kL)), nz = fma2(f, f2(-kL, -kL), zh);
+        const u64 nzl = fma2(fma2(yl, f2(kL, kL), mul2(f, f2(kLl, kLl))), one, nz);
         // exp(-z) = 1 - zh + b
-        const float b = __fmaf_rn(__fmul_rn(zh, zh),
-                                  __fmaf_rn(zh, __fmaf_rn(zh, 1.0f / 24.0f, -1.0f / 6.0f), 0.5f), -zl);
-        const float a = __shfl_sync(0xffffffffu, th, n & 31), al = __shfl_sync(0xffffffffu, tl, n & 31);
-        const float ph = __fmul_rn(a, zh), pl = __fmaf_rn(a, zh, -ph), hi = __fsub_rn(a, ph);
-        float lo = __fsub_rn(__fsub_rn(__fsub_rn(a, hi), ph), pl);
-        lo = __fadd_rn(__fmaf_rn(a, b, lo), __fmaf_rn(-al, zh, al));
-        if (!on) return 0;
-        // (hi is a whole number of halves up to 2^24 and a little, lo below 2^10)
-        const int64_t v = (int64_t)__float2int_rn(__fmul_rn(hi, 2.0f)) * (1 << 19) + __float2int_rn(__fmul_rn(lo, 1048576.0f));
-        const int sh = (n >> 5) + A.drop;
-        return sh ? (u64)(v + ((int64_t)1 << (sh - 1))) >> sh : (u64)v;
+        const u64 b = fma2(mul2(zh, zh),
+                           fma2(zh, fma2(zh, f2(1.0f / 24.0f, 1.0f / 24.0f), f2(-1.0f / 6.0f, -1.0f / 6.0f)), f2(0.5f, 0.5f)), nzl);
+        const float2 tt = of_f2(t), yy = of_f2(yh);
+        const int n[2] = {__float_as_int(tt.x) - kMagicBits, __float_as_int(tt.y) - kMagicBits};
+        const u64 a = f2(__shfl_sync(0xffffffffu, th, n[0] & 31), __shfl_sync(0xffffffffu, th, n[1] & 31));
+        const u64 al = f2(__shfl_sync(0xffffffffu, tl, n[0] & 31), __shfl_sync(0xffffffffu, tl, n[1] & 31));
+        // the product as hi + lo, whole numbers of 1/2 up to 2^24 and a little, and below 2^10
+        const u64 nzh = mul2(zh, one), np = mul2(a, nzh), hi = add2(a, np);
+        u64 lo = fma2(fma2(a, zh, np), one, add2(fma2(hi, one, a), np));
+        lo = add2(fma2(a, b, lo), fma2(al, nzh, al));
+        const float2 hh = of_f2(mul2(hi, f2(2.0f, 2.0f))), ll = of_f2(mul2(lo, f2(1048576.0f, 1048576.0f)));
+        y[0] = yy.x, y[1] = yy.y;
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const int64_t v = (int64_t)__float2int_rn(k ? hh.y : hh.x) * (1 << 19) + __float2int_rn(k ? ll.y : ll.x);
+            const int sh = (n[k] >> 5) + A.drop;
+            const u64 r = (((u64)v << 1 >> (sh & 63)) + 1) >> 1;
+            w[k] = y[k] < kNoWeight ? r : 0;
+        }
+    }
+    // one word's; 0 where it is not on
+    __device__ __forceinline__ u64 weight(float x, bool on) const {
+        u64 w[2];
+        float y[2];
+        weigh2(x, x, w, y);
+        return on ? w[0] : 0;
     }
     // log(2) / 32
     static constexpr float kL = 0.021660849452018738f, kLl = -5.9520444e-11f;
 
-    // f(logit, word number) of the CTA's words, warp by warp in runs of `run` words from r0 on; all lanes of a warp at
-    // once (words that are not there are minus infinity)
+    // f(four logits, the first one's number) of the CTA's words, warp by warp in runs of run_length words; all lanes of a
+    // warp at once (words that are not there are minus infinity).  The next four are on their way meanwhile.
     template <typename F>
     __device__ __forceinline__ void words_of_warp(F f) const {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = run_length();
         const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
+        auto at = [&](int i) { return i < r1 ? quad(i) : make_float4(-kInf, -kInf, -kInf, -kInf); };
+        float4 next = at(r0 + 4 * lane);
         for (int b = r0; b < r1; b += 128) {
+            const float4 v = next;
             const int i = b + 4 * lane;
-            float4 v = make_float4(-kInf, -kInf, -kInf, -kInf);
-            if (i < r1) v = quad(i);
-            f(v.x, (uint32_t)(first + i)), f(v.y, (uint32_t)(first + i + 1)), f(v.z, (uint32_t)(first + i + 2)),
-                f(v.w, (uint32_t)(first + i + 3));
+            next = at(i + 128);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            f(x, (uint32_t)(first + i));
         }
+    }
+    // the same with every word's weight (0 where it is not kept) and y: f(logit, number, kept, weight, y)
+    template <typename F>
+    __device__ __forceinline__ void weights_of_warp(F f) const {
+        const bool cut = is_cut();
+        words_of_warp([&](const float (&x)[4], uint32_t i) {
+            u64 w[4];
+            float y[4];
+#pragma unroll
+            for (int q = 0; q < 4; q += 2)
+                weigh2(x[q], x[q + 1], reinterpret_cast<u64(&)[2]>(w[q]), reinterpret_cast<float(&)[2]>(y[q]));
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const bool on = cut ? keeps(key_of(x[q]), i + q) : x[q] > -kInf;
+                f(x[q], i + q, on, on ? w[q] : 0, y[q]);
+            }
+        });
     }
     // words i .. i + 3 (i a multiple of 4), minus infinity behind the last
     __device__ __forceinline__ float4 quad(int i) const {
         if (i < A.cached) return *reinterpret_cast<const float4 *>(words + i);
+        if (A.wide && i + 3 < n) return __ldg(reinterpret_cast<const float4 *>(from + i));
         float4 v;
         v.x = __ldg(from + i);
         v.y = i + 1 < n ? __ldg(from + i + 1) : -kInf;
@@ -314,21 +379,33 @@ struct Row {
         }
         return owner;
     }
-    // the same, the sums made first; c: whether a word counts
-    template <typename F, typename G, typename W>
-    __device__ __forceinline__ int search(F f, G c, W want, u64 &sum, u64 &count) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        u64 mine = 0, total;
+    // the same, the sums made first: of the weights of the kept words (and how many they are), or of f
+    template <typename W>
+    __device__ __forceinline__ int search_weights(W want, u64 &sum, u64 &count) {
+        u64 mine = 0;
         uint32_t many = 0;
-        words_of_warp([&](float x, uint32_t i) { mine += f(x, i), many += c(x, i); });
+        weights_of_warp([&](float, uint32_t, bool on, u64 w, float) { mine += w, many += on; });
+        sum_up(mine, many, count);
+        return find([&](float x, uint32_t i) { return weight(x, keeps(key_of(x), i)); }, want, sum, count);
+    }
+    template <typename F, typename W>
+    __device__ __forceinline__ int search(F f, W want, u64 &sum, u64 &count) {
+        u64 mine = 0;
+        words_of_warp([&](const float (&x)[4], uint32_t i) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) mine += f(x[q], i + q);
+        });
+        sum_up(mine, 0, count);
+        return find(f, want, sum, count);
+    }
+    // the warps' sums into S.scan, the CTA's words into count
+    __device__ __forceinline__ void sum_up(u64 mine, uint32_t many, u64 &count) {
         mine = warp_sum(mine);
         many = __reduce_add_sync(0xffffffffu, many);
-        before(lane == 0 ? (u64)many : 0, total);
+        before((threadIdx.x & 31) == 0 ? (u64)many : 0, count);
         __syncthreads();
-        if (lane == 0) S.scan[warp] = mine;
+        if ((threadIdx.x & 31) == 0) S.scan[threadIdx.x >> 5] = mine;
         __syncthreads();
-        count = total;
-        return find(f, want, sum, count);
     }
 
     // ---------------------------------------------------------------- a cut, by the whole cluster
@@ -421,9 +498,9 @@ struct Row {
                 n += __shfl_xor_sync(0xffffffffu, n, off), f += __shfl_xor_sync(0xffffffffu, f, off);
             if (sub || !n) continue;
             c[q] = n, cs += n;
-            // (the words' mean y: they lie (f + 1/2) / 8 of a bin above its lower border on average)
+            // (the words' mean y: they lie f / 8 of a bin above its lower border on average)
             if (b < kBins - 1)
-                m[q] = (float)n * exp2f(-((float)b - 0.5f + (__fdiv_rn((float)f, (float)n) + 0.5f) * 0.125f) / (kBinsPer * kPart));
+                m[q] = (float)n * exp2f(-((float)b - 0.5f + __fdiv_rn((float)f, (float)n) * 0.125f) / (kBinsPer * kPart));
             ms += m[q];
         }
         u64 ct;
@@ -477,21 +554,26 @@ struct Row {
         clear_hist<!PACKED, PACKED>();
         uint32_t rest = 0;
         uint32_t *const half = reinterpret_cast<uint32_t *>(S.hist.mass);
-        words_of_warp([&](float x, uint32_t i) {
-            if (!keeps(key_of(x), i)) return;
-            const float y = y_of(x);
-            if (!(y < kNoWeight)) {
-                rest++;  // (those of no weight, which may be most)
-                return;
-            }
-            const float z = __fmul_rn(y, kBinsPer);
-            const int b = bin_of(y);
-            const uint32_t f = (uint32_t)min(7.0f, fmaxf(0.0f, 8.0f * (z - (float)b + 0.5f)));
-            if (PACKED) {
-                atomicAdd(&S.hist.count[b], (1u << 17) + f);
-            } else {
-                atomicAdd(&half[2 * b], f);
-                atomicAdd(&half[2 * b + 1], 1u);
+        const bool cut = is_cut();
+        words_of_warp([&](const float (&x)[4], uint32_t i) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const bool on = cut ? keeps(key_of(x[q]), i + q) : x[q] > -kInf;
+                const float y = y_of(x[q]);
+                if (!on || !(y < kNoWeight)) {
+                    rest += on;  // (those of no weight, which may be most)
+                    continue;
+                }
+                // the nearest eighth of the bin that bin_of rounds to
+                const int z8 = __float_as_int(__fmaf_rn(y, 8.0f * kBinsPer, kMagic + 4.0f)) - kMagicBits;
+                const int b = bin_of(y);
+                const uint32_t f = (uint32_t)min(7, max(0, z8 - 8 * b));
+                if (PACKED) {
+                    atomicAdd(&S.hist.count[b], (1u << 17) + f);
+                } else {
+                    atomicAdd(&half[2 * b], f);
+                    atomicAdd(&half[2 * b + 1], 1u);
+                }
             }
         });
         rest = __reduce_add_sync(0xffffffffu, rest);
@@ -512,33 +594,34 @@ struct Row {
     __device__ __forceinline__ void weigh_by_y() {
         clear_hist<true, true>();
         uint32_t rest = 0;
-        words_of_warp([&](float x, uint32_t i) {
-            const bool on = keeps(key_of(x), i);
-            const u64 w = weight(x, on);
-            const int b = bin_of(y_of(x));
-            if (!on) return;
-            if (b == kBins - 1) {
-                rest++;
-                return;
+        weights_of_warp([&](float, uint32_t, bool on, u64 w, float y) {
+            const int b = bin_of(y);
+            if (on && b < kBins - 1) {
+                atomicAdd(&S.hist.mass[b], w);
+                atomicAdd(&S.hist.count[b], 1u);
+            } else {
+                rest += on;
             }
-            atomicAdd(&S.hist.mass[b], w);
-            atomicAdd(&S.hist.count[b], 1u);
         });
         rest = __reduce_add_sync(0xffffffffu, rest);
         if ((threadIdx.x & 31) == 0 && rest) atomicAdd(&S.hist.count[kBins - 1], rest);
     }
-    // The kept words that sel(key, logit) takes to the first CTA's list; also(logit, taken, kept) for every word.
-    // (find_bin and find_border leave the list empty, and the histogram's place free.)
-    template <typename F, typename G>
-    __device__ __forceinline__ void gather(F sel, G also) {
-        words_of_warp([&](float x, uint32_t i) {
-            const uint32_t k = key_of(x);
-            const bool on = keeps(k, i), take = on && sel(k, x);
-            also(x, take, on);
-            if (!take) return;
-            const uint32_t at = add_peer(&S.n_list, 0, 1), own = atomicAdd(&S.n_mine, 1u);
-            if (at < kList) st_peer(&S.list.word[at], 0, (u64)k << 32 | (uint32_t)~i);
-            if (own < kList) S.mine[own] = i;
+    // A word of this CTA's into the first CTA's list.  (find_bin and find_border leave the list empty, and the histogram's
+    // place free; a meeting of the CTAs closes it.)
+    __device__ __forceinline__ void enlist(uint32_t k, uint32_t i) {
+        const uint32_t at = add_peer(&S.n_list, 0, 1), own = atomicAdd(&S.n_mine, 1u);
+        if (at < kList) st_peer(&S.list.word[at], 0, (u64)k << 32 | (uint32_t)~i);
+        if (own < kList) S.mine[own] = i;
+    }
+    // the kept words that sel(key, logit) takes
+    template <typename F>
+    __device__ __forceinline__ void gather(F sel) {
+        words_of_warp([&](const float (&x)[4], uint32_t i) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const uint32_t k = key_of(x[q]);
+                if (keeps(k, i + q) && sel(k, x[q])) enlist(k, i + q);
+            }
         });
         cluster_sync();
     }
@@ -625,11 +708,9 @@ struct Row {
         while (in_n > kList && known < 32) {
             const int bits = known == 22 ? 10 : 11, sh = 32 - known - bits;
             clear_hist<true, true>();
-            words_of_warp([&](float x, uint32_t i) {
+            weights_of_warp([&](float x, uint32_t, bool on, u64 w, float) {
                 const uint32_t k = key_of(x);
-                const bool on = keeps(k, i) && in(k, x);
-                const u64 w = MASS ? weight(x, on) : 0;
-                if (!on) return;
+                if (!on || !in(k, x)) return;
                 const int b = (1 << bits) - 1 - (int)((k >> sh) & ((1u << bits) - 1));
                 if (MASS) atomicAdd(&S.hist.mass[b], w);
                 atomicAdd(&S.hist.count[b], 1u);
@@ -644,13 +725,13 @@ struct Row {
                 const uint32_t k = key_of(x);
                 const bool on = keeps(k, i) && in(k, x);
                 return MASS ? weight(x, on) : (u64)on;
-            }, [](float, uint32_t) { return 0u; }, [&](u64) { return target - 1; }, sum, many);
+            }, [&](u64) { return target - 1; }, sum, many);
             give(owner == rank, 0, 1);
             cluster_sync();
             kt = prefix, it = (uint32_t)S.result[0];
             return;
         }
-        gather(in, [](float, bool, bool) {});
+        gather(in);
         int place = -1;
         if (rank == 0) {
             const int n = sort_list();
@@ -751,8 +832,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         top = fmaxf(top, x);
     }
     for (int i = in_smem + tid; i < (in_smem + 3) / 4 * 4; i += kThreads) words[i] = -kInf;
+    const int vectors = A.wide && n > A.cached ? A.cached + (n - A.cached) / 4 * 4 : A.cached;
+#pragma unroll 8
+    for (int i = A.cached + 4 * tid; i < vectors; i += 4 * kThreads) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(from + i));
+        bad = bad || !(v.x < kInf && v.y < kInf && v.z < kInf && v.w < kInf);
+        top = fmaxf(fmaxf(top, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
+    }
 #pragma unroll 4
-    for (int i = A.cached + tid; i < n; i += kThreads) {
+    for (int i = vectors + tid; i < n; i += kThreads) {
         const float x = __ldg(from + i);
         bad = bad || !(x < kInf);
         top = fmaxf(top, x);
@@ -785,9 +873,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     u64 sum = 0, many = 0;
     bool exact;
     auto drawn = [&](u64 total) { return min(times(total, u, exact), total - 1); };
-    auto none = [](float, uint32_t) { return 0u; };
     if (!(T > 0.0f)) {  // the first of the largest
-        const int owner = R.search([&](float x, uint32_t) { return (u64)(x == M); }, none, [](u64) { return (u64)0; }, sum, many);
+        const int owner = R.search([&](float x, uint32_t) { return (u64)(x == M); }, [](u64) { return (u64)0; }, sum, many);
         if (owner == rank && tid == 0) R.write(row, (int64_t)S.found[0], 1, 1, 1);
         return;
     }
@@ -797,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const Row::Border c = R.find_border((u64)k, 0.0f);
         auto bin = [&](float x) { return R.bin_of(R.y_of(x)); };
         if (c.upto <= kList) {
-            R.gather([&](uint32_t, float x) { return bin(x) <= c.hi; }, [](float, bool, bool) {});
+            R.gather([&](uint32_t, float x) { return bin(x) <= c.hi; });
             if (rank == 0) R.finish_list(row, (u64)k, p, min_p, u);
             return;
         }
@@ -805,7 +892,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const u64 above = c.upto - c.between;
         if (c.upto >= k) R.cut_in_bin<false>([&](uint32_t, float x) { return bin(x) == c.hi; }, c.between, (u64)k - above);
     }
-    auto keeps = [&](float x, uint32_t i) { return (uint32_t)R.keeps(key_of(x), i); };
     auto weigh = [&](float x, uint32_t i) { return R.weight(x, R.keeps(key_of(x), i)); };
     bool summed = false;  // S.scan holds the warps' sums of what is left, many the CTA's words
     if (by_p) {
@@ -816,15 +902,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             // the exact weights of the words before the list's, and of all
             u64 before = 0, all = 0, total, ahead;
             uint32_t ahead_n = 0;
-            R.gather([&](uint32_t, float x) {
-                const int b = R.bin_of(R.y_of(x));
-                return b >= c.lo && b <= c.hi;
-            }, [&](float x, bool take, bool on) {
-                const u64 w = R.weight(x, on);
-                const bool in = on && !take && R.bin_of(R.y_of(x)) < c.lo;
+            R.weights_of_warp([&](float x, uint32_t i, bool on, u64 w, float y) {
+                const int b = R.bin_of(y);
                 all += w;
-                if (in) before += w, ahead_n++;
+                if (!on || b > c.hi) return;
+                if (b < c.lo)
+                    before += w, ahead_n++;
+                else
+                    R.enlist(key_of(x), i);
             });
+            cluster_sync();
             before = warp_sum(before);
             if (lane == 0) S.certain[warp] = before;
             ahead_n = __reduce_add_sync(0xffffffffu, ahead_n);
@@ -885,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
     }
     R.cut_min_p(min_p);
-    const int owner = summed ? R.find(weigh, drawn, sum, many) : R.search(weigh, keeps, drawn, sum, many);
+    const int owner = summed ? R.find(weigh, drawn, sum, many) : R.search_weights(drawn, sum, many);
     if (owner == rank && tid == 0) R.write(row, (int64_t)S.found[0], S.found[1], sum, (uint32_t)many);
 }
 
@@ -911,14 +998,16 @@ qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u,
                  QLIN_ERR_INVALID_ARG, "%s: pointer not 4-byte aligned", fn);
     SampleArgs A{logits, row_stride, u, temperature, top_k, top_p, min_p, vocab, tokens, probs, kept};
     const void *kern = (const void *)sample_kernel;
-    const int room = (max_smem_optin() - (int)sizeof(Shared) - 1024) / 4 / 4 * 4;  // words of a CTA in shared memory
+    // As many CTAs to a row as give two to every SM, for no fewer than 4096 words each.  (Rows past what the cluster's
+    // shared memory holds come from L2 again in every pass: 64 rows of 262144 words take 85 us by fours and 200 by
+    // sixteens, of which 11 run at a time, one after the other.)
     int c = 1;
-    while (c < kMaxCluster && (vocab + c - 1) / c > 16384) c *= 2;
+    while (c < kMaxCluster && (int64_t)n_rows * c * 2 <= 2 * sm_count() && vocab / c > 4096) c *= 2;
     size_t smem = 0;
     for (;; c /= 2) {
         A.cluster = c;
         A.slice = ((vocab + c - 1) / c + 3) / 4 * 4;
-        A.cached = A.slice < room ? A.slice : room;
+        A.cached = A.slice < kCached ? A.slice : kCached;
         smem = (size_t)A.cached * 4;
         if (c == 1) {
             blocks_per_sm(kern, smem);
