@@ -761,8 +761,8 @@ int qlin_attention_kv4_on_tensor_cores(const qlin_kv4 *kv, int n_lanes, int n_he
  * that holds a NaN or plus infinity or nothing but minus infinity, or whose
  * temperature is a NaN, gives -1, 0 and 0.
  * Weights are whole numbers of 2^-44 of the largest's (of 2^-(62 - b) where
- * vocab takes b > 18 bits), good to about 2^-38 of themselves, and their sums
- * exact: the same inputs give the same tokens.
+ * vocab - 1 takes b > 18 bits), rounded to nearest from what is good to 2^-29 of
+ * itself, and their sums exact: the same inputs give the same tokens.
  * n_rows: 1..65535; vocab: up to 2^24.  Pointers 4-byte aligned (logits 16-byte
  * aligned with row_stride % 4 == 0 are read fastest). */
 qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u, const float *temperature,

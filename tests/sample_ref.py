@@ -3,12 +3,13 @@ import numpy as np
 
 
 def draw(x, u, t=1.0, top_k=0, top_p=1.0, min_p=0.0):
-    """(token, its share, words left, how near the nearest decision was as a part of the sum)"""
+    """(token, its share, words left, how near the nearest decision was as a part of the sum, the root of the sum of the
+    weights' squares as a part of it)"""
     x = np.asarray(x, np.float64)
     if np.isnan(x).any() or (x == np.inf).any() or not (x > -np.inf).any() or np.isnan(t):
-        return -1, 0.0, 0, 1.0
+        return -1, 0.0, 0, 1.0, 1.0
     if t <= 0:
-        return int(x.argmax()), 1.0, 1, 1.0
+        return int(x.argmax()), 1.0, 1, 1.0, 1.0
     with np.errstate(invalid="ignore", over="ignore"):
         w = np.exp((x - x.max()) / np.float64(t)) if np.isfinite(t) else np.ones_like(x)
     w[x == -np.inf] = 0.0
@@ -37,4 +38,4 @@ def draw(x, u, t=1.0, top_k=0, top_p=1.0, min_p=0.0):
     n = int((run <= at).sum())
     if n >= len(ids):  # the last word with a weight
         n = int(np.nonzero(w[ids] > 0)[0][-1])
-    return int(ids[n]), float(w[ids[n]] / run[-1]), len(ids), float(near)
+    return int(ids[n]), float(w[ids[n]] / run[-1]), len(ids), float(near), float(np.sqrt((w[ids] ** 2).sum()) / run[-1])

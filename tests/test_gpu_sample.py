@@ -1,11 +1,10 @@
 """Sampling against the definition in 64 bits: tokens and numbers of words left exactly, shares to fp32.
 
-Tolerance.  A weight is good to 2^-37 of itself and rounded to a multiple of q = 2^-44 of the largest (a larger power of
-two above 2^18 words).  The roundings of V words are off by up to q / 2 each, either way: 0.29 q sqrt(V) together, and
-2 q sqrt(V) are seven deviations.  So a sum is off by at most 2^-37 + 2 q sqrt(V) of the whole (the largest weight is part
-of it): 6.5e-11 at 2^18 words.  A row in which a decision lies nearer than that to its border says nothing about the others
-and is not compared: at most one in a hundred, which is asserted.  The shares of the words that count are good to 2^-36 and
-then rounded to fp32."""
+Tolerance.  A weight is good to 2^-29 of itself (an error of its own for every logit) and rounded to a multiple of q = 2^-44
+of the largest (a larger power of two above 2^18 words).  Both are of either sign: the errors of a sum are at most some
+2^-30 sqrt(sum w^2) and 0.29 q sqrt(V) in deviations, so eight of both are 2^-27 sqrt(sum w^2) + 2.4 q sqrt(V).  A row in
+which a decision lies nearer than that to its border says nothing about the others and is not compared: at most one in a
+hundred, which is asserted.  A share is a float's weight over such a sum: good to two roundings, 2^-23 of itself."""
 import numpy as np
 import pytest
 
@@ -49,12 +48,12 @@ def _compare(x, u, t, k, p, m, got, most=0.01):
     at = lambda a, i, d: d if a is None else np.broadcast_to(a, R)[i].item()
     tok, probs, kept = got
     V = x.shape[1]
-    skipped, limit = 0, 2.0 ** -37 + 2 * V ** 0.5 * 2.0 ** (max(18, (V - 1).bit_length()) - 62)
+    skipped, rounding = 0, 2.4 * V ** 0.5 * 2.0 ** (max(18, (V - 1).bit_length()) - 62)
     for i in range(R):
         f32 = lambda v: float(np.float32(v))
         w = ref.draw(np.float32(x[i]), f32(np.broadcast_to(u, R)[i]), f32(at(t, i, 1.0)), int(at(k, i, 0)),
                      f32(at(p, i, 1.0)), f32(at(m, i, 0.0)))
-        if w[3] < limit and w[3] > 1e-15:  # (a border met exactly is no accident: equal weights)
+        if 1e-15 < w[3] < 2.0 ** -27 * w[4] + rounding:  # (a border met exactly is no accident: equal weights)
             skipped += 1
             continue
         assert (int(tok[i]), int(kept[i])) == (w[0], w[2]), (i, (tok[i], kept[i]), w)

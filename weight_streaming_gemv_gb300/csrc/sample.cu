@@ -11,10 +11,13 @@
 // The sums decide between neighbouring words, whose weights are 10^-6 of the
 // sum and less, so a float's 2^-24 would take the wrong one often.  A weight is
 // a whole number of 2^-44 (2^44 for the largest; fewer bits above 2^18 words),
-// good to about 2^-38 of itself, and sums of whole numbers do not depend on
-// their order.  2^-y: y as a pair of floats in units of 1/32, its whole part
-// split into an exponent and one of 32 numbers 2^(-j/32), which the lanes of a
-// warp hold and hand over by shuffles, and a series of four terms.
+// rounded to nearest from what is good to 2^-29 of itself, each word's error its
+// own, and sums of whole numbers do not depend on their order.  2^-y: y as a
+// pair of floats in units of 1/32, its whole part split into an exponent and one
+// of 32 numbers 2^(-j/32), a pair each, which the lanes of a warp hold and hand
+// over by shuffles, and a series of four terms for the rest: some 35
+// instructions a word.  (Two words at a time in packed fp32 took more: packed
+// operations have no immediate operands, and their constants no registers left.)
 //
 // One cluster of CTAs per row, whose shared memory holds the row: it is read
 // once.  A histogram of 2048 bins over y counts the words and adds up an eighth
@@ -50,6 +53,8 @@ constexpr float kPart = 32.0f;               // units of y to a factor of two
 constexpr float kNoWeight = 46.0f * kPart;   // y from which a weight is 0
 constexpr float kMagic = 12582912.0f;        // 1.5 * 2^23: adding it rounds to a whole number
 constexpr int kMagicBits = 0x4B400000;
+constexpr float kMagicHi = 50331648.0f, kMagicLo = 12.0f;    // 1.5 * 2^25 and 1.5 * 2^3: to fours, and to 2^-20
+constexpr int kMagicHiBits = 0x4C400000, kMagicLoBits = 0x41400000;
 constexpr float kBinsPer = 1.375f;           // bins to a unit of y
 constexpr float kNear = 1e-4f;               // how far the bins' weights may be off, as a part of the sum
 
@@ -167,33 +172,6 @@ __device__ __forceinline__ u64 times(u64 a, float b, bool &exact) {
     return hi << (64 - sh) | lo >> sh;
 }
 
-// Two floats in a register pair, and operations on both at once.
-__device__ __forceinline__ u64 f2(float a, float b) {
-    u64 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 of_f2(u64 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-    u64 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-    u64 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-    u64 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 struct Row {
     const SampleArgs &A;
     Shared &S;
@@ -213,47 +191,36 @@ struct Row {
     __device__ __forceinline__ int bin_of(float y) const {
         return y < kNoWeight ? __float_as_int(__fmaf_rn(y, kBinsPer, kMagic)) - kMagicBits : kBins - 1;
     }
-    // The weights of two words and their y; all lanes of the warp at once.
-    __device__ __forceinline__ void weigh2(float x0, float x1, u64 (&w)[2], float (&y)[2]) const {
-        const u64 x = f2(x0, x1), m = f2(M, M), mm = f2(-M, -M), one = f2(-1.0f, -1.0f), h = f2(ch, ch);
-        const u64 s = fma2(x, one, m), bb = add2(s, mm);
-        const u64 e = fma2(add2(x, bb), one, fma2(fma2(bb, one, s), one, m));  // M - x is s + e
-        const u64 yh = mul2(s, h), ny = fma2(s, f2(-ch, -ch), yh);             // (s ch is yh - ny)
-        const u64 yl = fma2(ny, one, fma2(s, f2(cl, cl), mul2(e, h)));
-        const u64 t = add2(yh, f2(kMagic, kMagic)), f = fma2(add2(t, f2(-kMagic, -kMagic)), one, yh);  // -1/2 .. 1/2, exact
-        // z = (f + yl) log(2) / 32 is zh - nzl
-        const u64 zh = mul2(f, f2(kL, kL)), nz = fma2(f, f2(-kL, -kL), zh);
-        const u64 nzl = fma2(fma2(yl, f2(kL, kL), mul2(f, f2(kLl, kLl))), one, nz);
-        // exp(-z) = 1 - zh + b
-        const u64 b = fma2(mul2(zh, zh),
-                           fma2(zh, fma2(zh, f2(1.0f / 24.0f, 1.0f / 24.0f), f2(-1.0f / 6.0f, -1.0f / 6.0f)), f2(0.5f, 0.5f)), nzl);
-        const float2 tt = of_f2(t), yy = of_f2(yh);
-        const int n[2] = {__float_as_int(tt.x) - kMagicBits, __float_as_int(tt.y) - kMagicBits};
-        const u64 a = f2(__shfl_sync(0xffffffffu, th, n[0] & 31), __shfl_sync(0xffffffffu, th, n[1] & 31));
-        const u64 al = f2(__shfl_sync(0xffffffffu, tl, n[0] & 31), __shfl_sync(0xffffffffu, tl, n[1] & 31));
-        // the product as hi + lo, whole numbers of 1/2 up to 2^24 and a little, and below 2^10
-        const u64 nzh = mul2(zh, one), np = mul2(a, nzh), hi = add2(a, np);
-        u64 lo = fma2(fma2(a, zh, np), one, add2(fma2(hi, one, a), np));
-        lo = add2(fma2(a, b, lo), fma2(al, nzh, al));
-        const float2 hh = of_f2(mul2(hi, f2(2.0f, 2.0f))), ll = of_f2(mul2(lo, f2(1048576.0f, 1048576.0f)));
-        y[0] = yy.x, y[1] = yy.y;
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            const int64_t v = (int64_t)__float2int_rn(k ? hh.y : hh.x) * (1 << 19) + __float2int_rn(k ? ll.y : ll.x);
-            const int sh = (n[k] >> 5) + A.drop;
-            const u64 r = (((u64)v << 1 >> (sh & 63)) + 1) >> 1;
-            w[k] = y[k] < kNoWeight ? r : 0;
-        }
+    // A word's weight and y, all lanes of the warp at once: w = (q - kMagicHiBits) 2^22 + r - kMagicLoBits.  Where y is
+    // kNoWeight or more, or not a number, q and r say nothing.  value: w 2^-20 as a float.
+    __device__ __forceinline__ void weigh(float x, int &q, int &r, float &y, float *value = nullptr) const {
+        const float s = __fsub_rn(M, x), bb = __fsub_rn(s, M);
+        const float e = __fsub_rn(__fsub_rn(M, __fsub_rn(s, bb)), __fadd_rn(x, bb));  // M - x is s + e
+        y = __fmul_rn(s, ch);
+        const float yl = __fmaf_rn(e, ch, __fmaf_rn(s, cl, __fmaf_rn(s, ch, -y)));
+        const float t = __fadd_rn(y, kMagic);
+        const float f = __fadd_rn(__fsub_rn(y, __fsub_rn(t, kMagic)), yl);  // what is left of y, up to 1/2 and a little
+        const int n = __float_as_int(t);  // (kMagic's bits end in 22 zeros: n's last five are j, those before the exponent)
+        const float a = __shfl_sync(0xffffffffu, th, n), al = __shfl_sync(0xffffffffu, tl, n);
+        // a + al times 2^(-f/32) = 1 - g
+        constexpr float k1 = 0.021660849392498290f, k2 = -k1 * k1 / 2.0f, k3 = k1 * k1 * k1 / 6.0f, k4 = -k1 * k1 * k1 * k1 / 24.0f;
+        const float g = __fmul_rn(f, __fmaf_rn(f, __fmaf_rn(f, __fmaf_rn(f, k4, k3), k2), k1));
+        const float lo = __fmaf_rn(-a, g, al);
+        // times the power of two, in fours and the rest
+        const float scale = __int_as_float(0x3f800000 - (A.drop << 23) - ((n & ~31) << 18));
+        const float u = __fmul_rn(a, scale), v = __fmaf_rn(lo, scale, u), top = __fadd_rn(v, kMagicHi);
+        if (value) *value = v;
+        q = __float_as_int(top);
+        r = __float_as_int(__fadd_rn(__fmaf_rn(lo, scale, __fsub_rn(u, __fsub_rn(top, kMagicHi))), kMagicLo));
     }
-    // one word's; 0 where it is not on
+    static __device__ __forceinline__ u64 whole(int q, int r) { return (u64)((int64_t)(q - kMagicHiBits) * (1 << 22) + (r - kMagicLoBits)); }
+    // one word's weight; 0 where it is not on
     __device__ __forceinline__ u64 weight(float x, bool on) const {
-        u64 w[2];
-        float y[2];
-        weigh2(x, x, w, y);
-        return on ? w[0] : 0;
+        int q, r;
+        float y;
+        weigh(x, q, r, y);
+        return on && y < kNoWeight ? whole(q, r) : 0;
     }
-    // log(2) / 32
-    static constexpr float kL = 0.021660849452018738f, kLl = -5.9520444e-11f;
 
     // f(four logits, the first one's number) of the CTA's words, warp by warp in runs of run_length words; all lanes of a
     // warp at once (words that are not there are minus infinity).  The next four are on their way meanwhile.
@@ -271,22 +238,37 @@ struct Row {
             f(x, (uint32_t)(first + i));
         }
     }
-    // the same with every word's weight (0 where it is not kept) and y: f(logit, number, kept, weight, y)
-    template <typename F>
-    __device__ __forceinline__ void weights_of_warp(F f) const {
+    // A sum of weights in two parts, of up to 512 words.
+    struct Sum {
+        uint32_t q = 0, r = 0, n = 0;
+        u64 all = 0;
+        __device__ __forceinline__ void add(bool on, int qq, int rr) {
+            if (on) q += (uint32_t)qq, r += (uint32_t)rr, n++;
+        }
+        // (behind 512 words, and before all is read)
+        __device__ __forceinline__ void flush() {
+            all += (u64)(q - n * (uint32_t)kMagicHiBits) * (1 << 22) + (u64)(int64_t)(int32_t)(r - n * (uint32_t)kMagicLoBits);
+            q = r = n = 0;
+        }
+    };
+    // the same with every word's weight and y: f(logit, number, kept, weighs, q, r, y); flush() every 512 words
+    template <typename F, typename G>
+    __device__ __forceinline__ void weights_of_warp(F f, G flush) const {
         const bool cut = is_cut();
+        int left = 128;
         words_of_warp([&](const float (&x)[4], uint32_t i) {
-            u64 w[4];
+            int q[4], r[4];
             float y[4];
 #pragma unroll
-            for (int q = 0; q < 4; q += 2)
-                weigh2(x[q], x[q + 1], reinterpret_cast<u64(&)[2]>(w[q]), reinterpret_cast<float(&)[2]>(y[q]));
+            for (int k = 0; k < 4; k++) weigh(x[k], q[k], r[k], y[k]);
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const bool on = cut ? keeps(key_of(x[q]), i + q) : x[q] > -kInf;
-                f(x[q], i + q, on, on ? w[q] : 0, y[q]);
+            for (int k = 0; k < 4; k++) {
+                const bool on = cut ? keeps(key_of(x[k]), i + k) : x[k] > -kInf;
+                f(x[k], i + k, on, on && y[k] < kNoWeight, q[k], r[k], y[k]);
             }
+            if (--left == 0) flush(), left = 128;
         });
+        flush();
     }
     // words i .. i + 3 (i a multiple of 4), minus infinity behind the last
     __device__ __forceinline__ float4 quad(int i) const {
@@ -340,7 +322,7 @@ struct Row {
     __device__ __forceinline__ int run_length() const { return (A.slice + 128 * kWarps - 1) / (128 * kWarps) * 128; }
     // The first word, by number, at which the running sum of f(logit, number) exceeds want(sum over all), f called by
     // whole warps.  sums: each warp's sum of its words, in S.scan; count: words to add up beside.  Returns the CTA in
-    // whose S.found the word's number and its f are, or -1 if the sum is 0.
+    // whose S.found the word's number is, or -1 if the sum is 0.
     template <typename F, typename W>
     __device__ __forceinline__ int find(F f, W want, u64 &sum, u64 &count) {
         u64 all = 0;
@@ -372,7 +354,7 @@ struct Row {
                 const int i = a + k;
                 const float x = i < r1 ? (i < A.cached ? words[i] : __ldg(from + i)) : -kInf;
                 const u64 g = f(x, (uint32_t)(first + i));
-                if (here && at <= target && target < at + g) S.found[0] = (u64)(first + i), S.found[1] = g;
+                if (here && at <= target && target < at + g) S.found[0] = (u64)(first + i);
                 at += g;
             }
             __syncthreads();
@@ -382,10 +364,11 @@ struct Row {
     // the same, the sums made first: of the weights of the kept words (and how many they are), or of f
     template <typename W>
     __device__ __forceinline__ int search_weights(W want, u64 &sum, u64 &count) {
-        u64 mine = 0;
+        Sum mine;
         uint32_t many = 0;
-        weights_of_warp([&](float, uint32_t, bool on, u64 w, float) { mine += w, many += on; });
-        sum_up(mine, many, count);
+        weights_of_warp([&](float, uint32_t, bool on, bool weighs, int q, int r, float) { mine.add(weighs, q, r), many += on; },
+                        [&]() { mine.flush(); });
+        sum_up(mine.all, many, count);
         return find([&](float x, uint32_t i) { return weight(x, keeps(key_of(x), i)); }, want, sum, count);
     }
     template <typename F, typename W>
@@ -594,15 +577,15 @@ struct Row {
     __device__ __forceinline__ void weigh_by_y() {
         clear_hist<true, true>();
         uint32_t rest = 0;
-        weights_of_warp([&](float, uint32_t, bool on, u64 w, float y) {
-            const int b = bin_of(y);
-            if (on && b < kBins - 1) {
-                atomicAdd(&S.hist.mass[b], w);
+        weights_of_warp([&](float, uint32_t, bool on, bool weighs, int q, int r, float y) {
+            if (weighs) {
+                const int b = bin_of(y);
+                atomicAdd(&S.hist.mass[b], whole(q, r));
                 atomicAdd(&S.hist.count[b], 1u);
             } else {
                 rest += on;
             }
-        });
+        }, []() {});
         rest = __reduce_add_sync(0xffffffffu, rest);
         if ((threadIdx.x & 31) == 0 && rest) atomicAdd(&S.hist.count[kBins - 1], rest);
     }
@@ -627,10 +610,25 @@ struct Row {
     }
 
     // ---------------------------------------------------------------- the first CTA's list
-    // The first P words (a power of two) sorted, the largest first.  A warp's 32 pairs of a step up to 32 words apart lie
-    // in 64 words of its own.
-    __device__ __forceinline__ void sort(u64 *w, int P) const {
+    // n words, all different, sorted, the largest first.  Up to 128 every word's place is counted, by four threads; more go through a network, in which a
+    // warp's 32 pairs of a step up to 32 words apart lie in 64 words of its own.  (70 words: 0.3 us against 1.4.)
+    __device__ __forceinline__ void sort(u64 *w, int n) const {
         const int tid = threadIdx.x;
+        __syncthreads();
+        if (n <= 128) {
+            const int e = tid >> 2;
+            const u64 mine = e < n ? w[e] : 0;
+            int place = 0;
+            for (int i = tid & 3; i < n; i += 4) place += w[i] > mine;
+            place += __shfl_xor_sync(0xffffffffu, place, 1);
+            place += __shfl_xor_sync(0xffffffffu, place, 2);
+            __syncthreads();
+            if (e < n && (tid & 3) == 0) w[place] = mine;
+            __syncthreads();
+            return;
+        }
+        const int P = 1 << (32 - __clz(n - 1));
+        for (int e = n + tid; e < P; e += kThreads) w[e] = 0;  // (behind every word)
         for (int k = 2; k <= P; k <<= 1)
             for (int j = k >> 1; j > 0; j >>= 1) {
                 if (j >= 32 || (k == 2))
@@ -645,13 +643,10 @@ struct Row {
             }
         __syncthreads();
     }
-    __device__ __forceinline__ static int pow2_of(int n) { return n <= 2 ? 2 : 1 << (32 - __clz(n - 1)); }
     // The first n words of the list sorted; returns n.
     __device__ __forceinline__ int sort_list() {
-        const int n = (int)min(S.n_list, (uint32_t)kList), P = pow2_of(n);
-        __syncthreads();
-        for (int e = n + threadIdx.x; e < P; e += kThreads) S.list.word[e] = 0;  // (behind every word)
-        sort(S.list.word, P);
+        const int n = (int)min(S.n_list, (uint32_t)kList);
+        sort(S.list.word, n);
         return n;
     }
     // The weights of the sorted list's first `n` words, and the sums up to and with each, in S.list.mass.
@@ -708,13 +703,13 @@ struct Row {
         while (in_n > kList && known < 32) {
             const int bits = known == 22 ? 10 : 11, sh = 32 - known - bits;
             clear_hist<true, true>();
-            weights_of_warp([&](float x, uint32_t, bool on, u64 w, float) {
+            weights_of_warp([&](float x, uint32_t, bool on, bool weighs, int q, int r, float) {
                 const uint32_t k = key_of(x);
                 if (!on || !in(k, x)) return;
                 const int b = (1 << bits) - 1 - (int)((k >> sh) & ((1u << bits) - 1));
-                if (MASS) atomicAdd(&S.hist.mass[b], w);
+                if (MASS && weighs) atomicAdd(&S.hist.mass[b], whole(q, r));
                 atomicAdd(&S.hist.count[b], 1u);
-            });
+            }, []() {});
             const Cut c = find_bin<MASS>([&](u64) { return target; });
             target -= c.above, in_n = c.in_n;
             prefix = prefix << bits | (uint32_t)((1 << bits) - 1 - c.bin), known += bits;
@@ -740,10 +735,20 @@ struct Row {
         }
         cut_at(place);
     }
-    __device__ __forceinline__ void write(int row, int64_t token, u64 mass, u64 sum, uint32_t kept) {
+    __device__ __forceinline__ void write(int row, int64_t token, float prob, u64 kept) const {
+        if (threadIdx.x) return;
         A.tokens[row] = (int32_t)token;
-        if (A.probs) A.probs[row] = sum ? (float)((double)mass / (double)sum) : 0.0f;
+        if (A.probs) A.probs[row] = prob;
         if (A.kept) A.kept[row] = (int32_t)kept;
+    }
+    // the token, the logit x of it, the sum of the weights and the words left; whole warps
+    __device__ __forceinline__ void write(int row, int64_t token, float x, u64 sum, u64 kept) const {
+        int q, r;
+        float y, v;
+        weigh(x, q, r, y, &v);  // (a small weight has few bits as a whole number)
+        v = __fmul_rn(v, 1048576.0f);
+        const float hi = __ull2float_rn(sum), lo = (float)((int64_t)sum - (int64_t)hi), p = __fdiv_rn(v, hi);
+        write(row, token, __fadd_rn(p, __fdiv_rn(__fmaf_rn(-p, lo, __fmaf_rn(-p, hi, v)), hi)), kept);
     }
     // The first CTA's list holds top-k's k words (or all there are) and maybe more: the rest of the row.
     __device__ __forceinline__ void finish_list(int row, u64 k, float p, float min_p, float u) {
@@ -768,7 +773,7 @@ struct Row {
         }
         const u64 sum = S.list.mass[n - 1], target = min(times(sum, u, exact), sum - 1);
         // the words that are left in the order of their numbers: ~number << 32 | place
-        const int P = pow2_of(n), e = 2 * threadIdx.x;
+        const int e = 2 * threadIdx.x;
         u64 *const order = S.list.word;
         u64 o[2] = {0, 0};
 #pragma unroll
@@ -777,8 +782,8 @@ struct Row {
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < 2; q++)
-            if (e + q < P) order[e + q] = o[q];
-        sort(order, P);
+            if (e + q < n) order[e + q] = o[q];
+        sort(order, n);
         u64 w[2] = {0, 0};
 #pragma unroll
         for (int q = 0; q < 2; q++)
@@ -789,9 +794,11 @@ struct Row {
         u64 at = before(w[0] + w[1], total);
 #pragma unroll
         for (int q = 0; q < 2; q++) {
-            if (at <= target && target < at + w[q]) write(row, (uint32_t)~(uint32_t)(order[e + q] >> 32), w[q], sum, (uint32_t)n);
+            if (at <= target && target < at + w[q]) S.found[0] = (uint32_t)~(uint32_t)(order[e + q] >> 32);
             at += w[q];
         }
+        __syncthreads();
+        write(row, (int64_t)S.found[0], __ldg(from + S.found[0]), sum, (u64)n);  // (the first CTA's words are the row's)
     }
 };
 
@@ -867,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     R.M = of_key(best);
     const float M = R.M;
     if (!(M < kInf) || !(M > -kInf) || !(T == T)) {  // a NaN or plus infinity, or no word at all
-        if (rank == 0 && tid == 0) R.write(row, -1, 0, 0, 0);
+        if (rank == 0) R.write(row, -1, 0.0f, 0);
         return;
     }
     u64 sum = 0, many = 0;
@@ -875,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     auto drawn = [&](u64 total) { return min(times(total, u, exact), total - 1); };
     if (!(T > 0.0f)) {  // the first of the largest
         const int owner = R.search([&](float x, uint32_t) { return (u64)(x == M); }, [](u64) { return (u64)0; }, sum, many);
-        if (owner == rank && tid == 0) R.write(row, (int64_t)S.found[0], 1, 1, 1);
+        if (owner == rank) R.write(row, (int64_t)S.found[0], 1.0f, 1);
         return;
     }
     const bool by_k = k > 0 && k < A.vocab, by_p = p < 1.0f;
@@ -892,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const u64 above = c.upto - c.between;
         if (c.upto >= k) R.cut_in_bin<false>([&](uint32_t, float x) { return bin(x) == c.hi; }, c.between, (u64)k - above);
     }
-    auto weigh = [&](float x, uint32_t i) { return R.weight(x, R.keeps(key_of(x), i)); };
+    auto kept_weight = [&](float x, uint32_t i) { return R.weight(x, R.keeps(key_of(x), i)); };
     bool summed = false;  // S.scan holds the warps' sums of what is left, many the CTA's words
     if (by_p) {
         R.count_by_y();
@@ -900,23 +907,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         bool done = false;
         if (c.between <= kList) {
             // the exact weights of the words before the list's, and of all
-            u64 before = 0, all = 0, total, ahead;
+            Row::Sum before, all;
+            u64 total, ahead;
             uint32_t ahead_n = 0;
-            R.weights_of_warp([&](float x, uint32_t i, bool on, u64 w, float y) {
+            R.weights_of_warp([&](float x, uint32_t i, bool, bool weighs, int q, int r, float y) {
                 const int b = R.bin_of(y);
-                all += w;
-                if (!on || b > c.hi) return;
-                if (b < c.lo)
-                    before += w, ahead_n++;
-                else
-                    R.enlist(key_of(x), i);
-            });
+                all.add(weighs, q, r);
+                before.add(weighs && b < c.lo, q, r);
+                ahead_n += weighs && b < c.lo;
+                if (weighs && b >= c.lo && b <= c.hi) R.enlist(key_of(x), i);
+            }, [&]() { all.flush(), before.flush(); });
             cluster_sync();
-            before = warp_sum(before);
-            if (lane == 0) S.certain[warp] = before;
+            const u64 ahead_w = warp_sum(before.all);
+            if (lane == 0) S.certain[warp] = ahead_w;
             ahead_n = __reduce_add_sync(0xffffffffu, ahead_n);
             u64 counted;
-            R.before(all, total);
+            R.before(all.all, total);
             R.before(lane == 0 ? (u64)ahead_n : 0, counted);
             u64 own = 0;
             for (int e = 0; e < kWarps; e++) own += S.certain[e];
@@ -972,8 +978,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
     }
     R.cut_min_p(min_p);
-    const int owner = summed ? R.find(weigh, drawn, sum, many) : R.search_weights(drawn, sum, many);
-    if (owner == rank && tid == 0) R.write(row, (int64_t)S.found[0], S.found[1], sum, (uint32_t)many);
+    const int owner = summed ? R.find(kept_weight, drawn, sum, many) : R.search_weights(drawn, sum, many);
+    if (owner == rank) R.write(row, (int64_t)S.found[0], __ldg(from + (S.found[0] - (u64)first)), sum, many);
 }
 
 }  // namespace
@@ -1016,7 +1022,7 @@ qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u,
         if (max_clusters(kern, smem, kThreads, c) >= 1) break;
     }
     A.drop = 0;
-    while (A.drop < 20 && ((int64_t)vocab >> A.drop) > 1 << 18) A.drop++;
+    while (((int64_t)(vocab - 1) >> A.drop) >= 1 << 18) A.drop++;
     A.wide = aligned16(logits) && row_stride % 4 == 0;
     void *args[] = {(void *)&A};
     return launch_pdl(kern, dim3((unsigned)(n_rows * c)), dim3(kThreads), smem, (cudaStream_t)stream, args, "sample_kernel", c);
