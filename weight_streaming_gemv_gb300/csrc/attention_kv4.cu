@@ -7,12 +7,6 @@
 //   o = sum_j w_j v_j,  w = softmax_j(q . k_j / sqrt(head_dim)),
 // zeros where no key is seen.
 //
-// A CTA takes one lane, up to GH query heads of one KV head and a run of the
-// keys that the lane sees, counted without gaps (first tokens, then the
-// window).  It goes through them 64 at a time with a running maximum and sum:
-// their codes and scales into shared memory, scores and weighted values in
-// fp32 on the CUDA cores.  The runs of one lane leave partial sums that a
-// second kernel joins by the weights 2^(maximum - largest maximum).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -25,10 +19,9 @@ namespace qlin {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKeys = 64;          // keys of a step
-constexpr int kParts = kThreads / kKeys;
 constexpr int kMaxSplits = 1024;
 constexpr int kMergeDims = 64;     // dims of a head per merging CTA
+constexpr int kCluster = 16;       // CTAs of a cluster at most
 
 struct Kv4Args {
     const float *q;
@@ -69,20 +62,38 @@ __device__ __forceinline__ void decode8f(uint32_t w, __half2 s, __half2 m24, flo
     }
 }
 
-// grid (splits, KV heads x blocks of GH query heads, lanes); span: keys of a CTA
-template <int HD, int GH>
+// Shared memory of a CTA of the kernel for little work: the keys' and values'
+// rows, later the sums of the groups of keys; then the scales.
+template <int HD, bool CL>
+struct FewCfg {
+    static constexpr int kKeys = CL ? 128 : 64;            // of a CTA at most
+    static constexpr int kParts = kThreads / kKeys;        // threads to a key
+    static constexpr int kRow = HD / 2 + 16;               // bytes between rows of codes
+    static constexpr int kPer = HD / 32;                   // 16-byte groups of a row, and scales
+    static constexpr int kWords = HD / 8, kGroups = kThreads / kWords;
+    static constexpr int kRows = kKeys * kRow;
+    static constexpr size_t bytes(int gh) {
+        const size_t rows = 2 * (kRows + kKeys * kPer), sums = (size_t)kGroups * gh * HD * 4;
+        return rows > sums ? rows : sums;
+    }
+};
+
+// grid (splits, KV heads x blocks of GH query heads, lanes); span: keys of a
+// CTA.  CL: the CTAs of a (lane, head block) are one cluster and merge among
+// themselves.
+template <int HD, int GH, bool CL>
 __global__ void __launch_bounds__(kThreads) kv4_few_kernel(const __grid_constant__ Kv4Args A, float2 *ml, float *part,
                                                            int splits, int span) {
-    constexpr int kRow = HD / 2 + 16, kPer = HD / 32;  // bytes between rows of codes; 16-byte groups, and scales, of a row
-    constexpr int kWords = HD / 8, kGroups = kThreads / kWords;
-    constexpr int kSums = kGroups * HD * 4, kBuf = 2 * kKeys * kRow > kSums ? 2 * kKeys * kRow : kSums;
-    __shared__ __align__(16) uint8_t buf[kBuf];  // the keys' and the values' rows, then sums
-    uint8_t *const rows[2] = {buf, buf + kKeys * kRow};
-    __shared__ __align__(16) uint8_t scales[2][kKeys * kPer];
+    using C = FewCfg<HD, CL>;
+    constexpr int KM = C::kKeys, PER = C::kPer;
+    extern __shared__ __align__(16) uint8_t few_smem[];
     __shared__ __align__(16) float qs[GH][HD];
-    __shared__ __align__(16) float ws[kKeys][GH];
-    __shared__ float sm[GH], sl[GH], sa[GH];  // running maximum and sum, the last step's factor
-    __shared__ int ok[kKeys];
+    __shared__ __align__(16) float ws[KM][GH];
+    __shared__ float inv[GH];
+    __shared__ float4 stat[GH];  // a cluster's: the largest score and the sum of the weights here
+    __shared__ int ok[KM];
+    uint8_t *const rows[2] = {few_smem, few_smem + C::kRows};
+    uint8_t *const scales[2] = {few_smem + 2 * C::kRows, few_smem + 2 * C::kRows + KM * PER};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int s = blockIdx.x, blocks = (A.group + GH - 1) / GH, kvh = blockIdx.y / blocks, h0 = (blockIdx.y % blocks) * GH;
     const int lane_i = blockIdx.z, heads = min(GH, A.group - h0), head0 = kvh * A.group + h0;
@@ -91,129 +102,167 @@ __global__ void __launch_bounds__(kThreads) kv4_few_kernel(const __grid_constant
     const LaneKeys L(A, lane_i);
     if (L.bad && s == 0 && blockIdx.y == 0 && tid == 0) raise_status(A.status, kStatusKv4Lane);
     const int n = min(span, L.count - s * span);
-    if (n <= 0) {
+    if (CL ? L.count <= 0 : n <= 0) {
         if (s == 0)
             for (int e = tid; e < heads * HD; e += kThreads) A.out[((int64_t)lane_i * A.n_heads + head0) * HD + e] = 0.0f;
         return;
     }
+    // a thread to 16 bytes of a key's codes and of its value's, and their scales
+    for (int e = tid; e < n * PER; e += kThreads) {
+        const int r = e / PER, c = e % PER;
+        const int64_t at = kv4_row(A.kv, A.n_kv, L.key(s * span + r), L.seq);
+        if (c == 0) ok[r] = at >= 0;
+        if (at < 0) continue;
+        const int64_t row = at + (int64_t)kvh * A.kv.page_rows;
+        cp_async16(rows[0] + r * C::kRow + c * 16, static_cast<const uint8_t *>(A.kv.k) + row * (HD / 2) + c * 16, 16);
+        cp_async16(rows[1] + r * C::kRow + c * 16, static_cast<const uint8_t *>(A.kv.v) + row * (HD / 2) + c * 16, 16);
+        scales[0][r * PER + c] = static_cast<const uint8_t *>(A.kv.k_scale)[row * PER + c];
+        scales[1][r * PER + c] = static_cast<const uint8_t *>(A.kv.v_scale)[row * PER + c];
+    }
+    cp_async_commit();
+    if (CL && tid < GH) stat[tid] = make_float4(-kInf, 0.0f, 0.0f, 0.0f);  // (no key)
     for (int e = tid; e < GH * HD; e += kThreads)
         qs[e / HD][e % HD] = e / HD < heads ? A.q[((int64_t)lane_i * A.n_heads + head0) * HD + e] * A.c : 0.0f;
-    if (tid < GH) sm[tid] = -kInf, sl[tid] = 0.0f;
+    cp_async_wait_pending<0>();
+    __syncthreads();
+    // scores: kParts threads share a key, 32 dims of it in turn
+    const int key = tid / C::kParts, pt = tid % C::kParts;
+    float sc[GH];
+#pragma unroll
+    for (int h = 0; h < GH; h++) sc[h] = 0.0f;
+    const bool seen = key < n && ok[key];
+    if (seen)
+        for (int c = pt; c < PER; c += C::kParts) {
+            const uint4 u = lds128(rows[0] + key * C::kRow + c * 16);
+            __half2 sc2, m24;
+            kv4_scale2(scales[0][key * PER + c], sc2, m24);
+            const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float f[8];
+                decode8f(words[i], sc2, m24, f);
+#pragma unroll
+                for (int h = 0; h < GH; h++)
+#pragma unroll
+                    for (int d = 0; d < 8; d += 4) {
+                        const float4 q = *reinterpret_cast<const float4 *>(&qs[h][c * 32 + i * 8 + d]);
+                        sc[h] = __fmaf_rn(q.x, f[d], sc[h]);
+                        sc[h] = __fmaf_rn(q.y, f[d + 1], sc[h]);
+                        sc[h] = __fmaf_rn(q.z, f[d + 2], sc[h]);
+                        sc[h] = __fmaf_rn(q.w, f[d + 3], sc[h]);
+                    }
+            }
+        }
+    if (key < n && pt == 0 && !seen) raise_status(A.status, kStatusKv4Lane);
+#pragma unroll
+    for (int off = 1; off < C::kParts; off <<= 1)
+#pragma unroll
+        for (int h = 0; h < GH; h++) sc[h] = __fadd_rn(sc[h], __shfl_xor_sync(0xffffffffu, sc[h], off));
+    if (pt == 0)
+#pragma unroll
+        for (int h = 0; h < GH; h++) ws[key][h] = seen ? sc[h] : -kInf;
+    __syncthreads();
+    // weights: a warp per head
+    const bool alone = !CL && L.count <= span;
+    const int64_t id0 = (int64_t)lane_i * A.n_heads + head0;
+    if (warp < GH && n > 0) {
+        float x[KM / 32], m = -kInf, l = 0.0f;
+#pragma unroll
+        for (int u = 0; u < KM / 32; u++) x[u] = ws[lane + 32 * u][warp], m = fmaxf(m, x[u]);
+        m = warp_max(m);
+        const bool some = m > -kInf;
+        if (!some) m = 0.0f;  // (nothing seen, scores of minus infinity or NaN alone)
+#pragma unroll
+        for (int u = 0; u < KM / 32; u++) {
+            x[u] = al_ex2(__fsub_rn(x[u], m));
+            l += x[u];
+            ws[lane + 32 * u][warp] = x[u];
+        }
+        l = warp_psum(l);
+        if (!some && l == 0.0f) m = -kInf;  // (no say in what the other pieces are relative to)
+        if (lane == 0) {
+            inv[warp] = !alone ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+            if (CL)
+                stat[warp] = make_float4(m, l, 0.0f, 0.0f);
+            else if (!alone && warp < heads)
+                ml[(id0 + warp) * splits + s] = make_float2(m, l);
+        }
+    }
+    __syncthreads();
+    // values: a word of eight dims of every kGroups-th key per thread
+    const int w = tid % C::kWords, gi = tid / C::kWords;
     float acc[GH][8];
 #pragma unroll
     for (int h = 0; h < GH; h++)
 #pragma unroll
         for (int d = 0; d < 8; d++) acc[h][d] = 0.0f;
-    const int w = tid % kWords, gi = tid / kWords;
-    for (int x0 = 0; x0 < n; x0 += kKeys) {
-        const int m = min(kKeys, n - x0);
-        __syncthreads();
-        for (int e = tid; e < m * kPer; e += kThreads) {
-            const int r = e / kPer, c = e % kPer;
-            const int64_t at = kv4_row(A.kv, A.n_kv, L.key(s * span + x0 + r), L.seq);
-            if (c == 0) ok[r] = at >= 0;
-            if (at < 0) continue;
-            const int64_t row = at + (int64_t)kvh * A.kv.page_rows;
-            cp_async16(rows[0] + r * kRow + c * 16, static_cast<const uint8_t *>(A.kv.k) + row * (HD / 2) + c * 16, 16);
-            cp_async16(rows[1] + r * kRow + c * 16, static_cast<const uint8_t *>(A.kv.v) + row * (HD / 2) + c * 16, 16);
-            scales[0][r * kPer + c] = static_cast<const uint8_t *>(A.kv.k_scale)[row * kPer + c];
-            scales[1][r * kPer + c] = static_cast<const uint8_t *>(A.kv.v_scale)[row * kPer + c];
-        }
-        cp_async_commit();
-        cp_async_wait_pending<0>();
-        __syncthreads();
-        // scores: kParts threads share a key, 32 dims of it in turn
-        const int key = tid / kParts, pt = tid % kParts;
-        float sc[GH];
+#pragma unroll 2
+    for (int j = gi; j < n; j += C::kGroups) {
+        if (!ok[j]) continue;
+        __half2 sc2, m24;
+        kv4_scale2(scales[1][j * PER + w / 4], sc2, m24);
+        float f[8];
+        decode8f(*reinterpret_cast<const uint32_t *>(rows[1] + j * C::kRow + w * 4), sc2, m24, f);
 #pragma unroll
-        for (int h = 0; h < GH; h++) sc[h] = 0.0f;
-        const bool seen = key < m && ok[key];
-        if (seen)
-            for (int c = pt; c < kPer; c += kParts) {
-                const uint4 u = lds128(rows[0] + key * kRow + c * 16);
-                __half2 sc2, m24;
-                kv4_scale2(scales[0][key * kPer + c], sc2, m24);
-                const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+        for (int h = 0; h < GH; h++) {
+            const float x = ws[j][h];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    float f[8];
-                    decode8f(words[i], sc2, m24, f);
-#pragma unroll
-                    for (int h = 0; h < GH; h++)
-#pragma unroll
-                        for (int d = 0; d < 8; d += 4) {
-                            const float4 q = *reinterpret_cast<const float4 *>(&qs[h][c * 32 + i * 8 + d]);
-                            sc[h] = __fmaf_rn(q.x, f[d], sc[h]);
-                            sc[h] = __fmaf_rn(q.y, f[d + 1], sc[h]);
-                            sc[h] = __fmaf_rn(q.z, f[d + 2], sc[h]);
-                            sc[h] = __fmaf_rn(q.w, f[d + 3], sc[h]);
-                        }
-                }
-            }
-        if (key < m && pt == 0 && !seen) raise_status(A.status, kStatusKv4Lane);
-#pragma unroll
-        for (int off = 1; off < kParts; off <<= 1)
-#pragma unroll
-            for (int h = 0; h < GH; h++) sc[h] = __fadd_rn(sc[h], __shfl_xor_sync(0xffffffffu, sc[h], off));
-        if (pt == 0)
-#pragma unroll
-            for (int h = 0; h < GH; h++) ws[key][h] = seen ? sc[h] : -kInf;
-        __syncthreads();
-        // weights: a warp per head
-        if (warp < GH) {
-            const float a = ws[lane][warp], b = ws[lane + 32][warp], old = sm[warp];
-            const float top = fmaxf(old, warp_max(fmaxf(a, b)));
-            const float base = top > -kInf ? top : 0.0f;  // (nothing seen yet)
-            const float ea = al_ex2(__fsub_rn(a, base)), eb = al_ex2(__fsub_rn(b, base));
-            const float sum = warp_psum(__fadd_rn(ea, eb));
-            ws[lane][warp] = ea, ws[lane + 32][warp] = eb;
-            if (lane == 0) {
-                const float f = old > -kInf ? al_ex2(__fsub_rn(old, base)) : 0.0f;
-                sl[warp] = __fmaf_rn(sl[warp], f, sum);
-                sm[warp] = top, sa[warp] = f;
-            }
-        }
-        __syncthreads();
-        // values: a word of eight dims of every kGroups-th key per thread
-#pragma unroll
-        for (int h = 0; h < GH; h++)
-#pragma unroll
-            for (int d = 0; d < 8; d++) acc[h][d] = __fmul_rn(acc[h][d], sa[h]);
-        for (int j = gi; j < m; j += kGroups) {
-            if (!ok[j]) continue;
-            __half2 sc2, m24;
-            kv4_scale2(scales[1][j * kPer + w / 4], sc2, m24);
-            float f[8];
-            decode8f(*reinterpret_cast<const uint32_t *>(rows[1] + j * kRow + w * 4), sc2, m24, f);
-#pragma unroll
-            for (int h = 0; h < GH; h++) {
-                const float x = ws[j][h];
-#pragma unroll
-                for (int d = 0; d < 8; d++) acc[h][d] = __fmaf_rn(x, f[d], acc[h][d]);
-            }
+            for (int d = 0; d < 8; d++) acc[h][d] = __fmaf_rn(x, f[d], acc[h][d]);
         }
     }
-    // the sum over the groups of keys: [kGroups][HD] for one head after the other, in the rows' place
-    __syncthreads();
-    float *red = reinterpret_cast<float *>(buf);
-    const bool alone = L.count <= span;
+    __syncthreads();  // the rows' place takes the groups' sums, [kGroups][GH][HD]
+    float *const red = reinterpret_cast<float *>(few_smem);
 #pragma unroll
-    for (int h = 0; h < GH; h++) {
-        if (h >= heads) break;
+    for (int h = 0; h < GH; h++)
 #pragma unroll
         for (int d = 0; d < 8; d += 4)
-            *reinterpret_cast<float4 *>(red + gi * HD + w * 8 + d) =
+            *reinterpret_cast<float4 *>(red + (gi * GH + h) * HD + w * 8 + d) =
                 make_float4(acc[h][d], acc[h][d + 1], acc[h][d + 2], acc[h][d + 3]);
-        __syncthreads();
-        const int64_t id = (int64_t)lane_i * A.n_heads + head0 + h, row = id * splits + s;
-        const float l = sl[h], inv = !alone ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-        for (int d = tid; d < HD; d += kThreads) {
-            float a = red[d];
-            for (int g = 1; g < kGroups; g++) a = __fadd_rn(a, red[g * HD + d]);
-            (alone ? A.out + id * HD : part + row * HD)[d] = a * inv;
+    __syncthreads();
+    constexpr int NV = HD / 4;
+    for (int e = tid; e < heads * NV; e += kThreads) {
+        const int h = e / NV, dd = (e % NV) * 4;
+        float4 a = *reinterpret_cast<const float4 *>(red + h * HD + dd);
+        for (int u = 1; u < C::kGroups; u++) {
+            const float4 b = *reinterpret_cast<const float4 *>(red + (u * GH + h) * HD + dd);
+            a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
         }
-        if (!alone && tid == 0) ml[row] = make_float2(sm[h], l);
-        __syncthreads();
+        if constexpr (CL) {
+            *reinterpret_cast<float4 *>(red + h * HD + dd) = a;
+            continue;
+        }
+        const float f = inv[h];
+        float *to = alone ? A.out + (id0 + h) * HD : part + ((id0 + h) * splits + s) * HD;
+        *reinterpret_cast<float4 *>(to + dd) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+    }
+    if constexpr (CL) {
+        // the cluster's CTAs share the outputs out: as many threads to four dims as there are CTAs (2, 4, 8 or 16), one
+        // for each one's sums
+        cluster_sync();
+        const int lg = splits <= 2 ? 1 : splits <= 4 ? 2 : splits <= 8 ? 3 : 4, r = tid & ((1 << lg) - 1);
+        const int items = heads * NV, share = (items + splits - 1) / splits;
+        for (int i0 = 0; i0 < share; i0 += kThreads >> lg) {
+            const int at = i0 + (tid >> lg), i = s * share + at, h = min(i, items - 1) / NV, dd = (i - h * NV) * 4;
+            const bool on = at < share && i < items;
+            float4 st = make_float4(-kInf, 0.0f, 0.0f, 0.0f), v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (on && r < splits) st = ld_peer_f4(&stat[h], (uint32_t)r);
+            const bool some = st.x > -kInf;
+            if (some) v = ld_peer_f4(red + h * HD + dd, (uint32_t)r);
+            float m = st.x;
+            for (int off = 1 << lg >> 1; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            const float x = some ? al_ex2(__fsub_rn(st.x, m)) : 0.0f;
+            float l = x * st.y;
+            v.x *= x, v.y *= x, v.z *= x, v.w *= x;
+            for (int off = 1 << lg >> 1; off > 0; off >>= 1) {
+                l += __shfl_xor_sync(0xffffffffu, l, off);
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, off), v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+                v.z += __shfl_xor_sync(0xffffffffu, v.z, off), v.w += __shfl_xor_sync(0xffffffffu, v.w, off);
+            }
+            const float f = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+            if (on && r == 0)
+                *reinterpret_cast<float4 *>(A.out + (id0 + h) * HD + dd) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+        }
+        cluster_sync();  // nobody leaves while its sums are read
     }
 }
 
@@ -989,14 +1038,19 @@ bool sizes_ok(int n_lanes, int n_heads, int n_kv, int hd) {
            n_heads <= 65535 && (hd == 64 || hd == 128 || hd == 256);
 }
 
-template <int HD>
-const void *few_kernel(int gh) {
+template <int HD, bool CL>
+const void *few_kernel(int gh, size_t &smem) {
+    smem = FewCfg<HD, CL>::bytes(gh);
     switch (gh) {
-        case 1: return (const void *)kv4_few_kernel<HD, 1>;
-        case 2: return (const void *)kv4_few_kernel<HD, 2>;
-        case 4: return (const void *)kv4_few_kernel<HD, 4>;
-        default: return (const void *)kv4_few_kernel<HD, 8>;
+        case 1: return (const void *)kv4_few_kernel<HD, 1, CL>;
+        case 2: return (const void *)kv4_few_kernel<HD, 2, CL>;
+        case 4: return (const void *)kv4_few_kernel<HD, 4, CL>;
+        default: return (const void *)kv4_few_kernel<HD, 8, CL>;
     }
+}
+template <bool CL>
+const void *few_kernel(int hd, int gh, size_t &smem) {
+    return hd == 64 ? few_kernel<64, CL>(gh, smem) : hd == 128 ? few_kernel<128, CL>(gh, smem) : few_kernel<256, CL>(gh, smem);
 }
 
 // The keys that a lane can see at most.
@@ -1005,8 +1059,15 @@ int64_t most_keys(const Kv4Args &A) {
     return A.window && (int64_t)A.window + A.sinks < rows ? (int64_t)A.window + A.sinks : rows;
 }
 
+// Whether a call is little work, by the caches' sizes (the positions are on the
+// device): the multiply-adds of all its lanes at most, and partial sums that the
+// workspace holds.
 bool few_fits(const Kv4Args &A) {
-    return (double)most_keys(A) * A.n_lanes * A.n_heads * A.hd * 2 <= 40e6;
+    const int64_t keys = most_keys(A), splits = (keys + 63) / 64;
+    int64_t rows;
+    carve(A.n_lanes, A.n_heads, A.n_kv, A.hd, nullptr, &rows);
+    return splits <= kMaxSplits && splits * A.n_lanes * A.n_heads <= rows &&
+           (double)keys * A.n_lanes * A.n_heads * A.hd * 2 <= 40e6;
 }
 
 // The checks of a call's sizes, and what they make of its arguments.
@@ -1023,18 +1084,26 @@ qlin_status describe(const char *fn, const qlin_kv4 *kv, int n_lanes, int n_head
     return QLIN_OK;
 }
 
-qlin_status attend_few(const Kv4Args &A, const AlWs &w, int64_t rows, cudaStream_t st) {
+qlin_status attend_few(const Kv4Args &A, const AlWs &w, cudaStream_t st) {
     const int64_t keys = most_keys(A);
-    int64_t span = (keys + kMaxSplits - 1) / kMaxSplits;
-    while ((keys + span - 1) / span * A.n_lanes * A.n_heads > rows) span *= 2;
-    span = (span + kKeys - 1) / kKeys * kKeys;
-    int splits = (int)((keys + span - 1) / span), ispan = (int)span;
     const int gh = few_heads(A.group);
-    void *args[] = {(void *)&A, (void *)&w.ml, (void *)&w.part, (void *)&splits, (void *)&ispan};
-    const void *kern = A.hd == 64 ? few_kernel<64>(gh) : A.hd == 128 ? few_kernel<128>(gh) : few_kernel<256>(gh);
-    if (qlin_status e = launch_pdl(kern, dim3(splits, A.n_kv * ((A.group + gh - 1) / gh), A.n_lanes), dim3(kThreads), 0, st,
-                                   args, "kv4_few_kernel"))
-        return e;
+    int splits = (int)((keys + 63) / 64), span = 64;
+    size_t smem;
+    void *args[] = {(void *)&A, (void *)&w.ml, (void *)&w.part, (void *)&splits, (void *)&span};
+    dim3 grid(splits, A.n_kv * ((A.group + gh - 1) / gh), A.n_lanes);
+    // One launch if the CTAs of every (lane, head block) can be a cluster and no cluster has to wait for another's SMs.
+    if (splits > 1 && keys <= kCluster * 128) {
+        const int c = splits < kCluster ? splits : kCluster;
+        const void *kern = few_kernel<true>(A.hd, gh, smem);
+        if (max_clusters(kern, smem, kThreads, c) >= (int64_t)grid.y * grid.z) {
+            splits = c, span = (int)((keys + c - 1) / c);
+            grid.x = c;
+            return launch_pdl(kern, grid, dim3(kThreads), smem, st, args, "kv4_few_kernel", c);
+        }
+    }
+    const void *kern = few_kernel<false>(A.hd, gh, smem);
+    blocks_per_sm(kern, smem);  // raises the dynamic shared-memory limit once
+    if (qlin_status e = launch_pdl(kern, grid, dim3(kThreads), smem, st, args, "kv4_few_kernel")) return e;
     if (splits == 1) return QLIN_OK;
     return launch_pdl((const void *)kv4_few_merge_kernel, dim3(A.n_heads, A.n_lanes, A.hd / kMergeDims), dim3(kThreads), 0,
                       st, args, "kv4_few_merge_kernel");
@@ -1132,12 +1201,11 @@ qlin_status qlin_attention_kv4(const float *q, const qlin_kv4 *kv, const int32_t
     QLIN_REQUIRE(aligned16(q) && aligned16(out) && aligned16(workspace) && aligned4(positions) && aligned4(seqs) &&
                      aligned4(status_word),
                  QLIN_ERR_INVALID_ARG, "%s: q, out and workspace are 16-byte aligned (positions, seqs, status_word: 4)", fn);
-    int64_t rows;
-    const AlWs w = carve(n_lanes, n_heads, n_kv, head_dim, (char *)workspace, &rows);
+    const AlWs w = carve(n_lanes, n_heads, n_kv, head_dim, (char *)workspace);
     QLIN_REQUIRE(workspace_bytes >= w.bytes, QLIN_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", fn, workspace_bytes,
                  w.bytes);
     A.q = q, A.positions = positions, A.seqs = seqs, A.out = out, A.status = status_word;
-    return few_fits(A) ? attend_few(A, w, rows, (cudaStream_t)stream) : attend_tc(A, w, (cudaStream_t)stream);
+    return few_fits(A) ? attend_few(A, w, (cudaStream_t)stream) : attend_tc(A, w, (cudaStream_t)stream);
 }
 
 }  // extern "C"
