@@ -769,6 +769,24 @@ qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u,
                         const int32_t *top_k, const float *top_p, const float *min_p, int n_rows, int vocab,
                         int32_t *tokens, float *probs, int32_t *kept, qlin_stream_t stream);
 
+/* decode_lanes_t158 over a paged cache of 4 bits a value: layer l's cache is
+ * kv with its codes code_bytes and its scales scale_bytes further on per layer
+ * (multiples of 32 and 16), one table for all layers.  The lanes' keys and values
+ * are appended with qlin_kv4_append and read with qlin_attention_kv4 (no window),
+ * everything else is decode_lanes_t158's arithmetic.  head_dim: 64, 128 or 256.
+ * A lane with a negative position is padding: it appends nothing, and what comes
+ * out for it says nothing (its token is looked up all the same).  decode_lanes_t158_status reports a lane, position or
+ * page out of range and a key or value that is not finite.  The workspace has
+ * decode_lanes_t158_kv4_workspace_size bytes, zero-filled before its first use. */
+typedef struct {
+    qlin_kv4 kv;
+    int64_t code_bytes, scale_bytes;
+} t158_kv4;
+qlin_status decode_lanes_t158_kv4_workspace_size(const t158_model *m, int max_lanes, size_t *bytes);
+qlin_status decode_lanes_t158_kv4(const t158_model *m, const t158_kv4 *cache, int n_lanes, const int32_t *tokens,
+                                  const int32_t *positions, const int32_t *seqs, float *logits, int32_t *next,
+                                  void *workspace, size_t workspace_bytes, int max_lanes, qlin_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

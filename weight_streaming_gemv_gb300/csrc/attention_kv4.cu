@@ -1061,13 +1061,20 @@ int64_t most_keys(const Kv4Args &A) {
 
 // Whether a call is little work, by the caches' sizes (the positions are on the
 // device): the multiply-adds of all its lanes at most, and partial sums that the
-// workspace holds.
+// workspace holds.  us per call here / on the tensor cores, whole caches in use:
+// 4 query heads on one KV head of 256: one lane of 1024 8.2 / 13.7, 16 of 1024
+// (34 M) 12.8 / 17.0, 16 of 2048 (67 M) 18.7 / 18.1, 16 of 4096 47 / 21; 8 on
+// each of two of 128: 16 of 512 (34 M) 10.4 / 14.4, 16 of 1024 (67 M) 30.0 /
+// 16.3; one on each of eight of 128: 16 of 1024 (34 M) 18.8 / 22.7, 64 of 1024
+// (134 M) 59 / 60, 64 of 2048 100 / 84; one on each of four of 64: 64 of 2048
+// (67 M) 32 / 43, 16 of 16384 (134 M) 63 / 58.
 bool few_fits(const Kv4Args &A) {
     const int64_t keys = most_keys(A), splits = (keys + 63) / 64;
+    const int gh = few_heads(A.group);
     int64_t rows;
     carve(A.n_lanes, A.n_heads, A.n_kv, A.hd, nullptr, &rows);
     return splits <= kMaxSplits && splits * A.n_lanes * A.n_heads <= rows &&
-           (double)keys * A.n_lanes * A.n_heads * A.hd * 2 <= 40e6;
+           (double)keys * A.n_lanes * A.n_heads * A.hd * 2 <= (gh >= 8 ? 40e6 : gh == 4 ? 55e6 : gh == 2 ? 80e6 : 110e6);
 }
 
 // The checks of a call's sizes, and what they make of its arguments.

@@ -23,6 +23,7 @@
 
 #include "common.cuh"
 #include "decode_ops.cuh"
+#include "kv4.cuh"
 #include "stream.cuh"
 
 namespace qlin {
@@ -43,6 +44,7 @@ qlin_status geglu_quant_tiles(const float *gate, const float *up, int8_t *xq, fl
 namespace {
 
 constexpr int kLaneStatusBad = 1;      // a lane's token, position or sequence slot out of range
+constexpr int kLaneStatusNotFinite = 4;  // a key or value that a 4-bit cache cannot hold
 constexpr int kLaneStatusTimeout = 2;  // a bounded wait inside the attention kernel gave up
 // Lanes from which every linear runs on the tensor cores (on activation tiles
 // the quantisers write, the linears sharing an input in one launch); below it
@@ -541,11 +543,13 @@ struct LanesWs {
     float *h, *xn, *xs, *q, *k, *v, *att, *y, *g, *u, *attn;
     int8_t *xq;
     void *lm, *tiles;  // tiles: fp16 activation tiles of the tensor-core linears
-    void *pre;         // the attention's, where prompts are kept apart
+    void *pre;         // the attention's, where prompts are kept apart or the cache is on pages
     size_t lm_bytes, pre_bytes, bytes;
 };
 
-LanesWs carve_lanes(const t158_model *m, int max_lanes, char *base, bool prompts) {
+enum LanesKind { kOwnCaches, kPrompts, kPaged4 };  // a cache per sequence, behind prompts, on pages of 4 bits a value
+
+LanesWs carve_lanes(const t158_model *m, int max_lanes, char *base, LanesKind kind) {
     LanesWs w{};
     size_t off = 0;
     auto take = [&](size_t b) {
@@ -568,11 +572,13 @@ LanesWs carve_lanes(const t158_model *m, int max_lanes, char *base, bool prompts
     w.y = (float *)take(4 * M * d);
     w.g = (float *)take(4 * M * f);
     w.u = (float *)take(4 * M * f);
-    w.attn = (float *)take(prompts ? 0 : 4 * M * m->n_heads * (size_t)attn_chunks(m->max_pos) * (2 + m->head_dim));
+    w.attn = (float *)take(kind != kOwnCaches ? 0 : 4 * M * m->n_heads * (size_t)attn_chunks(m->max_pos) * (2 + m->head_dim));
     w.lm_bytes = qlin_lm_head_lanes_workspace_size(m->vocab, m->dim);
     w.lm = take(w.lm_bytes);
     w.tiles = take(max_lanes >= kLanesTensorMin ? t158_tc_workspace_bytes(max_lanes, (int)big) : 0);
-    w.pre_bytes = prompts ? qlin_attention_lanes_workspace_size(max_lanes, m->n_heads, m->n_kv_heads, m->head_dim) : 0;
+    w.pre_bytes = kind == kPrompts   ? qlin_attention_lanes_workspace_size(max_lanes, m->n_heads, m->n_kv_heads, m->head_dim)
+                  : kind == kPaged4 ? qlin_attention_kv4_workspace_size(max_lanes, m->n_heads, m->n_kv_heads, m->head_dim)
+                                    : 0;
     w.pre = take(w.pre_bytes);
     w.bytes = off;
     return w;
@@ -617,20 +623,20 @@ qlin_status check_lanes_model(const t158_model *m) {
 
 // One step over lanes.  prompts null: every sequence has its whole cache,
 // max_pos rows; else the prompts' rows are in prompts->kv and kv_caches holds
-// own_rows rows of what follows them.
-qlin_status lanes_step(const t158_model *m, const t158_prompts *prompts, const int32_t *prefix_of, float *kv_caches,
+// own_rows rows of what follows them.  paged: the cache is there instead.
+qlin_status lanes_step(const t158_model *m, const t158_prompts *prompts, const t158_kv4 *paged, const int32_t *prefix_of, float *kv_caches,
                        int own_rows, int n_seqs, int n_lanes, const int32_t *tokens, const int32_t *positions,
                        const int32_t *seqs, float *logits, int32_t *next, void *workspace, size_t workspace_bytes,
                        int max_lanes, qlin_stream_t stream) {
     qlin_status st = check_lanes_model(m);
     if (st) return st;
-    QLIN_REQUIRE(kv_caches && tokens && positions && seqs && next && workspace, QLIN_ERR_INVALID_ARG,
+    QLIN_REQUIRE((kv_caches || paged) && tokens && positions && seqs && next && workspace, QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158: null pointer");
     QLIN_REQUIRE(n_seqs >= 1 && n_lanes >= 1 && n_lanes <= max_lanes && max_lanes <= 4096, QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158: n_seqs %d, n_lanes %d, max_lanes %d", n_seqs, n_lanes, max_lanes);
     QLIN_REQUIRE(aligned16(workspace) && aligned16(kv_caches), QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158: workspace or kv_caches not 16-byte aligned");
-    const LanesWs w = carve_lanes(m, max_lanes, (char *)workspace, prompts != nullptr);
+    const LanesWs w = carve_lanes(m, max_lanes, (char *)workspace, prompts ? kPrompts : paged ? kPaged4 : kOwnCaches);
     QLIN_REQUIRE(workspace_bytes >= w.bytes, QLIN_ERR_INVALID_ARG, "decode_lanes_t158: workspace %zu < %zu bytes",
                  workspace_bytes, w.bytes);
     cudaStream_t s = (cudaStream_t)stream;
@@ -702,12 +708,24 @@ qlin_status lanes_step(const t158_model *m, const t158_prompts *prompts, const i
             float *const qkv[3] = {w.q, w.k, w.v};
             if ((st = lin_group(l, 0, 3, qkv))) return st;
         }
-        lanes_rope_kv_kernel<<<M, 256, (size_t)kvd * sizeof(float), s>>>(
-            w.q, w.k, w.v, kv_caches, positions, seqs, n_seqs, l, L, m->max_pos, own_rows,
-            prompts ? prompts->len : nullptr, prefix_of, prompts ? prompts->n_prompts : 0, prompts ? prompts->rows : 0,
-            m->rope_cos, m->rope_sin, nh, nkv, hd, w.status);
-        QLIN_LAUNCHED("lanes_rope_kv_kernel");
-        if (prompts) {
+        if (!paged) {
+            lanes_rope_kv_kernel<<<M, 256, (size_t)kvd * sizeof(float), s>>>(
+                w.q, w.k, w.v, kv_caches, positions, seqs, n_seqs, l, L, m->max_pos, own_rows,
+                prompts ? prompts->len : nullptr, prefix_of, prompts ? prompts->n_prompts : 0, prompts ? prompts->rows : 0,
+                m->rope_cos, m->rope_sin, nh, nkv, hd, w.status);
+            QLIN_LAUNCHED("lanes_rope_kv_kernel");
+        }
+        if (paged) {
+            qlin_kv4 kv = paged->kv;
+            auto on = [&](void *p, int64_t bytes) { return (void *)((uint8_t *)p + l * bytes); };
+            kv.k = on(kv.k, paged->code_bytes), kv.v = on(kv.v, paged->code_bytes);
+            kv.k_scale = on(kv.k_scale, paged->scale_bytes), kv.v_scale = on(kv.v_scale, paged->scale_bytes);
+            if ((st = qlin_kv4_append(&kv, w.k, w.v, kvd, w.q, qd, w.q, m->rope_cos, m->rope_sin, m->max_pos, positions, seqs,
+                                      M, nh, nkv, hd, w.status, stream)) ||
+                (st = qlin_attention_kv4(w.q, &kv, positions, seqs, M, nh, nkv, hd, 0, 0, w.att, w.status, w.pre, w.pre_bytes,
+                                         stream)))
+                return st;
+        } else if (prompts) {
             auto layer = [&](const float *kv, int rows, int n) {
                 qlin_kv c{};
                 c.k = kv + (int64_t)2 * l * rows * kvd;
@@ -772,7 +790,7 @@ qlin_status decode_lanes_t158_workspace_size(const t158_model *m, int max_lanes,
     if (st) return st;
     QLIN_REQUIRE(bytes && max_lanes >= 1 && max_lanes <= 4096, QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158_workspace_size: max_lanes %d outside 1..4096", max_lanes);
-    *bytes = carve_lanes(m, max_lanes, nullptr, false).bytes;
+    *bytes = carve_lanes(m, max_lanes, nullptr, kOwnCaches).bytes;
     return QLIN_OK;
 }
 
@@ -781,7 +799,7 @@ qlin_status decode_lanes_t158(const t158_model *m, float *kv_caches, int n_seqs,
                               void *workspace, size_t workspace_bytes, int max_lanes, qlin_stream_t stream) {
     qlin::clear_error();
     if (qlin_status st = check_lanes_model(m)) return st;
-    return lanes_step(m, nullptr, nullptr, kv_caches, m->max_pos, n_seqs, n_lanes, tokens, positions, seqs, logits, next,
+    return lanes_step(m, nullptr, nullptr, nullptr, kv_caches, m->max_pos, n_seqs, n_lanes, tokens, positions, seqs, logits, next,
                       workspace, workspace_bytes, max_lanes, stream);
 }
 
@@ -790,7 +808,7 @@ qlin_status decode_lanes_t158_prefix_workspace_size(const t158_model *m, int max
     if (qlin_status st = check_lanes_model(m)) return st;
     QLIN_REQUIRE(bytes && max_lanes >= 1 && max_lanes <= 4096, QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158_prefix_workspace_size: max_lanes %d outside 1..4096", max_lanes);
-    *bytes = carve_lanes(m, max_lanes, nullptr, true).bytes;
+    *bytes = carve_lanes(m, max_lanes, nullptr, kPrompts).bytes;
     return QLIN_OK;
 }
 
@@ -812,8 +830,37 @@ qlin_status decode_lanes_t158_prefix(const t158_model *m, const t158_prompts *pr
                  (int)prompts->rows, own_rows);
     QLIN_REQUIRE(aligned16(prompts->kv) && aligned4(prompts->len) && aligned4(prefix_of), QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158_prefix: misaligned prompts");
-    return lanes_step(m, prompts, prefix_of, kv_caches, own_rows, n_seqs, n_lanes, tokens, positions, seqs, logits, next,
+    return lanes_step(m, prompts, nullptr, prefix_of, kv_caches, own_rows, n_seqs, n_lanes, tokens, positions, seqs, logits, next,
                       workspace, workspace_bytes, max_lanes, stream);
+}
+
+qlin_status decode_lanes_t158_kv4_workspace_size(const t158_model *m, int max_lanes, size_t *bytes) {
+    qlin::clear_error();
+    if (qlin_status st = check_lanes_model(m)) return st;
+    QLIN_REQUIRE(bytes && max_lanes >= 1 && max_lanes <= 4096, QLIN_ERR_INVALID_ARG,
+                 "decode_lanes_t158_kv4_workspace_size: max_lanes %d outside 1..4096", max_lanes);
+    *bytes = carve_lanes(m, max_lanes, nullptr, kPaged4).bytes;
+    return QLIN_OK;
+}
+
+qlin_status decode_lanes_t158_kv4(const t158_model *m, const t158_kv4 *cache, int n_lanes, const int32_t *tokens,
+                                  const int32_t *positions, const int32_t *seqs, float *logits, int32_t *next,
+                                  void *workspace, size_t workspace_bytes, int max_lanes, qlin_stream_t stream) {
+    qlin::clear_error();
+    const char *fn = "decode_lanes_t158_kv4";
+    if (qlin_status st = check_lanes_model(m)) return st;
+    QLIN_REQUIRE(cache, QLIN_ERR_INVALID_ARG, "%s: null pointer", fn);
+    // (what the append and the attention take: refused here, before anything is written)
+    if (qlin_status st = check_kv4(fn, &cache->kv, m->n_kv_heads, m->head_dim)) return st;
+    QLIN_REQUIRE(cache->code_bytes >= 0 && cache->scale_bytes >= 0 && cache->code_bytes % 32 == 0 &&
+                     cache->scale_bytes % 16 == 0,
+                 QLIN_ERR_INVALID_ARG, "%s: code_bytes %lld, scale_bytes %lld: multiples of 32 and 16", fn,
+                 (long long)cache->code_bytes, (long long)cache->scale_bytes);
+    QLIN_REQUIRE(m->n_heads <= 65535 && aligned16(m->rope_cos) && aligned16(m->rope_sin) && aligned4(positions) &&
+                     aligned4(seqs),
+                 QLIN_ERR_INVALID_ARG, "%s: more than 65535 heads, or a misaligned pointer", fn);
+    return lanes_step(m, nullptr, cache, nullptr, nullptr, 0, cache->kv.n_seqs, n_lanes, tokens, positions, seqs, logits,
+                      next, workspace, workspace_bytes, max_lanes, stream);
 }
 
 int decode_lanes_t158_launches(const t158_model *m, int n_lanes) {
@@ -836,6 +883,8 @@ qlin_status decode_lanes_t158_status(void *workspace, qlin_stream_t stream) {
     QLIN_CUDA(cudaMemset(workspace, 0, sizeof stw));
     QLIN_REQUIRE(!(stw[0] & kLaneStatusBad), QLIN_ERR_INVALID_ARG,
                  "decode_lanes_t158: a lane's token, position or sequence slot was out of range");
+    QLIN_REQUIRE(!(stw[0] & kLaneStatusNotFinite), QLIN_ERR_INVALID_ARG,
+                 "decode_lanes_t158: a key or value that is not finite went into a 4-bit cache");
     QLIN_REQUIRE(!(stw[0] & kLaneStatusTimeout), QLIN_ERR_TIMEOUT,
                  "decode_lanes_t158: a bounded wait in the attention kernel gave up");
     return QLIN_OK;

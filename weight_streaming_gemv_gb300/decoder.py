@@ -231,3 +231,71 @@ class T158Decoder:
             self.beam_status.zero_()
             raise qlin.QlinError("qlin_beam_reorder", qlin.ERR_TIMEOUT, "a bounded wait gave up: the beams' states are "
                                  "partly moved")
+
+    # ---------------------------------------------------------------- a paged cache of 4 bits a value, sampling
+    def prepare_paged(self, n_seqs: int, n_pages: int, max_lanes: int, page_rows: int = 64):
+        """A pool of n_pages pages of ``page_rows`` positions, 4 bits a value, that n_seqs sequences draw from (each up to
+        the model's max_pos), and the workspace of ``step_paged``.  ``paged_room`` gives a sequence pages before its
+        positions are written, ``paged_release`` takes them back; both write the table on torch's current stream."""
+        cfg, dev = self.cfg, self.emb.device
+        L, G, hd = cfg.n_layers, cfg.n_kv_heads, cfg.head_dim
+        u8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=dev)
+        i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
+        self.paged_max_lanes = max_lanes
+        # k and v, layer by layer
+        self.page_codes = u8(2, L, n_pages, G, page_rows, hd // 2)
+        self.page_scales = u8(2, L, n_pages, G, page_rows, hd // 32)
+        self.page_table = torch.full((n_seqs, -(-cfg.max_pos // page_rows)), -1, dtype=torch.int32, device=dev)
+        self.page_rows, self.pages_free, self.pages_of = page_rows, list(range(n_pages))[::-1], [[] for _ in range(n_seqs)]
+        c = qlin.T158Kv4C()
+        c.kv = qlin.kv4_cache(self.page_codes[0, 0], self.page_codes[1, 0], self.page_scales[0, 0], self.page_scales[1, 0],
+                              self.page_table)
+        c.code_bytes, c.scale_bytes = self.page_codes.stride(1), self.page_scales.stride(1)
+        self.paged = c
+        self.paged_ws_bytes = qlin.decode_lanes_t158_kv4_workspace_size(self.model, max_lanes)
+        self.paged_workspace = torch.zeros(self.paged_ws_bytes, dtype=torch.uint8, device=dev)
+        self.paged_tokens, self.paged_pos, self.paged_seq, self.paged_next = (i32(max_lanes) for _ in range(4))
+
+    def paged_room(self, seq: int, rows: int):
+        """Pages for the first ``rows`` positions of sequence ``seq``; raises MemoryError, and takes none, where the pool has
+        too few."""
+        if not 0 <= rows <= self.cfg.max_pos:
+            raise ValueError(f"paged_room: {rows} positions, and the model has {self.cfg.max_pos}")
+        have = self.pages_of[seq]
+        need = -(-rows // self.page_rows) - len(have)
+        if need > len(self.pages_free):
+            raise MemoryError(f"paged_room: {need} pages for sequence {seq}, {len(self.pages_free)} are free")
+        if need > 0:
+            new = [self.pages_free.pop() for _ in range(need)]
+            self.page_table[seq, len(have): len(have) + need] = torch.tensor(new, dtype=torch.int32).to(self.page_table.device)
+            have.extend(new)
+
+    def paged_release(self, seq: int):
+        """The sequence's pages go back to the pool."""
+        self.pages_free.extend(reversed(self.pages_of[seq]))
+        self.pages_of[seq] = []
+        self.page_table[seq].fill_(-1)
+
+    def step_paged(self, n_lanes: int, logits=None, stream=None):
+        """``step_lanes`` over the paged cache: lanes 0..n_lanes-1 of paged_tokens / paged_pos / paged_seq (a negative
+        position is padding); the greedy tokens go to paged_next, the logits [n_lanes][vocab] to ``logits`` if given."""
+        qlin.decode_lanes_t158_kv4(self.model, self.paged, n_lanes, self.paged_tokens, self.paged_pos, self.paged_seq, logits,
+                                   self.paged_next, self.paged_workspace, self.paged_ws_bytes, self.paged_max_lanes, stream)
+
+    def check_paged_status(self, stream=None):
+        qlin.decode_lanes_t158_status(self.paged_workspace, stream)
+
+    def sample(self, logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, kept=None,
+               stream=None):
+        """Draws a token for every row of ``logits`` [rows][vocab] (fp32, any stride between rows) into ``tokens`` (int32)
+        from the random numbers ``u`` [rows] in [0, 1); see qlin_sample for the bounds, tensors of one number per row."""
+        rows, vocab = logits.shape
+        if logits.dtype != torch.float32 or (vocab > 1 and logits.stride(1) != 1):
+            raise ValueError("sample: logits are fp32, a row's contiguous")
+        wants = ((u, torch.float32), (tokens, torch.int32), (temperature, torch.float32), (top_k, torch.int32),
+                 (top_p, torch.float32), (min_p, torch.float32), (probs, torch.float32), (kept, torch.int32))
+        for t, kind in wants:
+            if t is not None and (t.dtype != kind or t.numel() < rows or not t.is_contiguous()):
+                raise ValueError(f"sample: a tensor of {t.dtype} {tuple(t.shape)} for {rows} rows of {kind}")
+        qlin.qlin_sample(logits, logits.stride(0) if rows > 1 else vocab, u, temperature, top_k, top_p, min_p, rows, vocab, tokens, probs, kept,
+                         stream)

@@ -84,6 +84,12 @@ class T158PromptsC(ctypes.Structure):
                 ("rows", ctypes.c_int32)]
 
 
+class T158Kv4C(ctypes.Structure):
+    """Mirror of ``t158_kv4``."""
+
+    _fields_ = [("kv", QlinKv4C), ("code_bytes", ctypes.c_int64), ("scale_bytes", ctypes.c_int64)]
+
+
 _P, _I, _I64, _F, _D, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double,
                              ctypes.c_size_t)
 _ST = ctypes.c_int
@@ -159,6 +165,9 @@ SIGNATURES = {
     "qlin_kv4_read": ([ctypes.POINTER(QlinKv4C), _P, _P, _I, _I, _I, _P, _P, _P, _P], _ST),
     "qlin_sample": ([_P, _I64, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P], _ST),
     "qlin_attention_kv4_workspace_size": ([_I, _I, _I, _I], _SZ),
+    "decode_lanes_t158_kv4_workspace_size": ([ctypes.POINTER(T158ModelC), _I, ctypes.POINTER(_SZ)], _ST),
+    "decode_lanes_t158_kv4": ([ctypes.POINTER(T158ModelC), ctypes.POINTER(T158Kv4C), _I, _P, _P, _P, _P, _P, _P, _SZ, _I,
+                               _P], _ST),
     "qlin_attention_kv4_on_tensor_cores": ([ctypes.POINTER(QlinKv4C), _I, _I, _I, _I, _I, _I], _I),
     "qlin_attention_kv4": ([_P, ctypes.POINTER(QlinKv4C), _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P], _ST),
 }
@@ -621,3 +630,17 @@ def qlin_sample(logits, row_stride, u, temperature, top_k, top_p, min_p, n_rows,
     _check("qlin_sample", lib().qlin_sample(
         _ptr(logits), row_stride, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), n_rows, vocab,
         _ptr(tokens), _ptr(probs), _ptr(kept), _stream(stream)))
+
+
+def decode_lanes_t158_kv4_workspace_size(model: T158ModelC, max_lanes: int) -> int:
+    n = ctypes.c_size_t()
+    _check("decode_lanes_t158_kv4_workspace_size",
+           lib().decode_lanes_t158_kv4_workspace_size(ctypes.byref(model), max_lanes, ctypes.byref(n)))
+    return n.value
+
+
+def decode_lanes_t158_kv4(model: T158ModelC, cache: T158Kv4C, n_lanes, tokens, positions, seqs, logits, next_tokens,
+                          workspace, workspace_bytes, max_lanes, stream=None):
+    _check("decode_lanes_t158_kv4", lib().decode_lanes_t158_kv4(
+        ctypes.byref(model), ctypes.byref(cache), n_lanes, _ptr(tokens), _ptr(positions), _ptr(seqs), _ptr(logits),
+        _ptr(next_tokens), _ptr(workspace), workspace_bytes, max_lanes, _stream(stream)))
