@@ -395,3 +395,185 @@ def test_shared_pages(dev):
     call = Call(dev, 6, 4, 1, 256)
     call.go(pool, i32(pos, dev), i32(seqs, dev))
     _check(pool, call, pos, seqs, 0, 0)
+
+
+@pytest.mark.parametrize("tensor", [False, True])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("case", ["rising", "falling", "spikes", "large", "tiny", "flat"])
+def test_scores_of_any_kind(dev, tensor, hd, case):
+    """maxima that rise or fall along a sequence, single large scores, scores far apart and values near the least scale"""
+    import torch
+
+    from weight_streaming_gemv_gb300 import qlin
+
+    H, G, n, rows = 4, 1, 3, 1500
+    pool = Pool(dev, n, rows, G, hd, 64)
+    call = Call(dev, n, H, G, hd)
+    rng = np.random.default_rng(hd)
+    x = rng.standard_normal((2, n * pool.per, G, 64, hd), np.float32)
+    along = (np.arange(pool.rows) / pool.rows).astype(np.float32)
+    q = call.q.cpu().numpy()
+    if case in ("rising", "falling"):  # scores from -20 to 20 along a common direction of the queries
+        q = np.broadcast_to(q[:1, :1], q.shape).copy()
+        way = q[0, 0] / np.linalg.norm(q[0, 0]) ** 2 * np.sqrt(hd)
+        t = (40 * along - 20) * (1 if case == "rising" else -1)
+        x[0] = 0.1 * x[0] + t.reshape(1, -1, 1, 64, 1).repeat(n, 0).reshape(n * pool.per, 1, 64, 1) * way
+    elif case == "spikes":
+        x[0] *= np.where(rng.random(x[0].shape[:3]) < 0.01, 6, 0.2)[..., None]
+    elif case == "large":
+        q *= 300.0
+    elif case == "tiny":
+        x *= 3e-6
+        q *= 1e4
+    else:
+        x[0] = 0.0
+    call.q.copy_(torch.from_numpy(q))
+    code, b = ref.quantise(x)
+    own = pool.table.reshape(-1)
+    pool.codes[:, own], pool.scales[:, own] = ref.pack(code), b
+    pool.d_codes.copy_(torch.from_numpy(pool.codes)), pool.d_scales.copy_(torch.from_numpy(pool.scales))
+    pos, seqs = _lanes(pool, H, hd, np.array([rows - 1, 700, 130]), np.arange(n), 0, 0, tensor)
+    big = Call(dev, len(pos), H, G, hd)
+    big.q.copy_(call.q.repeat(len(pos) // n, 1, 1))
+    big.go(pool, i32(pos, dev), i32(seqs, dev))
+    if case != "large":
+        _check(pool, big, pos, seqs, 0, 0, lanes=list(range(n)) + [len(pos) - 1])
+        return
+    # scores of some hundreds: an error of 2^-22 of the score is an error of the weights; a factor 300 over the others
+    got, k = big.result(), [pool.host(s) for s in range(n)]
+    for i in range(n):
+        want = ref.attend(q[i], k[i][0], k[i][1], int(pos[i]), 0, 0, G)
+        e = np.linalg.norm(got[i] - want, axis=-1) / np.linalg.norm(want, axis=-1)
+        assert e.max() <= 300 * TOL, e
+
+
+@pytest.mark.parametrize("tensor", [False, True])
+def test_queries_that_are_not_finite(dev, tensor):
+    """a NaN or an infinity in a query stays with its lane and head's outputs; rows of zeros and of huge values are right"""
+    pool = Pool(dev, 4, 900, 2, 128, 32)
+    pos, seqs = _lanes(pool, 4, 128, np.array([899, 899, 500, 10]), np.arange(4), 0, 0, tensor)
+    call = Call(dev, len(pos), 4, 2, 128)
+    call.q[0, 1, 5] = float("nan")
+    call.q[1, 3, 7] = float("inf")
+    call.q[2, 0] = 0.0
+    call.q[3, 2] = 1e-30
+    call.go(pool, i32(pos, dev), i32(seqs, dev))
+    got, q = call.result(), call.q.cpu().numpy()
+    assert np.isnan(got[0, 1]).all() and np.isnan(got[1, 3]).any()
+    for i in range(4):
+        k, v, _ = pool.host(i)
+        heads = [h for h in range(4) if np.isfinite(q[i, h]).all()]
+        want = ref.attend(np.where(np.isfinite(q[i]), q[i], 0), k, v, int(pos[i]), 0, 0, 2)
+        e = np.linalg.norm(got[i] - want, axis=-1) / np.linalg.norm(want, axis=-1)
+        assert e[heads].max() <= TOL
+
+
+@pytest.mark.parametrize("tensor", [False, True])
+def test_same_bits_whatever_else_runs(dev, tensor):
+    """the same call twice, in a graph replayed with other positions, and beside another call on another stream"""
+    import torch
+
+    H, G, hd, n = 8, 2, 128, 6
+    pool = Pool(dev, n, 1200, G, hd, 16)
+    pos, seqs = _lanes(pool, H, hd, np.array([1199, 5, 640, 700, -1, 127]), np.arange(n), 0, 0, tensor)
+    d_pos, d_seqs = i32(pos, dev), i32(seqs, dev)
+    call, other = Call(dev, len(pos), H, G, hd), Call(dev, len(pos), H, G, hd, seed=9)
+    call.go(pool, d_pos, d_seqs)
+    want = call.result().copy()
+    other.go(pool, d_pos, d_seqs)
+    want2 = other.result().copy()
+    call.out.fill_(7.5)
+    call.go(pool, d_pos, d_seqs)
+    assert np.array_equal(call.result(), want)
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    live = d_pos.clone()
+    with torch.cuda.graph(g):
+        call.go(pool, live, d_seqs)
+    live.copy_(i32(np.where(pos > 0, pos // 2, pos), dev))
+    g.replay()
+    torch.cuda.synchronize()
+    _check(pool, call, np.where(pos > 0, pos // 2, pos), seqs, 0, 0, lanes=range(n))
+    live.copy_(d_pos)
+    g.replay()
+    assert np.array_equal(call.result(), want)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        call.go(pool, d_pos, d_seqs)
+        other.go(pool, d_pos, d_seqs, stream=s)
+    assert np.array_equal(call.result(), want) and np.array_equal(other.result(), want2)
+
+
+@pytest.mark.parametrize("tensor", [False, True])
+def test_pools_past_32_bits(dev, tensor):
+    """pages whose codes lie more than 2^32 bytes into the pool"""
+    import torch
+
+    from weight_streaming_gemv_gb300 import qlin
+
+    hd, G, page = 256, 1, 256
+    n_pages = (1 << 32) // (page * hd // 2) + 40
+    small = Pool(dev, 2, 1500, G, hd, page)
+    own = torch.from_numpy(small.table.reshape(-1).astype(np.int64)).to(dev)
+    codes = [torch.empty((n_pages, G, page, hd // 2), dtype=torch.uint8, device=dev) for _ in range(2)]
+    scales = [torch.empty((n_pages, G, page, hd // 32), dtype=torch.uint8, device=dev) for _ in range(2)]
+    at = torch.arange(n_pages - 1, n_pages - 1 - own.numel(), -1, device=dev)
+    for i in (0, 1):
+        codes[i][at], scales[i][at] = small.d_codes[i][own], small.d_scales[i][own]
+    table = at.int().view(2, -1).contiguous()
+    big = type("Big", (), dict(c=qlin.kv4_cache(codes[0], codes[1], scales[0], scales[1], table), n_kv=G))
+    pos, seqs = _lanes(big, 4, hd, np.array([1499, 800]), np.arange(2), 0, 0, tensor)
+    call = Call(dev, len(pos), 4, G, hd)
+    call.go(big, i32(pos, dev), i32(seqs, dev))
+    _check(small, call, pos, seqs, 0, 0, lanes=range(2))
+    # appending there and reading back
+    r = Rows(dev, 2, 4, G, hd)
+    big.codes, big.scales = None, None
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    _append(big, r, np.array([1400, 3]), np.array([1, 0]), status=status)
+    back = torch.empty((2, G, hd), device=dev)
+    qlin.qlin_kv4_read(big.c, i32([1400, 3], dev), i32([1, 0], dev), 2, G, hd, back, None, status)
+    code, b = ref.quantise(r.heads("k"))
+    assert int(status) == 0
+    assert np.array_equal(back.cpu().numpy(), ref.values(ref.pack(code), b).astype(np.float32))
+
+
+def test_append_graph_and_streams(dev):
+    """a captured append replayed with other rows and positions; two appends at once to different sequences"""
+    import torch
+
+    pool = Pool(dev, 2, 128, 2, 128, 32)
+    rope = _rope(dev, 128, 128)
+    from weight_streaming_gemv_gb300 import qlin
+
+    rows = [Rows(dev, 5, 4, 2, 128, seed=s) for s in range(3)]
+    live = rows[0].d.clone()
+    pos, seqs = i32(np.arange(5), dev), i32(np.zeros(5), dev)
+    out = torch.empty((5, 4, 128), device=dev)
+    go = lambda x, p, s, o, stream=None: qlin.qlin_kv4_append(
+        pool.c, rows[0].part("k", x), rows[0].part("v", x), x.stride(0), rows[0].part("q", x), x.stride(0), o, rope[0], rope[1],
+        128, p, s, 5, 4, 2, 128, None, stream)
+    go(live, pos, seqs, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go(live, pos, seqs, out)
+    for k in (1, 2):
+        live.copy_(rows[k].d), pos.copy_(i32(np.arange(5) + 7 * k, dev))
+        pool.refresh()
+        g.replay()
+        torch.cuda.synchronize()
+        codes, scales, q = _expect(pool, rows[k], np.arange(5) + 7 * k, np.zeros(5, int), rope, np.ones(5, bool))
+        assert np.array_equal(pool.d_codes.cpu().numpy(), codes) and np.array_equal(pool.d_scales.cpu().numpy(), scales)
+        assert np.array_equal(out.cpu().numpy(), q)
+    s = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(out) for _ in range(2)]
+    p2 = i32(np.arange(5) + 90, dev)
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        go(rows[i].d, p2, i32(np.full(5, i), dev), outs[i], s[i])
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        at = np.arange(5) + 90
+        k, v, _ = (pool.refresh(), pool.host(i))[1]
+        code, b = ref.quantise(rows[i].heads("v"))
+        assert np.array_equal(v[at], ref.values(ref.pack(code), b))
