@@ -357,7 +357,7 @@ struct KvCfg {
 };
 
 struct KvCtl {
-    uint64_t kfull[2], kempty[2], vfull[6], vempty[6];
+    uint64_t kfull[2], vfull[6], vempty[6];
     uint64_t kst_full[kMaxStages], kst_empty[kMaxStages], vst_full[kMaxStages], vst_empty[kMaxStages];
     uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready, drain;
     uint64_t pc_full[kPieceRing], pc_empty[kPieceRing];
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 32) {
-        for (int s = 0; s < 2; s++) mbar_init(&S.kfull[s], C::kKWarps), mbar_init(&S.kempty[s], 1);
+        for (int s = 0; s < 2; s++) mbar_init(&S.kfull[s], C::kKWarps);
         for (int s = 0; s < C::kHalves; s++) mbar_init(&S.vfull[s], C::kVWarps / 2), mbar_init(&S.vempty[s], 1);
         for (int s = 0; s < kMaxStages; s++) {
             mbar_init(&S.kst_full[s], 1), mbar_init(&S.kst_empty[s], C::kKWarps);
@@ -532,9 +532,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (lane == 0) mbar_arrive(&S.kst_empty[kst]);
                     if (++kst == L.nks) kst = 0, kpar ^= 1u;
                     const int slot = c & 1, round = c >> 1;
-                    if (round && !(ok = kv_wait_all(&S.kempty[slot], (uint32_t)(round - 1) & 1u, &S.abort))) break;
+                    if (round && !(ok = kv_wait_all(&S.s_full[slot], (uint32_t)(round - 1) & 1u, &S.abort))) break;
                     __syncwarp();
-                    tc_fence_after();  // (the products that read what lay there)
+                    tc_fence_after();  // (the scores that read what lay there)
                     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
@@ -719,7 +719,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < 4 * nK; kk++)
                             kv_mma_ta(d, a + 8u * kk, b0 + qstep * (kk / 4) + 2u * (kk % 4), hi128, ids, kk > 0);
-                        tc_commit(&S.kempty[g & 1]);
                         tc_commit(&S.s_full[g & 1]);
                     }
                     if (i >= 1) {

@@ -30,7 +30,7 @@ struct AppendArgs {
     const float *cos_t, *sin_t;
     int rope_rows;
     const int32_t *positions, *seqs;
-    int n_lanes, n_heads, n_kv, hd;
+    int n_heads, n_kv;
     int32_t *status;
 };
 
@@ -64,15 +64,15 @@ __device__ __forceinline__ bool finite4(const float (&x)[4]) {
     return ok;
 }
 
-// per: threads to a head's row.  The rows of a lane: the queries', then the
-// keys', then the values'.
+// Block x: a lane; y: its rows, PER threads to a head's row.  The rows of a
+// lane: the queries', then the keys', then the values'.
+template <int PER>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const __grid_constant__ AppendArgs A) {
-    const int per = A.hd / 8, heads = A.q ? A.n_heads : 0, rows = heads + 2 * A.n_kv;
-    const int64_t at = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x, total = (int64_t)A.n_lanes * rows * per;
-    const bool on = at < total;
-    const int64_t item = (on ? at : 0) / per;
-    const int j = (int)(at % per), lane = (int)(item / rows), row = (int)(item % rows);
-    const int what = row < heads ? 0 : row < heads + A.n_kv ? 1 : 2;  // query, key, value
+    constexpr int HD = 8 * PER;
+    const int heads = A.q ? A.n_heads : 0, rows = heads + 2 * A.n_kv, lane = blockIdx.x;
+    const int row = blockIdx.y * (blockDim.x / PER) + threadIdx.x / PER, j = threadIdx.x % PER;
+    const bool on = row < rows;
+    const int what = row < heads ? 0 : row < heads + A.n_kv ? 1 : 2;  // query, key, value (behind the last row: of no use)
     const int head = what == 0 ? row : row - heads - (what - 1) * A.n_kv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -85,11 +85,11 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const __grid_co
     float lo[4] = {}, hi[4] = {};
     if (live) {
         const float *src = what == 0 ? A.q + lane * A.q_stride : (what == 1 ? A.k : A.v) + lane * A.kv_stride;
-        src += head * A.hd + 4 * j;
-        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + A.hd / 2);
+        src += head * HD + 4 * j;
+        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + HD / 2);
         lo[0] = a.x, lo[1] = a.y, lo[2] = a.z, lo[3] = a.w, hi[0] = b.x, hi[1] = b.y, hi[2] = b.z, hi[3] = b.w;
         if (turned) {
-            const int64_t o = (int64_t)p * (A.hd / 2) + 4 * j;
+            const int64_t o = (int64_t)p * (HD / 2) + 4 * j;
             const float4 c4 = __ldg(reinterpret_cast<const float4 *>(A.cos_t + o));
             const float4 s4 = __ldg(reinterpret_cast<const float4 *>(A.sin_t + o));
             const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
@@ -102,9 +102,9 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const __grid_co
         }
     }
     if (on && what == 0) {
-        float *to = A.q_out + ((int64_t)lane * A.n_heads + head) * A.hd + 4 * j;
+        float *to = A.q_out + ((int64_t)lane * A.n_heads + head) * HD + 4 * j;
         *reinterpret_cast<float4 *>(to) = make_float4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<float4 *>(to + A.hd / 2) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<float4 *>(to + HD / 2) = make_float4(hi[0], hi[1], hi[2], hi[3]);
     }
     // (whole warps from here on: a row's threads are 8, 16 or 32 of one warp)
     const uint32_t bl = kv4_scale_byte(__fdiv_rn(top8(lo), 7.0f)), bh = kv4_scale_byte(__fdiv_rn(top8(hi), 7.0f));
@@ -115,10 +115,10 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const __grid_co
     const uint32_t word = odd ? other | h << 8 : l | other << 8;
     if (live && what > 0) {
         const int64_t r = place + (int64_t)head * A.kv.page_rows;
-        uint8_t *code = static_cast<uint8_t *>(what == 1 ? A.kv.k : A.kv.v) + r * (A.hd / 2);
-        uint8_t *sc = static_cast<uint8_t *>(what == 1 ? A.kv.k_scale : A.kv.v_scale) + r * (A.hd / kKv4Group);
-        *reinterpret_cast<uint32_t *>(code + (odd ? A.hd / 4 : 0) + (j >> 1) * 4) = word;
-        if ((j & 7) < 2) sc[(odd ? A.hd / 64 : 0) + (j >> 3)] = (uint8_t)(odd ? bh : bl);
+        uint8_t *code = static_cast<uint8_t *>(what == 1 ? A.kv.k : A.kv.v) + r * (HD / 2);
+        uint8_t *sc = static_cast<uint8_t *>(what == 1 ? A.kv.k_scale : A.kv.v_scale) + r * (HD / kKv4Group);
+        *reinterpret_cast<uint32_t *>(code + (odd ? HD / 4 : 0) + (j >> 1) * 4) = word;
+        if ((j & 7) < 2) sc[(odd ? HD / 64 : 0) + (j >> 3)] = (uint8_t)(odd ? bh : bl);
         if (!finite4(lo) || !finite4(hi)) raise_status(A.status, kStatusKv4NotFinite);
     }
 }
@@ -126,36 +126,50 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const __grid_co
 struct ReadArgs {
     qlin_kv4 kv;
     const int32_t *positions, *seqs;
-    int n_lanes, n_kv, hd;
+    int n_kv;
     float *k_out, *v_out;
     int32_t *status;
 };
 
-// a thread: a word of eight codes
+// Block x: a lane; y: its rows, the keys' and then the values'; a thread to a
+// word of eight codes.
+template <int PER>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const __grid_constant__ ReadArgs A) {
-    const int per = A.hd / 8;
-    const int64_t at = (int64_t)blockIdx.x * kKv4Threads + threadIdx.x;
-    if (at >= (int64_t)A.n_lanes * 2 * A.n_kv * per) return;
-    const int w = (int)(at % per), head = (int)(at / per % A.n_kv), which = (int)(at / per / A.n_kv % 2);
-    const int lane = (int)(at / per / A.n_kv / 2);
+    constexpr int HD = 8 * PER;
+    const int lane = blockIdx.x, row = blockIdx.y * (blockDim.x / PER) + threadIdx.x / PER, w = threadIdx.x % PER;
+    if (row >= 2 * A.n_kv) return;
+    const int which = row >= A.n_kv, head = row - which * A.n_kv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t place = kv4_row(A.kv, A.n_kv, A.positions[lane], A.seqs[lane]);
-    if (place == -2 && which == 0 && head == 0 && w == 0) raise_status(A.status, kStatusKv4Lane);
+    if (place == -2 && row == 0 && w == 0) raise_status(A.status, kStatusKv4Lane);
     float *to = which ? A.v_out : A.k_out;
     if (!to) return;
     float x[8] = {};
     if (place >= 0) {
         const int64_t r = place + (int64_t)head * A.kv.page_rows;
         const uint32_t word = *reinterpret_cast<const uint32_t *>(
-            static_cast<const uint8_t *>(which ? A.kv.v : A.kv.k) + r * (A.hd / 2) + 4 * w);
-        const float s = kv4_scale(static_cast<const uint8_t *>(which ? A.kv.v_scale : A.kv.k_scale)[r * (A.hd / kKv4Group) + w / 4]);
+            static_cast<const uint8_t *>(which ? A.kv.v : A.kv.k) + r * (HD / 2) + 4 * w);
+        const float s = kv4_scale(static_cast<const uint8_t *>(which ? A.kv.v_scale : A.kv.k_scale)[r * (HD / kKv4Group) + w / 4]);
 #pragma unroll
         for (int d = 0; d < 8; d++) x[d] = __fmul_rn((float)((int)(word >> (4 * (d >> 1) + 16 * (d & 1)) & 15u) - 8), s);
     }
-    to += ((int64_t)lane * A.n_kv + head) * A.hd + 8 * w;
+    to += ((int64_t)lane * A.n_kv + head) * HD + 8 * w;
     *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
     *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// The launch of one of the two, templated on the threads to a row, for `rows`
+// rows of every lane.
+template <typename Args>
+qlin_status launch_rows(const void *k8, const void *k16, const void *k32, const char *name, const Args &A, int n_lanes,
+                        int rows, int hd, cudaStream_t st) {
+    const int per = hd / 8, most = (rows * per + 31) / 32 * 32, threads = most < kKv4Threads ? most : kKv4Threads;
+    const int blocks = (rows + threads / per - 1) / (threads / per);
+    QLIN_REQUIRE(blocks <= 65535, QLIN_ERR_UNSUPPORTED, "%s: too many heads", name);
+    void *args[] = {(void *)&A};
+    return launch_pdl(per == 8 ? k8 : per == 16 ? k16 : k32, dim3((unsigned)n_lanes, (unsigned)blocks), dim3(threads), 0, st,
+                      args, name);
 }
 
 }  // namespace
@@ -188,14 +202,10 @@ qlin_status qlin_kv4_append(const qlin_kv4 *kv, const float *k, const float *v, 
                  (long long)kv_stride, (long long)q_stride);
     QLIN_REQUIRE(!q || q != q_out || q_stride == (int64_t)n_heads * head_dim, QLIN_ERR_INVALID_ARG,
                  "%s: in place with a q_stride of %lld", fn, (long long)q_stride);
-    AppendArgs A{*kv, k, v, q, kv_stride, q_stride, q_out, cos_t, sin_t, rope_rows, positions, seqs, n_lanes, n_heads,
-                 n_kv, head_dim, status_word};
-    const int64_t threads = (int64_t)n_lanes * ((q ? n_heads : 0) + 2 * n_kv) * (head_dim / 8);
-    const int64_t blocks = (threads + kKv4Threads - 1) / kKv4Threads;
-    QLIN_REQUIRE(blocks < (int64_t)1 << 31, QLIN_ERR_UNSUPPORTED, "%s: too many rows", fn);
-    void *args[] = {(void *)&A};
-    return launch_pdl((const void *)kv4_append_kernel, dim3((unsigned)blocks), dim3(kKv4Threads), 0, (cudaStream_t)stream,
-                      args, "kv4_append_kernel");
+    AppendArgs A{*kv, k, v, q, kv_stride, q_stride, q_out, cos_t, sin_t, rope_rows, positions, seqs, n_heads, n_kv, status_word};
+    return launch_rows((const void *)kv4_append_kernel<8>, (const void *)kv4_append_kernel<16>,
+                       (const void *)kv4_append_kernel<32>, "kv4_append_kernel", A, n_lanes, (q ? n_heads : 0) + 2 * n_kv,
+                       head_dim, (cudaStream_t)stream);
 }
 
 qlin_status qlin_kv4_read(const qlin_kv4 *kv, const int32_t *positions, const int32_t *seqs, int n_lanes, int n_kv,
@@ -209,12 +219,9 @@ qlin_status qlin_kv4_read(const qlin_kv4 *kv, const int32_t *positions, const in
                  fn, kKv4MaxRead, n_lanes);
     QLIN_REQUIRE(aligned16(k_out) && aligned16(v_out) && aligned4(positions) && aligned4(seqs) && aligned4(status_word),
                  QLIN_ERR_INVALID_ARG, "%s: a pointer is not 16-byte aligned (positions, seqs, status_word: 4)", fn);
-    ReadArgs A{*kv, positions, seqs, n_lanes, n_kv, head_dim, k_out, v_out, status_word};
-    const int64_t blocks = ((int64_t)n_lanes * 2 * n_kv * (head_dim / 8) + kKv4Threads - 1) / kKv4Threads;
-    QLIN_REQUIRE(blocks < (int64_t)1 << 31, QLIN_ERR_UNSUPPORTED, "%s: too many rows", fn);
-    void *args[] = {(void *)&A};
-    return launch_pdl((const void *)kv4_read_kernel, dim3((unsigned)blocks), dim3(kKv4Threads), 0, (cudaStream_t)stream, args,
-                      "kv4_read_kernel");
+    ReadArgs A{*kv, positions, seqs, n_kv, k_out, v_out, status_word};
+    return launch_rows((const void *)kv4_read_kernel<8>, (const void *)kv4_read_kernel<16>, (const void *)kv4_read_kernel<32>,
+                       "kv4_read_kernel", A, n_lanes, 2 * n_kv, head_dim, (cudaStream_t)stream);
 }
 
 }  // extern "C"
