@@ -117,6 +117,40 @@ def test_append_bit_exact(dev, H, G, hd, page, rotate, lanes):
     assert np.array_equal(out[:lanes], q) and (out[lanes] == 7.5).all()
 
 
+@pytest.mark.parametrize("H,G,hd,page", [(5, 1, 64, 16), (8, 2, 128, 32), (16, 4, 256, 64), (1, 1, 64, 256), (13, 13, 64, 16),
+                                         (4, 1, 256, 16)])
+@pytest.mark.parametrize("q", [True, False])
+def test_append_many_lanes(dev, H, G, hd, page, q):
+    """so many lanes that a thread takes several rows, numbers of rows that do not divide, padding, values that are not
+    finite, a position behind the tables"""
+    import torch
+
+    lanes, S = 1301, 7
+    rng = np.random.default_rng(H)
+    pool = Pool(dev, S, 260, G, hd, page)
+    seqs = np.arange(lanes) % S
+    pos = rng.permutation(250)[np.arange(lanes) // S]
+    pos[rng.random(lanes) < 0.1] = -1
+    r = Rows(dev, lanes, H, G, hd)
+    rope = _rope(dev, 249, hd)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    out = _append(pool, r, pos, seqs, rope, 249, q=q, status=status).cpu().numpy()
+    live = (pos >= 0) & (pos < 249)
+    codes, scales, want = _expect(pool, r, pos, seqs, rope, live)
+    assert int(status) == int((pos == 249).any())
+    assert np.array_equal(pool.d_scales.cpu().numpy(), scales)
+    assert np.array_equal(pool.d_codes.cpu().numpy(), codes)
+    if q:
+        assert np.array_equal(out[:lanes], want) and (out[lanes] == 7.5).all()
+    # a value of a key of the last lane that is not finite: its group's others are as without it
+    at = int(np.flatnonzero(live)[-1])
+    r.part("k")[at, (G - 1) * hd + 5] = np.inf
+    r.upload()
+    status.zero_()
+    _append(pool, r, np.where(np.arange(lanes) == at, pos, -1), seqs, None, 0, q=q, status=status)
+    assert int(status) == 4
+
+
 @pytest.mark.parametrize("hd", [64, 256])
 def test_append_every_scale_and_ties(dev, hd):
     """rows whose largest value walks over every scale, its neighbours included, and values half-way between codes"""

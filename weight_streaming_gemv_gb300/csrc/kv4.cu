@@ -64,62 +64,75 @@ __device__ __forceinline__ bool finite4(const float (&x)[4]) {
     return ok;
 }
 
-// Block x: a lane; y: its rows, PER threads to a head's row.  The rows of a
-// lane: the queries', then the keys', then the values'.
-template <int PER>
+// Block x: a lane; y: its rows, PER threads to a head's row and ROWS rows to
+// them, whose loads are on their way together.  The rows of a lane: the
+// queries', then the keys', then the values'.
+template <int PER, int ROWS>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const __grid_constant__ AppendArgs A) {
     constexpr int HD = 8 * PER;
-    const int heads = A.q ? A.n_heads : 0, rows = heads + 2 * A.n_kv, lane = blockIdx.x;
-    const int row = blockIdx.y * (blockDim.x / PER) + threadIdx.x / PER, j = threadIdx.x % PER;
-    const bool on = row < rows;
-    const int what = row < heads ? 0 : row < heads + A.n_kv ? 1 : 2;  // query, key, value (behind the last row: of no use)
-    const int head = what == 0 ? row : row - heads - (what - 1) * A.n_kv;
+    const int heads = A.q ? A.n_heads : 0, rows = heads + 2 * A.n_kv, lane = blockIdx.x, j = threadIdx.x % PER;
+    const int step = blockDim.x / PER, row0 = blockIdx.y * step * ROWS + threadIdx.x / PER;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int p = A.positions[lane];
-    const bool turned = A.cos_t && what < 2;
     int64_t place = kv4_row(A.kv, A.n_kv, p, A.seqs[lane]);
     if (place >= 0 && A.cos_t && p >= A.rope_rows) place = -2;
-    if (on && place == -2 && row == 0 && j == 0) raise_status(A.status, kStatusKv4Lane);
-    const bool live = on && place >= 0;
-    float lo[4] = {}, hi[4] = {};
+    const bool live = place >= 0;
+    if (place == -2 && row0 == 0 && j == 0) raise_status(A.status, kStatusKv4Lane);
+    float lo[ROWS][4] = {}, hi[ROWS][4] = {}, c[4] = {}, s[4] = {};
     if (live) {
-        const float *src = what == 0 ? A.q + lane * A.q_stride : (what == 1 ? A.k : A.v) + lane * A.kv_stride;
-        src += head * HD + 4 * j;
-        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + HD / 2);
-        lo[0] = a.x, lo[1] = a.y, lo[2] = a.z, lo[3] = a.w, hi[0] = b.x, hi[1] = b.y, hi[2] = b.z, hi[3] = b.w;
-        if (turned) {
+#pragma unroll
+        for (int i = 0; i < ROWS; i++) {
+            const int row = row0 + i * step, kv = row - heads, head = kv < 0 ? row : kv < A.n_kv ? kv : kv - A.n_kv;
+            if (row >= rows) continue;
+            const float *src = kv < 0 ? A.q + lane * A.q_stride : (kv < A.n_kv ? A.k : A.v) + lane * A.kv_stride;
+            src += head * HD + 4 * j;
+            const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + HD / 2);
+            lo[i][0] = a.x, lo[i][1] = a.y, lo[i][2] = a.z, lo[i][3] = a.w;
+            hi[i][0] = b.x, hi[i][1] = b.y, hi[i][2] = b.z, hi[i][3] = b.w;
+        }
+        if (A.cos_t && row0 < rows - A.n_kv) {
             const int64_t o = (int64_t)p * (HD / 2) + 4 * j;
             const float4 c4 = __ldg(reinterpret_cast<const float4 *>(A.cos_t + o));
             const float4 s4 = __ldg(reinterpret_cast<const float4 *>(A.sin_t + o));
-            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float x = lo[e], y = hi[e];
-                lo[e] = __fsub_rn(__fmul_rn(x, c[e]), __fmul_rn(y, s[e]));
-                hi[e] = __fadd_rn(__fmul_rn(x, s[e]), __fmul_rn(y, c[e]));
-            }
+            c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w, s[0] = s4.x, s[1] = s4.y, s[2] = s4.z, s[3] = s4.w;
         }
     }
-    if (on && what == 0) {
-        float *to = A.q_out + ((int64_t)lane * A.n_heads + head) * HD + 4 * j;
-        *reinterpret_cast<float4 *>(to) = make_float4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<float4 *>(to + HD / 2) = make_float4(hi[0], hi[1], hi[2], hi[3]);
-    }
-    // (whole warps from here on: a row's threads are 8, 16 or 32 of one warp)
-    const uint32_t bl = kv4_scale_byte(__fdiv_rn(top8(lo), 7.0f)), bh = kv4_scale_byte(__fdiv_rn(top8(hi), 7.0f));
-    const uint32_t l = code4(lo, kv4_scale(bl)), h = code4(hi, kv4_scale(bh));
-    // the even thread writes the low dims' word, the odd one the high dims'
-    const bool odd = j & 1;
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? l : h, 1);
-    const uint32_t word = odd ? other | h << 8 : l | other << 8;
-    if (live && what > 0) {
-        const int64_t r = place + (int64_t)head * A.kv.page_rows;
-        uint8_t *code = static_cast<uint8_t *>(what == 1 ? A.kv.k : A.kv.v) + r * (HD / 2);
-        uint8_t *sc = static_cast<uint8_t *>(what == 1 ? A.kv.k_scale : A.kv.v_scale) + r * (HD / kKv4Group);
-        *reinterpret_cast<uint32_t *>(code + (odd ? HD / 4 : 0) + (j >> 1) * 4) = word;
-        if ((j & 7) < 2) sc[(odd ? HD / 64 : 0) + (j >> 3)] = (uint8_t)(odd ? bh : bl);
-        if (!finite4(lo) || !finite4(hi)) raise_status(A.status, kStatusKv4NotFinite);
+#pragma unroll
+    for (int i = 0; i < ROWS; i++) {
+        const int row = row0 + i * step;
+        if (row0 + i * step - (int)threadIdx.x / PER >= rows) break;  // (nobody's row)
+        const int what = row < heads ? 0 : row < heads + A.n_kv ? 1 : 2;  // query, key, value (behind the last row: of no use)
+        const int head = what == 0 ? row : row - heads - (what - 1) * A.n_kv;
+        const bool on = row < rows;
+        if (live && A.cos_t && what < 2)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float x = lo[i][e], y = hi[i][e];
+                lo[i][e] = __fsub_rn(__fmul_rn(x, c[e]), __fmul_rn(y, s[e]));
+                hi[i][e] = __fadd_rn(__fmul_rn(x, s[e]), __fmul_rn(y, c[e]));
+            }
+        if (on && what == 0) {
+            float *to = A.q_out + ((int64_t)lane * A.n_heads + head) * HD + 4 * j;
+            *reinterpret_cast<float4 *>(to) = make_float4(lo[i][0], lo[i][1], lo[i][2], lo[i][3]);
+            *reinterpret_cast<float4 *>(to + HD / 2) = make_float4(hi[i][0], hi[i][1], hi[i][2], hi[i][3]);
+        }
+        if (!__any_sync(0xffffffffu, on && what > 0)) continue;
+        // (whole warps from here on: a row's threads are 8, 16 or 32 of one warp)
+        const uint32_t bl = kv4_scale_byte(__fdiv_rn(top8(lo[i]), 7.0f)), bh = kv4_scale_byte(__fdiv_rn(top8(hi[i]), 7.0f));
+        const uint32_t l = code4(lo[i], kv4_scale(bl)), h = code4(hi[i], kv4_scale(bh));
+        // the even thread writes the low dims' word, the odd one the high dims'
+        const bool odd = j & 1;
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? l : h, 1);
+        const uint32_t word = odd ? other | h << 8 : l | other << 8;
+        if (live && on && what > 0) {
+            const int64_t r = place + (int64_t)head * A.kv.page_rows;
+            uint8_t *code = static_cast<uint8_t *>(what == 1 ? A.kv.k : A.kv.v) + r * (HD / 2);
+            uint8_t *sc = static_cast<uint8_t *>(what == 1 ? A.kv.k_scale : A.kv.v_scale) + r * (HD / kKv4Group);
+            *reinterpret_cast<uint32_t *>(code + (odd ? HD / 4 : 0) + (j >> 1) * 4) = word;
+            if ((j & 7) < 2) sc[(odd ? HD / 64 : 0) + (j >> 3)] = (uint8_t)(odd ? bh : bl);
+            if (!finite4(lo[i]) || !finite4(hi[i])) raise_status(A.status, kStatusKv4NotFinite);
+        }
     }
 }
 
@@ -159,17 +172,24 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const __grid_cons
     *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// The launch of one of the two, templated on the threads to a row, for `rows`
-// rows of every lane.
+// The launch of one of the two for `rows` rows of every lane, `each` of them to
+// a thread; the kernel by the threads to a row.
 template <typename Args>
 qlin_status launch_rows(const void *k8, const void *k16, const void *k32, const char *name, const Args &A, int n_lanes,
-                        int rows, int hd, cudaStream_t st) {
-    const int per = hd / 8, most = (rows * per + 31) / 32 * 32, threads = most < kKv4Threads ? most : kKv4Threads;
-    const int blocks = (rows + threads / per - 1) / (threads / per);
+                        int rows, int each, int hd, cudaStream_t st) {
+    const int per = hd / 8, most = ((rows + each - 1) / each * per + 31) / 32 * 32;
+    const int threads = most < kKv4Threads ? most : kKv4Threads, block = threads / per * each;
+    const int blocks = (rows + block - 1) / block;
     QLIN_REQUIRE(blocks <= 65535, QLIN_ERR_UNSUPPORTED, "%s: too many heads", name);
     void *args[] = {(void *)&A};
     return launch_pdl(per == 8 ? k8 : per == 16 ? k16 : k32, dim3((unsigned)n_lanes, (unsigned)blocks), dim3(threads), 0, st,
                       args, name);
+}
+template <int ROWS>
+qlin_status launch_append(const AppendArgs &A, int n_lanes, int hd, cudaStream_t st) {
+    return launch_rows((const void *)kv4_append_kernel<8, ROWS>, (const void *)kv4_append_kernel<16, ROWS>,
+                       (const void *)kv4_append_kernel<32, ROWS>, "kv4_append_kernel", A, n_lanes,
+                       (A.q ? A.n_heads : 0) + 2 * A.n_kv, ROWS, hd, st);
 }
 
 }  // namespace
@@ -203,9 +223,8 @@ qlin_status qlin_kv4_append(const qlin_kv4 *kv, const float *k, const float *v, 
     QLIN_REQUIRE(!q || q != q_out || q_stride == (int64_t)n_heads * head_dim, QLIN_ERR_INVALID_ARG,
                  "%s: in place with a q_stride of %lld", fn, (long long)q_stride);
     AppendArgs A{*kv, k, v, q, kv_stride, q_stride, q_out, cos_t, sin_t, rope_rows, positions, seqs, n_heads, n_kv, status_word};
-    return launch_rows((const void *)kv4_append_kernel<8>, (const void *)kv4_append_kernel<16>,
-                       (const void *)kv4_append_kernel<32>, "kv4_append_kernel", A, n_lanes, (q ? n_heads : 0) + 2 * n_kv,
-                       head_dim, (cudaStream_t)stream);
+    return n_lanes <= 8 * sm_count() ? launch_append<1>(A, n_lanes, head_dim, (cudaStream_t)stream)
+                                     : launch_append<4>(A, n_lanes, head_dim, (cudaStream_t)stream);
 }
 
 qlin_status qlin_kv4_read(const qlin_kv4 *kv, const int32_t *positions, const int32_t *seqs, int n_lanes, int n_kv,
@@ -221,7 +240,7 @@ qlin_status qlin_kv4_read(const qlin_kv4 *kv, const int32_t *positions, const in
                  QLIN_ERR_INVALID_ARG, "%s: a pointer is not 16-byte aligned (positions, seqs, status_word: 4)", fn);
     ReadArgs A{*kv, positions, seqs, n_kv, k_out, v_out, status_word};
     return launch_rows((const void *)kv4_read_kernel<8>, (const void *)kv4_read_kernel<16>, (const void *)kv4_read_kernel<32>,
-                       "kv4_read_kernel", A, n_lanes, 2 * n_kv, head_dim, (cudaStream_t)stream);
+                       "kv4_read_kernel", A, n_lanes, 2 * n_kv, 1, head_dim, (cudaStream_t)stream);
 }
 
 }  // extern "C"
