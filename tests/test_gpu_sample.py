@@ -112,6 +112,33 @@ def test_rows_of_their_own_settings(dev):
     _compare(x, u, t, k, p, m, _run(dev, x, u, t, k, p, m))
 
 
+@pytest.mark.parametrize("V", [2100, 60000])
+def test_lists_of_any_length(dev, V):
+    """words left by top-k about the numbers at which a list, and a sort of it, is full"""
+    rng = np.random.default_rng(V)
+    k = np.array([127, 128, 129, 900, 1023, 1024, 1025, 1500, 1990, 2030, 2047, 2048, 2049, 2060, 2099, 2100, 3000] * 2)
+    R = len(k)
+    x, u = rng.standard_normal((R, V)) * rng.choice([1.0, 3.0], (R, 1)), rng.random(R)
+    p, m = rng.choice([1.0, 0.9, 0.99], R), rng.choice([0.0, 0.0, 1e-3], R)
+    t = rng.choice([0.8, 1.5], R)
+    _compare(x, u, t, k, p, m, _run(dev, x, u, t, k, p, m))
+
+
+@pytest.mark.parametrize("V", [500, 30000, 262144])
+def test_min_p_next_to_top_p(dev, V):
+    """min-p's border well before top-p's, well behind it, and next to it"""
+    rng = np.random.default_rng(V)
+    R = 60 if V < 100000 else 16
+    x, u = rng.standard_normal((R, V)) * 3, rng.random(R)
+    t, p = rng.uniform(0.5, 2.0, R), rng.uniform(0.3, 1.0, R)
+    m = np.exp(rng.uniform(np.log(1e-6), 0.0, R))
+    for i in range(0, R, 3):  # as much as the last word that top-p keeps weighs, and a little more or less
+        w = np.sort(np.exp((np.float32(x[i]).astype(np.float64) - np.float32(x[i]).max()) / np.float32(t[i])))[::-1]
+        at = min(V - 1, int(np.searchsorted(np.cumsum(w), np.float32(p[i]) * w.sum())))
+        m[i] = w[at] * rng.choice([1.0 - 1e-3, 1.0 - 1e-6, 1.0 + 1e-6, 1.0 + 1e-3, 1.02, 0.98])
+    _compare(x, u, t, None, p, m, _run(dev, x, u, t, None, p, m), most=0.05)
+
+
 @pytest.mark.parametrize("V", [7, 3000, 50000, 262144])
 @pytest.mark.parametrize("levels", [1, 2, 5])
 def test_equal_logits(dev, V, levels):

@@ -223,7 +223,11 @@ qlin_status qlin_kv4_append(const qlin_kv4 *kv, const float *k, const float *v, 
     QLIN_REQUIRE(!q || q != q_out || q_stride == (int64_t)n_heads * head_dim, QLIN_ERR_INVALID_ARG,
                  "%s: in place with a q_stride of %lld", fn, (long long)q_stride);
     AppendArgs A{*kv, k, v, q, kv_stride, q_stride, q_out, cos_t, sin_t, rope_rows, positions, seqs, n_heads, n_kv, status_word};
-    return n_lanes <= 8 * sm_count() ? launch_append<1>(A, n_lanes, head_dim, (cudaStream_t)stream)
+    // One row to a thread where there are few lanes, for the shorter way, and four where there are many, for more loads
+    // in flight.  us with one / with four: 8 + 2 + 2 heads of 128, 64 lanes 2.7 / 2.9, 608 3.2 / 3.3, 1216 4.1 / 3.9, 2432
+    // 6.8 / 5.3, 4864 12.5 / 10.1; 16 + 16 + 16 heads of 128, 64 lanes 3.0 / 4.8, 608 7.4 / 7.5, 1216 13.6 / 12.9, 4864
+    // 49 / 45.
+    return n_lanes <= 4 * sm_count() ? launch_append<1>(A, n_lanes, head_dim, (cudaStream_t)stream)
                                      : launch_append<4>(A, n_lanes, head_dim, (cudaStream_t)stream);
 }
 

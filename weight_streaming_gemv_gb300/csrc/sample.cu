@@ -43,7 +43,7 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kList = 1024;
+constexpr int kList = 2048, kEach = kList / kThreads;  // words of the list, and of a thread
 constexpr int kMaxCluster = 16;
 constexpr int kCached = 16384;  // words of a CTA in shared memory, so that an SM has room for two CTAs
 constexpr int kPacked = 16384;  // a CTA's words up to which a bin's numbers share 32 bits
@@ -635,8 +635,8 @@ struct Row {
                     __syncthreads();
                 else
                     __syncwarp();
-                if (tid < P / 2) {
-                    const int a = ((tid & ~(j - 1)) << 1) | (tid & (j - 1)), b = a | j;
+                for (int t = tid; t < P / 2; t += kThreads) {
+                    const int a = ((t & ~(j - 1)) << 1) | (t & (j - 1)), b = a | j;
                     const u64 x = w[a], y = w[b];
                     if ((x < y) == ((a & k) == 0)) w[a] = y, w[b] = x;
                 }
@@ -651,31 +651,42 @@ struct Row {
     }
     // The weights of the sorted list's first `n` words, and the sums up to and with each, in S.list.mass.
     __device__ __forceinline__ u64 sums_of_list(int n) {
-        const int e = 2 * threadIdx.x;
-        u64 w[2], total;
+        const int e = kEach * threadIdx.x;
+        u64 w[kEach] = {}, mine = 0, total;
+        if (kEach * (threadIdx.x & ~31) < n)  // (whole warps)
 #pragma unroll
-        for (int q = 0; q < 2; q++) w[q] = weight(e + q < n ? of_key((uint32_t)(S.list.word[e + q] >> 32)) : -kInf, e + q < n);
-        const u64 at = before(w[0] + w[1], total);
-        S.list.mass[e] = at + w[0], S.list.mass[e + 1] = at + w[0] + w[1];
+            for (int q = 0; q < kEach; q++) {
+                w[q] = weight(e + q < n ? of_key((uint32_t)(S.list.word[e + q] >> 32)) : -kInf, e + q < n);
+                mine += w[q];
+            }
+        u64 at = before(mine, total);
+#pragma unroll
+        for (int q = 0; q < kEach; q++) S.list.mass[e + q] = at += w[q];
         __syncthreads();
         return total;
     }
     // how many of the list's first n sums are below target
     __device__ __forceinline__ int below(int n, u64 target) {
-        const int e = 2 * threadIdx.x;
-        u64 total;
-        before((u64)((e < n && S.list.mass[e] < target) + (e + 1 < n && S.list.mass[e + 1] < target)), total);
+        const int e = kEach * threadIdx.x;
+        u64 mine = 0, total;
+#pragma unroll
+        for (int q = 0; q < kEach; q++) mine += e + q < n && S.list.mass[e + q] < target;
+        before(mine, total);
         return (int)total;
     }
 
     // ---------------------------------------------------------------- the parts of a row
-    // min-p's cut
-    __device__ __forceinline__ void cut_min_p(float min_p) {
-        if (!(min_p > 0.0f) || ch == 0.0f) return;  // (at an infinite temperature all weigh the same)
+    // the least logit that min-p keeps
+    __device__ __forceinline__ float floor_of(float min_p) const {
+        if (!(min_p > 0.0f) || ch == 0.0f) return -kInf;  // (at an infinite temperature all weigh the same)
         const double t = (double)M + S.thr;
         float x = (float)t;
         if ((double)x < t) x = nextafterf(x, kInf);
-        const uint32_t k = key_of(fminf(x, M));
+        return fminf(x, M);
+    }
+    // min-p's cut
+    __device__ __forceinline__ void cut_min_p(float min_p) {
+        const uint32_t k = key_of(floor_of(min_p));
         if (k > kt) kt = k, it = 0xffffffffu;
     }
     // kt and it from the place in the first CTA's list behind which it is cut, on every CTA; a place below 0: not there
@@ -762,40 +773,43 @@ struct Row {
         }
         cut_min_p(min_p);
         if (min_p > 0.0f) {
-            u64 many;
-            const int e = 2 * threadIdx.x;
-            auto kept = [&](int q) {
-                const u64 w = q < n ? S.list.word[q] : 0;
-                return q < n && keeps((uint32_t)(w >> 32), (uint32_t)~w);
-            };
-            before((u64)(kept(e) + kept(e + 1)), many);
+            u64 mine = 0, many;
+#pragma unroll
+            for (int q = 0; q < kEach; q++) {
+                const int at = kEach * threadIdx.x + q;
+                const u64 w = at < n ? S.list.word[at] : 0;
+                mine += at < n && keeps((uint32_t)(w >> 32), (uint32_t)~w);
+            }
+            before(mine, many);
             n = (int)many;
         }
         const u64 sum = S.list.mass[n - 1], target = min(times(sum, u, exact), sum - 1);
         // the words that are left in the order of their numbers: ~number << 32 | place
-        const int e = 2 * threadIdx.x;
+        const int e = kEach * threadIdx.x;
         u64 *const order = S.list.word;
-        u64 o[2] = {0, 0};
+        u64 o[kEach];
 #pragma unroll
-        for (int q = 0; q < 2; q++)
-            if (e + q < n) o[q] = S.list.word[e + q] << 32 | (uint32_t)(e + q);
+        for (int q = 0; q < kEach; q++) o[q] = e + q < n ? S.list.word[e + q] << 32 | (uint32_t)(e + q) : 0;
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 2; q++)
+        for (int q = 0; q < kEach; q++)
             if (e + q < n) order[e + q] = o[q];
         sort(order, n);
-        u64 w[2] = {0, 0};
+        u64 mine = 0;
 #pragma unroll
-        for (int q = 0; q < 2; q++)
+        for (int q = 0; q < kEach; q++) {
+            o[q] = 0;  // (the word's weight)
             if (e + q < n) {
                 const int at = (int)(uint32_t)order[e + q];
-                w[q] = S.list.mass[at] - (at ? S.list.mass[at - 1] : 0);
+                o[q] = S.list.mass[at] - (at ? S.list.mass[at - 1] : 0);
             }
-        u64 at = before(w[0] + w[1], total);
+            mine += o[q];
+        }
+        u64 at = before(mine, total);
 #pragma unroll
-        for (int q = 0; q < 2; q++) {
-            if (at <= target && target < at + w[q]) S.found[0] = (uint32_t)~(uint32_t)(order[e + q] >> 32);
-            at += w[q];
+        for (int q = 0; q < kEach; q++) {
+            if (at <= target && target < at + o[q]) S.found[0] = (uint32_t)~(uint32_t)(order[e + q] >> 32);
+            at += o[q];
         }
         __syncthreads();
         write(row, (int64_t)S.found[0], __ldg(from + S.found[0]), sum, (u64)n);  // (the first CTA's words are the row's)
@@ -904,8 +918,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (by_p) {
         R.count_by_y();
         const Row::Border c = R.find_border(0, p);
-        bool done = false;
-        if (c.between <= kList) {
+        const float floor_x = R.floor_of(min_p);
+        // (where min-p keeps words of bins before the border's only, top-p takes none of them)
+        bool done = floor_x > -kInf && R.bin_of(R.y_of(floor_x)) < c.lo;
+        if (!done && c.between <= kList) {
             // the exact weights of the words before the list's, and of all
             Row::Sum before, all;
             u64 total, ahead;
@@ -939,8 +955,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             done = R.cut_at(place);
             if (done) {
                 // the warps' sums of what is left: the words before, and those of the CTA's own in the list
-                const float floor_x = min_p > 0.0f ? (float)((double)M + S.thr) : -kInf;
-                summed = !(min_p > 0.0f) || !(R.y_of(floor_x) < ((float)c.hi + 1.0f) / kBinsPer);
+                summed = floor_x == -kInf || R.bin_of(R.y_of(floor_x)) > c.hi;
                 if (summed) {
                     const int run = R.run_length(), own_n = (int)S.n_mine;
                     __syncthreads();
