@@ -20,9 +20,9 @@
 // operations have no immediate operands, and their constants no registers left.)
 //
 // One cluster of CTAs per row, whose shared memory holds the row: it is read
-// once.  A histogram of 2048 bins over y counts the words and adds up an eighth
-// of a bin's width each lies above its border, which gives a bin's weight to
-// about 10^-4; a CTA sums a share of the bins over the cluster's.  So top-k's
+// once.  A histogram of 2048 bins over y counts the words and adds up how many
+// parts of a bin's width each lies above its border, which gives a bin's weight
+// to 10^-4 or so; a CTA sums a share of the bins over the cluster's.  So top-k's
 // border is known to a bin and top-p's to one or two.  Their words go to a list
 // in the first CTA, which sorts it, while every thread adds up the exact weights
 // of the words before them (and of all) in registers; the border is then a place
@@ -56,7 +56,8 @@ constexpr int kMagicBits = 0x4B400000;
 constexpr float kMagicHi = 50331648.0f, kMagicLo = 12.0f;    // 1.5 * 2^25 and 1.5 * 2^3: to fours, and to 2^-20
 constexpr int kMagicHiBits = 0x4C400000, kMagicLoBits = 0x41400000;
 constexpr float kBinsPer = 1.375f;           // bins to a unit of y
-constexpr float kNear = 1e-4f;               // how far the bins' weights may be off, as a part of the sum
+constexpr float kNear = 3e-5f;               // how far the bins' weights may be off as a part of the sum, by a bin's width
+constexpr float kBinPart = 0.69314718f / (kPart * kBinsPer);  // and a word's per bin that its y is off
 
 struct SampleArgs {
     const float *logits;
@@ -450,7 +451,11 @@ struct Row {
         return r;
     }
     // The bins of the words as they are counted by count_by_y: lo and hi, between which top-k's border (k > 0) or top-p's
-    // must be, and the words up to hi and between.  A count is exact, a weight an estimate.
+    // must be, and the words up to hi and between.  A count is exact, a weight an estimate: a word's y is known to a part
+    // of a bin, 1 / parts(), so a word's weight is off by kBinPart of that at most, half of it for most, each by its own.
+    // The sums are off by that share of the sum at most, and seldom by three deviations or more: by it times the root of
+    // the sum of the squares.  (Few heavy words make the latter large, many like ones small.  Where the border is not
+    // between lo and hi after all, the list does not hold it, and exact weights find it.)
     struct Border {
         int lo, hi;
         uint32_t upto, between;
@@ -460,7 +465,8 @@ struct Row {
         const int each = max(1, per / kThreads), share = max(1, kThreads / per), sub = tid & (share - 1);
         cluster_sync();
         u64 c[4], cs = 0;
-        float m[4], ms = 0.0f;
+        float m[4], squares = 0.0f;
+        const float part = 1.0f / (float)parts();
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             m[q] = 0.0f, c[q] = 0;
@@ -481,26 +487,30 @@ struct Row {
                 n += __shfl_xor_sync(0xffffffffu, n, off), f += __shfl_xor_sync(0xffffffffu, f, off);
             if (sub || !n) continue;
             c[q] = n, cs += n;
-            // (the words' mean y: they lie f / 8 of a bin above its lower border on average)
-            if (b < kBins - 1)
-                m[q] = (float)n * exp2f(-((float)b - 0.5f + __fdiv_rn((float)f, (float)n) * 0.125f) / (kBinsPer * kPart));
-            ms += m[q];
+            // (the words' mean y: they lie f / n parts of a bin above its lower border on average)
+            if (b == kBins - 1 || k) continue;  // (no weight; nobody asks)
+            m[q] = (float)n * exp2f(-((float)b - 0.5f + __fdiv_rn((float)f, (float)n) * part) / (kBinsPer * kPart));
+            squares += __fdiv_rn(m[q] * m[q], (float)n);
         }
         u64 ct;
         u64 cb = before(cs, ct);
-        // weights as whole numbers of 2^-20 of the largest, so that every CTA adds up the same
-        u64 mt, m64[4], mo = 0;
+        // weights as whole numbers of 2^-32 of the largest, so that every CTA adds up the same; the squares of 2^-14
+        u64 m64[4], mo = 0, mb = 0, mt = 0, sq = 0;
 #pragma unroll
-        for (int q = 0; q < 4; q++) m64[q] = (u64)(m[q] * 1048576.0f), mo += m64[q];
-        u64 mb = before(mo, mt);
-        tell(mt, ct);
+        for (int q = 0; q < 4; q++) m64[q] = (u64)(m[q] * 4294967296.0f), mo += m64[q];
+        if (!k) mb = before(mo, mt), before((u64)(squares * 16384.0f), sq);
+        constexpr u64 kCount = (1 << 25) - 1;
+        tell(mt, sq << 25 | ct);
         u64 mall = 0, call = 0;
+        sq = 0;
         for (int q = 0; q < C; q++) {
-            if (q < rank) mb += told(0, q), cb += told(1, q);
-            mall += told(0, q), call += told(1, q);
+            const u64 n = told(1, q) & kCount;
+            if (q < rank) mb += told(0, q), cb += n;
+            mall += told(0, q), call += n, sq += told(1, q) >> 25;
         }
         k = min(k, call);
-        const float want = p * (float)mall, off = kNear * (float)mall + 1.0f;
+        const float want = p * (float)mall, unit = kBinPart * part;
+        const float off = kNear * (float)mall + unit * fminf((float)mall, 33554432.0f * sqrtf((float)sq));
         const u64 lo_t = k ? k : (u64)fmaxf(want - off, 1.0f), hi_t = k ? k : min(mall, (u64)(want + off));
         if (tid < 4) S.found[tid] = 0;
         __syncthreads();
@@ -530,8 +540,9 @@ struct Row {
         }
         __syncthreads();
     }
-    // The kept words by y: a bin's count and eighths of a bin, in 15 and 17 bits of a word where the CTA's words cannot
-    // exceed those, else in 32 each.
+    // The kept words by y: a bin's count and how many parts of a bin each word lies in it.  Eighths, in 15 and 17 bits of
+    // a word, where the CTA's words cannot exceed those, else sixty-fourths, in 32 bits each.
+    __device__ __forceinline__ int parts() const { return A.slice <= kPacked ? 8 : 64; }
     template <bool PACKED>
     __device__ __forceinline__ void count_by_y() {
         clear_hist<!PACKED, PACKED>();
@@ -547,10 +558,11 @@ struct Row {
                     rest += on;  // (those of no weight, which may be most)
                     continue;
                 }
-                // the nearest eighth of the bin that bin_of rounds to
-                const int z8 = __float_as_int(__fmaf_rn(y, 8.0f * kBinsPer, kMagic + 4.0f)) - kMagicBits;
+                // the nearest part of the bin that bin_of rounds to
+                constexpr int kParts = PACKED ? 8 : 64;
+                const int z = __float_as_int(__fmaf_rn(y, kParts * kBinsPer, kMagic + kParts / 2)) - kMagicBits;
                 const int b = bin_of(y);
-                const uint32_t f = (uint32_t)min(7, max(0, z8 - 8 * b));
+                const uint32_t f = (uint32_t)min(kParts - 1, max(0, z - kParts * b));
                 if (PACKED) {
                     atomicAdd(&S.hist.count[b], (1u << 17) + f);
                 } else {
