@@ -942,9 +942,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 const int b = R.bin_of(y);
                 all.add(weighs, q, r);
                 before.add(weighs && b < c.lo, q, r);
-                ahead_n += weighs && b < c.lo;
-                if (weighs && b >= c.lo && b <= c.hi) R.enlist(key_of(x), i);
-            }, [&]() { all.flush(), before.flush(); });
+                if (weighs && (uint32_t)(b - c.lo) <= (uint32_t)(c.hi - c.lo)) R.enlist(key_of(x), i);
+            }, [&]() { all.flush(), ahead_n += before.n, before.flush(); });
             cluster_sync();
             const u64 ahead_w = warp_sum(before.all);
             if (lane == 0) S.certain[warp] = ahead_w;
