@@ -139,6 +139,23 @@ def test_min_p_next_to_top_p(dev, V):
     _compare(x, u, t, None, p, m, _run(dev, x, u, t, None, p, m), most=0.05)
 
 
+def test_min_p_just_behind_top_p(dev):
+    """min-p's border one word or a few behind top-p's, where 6000 equal words are half of the sum: what a histogram says of
+    their weight is off by as much for each"""
+    rng = np.random.default_rng(11)
+    R, V, n = 36, 131072, 6000
+    for _ in range(8):
+        x = -np.log(rng.uniform(np.exp(6.0), np.exp(10.0), (R, V)))  # as much weight in every part of the range
+        x[:, :n] = np.log(np.exp(x[:, n:]).sum(1, keepdims=True) / n) + rng.uniform(0.0, 0.05, (R, 1))
+        x[:, n] = x[:, 0] + rng.uniform(0.2, 0.4, R)
+        x = x[:, rng.permutation(V)]
+        u, p, m = rng.random(R), rng.uniform(0.53, 0.7, R), np.zeros(R)
+        for i in range(R):
+            w = np.sort(np.exp(np.float32(x[i]).astype(np.float64) - np.float32(x[i]).max()))[::-1]
+            m[i] = w[int(np.searchsorted(np.cumsum(w), np.float32(p[i]) * w.sum())) + 1 + i % 3]
+        _compare(x, u, None, None, p, m, _run(dev, x, u, None, None, p, m), most=0.03)
+
+
 @pytest.mark.parametrize("V", [7, 3000, 50000, 262144])
 @pytest.mark.parametrize("levels", [1, 2, 5])
 def test_equal_logits(dev, V, levels):

@@ -7,6 +7,11 @@
 //   o = sum_j w_j v_j,  w = softmax_j(q . k_j / sqrt(head_dim)),
 // zeros where no key is seen.
 //
+// A softmax over keys in any order: with m a number no smaller than some score,
+// weights 2^(s_j - m) (s in units of log(2), the factor log2(e) / sqrt(head_dim)
+// goes into the queries), their sum l and the sum of w_j v_j; parts of the keys
+// are joined by 2^(m_part - m).  Little work goes to CUDA cores (below), the
+// rest to the tensor cores (further down); few_fits tells them apart.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -78,6 +83,16 @@ struct FewCfg {
     }
 };
 
+// Little work: a CTA takes up to 64 or 128 of a lane's keys for one KV head and
+// up to eight of its query heads.  Scores: the threads of a key share its dims,
+// each decoding its 16 bytes at a time for all heads at once; outputs: a thread
+// per word of eight dims and group of keys.  Decoding is in fp16 (exact), the
+// rest in fp32.  Latency bounds it: the copy of the rows, one pass for the
+// scores, one for the outputs, and the merge.  Where the CTAs of a (lane, head
+// block) fit one cluster they merge through each other's shared memory, so that
+// there is one launch: a call for one token of 4 heads on one KV head of 256 and
+// 1024 keys takes 8.6 us, and 12.9 with the merge as a launch of its own.
+//
 // grid (splits, KV heads x blocks of GH query heads, lanes); span: keys of a
 // CTA.  CL: the CTAs of a (lane, head block) are one cluster and merge among
 // themselves.
@@ -323,6 +338,40 @@ __global__ void __launch_bounds__(kThreads) kv4_few_merge_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ the product
+// A tile is up to 32 rows (the query heads of one KV head, of lanes of one
+// sequence on end); the tiles' chunks of 128 keys are dealt to one CTA per SM in
+// equal runs, a run's parts of a tile joined by a merging launch: the plan and
+// its order are attention_lanes.cuh's.  Per chunk
+//   S^T [128 keys x rows] = K [128 x hd] q^T,   O^T [hd x rows] += V^T [hd x 128] P^T
+// with the codes decoded to fp16, which is exact: an fp16 has 11 bits and the
+// range of every code times its scale.  Queries and weights are two fp16 terms
+// each (22 bits; a row's queries times a power of two that puts the largest at
+// 2^13 .. 2^14), side by side as columns of one operand, so that the products
+// are good to fp32's rounding.  The keys are the products' rows because there
+// are 128 of them and few queries: the decoded operand is then the A of both, K
+// from tensor memory (written straight from registers) and V from shared memory
+// with the keys as its rows.
+//
+// Roles: one warp walks over the plan, one looks up pages and copies codes and
+// scales (2-D tensor copies, a page at a time, with the copy engine's swizzle),
+// 16 warps decode, a thread issues the MMAs, two warpgroups turn S^T into
+// weights and add up O^T, which is taken out of tensor memory after every chunk.
+// With up to 16 rows the warpgroups take the chunks in turn, each with running
+// maxima and outputs of its own, joined at the end of a tile; with more they
+// share the rows.  A maximum is only raised when a score exceeds it by kStale.
+//
+// Measured (4 query heads on one KV head of 256 unless said): 64 lanes of up to
+// 8192 keys 51 us for 106 MB of cache, 2.1 TB/s; 16 lanes of up to 32768 keys,
+// 8 heads on each of two of 128, 61 us for 111 MB; 64 lanes with a window of 1024
+// 25 us; two prompts of 1024 lanes with that window 73 us.  A chunk takes some
+// 3300 cycles, of which DRAM is busy 27% and the tensor cores 12%: the decoding
+// threads' instructions (58% of the issue slots, 7 us of the 51 without the
+// arithmetic) and the hand-overs from step to step bound it.  Around that a
+// start of 4 us, 5 us where a CTA goes from one tile to the next, and the merge
+// of 4 us, which is most of the window's 25.  Taken back after timing: the
+// decode with a packed add and multiply in place of three of the shifts (6 us
+// more), K's and V's slices by all producers in one order (slower), the next
+// tile's queries loaded under the last products (1 us more).
 constexpr int kR = 32;                // rows of a tile at most
 constexpr int kProd = 16;             // producer warps, in groups of four
 constexpr int kProd0 = 8;             // behind two warpgroups of the weights

@@ -8,7 +8,9 @@
 // least number (8 + m) 2^(e-24) that is at least max|x'| / 7.
 //
 // Everything is read once and written once, so memory bounds it, and a launch
-// where there is little.  A thread takes four dims i .. i+3 and their partners
+// where there is little: 4096 lanes of 8 + 2 + 2 heads of 128 take 10.4 us (47
+// MB, in good part in L2) and the reading back 4.6; one lane 2.6 and 1.7.  A
+// thread takes four dims i .. i+3 and their partners
 // i+h .. i+h+3, so that a rotation needs no other thread and may be in place;
 // the eight threads of four low dims each are the 32 of one scale, as are their
 // eight partners, and two neighbours' codes make a word.

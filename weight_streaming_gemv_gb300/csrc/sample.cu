@@ -29,7 +29,15 @@
 // in the list.  Where all words up to the border fit the list the first CTA does
 // the rest alone.  Where a list does not hold the border (many equal logits, a
 // top_p next to 1) a histogram of exact weights, and more of them over the bits
-// of the logits of one bin, narrow it down.
+// of the logits of one bin, narrow it down.  A min-p border before top-p's ends
+// the search for that.
+//
+// Instructions bound it, not memory: 64 rows of 262144 words with a top_p of 0.9
+// take 106 us for 67 MB; of the 130 warp instructions to 32 words the exact
+// weights are about half and the counting, whose shared-memory additions collide
+// (8 cycles each), a quarter.  256 rows of 32000 with no bound, one pass, take 30
+// us; one row of 262144 with a top_k of 64, 16.8 us, most of it waiting: the
+// cluster's meetings (some 1200 cycles each), the border, the sorted list.
 #include <cmath>
 
 #include "launch.cuh"
@@ -453,14 +461,14 @@ struct Row {
     // The bins of the words as they are counted by count_by_y: lo and hi, between which top-k's border (k > 0) or top-p's
     // must be, and the words up to hi and between.  A count is exact, a weight an estimate: a word's y is known to a part
     // of a bin, 1 / parts(), so a word's weight is off by kBinPart of that at most, half of it for most, each by its own.
-    // The sums are off by that share of the sum at most, and seldom by three deviations or more: by it times the root of
-    // the sum of the squares.  (Few heavy words make the latter large, many like ones small.  Where the border is not
-    // between lo and hi after all, the list does not hold it, and exact weights find it.)
+    // The sums are off by that share of the sum at most (sure), and seldom by three deviations or more: by it times the
+    // root of the sum of the squares.  (Few heavy words make the latter large, many like ones small.  Where the border is
+    // not between lo and hi after all, the list does not hold it, and exact weights find it.)
     struct Border {
         int lo, hi;
         uint32_t upto, between;
     };
-    __device__ __forceinline__ Border find_border(u64 k, float p) {
+    __device__ __forceinline__ Border find_border(u64 k, float p, bool sure) {
         const int tid = threadIdx.x, C = A.cluster, per = kBins / C, b0 = rank * per;
         const int each = max(1, per / kThreads), share = max(1, kThreads / per), sub = tid & (share - 1);
         cluster_sync();
@@ -510,7 +518,7 @@ struct Row {
         }
         k = min(k, call);
         const float want = p * (float)mall, unit = kBinPart * part;
-        const float off = kNear * (float)mall + unit * fminf((float)mall, 33554432.0f * sqrtf((float)sq));
+        const float off = kNear * (float)mall + unit * fminf((float)mall, sure ? kInf : 33554432.0f * sqrtf((float)sq));
         const u64 lo_t = k ? k : (u64)fmaxf(want - off, 1.0f), hi_t = k ? k : min(mall, (u64)(want + off));
         if (tid < 4) S.found[tid] = 0;
         __syncthreads();
@@ -914,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const bool by_k = k > 0 && k < A.vocab, by_p = p < 1.0f;
     if (by_k) {
         R.count_by_y();
-        const Row::Border c = R.find_border((u64)k, 0.0f);
+        const Row::Border c = R.find_border((u64)k, 0.0f, true);
         auto bin = [&](float x) { return R.bin_of(R.y_of(x)); };
         if (c.upto <= kList) {
             R.gather([&](uint32_t, float x) { return bin(x) <= c.hi; });
@@ -929,8 +937,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     bool summed = false;  // S.scan holds the warps' sums of what is left, many the CTA's words
     if (by_p) {
         R.count_by_y();
-        const Row::Border c = R.find_border(0, p);
         const float floor_x = R.floor_of(min_p);
+        const Row::Border c = R.find_border(0, p, floor_x > -kInf);
         // (where min-p keeps words of bins before the border's only, top-p takes none of them)
         bool done = floor_x > -kInf && R.bin_of(R.y_of(floor_x)) < c.lo;
         if (!done && c.between <= kList) {
@@ -1031,8 +1039,8 @@ qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u,
     SampleArgs A{logits, row_stride, u, temperature, top_k, top_p, min_p, vocab, tokens, probs, kept};
     const void *kern = (const void *)sample_kernel;
     // As many CTAs to a row as give two to every SM, for no fewer than 4096 words each.  (Rows past what the cluster's
-    // shared memory holds come from L2 again in every pass: 64 rows of 262144 words take 85 us by fours and 200 by
-    // sixteens, of which 11 run at a time, one after the other.)
+    // shared memory holds come from L2 again in every pass: 64 rows of 262144 words take 106 us by fours and 200
+    // by sixteens, of which 11 run at a time, one after the other.)
     int c = 1;
     while (c < kMaxCluster && (int64_t)n_rows * c * 2 <= 2 * sm_count() && vocab / c > 4096) c *= 2;
     size_t smem = 0;

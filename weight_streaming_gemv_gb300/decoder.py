@@ -295,7 +295,7 @@ class T158Decoder:
         wants = ((u, torch.float32), (tokens, torch.int32), (temperature, torch.float32), (top_k, torch.int32),
                  (top_p, torch.float32), (min_p, torch.float32), (probs, torch.float32), (kept, torch.int32))
         for t, kind in wants:
-            if t is not None and (t.dtype != kind or t.numel() < rows or not t.is_contiguous()):
-                raise ValueError(f"sample: a tensor of {t.dtype} {tuple(t.shape)} for {rows} rows of {kind}")
-        qlin.qlin_sample(logits, logits.stride(0) if rows > 1 else vocab, u, temperature, top_k, top_p, min_p, rows, vocab, tokens, probs, kept,
-                         stream)
+            if t is not None and (t.dtype != kind or t.numel() < rows or not t.is_contiguous() or t.device != logits.device):
+                raise ValueError(f"sample: a tensor of {t.dtype} {tuple(t.shape)} on {t.device} for {rows} rows of {kind}")
+        qlin.qlin_sample(logits, logits.stride(0) if rows > 1 else vocab, u, temperature, top_k, top_p, min_p, rows, vocab,
+                         tokens, probs, kept, stream)
