@@ -203,11 +203,13 @@ def _check(fn: str, s: int):
 
 def _ptr(t):
     """Device/host address of a torch tensor or numpy array; ints pass through; None is NULL."""
-    address = getattr(t, "data_ptr", None)
-    if address is not None:
-        return address()
     if t is None:
         return None
+    if type(t) is not int:
+        try:  # (looking data_ptr up first: 0.16 us a tensor against 0.11, of nine in a call of 5)
+            return t.data_ptr()
+        except AttributeError:
+            pass
     if isinstance(t, np.ndarray):
         return t.ctypes.data
     if isinstance(t, int):
