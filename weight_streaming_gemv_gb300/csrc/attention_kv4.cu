@@ -361,9 +361,9 @@ __global__ void __launch_bounds__(kThreads) kv4_few_merge_kernel(const __grid_co
 // share the rows.  A maximum is only raised when a score exceeds it by kStale.
 //
 // Measured (4 query heads on one KV head of 256 unless said): 64 lanes of up to
-// 8192 keys 51 us for 106 MB of cache, 2.1 TB/s; 16 lanes of up to 32768 keys,
+// 8192 keys 50 us for 106 MB of cache, 2.1 TB/s; 16 lanes of up to 32768 keys,
 // 8 heads on each of two of 128, 61 us for 111 MB; 64 lanes with a window of 1024
-// 25 us; two prompts of 1024 lanes with that window 73 us.  A chunk takes some
+// 25 us; two prompts of 1024 lanes with that window 71 us.  A chunk takes some
 // 3300 cycles, of which DRAM is busy 27% and the tensor cores 12%: the decoding
 // threads' instructions (58% of the issue slots, 7 us of the 51 without the
 // arithmetic) and the hand-overs from step to step bound it.  Around that a
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp >= kProd0 && warp < kMma) {
         // ---------------------------------------------------------- producers: a slice of K or V per group of four warps,
         // 64 dims of a key per thread
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int pg = (warp - kProd0) >> 2, t = tid & 127;
         const bool does_k = C::kBoth || pg < nK, does_v = C::kBoth || pg >= 2;
         const int ev = C::kBoth ? pg : pg - 2, kh = ev / nDH, dh = ev % nDH;  // (a slice of V: half the keys, 128 dims)
@@ -643,8 +643,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (!ok) give_up();
     } else if (warp >= kMma) {
-        // 896 threads are launched with 72 registers (64512 in all): 128 x 40 here, 256 x 104 for the weights and
-        // 512 x 64 for the producers are as many
+        // 896 threads are launched with 72 registers (64512 in all): 128 x 40 here, 256 x 120 for the weights and
+        // 512 x 56 for the producers are as many.  (With 40, 104 and 64 the weights spilled more: 64 lanes of up to 8192
+        // keys took 51.4 us, 50.3 now, two prompts 73.3, 70.6 now.  56, 128 and 48: 50.7 and 70.2.)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == kWalk && al_elect()) {
             // ------------------------------------------------------ describes the pieces
@@ -807,7 +808,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---------------------------------------------------------- weights and sums: thread t of a warpgroup owns key t of a
         // chunk, and of the outputs dims t and t + 128.  Up to 16 rows the warpgroups take the chunks in turn and add up at
         // the end; more, and warpgroup wg owns rows 16 wg .. 16 wg + 15 of every chunk.
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int wg = warp >> 2, t = tid & 127, own = 16 * wg;  // own: this warpgroup's place in what both have 16 of
         PieceRef ref;
         int it = 0;  // chunks so far
