@@ -20,9 +20,9 @@
 // operations have no immediate operands, and their constants no registers left.)
 //
 // One cluster of CTAs per row, whose shared memory holds the row: it is read
-// once.  A histogram of 2048 bins over y counts the words and adds up how many
-// parts of a bin's width each lies above its border, which gives a bin's weight
-// to 10^-4 or so; a CTA sums a share of the bins over the cluster's.  So top-k's
+// once.  A histogram of 2048 bins over y counts the words, or adds up their
+// weights by a line through the bin, good to 10^-5; a CTA sums a share of the
+// bins over the cluster's.  So top-k's
 // border is known to a bin and top-p's to one or two.  Their words go to a list
 // in the first CTA, which sorts it, while every thread adds up the exact weights
 // of the words before them (and of all) in registers; the border is then a place
@@ -33,11 +33,12 @@
 // the search for that.
 //
 // Instructions bound it, not memory: 64 rows of 262144 words with a top_p of 0.9
-// take 106 us for 67 MB; of the 130 warp instructions to 32 words the exact
-// weights are about half and the counting, whose shared-memory additions collide
-// (8 cycles each), a quarter.  256 rows of 32000 with no bound, one pass, take 30
-// us; one row of 262144 with a top_k of 64, 16.8 us, most of it waiting: the
-// cluster's meetings (some 1200 cycles each), the border, the sorted list.
+// take 98 us for 67 MB, about half of it the exact weights (some 60 instructions
+// a word); counting, one addition to shared memory a word (8 cycles a warp), is
+// the next.  (With counts and places in a bin as two additions it took 106.)
+// 256 rows of 32000 with no bound, one pass, take 30 us; one row of 262144 with a
+// top_k of 64, 15.8 us, most of it waiting: the cluster's meetings (some 1200
+// cycles each), the border, the sorted list.
 #include <cmath>
 
 #include "launch.cuh"
@@ -54,7 +55,6 @@ constexpr int kBins = 2048;
 constexpr int kList = 2048, kEach = kList / kThreads;  // words of the list, and of a thread
 constexpr int kMaxCluster = 16;
 constexpr int kCached = 16384;  // words of a CTA in shared memory, so that an SM has room for two CTAs
-constexpr int kPacked = 16384;  // a CTA's words up to which a bin's numbers share 32 bits
 constexpr int kMaxVocab = 1 << 24;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kPart = 32.0f;               // units of y to a factor of two
@@ -64,8 +64,8 @@ constexpr int kMagicBits = 0x4B400000;
 constexpr float kMagicHi = 50331648.0f, kMagicLo = 12.0f;    // 1.5 * 2^25 and 1.5 * 2^3: to fours, and to 2^-20
 constexpr int kMagicHiBits = 0x4C400000, kMagicLoBits = 0x41400000;
 constexpr float kBinsPer = 1.375f;           // bins to a unit of y
-constexpr float kNear = 3e-5f;               // how far the bins' weights may be off as a part of the sum, by a bin's width
-constexpr float kBinPart = 0.69314718f / (kPart * kBinsPer);  // and a word's per bin that its y is off
+constexpr float kBinPart = 0.69314718f / (kPart * kBinsPer);  // what a bin takes from a weight, as a part of it
+constexpr float kNear = 2e-5f;               // how far the bins' weights may be off as a part of the sum, beside rounding
 
 struct SampleArgs {
     const float *logits;
@@ -81,6 +81,7 @@ struct SampleArgs {
     int cached;          // of them in shared memory (a multiple of 4)
     int drop;            // bits of a weight that are left out, so that a row's sum stays below 2^63
     int wide;            // rows are 16-byte aligned
+    float unit;          // a bin's weights as whole numbers: what the one at its middle counts
 };
 
 struct Shared {
@@ -459,76 +460,58 @@ struct Row {
         return r;
     }
     // The bins of the words as they are counted by count_by_y: lo and hi, between which top-k's border (k > 0) or top-p's
-    // must be, and the words up to hi and between.  A count is exact, a weight an estimate: a word's y is known to a part
-    // of a bin, 1 / parts(), so a word's weight is off by kBinPart of that at most, half of it for most, each by its own.
-    // The sums are off by that share of the sum at most (sure), and seldom by three deviations or more: by it times the
-    // root of the sum of the squares.  (Few heavy words make the latter large, many like ones small.  Where the border is
-    // not between lo and hi after all, the list does not hold it, and exact weights find it.)
+    // must be, and the words up to hi and between; for top-p, `between` is a bound and `upto` says nothing.  Counts are
+    // exact.  A word's weight is off by kBinPart^2 / 16 of itself (a line in place of 2^-y) and by half a unit, which
+    // moves the border by half as much of the sum at most: what lies before it counts 1 - p times, the rest p times.
     struct Border {
         int lo, hi;
         uint32_t upto, between;
     };
-    __device__ __forceinline__ Border find_border(u64 k, float p, bool sure) {
+    __device__ __forceinline__ Border find_border(u64 k, float p) {
         const int tid = threadIdx.x, C = A.cluster, per = kBins / C, b0 = rank * per;
         const int each = max(1, per / kThreads), share = max(1, kThreads / per), sub = tid & (share - 1);
         cluster_sync();
-        u64 c[4], cs = 0;
-        float m[4], squares = 0.0f;
-        const float part = 1.0f / (float)parts();
+        u64 c[4], m[4], cs = 0, ms = 0;  // words, and weights as whole numbers of 2^-32, so that every CTA adds up the same
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            m[q] = 0.0f, c[q] = 0;
+            m[q] = c[q] = 0;
             if (q >= each) continue;
             const int b = b0 + tid / share * each + q;
-            uint32_t n = 0, f = 0;
+            u64 v = 0;
 #pragma unroll 4
-            for (int r = sub; r < C; r += share) {
-                if (A.slice <= kPacked) {
-                    const uint32_t v = ld_peer(&S.hist.count[b], (uint32_t)r);
-                    n += v >> 17, f += v & 0x1ffffu;
-                } else {
-                    const u64 v = ld_peer(&S.hist.mass[b], (uint32_t)r);
-                    n += (uint32_t)(v >> 32), f += (uint32_t)v;
-                }
+            for (int r = sub; r < C; r += share) v += ld_peer(&S.hist.count[b], (uint32_t)r);
+            for (int off = 1; off < share; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+            if (sub || !v) continue;
+            if (k) {
+                c[q] = v;
+            } else {
+                const float units = __fdiv_rn((float)v, A.unit);
+                c[q] = (u64)(units * (1.0f + kBinPart)) + 1;  // (a word counts at least 1 - kBinPart / 2)
+                m[q] = (u64)(units * exp2f((float)-b / (kBinsPer * kPart)) * 4294967296.0f);
             }
-            for (int off = 1; off < share; off <<= 1)
-                n += __shfl_xor_sync(0xffffffffu, n, off), f += __shfl_xor_sync(0xffffffffu, f, off);
-            if (sub || !n) continue;
-            c[q] = n, cs += n;
-            // (the words' mean y: they lie f / n parts of a bin above its lower border on average)
-            if (b == kBins - 1 || k) continue;  // (no weight; nobody asks)
-            m[q] = (float)n * exp2f(-((float)b - 0.5f + __fdiv_rn((float)f, (float)n) * part) / (kBinsPer * kPart));
-            squares += __fdiv_rn(m[q] * m[q], (float)n);
+            cs += c[q], ms += m[q];
         }
-        u64 ct;
+        u64 ct, mt = 0, mb = 0;
         u64 cb = before(cs, ct);
-        // weights as whole numbers of 2^-32 of the largest, so that every CTA adds up the same; the squares of 2^-14
-        u64 m64[4], mo = 0, mb = 0, mt = 0, sq = 0;
-#pragma unroll
-        for (int q = 0; q < 4; q++) m64[q] = (u64)(m[q] * 4294967296.0f), mo += m64[q];
-        if (!k) mb = before(mo, mt), before((u64)(squares * 16384.0f), sq);
-        constexpr u64 kCount = (1 << 25) - 1;
-        tell(mt, sq << 25 | ct);
+        if (!k) mb = before(ms, mt);
+        tell(mt, ct);
         u64 mall = 0, call = 0;
-        sq = 0;
         for (int q = 0; q < C; q++) {
-            const u64 n = told(1, q) & kCount;
-            if (q < rank) mb += told(0, q), cb += n;
-            mall += told(0, q), call += n, sq += told(1, q) >> 25;
+            if (q < rank) mb += told(0, q), cb += told(1, q);
+            mall += told(0, q), call += told(1, q);
         }
         k = min(k, call);
-        const float want = p * (float)mall, unit = kBinPart * part;
-        const float off = kNear * (float)mall + unit * fminf((float)mall, sure ? kInf : 33554432.0f * sqrtf((float)sq));
+        const float want = p * (float)mall, off = (kNear + __fdiv_rn(0.5f, A.unit)) * (float)mall;
         const u64 lo_t = k ? k : (u64)fmaxf(want - off, 1.0f), hi_t = k ? k : min(mall, (u64)(want + off));
         if (tid < 4) S.found[tid] = 0;
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            const u64 a = k ? cb : mb, v = k ? c[q] : m64[q];
+            const u64 a = k ? cb : mb, v = k ? c[q] : m[q];
             const int b = b0 + tid / share * each + q;
             if (a < lo_t && lo_t <= a + v) S.found[0] = (u64)b + 1, S.found[1] = cb;
             if (a < hi_t && hi_t <= a + v) S.found[2] = (u64)b + 1, S.found[3] = cb + c[q];
-            mb += m64[q], cb += c[q];
+            mb += m[q], cb += c[q];
         }
         __syncthreads();
         give(S.found[0] != 0, 0, 2);
@@ -548,15 +531,14 @@ struct Row {
         }
         __syncthreads();
     }
-    // The kept words by y: a bin's count and how many parts of a bin each word lies in it.  Eighths, in 15 and 17 bits of
-    // a word, where the CTA's words cannot exceed those, else sixty-fourths, in 32 bits each.
-    __device__ __forceinline__ int parts() const { return A.slice <= kPacked ? 8 : 64; }
-    template <bool PACKED>
+    // The kept words by y: a bin's count, or the sum of its words' weights (a line through the bin) in A.unit to one at
+    // its middle.  Either is one addition to shared memory, which is what bounds this.
+    template <bool MASS>
     __device__ __forceinline__ void count_by_y() {
-        clear_hist<!PACKED, PACKED>();
+        clear_hist<false, true>();
         uint32_t rest = 0;
-        uint32_t *const half = reinterpret_cast<uint32_t *>(S.hist.mass);
         const bool cut = is_cut();
+        const float slope = -kBinPart * A.unit, middle = kMagic + rintf(A.unit * (1.0f + kBinPart * kBinPart / 16.0f));
         words_of_warp([&](const float (&x)[4], uint32_t i) {
 #pragma unroll
             for (int q = 0; q < 4; q++) {
@@ -566,32 +548,19 @@ struct Row {
                     rest += on;  // (those of no weight, which may be most)
                     continue;
                 }
-                // the nearest part of the bin that bin_of rounds to
-                constexpr int kParts = PACKED ? 8 : 64;
-                const int z = __float_as_int(__fmaf_rn(y, kParts * kBinsPer, kMagic + kParts / 2)) - kMagicBits;
-                const int b = bin_of(y);
-                const uint32_t f = (uint32_t)min(kParts - 1, max(0, z - kParts * b));
-                if (PACKED) {
-                    atomicAdd(&S.hist.count[b], (1u << 17) + f);
+                const float t = __fmaf_rn(y, kBinsPer, kMagic);  // (as bin_of)
+                const int b = __float_as_int(t) - kMagicBits;
+                if (MASS) {
+                    const float g = __fmaf_rn(y, kBinsPer, -__fsub_rn(t, kMagic));  // -1/2 .. 1/2 of the bin
+                    atomicAdd(&S.hist.count[b], (uint32_t)(__float_as_int(__fmaf_rn(g, slope, middle)) - kMagicBits));
                 } else {
-                    atomicAdd(&half[2 * b], f);
-                    atomicAdd(&half[2 * b + 1], 1u);
+                    atomicAdd(&S.hist.count[b], 1u);
                 }
             }
         });
+        if (MASS) return;
         rest = __reduce_add_sync(0xffffffffu, rest);
-        if ((threadIdx.x & 31) == 0 && rest) {
-            if (PACKED)
-                atomicAdd(&S.hist.count[kBins - 1], rest << 17);
-            else
-                atomicAdd(&half[2 * kBins - 1], rest);
-        }
-    }
-    __device__ __forceinline__ void count_by_y() {
-        if (A.slice <= kPacked)
-            count_by_y<true>();
-        else
-            count_by_y<false>();
+        if ((threadIdx.x & 31) == 0 && rest) atomicAdd(&S.hist.count[kBins - 1], rest);
     }
     // the kept words' exact weights by y
     __device__ __forceinline__ void weigh_by_y() {
@@ -921,8 +890,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     const bool by_k = k > 0 && k < A.vocab, by_p = p < 1.0f;
     if (by_k) {
-        R.count_by_y();
-        const Row::Border c = R.find_border((u64)k, 0.0f, true);
+        R.count_by_y<false>();
+        const Row::Border c = R.find_border((u64)k, 0.0f);
         auto bin = [&](float x) { return R.bin_of(R.y_of(x)); };
         if (c.upto <= kList) {
             R.gather([&](uint32_t, float x) { return bin(x) <= c.hi; });
@@ -936,9 +905,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     auto kept_weight = [&](float x, uint32_t i) { return R.weight(x, R.keeps(key_of(x), i)); };
     bool summed = false;  // S.scan holds the warps' sums of what is left, many the CTA's words
     if (by_p) {
-        R.count_by_y();
+        R.count_by_y<true>();
         const float floor_x = R.floor_of(min_p);
-        const Row::Border c = R.find_border(0, p, floor_x > -kInf);
+        const Row::Border c = R.find_border(0, p);
         // (where min-p keeps words of bins before the border's only, top-p takes none of them)
         bool done = floor_x > -kInf && R.bin_of(R.y_of(floor_x)) < c.lo;
         if (!done && c.between <= kList) {
@@ -1039,7 +1008,7 @@ qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u,
     SampleArgs A{logits, row_stride, u, temperature, top_k, top_p, min_p, vocab, tokens, probs, kept};
     const void *kern = (const void *)sample_kernel;
     // As many CTAs to a row as give two to every SM, for no fewer than 4096 words each.  (Rows past what the cluster's
-    // shared memory holds come from L2 again in every pass: 64 rows of 262144 words take 106 us by fours and 200
+    // shared memory holds come from L2 again in every pass: 64 rows of 262144 words take 98 us by fours and 200
     // by sixteens, of which 11 run at a time, one after the other.)
     int c = 1;
     while (c < kMaxCluster && (int64_t)n_rows * c * 2 <= 2 * sm_count() && vocab / c > 4096) c *= 2;
@@ -1058,6 +1027,7 @@ qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u,
     A.drop = 0;
     while (((int64_t)(vocab - 1) >> A.drop) >= 1 << 18) A.drop++;
     A.wide = aligned16(logits) && row_stride % 4 == 0;
+    A.unit = (float)std::fmin(65000.0, std::floor(4.2e9 / A.slice));  // all of a CTA's words in one bin fit 32 bits
     void *args[] = {(void *)&A};
     return launch_pdl(kern, dim3((unsigned)(n_rows * c)), dim3(kThreads), smem, (cudaStream_t)stream, args, "sample_kernel", c);
 }
