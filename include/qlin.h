@@ -748,8 +748,8 @@ int qlin_attention_kv4_on_tensor_cores(const qlin_kv4 *kv, int n_lanes, int n_he
  * lower word first) are cut three times: behind the top_k[r]-th (0 or less, or
  * vocab and more: not at all); then behind the first at which the running sum
  * of the weights reaches top_p[r] times the sum over what top-k left (1 or
- * more: not at all; the first word always stays); then where w_v is below
- * min_p[r] (0 or less: not at all; above 1 counts as 1).  The token is the first
+ * more, or a NaN: not at all; 0 or less: behind the first word); then where w_v
+ * is below min_p[r] (0 or less, or a NaN: not at all; above 1 counts as 1).  The token is the first
  * word, by number, at which the running sum of the weights left exceeds u[r]
  * times their sum (u: given random numbers in [0, 1); from 1 on the last word
  * with a weight).  T <= 0 takes the first of the largest logits, as

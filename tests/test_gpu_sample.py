@@ -214,6 +214,21 @@ def test_temperatures(dev):
         _compare(x, u, t, k, p, m, _run(dev, x, u, t, k, p, m))
 
 
+@pytest.mark.parametrize("V", [3, 3000, 70001, 262144])
+@pytest.mark.parametrize("k,m", [(None, None), (40, None), (2500, None), (None, 0.3), (40, 0.01), (None, float("nan"))])
+def test_top_p_of_zero_and_less(dev, V, k, m):
+    """a top_p of 0 or less leaves the first word alone, whatever stands beside it; a NaN is no bound"""
+    rng = np.random.default_rng(V)
+    p = np.array([-1.0, -np.inf, -1e-30, -0.0, 0.0, -3e38, np.nan, np.nan, -1.0, 0.9])
+    R = len(p)
+    x, u = rng.standard_normal((R, V)) * 3, rng.random(R)
+    x[8] = 1.5  # all alike
+    got = _run(dev, x, u, 0.8, k, p, m)
+    for i in (0, 1, 2, 3, 4, 5, 8):
+        assert (got[0][i], got[1][i], got[2][i]) == (np.float32(x[i]).argmax(), 1.0, 1), i
+    _compare(x, u, 0.8, k, p, m, got, most=0.1)
+
+
 def test_rows_that_hold_no_answer(dev):
     x = np.random.default_rng(1).standard_normal((6, 40000))
     x[0, 39999] = np.nan

@@ -461,7 +461,7 @@ struct Row {
     }
     // The bins of the words as they are counted by count_by_y: lo and hi, between which top-k's border (k > 0) or top-p's
     // must be, and the words up to hi and between; for top-p, `between` is a bound and `upto` says nothing.  Counts are
-    // exact.  A word's weight is off by kBinPart^2 / 16 of itself (a line in place of 2^-y) and by half a unit, which
+    // exact.  p is 0 .. 1, so that both borders of it are in a bin.  A word's weight is off by kBinPart^2 / 16 of itself (a line in place of 2^-y) and by half a unit, which
     // moves the border by half as much of the sum at most: what lies before it counts 1 - p times, the rest p times.
     struct Border {
         int lo, hi;
@@ -816,7 +816,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const float *from = A.logits + (int64_t)row * A.row_stride + first;
-    const float T = A.temperature ? A.temperature[row] : 1.0f, p = A.top_p ? A.top_p[row] : 1.0f;
+    const float T = A.temperature ? A.temperature[row] : 1.0f, given_p = A.top_p ? A.top_p[row] : 1.0f;
+    const float p = given_p < 0.0f ? 0.0f : given_p;  // (the border is then at the first word; a NaN stays one: no border)
     const float min_p = A.min_p ? A.min_p[row] : 0.0f, u = A.u ? A.u[row] : 0.0f;
     const int64_t k = A.top_k ? A.top_k[row] : 0;
     const float2 pow = kPow[lane];
@@ -945,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 // the warps' sums of what is left: the words before, and those of the CTA's own in the list
                 summed = floor_x == -kInf || R.bin_of(R.y_of(floor_x)) > c.hi;
                 if (summed) {
-                    const int run = R.run_length(), own_n = (int)S.n_mine;
+                    const int run = R.run_length(), own_n = (int)min(S.n_mine, (uint32_t)kList);
                     __syncthreads();
                     if (tid < kWarps) S.scan[tid] = S.certain[tid];
                     __syncthreads();
