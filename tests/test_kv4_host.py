@@ -131,6 +131,19 @@ def test_binding_checks_tensors():
             qlin.kv4_cache(*bad)
 
 
+def test_binding_checks_the_tables_rows():
+    """rows of a table that lie in one another (an expanded one among them) would be read beyond its end"""
+    torch = pytest.importorskip("torch")
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    k, sc, flat = u8(3, 2, 16, 64), u8(3, 2, 16, 4), torch.zeros(64, dtype=torch.int32)
+    for shape, stride in (((5, 8), (0, 1)), ((5, 8), (7, 1)), ((2, 8), (1, 1))):
+        with pytest.raises(ValueError):
+            qlin.kv4_cache(k, k, sc, sc, flat.as_strided(shape, stride))
+    for shape, stride, want in (((1, 8), (0, 1), 8), ((1, 8), (3, 1), 8), ((5, 8), (8, 1), 8), ((5, 8), (11, 1), 11),
+                                ((5, 1), (1, 0), 1)):
+        assert qlin.kv4_cache(k, k, sc, sc, flat.as_strided(shape, stride)).table_stride == want
+
+
 def test_reference_format():
     """the numpy cache: every byte's scale, rounding, packing there and back"""
     assert SCALE_BITS(np.arange(256)).tolist() == ref.SCALES.tolist()
