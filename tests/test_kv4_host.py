@@ -144,6 +144,18 @@ def test_binding_checks_the_tables_rows():
         assert qlin.kv4_cache(k, k, sc, sc, flat.as_strided(shape, stride)).table_stride == want
 
 
+def test_binding_checks_devices():
+    """the five tensors of a cache lie on one device"""
+    torch = pytest.importorskip("torch")
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    k, sc, t = u8(3, 2, 16, 64), u8(3, 2, 16, 4), torch.zeros((5, 2), dtype=torch.int32)
+    for i in range(5):
+        a = [k, k, sc, sc, t]
+        a[i] = a[i].to("meta")
+        with pytest.raises(ValueError):
+            qlin.kv4_cache(*a)
+
+
 def test_reference_format():
     """the numpy cache: every byte's scale, rounding, packing there and back"""
     assert SCALE_BITS(np.arange(256)).tolist() == ref.SCALES.tolist()

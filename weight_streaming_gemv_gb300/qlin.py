@@ -579,7 +579,7 @@ def qlin_beam_reorder(cache, seq_stride, plane_stride, n_planes, row_bytes, max_
 def kv4_cache(k, v, k_scale, v_scale, table) -> QlinKv4C:
     """The ``qlin_kv4`` of four contiguous uint8 tensors, codes [n_pages][n_kv][page_rows][head_dim / 2] and scales
     [n_pages][n_kv][page_rows][head_dim / 32], and an int32 table [n_seqs][pages of a sequence] (any stride between
-    its rows from a row on), which the caller keeps."""
+    its rows from a row on), all on one device, which the caller keeps."""
     for t in (k, v, k_scale, v_scale):
         if t.dim() != 4 or str(t.dtype) != "torch.uint8" or not t.is_contiguous() or t.shape[:3] != k.shape[:3]:
             raise ValueError("kv4_cache: codes and scales are contiguous uint8 tensors [n_pages][n_kv][page_rows][...]")
@@ -588,6 +588,8 @@ def kv4_cache(k, v, k_scale, v_scale, table) -> QlinKv4C:
                          f"{tuple(v_scale.shape)}")
     if table.dim() != 2 or str(table.dtype) != "torch.int32" or (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError("kv4_cache: the table is int32 [n_seqs][pages], its rows contiguous")
+    if any(t.device != k.device for t in (v, k_scale, v_scale, table)):
+        raise ValueError("kv4_cache: codes, scales and the table are on one device")
     if table.shape[0] > 1 and table.stride(0) < table.shape[1]:
         raise ValueError(f"kv4_cache: the table's rows of {table.shape[1]} pages lie in one another (stride {table.stride(0)})")
     c = QlinKv4C()
