@@ -54,6 +54,19 @@ def test_pages_are_given_and_taken_back(paged):
             d.paged_room(0, rows)
 
 
+def test_sequences_out_of_range(paged):
+    """a number below 0 is no sequence: it neither takes the last one's pages nor gives it any"""
+    d = paged
+    d.paged_room(2, 40)
+    table, free = d.page_table.clone(), list(d.pages_free)
+    for seq in (-1, -3, 3):
+        with pytest.raises(IndexError):
+            d.paged_room(seq, 100)
+        with pytest.raises(IndexError):
+            d.paged_release(seq)
+    assert torch.equal(table, d.page_table) and free == d.pages_free and [len(p) for p in d.pages_of] == [0, 0, 3]
+
+
 def test_sample_checks_its_tensors(paged, monkeypatch):
     calls = []
     monkeypatch.setattr(qlin, "qlin_sample", lambda *a: calls.append(a))

@@ -256,12 +256,17 @@ class T158Decoder:
         self.paged_workspace = torch.zeros(self.paged_ws_bytes, dtype=torch.uint8, device=dev)
         self.paged_tokens, self.paged_pos, self.paged_seq, self.paged_next = (i32(max_lanes) for _ in range(4))
 
+    def _paged_pages(self, seq: int):
+        if not 0 <= seq < len(self.pages_of):
+            raise IndexError(f"sequence {seq} of {len(self.pages_of)}")
+        return self.pages_of[seq]
+
     def paged_room(self, seq: int, rows: int):
         """Pages for the first ``rows`` positions of sequence ``seq``; raises MemoryError, and takes none, where the pool has
         too few."""
         if not 0 <= rows <= self.cfg.max_pos:
             raise ValueError(f"paged_room: {rows} positions, and the model has {self.cfg.max_pos}")
-        have = self.pages_of[seq]
+        have = self._paged_pages(seq)
         need = -(-rows // self.page_rows) - len(have)
         if need > len(self.pages_free):
             raise MemoryError(f"paged_room: {need} pages for sequence {seq}, {len(self.pages_free)} are free")
@@ -272,7 +277,7 @@ class T158Decoder:
 
     def paged_release(self, seq: int):
         """The sequence's pages go back to the pool."""
-        self.pages_free.extend(reversed(self.pages_of[seq]))
+        self.pages_free.extend(reversed(self._paged_pages(seq)))
         self.pages_of[seq] = []
         self.page_table[seq].fill_(-1)
 
