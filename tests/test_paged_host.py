@@ -84,3 +84,12 @@ def test_sample_checks_its_tensors(paged, monkeypatch):
         with pytest.raises(ValueError):
             paged.sample(**a)
     assert len(calls) == 2
+
+
+def test_sample_wants_the_decoders_device(paged, monkeypatch):
+    monkeypatch.setattr(qlin, "qlin_sample", lambda *a: None)
+    f, i = torch.zeros(4), torch.zeros(4, dtype=torch.int32)
+    paged.sample(torch.zeros((4, 11)), f, i)
+    paged.emb = torch.zeros(1, device="meta")  # the weights elsewhere
+    with pytest.raises(ValueError):
+        paged.sample(torch.zeros((4, 11)), f, i)

@@ -297,6 +297,8 @@ class T158Decoder:
         rows, vocab = logits.shape
         if logits.dtype != torch.float32 or (vocab > 1 and logits.stride(1) != 1):
             raise ValueError("sample: logits are fp32, a row's contiguous")
+        if logits.device != self.emb.device:
+            raise ValueError(f"sample: logits on {logits.device}, the decoder is on {self.emb.device}")
         wants = ((u, torch.float32), (tokens, torch.int32), (temperature, torch.float32), (top_k, torch.int32),
                  (top_p, torch.float32), (min_p, torch.float32), (probs, torch.float32), (kept, torch.int32))
         for t, kind in wants:
