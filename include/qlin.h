@@ -771,8 +771,8 @@ qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u,
 
 /* decode_lanes_t158 over a paged cache of 4 bits a value: layer l's cache is
  * kv with its codes code_bytes and its scales scale_bytes further on per layer
- * (multiples of 32 and 16), one table for all layers.  The lanes' keys and values
- * are appended with qlin_kv4_append and read with qlin_attention_kv4 (no window),
+ * (multiples of 32 and 16; where there are several layers at least the pool's
+ * size), one table for all layers.  The lanes' keys and values are appended with qlin_kv4_append and read with qlin_attention_kv4 (no window),
  * everything else is decode_lanes_t158's arithmetic.  head_dim: 64, 128 or 256.
  * A lane with a negative position is padding: it appends nothing, and what comes
  * out for it says nothing (its token is looked up all the same).  decode_lanes_t158_status reports a lane, position or

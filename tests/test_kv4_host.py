@@ -193,3 +193,28 @@ def _sample(**kw):
 def test_sample_refuses(bad, status):
     assert _sample(**bad) == status
     assert qlin.lib().qlin_last_error().decode().startswith("qlin_sample")
+
+
+def _step(n_layers, code_bytes, scale_bytes):
+    """decode_lanes_t158_kv4 without its tokens, which it asks for last of all: 16 pages of 64 rows, 2 KV heads of 64"""
+    m = qlin.T158ModelC()
+    m.n_layers, m.dim, m.n_heads, m.n_kv_heads, m.head_dim, m.ffn, m.vocab, m.max_pos = n_layers, 64, 4, 2, 64, 64, 16, 128
+    for j in range(len(m.w)):
+        m.w[j], m.pitch[j] = 4096, 64
+    for name in ("scales", "g_attn", "g_ffn", "g_final", "emb", "rope_cos", "rope_sin"):
+        setattr(m, name, 4096)
+    c = qlin.T158Kv4C()
+    c.kv, c.code_bytes, c.scale_bytes = _kv(), code_bytes, scale_bytes
+    st = qlin.lib().decode_lanes_t158_kv4(ctypes.byref(m), ctypes.byref(c), 1, None, 4, 8, None, 12, 16, 1 << 30, 1, None)
+    return st, qlin.lib().qlin_last_error().decode()
+
+
+def test_step_refuses_layers_in_one_another():
+    codes, scales = 16 * 2 * 64 * 32, 16 * 2 * 64 * 2
+    for layers, a, b in ((2, codes - 32, scales), (2, codes, scales - 16), (2, 0, 0), (7, codes, 0), (3, codes + 16, scales),
+                         (3, codes, scales + 8), (1, -32, 0)):
+        st, said = _step(layers, a, b)
+        assert st == 1 and "code_bytes" in said, (layers, a, b, said)
+    for layers, a, b in ((2, codes, scales), (1, 0, 0), (5, 2 * codes, 2 * scales), (2, codes + 32, scales + 16)):
+        st, said = _step(layers, a, b)
+        assert st == 1 and "null pointer" in said, (layers, a, b, said)

@@ -852,9 +852,10 @@ qlin_status decode_lanes_t158_kv4(const t158_model *m, const t158_kv4 *cache, in
     QLIN_REQUIRE(cache, QLIN_ERR_INVALID_ARG, "%s: null pointer", fn);
     // (what the append and the attention take: refused here, before anything is written)
     if (qlin_status st = check_kv4(fn, &cache->kv, m->n_kv_heads, m->head_dim)) return st;
-    QLIN_REQUIRE(cache->code_bytes >= 0 && cache->scale_bytes >= 0 && cache->code_bytes % 32 == 0 &&
+    const int64_t pool = m->n_layers == 1 ? 0 : (int64_t)cache->kv.n_pages * m->n_kv_heads * cache->kv.page_rows * m->head_dim / 32;
+    QLIN_REQUIRE(cache->code_bytes >= 16 * pool && cache->scale_bytes >= pool && cache->code_bytes % 32 == 0 &&
                      cache->scale_bytes % 16 == 0,
-                 QLIN_ERR_INVALID_ARG, "%s: code_bytes %lld, scale_bytes %lld: multiples of 32 and 16", fn,
+                 QLIN_ERR_INVALID_ARG, "%s: code_bytes %lld, scale_bytes %lld: a layer's at least, multiples of 32 and 16", fn,
                  (long long)cache->code_bytes, (long long)cache->scale_bytes);
     QLIN_REQUIRE(m->n_heads <= 65535 && aligned16(m->rope_cos) && aligned16(m->rope_sin) && aligned4(positions) &&
                      aligned4(seqs),
