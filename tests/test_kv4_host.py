@@ -218,3 +218,22 @@ def test_step_refuses_layers_in_one_another():
     for layers, a, b in ((2, codes, scales), (1, 0, 0), (5, 2 * codes, 2 * scales), (2, codes + 32, scales + 16)):
         st, said = _step(layers, a, b)
         assert st == 1 and "null pointer" in said, (layers, a, b, said)
+
+
+@pytest.mark.parametrize("name", ["attention_kv4.cu"])
+def test_every_bounded_wait_is_heard(name):
+    """a wait that gives up has to be reported: no kernel drops the answer of one (but of those behind which it only
+    leaves), and the status is raised whoever saw it"""
+    import os
+    import re
+
+    here = os.path.dirname(os.path.abspath(qlin.__file__))
+    with open(os.path.join(here, "csrc", name)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    dropped = re.findall(r"(?:^|[;{})])\s*((?:al_wait|al_wait_at|kv_wait_all)\([^;]*\);)", text, re.M)
+    assert not dropped, dropped
+    # the weights' role, which may be the only one to see it, and the end of the kernel
+    weights = text[text.rindex("setmaxnreg.inc"):]
+    for m in re.finditer(r"al_wait\(&S\.pv_done", weights):
+        assert "S.abort = 1" in weights[m.start(): m.end() + 90]
+    assert re.search(r"__syncthreads\(\);\s*if \(tid == 0 && S\.abort\) raise_status\(A\.status, kStatusTimeout\);", weights)

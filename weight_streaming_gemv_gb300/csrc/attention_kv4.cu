@@ -798,11 +798,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 it += n;
                 if (ok) ref.done(S);
             }
-            if (!ok) {
-                give_up();
-                tc_commit(&S.drain);  // the MMAs in flight
-                mbar_wait(&S.drain, 0);
-            }
+            if (!ok) give_up();
+            tc_commit(&S.drain);  // the MMAs in flight (others may have given up)
+            mbar_wait(&S.drain, 0);
         }
     } else {
         // ---------------------------------------------------------- weights and sums: thread t of a warpgroup owns key t of a
@@ -958,7 +956,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     lsum[j] = __fadd_rn(lsum[j], s[j]);
                 }
                 if (last >= 0) {  // the products of the chunk before: P is read, and O^T is there
-                    al_wait(&S.pv_done[last & 1], (uint32_t)(last >> 1) & 1u, &S.abort);
+                    if (!al_wait(&S.pv_done[last & 1], (uint32_t)(last >> 1) & 1u, &S.abort)) S.abort = 1;
                     __syncwarp();
                 }
                 // the weights, as two fp16 terms, a key's rows side by side
@@ -994,7 +992,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             it += n;
             if (ok && last >= 0) {
-                ok = al_wait(&S.pv_done[last & 1], (uint32_t)(last >> 1) & 1u, &S.abort);
+                if (!(ok = al_wait(&S.pv_done[last & 1], (uint32_t)(last >> 1) & 1u, &S.abort))) S.abort = 1;
                 __syncwarp();
                 tc_fence_after();
                 take();
@@ -1075,6 +1073,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && S.abort) raise_status(A.status, kStatusTimeout);  // (whoever saw it)
     if (warp == kMma)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmCols) : "memory");
 }
