@@ -220,7 +220,7 @@ def test_step_refuses_layers_in_one_another():
         assert st == 1 and "null pointer" in said, (layers, a, b, said)
 
 
-@pytest.mark.parametrize("name", ["attention_kv4.cu"])
+@pytest.mark.parametrize("name", ["attention_kv4.cu", "attention_lanes.cu"])
 def test_every_bounded_wait_is_heard(name):
     """a wait that gives up has to be reported: no kernel drops the answer of one (but of those behind which it only
     leaves), and the status is raised whoever saw it"""
@@ -235,5 +235,5 @@ def test_every_bounded_wait_is_heard(name):
     # the weights' role, which may be the only one to see it, and the end of the kernel
     weights = text[text.rindex("setmaxnreg.inc"):]
     for m in re.finditer(r"al_wait\(&S\.pv_done", weights):
-        assert "S.abort = 1" in weights[m.start(): m.end() + 90]
+        assert "S.abort = 1" in weights[m.start(): m.end() + 150]
     assert re.search(r"__syncthreads\(\);\s*if \(tid == 0 && S\.abort\) raise_status\(A\.status, kStatusTimeout\);", weights)

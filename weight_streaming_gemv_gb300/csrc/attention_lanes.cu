@@ -594,9 +594,9 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             if (!ok) {
                 S.abort = 1;
                 raise_status(A.status, kStatusTimeout);
-                tc_commit(&S.drain);  // the MMAs in flight
-                mbar_wait(&S.drain, 0);
             }
+            tc_commit(&S.drain);  // the MMAs in flight (others may have given up)
+            mbar_wait(&S.drain, 0);
         }
     } else {
         // ---------------------------------------------------------- weights and sums: warpgroup wg owns rows
@@ -628,6 +628,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     ok = ok && al_wait(&S.pv_done, (uint32_t)it & 1u, &S.abort);
                     __syncwarp();
                 }
+                if (!ok) S.abort = 1;
                 ok = !al_bar_or(wg, !ok);
                 g += n * (nK + nV);
                 if (lane == 0) ref.done(S);
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     lsum[j] = __fadd_rn(lsum[j], s[j]);
                 }
                 if (i > 0) {  // the products of the chunk before: P is read, and O^T is there
-                    al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort);
+                    if (!al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort)) S.abort = 1;
                     __syncwarp();
                 }
                 // the weights, as three bf16 terms, a key's rows side by side
@@ -781,12 +782,12 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     // infinity or NaN is not.  The slices are dealt out to the warpgroups, half a key's values to a
                     // thread.  (With the scores of the next chunk there, what lay in these slots before is read, and
                     // what lies in them now stays until the weights are ready: the barriers' phases are the next ones.)
-                    if (i + 1 < n) al_wait(&S.s_full, (uint32_t)(it + 1) & 1u, &S.abort);
+                    if (i + 1 < n && !al_wait(&S.s_full, (uint32_t)(it + 1) & 1u, &S.abort)) S.abort = 1;
                     const int gv = g + min(i + 2, n) * nK + i * nV;
                     for (int vs = wg; vs < nV; vs += (nrows + 15) / 16) {
                         const int sl = (gv + vs) % slots, k0 = cr + 64 * (vs / nDH), y = k0 + (t & 63);
                         if (!p->edge_in(k0, k0 + 64)) continue;
-                        al_wait(&S.full[sl], (uint32_t)((gv + vs) / slots) & 1u, &S.abort);
+                        if (!al_wait(&S.full[sl], (uint32_t)((gv + vs) / slots) & 1u, &S.abort)) S.abort = 1;
                         if (p->edge_in(y, y + 1))
                             al_look<NT>(S, *p, y, smem_addr(ring + sl * C::kSlot) + (uint32_t)((t >> 6) * 8192 + (t & 63) * 128),
                                         t, hd - (vs % nDH) * 128 - (t >> 6) * 64);
@@ -803,7 +804,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
                     for (int vs = 0; vs < nV; vs++) {
                         const int sl = (gv + vs) % slots, k0 = cr + 64 * (vs / nDH), y = k0 + (t & 63);
                         if (!p->edge_in(k0, k0 + 64)) continue;
-                        al_wait(&S.fix_go, fixes & 1u, &S.abort);
+                        if (!al_wait(&S.fix_go, fixes & 1u, &S.abort)) S.abort = 1;
                         fixes++;
                         if (p->edge_in(y, y + 1))
                             al_look<NT>(S, *p, y, smem_addr(ring + sl * C::kSlot) + (uint32_t)((t >> 6) * 8192 + (t & 63) * 128),
@@ -820,7 +821,9 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
             // the sums over the keys
             const float l4 = al_reduce16<false>(lsum, lane);
             if (lane < 16) S.red[warp & 3][r0 + lane] = l4;
-            if (al_bar_or(wg, !al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort))) {
+            const bool gone = !al_wait(&S.pv_done, (uint32_t)(it - 1) & 1u, &S.abort);
+            if (gone) S.abort = 1;
+            if (al_bar_or(wg, gone)) {
                 ok = false;
                 break;
             }
@@ -865,6 +868,7 @@ __global__ void __launch_bounds__(AlCfg<NT>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && S.abort) raise_status(A.status, kStatusTimeout);  // (whoever saw it)
     if (warp == C::kMma)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
 }
