@@ -205,6 +205,35 @@ def test_low_values_count_as_they_are(dev):
     _compare(x, u, 0.7, k, p, None, _run(dev, x, u, 0.7, k, p, None))
 
 
+@pytest.mark.parametrize("V", [7, 3000, 50000])
+@pytest.mark.parametrize("k,p,m", [(None, None, None), (4, None, None), (2500, 0.7, None), (None, 0.8, None), (None, 0.9, 0.3),
+                                   (None, None, 1.0)])
+def test_logits_and_temperatures_next_to_the_types_range(dev, V, k, p, m):
+    """logits whose differences fp32 does not hold, and temperatures as large: their weights are those of the definition"""
+    rng = np.random.default_rng(V)
+    big = float(np.finfo(np.float32).max)
+    t = np.array([1e38, 3e38, 2e37, 1e38, big, 1e30, 1.0, 1e-20, 3e31, 1e38, 1e33, np.inf])
+    R = len(t)
+    x = rng.uniform(-1, 1, (R, V)) * big
+    x[3] = rng.choice([-big, big], V)
+    x[3, 1] = big
+    x[5] = 1e31 * rng.standard_normal(V) + 3e38  # beside one another, far from 0
+    x[7] = np.float32(2e30) + 1e24 * rng.integers(0, 1 << 20, V)
+    x[8] = 1e31 * rng.standard_normal(V)
+    x[9] = -1e-40  # the largest's share of the temperature is nothing
+    x[9, ::2] = -big
+    x[10] = 5.0 * rng.standard_normal(V)
+    u = rng.random(R)
+    got = _run(dev, x, u, t, k, p, m)
+    if m == 1.0:
+        # at a finite temperature only the words of the largest logit weigh 1: exp(-1e-33), below it, is 1 in 64 bits, so
+        # that the definition's cut has to be made by the logits here (row 10)
+        f = np.float32(x)
+        x = np.where(np.isfinite(t)[:, None] & (f < f.max(1, keepdims=True)), -np.inf, x)
+        m = None
+    _compare(x, u, t, k, p, m, got, most=0.2)
+
+
 def test_temperatures(dev):
     rng = np.random.default_rng(9)
     t = np.array([1e-45, 1e-38, 1e-6, 0.01, 1e3, 1e30, np.inf, np.nan, -1.0, -0.0, 3e38, 1e-3])

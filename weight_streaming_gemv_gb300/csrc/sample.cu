@@ -65,6 +65,9 @@ constexpr float kMagicHi = 50331648.0f, kMagicLo = 12.0f;    // 1.5 * 2^25 and 1
 constexpr int kMagicHiBits = 0x4C400000, kMagicLoBits = 0x41400000;
 constexpr float kBinsPer = 1.375f;           // bins to a unit of y
 constexpr float kBinPart = 0.69314718f / (kPart * kBinsPer);  // what a bin takes from a weight, as a part of it
+// Logits' differences overflow fp32, and what their factor's second part is becomes too small for it, only beside a largest
+// one of kFarLogit or at a temperature of kFarT and more: there everything is taken times kFar.
+constexpr float kFar = 0x1p-24f, kFarLogit = 0x1p102f, kFarT = 0x1p100f;
 constexpr float kNear = 2e-5f;               // how far the bins' weights may be off as a part of the sum, beside rounding
 
 struct SampleArgs {
@@ -103,7 +106,8 @@ struct Shared {
     u64 result[4];          // and what some CTA's ended with
     uint32_t n_list, n_mine;
     double thr;             // the least logit that min-p keeps, less the largest
-    float ch, cl;
+    float ch[2], cl[2];     // y's factor as a pair, for h = 1 and h = kFar
+    float top;              // the largest logit
 };
 
 // 2^(24 - j/32) as a pair
@@ -189,7 +193,8 @@ struct Row {
     const float *from;
     int rank, n;   // n words of its own, from word `first` on
     int first;
-    float M, ch, cl;  // the largest logit; y = (M - x) (ch + cl)
+    float M, ch, cl;  // the largest logit, times h; y = (M - h x) (ch + cl)
+    float h;          // a power of two that keeps the differences in range
     float th, tl;     // this lane's number 2^(-lane/32), times 2^24
     uint32_t kt, it;  // kept: a key above kt, or equal and a word number up to it (first: all finite ones)
     int turn = 0;
@@ -197,15 +202,15 @@ struct Row {
     __device__ __forceinline__ bool keeps(uint32_t k, uint32_t i) const { return k > kt || (k == kt && i <= it); }
     // (the lowest finite number may be a word's, and the cut among its equals)
     __device__ __forceinline__ bool is_cut() const { return kt != kKeyNegInf + 1 || it != 0xffffffffu; }
-    __device__ __forceinline__ float y_of(float x) const { return __fmul_rn(__fsub_rn(M, x), ch); }
+    __device__ __forceinline__ float y_of(float x) const { return __fmul_rn(__fmaf_rn(-h, x, M), ch); }
     __device__ __forceinline__ int bin_of(float y) const {
         return y < kNoWeight ? __float_as_int(__fmaf_rn(y, kBinsPer, kMagic)) - kMagicBits : kBins - 1;
     }
     // A word's weight and y, all lanes of the warp at once: w = (q - kMagicHiBits) 2^22 + r - kMagicLoBits.  Where y is
     // kNoWeight or more, or not a number, q and r say nothing.  value: w 2^-20 as a float.
     __device__ __forceinline__ void weigh(float x, int &q, int &r, float &y, float *value = nullptr) const {
-        const float s = __fsub_rn(M, x), bb = __fsub_rn(s, M);
-        const float e = __fsub_rn(__fsub_rn(M, __fsub_rn(s, bb)), __fadd_rn(x, bb));  // M - x is s + e
+        const float s = __fmaf_rn(-h, x, M), bb = __fsub_rn(s, M);
+        const float e = __fsub_rn(__fsub_rn(M, __fsub_rn(s, bb)), __fmaf_rn(h, x, bb));  // M - h x is s + e
         y = __fmul_rn(s, ch);
         const float yl = __fmaf_rn(e, ch, __fmaf_rn(s, cl, __fmaf_rn(s, ch, -y)));
         const float t = __fadd_rn(y, kMagic);
@@ -668,10 +673,11 @@ struct Row {
     // the least logit that min-p keeps
     __device__ __forceinline__ float floor_of(float min_p) const {
         if (!(min_p > 0.0f) || ch == 0.0f) return -kInf;  // (at an infinite temperature all weigh the same)
-        const double t = (double)M + S.thr;
+        const float top = S.top;
+        const double t = (double)top + S.thr;
         float x = (float)t;
         if ((double)x < t) x = nextafterf(x, kInf);
-        return fminf(x, M);
+        return fminf(x, top);
     }
     // min-p's cut
     __device__ __forceinline__ void cut_min_p(float min_p) {
@@ -856,12 +862,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         bad = bad || !(x < kInf);
         top = fmaxf(top, x);
     }
-    if (tid == 0) {
+    if (tid < 2) {
         // y's factor, 32 / (T log(2)), as a pair; a temperature next to 0 leaves the largest logits only
         constexpr float C = 46.16624069213867f, Cl = 6.1630817e-07f;
-        const float c = fminf(__fdiv_rn(C, T), 3e38f);
-        const float rest = c < 3e38f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-c, T, C), Cl), T) : 0.0f;
-        S.ch = c, S.cl = rest == rest ? rest : 0.0f;
+        const float Th = tid ? __fmul_rn(T, kFar) : T, c = fminf(__fdiv_rn(C, Th), 3e38f);
+        const float rest = c < 3e38f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-c, Th, C), Cl), Th) : 0.0f;
+        S.ch[tid] = c, S.cl[tid] = rest == rest ? rest : 0.0f;
     }
     if (tid == 32 && min_p > 0.0f) S.thr = (double)T * log((double)fminf(min_p, 1.0f));
     top = warp_max(top);
@@ -870,13 +876,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < kWarps; e++) top = fmaxf(top, red[e]);
-    Row R{A, S, words, from, rank, n, first, 0.0f, S.ch, S.cl, pow.x, pow.y, kKeyNegInf + 1, 0xffffffffu};
+    Row R{A, S, words, from, rank, n, first, 0.0f, 0.0f, 0.0f, 0.0f, pow.x, pow.y, kKeyNegInf + 1, 0xffffffffu};
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // (all are: their memory may be written)
     R.tell((u64)key_of(top));
     uint32_t best = 0;
     for (int e = 0; e < A.cluster; e++) best = max(best, (uint32_t)R.told(0, e));
-    R.M = of_key(best);
-    const float M = R.M;
+    const float M = of_key(best);
+    S.top = M;  // (all threads the same)
+    const int far = M > kFarLogit || T > kFarT;
+    R.h = far ? kFar : 1.0f;
+    R.M = __fmul_rn(M, R.h), R.ch = S.ch[far], R.cl = S.cl[far];
     if (!(M < kInf) || !(M > -kInf) || !(T == T)) {  // a NaN or plus infinity, or no word at all
         if (rank == 0) R.write(row, -1, 0.0f, 0);
         return;
