@@ -725,7 +725,8 @@ qlin_status qlin_kv4_read(const qlin_kv4 *kv, const int32_t *positions, const in
  * are padding or out of range get zeros.  Keys whose page is out of range count
  * as not seen and set bit 0 of *status_word (bit 1: a bounded device wait gave
  * up).  A NaN or an infinity in a lane's q can make the outputs of its heads
- * NaN; a score below fp32's range has no weight.  fp32 accuracy for the values
+ * NaN, and a score (in units of log 2) above fp32's range does; one below it has
+ * no weight.  fp32 accuracy for the values
  * that the cache holds.  n_lanes: 1..4096.
  * workspace: device, 16-byte aligned, qlin_attention_kv4_workspace_size bytes
  * (0 for sizes out of range), owned by the caller, any content; calls sharing

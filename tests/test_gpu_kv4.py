@@ -502,6 +502,38 @@ def test_queries_that_are_not_finite(dev, tensor):
         assert e[heads].max() <= TOL
 
 
+@pytest.mark.parametrize("case", ["few", "users", "chunk", "long"])
+def test_scores_past_the_types_range(dev, case):
+    """finite queries whose scores fp32 does not hold: NaN for their lane and head, never a number; the others are right"""
+    import torch
+
+    from weight_streaming_gemv_gb300 import qlin
+
+    H, G, hd = 4, 1, 256
+    pool = Pool(dev, 3, 20000 if case == "long" else 700, G, hd, 64)
+    pos, seqs = {"few": ([100, 699, 5], [0, 1, 2]), "users": (list(range(0, 700, 2)) * 3, [0] * 350 + [1] * 350 + [2] * 350),
+                 "chunk": (list(range(100)) * 12, ([0] * 100 + [1] * 100) * 6), "long": ([19999, 15000, 700], [2, 0, 1])}[case]
+    assert qlin.qlin_attention_kv4_on_tensor_cores(pool.c, len(pos), H, G, hd, 0, 0) == (case != "few")
+    call = Call(dev, len(pos), H, G, hd)
+    # along a key that the lane sees: its score is some 3e38 * 20, the others' may be anything
+    hot = [i for i in range(len(pos)) if i % 7 == 0]
+    host = [pool.host(s)[0] for s in range(3)]
+    q = call.q.cpu().numpy()
+    for i in hot:
+        q[i, i % H] = np.sign(host[seqs[i]][pos[i] // 2, 0]) * 3e38
+    call.q.copy_(torch.from_numpy(q))
+    call.go(pool, i32(pos, dev), i32(seqs, dev))
+    got = call.result()
+    for i in hot:
+        assert np.isnan(got[i, i % H]).all(), (i, pos[i])
+    full = [pool.host(s) for s in range(3)]
+    for i in list(range(min(24, len(pos)))) + list(range(0, len(pos), 61)):
+        heads = [h for h in range(H) if i not in hot or h != i % H]
+        want = ref.attend(np.where(np.abs(q[i]) > 1e30, 0, q[i]), full[seqs[i]][0], full[seqs[i]][1], pos[i], 0, 0, G)
+        e = np.linalg.norm(got[i] - want, axis=-1) / np.linalg.norm(want, axis=-1)
+        assert e[heads].max() <= TOL, (i, e)
+
+
 @pytest.mark.parametrize("tensor", [False, True])
 def test_same_bits_whatever_else_runs(dev, tensor):
     """the same call twice, in a graph replayed with other positions, and beside another call on another stream"""

@@ -1027,6 +1027,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         l = f0 * l + f1 * S.sum[(own ^ 16) + t];
                         mc = m;
                     }
+                    if (mc == kInf) l = __int_as_float(0x7fc00000);  // (a score past fp32's range)
                     const int64_t id = S.rowid[r];
                     float inv = 1.0f;
                     if (p->whole) {
