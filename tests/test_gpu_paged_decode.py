@@ -119,6 +119,50 @@ def test_step_is_its_calls(dev, hd, G, page):
             lens[1] = 0
 
 
+@pytest.mark.parametrize("hd,G,page", [(256, 1, 64), (128, 2, 256), (64, 4, 16)])
+def test_step_on_the_tensor_cores(dev, hd, G, page):
+    """steps whose attention goes to the tensor cores: chunks of three prompts in more than 64 lanes, then 70 users' single
+    tokens, over two layers' pools"""
+    import torch
+
+    from weight_streaming_gemv_gb300 import qlin
+    from weight_streaming_gemv_gb300.decoder import T158Decoder
+
+    cfg = synth.DecoderConfig(max_pos=4096, **dict(SHAPE, head_dim=hd, n_kv_heads=G))
+    d = T158Decoder(cfg, synth.decoder_weights(cfg, seed=5), device=dev)
+    S = 70
+    pages = 3 * (-(-600 // page)) + S * (-(-40 // page))
+    d.prepare_paged(n_seqs=S, n_pages=pages, max_lanes=640, page_rows=page)
+    codes, scales = d.page_codes.clone(), d.page_scales.clone()
+    rng = np.random.default_rng(hd)
+    lens = np.zeros(S, int)
+
+    def step(counts):
+        """counts[s] more tokens of every sequence"""
+        for s in np.nonzero(counts)[0]:
+            d.paged_room(int(s), int(lens[s] + counts[s]))
+        pos = np.concatenate([lens[s] + np.arange(counts[s]) for s in range(S)])
+        seqs = np.repeat(np.arange(S), counts)
+        n = len(pos)
+        assert qlin.qlin_attention_kv4_on_tensor_cores(d.paged.kv, n, 4, G, hd, 0, 0)
+        for t, x in ((d.paged_tokens, rng.integers(0, cfg.vocab, n)), (d.paged_pos, pos), (d.paged_seq, seqs)):
+            t[:n].copy_(torch.as_tensor(x.astype(np.int32)))
+        lg = torch.empty((n, cfg.vocab), device=dev)
+        d.step_paged(n, logits=lg)
+        d.check_paged_status()
+        want, nxt = _by_calls(d, codes, scales, d.paged_tokens[:n], d.paged_pos[:n], d.paged_seq[:n])
+        assert torch.equal(codes, d.page_codes) and torch.equal(scales, d.page_scales)
+        assert torch.equal(lg, want) and torch.equal(d.paged_next[:n], nxt)
+        lens[:] = lens + counts
+
+    first = np.zeros(S, int)
+    first[[0, 33, 69]] = 300, 1, 137
+    step(first)
+    step(np.where(np.arange(S) == 33, 400, rng.integers(0, 4, S)))
+    for _ in range(2):
+        step(np.ones(S, int))
+
+
 def test_status_and_padding(dev):
     import torch
 
