@@ -362,10 +362,10 @@ __global__ void __launch_bounds__(kThreads) kv4_few_merge_kernel(const __grid_co
 //
 // Measured (4 query heads on one KV head of 256 unless said): 64 lanes of up to
 // 8192 keys 50 us for 106 MB of cache, 2.1 TB/s; 16 lanes of up to 32768 keys,
-// 8 heads on each of two of 128, 61 us for 111 MB; 64 lanes with a window of 1024
-// 25 us; two prompts of 1024 lanes with that window 71 us.  A chunk takes some
-// 3300 cycles, of which DRAM is busy 27% and the tensor cores 12%: the decoding
-// threads' instructions (58% of the issue slots, 7 us of the 51 without the
+// 8 heads on each of two of 128, 60 us for 111 MB; 64 lanes with a window of 1024
+// 25 us; two prompts of 1024 lanes with that window 70 us.  A chunk takes some
+// 3200 cycles, of which DRAM is busy 28% and the tensor cores 12%: the decoding
+// threads' instructions (60% of the issue slots, 7 us of the 51 without the
 // arithmetic) and the hand-overs from step to step bound it.  Around that a
 // start of 4 us, 5 us where a CTA goes from one tile to the next, and the merge
 // of 4 us, which is most of the window's 25.  Taken back after timing: the

@@ -19,8 +19,10 @@
 // instructions a word.  (Two words at a time in packed fp32 took more: packed
 // operations have no immediate operands, and their constants no registers left.)
 //
-// One cluster of CTAs per row, whose shared memory holds the row: it is read
-// once.  A histogram of 2048 bins over y counts the words, or adds up their
+// One cluster of CTAs per row.  The logits come from memory once: a CTA keeps its
+// first 16384 words in shared memory, and those behind them, where a row is dealt
+// to few CTAs, come from L2 again in every pass (three quarters of 64 rows of
+// 262144 by fours, half of 256 rows of 32000).  A histogram of 2048 bins over y counts the words, or adds up their
 // weights by a line through the bin, good to 10^-5; a CTA sums a share of the
 // bins over the cluster's.  So top-k's
 // border is known to a bin and top-p's to one or two.  Their words go to a list
@@ -33,12 +35,14 @@
 // the search for that.
 //
 // Instructions bound it, not memory: 64 rows of 262144 words with a top_p of 0.9
-// take 98 us for 67 MB, about half of it the exact weights (some 60 instructions
+// take 100 us for 67 MB, about half of it the exact weights (some 60 instructions
 // a word); counting, one addition to shared memory a word (8 cycles a warp), is
-// the next.  (With counts and places in a bin as two additions it took 106.)
-// 256 rows of 32000 with no bound, one pass, take 30 us; one row of 262144 with a
-// top_k of 64, 15.8 us, most of it waiting: the cluster's meetings (some 1200
-// cycles each), the border, the sorted list.
+// the next.  256 rows of 32000 with no bound, one pass, take 30 us.  One row of
+// 262144 with a top_k of 64 takes 16 us, some 32,500 cycles of its first CTA:
+// 3,100 to load, 2,100 for the first meeting, 4,900 to count, 7,500 for the border
+// with three meetings, 6,000 until the list is there, 8,900 to sort it and draw.
+// Where a row has only a few different logits most words meet in a few bins, and
+// the additions to them queue: 64 rows of 262144 words on eight levels take 4.4 ms.
 #include <cmath>
 
 #include "launch.cuh"
@@ -1018,7 +1022,7 @@ qlin_status qlin_sample(const float *logits, int64_t row_stride, const float *u,
     SampleArgs A{logits, row_stride, u, temperature, top_k, top_p, min_p, vocab, tokens, probs, kept};
     const void *kern = (const void *)sample_kernel;
     // As many CTAs to a row as give two to every SM, for no fewer than 4096 words each.  (Rows past what the cluster's
-    // shared memory holds come from L2 again in every pass: 64 rows of 262144 words take 98 us by fours and 200
+    // shared memory holds come from L2 again in every pass: 64 rows of 262144 words take 100 us by fours and 200
     // by sixteens, of which 11 run at a time, one after the other.)
     int c = 1;
     while (c < kMaxCluster && (int64_t)n_rows * c * 2 <= 2 * sm_count() && vocab / c > 4096) c *= 2;
